@@ -19,3 +19,7 @@ from .dash_attn import (  # noqa: F401
     dash_status_string, load, new_workspace, TRACE_SITES, TRACE_DQ_TURN_WAIT, TRACE_DQ_ADD,
     TRACE_TOTAL,
 )
+from .train_ops import (  # noqa: F401
+    DASH_BF16, DASH_FP16, DASH_FP32, dash_linear_xent_workspace_size, linear_xent_backward,
+    linear_xent_forward, new_linear_xent_workspace,
+)

@@ -31,7 +31,11 @@ constexpr size_t kWsHeaderBytes = 256;
 constexpr int kStatusSyncTimeout = 5;
 constexpr int kStatusBounds = 7;
 // Sites of a failed bounds check (WS_QTILE)
-enum : int { CHK_CTA_RANGE = 1, CHK_PIECE = 2, CHK_TASK = 3, CHK_ORDINAL = 4 };
+enum : int {
+  CHK_CTA_RANGE = 1, CHK_PIECE = 2, CHK_TASK = 3, CHK_ORDINAL = 4,
+  // checked in every build: indexes that come from the caller's tensors
+  CHK_TOKEN_ID = 5, CHK_POSITION = 6, CHK_TARGET = 7
+};
 // The fixed dQ order of a block runs as k = deterministic interleaved chains (1 <= k <=
 // kDqChains): contribution o adds, in order, into accumulator copy o % k after
 // contribution o - k, so k = 1 is one serial chain; the convert adds the copies in index
@@ -147,7 +151,7 @@ __device__ __forceinline__ void red_release_add_gpu(int* p, int v) {
 
 #if DASH_BOUNDS_CHECKS
 // Records the first failed bounds check of a launch (any thread; the first one wins).
-__device__ __noinline__ void report_bounds(int* ws, int site, int bh, int value, int bound) {
+__device__ __noinline__ inline void report_bounds(int* ws, int site, int bh, int value, int bound) {
   if (atomicCAS(ws + WS_STATUS, 0, kStatusBounds) == 0) {
     ws[WS_BH] = bh;
     ws[WS_QTILE] = site;
@@ -161,7 +165,7 @@ __device__ __noinline__ void report_bounds(int* ws, int site, int bh, int value,
 // Spin (one thread) until *sem == target. Gives up when another CTA has already
 // reported a failure, or after timeout_ns, recording the first failure in the
 // workspace header. Returns true when it is this CTA's turn.
-__device__ __noinline__ bool wait_turn(const int* sem, int target, int* ws, long long timeout_ns,
+__device__ __noinline__ inline bool wait_turn(const int* sem, int target, int* ws, long long timeout_ns,
                                        int bh, int qtile) {
   int seen = ld_acquire_gpu(sem);
   if (seen == target) return true;
@@ -192,7 +196,7 @@ __device__ __noinline__ bool wait_turn(const int* sem, int target, int* ws, long
 // Spin (one thread) until *sem >= target (a counter that only grows). Gives up when another CTA has already
 // reported a failure, or after timeout_ns, recording the first failure in the
 // workspace header. Returns true when it is this CTA's turn.
-__device__ __noinline__ bool wait_at_least(const int* sem, int target, int* ws, long long timeout_ns,
+__device__ __noinline__ inline bool wait_at_least(const int* sem, int target, int* ws, long long timeout_ns,
                                        int bh, int qtile) {
   int seen = ld_acquire_gpu(sem);
   if (seen >= target) return true;

@@ -21,6 +21,7 @@
 #include "bwd_main.cuh"
 #include "fwd_tc.cuh"
 #include "gemm_splitk.cuh"
+#include "host_common.h"
 #include "sched.h"
 
 static_assert(dash::kStatusBounds == DASH_ERR_BOUNDS, "bounds status: one code");
@@ -275,11 +276,7 @@ cudaEvent_t prof_event(bool stop) {
   return e;
 }
 
-// cuTensorMapEncodeTiled from the driver, fetched through the runtime (no -lcuda).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using dash::EncodeTiledFn;
 
 EncodeTiledFn encoder() {
   static EncodeTiledFn fn = nullptr;
@@ -348,6 +345,13 @@ WsLayout ws_layout(int B, int S, int H, int D) {
 }
 
 }  // namespace
+
+// host_common.h: what the other translation units take from here
+namespace dash {
+void set_last_error(const std::string& text) { g_last_error = text; }
+EncodeTiledFn tensor_map_encoder() { return encoder(); }
+long long sync_timeout_ns() { return g_timeout_ns; }
+}  // namespace dash
 
 extern "C" {
 
@@ -600,11 +604,12 @@ dash_status_t dash_attn_get_status(const void* workspace, cudaStream_t stream) {
   }
   if (words[dash::WS_STATUS] == dash::kStatusBounds) {
     static const char* const sites[] = {"?", "a CTA's piece range", "a piece", "a task",
-                                         "a dQ ordinal"};
+                                         "a dQ ordinal", "a token id", "a position", "a target"};
     const int site = words[dash::WS_QTILE];
     char buf[200];
-    snprintf(buf, sizeof(buf), "bounds check failed on %s: bh/cta=%d value=%d bound=%d",
-             sites[site >= 1 && site <= 4 ? site : 0], words[dash::WS_BH],
+    snprintf(buf, sizeof(buf), "bounds check failed on %s: %s=%d value=%d bound=%d",
+             sites[site >= 1 && site <= dash::CHK_TARGET ? site : 0],
+             site >= dash::CHK_TOKEN_ID ? "row" : "bh/cta", words[dash::WS_BH],
              words[dash::WS_EXPECT], words[dash::WS_SEEN]);
     g_last_error = buf;
     return DASH_ERR_BOUNDS;

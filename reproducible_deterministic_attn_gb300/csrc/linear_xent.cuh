@@ -1,0 +1,418 @@
+// Softmax cross entropy from hidden states (X [T, D], W [V, D], both bf16) without stored
+// logits, and its gradient. Four products share one persistent tensor-core kernel:
+//   LSE   Z = X W^T        a 128 x 256 tile of logits is reduced to (max, sum of exp2) per
+//                          row and half tile; the target's logit is stored
+//   GRAD  Z = X W^T again  the tile becomes G = g (exp(z - lse) - [v = y]) in bf16
+//   DX    dX = G W         K = the vocabulary (of one piece), W read N-major
+//   DW    dW = G^T X       K = the tokens, both operands MN-major
+// A unit of work is one output tile of 128 x 256 (for DX one K range of it), dealt round
+// robin to one CTA per SM.
+//
+// Warp roles (384 threads): 0 = TMA producer (64 of K per stage, 4 stages of 48 KB), 1 = MMA
+// issuer, 4..11 = epilogue (one 32-row quarter and one half of the columns each). Two
+// 256-column accumulators in TMEM, so that the next tile's MMAs run while one is read out.
+#pragma once
+
+#include "tc_shared.cuh"
+#include "train_common.cuh"
+
+namespace dash {
+namespace xent {
+
+using namespace dash::tc;
+
+enum Op : int { LSE = 0, GRAD = 1, DX = 2, DW = 3 };
+
+// What DX does with a finished tile, and DW by type and accumulation.
+enum OutMode : int {
+  OUT_BF16 = 0,        // dX or dW, final
+  OUT_F32 = 1,         // dW in fp32, final; dX of the first of several pieces
+  OUT_F32_ADD = 2,     // dX += (a middle piece); dW fp32 accumulated
+  OUT_BF16_ADD = 3,    // dX final = fp32 sum of the pieces before + this one; dW bf16 accumulated
+  OUT_PART = 4         // dX: this K range's partial
+};
+
+struct Params {
+  int M, N, K;               // extents of this product (valid rows, columns, K)
+  int b_row0;                // LSE/GRAD/DX: first vocabulary row of the piece
+  int tiles_m, tiles_n, splits, ksteps_per_split;
+  int id_bits;
+  const void* targets;
+  long long ignore_index;
+  float scale, scale_log2;
+  // LSE
+  float2* part;              // [2 * tiles_n][M]
+  float* ztgt;               // [M]
+  // GRAD
+  const float* lse;
+  const float* dloss;
+  __nv_bfloat16* g;          // [M][ldg]
+  long long ldg;
+  long long V;
+  // DX, DW
+  int out_mode;
+  void* out;                 // dx, or dw at the piece's first row
+  float* acc;                // DX: fp32 [M][N] over the pieces, or the K ranges' partials
+  int* header;
+  long long timeout_ns;
+};
+
+struct Maps {
+  CUtensorMap a, b;
+};
+
+constexpr int kXentThreads = 384;
+constexpr int kTM = 128, kTN = 256, kTK = 64;
+constexpr int kStages = 4;
+constexpr int kGroupM = 16;
+constexpr int kABytes = kTM * kTK * 2, kBBytes = kTN * kTK * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kBarOff = kStages * kStageBytes;
+constexpr int kSmem = kBarOff + 256 + 1024;
+static_assert(kSmem <= 232448, "shared memory budget");
+enum { B_FULL = 0, B_EMPTY = B_FULL + kStages, B_ACC_FULL = B_EMPTY + kStages,
+       B_ACC_EMPTY = B_ACC_FULL + 2, B_DRAIN = B_ACC_EMPTY + 2, B_COUNT };
+
+// Unit -> (m tile, n tile, K range). Tiles are numbered in groups of kGroupM m-tiles, m
+// first, so that concurrent units share their A and B panels in L2.
+__device__ __forceinline__ void unit_of(const Params& p, int u, int& mi, int& ni, int& split) {
+  split = u % p.splits;
+  const int tile = u / p.splits;
+  const int per_group = kGroupM * p.tiles_n;
+  const int first_m = (tile / per_group) * kGroupM;
+  const int gm = min(kGroupM, p.tiles_m - first_m);
+  const int r = tile % per_group;
+  mi = first_m + r % gm;
+  ni = r / gm;
+}
+
+// 32 consecutive columns of one output row: fp32 values to bf16 or fp32, added to what is
+// there where the mode says so. `n` columns are valid (a multiple of 8).
+template <bool ADD>
+__device__ __forceinline__ void put_bf16(__nv_bfloat16* dst, const float* old32, const float (&v)[32],
+                                         int n) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 8) {
+    if (c < n) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = v[c + i];
+      if (ADD) {
+        float o[8];
+        if (old32) train::load_f32<float, 8>(old32 + c, o);
+        else train::load_f32<__nv_bfloat16, 8>(dst + c, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] += o[i];
+      }
+      train::store_f32<__nv_bfloat16, 8>(dst + c, x);
+    }
+  }
+}
+template <bool ADD>
+__device__ __forceinline__ void put_f32(float* dst, const float (&v)[32], int n) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 8) {
+    if (c < n) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = v[c + i];
+      if (ADD) {
+        float o[8];
+        train::load_f32<float, 8>(dst + c, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] += o[i];
+      }
+      train::store_f32<float, 8>(dst + c, x);
+    }
+  }
+}
+
+template <int OP>
+__global__ void __launch_bounds__(kXentThreads, 1)
+    gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+  constexpr bool A_MN = OP == DW, B_MN = OP == DX || OP == DW;
+  extern __shared__ uint8_t smem_xent[];
+  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_xent + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = (uint64_t*)(sm + kBarOff);
+  uint32_t* tmem_slot = (uint32_t*)(sm + kBarOff + 8 * B_COUNT);
+  volatile int* abort_flag = (volatile int*)(sm + kBarOff + 8 * B_COUNT + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long tmo = p.timeout_ns;
+  const int units = p.tiles_m * p.tiles_n * p.splits;
+  const int ksteps = (p.K + kTK - 1) / kTK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(bars + B_FULL + s, 1);
+      ptx::mbar_init(bars + B_EMPTY + s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(bars + B_ACC_FULL + a, 1);
+      ptx::mbar_init(bars + B_ACC_EMPTY + a, 8);
+    }
+    ptx::mbar_init(bars + B_DRAIN, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) ptx::tmem_alloc(tmem_slot, 512);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ===================================== TMA producer =====================================
+    if (lane == 0) {
+      long long kb = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        int mi, ni, split;
+        unit_of(p, u, mi, ni, split);
+        const int m0 = mi * kTM, n0 = ni * kTN;
+        const int k_end = min(ksteps, (split + 1) * p.ksteps_per_split);
+        for (int k = split * p.ksteps_per_split; k < k_end; ++k, ++kb) {
+          const int s = (int)(kb % kStages);
+          if (kb >= kStages &&
+              !(ok = ptx::mbar_wait(bars + B_EMPTY + s, (int)((kb / kStages) - 1) & 1, abort_flag, tmo)))
+            break;
+          uint64_t* full = bars + B_FULL + s;
+          uint8_t* sa = sm + s * kStageBytes;
+          uint8_t* sb = sa + kABytes;
+          const int k0 = k * kTK;
+          ptx::mbar_expect_tx(full, kStageBytes);
+          if (A_MN) {
+            for (int i = 0; i < kTM / 64; ++i)
+              ptx::tma_load_2d(sa + i * 8192, &maps.a, m0 + i * 64, k0, full);
+          } else {
+            ptx::tma_load_2d(sa, &maps.a, k0, m0, full);
+          }
+          if (B_MN) {
+            const int kr = OP == DX ? p.b_row0 + k0 : k0;
+            for (int i = 0; i < kTN / 64; ++i)
+              ptx::tma_load_2d(sb + i * 8192, &maps.b, n0 + i * 64, kr, full);
+          } else {
+            ptx::tma_load_2d(sb, &maps.b, k0, p.b_row0 + n0, full);
+          }
+        }
+      }
+      for (long long k = (kb > kStages ? kb - kStages : 0); k < kb; ++k)
+        ptx::mbar_drain(bars + B_FULL + (int)(k % kStages), (int)(k / kStages) & 1, 100000000ll);
+    }
+  } else if (warp == 1) {
+    // ====================================== MMA issuer ======================================
+    if (lane == 0) {
+      constexpr uint32_t ID = ptx::idesc_bf16(kTM, kTN, A_MN, B_MN);
+      // a K step of 16: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major block
+      constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
+      const uint32_t s0 = ptx::smem_u32(sm);
+      long long kb = 0;
+      int it = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++it) {
+        const int acc = it & 1;
+        int mi, ni, split;
+        unit_of(p, u, mi, ni, split);
+        const int k_begin = split * p.ksteps_per_split;
+        const int k_end = min(ksteps, (split + 1) * p.ksteps_per_split);
+        if (it >= 2 && !(ok = ptx::mbar_wait(bars + B_ACC_EMPTY + acc, ((it >> 1) - 1) & 1, abort_flag, tmo)))
+          break;
+        ptx::tc_fence_after();
+        for (int k = k_begin; k < k_end; ++k, ++kb) {
+          const int s = (int)(kb % kStages);
+          if (!(ok = ptx::mbar_wait(bars + B_FULL + s, (int)(kb / kStages) & 1, abort_flag, tmo))) break;
+          ptx::tc_fence_after();
+          const uint32_t a_lo = ptx::sdesc_lo(s0 + s * kStageBytes, A_MN ? 8192 : 16);
+          const uint32_t b_lo = ptx::sdesc_lo(s0 + s * kStageBytes + kABytes, B_MN ? 8192 : 16);
+#pragma unroll
+          for (int ks = 0; ks < kTK / 16; ++ks)
+            ptx::mma_lo(tmem + acc * kTN, a_lo + ks * A_STEP, b_lo + ks * B_STEP, ID,
+                        (k > k_begin || ks > 0) ? 1u : 0u);
+          ptx::mma_commit(bars + B_EMPTY + s);
+        }
+        if (!ok) break;
+        ptx::mma_commit(bars + B_ACC_FULL + acc);
+      }
+      ptx::mma_commit(bars + B_DRAIN);
+      ptx::mbar_drain(bars + B_DRAIN, 0, 1000000000ll);
+    }
+  } else if (warp >= 4) {
+    // ======================================= epilogue =======================================
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
+    int it = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++it) {
+      const int acc = it & 1;
+      int mi, ni, split;
+      unit_of(p, u, mi, ni, split);
+      const int row = mi * kTM + quarter * 32 + lane;
+      const int col0 = ni * kTN + half * (kTN / 2);
+      const bool live = row < p.M;
+      // what the row needs besides the tile, fetched before the wait
+      long long tgt = -1;
+      float nlse2 = 0.f, gs = 0.f;
+      if (OP == LSE || OP == GRAD) {
+        if (live) tgt = train::load_index(p.targets, row, p.id_bits);
+        if (OP == GRAD && live) {
+          const bool used = tgt != p.ignore_index && tgt >= 0 && tgt < p.V;
+          gs = used ? p.scale * __ldg(p.dloss + row) : 0.f;
+          nlse2 = -__ldg(p.lse + row) * kLog2e;
+          if (!used) tgt = -1;
+        }
+        if (tgt == p.ignore_index) tgt = -1;
+        tgt -= p.b_row0;
+      }
+      if (!ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo)) break;
+      ptx::tc_fence_after();
+      float m2 = -INFINITY, sum = 0.f;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kTN / 2; c0 += 32) {
+        float v[32];
+        ptx::tmem_ld32(tmem + lane_addr + acc * kTN + half * (kTN / 2) + c0, v);
+        const int col = col0 + c0;                       // first column of the 32
+        const int n = p.N - col;                         // valid ones
+        if (OP == LSE) {
+          if (n <= 0) break;
+          const long long tc = tgt - col;
+          float cm = -INFINITY;
+          float zt = 0.f;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (c == tc) zt = v[c];
+            v[c] = c < n ? v[c] * p.scale_log2 : -INFINITY;
+            cm = fmaxf(cm, v[c]);
+          }
+          if (tc >= 0 && tc < 32 && tc < n) p.ztgt[row] = zt * p.scale;
+          const float nm = fmaxf(m2, cm);
+          const float base = nm == -INFINITY ? 0.f : nm;
+          float s = 0.f;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s += ptx::ex2(v[c] - base);
+          sum = sum * ptx::ex2(m2 - base) + s;
+          m2 = nm;
+        } else if (OP == GRAD) {
+          const long long tc = tgt - col;
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float a = ptx::ex2(fmaf(v[c], p.scale_log2, nlse2));
+            float b = ptx::ex2(fmaf(v[c + 1], p.scale_log2, nlse2));
+            if (c == tc) a -= 1.f;
+            if (c + 1 == tc) b -= 1.f;
+            w[c >> 1] = gs == 0.f ? 0u : ptx::pack_bf16(a * gs, b * gs);
+          }
+          if (live && n > 0) {
+            uint4* dst = reinterpret_cast<uint4*>(p.g + (size_t)row * p.ldg + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        } else {
+          if (live && n > 0) {
+            const size_t at = (size_t)row * p.N + col;
+            __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+            if (p.out_mode == OUT_BF16) put_bf16<false>(ob, nullptr, v, n);
+            else if (p.out_mode == OUT_BF16_ADD) put_bf16<true>(ob, OP == DX ? p.acc + at : nullptr, v, n);
+            else if (OP == DX && p.out_mode == OUT_PART) put_f32<false>(p.acc + (size_t)split * p.M * p.N + at, v, n);
+            else {
+              float* of = (OP == DX ? p.acc : reinterpret_cast<float*>(p.out)) + at;
+              if (p.out_mode == OUT_F32) put_f32<false>(of, v, n);
+              else put_f32<true>(of, v, n);
+            }
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars + B_ACC_EMPTY + acc);
+      if (OP == LSE && live) p.part[(size_t)(ni * 2 + half) * p.M + row] = make_float2(m2, sum);
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag && atomicCAS(p.header + WS_STATUS, 0, kStatusSyncTimeout) == 0) {
+    p.header[WS_BH] = -1;
+    p.header[WS_QTILE] = blockIdx.x;
+  }
+}
+
+// Joins the half tiles' (max, sum) of every row in a fixed order: 32 rows a block, the parts
+// cut into 8 runs, one thread each, then the runs in order.
+__global__ void __launch_bounds__(256) lse_join_kernel(const float2* part, const float* ztgt, int parts,
+                                                       int T, const void* targets, int id_bits,
+                                                       long long ignore_index, long long V, float* loss,
+                                                       float* lse, int* header) {
+  __shared__ float2 runs[8][32];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.f;
+  if (row < T) {
+    const int per = (parts + 7) / 8;
+    const int end = min(parts, (g + 1) * per);
+    for (int k = g * per; k < end; ++k) {
+      const float2 x = part[(size_t)k * T + row];
+      const float nm = fmaxf(m, x.x);
+      const float base = nm == -INFINITY ? 0.f : nm;
+      s = s * ptx::ex2(m - base) + x.y * ptx::ex2(x.x - base);
+      m = nm;
+    }
+  }
+  runs[g][lane] = make_float2(m, s);
+  __syncthreads();
+  if (g == 0 && row < T) {
+    for (int k = 1; k < 8; ++k) {
+      const float2 x = runs[k][lane];
+      const float nm = fmaxf(m, x.x);
+      const float base = nm == -INFINITY ? 0.f : nm;
+      s = s * ptx::ex2(m - base) + x.y * ptx::ex2(x.x - base);
+      m = nm;
+    }
+    const float l = (m == -INFINITY ? 0.f : m) * kLn2 + logf(s);
+    lse[row] = l;
+    const long long y = train::load_index(targets, row, id_bits);
+    float out = 0.f;
+    if (y != ignore_index) {
+      if (y < 0 || y >= V) {
+        train::report_index(header, CHK_TARGET, row, y, V);
+        out = NAN;
+      } else {
+        out = l - ztgt[row];
+      }
+    }
+    loss[row] = out;
+  }
+}
+
+// dX from the K ranges' partials, added in order (after what the pieces before left in acc,
+// when there are any); the last piece stores bf16.
+__global__ void __launch_bounds__(256) dx_join_kernel(const float* part, int splits, size_t n, float* acc,
+                                                      int first, int last, __nv_bfloat16* dx) {
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  float x[8] = {};
+  if (!first) train::load_f32<float, 8>(acc + i, x);
+  for (int s = 0; s < splits; ++s) {
+    float y[8];
+    train::load_f32<float, 8>(part + (size_t)s * n + i, y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] += y[k];
+  }
+  if (last) train::store_f32<__nv_bfloat16, 8>(dx + i, x);
+  else train::store_f32<float, 8>(acc + i, x);
+}
+
+// Reports targets out of range (the backward treats them as ignored).
+__global__ void __launch_bounds__(256) check_targets_kernel(const void* targets, int id_bits, int T,
+                                                            long long ignore_index, long long V,
+                                                            int* header) {
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= T) return;
+  const long long y = train::load_index(targets, t, id_bits);
+  if (y != ignore_index && (y < 0 || y >= V)) train::report_index(header, CHK_TARGET, t, y, V);
+}
+
+}  // namespace xent
+}  // namespace dash

@@ -1,0 +1,523 @@
+// Token embedding (dash_embed_fwd) and its gradient by sorted tokens (dash_embed_bwd).
+//
+// The forward is a gather of rows: one load and one store of 16 bytes a thread and four rows
+// in flight, bound by HBM. The gradient has three launches:
+//   embed_sort  one cluster of 8 CTAs sorts the tokens by id: a stable counting sort by
+//               digits of at most 9 bits, so two passes up to 2^18 ids. Each warp counts a
+//               run of tokens of its own, so ranks within a digit follow the token order
+//               without atomics; the CTAs' counts meet in distributed shared memory.
+//   embed_rows  runs of 32 sorted places times column tiles: an id's rows are added in
+//               order in registers; ids that lie within one run are stored, the parts of
+//               those that cross runs go to the workspace. The same launch zeroes the rows
+//               of ids that do not occur (a bit for each id, set by the sort).
+//   embed_join  adds the parts of the ids that cross runs, in order.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "dash_train.h"
+#include "host_common.h"
+#include "train_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+using namespace dash;
+using namespace dash::train;
+
+constexpr int kRun = 32;                // sorted places a run
+constexpr int kSortCtas = 8;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxDigitBits = 9;
+
+// ---- forward ------------------------------------------------------------------------------
+
+constexpr int kFwdThreads = 256;
+constexpr int kFwdRows = 4;             // rows a team of threads has in flight
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kFwdThreads)
+    embed_fwd_kernel(const T* table, const void* ids, T* out, int* status, long long n, long long V, int D,
+                     long long ld_table, long long ld_out, float scale, int id_bits, int tx) {
+  const int x = threadIdx.x % tx, y = threadIdx.x / tx, ty = kFwdThreads / tx;
+  const long long row0 = (long long)blockIdx.x * ty * kFwdRows + y;
+  long long id[kFwdRows];
+#pragma unroll
+  for (int r = 0; r < kFwdRows; ++r) {
+    const long long row = row0 + r * ty;
+    id[r] = row < n ? load_index(ids, row, id_bits) : -2;
+    if (row < n && (id[r] < 0 || id[r] >= V)) {
+      id[r] = -1;
+      if (x == 0 && status) *status = kStatusBounds;
+    }
+  }
+  for (int c = x * VEC; c < D; c += tx * VEC) {
+    Vec<T, VEC> v[kFwdRows];
+#pragma unroll
+    for (int r = 0; r < kFwdRows; ++r)
+      if (id[r] >= 0) v[r] = load_vec<T, VEC>(table + id[r] * ld_table + c);
+#pragma unroll
+    for (int r = 0; r < kFwdRows; ++r) {
+      if (id[r] == -2) continue;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        if (id[r] < 0) v[r].v[i] = from_f32<T>(NAN);
+        else if (scale != 1.f) v[r].v[i] = from_f32<T>(to_f32(v[r].v[i]) * scale);
+      }
+      store_vec<T, VEC>(out + (row0 + r * ty) * ld_out + c, v[r]);
+    }
+  }
+}
+
+// ---- the sort -----------------------------------------------------------------------------
+
+struct SortArgs {
+  const void* ids;
+  int id_bits;
+  long long T, V, padding_idx;
+  int passes, digit_bits;
+  int* header;
+  unsigned* present;          // bit v: id v occurs
+  long long present_words;
+  unsigned *keys[2], *toks[2];   // the last pass writes index (passes - 1) & 1
+};
+
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads)
+    embed_sort_kernel(const SortArgs a) {
+  extern __shared__ unsigned sort_smem[];
+  const int bins = 1 << a.digit_bits;
+  unsigned* hist = sort_smem;                       // [warps][bins]
+  unsigned* cta_total = hist + kSortWarps * bins;   // [bins]
+  unsigned* base = cta_total + bins;                // [bins]
+  __shared__ unsigned warp_sums[kSortWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned lt = (1u << lane) - 1;
+
+  for (long long i = (long long)rank * kSortThreads + threadIdx.x; i < a.present_words;
+       i += kSortCtas * kSortThreads)
+    a.present[i] = 0;
+  if (rank == 0 && threadIdx.x < kWsHeaderBytes / 4) a.header[threadIdx.x] = 0;
+
+  // this warp's run of whole 32-token strips
+  const long long strips = (a.T + 31) / 32;
+  const long long per_warp = (strips + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps);
+  const long long first = ((long long)rank * kSortWarps + warp) * per_warp;
+  const long long last = min(strips, first + per_warp);
+  unsigned* mine = hist + warp * bins;
+
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.digit_bits;
+    const unsigned* kin = a.keys[(pass + 1) & 1];
+    const unsigned* tin = a.toks[(pass + 1) & 1];
+    unsigned* kout = a.keys[pass & 1];
+    unsigned* tout = a.toks[pass & 1];
+    auto key_at = [&](long long t) -> unsigned {
+      if (pass > 0) return __ldcg(kin + t);
+      const long long id = load_index(a.ids, t, a.id_bits);
+      return id < 0 || id >= a.V || id == a.padding_idx ? (unsigned)a.V : (unsigned)id;
+    };
+    for (int d = lane; d < bins; d += 32) mine[d] = 0;
+    __syncwarp();
+    for (long long s = first; s < last; ++s) {
+      const long long t = s * 32 + lane;
+      const bool in = t < a.T;
+      const unsigned live = __ballot_sync(0xffffffffu, in);
+      if (in) {
+        const unsigned d = (key_at(t) >> shift) & (bins - 1);
+        const unsigned peers = __match_any_sync(live, d);
+        if ((peers & lt) == 0) mine[d] += __popc(peers);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    // counts -> offsets of the warps within the CTA, and the CTA's totals
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) {
+      unsigned run = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const unsigned c = hist[w * bins + d];
+        hist[w * bins + d] = run;
+        run += c;
+      }
+      cta_total[d] = run;
+    }
+    cluster.sync();
+    // offset of each digit over all CTAs (bins <= threads)
+    unsigned lower = 0, total = 0;
+    const int d = threadIdx.x;
+    if (d < bins) {
+      for (int c = 0; c < kSortCtas; ++c) {
+        const unsigned v = *cluster.map_shared_rank(cta_total + d, c);
+        if (c < rank) lower += v;
+        total += v;
+      }
+    }
+    unsigned scan = total;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned up = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += up;
+    }
+    if (lane == 31) warp_sums[warp] = scan;
+    __syncthreads();
+    unsigned before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sums[w];
+    if (d < bins) base[d] = before + scan - total + lower;
+    __syncthreads();
+    for (long long s = first; s < last; ++s) {
+      const long long t = s * 32 + lane;
+      const bool in = t < a.T;
+      const unsigned live = __ballot_sync(0xffffffffu, in);
+      unsigned key = 0, dg = 0, peers = 0;
+      if (in) {
+        key = key_at(t);
+        dg = (key >> shift) & (bins - 1);
+        peers = __match_any_sync(live, dg);
+        const unsigned at = base[dg] + mine[dg] + __popc(peers & lt);
+        kout[at] = key;
+        tout[at] = pass > 0 ? __ldcg(tin + t) : (unsigned)t;
+        if (pass == 0) {
+          if (key < a.V) {
+            atomicOr(a.present + (key >> 5), 1u << (key & 31));
+          } else {
+            const long long id = load_index(a.ids, t, a.id_bits);
+            if (id < 0 || id >= a.V) report_index(a.header, CHK_TOKEN_ID, t, id, a.V);
+          }
+        }
+      }
+      __syncwarp();
+      if (in && (peers & lt) == 0) mine[dg] += __popc(peers);
+      __syncwarp();
+    }
+    cluster.sync();   // the totals have been read; the sorted arrays are visible
+  }
+}
+
+// ---- the rows -----------------------------------------------------------------------------
+
+struct RowArgs {
+  const unsigned *keys, *toks, *present;
+  long long T, V;
+  int D;
+  long long ld_dout;
+  float scale;
+  int accumulate;
+  float* part;                // [runs][2][Dp]: 0 = of an id begun in an earlier run, 1 = of one
+  int Dp;                     //     that goes on in the next
+  int tx, col_tiles;
+  long long runs, run_blocks;
+};
+
+constexpr int kRowThreads = 128;
+constexpr int kZeroRows = 64;           // table rows a zeroing block looks at
+
+template <typename TO, int VEC>
+__device__ __forceinline__ void put_row(TO* dst, const float (&acc)[VEC], float scale, int accumulate) {
+  float x[VEC];
+  if (accumulate) {
+    load_f32<TO, VEC>(dst, x);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = fmaf(acc[i], scale, x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = acc[i] * scale;
+  }
+  store_f32<TO, VEC>(dst, x);
+}
+
+template <typename TI, typename TO, int VEC>
+__global__ void __launch_bounds__(kRowThreads)
+    embed_rows_kernel(const TI* dout, TO* dtable, const RowArgs a) {
+  const int x = threadIdx.x % a.tx, y = threadIdx.x / a.tx, ty = kRowThreads / a.tx;
+  if (blockIdx.x >= a.run_blocks) {
+    const long long v0 = (blockIdx.x - a.run_blocks) * kZeroRows;
+    float zero[VEC] = {};
+    for (long long v = v0 + y; v < min(a.V, v0 + kZeroRows); v += ty) {
+      if ((__ldg(a.present + (v >> 5)) >> (v & 31)) & 1u) continue;
+      for (int c = x * VEC; c < a.D; c += a.tx * VEC) store_f32<TO, VEC>(dtable + v * a.D + c, zero);
+    }
+    return;
+  }
+  const long long run = (blockIdx.x / a.col_tiles) * (long long)ty + y;
+  const int col = ((int)(blockIdx.x % a.col_tiles) * a.tx + x) * VEC;
+  if (run >= a.runs || col >= a.D) return;
+  const long long p0 = run * kRun;
+  const int n = (int)min((long long)kRun, a.T - p0);
+  const unsigned V = (unsigned)a.V;
+  const unsigned* keys = a.keys + p0;
+  const unsigned* toks = a.toks + p0;
+  unsigned key = __ldg(keys);
+  bool begun = run > 0 && __ldg(keys - 1) == key;
+  float acc[VEC] = {};
+  constexpr int U = 8;
+#pragma unroll 1
+  for (int p = 0; p < n && key < V; p += U) {
+    Vec<TI, VEC> v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (p + i < n) v[i] = load_vec<TI, VEC>(dout + __ldg(toks + p + i) * a.ld_dout + col);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (p + i < n && key < V) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] += to_f32(v[i].v[k]);
+        const bool more = p0 + p + i + 1 < a.T;
+        const unsigned next = more ? __ldg(keys + p + i + 1) : 0xffffffffu;
+        if (next != key || p + i + 1 == n) {
+          const bool goes_on = next == key;
+          if (!begun && !goes_on) {
+            put_row<TO, VEC>(dtable + (long long)key * a.D + col, acc, a.scale, a.accumulate);
+          } else {
+            store_f32<float, VEC>(a.part + (run * 2 + (begun ? 0 : 1)) * a.Dp + col, acc);
+          }
+          begun = false;
+          key = next;
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+        }
+      }
+    }
+  }
+}
+
+// One block for each run in which an id begins that goes on in the next, and 128 columns: 8
+// groups of 32 threads add an eighth of the following runs' parts each, in order; then the
+// eighths are added in order.
+template <typename TO>
+__global__ void __launch_bounds__(256) embed_join_kernel(TO* dtable, const RowArgs a) {
+  const long long run = blockIdx.x;
+  const long long p0 = run * kRun;
+  if (p0 + kRun >= a.T) return;
+  const unsigned key = __ldg(a.keys + p0 + kRun - 1);
+  if (key >= (unsigned)a.V || __ldg(a.keys + p0 + kRun) != key) return;
+  if (run > 0 && __ldg(a.keys + p0 - 1) == key) return;   // begun in an earlier run
+  __shared__ float4 sums[8][32];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  // the following runs that start with this id
+  long long follow = 1;
+  for (;;) {
+    const long long r = run + 1 + follow + lane;
+    const unsigned same = __ballot_sync(0xffffffffu, r < a.runs && __ldg(a.keys + r * kRun) == key);
+    if (same == 0xffffffffu) {
+      follow += 32;
+      continue;
+    }
+    follow += __ffs(~same) - 1;
+    break;
+  }
+  const int col = (blockIdx.y * 32 + lane) * 4;
+  const long long per = (follow + 7) / 8;
+  const long long end = min(follow, (g + 1) * per);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < a.Dp) {
+#pragma unroll 4
+    for (long long r = g * per; r < end; ++r) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (run + 1 + r) * 2 * a.Dp + col));
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  }
+  sums[g][lane] = s;
+  __syncthreads();
+  if (g == 0 && col < a.Dp) {
+    float4 t = __ldcg(reinterpret_cast<const float4*>(a.part + (run * 2 + 1) * a.Dp + col));
+    for (int k = 0; k < 8; ++k) {
+      t.x += sums[k][lane].x;
+      t.y += sums[k][lane].y;
+      t.z += sums[k][lane].z;
+      t.w += sums[k][lane].w;
+    }
+    const float v[4] = {t.x, t.y, t.z, t.w};
+    for (int i = 0; i < 4; ++i)
+      if (col + i < a.D) {
+        const float one[1] = {v[i]};
+        put_row<TO, 1>(dtable + (long long)key * a.D + col + i, one, a.scale, a.accumulate);
+      }
+  }
+}
+
+// ---- host ---------------------------------------------------------------------------------
+
+size_t elt_bytes(int dtype) { return dtype == DASH_FP32 ? 4 : 2; }
+
+bool sizes_ok(long long T, long long V, int D) {
+  const long long lim = (1ll << 31) - 256;
+  return T >= 0 && T < lim && V >= 1 && V < lim && D >= 1 && D <= (1 << 20);
+}
+
+int pow2_lanes(int need, int most) {
+  int t = 1;
+  while (t < need && t < most) t *= 2;
+  return t;
+}
+
+struct Layout {
+  size_t present, keys0, keys1, toks0, toks1, part, total;
+  long long runs;
+  int Dp;
+};
+
+Layout layout(long long T, long long V, int D) {
+  Layout l;
+  size_t at = kWsHeaderBytes;
+  auto take = [&at](size_t bytes) {
+    const size_t here = at;
+    at = round_up_to(at + bytes, 256);
+    return here;
+  };
+  l.runs = ceil_div<long long>(T, kRun);
+  l.Dp = (int)round_up_to(D, 8);
+  l.present = take((size_t)ceil_div<long long>(V, 32) * 4);
+  l.keys0 = take((size_t)T * 4);
+  l.keys1 = take((size_t)T * 4);
+  l.toks0 = take((size_t)T * 4);
+  l.toks1 = take((size_t)T * 4);
+  l.part = take((size_t)l.runs * 2 * l.Dp * 4);
+  l.total = at;
+  return l;
+}
+
+template <typename T>
+dash_status_t fwd_typed(const void* table, const void* ids, void* out, int* status, long long n, long long V,
+                        int D, long long ldt, long long ldo, float scale, int id_bits, cudaStream_t stream) {
+  constexpr int W = 16 / sizeof(T);
+  const bool wide = D % W == 0 && ldt % W == 0 && ldo % W == 0 && is_aligned(table, 16) && is_aligned(out, 16);
+  const int tx = pow2_lanes(wide ? D / W : D, kFwdThreads);
+  const long long blocks = ceil_div<long long>(n, (long long)(kFwdThreads / tx) * kFwdRows);
+  if (wide)
+    embed_fwd_kernel<T, W><<<(unsigned)blocks, kFwdThreads, 0, stream>>>((const T*)table, ids, (T*)out, status,
+                                                                         n, V, D, ldt, ldo, scale, id_bits, tx);
+  else
+    embed_fwd_kernel<T, 1><<<(unsigned)blocks, kFwdThreads, 0, stream>>>((const T*)table, ids, (T*)out, status,
+                                                                         n, V, D, ldt, ldo, scale, id_bits, tx);
+  DASH_TRY(cudaGetLastError());
+  return DASH_OK;
+}
+
+template <typename TI, typename TO>
+dash_status_t rows_typed(const void* dout, void* dtable, RowArgs a, cudaStream_t stream) {
+  constexpr int W = 16 / sizeof(TI);
+  const bool wide = a.D % W == 0 && a.ld_dout % W == 0 && is_aligned(dout, 16) && is_aligned(dtable, 16);
+  const int vec = wide ? W : 1;
+  a.tx = pow2_lanes(ceil_div(a.D, vec), kRowThreads);
+  a.col_tiles = ceil_div(a.D, a.tx * vec);
+  a.run_blocks = ceil_div<long long>(a.runs, kRowThreads / a.tx) * a.col_tiles;
+  const long long zero_blocks = a.accumulate ? 0 : ceil_div<long long>(a.V, kZeroRows);
+  const long long blocks = a.run_blocks + zero_blocks;
+  if (blocks >= (1ll << 31)) return DASH_ERR_UNSUPPORTED;
+  if (wide)
+    embed_rows_kernel<TI, TO, W><<<(unsigned)blocks, kRowThreads, 0, stream>>>((const TI*)dout, (TO*)dtable, a);
+  else
+    embed_rows_kernel<TI, TO, 1><<<(unsigned)blocks, kRowThreads, 0, stream>>>((const TI*)dout, (TO*)dtable, a);
+  DASH_TRY(cudaGetLastError());
+  if (a.runs > 1) {
+    embed_join_kernel<TO><<<dim3((unsigned)a.runs, (unsigned)ceil_div(a.Dp, 128)), 256, 0, stream>>>(
+        (TO*)dtable, a);
+    DASH_TRY(cudaGetLastError());
+  }
+  return DASH_OK;
+}
+
+bool dtype_ok(int d) { return d == DASH_BF16 || d == DASH_FP16 || d == DASH_FP32; }
+
+}  // namespace
+
+extern "C" {
+
+dash_status_t dash_embed_fwd(const void* table, const void* ids, void* out, int* status,
+                             long long T, long long V, int D, long long ld_table, long long ld_out,
+                             float scale, int dtype, int id_bits, cudaStream_t stream) {
+  if (!table || (T > 0 && (!ids || !out))) return DASH_ERR_INVALID_ARG;
+  if (T < 0 || V < 1 || D < 1 || ld_table < D || ld_out < D) return DASH_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || (id_bits != 32 && id_bits != 64)) return DASH_ERR_INVALID_ARG;
+  if (!sizes_ok(T, V, D) || ld_table > (1ll << 31) || ld_out > (1ll << 31)) return DASH_ERR_UNSUPPORTED;
+  if (!is_aligned(table, elt_bytes(dtype)) || !is_aligned(out, elt_bytes(dtype)) ||
+      !is_aligned(ids, id_bits / 8) || !is_aligned(status, 4))
+    return DASH_ERR_INVALID_ARG;
+  if (status) DASH_TRY(cudaMemsetAsync(status, 0, sizeof(int), stream));
+  if (T == 0) return DASH_OK;
+  switch (dtype) {
+    case DASH_BF16:
+      return fwd_typed<__nv_bfloat16>(table, ids, out, status, T, V, D, ld_table, ld_out, scale, id_bits, stream);
+    case DASH_FP16:
+      return fwd_typed<__half>(table, ids, out, status, T, V, D, ld_table, ld_out, scale, id_bits, stream);
+    default:
+      return fwd_typed<float>(table, ids, out, status, T, V, D, ld_table, ld_out, scale, id_bits, stream);
+  }
+}
+
+size_t dash_embed_bwd_workspace_size(long long T, long long V, int D) {
+  return sizes_ok(T, V, D) ? layout(T, V, D).total : 0;
+}
+
+dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, void* workspace,
+                             size_t workspace_bytes, long long T, long long V, int D,
+                             long long ld_dout, float scale, long long padding_idx, int accumulate,
+                             int dout_dtype, int dtable_dtype, int id_bits, cudaStream_t stream) {
+  if (!dtable || !workspace || (T > 0 && (!dout || !ids))) return DASH_ERR_INVALID_ARG;
+  if (T < 0 || V < 1 || D < 1 || ld_dout < D || padding_idx < -1) return DASH_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return DASH_ERR_INVALID_ARG;
+  if (!dtype_ok(dout_dtype) || !dtype_ok(dtable_dtype) || (id_bits != 32 && id_bits != 64))
+    return DASH_ERR_INVALID_ARG;
+  if (dtable_dtype != dout_dtype && dtable_dtype != DASH_FP32) return DASH_ERR_UNSUPPORTED;
+  if (!sizes_ok(T, V, D) || ld_dout > (1ll << 31)) return DASH_ERR_UNSUPPORTED;
+  if (!is_aligned(dout, elt_bytes(dout_dtype)) || !is_aligned(dtable, elt_bytes(dtable_dtype)) ||
+      !is_aligned(ids, id_bits / 8) || !is_aligned(workspace, 256))
+    return DASH_ERR_INVALID_ARG;
+  const Layout l = layout(T, V, D);
+  if (workspace_bytes < l.total) return DASH_ERR_WORKSPACE_TOO_SMALL;
+  char* ws = (char*)workspace;
+  if (T == 0) {
+    DASH_TRY(cudaMemsetAsync(ws, 0, kWsHeaderBytes, stream));
+    if (!accumulate) DASH_TRY(cudaMemsetAsync(dtable, 0, (size_t)V * D * elt_bytes(dtable_dtype), stream));
+    return DASH_OK;
+  }
+  SortArgs s;
+  s.ids = ids;
+  s.id_bits = id_bits;
+  s.T = T;
+  s.V = V;
+  s.padding_idx = padding_idx;
+  int bits = 1;
+  while ((V >> bits) != 0) ++bits;          // keys 0 .. V (V: left out)
+  s.passes = ceil_div(bits, kMaxDigitBits);
+  s.digit_bits = ceil_div(bits, s.passes);
+  s.header = (int*)ws;
+  s.present = (unsigned*)(ws + l.present);
+  s.present_words = ceil_div<long long>(V, 32);
+  s.keys[0] = (unsigned*)(ws + l.keys0);
+  s.keys[1] = (unsigned*)(ws + l.keys1);
+  s.toks[0] = (unsigned*)(ws + l.toks0);
+  s.toks[1] = (unsigned*)(ws + l.toks1);
+  const size_t smem = ((size_t)(kSortWarps + 2) << s.digit_bits) * 4;
+  DASH_TRY(cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(((size_t)(kSortWarps + 2) << kMaxDigitBits) * 4)));
+  embed_sort_kernel<<<kSortCtas, kSortThreads, smem, stream>>>(s);
+  DASH_TRY(cudaGetLastError());
+  RowArgs a;
+  a.keys = s.keys[(s.passes - 1) & 1];
+  a.toks = s.toks[(s.passes - 1) & 1];
+  a.present = s.present;
+  a.T = T;
+  a.V = V;
+  a.D = D;
+  a.ld_dout = ld_dout;
+  a.scale = scale;
+  a.accumulate = accumulate;
+  a.part = (float*)(ws + l.part);
+  a.Dp = l.Dp;
+  a.runs = l.runs;
+  if (dout_dtype == DASH_BF16)
+    return dtable_dtype == DASH_BF16 ? rows_typed<__nv_bfloat16, __nv_bfloat16>(dout, dtable, a, stream)
+                                     : rows_typed<__nv_bfloat16, float>(dout, dtable, a, stream);
+  if (dout_dtype == DASH_FP16)
+    return dtable_dtype == DASH_FP16 ? rows_typed<__half, __half>(dout, dtable, a, stream)
+                                     : rows_typed<__half, float>(dout, dtable, a, stream);
+  return rows_typed<float, float>(dout, dtable, a, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,277 @@
+// Global gradient norm over many tensors and clipping (dash_grad_clip*).
+//
+// A plan is a device table of pieces of at most 32768 elements. clip_norm walks it with a
+// fixed number of blocks: a thread sums the squares of its elements of a piece in fp32 and
+// adds the piece's sum to an fp64 total, a block's totals are added by a fixed tree, and the
+// last block to finish adds the blocks' totals in order (so the sum's order never depends on
+// which block that is). clip_scale then walks the pieces from the end, where the cache still
+// holds what the norm read last, and returns at once when nothing has to be written. Both
+// are bound by HBM.
+#include <algorithm>
+#include <exception>
+#include <vector>
+
+#include "dash_train.h"
+#include "host_common.h"
+#include "train_common.cuh"
+
+namespace {
+
+using namespace dash;
+using namespace dash::train;
+
+constexpr int kPiece = 32768;
+constexpr int kThreads = 512;
+constexpr int kBlocks = 608;             // fixes the order of the sum: not the SM count
+constexpr unsigned long long kMagic = 0x64617368636c6970ull;
+
+struct Piece {
+  const void* grad;
+  void* out;
+  int count, dtype;
+};
+static_assert(sizeof(Piece) == 24, "table layout");
+
+struct Header {
+  unsigned long long magic;
+  long long pieces;
+  int all_in_place;
+  unsigned done;                         // blocks that have left their total; ends at 0
+  double norm;
+  double totals[kBlocks];
+};
+constexpr size_t kTableOff = (sizeof(Header) + 255) / 256 * 256;
+
+// Sum of squares of this thread's elements of a piece. 32 bits hold the sum unless it
+// overflows or is so small that squares may have vanished; then the elements are scaled by
+// the power of two that brings their largest to [1/2, 1).
+template <typename T, int VEC>
+__device__ __forceinline__ double squares(const T* x, int count) {
+  float s[4] = {};
+  bool any = false;
+  const int whole = count / VEC * VEC;
+  constexpr int U = 4;
+  for (int i = threadIdx.x * VEC; i < whole; i += kThreads * VEC * U) {
+    Vec<T, VEC> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = i + u * kThreads * VEC;
+      if (at < whole) v[u] = load_vec<T, VEC>(x + at);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * kThreads * VEC < whole) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          const float f = to_f32(v[u].v[k]);
+          any |= f != 0.f;
+          s[k & 3] = fmaf(f, f, s[k & 3]);
+        }
+      }
+  }
+  for (int i = whole + threadIdx.x; i < count; i += kThreads) {
+    const float f = to_f32(x[i]);
+    any |= f != 0.f;
+    s[0] = fmaf(f, f, s[0]);
+  }
+  const float t = (s[0] + s[1]) + (s[2] + s[3]);
+  if (!any) return 0.0;
+  if (t > 0x1p-90f && t < 0x1p126f) return (double)t;
+  // the thread's elements once more: the same ones as above
+  auto each = [&](auto f) {
+    for (int i = threadIdx.x * VEC; i < whole; i += kThreads * VEC)
+      for (int k = 0; k < VEC; ++k) f(to_f32(x[i + k]));
+    for (int i = whole + threadIdx.x; i < count; i += kThreads) f(to_f32(x[i]));
+  };
+  float big = 0.f;
+  bool nan = false;
+  each([&](float f) {
+    nan |= f != f;
+    big = fmaxf(big, fabsf(f));
+  });
+  if (nan) return (double)NAN;
+  if (isinf(big)) return (double)INFINITY;
+  int e;
+  frexpf(big, &e);
+  float p = 0.f;
+  each([&](float f) {
+    f = ldexpf(f, -e);
+    p = fmaf(f, f, p);
+  });
+  return ldexp((double)p, 2 * e);
+}
+
+template <typename T>
+__device__ __forceinline__ double squares_of(const Piece& pc) {
+  constexpr int W = 16 / sizeof(T);
+  const T* x = (const T*)pc.grad;
+  return ((uintptr_t)x & 15) == 0 ? squares<T, W>(x, pc.count) : squares<T, 1>(x, pc.count);
+}
+
+__device__ __forceinline__ double block_sum(double v, double* shared) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double t = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kThreads / 32; ++w) t += shared[w];
+  return t;                              // thread 0's
+}
+
+__global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const Piece* table, float* norm) {
+  __shared__ double shared[kThreads / 32];
+  __shared__ bool last;
+  if (h->magic != kMagic) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = NAN;
+    return;
+  }
+  double sum = 0.0;
+  for (long long i = blockIdx.x; i < h->pieces; i += kBlocks) {
+    const Piece pc = table[i];
+    sum += pc.dtype == DASH_BF16   ? squares_of<__nv_bfloat16>(pc)
+           : pc.dtype == DASH_FP16 ? squares_of<__half>(pc)
+                                   : squares_of<float>(pc);
+  }
+  const double mine = block_sum(sum, shared);
+  if (threadIdx.x == 0) {
+    h->totals[blockIdx.x] = mine;
+    __threadfence();
+    last = atomicAdd(&h->done, 1u) == kBlocks - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double v = 0.0;
+  for (int i = threadIdx.x; i < kBlocks; i += kThreads) v += __ldcg(&h->totals[i]);
+  const double all = block_sum(v, shared);
+  if (threadIdx.x == 0) {
+    const double n = sqrt(all);
+    h->norm = n;
+    *norm = (float)n;
+    h->done = 0;
+  }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void scale_piece(const T* x, T* y, int count, float f, bool copy) {
+  const int whole = count / VEC * VEC;
+  constexpr int U = 4;
+  for (int i = threadIdx.x * VEC; i < whole; i += kThreads * VEC * U) {
+    Vec<T, VEC> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = i + u * kThreads * VEC;
+      if (at < whole) v[u] = load_vec<T, VEC>(x + at);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = i + u * kThreads * VEC;
+      if (at < whole) {
+        if (!copy)
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) v[u].v[k] = from_f32<T>(to_f32(v[u].v[k]) * f);
+        store_vec<T, VEC>(y + at, v[u]);
+      }
+    }
+  }
+  for (int i = whole + threadIdx.x; i < count; i += kThreads)
+    y[i] = copy ? x[i] : from_f32<T>(to_f32(x[i]) * f);
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_of(const Piece& pc, float f, bool copy) {
+  constexpr int W = 16 / sizeof(T);
+  const T* x = (const T*)pc.grad;
+  T* y = (T*)pc.out;
+  if ((((uintptr_t)x | (uintptr_t)y) & 15) == 0) scale_piece<T, W>(x, y, pc.count, f, copy);
+  else scale_piece<T, 1>(x, y, pc.count, f, copy);
+}
+
+__global__ void __launch_bounds__(kThreads, 2) clip_scale_kernel(const Header* h, const Piece* table,
+                                                              float max_norm) {
+  if (h->magic != kMagic) return;
+  const double n = h->norm;
+  const bool copy = !(n > (double)max_norm) || isinf(n);
+  if (copy && h->all_in_place) return;
+  const float f = copy ? 1.f : (float)((double)max_norm / n);
+  for (long long i = h->pieces - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
+    const Piece pc = table[i];
+    if (copy && pc.out == pc.grad) continue;
+    if (pc.dtype == DASH_BF16) scale_of<__nv_bfloat16>(pc, f, copy);
+    else if (pc.dtype == DASH_FP16) scale_of<__half>(pc, f, copy);
+    else scale_of<float>(pc, f, copy);
+  }
+}
+
+// Number of pieces of a list, or a negative status.
+long long count_pieces(const dash_clip_tensor_t* t, int n) {
+  if (!t || n < 1) return -(long long)DASH_ERR_INVALID_ARG;
+  long long pieces = 0;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].numel < 0 || t[i].dtype < DASH_BF16 || t[i].dtype > DASH_FP32)
+      return -(long long)DASH_ERR_INVALID_ARG;
+    const uintptr_t e = t[i].dtype == DASH_FP32 ? 4 : 2;
+    if (t[i].numel > 0 && (!t[i].grad || !t[i].out)) return -(long long)DASH_ERR_INVALID_ARG;
+    if (!is_aligned(t[i].grad, e) || !is_aligned(t[i].out, e)) return -(long long)DASH_ERR_INVALID_ARG;
+    if (t[i].numel > (1ll << 46)) return -(long long)DASH_ERR_UNSUPPORTED;
+    pieces += ceil_div<long long>(t[i].numel, kPiece);
+    if (pieces > (1ll << 31)) return -(long long)DASH_ERR_UNSUPPORTED;
+  }
+  return pieces;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dash_grad_clip_plan_size(const dash_clip_tensor_t* tensors, int n) {
+  const long long pieces = count_pieces(tensors, n);
+  return pieces < 0 ? 0 : kTableOff + round_up_to((size_t)pieces * sizeof(Piece), 256);
+}
+
+dash_status_t dash_grad_clip_plan(const dash_clip_tensor_t* tensors, int n, void* plan,
+                                  size_t plan_bytes, cudaStream_t stream) {
+  const long long pieces = count_pieces(tensors, n);
+  if (pieces < 0) return (dash_status_t)-pieces;
+  if (!plan || !is_aligned(plan, 256)) return DASH_ERR_INVALID_ARG;
+  if (plan_bytes < kTableOff + (size_t)pieces * sizeof(Piece)) return DASH_ERR_WORKSPACE_TOO_SMALL;
+  try {
+    std::vector<Piece> table;
+    table.reserve(pieces);
+    Header h = {};
+    h.magic = kMagic;
+    h.pieces = pieces;
+    h.all_in_place = 1;
+    for (int i = 0; i < n; ++i) {
+      const size_t e = tensors[i].dtype == DASH_FP32 ? 4 : 2;
+      if (tensors[i].numel > 0 && tensors[i].grad != tensors[i].out) h.all_in_place = 0;
+      for (long long at = 0; at < tensors[i].numel; at += kPiece)
+        table.push_back({(const char*)tensors[i].grad + at * e, (char*)tensors[i].out + at * e,
+                         (int)std::min<long long>(kPiece, tensors[i].numel - at), tensors[i].dtype});
+    }
+    DASH_TRY(cudaMemcpyAsync(plan, &h, sizeof(h), cudaMemcpyHostToDevice, stream));
+    if (pieces > 0)
+      DASH_TRY(cudaMemcpyAsync((char*)plan + kTableOff, table.data(), table.size() * sizeof(Piece),
+                               cudaMemcpyHostToDevice, stream));
+    DASH_TRY(cudaStreamSynchronize(stream));
+  } catch (const std::exception& e) {
+    set_last_error(std::string("dash_grad_clip_plan: ") + e.what());
+    return DASH_ERR_UNSUPPORTED;
+  }
+  return DASH_OK;
+}
+
+dash_status_t dash_grad_clip(void* plan, float max_norm, float* norm, cudaStream_t stream) {
+  if (!plan || !norm || !is_aligned(plan, 256) || !is_aligned(norm, 4)) return DASH_ERR_INVALID_ARG;
+  if (!(max_norm >= 0.f)) return DASH_ERR_INVALID_ARG;
+  Header* h = (Header*)plan;
+  const Piece* table = (const Piece*)((char*)plan + kTableOff);
+  clip_norm_kernel<<<kBlocks, kThreads, 0, stream>>>(h, table, norm);
+  DASH_TRY(cudaGetLastError());
+  clip_scale_kernel<<<kBlocks, kThreads, 0, stream>>>(h, table, max_norm);
+  DASH_TRY(cudaGetLastError());
+  return DASH_OK;
+}
+
+}  // extern "C"

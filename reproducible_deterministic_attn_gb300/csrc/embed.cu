@@ -31,6 +31,7 @@ constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigitBits = 9;
+constexpr int kAheadStrips = 4;         // strips of 32 tokens a warp has in flight
 
 // ---- forward ------------------------------------------------------------------------------
 
@@ -56,15 +57,19 @@ __global__ void __launch_bounds__(kFwdThreads)
   for (int c = x * VEC; c < D; c += tx * VEC) {
     Vec<T, VEC> v[kFwdRows];
 #pragma unroll
-    for (int r = 0; r < kFwdRows; ++r)
+    for (int r = 0; r < kFwdRows; ++r) {
+      v[r] = {};
       if (id[r] >= 0) v[r] = load_vec<T, VEC>(table + id[r] * ld_table + c);
+    }
 #pragma unroll
     for (int r = 0; r < kFwdRows; ++r) {
       if (id[r] == -2) continue;
+      if (id[r] < 0 || scale != 1.f) {
+        float f[VEC];
+        unpack<T, VEC>(v[r], f);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        if (id[r] < 0) v[r].v[i] = from_f32<T>(NAN);
-        else if (scale != 1.f) v[r].v[i] = from_f32<T>(to_f32(v[r].v[i]) * scale);
+        for (int i = 0; i < VEC; ++i) f[i] = id[r] < 0 ? NAN : f[i] * scale;
+        v[r] = pack<T, VEC>(f);
       }
       store_vec<T, VEC>(out + (row0 + r * ty) * ld_out + c, v[r]);
     }
@@ -122,33 +127,48 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     };
     for (int d = lane; d < bins; d += 32) mine[d] = 0;
     __syncwarp();
-    for (long long s = first; s < last; ++s) {
-      const long long t = s * 32 + lane;
-      const bool in = t < a.T;
-      const unsigned live = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        const unsigned d = (key_at(t) >> shift) & (bins - 1);
-        const unsigned peers = __match_any_sync(live, d);
-        if ((peers & lt) == 0) mine[d] += __popc(peers);
+    for (long long s = first; s < last; s += kAheadStrips) {
+      unsigned key[kAheadStrips];
+#pragma unroll
+      for (int k = 0; k < kAheadStrips; ++k) {
+        const long long t = (s + k) * 32 + lane;
+        key[k] = s + k < last && t < a.T ? key_at(t) : 0;
       }
-      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kAheadStrips; ++k) {
+        const bool in = s + k < last && (s + k) * 32 + lane < a.T;
+        const unsigned live = __ballot_sync(0xffffffffu, in);
+        if (in) {
+          const unsigned d = (key[k] >> shift) & (bins - 1);
+          const unsigned peers = __match_any_sync(live, d);
+          if ((peers & lt) == 0) mine[d] += __popc(peers);
+        }
+        __syncwarp();
+      }
     }
     __syncthreads();
-    // counts -> offsets of the warps within the CTA, and the CTA's totals
-    for (int d = threadIdx.x; d < bins; d += kSortThreads) {
+    // counts -> offsets of the warps within the CTA, and the CTA's totals (bins <= threads)
+    const int d = threadIdx.x;
+    if (d < bins) {
       unsigned run = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const unsigned c = hist[w * bins + d];
-        hist[w * bins + d] = run;
-        run += c;
+#pragma unroll 1
+      for (int w0 = 0; w0 < kSortWarps; w0 += 8) {
+        unsigned c[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) c[w] = hist[(w0 + w) * bins + d];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          hist[(w0 + w) * bins + d] = run;
+          run += c[w];
+        }
       }
       cta_total[d] = run;
     }
     cluster.sync();
-    // offset of each digit over all CTAs (bins <= threads)
+    // offset of each digit over all CTAs
     unsigned lower = 0, total = 0;
-    const int d = threadIdx.x;
     if (d < bins) {
+#pragma unroll
       for (int c = 0; c < kSortCtas; ++c) {
         const unsigned v = *cluster.map_shared_rank(cta_total + d, c);
         if (c < rank) lower += v;
@@ -156,40 +176,53 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       }
     }
     unsigned scan = total;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned up = __shfl_up_sync(0xffffffffu, scan, o);
       if (lane >= o) scan += up;
     }
     if (lane == 31) warp_sums[warp] = scan;
     __syncthreads();
-    unsigned before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sums[w];
+    const unsigned before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0u);
     if (d < bins) base[d] = before + scan - total + lower;
     __syncthreads();
-    for (long long s = first; s < last; ++s) {
-      const long long t = s * 32 + lane;
-      const bool in = t < a.T;
-      const unsigned live = __ballot_sync(0xffffffffu, in);
-      unsigned key = 0, dg = 0, peers = 0;
-      if (in) {
-        key = key_at(t);
-        dg = (key >> shift) & (bins - 1);
-        peers = __match_any_sync(live, dg);
-        const unsigned at = base[dg] + mine[dg] + __popc(peers & lt);
-        kout[at] = key;
-        tout[at] = pass > 0 ? __ldcg(tin + t) : (unsigned)t;
-        if (pass == 0) {
-          if (key < a.V) {
-            atomicOr(a.present + (key >> 5), 1u << (key & 31));
-          } else {
-            const long long id = load_index(a.ids, t, a.id_bits);
-            if (id < 0 || id >= a.V) report_index(a.header, CHK_TOKEN_ID, t, id, a.V);
+    for (long long s = first; s < last; s += kAheadStrips) {
+      unsigned key[kAheadStrips], tok[kAheadStrips];
+#pragma unroll
+      for (int k = 0; k < kAheadStrips; ++k) {
+        const long long t = (s + k) * 32 + lane;
+        const bool in = s + k < last && t < a.T;
+        key[k] = in ? key_at(t) : 0;
+        tok[k] = in && pass > 0 ? __ldcg(tin + t) : (unsigned)t;
+      }
+#pragma unroll
+      for (int k = 0; k < kAheadStrips; ++k) {
+        const long long t = (s + k) * 32 + lane;
+        const bool in = s + k < last && t < a.T;
+        const unsigned live = __ballot_sync(0xffffffffu, in);
+        unsigned dg = 0, peers = 0;
+        if (in) {
+          dg = (key[k] >> shift) & (bins - 1);
+          peers = __match_any_sync(live, dg);
+          const unsigned at = base[dg] + mine[dg] + __popc(peers & lt);
+          kout[at] = key[k];
+          tout[at] = tok[k];
+          if (pass == 0) {
+            // the lowest of the lanes with one id sets its bit
+            const unsigned same = __match_any_sync(live, key[k]);
+            if (key[k] < a.V) {
+              if ((same & lt) == 0)
+                atomicOr(a.present + (key[k] >> 5), 1u << (key[k] & 31));
+            } else {
+              const long long id = load_index(a.ids, t, a.id_bits);
+              if (id < 0 || id >= a.V) report_index(a.header, CHK_TOKEN_ID, t, id, a.V);
+            }
           }
         }
+        __syncwarp();
+        if (in && (peers & lt) == 0) mine[dg] += __popc(peers);
+        __syncwarp();
       }
-      __syncwarp();
-      if (in && (peers & lt) == 0) mine[dg] += __popc(peers);
-      __syncwarp();
     }
     cluster.sync();   // the totals have been read; the sorted arrays are visible
   }
@@ -211,7 +244,54 @@ struct RowArgs {
 };
 
 constexpr int kRowThreads = 128;
-constexpr int kZeroRows = 64;           // table rows a zeroing block looks at
+constexpr int kZeroRows = 8;            // table rows a zeroing block looks at
+
+// A thread's columns of a row: VEC consecutive ones in whole 16-byte pieces, or four ones that
+// lie tx apart (STRIDED: rows that are no whole pieces), of which `n` are there.
+constexpr int kStridedCols = 4;
+template <typename T, int N, bool STRIDED>
+struct Cols;
+template <typename T, int N>
+struct Cols<T, N, false> {
+  Vec<T, N> v;
+  __device__ __forceinline__ void load(const T* p, int, int) { v = load_vec<T, N>(p); }
+  __device__ __forceinline__ void get(float (&f)[N]) const { unpack<T, N>(v, f); }
+  __device__ __forceinline__ void put(T* p, const float (&f)[N], int, int) const { store_f32<T, N>(p, f); }
+};
+template <typename T, int N>
+struct Cols<T, N, true> {
+  T v[N];
+  __device__ __forceinline__ void load(const T* p, int tx, int n) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < n ? p[i * tx] : from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = to_f32(v[i]);
+  }
+  __device__ __forceinline__ void put(T* p, const float (&f)[N], int tx, int n) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i * tx] = from_f32<T>(f[i]);
+  }
+};
+
+template <typename TO, int N, bool STRIDED>
+__device__ __forceinline__ void put_cols(TO* dst, const float (&acc)[N], float scale, int accumulate, int tx,
+                                         int n) {
+  Cols<TO, N, STRIDED> c;
+  float x[N];
+  if (accumulate) {
+    c.load(dst, tx, n);
+    c.get(x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = fmaf(acc[i], scale, x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = acc[i] * scale;
+  }
+  c.put(dst, x, tx, n);
+}
 
 template <typename TO, int VEC>
 __device__ __forceinline__ void put_row(TO* dst, const float (&acc)[VEC], float scale, int accumulate) {
@@ -227,22 +307,29 @@ __device__ __forceinline__ void put_row(TO* dst, const float (&acc)[VEC], float 
   store_f32<TO, VEC>(dst, x);
 }
 
-template <typename TI, typename TO, int VEC>
+template <typename TI, typename TO, bool STRIDED>
 __global__ void __launch_bounds__(kRowThreads)
     embed_rows_kernel(const TI* dout, TO* dtable, const RowArgs a) {
+  constexpr int N = STRIDED ? kStridedCols : 16 / sizeof(TI);
   const int x = threadIdx.x % a.tx, y = threadIdx.x / a.tx, ty = kRowThreads / a.tx;
+  const int tile = a.tx * N;                       // columns a team of tx threads covers
+  const int off = STRIDED ? x : x * N;
+  // columns of this thread's that are there, when its tile starts at column c
+  auto there = [&](int c) { return STRIDED ? min(N, (a.D - c - off + a.tx - 1) / a.tx) : N; };
   if (blockIdx.x >= a.run_blocks) {
     const long long v0 = (blockIdx.x - a.run_blocks) * kZeroRows;
-    float zero[VEC] = {};
+    const float zero[N] = {};
     for (long long v = v0 + y; v < min(a.V, v0 + kZeroRows); v += ty) {
       if ((__ldg(a.present + (v >> 5)) >> (v & 31)) & 1u) continue;
-      for (int c = x * VEC; c < a.D; c += a.tx * VEC) store_f32<TO, VEC>(dtable + v * a.D + c, zero);
+      for (int c = 0; c + off < a.D; c += tile)
+        put_cols<TO, N, STRIDED>(dtable + v * a.D + c + off, zero, 1.f, 0, a.tx, there(c));
     }
     return;
   }
   const long long run = (blockIdx.x / a.col_tiles) * (long long)ty + y;
-  const int col = ((int)(blockIdx.x % a.col_tiles) * a.tx + x) * VEC;
+  const int c0 = (int)(blockIdx.x % a.col_tiles) * tile, col = c0 + off;
   if (run >= a.runs || col >= a.D) return;
+  const int nc = there(c0);
   const long long p0 = run * kRun;
   const int n = (int)min((long long)kRun, a.T - p0);
   const unsigned V = (unsigned)a.V;
@@ -250,93 +337,115 @@ __global__ void __launch_bounds__(kRowThreads)
   const unsigned* toks = a.toks + p0;
   unsigned key = __ldg(keys);
   bool begun = run > 0 && __ldg(keys - 1) == key;
-  float acc[VEC] = {};
+  float acc[N] = {};
   constexpr int U = 8;
 #pragma unroll 1
   for (int p = 0; p < n && key < V; p += U) {
-    Vec<TI, VEC> v[U];
+    Cols<TI, N, STRIDED> v[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (p + i < n) v[i] = load_vec<TI, VEC>(dout + __ldg(toks + p + i) * a.ld_dout + col);
+    for (int i = 0; i < U; ++i) {
+      v[i] = {};
+      if (p + i < n) v[i].load(dout + __ldg(toks + p + i) * a.ld_dout + col, a.tx, nc);
+    }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (p + i < n && key < V) {
+        float f[N];
+        v[i].get(f);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] += to_f32(v[i].v[k]);
+        for (int k = 0; k < N; ++k) acc[k] += f[k];
         const bool more = p0 + p + i + 1 < a.T;
         const unsigned next = more ? __ldg(keys + p + i + 1) : 0xffffffffu;
         if (next != key || p + i + 1 == n) {
           const bool goes_on = next == key;
           if (!begun && !goes_on) {
-            put_row<TO, VEC>(dtable + (long long)key * a.D + col, acc, a.scale, a.accumulate);
+            put_cols<TO, N, STRIDED>(dtable + (long long)key * a.D + col, acc, a.scale, a.accumulate, a.tx, nc);
           } else {
-            store_f32<float, VEC>(a.part + (run * 2 + (begun ? 0 : 1)) * a.Dp + col, acc);
+            put_cols<float, N, STRIDED>(a.part + (run * 2 + (begun ? 0 : 1)) * a.Dp + col, acc, 1.f, 0, a.tx, nc);
           }
           begun = false;
           key = next;
 #pragma unroll
-          for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+          for (int k = 0; k < N; ++k) acc[k] = 0.f;
         }
       }
     }
   }
 }
 
-// One block for each run in which an id begins that goes on in the next, and 128 columns: 8
-// groups of 32 threads add an eighth of the following runs' parts each, in order; then the
-// eighths are added in order.
+// Joins the parts of the ids that cross runs. A block looks at 8 runs, a warp each: where an id
+// begins that goes on in the next run, the 8 groups of 32 threads add an eighth of the
+// following runs' parts each, in order, 4 columns a thread; then the eighths are added in
+// order.
 template <typename TO>
 __global__ void __launch_bounds__(256) embed_join_kernel(TO* dtable, const RowArgs a) {
-  const long long run = blockIdx.x;
-  const long long p0 = run * kRun;
-  if (p0 + kRun >= a.T) return;
-  const unsigned key = __ldg(a.keys + p0 + kRun - 1);
-  if (key >= (unsigned)a.V || __ldg(a.keys + p0 + kRun) != key) return;
-  if (run > 0 && __ldg(a.keys + p0 - 1) == key) return;   // begun in an earlier run
   __shared__ float4 sums[8][32];
+  __shared__ unsigned crossing[8];
+  __shared__ int follows[8];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  // the following runs that start with this id
-  long long follow = 1;
-  for (;;) {
-    const long long r = run + 1 + follow + lane;
-    const unsigned same = __ballot_sync(0xffffffffu, r < a.runs && __ldg(a.keys + r * kRun) == key);
-    if (same == 0xffffffffu) {
-      follow += 32;
-      continue;
+  {
+    const long long run = (long long)blockIdx.x * 8 + g, p0 = run * kRun;
+    // the run's last key, the next one and the one before the run, at once
+    unsigned k = 0xffffffffu;
+    if (p0 + kRun < a.T) {
+      if (lane == 0) k = __ldg(a.keys + p0 + kRun - 1);
+      if (lane == 1) k = __ldg(a.keys + p0 + kRun);
+      if (lane == 2 && run > 0) k = __ldg(a.keys + p0 - 1);
     }
-    follow += __ffs(~same) - 1;
-    break;
-  }
-  const int col = (blockIdx.y * 32 + lane) * 4;
-  const long long per = (follow + 7) / 8;
-  const long long end = min(follow, (g + 1) * per);
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (col < a.Dp) {
-#pragma unroll 4
-    for (long long r = g * per; r < end; ++r) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (run + 1 + r) * 2 * a.Dp + col));
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-  }
-  sums[g][lane] = s;
-  __syncthreads();
-  if (g == 0 && col < a.Dp) {
-    float4 t = __ldcg(reinterpret_cast<const float4*>(a.part + (run * 2 + 1) * a.Dp + col));
-    for (int k = 0; k < 8; ++k) {
-      t.x += sums[k][lane].x;
-      t.y += sums[k][lane].y;
-      t.z += sums[k][lane].z;
-      t.w += sums[k][lane].w;
-    }
-    const float v[4] = {t.x, t.y, t.z, t.w};
-    for (int i = 0; i < 4; ++i)
-      if (col + i < a.D) {
-        const float one[1] = {v[i]};
-        put_row<TO, 1>(dtable + (long long)key * a.D + col + i, one, a.scale, a.accumulate);
+    const unsigned key = __shfl_sync(0xffffffffu, k, 0);
+    const bool cross = key < (unsigned)a.V && __shfl_sync(0xffffffffu, k, 1) == key &&
+                       __shfl_sync(0xffffffffu, k, 2) != key;
+    int follow = 0;                                // the following runs that start with this id
+    if (cross) {
+      for (;;) {
+        const long long r = run + 1 + follow + lane;
+        const unsigned same = __ballot_sync(0xffffffffu, r < a.runs && __ldg(a.keys + r * kRun) == key);
+        follow += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+        if (same != 0xffffffffu) break;
       }
+    }
+    if (lane == 0) {
+      crossing[g] = key;
+      follows[g] = follow;
+    }
+  }
+  __syncthreads();
+  const int col = (blockIdx.y * 32 + lane) * 4;
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) {
+    const int follow = follows[j];
+    if (follow == 0) continue;
+    const long long run = (long long)blockIdx.x * 8 + j;
+    const int per = (follow + 7) / 8, end = min(follow, (g + 1) * per);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f), head = s;
+    if (col < a.Dp) {
+      if (g == 0) head = __ldcg(reinterpret_cast<const float4*>(a.part + (run * 2 + 1) * a.Dp + col));
+#pragma unroll 4
+      for (int r = g * per; r < end; ++r) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (run + 1 + r) * 2 * a.Dp + col));
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+    }
+    sums[g][lane] = s;
+    __syncthreads();
+    if (g == 0 && col < a.Dp) {
+      for (int k = 0; k < 8; ++k) {
+        head.x += sums[k][lane].x;
+        head.y += sums[k][lane].y;
+        head.z += sums[k][lane].z;
+        head.w += sums[k][lane].w;
+      }
+      const float v[4] = {head.x, head.y, head.z, head.w};
+      for (int i = 0; i < 4; ++i)
+        if (col + i < a.D) {
+          const float one[1] = {v[i]};
+          put_row<TO, 1>(dtable + (long long)crossing[j] * a.D + col + i, one, a.scale, a.accumulate);
+        }
+    }
+    __syncthreads();
   }
 }
 
@@ -402,21 +511,19 @@ template <typename TI, typename TO>
 dash_status_t rows_typed(const void* dout, void* dtable, RowArgs a, cudaStream_t stream) {
   constexpr int W = 16 / sizeof(TI);
   const bool wide = a.D % W == 0 && a.ld_dout % W == 0 && is_aligned(dout, 16) && is_aligned(dtable, 16);
-  const int vec = wide ? W : 1;
-  a.tx = pow2_lanes(ceil_div(a.D, vec), kRowThreads);
-  a.col_tiles = ceil_div(a.D, a.tx * vec);
+  const int per = wide ? W : kStridedCols;
+  a.tx = pow2_lanes(ceil_div(a.D, per), kRowThreads);
+  a.col_tiles = ceil_div(a.D, a.tx * per);
   a.run_blocks = ceil_div<long long>(a.runs, kRowThreads / a.tx) * a.col_tiles;
   const long long zero_blocks = a.accumulate ? 0 : ceil_div<long long>(a.V, kZeroRows);
   const long long blocks = a.run_blocks + zero_blocks;
   if (blocks >= (1ll << 31)) return DASH_ERR_UNSUPPORTED;
-  if (wide)
-    embed_rows_kernel<TI, TO, W><<<(unsigned)blocks, kRowThreads, 0, stream>>>((const TI*)dout, (TO*)dtable, a);
-  else
-    embed_rows_kernel<TI, TO, 1><<<(unsigned)blocks, kRowThreads, 0, stream>>>((const TI*)dout, (TO*)dtable, a);
+  if (wide) embed_rows_kernel<TI, TO, false><<<(unsigned)blocks, kRowThreads, 0, stream>>>((const TI*)dout, (TO*)dtable, a);
+  else embed_rows_kernel<TI, TO, true><<<(unsigned)blocks, kRowThreads, 0, stream>>>((const TI*)dout, (TO*)dtable, a);
   DASH_TRY(cudaGetLastError());
   if (a.runs > 1) {
-    embed_join_kernel<TO><<<dim3((unsigned)a.runs, (unsigned)ceil_div(a.Dp, 128)), 256, 0, stream>>>(
-        (TO*)dtable, a);
+    embed_join_kernel<TO><<<dim3((unsigned)ceil_div<long long>(a.runs, 8), (unsigned)ceil_div(a.Dp, 128)), 256, 0,
+                            stream>>>((TO*)dtable, a);
     DASH_TRY(cudaGetLastError());
   }
   return DASH_OK;

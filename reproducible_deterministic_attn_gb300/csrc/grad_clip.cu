@@ -22,6 +22,7 @@ using namespace dash::train;
 
 constexpr int kPiece = 32768;
 constexpr int kThreads = 512;
+constexpr int kAhead = 8;                // loads of 16 bytes a thread has in flight
 constexpr int kBlocks = 608;             // fixes the order of the sum: not the SM count
 constexpr unsigned long long kMagic = 0x64617368636c6970ull;
 
@@ -47,41 +48,45 @@ constexpr size_t kTableOff = (sizeof(Header) + 255) / 256 * 256;
 // the power of two that brings their largest to [1/2, 1).
 template <typename T, int VEC>
 __device__ __forceinline__ double squares(const T* x, int count) {
+  constexpr int kStep = kThreads * VEC;
   float s[4] = {};
-  bool any = false;
   const int whole = count / VEC * VEC;
-  constexpr int U = 4;
-  for (int i = threadIdx.x * VEC; i < whole; i += kThreads * VEC * U) {
-    Vec<T, VEC> v[U];
+  int i = threadIdx.x * VEC;
+#pragma unroll 1
+  for (; i + (kAhead - 1) * kStep < whole; i += kAhead * kStep) {
+    Vec<T, VEC> v[kAhead];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = i + u * kThreads * VEC;
-      if (at < whole) v[u] = load_vec<T, VEC>(x + at);
+    for (int u = 0; u < kAhead; ++u) v[u] = load_vec<T, VEC>(x + i + u * kStep);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float f[VEC];
+      unpack<T, VEC>(v[u], f);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) s[k & 3] = fmaf(f[k], f[k], s[k & 3]);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * kThreads * VEC < whole) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const float f = to_f32(v[u].v[k]);
-          any |= f != 0.f;
-          s[k & 3] = fmaf(f, f, s[k & 3]);
-        }
-      }
   }
-  for (int i = whole + threadIdx.x; i < count; i += kThreads) {
-    const float f = to_f32(x[i]);
-    any |= f != 0.f;
+#pragma unroll 1
+  for (; i < whole; i += kStep) {
+    float f[VEC];
+    load_f32<T, VEC>(x + i, f);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) s[k & 3] = fmaf(f[k], f[k], s[k & 3]);
+  }
+#pragma unroll 1
+  for (int j = whole + threadIdx.x; j < count; j += kThreads) {
+    const float f = to_f32(x[j]);
     s[0] = fmaf(f, f, s[0]);
   }
   const float t = (s[0] + s[1]) + (s[2] + s[3]);
-  if (!any) return 0.0;
   if (t > 0x1p-90f && t < 0x1p126f) return (double)t;
   // the thread's elements once more: the same ones as above
   auto each = [&](auto f) {
-    for (int i = threadIdx.x * VEC; i < whole; i += kThreads * VEC)
-      for (int k = 0; k < VEC; ++k) f(to_f32(x[i + k]));
-    for (int i = whole + threadIdx.x; i < count; i += kThreads) f(to_f32(x[i]));
+#pragma unroll 1
+    for (int j = threadIdx.x * VEC; j < whole; j += kStep)
+#pragma unroll 1
+      for (int k = 0; k < VEC; ++k) f(to_f32(x[j + k]));
+#pragma unroll 1
+    for (int j = whole + threadIdx.x; j < count; j += kThreads) f(to_f32(x[j]));
   };
   float big = 0.f;
   bool nan = false;
@@ -91,6 +96,7 @@ __device__ __forceinline__ double squares(const T* x, int count) {
   });
   if (nan) return (double)NAN;
   if (isinf(big)) return (double)INFINITY;
+  if (big == 0.f) return 0.0;
   int e;
   frexpf(big, &e);
   float p = 0.f;
@@ -127,8 +133,12 @@ __global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const
     return;
   }
   double sum = 0.0;
-  for (long long i = blockIdx.x; i < h->pieces; i += kBlocks) {
-    const Piece pc = table[i];
+  const long long pieces = h->pieces;
+  Piece next = {};
+  if (blockIdx.x < pieces) next = table[blockIdx.x];
+  for (long long i = blockIdx.x; i < pieces; i += kBlocks) {
+    const Piece pc = next;
+    if (i + kBlocks < pieces) next = table[i + kBlocks];
     sum += pc.dtype == DASH_BF16   ? squares_of<__nv_bfloat16>(pc)
            : pc.dtype == DASH_FP16 ? squares_of<__half>(pc)
                                    : squares_of<float>(pc);
@@ -154,29 +164,32 @@ __global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const
 }
 
 template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> scaled(const Vec<T, VEC>& v, float f, bool copy) {
+  float z[VEC];
+  unpack<T, VEC>(v, z);
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) z[k] *= f;
+  return copy ? v : pack<T, VEC>(z);
+}
+
+template <typename T, int VEC>
 __device__ __forceinline__ void scale_piece(const T* x, T* y, int count, float f, bool copy) {
+  constexpr int kStep = kThreads * VEC;
   const int whole = count / VEC * VEC;
-  constexpr int U = 4;
-  for (int i = threadIdx.x * VEC; i < whole; i += kThreads * VEC * U) {
-    Vec<T, VEC> v[U];
+  int i = threadIdx.x * VEC;
+#pragma unroll 1
+  for (; i + (kAhead - 1) * kStep < whole; i += kAhead * kStep) {
+    Vec<T, VEC> v[kAhead];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = i + u * kThreads * VEC;
-      if (at < whole) v[u] = load_vec<T, VEC>(x + at);
-    }
+    for (int u = 0; u < kAhead; ++u) v[u] = load_vec<T, VEC>(x + i + u * kStep);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = i + u * kThreads * VEC;
-      if (at < whole) {
-        if (!copy)
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) v[u].v[k] = from_f32<T>(to_f32(v[u].v[k]) * f);
-        store_vec<T, VEC>(y + at, v[u]);
-      }
-    }
+    for (int u = 0; u < kAhead; ++u) store_vec<T, VEC>(y + i + u * kStep, scaled<T, VEC>(v[u], f, copy));
   }
-  for (int i = whole + threadIdx.x; i < count; i += kThreads)
-    y[i] = copy ? x[i] : from_f32<T>(to_f32(x[i]) * f);
+#pragma unroll 1
+  for (; i < whole; i += kStep) store_vec<T, VEC>(y + i, scaled<T, VEC>(load_vec<T, VEC>(x + i), f, copy));
+#pragma unroll 1
+  for (int j = whole + threadIdx.x; j < count; j += kThreads)
+    y[j] = copy ? x[j] : from_f32<T>(to_f32(x[j]) * f);
 }
 
 template <typename T>
@@ -195,8 +208,12 @@ __global__ void __launch_bounds__(kThreads, 2) clip_scale_kernel(const Header* h
   const bool copy = !(n > (double)max_norm) || isinf(n);
   if (copy && h->all_in_place) return;
   const float f = copy ? 1.f : (float)((double)max_norm / n);
-  for (long long i = h->pieces - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
-    const Piece pc = table[i];
+  const long long first = h->pieces - 1 - blockIdx.x;
+  Piece next = {};
+  if (first >= 0) next = table[first];
+  for (long long i = first; i >= 0; i -= kBlocks) {
+    const Piece pc = next;
+    if (i >= kBlocks) next = table[i - kBlocks];
     if (copy && pc.out == pc.grad) continue;
     if (pc.dtype == DASH_BF16) scale_of<__nv_bfloat16>(pc, f, copy);
     else if (pc.dtype == DASH_FP16) scale_of<__half>(pc, f, copy);

@@ -20,9 +20,10 @@ using namespace dash::train;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 256;
-// Blocks of the backward that share the rows of one tensor: their number fixes how dw's sum
-// is split, so it is a constant and not the device's SM count.
-constexpr int kBwdBlocks = 608;
+// Blocks that share the rows. The backward's number fixes how dw's sum is split, so it is a
+// constant and not the device's SM count: one block for each that 152 SMs hold.
+constexpr int kFwdBlocks = 608 * 2;
+constexpr int kBwdBlocks = 304;
 
 struct Side {                       // queries or keys
   const void* x;
@@ -55,38 +56,65 @@ struct Angles {
   float c[IL ? 4 : 8], s[IL ? 4 : 8];
 };
 
-// Position of a token, -1 when it is out of range (reported by one lane of the warp).
-template <bool BWD>
-__device__ __forceinline__ long long position(const Args& a, int token) {
+// Position of a token, out of range or not.
+__device__ __forceinline__ long long load_position(const Args& a, int token) {
   const int b = token / a.S, s = token - b * a.S;
-  long long p = s;
-  if (a.pos) p = load_index(a.pos, b * a.pos_stride + s, a.id_bits);
-  if (p < 0 || p >= a.P) {
-    if ((threadIdx.x & 31) == 0) {
-      if (BWD) report_index(a.header, CHK_POSITION, token, p, a.P);
-      else if (a.status) *a.status = kStatusBounds;
-    }
-    return -1;
-  }
-  return p;
+  return a.pos ? load_index(a.pos, b * a.pos_stride + s, a.id_bits) : (long long)s;
 }
 
-template <bool IL>
+// -1 for a position out of range, which one lane of the warp reports.
+template <bool BWD>
+__device__ __forceinline__ long long check_position(const Args& a, int token, long long p) {
+  if (p >= 0 && p < a.P) return p;
+  if ((threadIdx.x & 31) == 0) {
+    if (BWD) report_index(a.header, CHK_POSITION, token, p, a.P);
+    else if (a.status) *a.status = kStatusBounds;
+  }
+  return -1;
+}
+
+__device__ __forceinline__ void four(const float* p, float* v) {
+  const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = x.x;
+  v[1] = x.y;
+  v[2] = x.z;
+  v[3] = x.w;
+}
+
+// FAST: a lane's columns are all rotated or none, and its angles are whole 16-byte pieces.
+template <bool IL, bool FAST>
 __device__ __forceinline__ void load_angles(const Args& a, long long p, int col, Angles<IL>& g) {
   const int half = a.R >> 1;
   constexpr int N = IL ? 4 : 8;
+  if (FAST) {
+    if (col < a.R && p >= 0) {
+      const long long at = p * half + (IL ? col >> 1 : col < half ? col : col - half);
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        four(a.cos + at + i, g.c + i);
+        four(a.sin + at + i, g.s + i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        g.c[i] = 1.f;      // a position out of range makes the norm NaN
+        g.s[i] = 0.f;
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int j = IL ? (col >> 1) + i : (col + i < half ? col + i : col + i - half);
-    const bool in = IL ? col + 2 * i < a.R : col + i < a.R;
-    g.c[i] = in ? (p < 0 ? NAN : __ldg(a.cos + p * half + j)) : 1.f;
-    g.s[i] = in ? (p < 0 ? NAN : __ldg(a.sin + p * half + j)) : 0.f;
+    const bool in = (IL ? col + 2 * i : col + i) < a.R && p >= 0;
+    g.c[i] = in ? __ldg(a.cos + p * half + j) : 1.f;
+    g.s[i] = in ? __ldg(a.sin + p * half + j) : 0.f;
   }
 }
 
 // Rotates the 8 values y of columns col.. (sign +1) or applies the transpose (sign -1).
-// FAST: pairs lie whole lanes apart (R / 2 a multiple of 8); else `partner(c)` gives the value
-// of column c.
+// Half-split pairs, FAST: they lie whole lanes apart (R / 2 a multiple of 8); else `partner(c)`
+// gives the value of column c.
 template <bool IL, bool FAST, typename F>
 __device__ __forceinline__ void rotate(const Args& a, const Angles<IL>& g, int col, float sign, float (&y)[8],
                                        F partner) {
@@ -128,52 +156,66 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
-// Forward. A warp takes one token and a group of U * 32 / L heads.
+__device__ __forceinline__ void load_weights(const float* w, int col, bool in, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 1.f;
+  if (w && in) {
+    four(w + col, v);
+    four(w + col + 4, v + 4);
+  }
+}
+
+// Forward. A warp walks over items of one token and U * 32 / L heads, the grid's warps apart.
+// The next item's position is fetched an item ahead, so that the angles' loads, which need
+// it, start together with the data's.
 template <typename T, int L, bool IL, bool FAST, int U>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args a) {
   constexpr int RW = 32 / L;                       // heads a warp handles at once
   const int which = blockIdx.x >= a.side[0].blocks;
   const Side& sd = a.side[which];
   const int lane = threadIdx.x & 31, sub = lane / L, col = (lane % L) * 8;
-  const int groups = (sd.H + U * RW - 1) / (U * RW);
-  const long long item = (long long)(blockIdx.x - (which ? a.side[0].blocks : 0)) * kWarps + (threadIdx.x >> 5);
-  if (item >= (long long)a.tokens * groups) return;
-  const int token = (int)(item / groups), h0 = (int)(item % groups) * U * RW + sub;
-  const int b = token / a.S, s = token - b * a.S;
+  const unsigned groups = (unsigned)(sd.H + U * RW - 1) / (U * RW), items = (unsigned)a.tokens * groups;
+  const unsigned step = (unsigned)sd.blocks * kWarps;
+  unsigned item = (blockIdx.x - (which ? a.side[0].blocks : 0)) * kWarps + (threadIdx.x >> 5);
+  if (item >= items) return;
   const bool in = col < a.D;
-  const T* x = (const T*)sd.x + b * sd.sb + s * sd.ss;
-  T* out = (T*)sd.out + b * sd.ob + s * sd.os;
-  Vec<T, 8> raw[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * RW;
-    if (in && h < sd.H) raw[u] = load_vec<T, 8>(x + h * sd.sh + col);
-  }
-  const long long p = position<false>(a, token);
-  Angles<IL> g;
-  load_angles<IL>(a, p, col, g);
-  float w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = in && sd.w ? __ldg(sd.w + col + i) : 1.f;
   const float inv_d = 1.f / a.D;
+  float w[8];
+  load_weights(sd.w, col, in, w);
+  long long next_p = load_position(a, (int)(item / groups));
+  for (; item < items; item += step) {
+    const int token = (int)(item / groups), h0 = (int)(item % groups) * U * RW + sub;
+    const int b = token / a.S, s = token - b * a.S;
+    const T* x = (const T*)sd.x + b * sd.sb + s * sd.ss;
+    T* out = (T*)sd.out + b * sd.ob + s * sd.os;
+    Vec<T, 8> raw[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * RW;
-    const bool live = in && h < sd.H;
-    float y[8], q = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[i] = live ? to_f32(raw[u].v[i]) : 0.f;
-      q = fmaf(y[i], y[i], q);
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * RW;
+      raw[u] = {};
+      if (in && h < sd.H) raw[u] = load_vec<T, 8>(x + h * sd.sh + col);
     }
-    const float r = p < 0 ? NAN : rsqrtf(lanes_sum<L>(q) * inv_d + a.eps);
+    const long long p = check_position<false>(a, token, next_p);
+    Angles<IL> g;
+    load_angles<IL, FAST>(a, p, col, g);
+    if (items - item > step) next_p = load_position(a, (int)((item + step) / groups));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
-    const T* row = x + (long long)h * sd.sh;
-    rotate<IL, FAST>(a, g, col, 1.f, y, [&](int c) {
-      return live ? to_f32(row[c]) * r * (sd.w ? __ldg(sd.w + c) : 1.f) : 0.f;
-    });
-    if (live) store_f32<T, 8>(out + h * sd.oh + col, y);
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * RW;
+      const bool live = in && h < sd.H;
+      float y[8], q = 0.f;
+      unpack<T, 8>(raw[u], y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q = fmaf(y[i], y[i], q);
+      const float r = p < 0 ? NAN : rsqrtf(lanes_sum<L>(q) * inv_d + a.eps);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
+      const T* row = x + (long long)h * sd.sh;
+      rotate<IL, FAST>(a, g, col, 1.f, y, [&](int c) {
+        return live ? to_f32(row[c]) * r * (sd.w ? __ldg(sd.w + c) : 1.f) : 0.f;
+      });
+      if (live) store_f32<T, 8>(out + h * sd.oh + col, y);
+    }
   }
 }
 
@@ -187,14 +229,15 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args a) {
   const Side& sd = a.side[which];
   const int block = blockIdx.x - (which ? a.side[0].blocks : 0);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L, col = (lane % L) * 8;
-  const int groups = (sd.H + U * RW - 1) / (U * RW);
-  const long long items = (long long)a.tokens * groups;
+  const unsigned groups = (unsigned)(sd.H + U * RW - 1) / (U * RW), items = (unsigned)a.tokens * groups;
+  const unsigned step = (unsigned)sd.blocks * kWarps;
   const bool in = col < a.D;
-  float w[8], dw[8] = {};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = in && sd.w ? __ldg(sd.w + col + i) : 1.f;
   const float inv_d = 1.f / a.D;
-  for (long long item = (long long)block * kWarps + warp; item < items; item += (long long)sd.blocks * kWarps) {
+  float w[8], dw[8] = {};
+  load_weights(sd.w, col, in, w);
+  unsigned item = (unsigned)block * kWarps + warp;
+  long long next_p = item < items ? load_position(a, (int)(item / groups)) : 0;
+  for (; item < items; item += step) {
     const int token = (int)(item / groups), h0 = (int)(item % groups) * U * RW + sub;
     const int b = token / a.S, s = token - b * a.S;
     const T* x = (const T*)sd.x + b * sd.sb + s * sd.ss;
@@ -204,25 +247,25 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * RW;
+      rx[u] = rd[u] = {};
       if (in && h < sd.H) {
         rx[u] = load_vec<T, 8>(x + h * sd.sh + col);
         rd[u] = load_vec<T, 8>(d + (long long)h * a.D + col);
       }
     }
-    const long long p = position<true>(a, token);
+    const long long p = check_position<true>(a, token, next_p);
     Angles<IL> g;
-    load_angles<IL>(a, p, col, g);
+    load_angles<IL, FAST>(a, p, col, g);
+    if (items - item > step) next_p = load_position(a, (int)((item + step) / groups));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * RW;
       const bool live = in && h < sd.H;
       float n[8], dy[8], q = 0.f;
+      unpack<T, 8>(rx[u], n);
+      unpack<T, 8>(rd[u], dy);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        n[i] = live ? to_f32(rx[u].v[i]) : 0.f;
-        dy[i] = live ? to_f32(rd[u].v[i]) : 0.f;
-        q = fmaf(n[i], n[i], q);
-      }
+      for (int i = 0; i < 8; ++i) q = fmaf(n[i], n[i], q);
       const float r = p < 0 ? NAN : rsqrtf(lanes_sum<L>(q) * inv_d + a.eps);
       rotate<IL, FAST>(a, g, col, -1.f, dy, [&](int c) {
         return live ? to_f32(d[(long long)h * a.D + c]) : 0.f;
@@ -256,14 +299,15 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args a) {
   }
 }
 
-// dw = the blocks' parts, added in order: 8 groups of blocks, then the groups.
+// dw = the blocks' parts, added in order: 32 groups of consecutive blocks, then the groups.
+// One block for each 32 columns of one tensor.
 __global__ void __launch_bounds__(1024) dw_join_kernel(const Args a) {
-  __shared__ float sums[8][128];
+  __shared__ float sums[32][33];
   const Side& sd = a.side[blockIdx.x];
   if (!sd.dw) return;
-  const int x = threadIdx.x & 127, g = threadIdx.x >> 7;
-  const int c = blockIdx.y * 128 + x;
-  const int per = (sd.blocks + 7) / 8;
+  const int x = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = blockIdx.y * 32 + x;
+  const int per = (sd.blocks + 31) / 32;
   const int end = min(sd.blocks, (g + 1) * per);
   float t = 0.f;
   if (c < a.D)
@@ -272,7 +316,7 @@ __global__ void __launch_bounds__(1024) dw_join_kernel(const Args a) {
   sums[g][x] = t;
   __syncthreads();
   if (g == 0 && c < a.D) {
-    for (int k = 1; k < 8; ++k) t += sums[k][x];
+    for (int k = 1; k < 32; ++k) t += sums[k][x];
     sd.dw[c] = t;
   }
 }
@@ -288,11 +332,12 @@ dash_status_t launch(Args a, bool bwd, cudaStream_t stream) {
   const long long rows = (long long)a.tokens * (a.side[0].H + a.side[1].H);
   const bool many = rows / (U * RW) >= 9728;
   const int per = many ? U * RW : RW;
+  // each tensor's share of the blocks goes by its heads
+  const int H = a.side[0].H + a.side[1].H, most = bwd ? kBwdBlocks : kFwdBlocks;
   for (int i = 0; i < 2; ++i) {
     const long long items = (long long)a.tokens * ceil_div(a.side[i].H, per);
-    long long blocks = ceil_div<long long>(items, kWarps);
-    if (bwd) blocks = std::min<long long>(blocks, kBwdBlocks);
-    a.side[i].blocks = (int)blocks;
+    const long long share = H > 0 ? std::max<long long>(1, ((long long)most * a.side[i].H + H / 2) / H) : 0;
+    a.side[i].blocks = (int)std::min<long long>(ceil_div<long long>(items, kWarps), share);
   }
   const unsigned grid = a.side[0].blocks + a.side[1].blocks;
   if (grid > 0) {
@@ -306,7 +351,7 @@ dash_status_t launch(Args a, bool bwd, cudaStream_t stream) {
     DASH_TRY(cudaGetLastError());
   }
   if (bwd && (a.side[0].dw || a.side[1].dw)) {
-    dw_join_kernel<<<dim3(2, ceil_div(a.D, 128)), 1024, 0, stream>>>(a);
+    dw_join_kernel<<<dim3(2, ceil_div(a.D, 32)), 1024, 0, stream>>>(a);
     DASH_TRY(cudaGetLastError());
   }
   return DASH_OK;
@@ -314,7 +359,8 @@ dash_status_t launch(Args a, bool bwd, cudaStream_t stream) {
 
 template <typename T, int L>
 dash_status_t by_pairs(const Args& a, bool bwd, bool interleaved, cudaStream_t stream) {
-  if (interleaved) return launch<T, L, true, true>(a, bwd, stream);
+  if (interleaved)
+    return a.R % 8 == 0 ? launch<T, L, true, true>(a, bwd, stream) : launch<T, L, true, false>(a, bwd, stream);
   if ((a.R / 2) % 8 == 0) return launch<T, L, false, true>(a, bwd, stream);
   return launch<T, L, false, false>(a, bwd, stream);
 }
@@ -431,7 +477,7 @@ dash_status_t dash_qk_norm_rope_fwd(const void* q, const void* k, const float* w
 
 size_t dash_qk_norm_rope_bwd_workspace_size(int B, int S, int Hq, int Hk, int D) {
   if (!shape_ok(B, S, Hq, Hk, D)) return 0;
-  return kWsHeaderBytes + round_up_to((size_t)2 * kBwdBlocks * D * sizeof(float), 256);
+  return kWsHeaderBytes + round_up_to((size_t)2 * (kBwdBlocks + 1) * D * sizeof(float), 256);
 }
 
 dash_status_t dash_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
@@ -469,7 +515,7 @@ dash_status_t dash_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
     sd.ob = os[i][0];
     sd.os = os[i][1];
     sd.oh = os[i][2];
-    sd.part = part + (size_t)i * kBwdBlocks * D;
+    sd.part = part + (size_t)i * (kBwdBlocks + 1) * D;
   }
   a.header = (int*)workspace;
   DASH_TRY(cudaMemsetAsync(workspace, 0, kWsHeaderBytes, stream));

@@ -5,11 +5,12 @@
 //   embed_sort  one cluster of 8 CTAs sorts the tokens by id: a stable counting sort by
 //               digits of at most 9 bits, so two passes up to 2^18 ids. Each warp counts a
 //               run of tokens of its own, so ranks within a digit follow the token order
-//               without atomics; the CTAs' counts meet in distributed shared memory.
+//               without atomics; the CTAs' counts meet in distributed shared memory. It is
+//               bound by latency (some 20 k cycles), so the launch's other clusters zero the
+//               whole table meanwhile; the rows of ids that occur are then stored over it.
 //   embed_rows  runs of 32 sorted places times column tiles: an id's rows are added in
 //               order in registers; ids that lie within one run are stored, the parts of
-//               those that cross runs go to the workspace. The same launch zeroes the rows
-//               of ids that do not occur (a bit for each id, set by the sort).
+//               those that cross runs go to the workspace.
 //   embed_join  adds the parts of the ids that cross runs, in order.
 #include <cooperative_groups.h>
 
@@ -31,6 +32,7 @@ constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigitBits = 9;
+constexpr size_t kFillBytes = 1 << 18;  // of the table that one CTA zeroes
 constexpr int kAheadStrips = 4;         // strips of 32 tokens a warp has in flight
 
 // ---- forward ------------------------------------------------------------------------------
@@ -84,10 +86,18 @@ struct SortArgs {
   long long T, V, padding_idx;
   int passes, digit_bits;
   int* header;
-  unsigned* present;          // bit v: id v occurs
-  long long present_words;
   unsigned *keys[2], *toks[2];   // the last pass writes index (passes - 1) & 1
+  char* fill;                 // bytes to zero (the table), of an even number and address
+  size_t fill_bytes;
 };
+
+// Zeroes [p, p + n) with `threads` threads, of which this is number `t`.
+__device__ __forceinline__ void zero_bytes(char* p, size_t n, size_t t, size_t threads) {
+  const size_t head = min(n, (size_t)(-(intptr_t)p & 15)), body = (n - head) / 16, tail = n - head - body * 16;
+  for (size_t i = t; i < body; i += threads) reinterpret_cast<uint4*>(p + head)[i] = make_uint4(0, 0, 0, 0);
+  if (t < head / 2) reinterpret_cast<uint16_t*>(p)[t] = 0;
+  if (t < tail / 2) reinterpret_cast<uint16_t*>(p + head + body * 16)[t] = 0;
+}
 
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads)
     embed_sort_kernel(const SortArgs a) {
@@ -102,9 +112,13 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned lt = (1u << lane) - 1;
 
-  for (long long i = (long long)rank * kSortThreads + threadIdx.x; i < a.present_words;
-       i += kSortCtas * kSortThreads)
-    a.present[i] = 0;
+  grid_next();
+  if (blockIdx.x >= kSortCtas) {
+    const size_t at = (size_t)(blockIdx.x - kSortCtas) * kFillBytes;
+    if (at < a.fill_bytes)
+      zero_bytes(a.fill + at, min(kFillBytes, a.fill_bytes - at), threadIdx.x, kSortThreads);
+    return;
+  }
   if (rank == 0 && threadIdx.x < kWsHeaderBytes / 4) a.header[threadIdx.x] = 0;
 
   // this warp's run of whole 32-token strips
@@ -125,15 +139,18 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       const long long id = load_index(a.ids, t, a.id_bits);
       return id < 0 || id >= a.V || id == a.padding_idx ? (unsigned)a.V : (unsigned)id;
     };
-    for (int d = lane; d < bins; d += 32) mine[d] = 0;
-    __syncwarp();
-    for (long long s = first; s < last; s += kAheadStrips) {
-      unsigned key[kAheadStrips];
+    auto load_strips = [&](long long s, unsigned (&key)[kAheadStrips]) {
 #pragma unroll
       for (int k = 0; k < kAheadStrips; ++k) {
         const long long t = (s + k) * 32 + lane;
         key[k] = s + k < last && t < a.T ? key_at(t) : 0;
       }
+    };
+    for (int d = lane; d < bins; d += 32) mine[d] = 0;
+    __syncwarp();
+    unsigned key[kAheadStrips];
+    for (long long s = first; s < last; s += kAheadStrips) {
+      load_strips(s, key);
 #pragma unroll
       for (int k = 0; k < kAheadStrips; ++k) {
         const bool in = s + k < last && (s + k) * 32 + lane < a.T;
@@ -187,13 +204,12 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     if (d < bins) base[d] = before + scan - total + lower;
     __syncthreads();
     for (long long s = first; s < last; s += kAheadStrips) {
-      unsigned key[kAheadStrips], tok[kAheadStrips];
+      unsigned tok[kAheadStrips];
+      if (last - first > kAheadStrips) load_strips(s, key);   // else they are still there
 #pragma unroll
       for (int k = 0; k < kAheadStrips; ++k) {
         const long long t = (s + k) * 32 + lane;
-        const bool in = s + k < last && t < a.T;
-        key[k] = in ? key_at(t) : 0;
-        tok[k] = in && pass > 0 ? __ldcg(tin + t) : (unsigned)t;
+        tok[k] = pass > 0 && s + k < last && t < a.T ? __ldcg(tin + t) : (unsigned)t;
       }
 #pragma unroll
       for (int k = 0; k < kAheadStrips; ++k) {
@@ -207,16 +223,9 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
           const unsigned at = base[dg] + mine[dg] + __popc(peers & lt);
           kout[at] = key[k];
           tout[at] = tok[k];
-          if (pass == 0) {
-            // the lowest of the lanes with one id sets its bit
-            const unsigned same = __match_any_sync(live, key[k]);
-            if (key[k] < a.V) {
-              if ((same & lt) == 0)
-                atomicOr(a.present + (key[k] >> 5), 1u << (key[k] & 31));
-            } else {
-              const long long id = load_index(a.ids, t, a.id_bits);
-              if (id < 0 || id >= a.V) report_index(a.header, CHK_TOKEN_ID, t, id, a.V);
-            }
+          if (pass == 0 && key[k] >= a.V) {
+            const long long id = load_index(a.ids, t, a.id_bits);
+            if (id < 0 || id >= a.V) report_index(a.header, CHK_TOKEN_ID, t, id, a.V);
           }
         }
         __syncwarp();
@@ -231,7 +240,7 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 // ---- the rows -----------------------------------------------------------------------------
 
 struct RowArgs {
-  const unsigned *keys, *toks, *present;
+  const unsigned *keys, *toks;
   long long T, V;
   int D;
   long long ld_dout;
@@ -240,11 +249,10 @@ struct RowArgs {
   float* part;                // [runs][2][Dp]: 0 = of an id begun in an earlier run, 1 = of one
   int Dp;                     //     that goes on in the next
   int tx, col_tiles;
-  long long runs, run_blocks;
+  long long runs;
 };
 
 constexpr int kRowThreads = 128;
-constexpr int kZeroRows = 8;            // table rows a zeroing block looks at
 
 // A thread's columns of a row: VEC consecutive ones in whole 16-byte pieces, or four ones that
 // lie tx apart (STRIDED: rows that are no whole pieces), of which `n` are there.
@@ -293,43 +301,19 @@ __device__ __forceinline__ void put_cols(TO* dst, const float (&acc)[N], float s
   c.put(dst, x, tx, n);
 }
 
-template <typename TO, int VEC>
-__device__ __forceinline__ void put_row(TO* dst, const float (&acc)[VEC], float scale, int accumulate) {
-  float x[VEC];
-  if (accumulate) {
-    load_f32<TO, VEC>(dst, x);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = fmaf(acc[i], scale, x[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = acc[i] * scale;
-  }
-  store_f32<TO, VEC>(dst, x);
-}
-
 template <typename TI, typename TO, bool STRIDED>
 __global__ void __launch_bounds__(kRowThreads)
     embed_rows_kernel(const TI* dout, TO* dtable, const RowArgs a) {
   constexpr int N = STRIDED ? kStridedCols : 16 / sizeof(TI);
+  grid_next();
+  grid_wait();
   const int x = threadIdx.x % a.tx, y = threadIdx.x / a.tx, ty = kRowThreads / a.tx;
   const int tile = a.tx * N;                       // columns a team of tx threads covers
   const int off = STRIDED ? x : x * N;
-  // columns of this thread's that are there, when its tile starts at column c
-  auto there = [&](int c) { return STRIDED ? min(N, (a.D - c - off + a.tx - 1) / a.tx) : N; };
-  if (blockIdx.x >= a.run_blocks) {
-    const long long v0 = (blockIdx.x - a.run_blocks) * kZeroRows;
-    const float zero[N] = {};
-    for (long long v = v0 + y; v < min(a.V, v0 + kZeroRows); v += ty) {
-      if ((__ldg(a.present + (v >> 5)) >> (v & 31)) & 1u) continue;
-      for (int c = 0; c + off < a.D; c += tile)
-        put_cols<TO, N, STRIDED>(dtable + v * a.D + c + off, zero, 1.f, 0, a.tx, there(c));
-    }
-    return;
-  }
   const long long run = (blockIdx.x / a.col_tiles) * (long long)ty + y;
   const int c0 = (int)(blockIdx.x % a.col_tiles) * tile, col = c0 + off;
   if (run >= a.runs || col >= a.D) return;
-  const int nc = there(c0);
+  const int nc = STRIDED ? min(N, (a.D - col + a.tx - 1) / a.tx) : N;   // columns that are there
   const long long p0 = run * kRun;
   const int n = (int)min((long long)kRun, a.T - p0);
   const unsigned V = (unsigned)a.V;
@@ -373,16 +357,39 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// Joins the parts of the ids that cross runs. A block looks at 8 runs, a warp each: where an id
-// begins that goes on in the next run, the 8 groups of 32 threads add an eighth of the
-// following runs' parts each, in order, 4 columns a thread; then the eighths are added in
-// order.
+__device__ __forceinline__ float4 part_at(const RowArgs& a, long long run, int slot, int col) {
+  return __ldcg(reinterpret_cast<const float4*>(a.part + (run * 2 + slot) * a.Dp + col));
+}
+__device__ __forceinline__ void add4(float4& s, const float4& v) {
+  s.x += v.x;
+  s.y += v.y;
+  s.z += v.z;
+  s.w += v.w;
+}
+template <typename TO>
+__device__ __forceinline__ void put4(TO* row, const float4& s, int col, const RowArgs& a) {
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + i < a.D) {
+      const float one[1] = {v[i]};
+      put_cols<TO, 1, false>(row + col + i, one, a.scale, a.accumulate, 1, 1);
+    }
+}
+
+// Joins the parts of the ids that cross runs. A block looks at 8 runs, a warp each, and 128
+// columns, 4 a thread. Where an id begins that goes on in the next run, the run's warp adds
+// the parts of the following runs in order when they are at most kShort; else the 8 warps add
+// an eighth of them each, in order, and then the eighths are added in order.
+constexpr int kShort = 4;
 template <typename TO>
 __global__ void __launch_bounds__(256) embed_join_kernel(TO* dtable, const RowArgs a) {
   __shared__ float4 sums[8][32];
   __shared__ unsigned crossing[8];
   __shared__ int follows[8];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int col = (blockIdx.y * 32 + lane) * 4;
+  grid_wait();
   {
     const long long run = (long long)blockIdx.x * 8 + g, p0 = run * kRun;
     // the run's last key, the next one and the one before the run, at once
@@ -403,6 +410,16 @@ __global__ void __launch_bounds__(256) embed_join_kernel(TO* dtable, const RowAr
         follow += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
         if (same != 0xffffffffu) break;
       }
+      if (follow <= kShort && col < a.Dp) {
+        float4 s = part_at(a, run, 1, col);
+        float4 v[kShort];
+#pragma unroll
+        for (int r = 0; r < kShort; ++r) v[r] = r < follow ? part_at(a, run + 1 + r, 0, col) : make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < kShort; ++r)
+          if (r < follow) add4(s, v[r]);
+        put4(dtable + (long long)key * a.D, s, col, a);
+      }
     }
     if (lane == 0) {
       crossing[g] = key;
@@ -410,40 +427,23 @@ __global__ void __launch_bounds__(256) embed_join_kernel(TO* dtable, const RowAr
     }
   }
   __syncthreads();
-  const int col = (blockIdx.y * 32 + lane) * 4;
 #pragma unroll 1
   for (int j = 0; j < 8; ++j) {
     const int follow = follows[j];
-    if (follow == 0) continue;
+    if (follow <= kShort) continue;
     const long long run = (long long)blockIdx.x * 8 + j;
     const int per = (follow + 7) / 8, end = min(follow, (g + 1) * per);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f), head = s;
     if (col < a.Dp) {
-      if (g == 0) head = __ldcg(reinterpret_cast<const float4*>(a.part + (run * 2 + 1) * a.Dp + col));
-#pragma unroll 4
-      for (int r = g * per; r < end; ++r) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (run + 1 + r) * 2 * a.Dp + col));
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
-      }
+      if (g == 0) head = part_at(a, run, 1, col);
+#pragma unroll 8
+      for (int r = g * per; r < end; ++r) add4(s, part_at(a, run + 1 + r, 0, col));
     }
     sums[g][lane] = s;
     __syncthreads();
     if (g == 0 && col < a.Dp) {
-      for (int k = 0; k < 8; ++k) {
-        head.x += sums[k][lane].x;
-        head.y += sums[k][lane].y;
-        head.z += sums[k][lane].z;
-        head.w += sums[k][lane].w;
-      }
-      const float v[4] = {head.x, head.y, head.z, head.w};
-      for (int i = 0; i < 4; ++i)
-        if (col + i < a.D) {
-          const float one[1] = {v[i]};
-          put_row<TO, 1>(dtable + (long long)crossing[j] * a.D + col + i, one, a.scale, a.accumulate);
-        }
+      for (int k = 0; k < 8; ++k) add4(head, sums[k][lane]);
+      put4(dtable + (long long)crossing[j] * a.D, head, col, a);
     }
     __syncthreads();
   }
@@ -465,12 +465,12 @@ int pow2_lanes(int need, int most) {
 }
 
 struct Layout {
-  size_t present, keys0, keys1, toks0, toks1, part, total;
+  size_t keys0, keys1, toks0, toks1, part, total;
   long long runs;
   int Dp;
 };
 
-Layout layout(long long T, long long V, int D) {
+Layout layout(long long T, int D) {
   Layout l;
   size_t at = kWsHeaderBytes;
   auto take = [&at](size_t bytes) {
@@ -480,7 +480,6 @@ Layout layout(long long T, long long V, int D) {
   };
   l.runs = ceil_div<long long>(T, kRun);
   l.Dp = (int)round_up_to(D, 8);
-  l.present = take((size_t)ceil_div<long long>(V, 32) * 4);
   l.keys0 = take((size_t)T * 4);
   l.keys1 = take((size_t)T * 4);
   l.toks0 = take((size_t)T * 4);
@@ -514,18 +513,14 @@ dash_status_t rows_typed(const void* dout, void* dtable, RowArgs a, cudaStream_t
   const int per = wide ? W : kStridedCols;
   a.tx = pow2_lanes(ceil_div(a.D, per), kRowThreads);
   a.col_tiles = ceil_div(a.D, a.tx * per);
-  a.run_blocks = ceil_div<long long>(a.runs, kRowThreads / a.tx) * a.col_tiles;
-  const long long zero_blocks = a.accumulate ? 0 : ceil_div<long long>(a.V, kZeroRows);
-  const long long blocks = a.run_blocks + zero_blocks;
+  const long long blocks = ceil_div<long long>(a.runs, kRowThreads / a.tx) * a.col_tiles;
   if (blocks >= (1ll << 31)) return DASH_ERR_UNSUPPORTED;
-  if (wide) embed_rows_kernel<TI, TO, false><<<(unsigned)blocks, kRowThreads, 0, stream>>>((const TI*)dout, (TO*)dtable, a);
-  else embed_rows_kernel<TI, TO, true><<<(unsigned)blocks, kRowThreads, 0, stream>>>((const TI*)dout, (TO*)dtable, a);
-  DASH_TRY(cudaGetLastError());
-  if (a.runs > 1) {
-    embed_join_kernel<TO><<<dim3((unsigned)ceil_div<long long>(a.runs, 8), (unsigned)ceil_div(a.Dp, 128)), 256, 0,
-                            stream>>>((TO*)dtable, a);
-    DASH_TRY(cudaGetLastError());
-  }
+  DASH_TRY(launch_after(wide ? embed_rows_kernel<TI, TO, false> : embed_rows_kernel<TI, TO, true>,
+                        dim3((unsigned)blocks), kRowThreads, 0, stream, (const TI*)dout, (TO*)dtable, a));
+  if (a.runs > 1)
+    DASH_TRY(launch_after(embed_join_kernel<TO>,
+                          dim3((unsigned)ceil_div<long long>(a.runs, 8), (unsigned)ceil_div(a.Dp, 128)), 256, 0,
+                          stream, (TO*)dtable, a));
   return DASH_OK;
 }
 
@@ -558,7 +553,7 @@ dash_status_t dash_embed_fwd(const void* table, const void* ids, void* out, int*
 }
 
 size_t dash_embed_bwd_workspace_size(long long T, long long V, int D) {
-  return sizes_ok(T, V, D) ? layout(T, V, D).total : 0;
+  return sizes_ok(T, V, D) ? layout(T, D).total : 0;
 }
 
 dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, void* workspace,
@@ -575,7 +570,7 @@ dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, vo
   if (!is_aligned(dout, elt_bytes(dout_dtype)) || !is_aligned(dtable, elt_bytes(dtable_dtype)) ||
       !is_aligned(ids, id_bits / 8) || !is_aligned(workspace, 256))
     return DASH_ERR_INVALID_ARG;
-  const Layout l = layout(T, V, D);
+  const Layout l = layout(T, D);
   if (workspace_bytes < l.total) return DASH_ERR_WORKSPACE_TOO_SMALL;
   char* ws = (char*)workspace;
   if (T == 0) {
@@ -594,8 +589,8 @@ dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, vo
   s.passes = ceil_div(bits, kMaxDigitBits);
   s.digit_bits = ceil_div(bits, s.passes);
   s.header = (int*)ws;
-  s.present = (unsigned*)(ws + l.present);
-  s.present_words = ceil_div<long long>(V, 32);
+  s.fill = (char*)dtable;
+  s.fill_bytes = accumulate ? 0 : (size_t)V * D * elt_bytes(dtable_dtype);
   s.keys[0] = (unsigned*)(ws + l.keys0);
   s.keys[1] = (unsigned*)(ws + l.keys1);
   s.toks[0] = (unsigned*)(ws + l.toks0);
@@ -603,12 +598,13 @@ dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, vo
   const size_t smem = ((size_t)(kSortWarps + 2) << s.digit_bits) * 4;
   DASH_TRY(cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)(((size_t)(kSortWarps + 2) << kMaxDigitBits) * 4)));
-  embed_sort_kernel<<<kSortCtas, kSortThreads, smem, stream>>>(s);
+  const size_t fillers = ceil_div<size_t>(s.fill_bytes, kFillBytes);
+  if (fillers >= (1ull << 31) - 64) return DASH_ERR_UNSUPPORTED;
+  embed_sort_kernel<<<(unsigned)(kSortCtas + round_up_to(fillers, kSortCtas)), kSortThreads, smem, stream>>>(s);
   DASH_TRY(cudaGetLastError());
   RowArgs a;
   a.keys = s.keys[(s.passes - 1) & 1];
   a.toks = s.toks[(s.passes - 1) & 1];
-  a.present = s.present;
   a.T = T;
   a.V = V;
   a.D = D;

@@ -1,6 +1,6 @@
 // Global gradient norm over many tensors and clipping (dash_grad_clip*).
 //
-// A plan is a device table of pieces of at most 32768 elements. clip_norm walks it with a
+// A plan is a device table of pieces of 4096 to 32768 elements. clip_norm walks it with a
 // fixed number of blocks: a thread sums the squares of its elements of a piece in fp32 and
 // adds the piece's sum to an fp64 total, a block's totals are added by a fixed tree, and the
 // last block to finish adds the blocks' totals in order (so the sum's order never depends on
@@ -20,7 +20,7 @@ namespace {
 using namespace dash;
 using namespace dash::train;
 
-constexpr int kPiece = 32768;
+constexpr int kMaxPiece = 32768, kMinPiece = 4096;
 constexpr int kThreads = 512;
 constexpr int kAhead = 8;                // loads of 16 bytes a thread has in flight
 constexpr int kBlocks = 608;             // fixes the order of the sum: not the SM count
@@ -36,6 +36,7 @@ static_assert(sizeof(Piece) == 24, "table layout");
 struct Header {
   unsigned long long magic;
   long long pieces;
+  int blocks;                            // that share the sum: min(pieces, kBlocks)
   int all_in_place;
   unsigned done;                         // blocks that have left their total; ends at 0
   double norm;
@@ -128,12 +129,15 @@ __device__ __forceinline__ double block_sum(double v, double* shared) {
 __global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const Piece* table, float* norm) {
   __shared__ double shared[kThreads / 32];
   __shared__ bool last;
+  grid_next();
   if (h->magic != kMagic) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = NAN;
     return;
   }
-  double sum = 0.0;
   const long long pieces = h->pieces;
+  const int blocks = h->blocks;
+  if (blockIdx.x >= blocks) return;
+  double sum = 0.0;
   Piece next = {};
   if (blockIdx.x < pieces) next = table[blockIdx.x];
   for (long long i = blockIdx.x; i < pieces; i += kBlocks) {
@@ -147,13 +151,13 @@ __global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const
   if (threadIdx.x == 0) {
     h->totals[blockIdx.x] = mine;
     __threadfence();
-    last = atomicAdd(&h->done, 1u) == kBlocks - 1;
+    last = atomicAdd(&h->done, 1u) == blocks - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
   double v = 0.0;
-  for (int i = threadIdx.x; i < kBlocks; i += kThreads) v += __ldcg(&h->totals[i]);
+  for (int i = threadIdx.x; i < blocks; i += kThreads) v += __ldcg(&h->totals[i]);
   const double all = block_sum(v, shared);
   if (threadIdx.x == 0) {
     const double n = sqrt(all);
@@ -203,6 +207,7 @@ __device__ __forceinline__ void scale_of(const Piece& pc, float f, bool copy) {
 
 __global__ void __launch_bounds__(kThreads, 2) clip_scale_kernel(const Header* h, const Piece* table,
                                                               float max_norm) {
+  grid_wait();
   if (h->magic != kMagic) return;
   const double n = h->norm;
   const bool copy = !(n > (double)max_norm) || isinf(n);
@@ -221,21 +226,24 @@ __global__ void __launch_bounds__(kThreads, 2) clip_scale_kernel(const Header* h
   }
 }
 
-// Number of pieces of a list, or a negative status.
-long long count_pieces(const dash_clip_tensor_t* t, int n) {
-  if (!t || n < 1) return -(long long)DASH_ERR_INVALID_ARG;
-  long long pieces = 0;
+// Checks a list; its number of pieces and their size, or a status. Pieces are halved while
+// there are too few for all blocks, so that few elements still spread over the chip.
+dash_status_t cut(const dash_clip_tensor_t* t, int n, long long* pieces, int* piece) {
+  if (!t || n < 1) return DASH_ERR_INVALID_ARG;
+  long long total = 0;
   for (int i = 0; i < n; ++i) {
-    if (t[i].numel < 0 || t[i].dtype < DASH_BF16 || t[i].dtype > DASH_FP32)
-      return -(long long)DASH_ERR_INVALID_ARG;
+    if (t[i].numel < 0 || t[i].dtype < DASH_BF16 || t[i].dtype > DASH_FP32) return DASH_ERR_INVALID_ARG;
     const uintptr_t e = t[i].dtype == DASH_FP32 ? 4 : 2;
-    if (t[i].numel > 0 && (!t[i].grad || !t[i].out)) return -(long long)DASH_ERR_INVALID_ARG;
-    if (!is_aligned(t[i].grad, e) || !is_aligned(t[i].out, e)) return -(long long)DASH_ERR_INVALID_ARG;
-    if (t[i].numel > (1ll << 46)) return -(long long)DASH_ERR_UNSUPPORTED;
-    pieces += ceil_div<long long>(t[i].numel, kPiece);
-    if (pieces > (1ll << 31)) return -(long long)DASH_ERR_UNSUPPORTED;
+    if (t[i].numel > 0 && (!t[i].grad || !t[i].out)) return DASH_ERR_INVALID_ARG;
+    if (!is_aligned(t[i].grad, e) || !is_aligned(t[i].out, e)) return DASH_ERR_INVALID_ARG;
+    if (t[i].numel > (1ll << 45) || total > (1ll << 45)) return DASH_ERR_UNSUPPORTED;
+    total += t[i].numel;
   }
-  return pieces;
+  *piece = kMaxPiece;
+  while (*piece > kMinPiece && total / *piece < kBlocks) *piece /= 2;
+  *pieces = 0;
+  for (int i = 0; i < n; ++i) *pieces += ceil_div<long long>(t[i].numel, *piece);
+  return *pieces > (1ll << 31) ? DASH_ERR_UNSUPPORTED : DASH_OK;
 }
 
 }  // namespace
@@ -243,14 +251,17 @@ long long count_pieces(const dash_clip_tensor_t* t, int n) {
 extern "C" {
 
 size_t dash_grad_clip_plan_size(const dash_clip_tensor_t* tensors, int n) {
-  const long long pieces = count_pieces(tensors, n);
-  return pieces < 0 ? 0 : kTableOff + round_up_to((size_t)pieces * sizeof(Piece), 256);
+  long long pieces;
+  int piece;
+  return cut(tensors, n, &pieces, &piece) != DASH_OK ? 0 : kTableOff + round_up_to((size_t)pieces * sizeof(Piece), 256);
 }
 
 dash_status_t dash_grad_clip_plan(const dash_clip_tensor_t* tensors, int n, void* plan,
                                   size_t plan_bytes, cudaStream_t stream) {
-  const long long pieces = count_pieces(tensors, n);
-  if (pieces < 0) return (dash_status_t)-pieces;
+  long long pieces;
+  int piece;
+  const dash_status_t st = cut(tensors, n, &pieces, &piece);
+  if (st != DASH_OK) return st;
   if (!plan || !is_aligned(plan, 256)) return DASH_ERR_INVALID_ARG;
   if (plan_bytes < kTableOff + (size_t)pieces * sizeof(Piece)) return DASH_ERR_WORKSPACE_TOO_SMALL;
   try {
@@ -259,13 +270,14 @@ dash_status_t dash_grad_clip_plan(const dash_clip_tensor_t* tensors, int n, void
     Header h = {};
     h.magic = kMagic;
     h.pieces = pieces;
+    h.blocks = (int)std::min<long long>(kBlocks, std::max<long long>(pieces, 1));
     h.all_in_place = 1;
     for (int i = 0; i < n; ++i) {
       const size_t e = tensors[i].dtype == DASH_FP32 ? 4 : 2;
       if (tensors[i].numel > 0 && tensors[i].grad != tensors[i].out) h.all_in_place = 0;
-      for (long long at = 0; at < tensors[i].numel; at += kPiece)
+      for (long long at = 0; at < tensors[i].numel; at += piece)
         table.push_back({(const char*)tensors[i].grad + at * e, (char*)tensors[i].out + at * e,
-                         (int)std::min<long long>(kPiece, tensors[i].numel - at), tensors[i].dtype});
+                         (int)std::min<long long>(piece, tensors[i].numel - at), tensors[i].dtype});
     }
     DASH_TRY(cudaMemcpyAsync(plan, &h, sizeof(h), cudaMemcpyHostToDevice, stream));
     if (pieces > 0)
@@ -286,8 +298,7 @@ dash_status_t dash_grad_clip(void* plan, float max_norm, float* norm, cudaStream
   const Piece* table = (const Piece*)((char*)plan + kTableOff);
   clip_norm_kernel<<<kBlocks, kThreads, 0, stream>>>(h, table, norm);
   DASH_TRY(cudaGetLastError());
-  clip_scale_kernel<<<kBlocks, kThreads, 0, stream>>>(h, table, max_norm);
-  DASH_TRY(cudaGetLastError());
+  DASH_TRY(launch_after(clip_scale_kernel, dim3(kBlocks), kThreads, 0, stream, h, table, max_norm));
   return DASH_OK;
 }
 

@@ -37,6 +37,25 @@ inline size_t round_up_to(size_t x, size_t a) { return (x + a - 1) / a * a; }
 template <typename T>
 inline T ceil_div(T a, T b) { return (a + b - 1) / b; }
 
+// Launches a kernel that may start while the kernel before it on `stream` is still running:
+// its blocks take their places as that one's leave, and wait for its results with
+// grid_wait() before they touch memory. The kernel before must have called grid_next().
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 }  // namespace dash
 
 #define DASH_TRY(call)                                          \

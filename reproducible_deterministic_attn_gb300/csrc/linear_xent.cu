@@ -105,7 +105,7 @@ dash_status_t check_args(const void* x, const void* w, const void* targets, cons
 }
 
 template <int OP>
-dash_status_t launch(Params p, const Maps& maps, int sms, cudaStream_t stream) {
+dash_status_t launch(Params p, const Maps& maps, int sms, bool first, cudaStream_t stream) {
   p.tiles_m = ceil_div(p.M, kTM);
   p.tiles_n = ceil_div(p.N, kTN);
   const long long units = (long long)p.tiles_m * p.tiles_n * p.splits;
@@ -115,8 +115,12 @@ dash_status_t launch(Params p, const Maps& maps, int sms, cudaStream_t stream) {
   }
   DASH_TRY(cudaFuncSetAttribute(gemm_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
   const int grid = (int)std::min<long long>(units, sms);
-  gemm_kernel<OP><<<grid, kXentThreads, kSmem, stream>>>(p, maps);
-  DASH_TRY(cudaGetLastError());
+  if (first) {
+    gemm_kernel<OP><<<grid, kXentThreads, kSmem, stream>>>(p, maps);
+    DASH_TRY(cudaGetLastError());
+  } else {
+    DASH_TRY(dash::launch_after(gemm_kernel<OP>, dim3(grid), kXentThreads, kSmem, stream, p, maps));
+  }
   return DASH_OK;
 }
 
@@ -175,11 +179,11 @@ dash_status_t dash_linear_xent_fwd(const void* x, const void* w, const void* tar
   p.header = (int*)ws;
   p.timeout_ns = dash::sync_timeout_ns();
   DASH_TRY(cudaMemsetAsync(ws, 0, dash::kWsHeaderBytes, stream));
-  st = launch<LSE>(p, maps, sms, stream);
+  st = launch<LSE>(p, maps, sms, true, stream);
   if (st != DASH_OK) return st;
-  lse_join_kernel<<<(unsigned)ceil_div<long long>(T, 32), 256, 0, stream>>>(
-      p.part, p.ztgt, 2 * ceil_div((int)V, kTN), (int)T, targets, id_bits, ignore_index, V, loss, lse, p.header);
-  DASH_TRY(cudaGetLastError());
+  DASH_TRY(dash::launch_after(lse_join_kernel, dim3((unsigned)ceil_div<long long>(T, 32)), 256, 0, stream, p.part,
+                              p.ztgt, 2 * ceil_div((int)V, kTN), (int)T, targets, id_bits, ignore_index, V, loss,
+                              lse, p.header));
   return DASH_OK;
 }
 
@@ -201,8 +205,8 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   if (st != DASH_OK) return st;
   char* ws = (char*)workspace;
   const size_t dw_elt = dw_dtype == DASH_FP32 ? 4 : 2;
-  DASH_TRY(cudaMemsetAsync(ws, 0, dash::kWsHeaderBytes, stream));
   if (T == 0) {
+    DASH_TRY(cudaMemsetAsync(ws, 0, dash::kWsHeaderBytes, stream));
     if (!accumulate) DASH_TRY(cudaMemsetAsync(dw, 0, (size_t)V * D * dw_elt, stream));
     return DASH_OK;
   }
@@ -226,7 +230,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   if (!map_2d(&grad.a, x, T, D, ldx, kTM) || !map_2d(&grad.b, w, V, D, ldw, kTN) ||
       !map_2d(&dxm.b, w, V, D, ldw, kTK) || !map_2d(&dwm.b, x, T, D, ldx, kTK))
     return bad_map();
-  check_targets_kernel<<<(unsigned)ceil_div<long long>(T, 256), 256, 0, stream>>>(
+  check_targets_kernel<<<1, 1024, 0, stream>>>(
       targets, id_bits, (int)T, ignore_index, V, base.header);
   DASH_TRY(cudaGetLastError());
   for (int i = 0; i < pl.pieces; ++i) {
@@ -240,7 +244,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     p.N = (int)vp;
     p.K = D;
     p.ksteps_per_split = ceil_div(D, kTK);
-    st = launch<GRAD>(p, grad, sms, stream);
+    st = launch<GRAD>(p, grad, sms, false, stream);
     if (st != DASH_OK) return st;
     // dX += G W
     p.N = D;
@@ -256,13 +260,12 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
       p.out_mode = OUT_PART;
       p.acc = (float*)(ws + pl.dx_part);
     }
-    st = launch<DX>(p, dxm, sms, stream);
+    st = launch<DX>(p, dxm, sms, false, stream);
     if (st != DASH_OK) return st;
     if (pl.dx_splits > 1) {
       const size_t n = (size_t)T * D;
-      dx_join_kernel<<<(unsigned)ceil_div<size_t>(n, 2048), 256, 0, stream>>>(
-          p.acc, p.splits, n, (float*)(ws + pl.acc), first, last, (__nv_bfloat16*)dx);
-      DASH_TRY(cudaGetLastError());
+      DASH_TRY(dash::launch_after(dx_join_kernel, dim3((unsigned)ceil_div<size_t>(n, 2048)), 256, 0, stream, p.acc,
+                                  p.splits, n, (float*)(ws + pl.acc), (int)first, (int)last, (__nv_bfloat16*)dx));
     }
     // dW of the piece = G^T X
     p.M = (int)vp;
@@ -273,7 +276,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     p.out = (char*)dw + (size_t)v0 * D * dw_elt;
     p.out_mode = dw_dtype == DASH_FP32 ? (accumulate ? OUT_F32_ADD : OUT_F32)
                                        : (accumulate ? OUT_BF16_ADD : OUT_BF16);
-    st = launch<DW>(p, dwm, sms, stream);
+    st = launch<DW>(p, dwm, sms, false, stream);
     if (st != DASH_OK) return st;
   }
   return DASH_OK;

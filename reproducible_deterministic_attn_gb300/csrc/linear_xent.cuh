@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kXentThreads, 1)
     gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   constexpr bool A_MN = OP == DW, B_MN = OP == DX || OP == DW;
   extern __shared__ uint8_t smem_xent[];
+  train::grid_next();
   uint8_t* sm = (uint8_t*)(((uintptr_t)smem_xent + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = (uint64_t*)(sm + kBarOff);
   uint32_t* tmem_slot = (uint32_t*)(sm + kBarOff + 8 * B_COUNT);
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(kXentThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  train::grid_wait();
 
   if (warp == 0) {
     // ===================================== TMA producer =====================================
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__(256) lse_join_kernel(const float2* part, const
                                                        long long ignore_index, long long V, float* loss,
                                                        float* lse, int* header) {
   __shared__ float2 runs[8][32];
+  train::grid_wait();
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int row = blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.f;
@@ -391,6 +394,8 @@ __global__ void __launch_bounds__(256) lse_join_kernel(const float2* part, const
 __global__ void __launch_bounds__(256) dx_join_kernel(const float* part, int splits, size_t n, float* acc,
                                                       int first, int last, __nv_bfloat16* dx) {
   const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  train::grid_next();
+  train::grid_wait();
   if (i >= n) return;
   float x[8] = {};
   if (!first) train::load_f32<float, 8>(acc + i, x);
@@ -404,14 +409,18 @@ __global__ void __launch_bounds__(256) dx_join_kernel(const float* part, int spl
   else train::store_f32<float, 8>(acc + i, x);
 }
 
-// Reports targets out of range (the backward treats them as ignored).
-__global__ void __launch_bounds__(256) check_targets_kernel(const void* targets, int id_bits, int T,
-                                                            long long ignore_index, long long V,
-                                                            int* header) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= T) return;
-  const long long y = train::load_index(targets, t, id_bits);
-  if (y != ignore_index && (y < 0 || y >= V)) train::report_index(header, CHK_TARGET, t, y, V);
+// Clears the header and reports targets out of range (the backward treats them as ignored).
+__global__ void __launch_bounds__(1024) check_targets_kernel(const void* targets, int id_bits, int T,
+                                                             long long ignore_index, long long V,
+                                                             int* header) {
+  train::grid_next();
+  if (threadIdx.x < kWsHeaderBytes / 4) header[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int t = threadIdx.x; t < T; t += 1024) {
+    const long long y = train::load_index(targets, t, id_bits);
+    if (y != ignore_index && (y < 0 || y >= V)) train::report_index(header, CHK_TARGET, t, y, V);
+  }
 }
 
 }  // namespace xent

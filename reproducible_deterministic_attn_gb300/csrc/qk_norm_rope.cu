@@ -24,6 +24,7 @@ constexpr int kMaxD = 256;
 // constant and not the device's SM count: one block for each that 152 SMs hold.
 constexpr int kFwdBlocks = 608 * 2;
 constexpr int kBwdBlocks = 304;
+static_assert(2 * (kBwdBlocks + 1) <= 1024, "dw_join looks at all blocks at once");
 
 struct Side {                       // queries or keys
   const void* x;
@@ -34,6 +35,7 @@ struct Side {                       // queries or keys
   long long ob, os, oh;             // strides of out
   float* dw;
   float* part;                      // backward: [blocks][D]
+  int* bad;                         // backward: [blocks], lowest token whose position is out of range
   int H;
   int blocks;                       // of the grid
 };
@@ -62,16 +64,7 @@ __device__ __forceinline__ long long load_position(const Args& a, int token) {
   return a.pos ? load_index(a.pos, b * a.pos_stride + s, a.id_bits) : (long long)s;
 }
 
-// -1 for a position out of range, which one lane of the warp reports.
-template <bool BWD>
-__device__ __forceinline__ long long check_position(const Args& a, int token, long long p) {
-  if (p >= 0 && p < a.P) return p;
-  if ((threadIdx.x & 31) == 0) {
-    if (BWD) report_index(a.header, CHK_POSITION, token, p, a.P);
-    else if (a.status) *a.status = kStatusBounds;
-  }
-  return -1;
-}
+constexpr int kNoToken = 0x7fffffff;
 
 __device__ __forceinline__ void four(const float* p, float* v) {
   const float4 x = __ldg(reinterpret_cast<const float4*>(p));
@@ -86,7 +79,7 @@ template <bool IL, bool FAST>
 __device__ __forceinline__ void load_angles(const Args& a, long long p, int col, Angles<IL>& g) {
   const int half = a.R >> 1;
   constexpr int N = IL ? 4 : 8;
-  if (FAST) {
+  if constexpr (FAST) {
     if (col < a.R && p >= 0) {
       const long long at = p * half + (IL ? col >> 1 : col < half ? col : col - half);
 #pragma unroll
@@ -101,14 +94,14 @@ __device__ __forceinline__ void load_angles(const Args& a, long long p, int col,
         g.s[i] = 0.f;
       }
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int j = IL ? (col >> 1) + i : (col + i < half ? col + i : col + i - half);
-    const bool in = (IL ? col + 2 * i : col + i) < a.R && p >= 0;
-    g.c[i] = in ? __ldg(a.cos + p * half + j) : 1.f;
-    g.s[i] = in ? __ldg(a.sin + p * half + j) : 0.f;
+    for (int i = 0; i < N; ++i) {
+      const int j = IL ? (col >> 1) + i : (col + i < half ? col + i : col + i - half);
+      const bool in = (IL ? col + 2 * i : col + i) < a.R && p >= 0;
+      g.c[i] = in ? __ldg(a.cos + p * half + j) : 1.f;
+      g.s[i] = in ? __ldg(a.sin + p * half + j) : 0.f;
+    }
   }
 }
 
@@ -195,7 +188,11 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args a) {
       raw[u] = {};
       if (in && h < sd.H) raw[u] = load_vec<T, 8>(x + h * sd.sh + col);
     }
-    const long long p = check_position<false>(a, token, next_p);
+    long long p = next_p;
+    if (p < 0 || p >= a.P) {
+      p = -1;
+      if (a.status) *a.status = kStatusBounds;
+    }
     Angles<IL> g;
     load_angles<IL, FAST>(a, p, col, g);
     if (items - item > step) next_p = load_position(a, (int)((item + step) / groups));
@@ -225,6 +222,10 @@ template <typename T, int L, bool IL, bool FAST, int U>
 __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args a) {
   constexpr int RW = 32 / L;
   __shared__ float dws[kWarps][kMaxD];
+  __shared__ int bad;
+  grid_next();
+  if (threadIdx.x == 0) bad = kNoToken;
+  __syncthreads();
   const int which = blockIdx.x >= a.side[0].blocks;
   const Side& sd = a.side[which];
   const int block = blockIdx.x - (which ? a.side[0].blocks : 0);
@@ -253,7 +254,11 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args a) {
         rd[u] = load_vec<T, 8>(d + (long long)h * a.D + col);
       }
     }
-    const long long p = check_position<true>(a, token, next_p);
+    long long p = next_p;
+    if (p < 0 || p >= a.P) {
+      p = -1;
+      if (lane == 0) atomicMin(&bad, token);
+    }
     Angles<IL> g;
     load_angles<IL, FAST>(a, p, col, g);
     if (items - item > step) next_p = load_position(a, (int)((item + step) / groups));
@@ -297,13 +302,37 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args a) {
     for (int k = 0; k < kWarps; ++k) t += dws[k][c];
     sd.part[(long long)block * a.D + c] = t;
   }
+  if (threadIdx.x == 0) sd.bad[block] = bad;
 }
 
 // dw = the blocks' parts, added in order: 32 groups of consecutive blocks, then the groups.
-// One block for each 32 columns of one tensor.
+// One block for each 32 columns of one tensor; the first also writes the call's status.
 __global__ void __launch_bounds__(1024) dw_join_kernel(const Args a) {
   __shared__ float sums[32][33];
+  __shared__ int first;
+  grid_wait();
   const Side& sd = a.side[blockIdx.x];
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (threadIdx.x == 0) first = kNoToken;
+    __syncthreads();
+    const int n = a.side[0].blocks, b = threadIdx.x;      // at most 1024 blocks
+    if (b < n + a.side[1].blocks) {
+      const int t = b < n ? a.side[0].bad[b] : a.side[1].bad[b - n];
+      if (t != kNoToken) atomicMin(&first, t);
+    }
+    __syncthreads();
+    if (threadIdx.x < kWsHeaderBytes / 4) {
+      int v = 0;
+      if (first != kNoToken) {
+        if (threadIdx.x == WS_STATUS) v = kStatusBounds;
+        if (threadIdx.x == WS_BH) v = first;
+        if (threadIdx.x == WS_QTILE) v = CHK_POSITION;
+        if (threadIdx.x == WS_EXPECT) v = (int)load_position(a, first);
+        if (threadIdx.x == WS_SEEN) v = (int)a.P;
+      }
+      a.header[threadIdx.x] = v;
+    }
+  }
   if (!sd.dw) return;
   const int x = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.y * 32 + x;
@@ -350,10 +379,7 @@ dash_status_t launch(Args a, bool bwd, cudaStream_t stream) {
     }
     DASH_TRY(cudaGetLastError());
   }
-  if (bwd && (a.side[0].dw || a.side[1].dw)) {
-    dw_join_kernel<<<dim3(2, ceil_div(a.D, 32)), 1024, 0, stream>>>(a);
-    DASH_TRY(cudaGetLastError());
-  }
+  if (bwd) DASH_TRY(launch_after(dw_join_kernel, dim3(2, ceil_div(a.D, 32)), 1024, 0, stream, a));
   return DASH_OK;
 }
 
@@ -477,7 +503,7 @@ dash_status_t dash_qk_norm_rope_fwd(const void* q, const void* k, const float* w
 
 size_t dash_qk_norm_rope_bwd_workspace_size(int B, int S, int Hq, int Hk, int D) {
   if (!shape_ok(B, S, Hq, Hk, D)) return 0;
-  return kWsHeaderBytes + round_up_to((size_t)2 * (kBwdBlocks + 1) * D * sizeof(float), 256);
+  return kWsHeaderBytes + round_up_to((size_t)2 * (kBwdBlocks + 1) * (D + 1) * sizeof(float), 256);
 }
 
 dash_status_t dash_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
@@ -516,9 +542,9 @@ dash_status_t dash_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
     sd.os = os[i][1];
     sd.oh = os[i][2];
     sd.part = part + (size_t)i * (kBwdBlocks + 1) * D;
+    sd.bad = (int*)(part + (size_t)2 * (kBwdBlocks + 1) * D) + i * (kBwdBlocks + 1);
   }
   a.header = (int*)workspace;
-  DASH_TRY(cudaMemsetAsync(workspace, 0, kWsHeaderBytes, stream));
   return by_type(a, true, interleaved != 0, dtype, stream);
 }
 

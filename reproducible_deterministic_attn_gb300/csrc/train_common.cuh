@@ -10,6 +10,12 @@
 namespace dash {
 namespace train {
 
+// Kernels of one call overlap their starts: each lets the next one's blocks take their places
+// once all of its own run (grid_next), and each but the first waits for the memory of those
+// before it (grid_wait) before it reads or writes any.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

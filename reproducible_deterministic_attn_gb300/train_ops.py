@@ -11,6 +11,7 @@ to dash_attn_get_status(workspace).
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -54,36 +55,68 @@ _core._SIGNATURES.update({
 })
 
 
+# The checks below run on every call, next to kernels of a few microseconds: conditions first,
+# messages only once one has failed.
+
 def _raise(status: int, where: str):
     if status:
         raise DashError(status, where)
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+def _bad(what: str):
+    raise ValueError(what)
+
+
+def _stream(t, stream) -> int:
+    """The raw handle of `stream`, or of torch's current stream on t's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return _core._stream(t, stream)
 
 
 def _cuda(t, name: str, device=None):
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name}: expected a CUDA tensor")
-    _need(device is None or t.device == device, f"{name}: expected a tensor on {device}")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _bad(f"{name}: expected a CUDA tensor")
+    if device is not None and t.device != device:
+        _bad(f"{name}: expected a tensor on {device}")
 
 
 def _rows(t, name: str):
     """A 2-D tensor whose rows are contiguous; returns the elements between rows."""
-    _need(t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1),
-          f"{name}: expected 2-D rows of contiguous elements")
+    if t.dim() != 2 or (t.shape[1] != 1 and t.stride(1) != 1):
+        _bad(f"{name}: expected 2-D rows of contiguous elements")
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
 def _index(t, name: str, device):
     _cuda(t, name, device)
-    _need(t.dtype in _ID_BITS and t.is_contiguous(), f"{name}: expected contiguous int32 or int64")
-    return _ID_BITS[t.dtype]
+    bits = _ID_BITS.get(t.dtype)
+    if bits is None or not t.is_contiguous():
+        _bad(f"{name}: expected contiguous int32 or int64")
+    return bits
 
 
-def _ws(workspace, name: str = "workspace"):
-    _need(workspace.is_cuda and workspace.is_contiguous(), f"{name}: expected a contiguous CUDA tensor")
+def _vector(t, name: str, n: int, device):
+    """A contiguous fp32 [n] tensor's address."""
+    _cuda(t, name, device)
+    if t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
+        _bad(f"{name}: expected contiguous float32 [{n}]")
+    return t.data_ptr()
+
+
+def _status_word(t, device):
+    if t is None:
+        return None
+    _cuda(t, "status", device)
+    if t.dtype != torch.int32 or t.numel() != 1:
+        _bad("status: expected one int32")
+    return t.data_ptr()
+
+
+def _ws(workspace, device):
+    _cuda(workspace, "workspace", device)
+    if not workspace.is_contiguous():
+        _bad("workspace: expected contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -101,23 +134,21 @@ def embed_forward(table, ids, scale: float = 1.0, out=None, status=None, stream=
     any shape. status: an optional int32 CUDA tensor of one element, which reads
     DASH_ERR_BOUNDS when an id was out of range (its row is NaN). Returns [*ids.shape, D]."""
     _cuda(table, "table")
-    _need(table.dtype in _DTYPE, "table: expected bfloat16, float16 or float32")
+    dtype, dev = table.dtype, table.device
+    if dtype not in _DTYPE:
+        _bad("table: expected bfloat16, float16 or float32")
     ld = _rows(table, "table")
-    bits = _index(ids, "ids", table.device)
+    bits = _index(ids, "ids", dev)
     V, D = table.shape
     if out is None:
-        out = torch.empty(*ids.shape, D, dtype=table.dtype, device=table.device)
+        out = torch.empty((*ids.shape, D), dtype=dtype, device=dev)
     else:
-        _cuda(out, "out", table.device)
-        _need(out.dtype == table.dtype and tuple(out.shape) == (*ids.shape, D) and out.is_contiguous(),
-              "out: expected contiguous [*ids.shape, D] of the table's type")
-    if status is not None:
-        _cuda(status, "status", table.device)
-        _need(status.dtype == torch.int32 and status.numel() == 1, "status: expected one int32")
+        _cuda(out, "out", dev)
+        if out.dtype != dtype or out.shape != (*ids.shape, D) or not out.is_contiguous():
+            _bad("out: expected contiguous [*ids.shape, D] of the table's type")
     _raise(_core.load().dash_embed_fwd(
-        table.data_ptr(), ids.data_ptr(), out.data_ptr(), None if status is None else status.data_ptr(),
-        ids.numel(), V, D, ld, D, scale, _DTYPE[table.dtype], bits, _core._stream(table, stream)),
-        "dash_embed_fwd")
+        table.data_ptr(), ids.data_ptr(), out.data_ptr(), _status_word(status, dev), ids.numel(), V, D, ld, D,
+        scale, _DTYPE[dtype], bits, _stream(table, stream)), "dash_embed_fwd")
     return out
 
 
@@ -141,30 +172,36 @@ def embed_backward(dout, ids, vocab: int, scale: float = 1.0, padding_idx=None, 
     an id whose tokens are left out. dtable: an optional contiguous [vocab, D] tensor of
     dout's type or fp32 to write to, or to add to with accumulate=True. Returns dtable."""
     _cuda(dout, "dout")
-    _need(dout.dtype in _DTYPE, "dout: expected bfloat16, float16 or float32")
-    bits = _index(ids, "ids", dout.device)
-    _need(dout.dim() >= 1 and tuple(dout.shape[:-1]) == tuple(ids.shape), "dout: expected [*ids.shape, D]")
+    dtype, dev = dout.dtype, dout.device
+    if dtype not in _DTYPE:
+        _bad("dout: expected bfloat16, float16 or float32")
+    bits = _index(ids, "ids", dev)
+    if dout.dim() < 1 or dout.shape[:-1] != ids.shape:
+        _bad("dout: expected [*ids.shape, D]")
     T, D = ids.numel(), dout.shape[-1]
     if dout.dim() == 2:
         ld = _rows(dout, "dout")
     else:
-        _need(dout.is_contiguous(), "dout: expected contiguous")
+        if not dout.is_contiguous():
+            _bad("dout: expected contiguous")
         ld = D
     if dtable is None:
-        _need(not accumulate, "accumulate: needs dtable")
-        dtable = torch.empty((vocab, D), dtype=dout.dtype, device=dout.device)
+        if accumulate:
+            _bad("accumulate: needs dtable")
+        dtable = torch.empty((vocab, D), dtype=dtype, device=dev)
     else:
-        _cuda(dtable, "dtable", dout.device)
-        _need(dtable.dtype in (dout.dtype, torch.float32) and tuple(dtable.shape) == (vocab, D)
-              and dtable.is_contiguous(), "dtable: expected contiguous [vocab, D] of dout's type or float32")
-    _need(padding_idx is None or 0 <= padding_idx < vocab, "padding_idx: out of range")
+        _cuda(dtable, "dtable", dev)
+        if dtable.dtype not in (dtype, torch.float32) or dtable.shape != (vocab, D) or not dtable.is_contiguous():
+            _bad("dtable: expected contiguous [vocab, D] of dout's type or float32")
+    if padding_idx is not None and not 0 <= padding_idx < vocab:
+        _bad("padding_idx: out of range")
     if workspace is None:
-        workspace = new_embed_workspace(T, vocab, D, dout.device)
-    ws, nbytes = _ws(workspace)
+        workspace = new_embed_workspace(T, vocab, D, dev)
+    ws, nbytes = _ws(workspace, dev)
     _raise(_core.load().dash_embed_bwd(
         dout.data_ptr(), ids.data_ptr(), dtable.data_ptr(), ws, nbytes, T, vocab, D, ld, scale,
-        -1 if padding_idx is None else padding_idx, int(accumulate), _DTYPE[dout.dtype],
-        _DTYPE[dtable.dtype], bits, _core._stream(dout, stream)), "dash_embed_bwd")
+        -1 if padding_idx is None else padding_idx, int(accumulate), _DTYPE[dtype], _DTYPE[dtable.dtype], bits,
+        _stream(dout, stream)), "dash_embed_bwd")
     _finish(workspace, stream, check, "dash_embed_bwd")
     return dtable
 
@@ -179,44 +216,49 @@ def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, device="c
     return ang.cos().float(), ang.sin().float()
 
 
-def _heads(t, name: str, like=None):
-    """[B, S, H, D] with contiguous D; returns its {batch, token, head} strides. Strides of
+@functools.lru_cache(maxsize=1024)
+def _strides(batch: int, token: int, head: int):
+    return _c3(batch, token, head)
+
+
+def _heads(t, name: str):
+    """[B, S, H, D] with contiguous D: its sizes and its {batch, token, head} strides. Strides of
     dimensions of one element are never used and count as zero."""
-    _need(t.dim() == 4 and (t.shape[3] == 1 or t.stride(3) == 1), f"{name}: expected [B, S, H, D], D contiguous")
-    if like is not None:
-        _need(t.dtype == like.dtype and t.device == like.device and t.shape[:2] == like.shape[:2]
-              and t.shape[3] == like.shape[3], f"{name}: expected the type, device and [B, S, ., D] of q")
-    n, st = t.shape, t.stride()
-    return _c3(st[0] if n[0] > 1 else 0, st[1] if n[1] > 1 else 0, st[2] if n[2] > 1 else 0)
+    if t.dim() != 4 or (t.shape[3] != 1 and t.stride(3) != 1):
+        _bad(f"{name}: expected [B, S, H, D], D contiguous")
+    B, S, H, D = t.shape
+    sb, ss, sh, _ = t.stride()
+    return B, S, H, D, _strides(sb if B > 1 else 0, ss if S > 1 else 0, sh if H > 1 else 0)
 
 
 def _qk_args(q, k, wq, wk, cos, sin, positions):
+    dev = q.device
     _cuda(q, "q")
-    _cuda(k, "k", q.device)
-    _need(q.dtype in _DTYPE, "q: expected bfloat16, float16 or float32")
-    qs, ks = _heads(q, "q"), _heads(k, "k", q)
-    B, S, Hq, D = q.shape
-    for w, name in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _cuda(w, name, q.device)
-            _need(w.dtype == torch.float32 and tuple(w.shape) == (D,) and w.is_contiguous(),
-                  f"{name}: expected contiguous float32 [D]")
-    _cuda(cos, "cos", q.device)
-    _cuda(sin, "sin", q.device)
-    _need(cos.dtype == torch.float32 and sin.dtype == torch.float32 and cos.dim() == 2
-          and cos.shape == sin.shape and cos.is_contiguous() and sin.is_contiguous(),
-          "cos and sin: expected contiguous float32 [P, R / 2]")
-    P, R = cos.shape[0], 2 * cos.shape[1]
+    _cuda(k, "k", dev)
+    if q.dtype not in _DTYPE or k.dtype != q.dtype:
+        _bad("q and k: expected bfloat16, float16 or float32, both alike")
+    B, S, Hq, D, qs = _heads(q, "q")
+    Bk, Sk, Hk, Dk, ks = _heads(k, "k")
+    if (Bk, Sk, Dk) != (B, S, D):
+        _bad("k: expected the [B, S, ., D] of q")
+    pwq = None if wq is None else _vector(wq, "wq", D, dev)
+    pwk = None if wk is None else _vector(wk, "wk", D, dev)
+    _cuda(cos, "cos", dev)
+    _cuda(sin, "sin", dev)
+    if (cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape
+            or not cos.is_contiguous() or not sin.is_contiguous()):
+        _bad("cos and sin: expected contiguous float32 [P, R / 2]")
+    P, half = cos.shape
     pos, stride, bits = None, 0, 32
     if positions is not None:
-        bits = _index(positions, "positions", q.device)
-        _need(tuple(positions.shape) in ((B, S), (S,), (1, S)), "positions: expected [B, S] or [S]")
-        pos, stride = positions.data_ptr(), S if positions.dim() == 2 and positions.shape[0] == B else 0
-    return qs, ks, B, S, Hq, k.shape[2], D, R, P, pos, stride, bits
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+        bits = _index(positions, "positions", dev)
+        shape = positions.shape
+        if shape == (B, S):
+            stride = S
+        elif shape != (S,) and shape != (1, S):
+            _bad("positions: expected [B, S] or [S]")
+        pos = positions.data_ptr()
+    return (pwq, pwk, cos.data_ptr(), sin.data_ptr(), pos), (B, S, Hq, Hk, D, 2 * half, P, qs, ks), stride, bits
 
 
 def qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -228,16 +270,13 @@ def qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions=None, eps: float = 1e
     None; cos, sin: fp32 [P, R / 2] (rope_table); positions: int [B, S] or [S], default 0 .. S - 1;
     interleaved: pairs (2i, 2i + 1) rather than (i, i + R / 2). status as in embed_forward.
     Returns contiguous (q_out, k_out) as attn_forward takes them."""
-    qs, ks, B, S, Hq, Hk, D, R, P, pos, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
-    q_out = torch.empty((B, S, Hq, D), dtype=q.dtype, device=q.device)
-    k_out = torch.empty((B, S, Hk, D), dtype=q.dtype, device=q.device)
-    if status is not None:
-        _cuda(status, "status", q.device)
-        _need(status.dtype == torch.int32 and status.numel() == 1, "status: expected one int32")
+    tables, sizes, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
+    dev, dtype = q.device, q.dtype
+    q_out = torch.empty(q.shape, dtype=dtype, device=dev)
+    k_out = torch.empty(k.shape, dtype=dtype, device=dev)
     _raise(_core.load().dash_qk_norm_rope_fwd(
-        q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), cos.data_ptr(), sin.data_ptr(), pos,
-        q_out.data_ptr(), k_out.data_ptr(), _ptr(status), B, S, Hq, Hk, D, R, P, qs, ks, stride, eps,
-        int(interleaved), _DTYPE[q.dtype], bits, _core._stream(q, stream)), "dash_qk_norm_rope_fwd")
+        q.data_ptr(), k.data_ptr(), *tables, q_out.data_ptr(), k_out.data_ptr(), _status_word(status, dev),
+        *sizes, stride, eps, int(interleaved), _DTYPE[dtype], bits, _stream(q, stream)), "dash_qk_norm_rope_fwd")
     return q_out, k_out
 
 
@@ -261,29 +300,32 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None
     dq_out, dk_out: contiguous, as attn_backward returns them. dq, dk: optional tensors to
     write to, strided like q and k may be (parts of a fused projection's gradient). Returns
     (dq, dk, dwq, dwk), the last two fp32 [D] or None where the weight is None."""
-    qs, ks, B, S, Hq, Hk, D, R, P, pos, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
+    tables, sizes, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
+    dev, dtype = q.device, q.dtype
+    B, S, Hq, Hk, D = sizes[:5]
     for t, like, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
-        _cuda(t, name, q.device)
-        _need(t.dtype == q.dtype and t.shape == like.shape and t.is_contiguous(),
-              f"{name}: expected contiguous, of the input's type and shape")
+        _cuda(t, name, dev)
+        if t.dtype != dtype or t.shape != like.shape or not t.is_contiguous():
+            _bad(f"{name}: expected contiguous, of the input's type and shape")
     if dq is None:
-        dq = torch.empty((B, S, Hq, D), dtype=q.dtype, device=q.device)
+        dq = torch.empty(q.shape, dtype=dtype, device=dev)
     if dk is None:
-        dk = torch.empty((B, S, Hk, D), dtype=q.dtype, device=q.device)
+        dk = torch.empty(k.shape, dtype=dtype, device=dev)
     for t, like, name in ((dq, q, "dq"), (dk, k, "dk")):
-        _cuda(t, name, q.device)
-        _need(t.dtype == q.dtype and t.shape == like.shape, f"{name}: expected the input's type and shape")
-    dqs, dks = _heads(dq, "dq"), _heads(dk, "dk")
-    dwq = None if wq is None else torch.empty(D, dtype=torch.float32, device=q.device)
-    dwk = None if wk is None else torch.empty(D, dtype=torch.float32, device=q.device)
+        _cuda(t, name, dev)
+        if t.dtype != dtype or t.shape != like.shape:
+            _bad(f"{name}: expected the input's type and shape")
+    dqs, dks = _heads(dq, "dq")[4], _heads(dk, "dk")[4]
+    dws = torch.empty((2, D), dtype=torch.float32, device=dev)
+    dwq, dwk = (None if wq is None else dws[0]), (None if wk is None else dws[1])
     if workspace is None:
-        workspace = new_qk_norm_rope_workspace(B, S, Hq, Hk, D, q.device)
-    ws, nbytes = _ws(workspace)
+        workspace = new_qk_norm_rope_workspace(B, S, Hq, Hk, D, dev)
+    ws, nbytes = _ws(workspace, dev)
     _raise(_core.load().dash_qk_norm_rope_bwd(
-        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk),
-        cos.data_ptr(), sin.data_ptr(), pos, dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), ws, nbytes,
-        B, S, Hq, Hk, D, R, P, qs, ks, dqs, dks, stride, eps, int(interleaved), _DTYPE[q.dtype], bits,
-        _core._stream(q, stream)), "dash_qk_norm_rope_bwd")
+        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), *tables, dq.data_ptr(), dk.data_ptr(),
+        None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), ws, nbytes, *sizes,
+        dqs, dks, stride, eps, int(interleaved), _DTYPE[dtype], bits, _stream(q, stream)),
+        "dash_qk_norm_rope_bwd")
     _finish(workspace, stream, check, "dash_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -304,27 +346,31 @@ def grad_clip_plan(grads, out=None, stream=None) -> GradClipPlan:
     types."""
     grads = list(grads)
     outs = grads if out is None else list(out)
-    _need(len(grads) > 0 and len(outs) == len(grads), "grads: expected tensors, as many as out")
+    if not grads or len(outs) != len(grads):
+        _bad("grads: expected tensors, as many as out")
+    _cuda(grads[0], "grads[0]")
     dev = grads[0].device
     arr = (_ClipTensor * len(grads))()
     spans = set()
     for i, (g, o) in enumerate(zip(grads, outs)):
         for t, name in ((g, "grads"), (o, "out")):
             _cuda(t, f"{name}[{i}]", dev)
-            _need(t.dtype in _DTYPE and t.is_contiguous(),
-                  f"{name}[{i}]: expected contiguous bfloat16, float16 or float32")
+            if t.dtype not in _DTYPE or not t.is_contiguous():
+                _bad(f"{name}[{i}]: expected contiguous bfloat16, float16 or float32")
             if t.numel():
                 spans.add((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i))
-        _need(o.dtype == g.dtype and o.shape == g.shape, f"out[{i}]: expected the type and shape of grads[{i}]")
+        if o.dtype != g.dtype or o.shape != g.shape:
+            _bad(f"out[{i}]: expected the type and shape of grads[{i}]")
         arr[i] = _ClipTensor(g.data_ptr(), o.data_ptr(), g.numel(), _DTYPE[g.dtype])
     spans = sorted(spans)
-    _need(all(a[1] <= b[0] for a, b in zip(spans, spans[1:])), "grads and out: tensors overlap")
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        _bad("grads and out: tensors overlap")
     lib = _core.load()
     nbytes = lib.dash_grad_clip_plan_size(arr, len(grads))
     if nbytes == 0:
         raise DashError(DASH_ERR_UNSUPPORTED, "dash_grad_clip_plan_size")
     table = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _raise(lib.dash_grad_clip_plan(arr, len(grads), table.data_ptr(), nbytes, _core._stream(table, stream)),
+    _raise(lib.dash_grad_clip_plan(arr, len(grads), table.data_ptr(), nbytes, _stream(table, stream)),
            "dash_grad_clip_plan")
     return GradClipPlan(grads, outs, table, torch.empty((), dtype=torch.float32, device=dev))
 
@@ -334,7 +380,7 @@ def grad_clip(plan: GradClipPlan, max_norm: float, stream=None):
     above max_norm. Returns (norm, tensors): norm is a device fp32 scalar that the next call
     overwrites."""
     _raise(_core.load().dash_grad_clip(plan.table.data_ptr(), max_norm, plan.norm.data_ptr(),
-                                       _core._stream(plan.table, stream)), "dash_grad_clip")
+                                       _stream(plan.table, stream)), "dash_grad_clip")
     return plan.norm, plan.outs
 
 
@@ -353,14 +399,18 @@ def new_linear_xent_workspace(T: int, V: int, D: int, device) -> torch.Tensor:
 
 
 def _xent_args(x, w, targets):
+    dev = x.device
     _cuda(x, "x")
-    _cuda(w, "w", x.device)
-    _need(x.dtype == torch.bfloat16 and w.dtype == torch.bfloat16, "x and w: expected bfloat16")
+    _cuda(w, "w", dev)
+    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        _bad("x and w: expected bfloat16")
     ldx, ldw = _rows(x, "x"), _rows(w, "w")
-    bits = _index(targets, "targets", x.device)
+    bits = _index(targets, "targets", dev)
     T, D = x.shape
-    _need(w.shape[1] == D, "w: expected as many columns as x")
-    _need(targets.dim() == 1 and targets.shape[0] == T, "targets: expected one index a row of x")
+    if w.shape[1] != D:
+        _bad("w: expected as many columns as x")
+    if targets.shape != (T,):
+        _bad("targets: expected one index a row of x")
     return T, w.shape[0], D, ldx, ldw, bits
 
 
@@ -375,10 +425,10 @@ def linear_xent_forward(x, w, targets, ignore_index: int = -100, scale: float = 
         workspace = new_linear_xent_workspace(T, V, D, x.device)
     out = torch.empty((2, T), dtype=torch.float32, device=x.device)
     loss, lse = out[0], out[1]
-    ws, nbytes = _ws(workspace)
+    ws, nbytes = _ws(workspace, x.device)
     _raise(_core.load().dash_linear_xent_fwd(
         x.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws, nbytes,
-        T, V, D, ldx, ldw, scale, ignore_index, bits, _core._stream(x, stream)), "dash_linear_xent_fwd")
+        T, V, D, ldx, ldw, scale, ignore_index, bits, _stream(x, stream)), "dash_linear_xent_fwd")
     _finish(workspace, stream, check, "dash_linear_xent_fwd")
     return loss, lse
 
@@ -392,23 +442,22 @@ def linear_xent_backward(x, w, targets, lse, dloss, ignore_index: int = -100, sc
     tensor to write to, or to add to with accumulate=True (tied embeddings, several
     micro-batches); else one of dw_dtype (bf16) is allocated. Returns (dx, dw)."""
     T, V, D, ldx, ldw, bits = _xent_args(x, w, targets)
-    for t, name in ((lse, "lse"), (dloss, "dloss")):
-        _cuda(t, name, x.device)
-        _need(t.dtype == torch.float32 and tuple(t.shape) == (T,) and t.is_contiguous(),
-              f"{name}: expected contiguous float32 [T]")
+    dev = x.device
+    plse, pdloss = _vector(lse, "lse", T, dev), _vector(dloss, "dloss", T, dev)
     if dw is None:
-        _need(not accumulate, "accumulate: needs dw")
-        dw = torch.empty((V, D), dtype=dw_dtype or torch.bfloat16, device=x.device)
-    _cuda(dw, "dw", x.device)
-    _need(dw.dtype in (torch.bfloat16, torch.float32) and tuple(dw.shape) == (V, D) and dw.is_contiguous(),
-          "dw: expected contiguous bfloat16 or float32 [V, D]")
+        if accumulate:
+            _bad("accumulate: needs dw")
+        dw = torch.empty((V, D), dtype=dw_dtype or torch.bfloat16, device=dev)
+    _cuda(dw, "dw", dev)
+    if dw.dtype not in (torch.bfloat16, torch.float32) or dw.shape != (V, D) or not dw.is_contiguous():
+        _bad("dw: expected contiguous bfloat16 or float32 [V, D]")
     if workspace is None:
         workspace = new_linear_xent_workspace(T, V, D, x.device)
     dx = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
-    ws, nbytes = _ws(workspace)
+    ws, nbytes = _ws(workspace, x.device)
     _raise(_core.load().dash_linear_xent_bwd(
-        x.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(),
+        x.data_ptr(), w.data_ptr(), targets.data_ptr(), plse, pdloss, dx.data_ptr(),
         dw.data_ptr(), ws, nbytes, T, V, D, ldx, ldw, scale, ignore_index, bits, _DTYPE[dw.dtype],
-        int(accumulate), _core._stream(x, stream)), "dash_linear_xent_bwd")
+        int(accumulate), _stream(x, stream)), "dash_linear_xent_bwd")
     _finish(workspace, stream, check, "dash_linear_xent_bwd")
     return dx, dw

@@ -50,7 +50,7 @@ def test_embed_bwd_refuses(lib, kw, want):
 
 def test_workspace_sizes(lib):
     T, V, D = 1000, 5000, 72
-    need = 256 + V // 8 + 4 * T * 4 + 2 * 32 * D * 4
+    need = 256 + 4 * T * 4 + 2 * 32 * D * 4
     assert need <= da.dash_embed_bwd_workspace_size(T, V, D) <= need + 8 * 256
     assert da.dash_embed_bwd_workspace_size(-1, 5, 8) == 0 and da.dash_embed_bwd_workspace_size(1, 0, 8) == 0
     assert da.dash_qk_norm_rope_bwd_workspace_size(1, 1, 1, 1, 264) == 0

@@ -1,13 +1,14 @@
 // Token embedding (dash_embed_fwd) and its gradient by sorted tokens (dash_embed_bwd).
 //
 // The forward is a gather of rows: one load and one store of 16 bytes a thread and four rows
-// in flight, bound by HBM. The gradient has three launches:
+// in flight, bound by HBM. The gradient has four launches:
 //   embed_sort  one cluster of 8 CTAs sorts the tokens by id: a stable counting sort by
 //               digits of at most 9 bits, so two passes up to 2^18 ids. Each warp counts a
 //               run of tokens of its own, so ranks within a digit follow the token order
 //               without atomics; the CTAs' counts meet in distributed shared memory. It is
-//               bound by latency (some 20 k cycles), so the launch's other clusters zero the
-//               whole table meanwhile; the rows of ids that occur are then stored over it.
+//               bound by latency (some 20 k cycles).
+//   embed_zero  zeroes the whole table meanwhile: it starts beside the sort and does not wait
+//               for it; the rows of ids that occur are then stored over the zeroes.
 //   embed_rows  runs of 32 sorted places times column tiles: an id's rows are added in
 //               order in registers; ids that lie within one run are stored, the parts of
 //               those that cross runs go to the workspace.
@@ -32,7 +33,6 @@ constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigitBits = 9;
-constexpr size_t kFillBytes = 1 << 18;  // of the table that one CTA zeroes
 constexpr int kAheadStrips = 4;         // strips of 32 tokens a warp has in flight
 
 // ---- forward ------------------------------------------------------------------------------
@@ -87,16 +87,25 @@ struct SortArgs {
   int passes, digit_bits;
   int* header;
   unsigned *keys[2], *toks[2];   // the last pass writes index (passes - 1) & 1
-  char* fill;                 // bytes to zero (the table), of an even number and address
-  size_t fill_bytes;
 };
 
-// Zeroes [p, p + n) with `threads` threads, of which this is number `t`.
-__device__ __forceinline__ void zero_bytes(char* p, size_t n, size_t t, size_t threads) {
+// Zeroes n bytes at p, both even. The kernel before it is this call's sort, which starts only
+// when all earlier work is done, so the table may be written at once. Its first block then
+// waits for the sort, so that what waits for this kernel waits for both.
+constexpr int kZeroThreads = 256;
+constexpr size_t kZeroBytes = 1 << 16;  // of one block
+__global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(char* p, size_t n) {
+  grid_next();
+  const size_t from = blockIdx.x * kZeroBytes;
+  p += from;
+  n = min(kZeroBytes, n - from);
   const size_t head = min(n, (size_t)(-(intptr_t)p & 15)), body = (n - head) / 16, tail = n - head - body * 16;
-  for (size_t i = t; i < body; i += threads) reinterpret_cast<uint4*>(p + head)[i] = make_uint4(0, 0, 0, 0);
-  if (t < head / 2) reinterpret_cast<uint16_t*>(p)[t] = 0;
-  if (t < tail / 2) reinterpret_cast<uint16_t*>(p + head + body * 16)[t] = 0;
+#pragma unroll 8
+  for (size_t i = threadIdx.x; i < body; i += kZeroThreads)
+    reinterpret_cast<uint4*>(p + head)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < head / 2) reinterpret_cast<uint16_t*>(p)[threadIdx.x] = 0;
+  if (threadIdx.x < tail / 2) reinterpret_cast<uint16_t*>(p + head + body * 16)[threadIdx.x] = 0;
+  if (blockIdx.x == 0) grid_wait();
 }
 
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads)
@@ -113,12 +122,6 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
   const unsigned lt = (1u << lane) - 1;
 
   grid_next();
-  if (blockIdx.x >= kSortCtas) {
-    const size_t at = (size_t)(blockIdx.x - kSortCtas) * kFillBytes;
-    if (at < a.fill_bytes)
-      zero_bytes(a.fill + at, min(kFillBytes, a.fill_bytes - at), threadIdx.x, kSortThreads);
-    return;
-  }
   if (rank == 0 && threadIdx.x < kWsHeaderBytes / 4) a.header[threadIdx.x] = 0;
 
   // this warp's run of whole 32-token strips
@@ -319,8 +322,8 @@ __global__ void __launch_bounds__(kRowThreads)
   const unsigned V = (unsigned)a.V;
   const unsigned* keys = a.keys + p0;
   const unsigned* toks = a.toks + p0;
-  unsigned key = __ldg(keys);
-  bool begun = run > 0 && __ldg(keys - 1) == key;
+  unsigned key = keys[0];
+  bool begun = run > 0 && keys[-1] == key;
   float acc[N] = {};
   constexpr int U = 8;
 #pragma unroll 1
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       v[i] = {};
-      if (p + i < n) v[i].load(dout + __ldg(toks + p + i) * a.ld_dout + col, a.tx, nc);
+      if (p + i < n) v[i].load(dout + toks[p + i] * a.ld_dout + col, a.tx, nc);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
         for (int k = 0; k < N; ++k) acc[k] += f[k];
         const bool more = p0 + p + i + 1 < a.T;
-        const unsigned next = more ? __ldg(keys + p + i + 1) : 0xffffffffu;
+        const unsigned next = more ? keys[p + i + 1] : 0xffffffffu;
         if (next != key || p + i + 1 == n) {
           const bool goes_on = next == key;
           if (!begun && !goes_on) {
@@ -395,9 +398,9 @@ __global__ void __launch_bounds__(256) embed_join_kernel(TO* dtable, const RowAr
     // the run's last key, the next one and the one before the run, at once
     unsigned k = 0xffffffffu;
     if (p0 + kRun < a.T) {
-      if (lane == 0) k = __ldg(a.keys + p0 + kRun - 1);
-      if (lane == 1) k = __ldg(a.keys + p0 + kRun);
-      if (lane == 2 && run > 0) k = __ldg(a.keys + p0 - 1);
+      if (lane == 0) k = a.keys[p0 + kRun - 1];
+      if (lane == 1) k = a.keys[p0 + kRun];
+      if (lane == 2 && run > 0) k = a.keys[p0 - 1];
     }
     const unsigned key = __shfl_sync(0xffffffffu, k, 0);
     const bool cross = key < (unsigned)a.V && __shfl_sync(0xffffffffu, k, 1) == key &&
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(TO* dtable, const RowAr
     if (cross) {
       for (;;) {
         const long long r = run + 1 + follow + lane;
-        const unsigned same = __ballot_sync(0xffffffffu, r < a.runs && __ldg(a.keys + r * kRun) == key);
+        const unsigned same = __ballot_sync(0xffffffffu, r < a.runs && a.keys[r * kRun] == key);
         follow += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
         if (same != 0xffffffffu) break;
       }
@@ -589,8 +592,9 @@ dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, vo
   s.passes = ceil_div(bits, kMaxDigitBits);
   s.digit_bits = ceil_div(bits, s.passes);
   s.header = (int*)ws;
-  s.fill = (char*)dtable;
-  s.fill_bytes = accumulate ? 0 : (size_t)V * D * elt_bytes(dtable_dtype);
+  const size_t table_bytes = (size_t)V * D * elt_bytes(dtable_dtype);
+  const size_t zero_blocks = ceil_div<size_t>(table_bytes, kZeroBytes);
+  if (zero_blocks >= (1ull << 31)) return DASH_ERR_UNSUPPORTED;
   s.keys[0] = (unsigned*)(ws + l.keys0);
   s.keys[1] = (unsigned*)(ws + l.keys1);
   s.toks[0] = (unsigned*)(ws + l.toks0);
@@ -598,10 +602,11 @@ dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, vo
   const size_t smem = ((size_t)(kSortWarps + 2) << s.digit_bits) * 4;
   DASH_TRY(cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)(((size_t)(kSortWarps + 2) << kMaxDigitBits) * 4)));
-  const size_t fillers = ceil_div<size_t>(s.fill_bytes, kFillBytes);
-  if (fillers >= (1ull << 31) - 64) return DASH_ERR_UNSUPPORTED;
-  embed_sort_kernel<<<(unsigned)(kSortCtas + round_up_to(fillers, kSortCtas)), kSortThreads, smem, stream>>>(s);
+  embed_sort_kernel<<<kSortCtas, kSortThreads, smem, stream>>>(s);
   DASH_TRY(cudaGetLastError());
+  if (!accumulate)
+    DASH_TRY(launch_after(embed_zero_kernel, dim3((unsigned)zero_blocks), kZeroThreads, 0, stream, (char*)dtable,
+                          table_bytes));
   RowArgs a;
   a.keys = s.keys[(s.passes - 1) & 1];
   a.toks = s.toks[(s.passes - 1) & 1];

@@ -1,11 +1,16 @@
 // Norm of queries and keys per head with the rotation in the same pass (dash_qk_norm_rope_*).
 //
-// A head's D values lie in L = D / 8 lanes of a warp (rounded up to a power of two), 8 values
-// and one 16-byte access a lane (two in fp32), so the mean of squares is a shuffle tree and
-// the rotation's partner values come from the lane R / 16 away, or, where R / 2 is no
-// multiple of 8, from a second read of the row (which hits L1). A warp keeps one token's
-// angles and weights in registers over several heads. Both directions read and write every
-// value once: bound by HBM.
+// A lane holds two chunks of 8 consecutive values of a head, so a head lies in L = D / 16 lanes
+// (rounded up to a power of two) and the mean of squares is a shuffle tree over them. The
+// chunks are chosen so that rotation partners meet in one lane: chunks j and j + R / 16 for
+// half-split pairs, neighbours for interleaved ones. (Where R / 2 is no multiple of 8, or of 4
+// for interleaved pairs, a value's partner is read once more, which hits L1.)
+// Both directions read and write every value once: bound by HBM, with the instructions next
+// (8 values a lane and shuffled partners took 22 an element forward, 31 backward, and 105 and
+// 167 us for 16384 tokens x 64 heads x 128, where the bytes take 80 and 119). A warp walks over
+// a run of (token, heads) items of its own and copies the next items' rows into its part of
+// shared memory while it computes one (cp.async, two items ahead), so that loads are in flight
+// all the time without registers; a token's angles are loaded once for all its heads.
 #include <algorithm>
 
 #include "dash_train.h"
@@ -22,7 +27,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 256;
 // Blocks that share the rows. The backward's number fixes how dw's sum is split, so it is a
 // constant and not the device's SM count: one block for each that 152 SMs hold.
-constexpr int kFwdBlocks = 608 * 2;
+constexpr int kFwdBlocks = 456;
 constexpr int kBwdBlocks = 304;
 static_assert(2 * (kBwdBlocks + 1) <= 1024, "dw_join looks at all blocks at once");
 
@@ -46,25 +51,15 @@ struct Args {
   const void* pos;
   long long pos_stride, P;
   int id_bits;
-  int tokens, S, D, R;
+  int tokens, S, D, R, interleaved;
   float eps;
   int* header;                      // backward: workspace header
   int* status;                      // forward: optional status word
 };
 
-// cos and sin of the pairs that a lane's 8 columns belong to.
-template <bool IL>
-struct Angles {
-  float c[IL ? 4 : 8], s[IL ? 4 : 8];
-};
-
-// Position of a token, out of range or not.
-__device__ __forceinline__ long long load_position(const Args& a, int token) {
-  const int b = token / a.S, s = token - b * a.S;
-  return a.pos ? load_index(a.pos, b * a.pos_stride + s, a.id_bits) : (long long)s;
-}
-
 constexpr int kNoToken = 0x7fffffff;
+
+enum Mode : int { HALF = 0, PAIRS = 1, ANY = 2 };
 
 __device__ __forceinline__ void four(const float* p, float* v) {
   const float4 x = __ldg(reinterpret_cast<const float4*>(p));
@@ -74,72 +69,82 @@ __device__ __forceinline__ void four(const float* p, float* v) {
   v[3] = x.w;
 }
 
-// FAST: a lane's columns are all rotated or none, and its angles are whole 16-byte pieces.
-template <bool IL, bool FAST>
-__device__ __forceinline__ void load_angles(const Args& a, long long p, int col, Angles<IL>& g) {
+// A lane's 16 values: v[0..7] are the columns from c0, v[8..15] those from c1 (at D or beyond:
+// not there). Its 8 pairs are (v[i], v[8 + i]) in mode HALF, (v[2i], v[2i + 1]) in mode PAIRS.
+template <int M>
+struct Lane {
+  int c0, c1;
+  bool in0, in1;
+  __device__ __forceinline__ Lane(const Args& a, int j) {
+    const int rot = M == HALF ? a.R >> 4 : 0;      // lanes whose chunks are rotated
+    c0 = j < rot ? 8 * j : 16 * rot + 16 * (j - rot);
+    c1 = j < rot ? c0 + 8 * rot : c0 + 8;
+    in0 = c0 < a.D;
+    in1 = c1 < a.D;
+  }
+};
+template <int M>
+__device__ __forceinline__ constexpr int first_of(int i) { return M == HALF ? i : 2 * i; }
+template <int M>
+__device__ __forceinline__ constexpr int second_of(int i) { return M == HALF ? 8 + i : 2 * i + 1; }
+
+// cos and sin of the lane's 8 pairs at position p (none rotated: p < 0, or columns beyond R).
+template <int M>
+__device__ __forceinline__ void load_angles(const Args& a, const Lane<M>& ln, long long p, float (&c)[8],
+                                            float (&s)[8]) {
   const int half = a.R >> 1;
-  constexpr int N = IL ? 4 : 8;
-  if constexpr (FAST) {
-    if (col < a.R && p >= 0) {
-      const long long at = p * half + (IL ? col >> 1 : col < half ? col : col - half);
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        four(a.cos + at + i, g.c + i);
-        four(a.sin + at + i, g.s + i);
-      }
+  for (int k = 0; k < 2; ++k) {                    // four pairs at a time
+    const int col = M == HALF ? ln.c0 + 4 * k : k == 0 ? ln.c0 : ln.c1;
+    const bool rotated = p >= 0 && (M == HALF ? ln.c0 < half : col < a.R);
+    if (rotated) {
+      const long long at = p * half + (M == HALF ? col : col >> 1);
+      four(a.cos + at, c + 4 * k);
+      four(a.sin + at, s + 4 * k);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        g.c[i] = 1.f;      // a position out of range makes the norm NaN
-        g.s[i] = 0.f;
+      for (int i = 4 * k; i < 4 * k + 4; ++i) {
+        c[i] = 1.f;
+        s[i] = 0.f;
       }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int j = IL ? (col >> 1) + i : (col + i < half ? col + i : col + i - half);
-      const bool in = (IL ? col + 2 * i : col + i) < a.R && p >= 0;
-      g.c[i] = in ? __ldg(a.cos + p * half + j) : 1.f;
-      g.s[i] = in ? __ldg(a.sin + p * half + j) : 0.f;
     }
   }
 }
 
-// Rotates the 8 values y of columns col.. (sign +1) or applies the transpose (sign -1).
-// Half-split pairs, FAST: they lie whole lanes apart (R / 2 a multiple of 8); else `partner(c)`
-// gives the value of column c.
-template <bool IL, bool FAST, typename F>
-__device__ __forceinline__ void rotate(const Args& a, const Angles<IL>& g, int col, float sign, float (&y)[8],
-                                       F partner) {
+template <int M>
+__device__ __forceinline__ void load_weights(const float* w, const Lane<M>& ln, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 1.f;
+  if (w && ln.in0) {
+    four(w + ln.c0, v);
+    four(w + ln.c0 + 4, v + 4);
+  }
+  if (w && ln.in1) {
+    four(w + ln.c1, v + 8);
+    four(w + ln.c1 + 4, v + 12);
+  }
+}
+
+// Mode ANY: rotates the 16 values by themselves (sign +1; -1: the transpose); `partner(c)` gives
+// the value of column c.
+template <typename F>
+__device__ __forceinline__ void rotate_any(const Args& a, const Lane<ANY>& ln, long long p, float sign,
+                                           float (&y)[16], F partner) {
   const int half = a.R >> 1;
-  if (IL) {
+  float z[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float u = y[2 * i], v = y[2 * i + 1], s = sign * g.s[i];
-      y[2 * i] = u * g.c[i] - v * s;
-      y[2 * i + 1] = v * g.c[i] + u * s;
-    }
-  } else if (FAST) {
-    const int d = half >> 3;
-    const int lane = threadIdx.x & 31;
-    const bool lo = col < half;
-    const int src = lo ? lane + d : lane - d;
-    const float sg = lo ? -sign : sign;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, y[i], src);
-      if (col < a.R) y[i] = y[i] * g.c[i] + o * (sg * g.s[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = col + i;
-      if (c < a.R) {
-        const float o = partner(c < half ? c + half : c - half);
-        y[i] = y[i] * g.c[i] + (c < half ? -sign : sign) * (o * g.s[i]);
-      }
+  for (int i = 0; i < 16; ++i) {
+    const int c = (i < 8 ? ln.c0 : ln.c1) + (i & 7);
+    z[i] = y[i];
+    if (c < a.R && p >= 0) {
+      const bool lo = a.interleaved ? (c & 1) == 0 : c < half;
+      const int k = a.interleaved ? c >> 1 : lo ? c : c - half;
+      const int o = a.interleaved ? c ^ 1 : lo ? c + half : c - half;
+      z[i] = y[i] * __ldg(a.cos + p * half + k) + (lo ? -sign : sign) * __ldg(a.sin + p * half + k) * partner(o);
     }
   }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = z[i];
 }
 
 template <int L>
@@ -149,78 +154,201 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ void load_weights(const float* w, int col, bool in, float (&v)[8]) {
+// A warp's place in its run of items: item = (token, head group), groups first.
+struct Cursor {
+  int b, s, grp, groups, S;
+  unsigned left;                                  // items from here on
+  __device__ __forceinline__ Cursor(unsigned item, unsigned end, int groups_, int S_)
+      : groups(groups_), S(S_), left(end - item) {
+    const unsigned token = item / groups;
+    grp = (int)(item - token * groups);
+    b = (int)(token / S);
+    s = (int)(token - b * S);
+  }
+  __device__ __forceinline__ void next() {
+    --left;
+    if (++grp == groups) {
+      grp = 0;
+      if (++s == S) {
+        s = 0;
+        ++b;
+      }
+    }
+  }
+};
+
+// 8 values from global to shared memory without registers; zeros where `live` is false. A warp's
+// 16-byte pieces lie side by side, 512 bytes a piece of every lane.
+template <typename T>
+__device__ __forceinline__ void copy8(uint32_t dst, const T* src, bool live) {
+  const int n = live ? 16 : 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 1.f;
-  if (w && in) {
-    four(w + col, v);
-    four(w + col + 4, v + 4);
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512),
+                 "l"(reinterpret_cast<const char*>(src) + (live ? i * 16 : 0)), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void from_shared(const char* at, float* f) {
+  Vec<T, 8> x;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at + i * 512);
+    x.w[4 * i] = v.x;
+    x.w[4 * i + 1] = v.y;
+    x.w[4 * i + 2] = v.z;
+    x.w[4 * i + 3] = v.w;
+  }
+  float y[8];
+  unpack<T, 8>(x, y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = y[i];
+}
+template <typename T, int M>
+__device__ __forceinline__ void store16(T* row, const Lane<M>& ln, const float (&v)[16]) {
+  float x[8];
+  if (ln.in0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i];
+    store_f32<T, 8>(row + ln.c0, x);
+  }
+  if (ln.in1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[8 + i];
+    store_f32<T, 8>(row + ln.c1, x);
   }
 }
 
-// Forward. A warp walks over items of one token and U * 32 / L heads, the grid's warps apart.
-// The next item's position is fetched an item ahead, so that the angles' loads, which need
-// it, start together with the data's.
-template <typename T, int L, bool IL, bool FAST, int U>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(const Args a) {
-  constexpr int RW = 32 / L;                       // heads a warp handles at once
+constexpr int kItemsAhead = 2;                    // items in shared memory beside the one in work
+
+// Bytes of one row of every lane group of a warp: 8 values a lane, twice.
+template <typename T>
+constexpr int kChunkBytes = 32 * 8 * (int)sizeof(T);
+template <typename T, int U, bool BWD>
+constexpr int kSharedBytes = kWarps * (kItemsAhead + 1) * U * (BWD ? 4 : 2) * kChunkBytes<T>;
+
+// This warp's run of a tensor's items.
+template <int U, int L>
+__device__ __forceinline__ Cursor warp_items(const Args& a, const Side& sd, int block) {
+  constexpr int RW = 32 / L;
+  const unsigned groups = (unsigned)(sd.H + U * RW - 1) / (U * RW), items = (unsigned)a.tokens * groups;
+  const unsigned warps = (unsigned)sd.blocks * kWarps, per = (items + warps - 1) / warps;
+  const unsigned first = min(items, ((unsigned)block * kWarps + (threadIdx.x >> 5)) * per);
+  return Cursor(first, min(items, first + per), (int)groups, a.S);
+}
+
+// The token's position, -1 when it is out of range.
+__device__ __forceinline__ long long position(const Args& a, int b, int s) {
+  const long long p = a.pos ? load_index(a.pos, b * a.pos_stride + s, a.id_bits) : (long long)s;
+  return p >= 0 && p < a.P ? p : -1;
+}
+
+template <typename T, int L, int M, int U>
+__global__ void __launch_bounds__(kThreads, M == ANY ? 2 : 3) fwd_kernel(const Args a) {
+  constexpr int RW = 32 / L, kStages = kItemsAhead + 1;   // RW: heads a warp handles at once
+  extern __shared__ char qk_smem[];
   const int which = blockIdx.x >= a.side[0].blocks;
   const Side& sd = a.side[which];
-  const int lane = threadIdx.x & 31, sub = lane / L, col = (lane % L) * 8;
-  const unsigned groups = (unsigned)(sd.H + U * RW - 1) / (U * RW), items = (unsigned)a.tokens * groups;
-  const unsigned step = (unsigned)sd.blocks * kWarps;
-  unsigned item = (blockIdx.x - (which ? a.side[0].blocks : 0)) * kWarps + (threadIdx.x >> 5);
-  if (item >= items) return;
-  const bool in = col < a.D;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L;
+  const Lane<M> ln(a, lane % L);
   const float inv_d = 1.f / a.D;
-  float w[8];
-  load_weights(sd.w, col, in, w);
-  long long next_p = load_position(a, (int)(item / groups));
-  for (; item < items; item += step) {
-    const int token = (int)(item / groups), h0 = (int)(item % groups) * U * RW + sub;
-    const int b = token / a.S, s = token - b * a.S;
-    const T* x = (const T*)sd.x + b * sd.sb + s * sd.ss;
-    T* out = (T*)sd.out + b * sd.ob + s * sd.os;
-    Vec<T, 8> raw[U];
+  char* mine = qk_smem + warp * (kStages * U * 2 * kChunkBytes<T>) + lane * 16;
+  const uint32_t mine_s = (uint32_t)__cvta_generic_to_shared(mine);
+  Cursor at = warp_items<U, L>(a, sd, blockIdx.x - (which ? a.side[0].blocks : 0));
+  Cursor ahead = at;
+  auto fetch = [&](int stage) {                    // the item at `ahead`; an empty group past the end
+    if (ahead.left > 0) {
+      const T* x = (const T*)sd.x + ahead.b * sd.sb + ahead.s * sd.ss;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = (ahead.grp * U + u) * RW + sub;
+        const bool live = h < sd.H;
+        const T* row = live ? x + h * sd.sh : (const T*)sd.x;
+        const uint32_t to = mine_s + (stage * U + u) * 2 * kChunkBytes<T>;
+        copy8<T>(to, live && ln.in0 ? row + ln.c0 : row, live && ln.in0);
+        copy8<T>(to + kChunkBytes<T>, live && ln.in1 ? row + ln.c1 : row, live && ln.in1);
+      }
+      ahead.next();
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kItemsAhead; ++k) fetch(k);
+  // a pair's output is r (x_a (w_a c) - x_b (w_b s)), r (x_b (w_b c) + x_a (w_a s))
+  float ac[8], bs[8], bc[8], as[8], w[16];
+  if (M == ANY) load_weights(sd.w, ln, w);
+  long long p = 0;
+  bool fresh = true;                               // the token's angles are not here yet
+  for (int stage = 0; at.left > 0;) {
+    fetch(stage >= 1 ? stage - 1 : kStages - 1);   // into the stage that the last item left
+    if (fresh || at.grp == 0) {
+      p = position(a, at.b, at.s);
+      if (p < 0 && a.status) *a.status = kStatusBounds;
+      if constexpr (M != ANY) {
+        float c[8], s[8];
+        load_weights(sd.w, ln, w);
+        load_angles<M>(a, ln, p, c, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float wa = w[first_of<M>(i)], wb = w[second_of<M>(i)];
+          ac[i] = wa * c[i];
+          bs[i] = wb * s[i];
+          bc[i] = wb * c[i];
+          as[i] = wa * s[i];
+        }
+      }
+      fresh = false;
+    }
+    copies_wait<kItemsAhead>();
+    T* out = (T*)sd.out + at.b * sd.ob + at.s * sd.os;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * RW;
-      raw[u] = {};
-      if (in && h < sd.H) raw[u] = load_vec<T, 8>(x + h * sd.sh + col);
-    }
-    long long p = next_p;
-    if (p < 0 || p >= a.P) {
-      p = -1;
-      if (a.status) *a.status = kStatusBounds;
-    }
-    Angles<IL> g;
-    load_angles<IL, FAST>(a, p, col, g);
-    if (items - item > step) next_p = load_position(a, (int)((item + step) / groups));
+      const int h = (at.grp * U + u) * RW + sub;
+      float x[16], q0 = 0.f, q1 = 0.f;
+      const char* from = mine + (stage * U + u) * 2 * kChunkBytes<T>;
+      from_shared<T>(from, x);
+      from_shared<T>(from + kChunkBytes<T>, x + 8);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * RW;
-      const bool live = in && h < sd.H;
-      float y[8], q = 0.f;
-      unpack<T, 8>(raw[u], y);
+      for (int i = 0; i < 8; ++i) {
+        q0 = fmaf(x[i], x[i], q0);
+        q1 = fmaf(x[8 + i], x[8 + i], q1);
+      }
+      const float r = p < 0 ? NAN : rsqrtf(lanes_sum<L>(q0 + q1) * inv_d + a.eps);
+      float y[16];
+      if constexpr (M == ANY) {
+        const T* row = (const T*)sd.x + at.b * sd.sb + at.s * sd.ss + h * sd.sh;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q = fmaf(y[i], y[i], q);
-      const float r = p < 0 ? NAN : rsqrtf(lanes_sum<L>(q) * inv_d + a.eps);
+        for (int i = 0; i < 16; ++i) y[i] = x[i] * w[i] * r;
+        rotate_any(a, ln, h < sd.H ? p : -1, 1.f, y, [&](int c) {
+          return to_f32(row[c]) * (sd.w ? __ldg(sd.w + c) : 1.f) * r;
+        });
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
-      const T* row = x + (long long)h * sd.sh;
-      rotate<IL, FAST>(a, g, col, 1.f, y, [&](int c) {
-        return live ? to_f32(row[c]) * r * (sd.w ? __ldg(sd.w + c) : 1.f) : 0.f;
-      });
-      if (live) store_f32<T, 8>(out + h * sd.oh + col, y);
+        for (int i = 0; i < 8; ++i) {
+          const float xa = x[first_of<M>(i)], xb = x[second_of<M>(i)];
+          y[first_of<M>(i)] = (xa * ac[i] - xb * bs[i]) * r;
+          y[second_of<M>(i)] = (xb * bc[i] + xa * as[i]) * r;
+        }
+      }
+      if (h < sd.H) store16<T, M>(out + h * sd.oh, ln, y);
     }
+    at.next();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 }
 
-// Backward. A warp walks over (token, head group) items, `blocks` blocks apart, and keeps its
+// Backward: the same walk over the rows of x and of the output's gradient. With e the rotated
+// gradient, t = e x and m = sum(w t) / D: dw += r t, dx = r (w e - r^2 m x). A warp keeps its
 // columns' part of dw in registers; the block's warps are added in order.
-template <typename T, int L, bool IL, bool FAST, int U>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(const Args a) {
-  constexpr int RW = 32 / L;
+template <typename T, int L, int M, int U>
+__global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args a) {
+  constexpr int RW = 32 / L, kStages = kItemsAhead + 1;
+  extern __shared__ char qk_smem[];
   __shared__ float dws[kWarps][kMaxD];
   __shared__ int bad;
   grid_next();
@@ -229,78 +357,104 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args a) {
   const int which = blockIdx.x >= a.side[0].blocks;
   const Side& sd = a.side[which];
   const int block = blockIdx.x - (which ? a.side[0].blocks : 0);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L, col = (lane % L) * 8;
-  const unsigned groups = (unsigned)(sd.H + U * RW - 1) / (U * RW), items = (unsigned)a.tokens * groups;
-  const unsigned step = (unsigned)sd.blocks * kWarps;
-  const bool in = col < a.D;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L;
+  const Lane<M> ln(a, lane % L);
   const float inv_d = 1.f / a.D;
-  float w[8], dw[8] = {};
-  load_weights(sd.w, col, in, w);
-  unsigned item = (unsigned)block * kWarps + warp;
-  long long next_p = item < items ? load_position(a, (int)(item / groups)) : 0;
-  for (; item < items; item += step) {
-    const int token = (int)(item / groups), h0 = (int)(item % groups) * U * RW + sub;
-    const int b = token / a.S, s = token - b * a.S;
-    const T* x = (const T*)sd.x + b * sd.sb + s * sd.ss;
-    const T* d = (const T*)sd.dout + (long long)token * sd.H * a.D;
-    T* out = (T*)sd.out + b * sd.ob + s * sd.os;
-    Vec<T, 8> rx[U], rd[U];
+  char* mine = qk_smem + warp * (kStages * U * 4 * kChunkBytes<T>) + lane * 16;
+  const uint32_t mine_s = (uint32_t)__cvta_generic_to_shared(mine);
+  Cursor at = warp_items<U, L>(a, sd, block);
+  Cursor ahead = at;
+  auto fetch = [&](int stage) {
+    if (ahead.left > 0) {
+      const T* x = (const T*)sd.x + ahead.b * sd.sb + ahead.s * sd.ss;
+      const T* d = (const T*)sd.dout + ((long long)ahead.b * a.S + ahead.s) * sd.H * a.D;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * RW;
-      rx[u] = rd[u] = {};
-      if (in && h < sd.H) {
-        rx[u] = load_vec<T, 8>(x + h * sd.sh + col);
-        rd[u] = load_vec<T, 8>(d + (long long)h * a.D + col);
+      for (int u = 0; u < U; ++u) {
+        const int h = (ahead.grp * U + u) * RW + sub;
+        const bool live = h < sd.H, l0 = live && ln.in0, l1 = live && ln.in1;
+        const T* xr = live ? x + h * sd.sh : (const T*)sd.x;
+        const T* dr = live ? d + h * a.D : (const T*)sd.dout;
+        const uint32_t to = mine_s + (stage * U + u) * 4 * kChunkBytes<T>;
+        copy8<T>(to, l0 ? xr + ln.c0 : xr, l0);
+        copy8<T>(to + kChunkBytes<T>, l1 ? xr + ln.c1 : xr, l1);
+        copy8<T>(to + 2 * kChunkBytes<T>, l0 ? dr + ln.c0 : dr, l0);
+        copy8<T>(to + 3 * kChunkBytes<T>, l1 ? dr + ln.c1 : dr, l1);
       }
+      ahead.next();
     }
-    long long p = next_p;
-    if (p < 0 || p >= a.P) {
-      p = -1;
-      if (lane == 0) atomicMin(&bad, token);
+    copies_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kItemsAhead; ++k) fetch(k);
+  float w[16], dw[16] = {}, c[8], s[8];
+  load_weights(sd.w, ln, w);
+  long long p = 0;
+  bool fresh = true;
+  for (int stage = 0; at.left > 0;) {
+    fetch(stage >= 1 ? stage - 1 : kStages - 1);
+    if (fresh || at.grp == 0) {
+      p = position(a, at.b, at.s);
+      if (p < 0 && lane == 0) atomicMin(&bad, at.b * a.S + at.s);
+      if constexpr (M != ANY) load_angles<M>(a, ln, p, c, s);
+      fresh = false;
     }
-    Angles<IL> g;
-    load_angles<IL, FAST>(a, p, col, g);
-    if (items - item > step) next_p = load_position(a, (int)((item + step) / groups));
+    copies_wait<kItemsAhead>();
+    T* out = (T*)sd.out + at.b * sd.ob + at.s * sd.os;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * RW;
-      const bool live = in && h < sd.H;
-      float n[8], dy[8], q = 0.f;
-      unpack<T, 8>(rx[u], n);
-      unpack<T, 8>(rd[u], dy);
+      const int h = (at.grp * U + u) * RW + sub;
+      float x[16], e[16], q0 = 0.f, q1 = 0.f;
+      const char* from = mine + (stage * U + u) * 4 * kChunkBytes<T>;
+      from_shared<T>(from, x);
+      from_shared<T>(from + kChunkBytes<T>, x + 8);
+      from_shared<T>(from + 2 * kChunkBytes<T>, e);
+      from_shared<T>(from + 3 * kChunkBytes<T>, e + 8);
+      if constexpr (M == ANY) {
+        const T* row = (const T*)sd.dout + (((long long)at.b * a.S + at.s) * sd.H + h) * a.D;
+        rotate_any(a, ln, h < sd.H ? p : -1, -1.f, e, [&](int col) { return to_f32(row[col]); });
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q = fmaf(n[i], n[i], q);
-      const float r = p < 0 ? NAN : rsqrtf(lanes_sum<L>(q) * inv_d + a.eps);
-      rotate<IL, FAST>(a, g, col, -1.f, dy, [&](int c) {
-        return live ? to_f32(d[(long long)h * a.D + c]) : 0.f;
-      });
-      float dot = 0.f;
+        for (int i = 0; i < 8; ++i) {
+          const float da = e[first_of<M>(i)], db = e[second_of<M>(i)];
+          e[first_of<M>(i)] = da * c[i] + db * s[i];
+          e[second_of<M>(i)] = db * c[i] - da * s[i];
+        }
+      }
+      float m0 = 0.f, m1 = 0.f, t[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        n[i] *= r;
-        if (live) dw[i] = fmaf(dy[i], n[i], dw[i]);
-        dy[i] *= w[i];
-        dot = fmaf(dy[i], n[i], dot);
+        q0 = fmaf(x[i], x[i], q0);
+        q1 = fmaf(x[8 + i], x[8 + i], q1);
+        t[i] = e[i] * x[i];
+        t[8 + i] = e[8 + i] * x[8 + i];
+        m0 = fmaf(w[i], t[i], m0);
+        m1 = fmaf(w[8 + i], t[8 + i], m1);
       }
-      dot = lanes_sum<L>(dot) * inv_d;
+      const float r = p < 0 ? NAN : rsqrtf(lanes_sum<L>(q0 + q1) * inv_d + a.eps);
+      const float k = r * r * (lanes_sum<L>(m0 + m1) * inv_d);
+      const float rd = h < sd.H ? r : 0.f;         // rows that are not there are all zeros
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dy[i] = r * (dy[i] - n[i] * dot);
-      if (live) store_f32<T, 8>(out + h * sd.oh + col, dy);
+      for (int i = 0; i < 16; ++i) {
+        dw[i] = fmaf(rd, t[i], dw[i]);
+        e[i] = fmaf(-k, x[i], e[i] * w[i]) * r;
+      }
+      if (h < sd.H) store16<T, M>(out + h * sd.oh, ln, e);
     }
+    at.next();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   // heads of the warp, then warps, in order
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
 #pragma unroll
     for (int o = L; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-    if (sub == 0 && in) dws[warp][col + i] = dw[i];
+    if (sub == 0 && (i < 8 ? ln.in0 : ln.in1)) dws[warp][(i < 8 ? ln.c0 : ln.c1) + (i & 7)] = dw[i];
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < a.D; c += kThreads) {
+  for (int col = threadIdx.x; col < a.D; col += kThreads) {
     float t = 0.f;
-    for (int k = 0; k < kWarps; ++k) t += dws[k][c];
-    sd.part[(long long)block * a.D + c] = t;
+    for (int k = 0; k < kWarps; ++k) t += dws[k][col];
+    sd.part[(long long)block * a.D + col] = t;
   }
   if (threadIdx.x == 0) sd.bad[block] = bad;
 }
@@ -327,7 +481,9 @@ __global__ void __launch_bounds__(1024) dw_join_kernel(const Args a) {
         if (threadIdx.x == WS_STATUS) v = kStatusBounds;
         if (threadIdx.x == WS_BH) v = first;
         if (threadIdx.x == WS_QTILE) v = CHK_POSITION;
-        if (threadIdx.x == WS_EXPECT) v = (int)load_position(a, first);
+        if (threadIdx.x == WS_EXPECT && a.pos)
+          v = (int)load_index(a.pos, first / a.S * a.pos_stride + first % a.S, a.id_bits);
+        if (threadIdx.x == WS_EXPECT && !a.pos) v = first % a.S;
         if (threadIdx.x == WS_SEEN) v = (int)a.P;
       }
       a.header[threadIdx.x] = v;
@@ -352,10 +508,10 @@ __global__ void __launch_bounds__(1024) dw_join_kernel(const Args a) {
 
 // ---- host ---------------------------------------------------------------------------------
 
-template <typename T, int L, bool IL, bool FAST>
+template <typename T, int L, int M>
 dash_status_t launch(Args a, bool bwd, cudaStream_t stream) {
   constexpr int RW = 32 / L;
-  constexpr int U = sizeof(T) == 4 ? 2 : 4;
+  constexpr int U = sizeof(T) == 4 ? 1 : 2;
   // heads in flight a warp: U when that leaves every warp of the chip (about 10^4) an item,
   // else one, which spreads few tokens over more warps
   const long long rows = (long long)a.tokens * (a.side[0].H + a.side[1].H);
@@ -370,13 +526,13 @@ dash_status_t launch(Args a, bool bwd, cudaStream_t stream) {
   }
   const unsigned grid = a.side[0].blocks + a.side[1].blocks;
   if (grid > 0) {
-    if (bwd) {
-      if (many) bwd_kernel<T, L, IL, FAST, U><<<grid, kThreads, 0, stream>>>(a);
-      else bwd_kernel<T, L, IL, FAST, 1><<<grid, kThreads, 0, stream>>>(a);
-    } else {
-      if (many) fwd_kernel<T, L, IL, FAST, U><<<grid, kThreads, 0, stream>>>(a);
-      else fwd_kernel<T, L, IL, FAST, 1><<<grid, kThreads, 0, stream>>>(a);
-    }
+    const auto kernel = bwd ? (many ? bwd_kernel<T, L, M, U> : bwd_kernel<T, L, M, 1>)
+                            : (many ? fwd_kernel<T, L, M, U> : fwd_kernel<T, L, M, 1>);
+    const int smem = bwd ? (many ? kSharedBytes<T, U, true> : kSharedBytes<T, 1, true>)
+                         : (many ? kSharedBytes<T, U, false> : kSharedBytes<T, 1, false>);
+    if (smem > 32 * 1024)   // with the static part, more than a block has unasked
+      DASH_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    kernel<<<grid, kThreads, smem, stream>>>(a);
     DASH_TRY(cudaGetLastError());
   }
   if (bwd) DASH_TRY(launch_after(dw_join_kernel, dim3(2, ceil_div(a.D, 32)), 1024, 0, stream, a));
@@ -384,25 +540,23 @@ dash_status_t launch(Args a, bool bwd, cudaStream_t stream) {
 }
 
 template <typename T, int L>
-dash_status_t by_pairs(const Args& a, bool bwd, bool interleaved, cudaStream_t stream) {
-  if (interleaved)
-    return a.R % 8 == 0 ? launch<T, L, true, true>(a, bwd, stream) : launch<T, L, true, false>(a, bwd, stream);
-  if ((a.R / 2) % 8 == 0) return launch<T, L, false, true>(a, bwd, stream);
-  return launch<T, L, false, false>(a, bwd, stream);
+dash_status_t by_pairs(const Args& a, bool bwd, cudaStream_t stream) {
+  if (a.interleaved && a.R % 8 == 0) return launch<T, L, PAIRS>(a, bwd, stream);
+  if (!a.interleaved && a.R % 16 == 0) return launch<T, L, HALF>(a, bwd, stream);
+  return launch<T, L, ANY>(a, bwd, stream);
 }
 
 template <typename T>
-dash_status_t by_lanes(const Args& a, bool bwd, bool interleaved, cudaStream_t stream) {
-  const int lanes = a.D / 8;
-  if (lanes <= 8) return by_pairs<T, 8>(a, bwd, interleaved, stream);
-  if (lanes <= 16) return by_pairs<T, 16>(a, bwd, interleaved, stream);
-  return by_pairs<T, 32>(a, bwd, interleaved, stream);
+dash_status_t by_lanes(const Args& a, bool bwd, cudaStream_t stream) {
+  if (a.D <= 64) return by_pairs<T, 4>(a, bwd, stream);
+  if (a.D <= 128) return by_pairs<T, 8>(a, bwd, stream);
+  return by_pairs<T, 16>(a, bwd, stream);
 }
 
-dash_status_t by_type(const Args& a, bool bwd, bool interleaved, int dtype, cudaStream_t stream) {
-  if (dtype == DASH_BF16) return by_lanes<__nv_bfloat16>(a, bwd, interleaved, stream);
-  if (dtype == DASH_FP16) return by_lanes<__half>(a, bwd, interleaved, stream);
-  return by_lanes<float>(a, bwd, interleaved, stream);
+dash_status_t by_type(const Args& a, bool bwd, int dtype, cudaStream_t stream) {
+  if (dtype == DASH_BF16) return by_lanes<__nv_bfloat16>(a, bwd, stream);
+  if (dtype == DASH_FP16) return by_lanes<__half>(a, bwd, stream);
+  return by_lanes<float>(a, bwd, stream);
 }
 
 bool shape_ok(int B, int S, int Hq, int Hk, int D) {
@@ -440,7 +594,7 @@ dash_status_t check(const void* q, const void* k, const float* wq, const float* 
 
 Args common(const void* q, const void* k, const float* wq, const float* wk, const float* cos, const float* sin,
             const void* positions, int B, int S, int Hq, int Hk, int D, int R, long long P, const long long* qs,
-            const long long* ks, long long pos_stride, float eps, int id_bits) {
+            const long long* ks, long long pos_stride, float eps, int interleaved, int id_bits) {
   Args a = {};
   const void* xs[2] = {q, k};
   const float* ws[2] = {wq, wk};
@@ -466,6 +620,7 @@ Args common(const void* q, const void* k, const float* wq, const float* wk, cons
   a.D = D;
   a.R = R;
   a.eps = eps;
+  a.interleaved = interleaved;
   return a;
 }
 
@@ -486,7 +641,7 @@ dash_status_t dash_qk_norm_rope_fwd(const void* q, const void* k, const float* w
   if (any && ((Hq > 0 && !q_out) || (Hk > 0 && !k_out))) return DASH_ERR_INVALID_ARG;
   if (!is_aligned(q_out, 16) || !is_aligned(k_out, 16) || !is_aligned(status, 4)) return DASH_ERR_INVALID_ARG;
   Args a = common(q, k, wq, wk, cos, sin, positions, B, S, Hq, Hk, D, R, P, q_strides, k_strides, pos_stride,
-                  eps, id_bits);
+                  eps, interleaved, id_bits);
   void* outs[2] = {q_out, k_out};
   for (int i = 0; i < 2; ++i) {
     Side& sd = a.side[i];
@@ -498,7 +653,7 @@ dash_status_t dash_qk_norm_rope_fwd(const void* q, const void* k, const float* w
   a.status = status;
   if (status) DASH_TRY(cudaMemsetAsync(status, 0, sizeof(int), stream));
   if (!any) return DASH_OK;
-  return by_type(a, false, interleaved != 0, dtype, stream);
+  return by_type(a, false, dtype, stream);
 }
 
 size_t dash_qk_norm_rope_bwd_workspace_size(int B, int S, int Hq, int Hk, int D) {
@@ -527,7 +682,7 @@ dash_status_t dash_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
   if (!is_aligned(dwq, 4) || !is_aligned(dwk, 4) || !is_aligned(workspace, 256)) return DASH_ERR_INVALID_ARG;
   if (workspace_bytes < dash_qk_norm_rope_bwd_workspace_size(B, S, Hq, Hk, D)) return DASH_ERR_WORKSPACE_TOO_SMALL;
   Args a = common(q, k, wq, wk, cos, sin, positions, B, S, Hq, Hk, D, R, P, q_strides, k_strides, pos_stride,
-                  eps, id_bits);
+                  eps, interleaved, id_bits);
   const void* douts[2] = {dq_out, dk_out};
   void* outs[2] = {dq, dk};
   float* dws[2] = {dwq, dwk};
@@ -545,7 +700,7 @@ dash_status_t dash_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
     sd.bad = (int*)(part + (size_t)2 * (kBwdBlocks + 1) * D) + i * (kBwdBlocks + 1);
   }
   a.header = (int*)workspace;
-  return by_type(a, true, interleaved != 0, dtype, stream);
+  return by_type(a, true, dtype, stream);
 }
 
 }  // extern "C"

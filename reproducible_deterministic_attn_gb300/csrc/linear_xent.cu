@@ -17,7 +17,7 @@ using dash::round_up_to;
 // bytes (a piece is at least one 256-column tile).
 constexpr size_t kPieceBytes = 256ull << 20;
 constexpr int kMinSplitKSteps = 8;      // a K range of dX is at least 512 wide
-constexpr int kSplitTarget = 152;       // units that a split dX aims for (one GB300's SMs)
+constexpr int kSplitTarget = 76;        // units that a split dX aims for (one GB300's pairs of SMs)
 
 struct Plan {
   long long piece;            // vocabulary rows a piece, a multiple of 256
@@ -114,7 +114,7 @@ dash_status_t launch(Params p, const Maps& maps, int sms, bool first, cudaStream
     return DASH_ERR_UNSUPPORTED;
   }
   DASH_TRY(cudaFuncSetAttribute(gemm_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-  const int grid = (int)std::min<long long>(units, sms);
+  const int grid = 2 * (int)std::min<long long>(units, sms / 2);
   if (first) {
     gemm_kernel<OP><<<grid, kXentThreads, kSmem, stream>>>(p, maps);
     DASH_TRY(cudaGetLastError());
@@ -161,7 +161,7 @@ dash_status_t dash_linear_xent_fwd(const void* x, const void* w, const void* tar
   }
   const Plan pl = make_plan(T, V, D);
   Maps maps;
-  if (!map_2d(&maps.a, x, T, D, ldx, kTM) || !map_2d(&maps.b, w, V, D, ldw, kTN)) return bad_map();
+  if (!map_2d(&maps.a, x, T, D, ldx, kCtaM) || !map_2d(&maps.b, w, V, D, ldw, kCtaN)) return bad_map();
   Params p = {};
   p.M = (int)T;
   p.N = (int)V;
@@ -227,7 +227,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   base.timeout_ns = dash::sync_timeout_ns();
   base.splits = 1;
   Maps grad, dxm, dwm;
-  if (!map_2d(&grad.a, x, T, D, ldx, kTM) || !map_2d(&grad.b, w, V, D, ldw, kTN) ||
+  if (!map_2d(&grad.a, x, T, D, ldx, kCtaM) || !map_2d(&grad.b, w, V, D, ldw, kCtaN) ||
       !map_2d(&dxm.b, w, V, D, ldw, kTK) || !map_2d(&dwm.b, x, T, D, ldx, kTK))
     return bad_map();
   check_targets_kernel<<<1, 1024, 0, stream>>>(
@@ -236,7 +236,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   for (int i = 0; i < pl.pieces; ++i) {
     const long long v0 = i * pl.piece, vp = std::min(pl.piece, V - v0);
     const bool first = i == 0, last = i == pl.pieces - 1;
-    if (!map_2d(&dxm.a, g, T, vp, pl.ldg, kTM) || !map_2d(&dwm.a, g, T, vp, pl.ldg, kTK)) return bad_map();
+    if (!map_2d(&dxm.a, g, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a, g, T, vp, pl.ldg, kTK)) return bad_map();
     Params p = base;
     p.b_row0 = (int)v0;
     // G of the piece

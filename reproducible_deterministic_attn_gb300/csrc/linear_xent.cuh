@@ -1,16 +1,24 @@
 // Softmax cross entropy from hidden states (X [T, D], W [V, D], both bf16) without stored
 // logits, and its gradient. Four products share one persistent tensor-core kernel:
-//   LSE   Z = X W^T        a 128 x 256 tile of logits is reduced to (max, sum of exp2) per
+//   LSE   Z = X W^T        a 256 x 256 tile of logits is reduced to (max, sum of exp2) per
 //                          row and half tile; the target's logit is stored
 //   GRAD  Z = X W^T again  the tile becomes G = g (exp(z - lse) - [v = y]) in bf16
 //   DX    dX = G W         K = the vocabulary (of one piece), W read N-major
 //   DW    dW = G^T X       K = the tokens, both operands MN-major
-// A unit of work is one output tile of 128 x 256 (for DX one K range of it), dealt round
-// robin to one CTA per SM.
+// A unit of work is one output tile of 256 x 256 (for DX one K range of it), dealt round robin
+// to pairs of CTAs on neighbouring SMs (cta_group::2): each CTA loads its 128 rows of A and
+// its 128 columns of B, one thread of the pair issues MMAs of 256 x 256 x 16 over both, and
+// each CTA's TMEM gets its 128 rows of the product. So an SM reads half of B that a tile of
+// its own would need.
 //
-// Warp roles (384 threads): 0 = TMA producer (64 of K per stage, 4 stages of 48 KB), 1 = MMA
-// issuer, 4..11 = epilogue (one 32-row quarter and one half of the columns each). Two
-// 256-column accumulators in TMEM, so that the next tile's MMAs run while one is read out.
+// Warp roles (384 threads a CTA): 0 = TMA producer (64 of K per stage, 6 stages of 32 KB), 1 =
+// MMA issuer (the pair's first CTA), 4..11 = epilogue (one 32-row quarter and one half of the
+// columns each). Two 256-column accumulators in TMEM, so that the next tile's MMAs run while
+// one is read out.
+//
+// Barriers: a stage's FULL and an accumulator's EMPTY live in the first CTA, where the issuer
+// waits for both CTAs' copies and read-outs; a stage's EMPTY and an accumulator's FULL live in
+// both, arrived at by the issuer's commits.
 #pragma once
 
 #include "tc_shared.cuh"
@@ -62,16 +70,18 @@ struct Maps {
 };
 
 constexpr int kXentThreads = 384;
-constexpr int kTM = 128, kTN = 256, kTK = 64;
-constexpr int kStages = 4;
-constexpr int kGroupM = 16;
-constexpr int kABytes = kTM * kTK * 2, kBBytes = kTN * kTK * 2;
+constexpr int kTM = 256, kTN = 256, kTK = 64;         // of a pair
+constexpr int kCtaM = kTM / 2, kCtaN = kTN / 2;       // what one CTA loads
+constexpr int kStages = 6;
+constexpr int kGroupM = 8;
+constexpr int kABytes = kCtaM * kTK * 2, kBBytes = kCtaN * kTK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kBarOff = kStages * kStageBytes;
 constexpr int kSmem = kBarOff + 256 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 enum { B_FULL = 0, B_EMPTY = B_FULL + kStages, B_ACC_FULL = B_EMPTY + kStages,
        B_ACC_EMPTY = B_ACC_FULL + 2, B_DRAIN = B_ACC_EMPTY + 2, B_COUNT };
+static_assert(8 * B_COUNT + 8 <= 256, "barrier space");
 
 // Unit -> (m tile, n tile, K range). Tiles are numbered in groups of kGroupM m-tiles, m
 // first, so that concurrent units share their A and B panels in L2.
@@ -128,7 +138,7 @@ __device__ __forceinline__ void put_f32(float* dst, const float (&v)[32], int n)
 }
 
 template <int OP>
-__global__ void __launch_bounds__(kXentThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
     gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   constexpr bool A_MN = OP == DW, B_MN = OP == DX || OP == DW;
   extern __shared__ uint8_t smem_xent[];
@@ -138,6 +148,8 @@ __global__ void __launch_bounds__(kXentThreads, 1)
   uint32_t* tmem_slot = (uint32_t*)(sm + kBarOff + 8 * B_COUNT);
   volatile int* abort_flag = (volatile int*)(sm + kBarOff + 8 * B_COUNT + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)ptx::cluster_rank();               // 0: the pair's first CTA
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const long long tmo = p.timeout_ns;
   const int units = p.tiles_m * p.tiles_n * p.splits;
   const int ksteps = (p.K + kTK - 1) / kTK;
@@ -149,15 +161,16 @@ __global__ void __launch_bounds__(kXentThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(bars + B_ACC_FULL + a, 1);
-      ptx::mbar_init(bars + B_ACC_EMPTY + a, 8);
+      ptx::mbar_init(bars + B_ACC_EMPTY + a, 16);          // 8 epilogue warps of each CTA
     }
     ptx::mbar_init(bars + B_DRAIN, 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 1) ptx::tmem_alloc(tmem_slot, 512);
+  __syncwarp();
+  if (warp == 1) ptx::tmem_alloc_pair(tmem_slot, 512);
   ptx::tc_fence_before();
-  __syncthreads();
+  ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   train::grid_wait();
@@ -167,42 +180,41 @@ __global__ void __launch_bounds__(kXentThreads, 1)
     if (lane == 0) {
       long long kb = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = pair; ok && u < units; u += pairs) {
         int mi, ni, split;
         unit_of(p, u, mi, ni, split);
-        const int m0 = mi * kTM, n0 = ni * kTN;
+        const int m0 = mi * kTM + rank * kCtaM, n0 = ni * kTN + rank * kCtaN;
         const int k_end = min(ksteps, (split + 1) * p.ksteps_per_split);
         for (int k = split * p.ksteps_per_split; k < k_end; ++k, ++kb) {
           const int s = (int)(kb % kStages);
           if (kb >= kStages &&
               !(ok = ptx::mbar_wait(bars + B_EMPTY + s, (int)((kb / kStages) - 1) & 1, abort_flag, tmo)))
             break;
-          uint64_t* full = bars + B_FULL + s;
+          // the first CTA expects both CTAs' bytes; the other's may arrive before that
+          const uint32_t full = ptx::peer_smem(bars + B_FULL + s, 0);
+          if (rank == 0) ptx::mbar_expect_tx(bars + B_FULL + s, 2 * kStageBytes);
           uint8_t* sa = sm + s * kStageBytes;
           uint8_t* sb = sa + kABytes;
           const int k0 = k * kTK;
-          ptx::mbar_expect_tx(full, kStageBytes);
           if (A_MN) {
-            for (int i = 0; i < kTM / 64; ++i)
-              ptx::tma_load_2d(sa + i * 8192, &maps.a, m0 + i * 64, k0, full);
+            for (int i = 0; i < kCtaM / 64; ++i)
+              ptx::tma_load_2d_pair(sa + i * 8192, &maps.a, m0 + i * 64, k0, full);
           } else {
-            ptx::tma_load_2d(sa, &maps.a, k0, m0, full);
+            ptx::tma_load_2d_pair(sa, &maps.a, k0, m0, full);
           }
           if (B_MN) {
             const int kr = OP == DX ? p.b_row0 + k0 : k0;
-            for (int i = 0; i < kTN / 64; ++i)
-              ptx::tma_load_2d(sb + i * 8192, &maps.b, n0 + i * 64, kr, full);
+            for (int i = 0; i < kCtaN / 64; ++i)
+              ptx::tma_load_2d_pair(sb + i * 8192, &maps.b, n0 + i * 64, kr, full);
           } else {
-            ptx::tma_load_2d(sb, &maps.b, k0, p.b_row0 + n0, full);
+            ptx::tma_load_2d_pair(sb, &maps.b, k0, p.b_row0 + n0, full);
           }
         }
       }
-      for (long long k = (kb > kStages ? kb - kStages : 0); k < kb; ++k)
-        ptx::mbar_drain(bars + B_FULL + (int)(k % kStages), (int)(k / kStages) & 1, 100000000ll);
     }
   } else if (warp == 1) {
     // ====================================== MMA issuer ======================================
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       constexpr uint32_t ID = ptx::idesc_bf16(kTM, kTN, A_MN, B_MN);
       // a K step of 16: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major block
       constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
@@ -210,7 +222,7 @@ __global__ void __launch_bounds__(kXentThreads, 1)
       long long kb = 0;
       int it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++it) {
+      for (int u = pair; ok && u < units; u += pairs, ++it) {
         const int acc = it & 1;
         int mi, ni, split;
         unit_of(p, u, mi, ni, split);
@@ -227,26 +239,25 @@ __global__ void __launch_bounds__(kXentThreads, 1)
           const uint32_t b_lo = ptx::sdesc_lo(s0 + s * kStageBytes + kABytes, B_MN ? 8192 : 16);
 #pragma unroll
           for (int ks = 0; ks < kTK / 16; ++ks)
-            ptx::mma_lo(tmem + acc * kTN, a_lo + ks * A_STEP, b_lo + ks * B_STEP, ID,
-                        (k > k_begin || ks > 0) ? 1u : 0u);
-          ptx::mma_commit(bars + B_EMPTY + s);
+            ptx::mma_lo_pair(tmem + acc * kTN, a_lo + ks * A_STEP, b_lo + ks * B_STEP, ID,
+                             (k > k_begin || ks > 0) ? 1u : 0u);
+          ptx::mma_commit_pair(bars + B_EMPTY + s);
         }
         if (!ok) break;
-        ptx::mma_commit(bars + B_ACC_FULL + acc);
+        ptx::mma_commit_pair(bars + B_ACC_FULL + acc);
       }
-      ptx::mma_commit(bars + B_DRAIN);
-      ptx::mbar_drain(bars + B_DRAIN, 0, 1000000000ll);
+      ptx::mma_commit_pair(bars + B_DRAIN);
     }
   } else if (warp >= 4) {
     // ======================================= epilogue =======================================
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
     int it = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++it) {
+    for (int u = pair; u < units; u += pairs, ++it) {
       const int acc = it & 1;
       int mi, ni, split;
       unit_of(p, u, mi, ni, split);
-      const int row = mi * kTM + quarter * 32 + lane;
+      const int row = mi * kTM + rank * kCtaM + quarter * 32 + lane;
       const int col0 = ni * kTN + half * (kTN / 2);
       const bool live = row < p.M;
       // what the row needs besides the tile, fetched before the wait
@@ -324,16 +335,20 @@ __global__ void __launch_bounds__(kXentThreads, 1)
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + B_ACC_EMPTY + acc);
+      if (lane == 0) ptx::mbar_arrive_peer(ptx::peer_smem(bars + B_ACC_EMPTY + acc, 0));
       if (OP == LSE && live) p.part[(size_t)(ni * 2 + half) * p.M + row] = make_float2(m2, sum);
     }
   }
 
+  // Every MMA and with it every copy of the pair has ended once DRAIN completes; neither CTA
+  // leaves before the other, whose barriers and copies it may signal.
+  if (threadIdx.x == 0) ptx::mbar_drain(bars + B_DRAIN, 0, 1000000000ll);
+  __syncwarp();
   ptx::tc_fence_before();
-  __syncthreads();
+  ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc_pair(tmem, 512);
   }
   if (threadIdx.x == 0 && *abort_flag && atomicCAS(p.header + WS_STATUS, 0, kStatusSyncTimeout) == 0) {
     p.header[WS_BH] = -1;

@@ -204,7 +204,8 @@ void dash_attn_shutdown(void);
  * Testing hook for the failure paths. Sets, for later dash_attn_bwd and dash_attn_fwd(_ex)
  * calls in this process, the time limit of one wait (timeout_ns <= 0 restores the default
  * of 10 s) and a skew. In the backward the skew is added to every awaited dQ ordinal; in
- * the forward a skew > 0 makes the kernel load no K/V tiles. Either way no wait on them
+ * the forward a skew > 0 makes the kernel load no K/V tiles (dash_linear_xent_*, dash_train.h:
+ * no tiles at all, DASH_ERR_SYNC_TIMEOUT in the workspace). Either way no wait on them
  * can be satisfied: each one runs out its limit, the kernel records DASH_ERR_SYNC_TIMEOUT
  * (backward: in the workspace; forward: in dash_attn_fwd_ex's status word) and returns,
  * and the CUDA context stays usable. Not thread-safe against concurrent calls.

@@ -351,6 +351,7 @@ namespace dash {
 void set_last_error(const std::string& text) { g_last_error = text; }
 EncodeTiledFn tensor_map_encoder() { return encoder(); }
 long long sync_timeout_ns() { return g_timeout_ns; }
+bool sync_withheld() { return g_ordinal_skew > 0; }
 }  // namespace dash
 
 extern "C" {

@@ -26,6 +26,8 @@ EncodeTiledFn tensor_map_encoder();
 
 // Bound on one in-kernel wait (dash_debug_set_sync).
 long long sync_timeout_ns();
+// Whether the testing hook asks for waits that cannot be satisfied (a skew > 0).
+bool sync_withheld();
 
 inline dash_status_t cuda_failed(cudaError_t e, const char* what) {
   set_last_error(std::string(what) + ": " + cudaGetErrorString(e));

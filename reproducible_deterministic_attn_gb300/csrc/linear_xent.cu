@@ -178,6 +178,7 @@ dash_status_t dash_linear_xent_fwd(const void* x, const void* w, const void* tar
   p.V = V;
   p.header = (int*)ws;
   p.timeout_ns = dash::sync_timeout_ns();
+  p.withhold = dash::sync_withheld();
   DASH_TRY(cudaMemsetAsync(ws, 0, dash::kWsHeaderBytes, stream));
   st = launch<LSE>(p, maps, sms, true, stream);
   if (st != DASH_OK) return st;
@@ -225,6 +226,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   base.V = V;
   base.header = (int*)ws;
   base.timeout_ns = dash::sync_timeout_ns();
+  base.withhold = dash::sync_withheld();
   base.splits = 1;
   Maps grad, dxm, dwm;
   if (!map_2d(&grad.a, x, T, D, ldx, kCtaM) || !map_2d(&grad.b, w, V, D, ldw, kCtaN) ||

@@ -63,6 +63,7 @@ struct Params {
   float* acc;                // DX: fp32 [M][N] over the pieces, or the K ranges' partials
   int* header;
   long long timeout_ns;
+  int withhold;              // testing hook: load no tiles, so the waits for them run out
 };
 
 struct Maps {
@@ -155,6 +156,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
   const int ksteps = (p.K + kTK - 1) / kTK;
 
   if (threadIdx.x == 0) {
+    ptx::prefetch_map(&maps.a);
+    ptx::prefetch_map(&maps.b);
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(bars + B_FULL + s, 1);
       ptx::mbar_init(bars + B_EMPTY + s, 1);
@@ -179,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
     // ===================================== TMA producer =====================================
     if (lane == 0) {
       long long kb = 0;
-      bool ok = true;
+      bool ok = p.withhold == 0;
       for (int u = pair; ok && u < units; u += pairs) {
         int mi, ni, split;
         unit_of(p, u, mi, ni, split);

@@ -229,3 +229,23 @@ def test_gradient_matches_differences_of_the_forward():
     tol = float((dl.double().abs() * (h * h / 6 * dz ** 3 + 2.0 ** -16 / h)).sum()
                 + 2 * U * ref.xent_grad(x, w, y, dl, IGN)[2].abs().sum() * dz)
     assert abs((L(up) - L(dn)) / (2 * h) - got) <= tol
+
+
+def test_waits_that_run_out_are_reported_and_the_context_survives():
+    """The testing hook withholds the tiles: every wait for them runs out, the workspace says
+    so, and the next call computes the normal result."""
+    x, w, y, dl = _inputs(300, 600, 64, seed=17)
+    ws = da.new_linear_xent_workspace(300, 600, 64, "cuda")
+    loss, lse = da.linear_xent_forward(x, w, y, workspace=ws)
+    want = (loss, lse) + da.linear_xent_backward(x, w, y, lse, dl, workspace=ws)
+    try:
+        da.dash_debug_set_sync(50_000_000, 1)
+        da.linear_xent_forward(x, w, y, workspace=ws, check=False)
+        assert da.dash_attn_get_status(ws) == da.DASH_ERR_SYNC_TIMEOUT
+        da.linear_xent_backward(x, w, y, lse, dl, workspace=ws, check=False)
+        assert da.dash_attn_get_status(ws) == da.DASH_ERR_SYNC_TIMEOUT
+    finally:
+        da.dash_debug_set_sync(0, 0)
+    loss, lse = da.linear_xent_forward(x, w, y, workspace=ws)
+    got = (loss, lse) + da.linear_xent_backward(x, w, y, lse, dl, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -352,6 +352,23 @@ void set_last_error(const std::string& text) { g_last_error = text; }
 EncodeTiledFn tensor_map_encoder() { return encoder(); }
 long long sync_timeout_ns() { return g_timeout_ns; }
 bool sync_withheld() { return g_ordinal_skew > 0; }
+cudaError_t allow_shared(const void* kernel, int bytes) {
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, int> allowed;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  try {
+    std::lock_guard<std::mutex> lk(mu);
+    int& have = allowed[{kernel, dev}];
+    if (have >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) have = bytes;
+    return e;
+  } catch (const std::exception&) {   // no memory for the note: ask every time
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  }
+}
 }  // namespace dash
 
 extern "C" {

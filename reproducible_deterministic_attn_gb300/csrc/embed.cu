@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kRowThreads)
   unsigned key = keys[0];
   bool begun = run > 0 && keys[-1] == key;
   float acc[N] = {};
-  constexpr int U = 8;
+  constexpr int U = 8;                             // rows in flight a thread (16: 17 -> 23 us for 16384 x 2048)
 #pragma unroll 1
   for (int p = 0; p < n && key < V; p += U) {
     Cols<TI, N, STRIDED> v[U];
@@ -600,8 +600,7 @@ dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, vo
   s.toks[0] = (unsigned*)(ws + l.toks0);
   s.toks[1] = (unsigned*)(ws + l.toks1);
   const size_t smem = ((size_t)(kSortWarps + 2) << s.digit_bits) * 4;
-  DASH_TRY(cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)(((size_t)(kSortWarps + 2) << kMaxDigitBits) * 4)));
+  DASH_TRY(allow_shared((const void*)embed_sort_kernel, (int)(((size_t)(kSortWarps + 2) << kMaxDigitBits) * 4)));
   embed_sort_kernel<<<kSortCtas, kSortThreads, smem, stream>>>(s);
   DASH_TRY(cudaGetLastError());
   if (!accumulate)

@@ -39,6 +39,10 @@ inline size_t round_up_to(size_t x, size_t a) { return (x + a - 1) / a * a; }
 template <typename T>
 inline T ceil_div(T a, T b) { return (a + b - 1) / b; }
 
+// Lets a kernel use `bytes` of dynamic shared memory on the current device (asked of the driver
+// once for each kernel and device).
+cudaError_t allow_shared(const void* kernel, int bytes);
+
 // Launches a kernel that may start while the kernel before it on `stream` is still running:
 // its blocks take their places as that one's leave, and wait for its results with
 // grid_wait() before they touch memory. The kernel before must have called grid_next().

@@ -113,7 +113,7 @@ dash_status_t launch(Params p, const Maps& maps, int sms, bool first, cudaStream
     dash::set_last_error("too many output tiles for one call");
     return DASH_ERR_UNSUPPORTED;
   }
-  DASH_TRY(cudaFuncSetAttribute(gemm_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  DASH_TRY(dash::allow_shared((const void*)gemm_kernel<OP>, kSmem));
   const int grid = 2 * (int)std::min<long long>(units, sms / 2);
   if (first) {
     gemm_kernel<OP><<<grid, kXentThreads, kSmem, stream>>>(p, maps);

@@ -530,8 +530,7 @@ dash_status_t launch(Args a, bool bwd, cudaStream_t stream) {
                             : (many ? fwd_kernel<T, L, M, U> : fwd_kernel<T, L, M, 1>);
     const int smem = bwd ? (many ? kSharedBytes<T, U, true> : kSharedBytes<T, 1, true>)
                          : (many ? kSharedBytes<T, U, false> : kSharedBytes<T, 1, false>);
-    if (smem > 32 * 1024)   // with the static part, more than a block has unasked
-      DASH_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    DASH_TRY(allow_shared((const void*)kernel, smem));
     kernel<<<grid, kThreads, smem, stream>>>(a);
     DASH_TRY(cudaGetLastError());
   }

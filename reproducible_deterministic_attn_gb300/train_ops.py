@@ -21,11 +21,11 @@ from .dash_attn import DASH_ERR_UNSUPPORTED, DashError, dash_attn_get_status
 DASH_BF16, DASH_FP16, DASH_FP32 = 0, 1, 2
 _DTYPE = {torch.bfloat16: DASH_BF16, torch.float16: DASH_FP16, torch.float32: DASH_FP32}
 _ID_BITS = {torch.int32: 32, torch.int64: 64}
+_F32, _BF16 = torch.float32, torch.bfloat16
 
 _c_int, _c_float, _c_size, _vp, _ll = (ctypes.c_int, ctypes.c_float, ctypes.c_size_t,
                                        ctypes.c_void_p, ctypes.c_longlong)
 
-_llp = ctypes.POINTER(_ll)
 _c3 = _ll * 3
 
 
@@ -38,11 +38,10 @@ _core._SIGNATURES.update({
     "dash_embed_bwd_workspace_size": (_c_size, [_ll, _ll, _c_int]),
     "dash_embed_bwd": (_c_int, [_vp] * 4 + [_c_size, _ll, _ll, _c_int, _ll, _c_float, _ll] + [_c_int] * 4
                        + [_vp]),
-    "dash_qk_norm_rope_fwd": (_c_int, [_vp] * 10 + [_c_int] * 6 + [_ll, _llp, _llp, _ll, _c_float]
+    "dash_qk_norm_rope_fwd": (_c_int, [_vp] * 10 + [_c_int] * 6 + [_ll, _vp, _vp, _ll, _c_float]
                               + [_c_int] * 3 + [_vp]),
     "dash_qk_norm_rope_bwd_workspace_size": (_c_size, [_c_int] * 5),
-    "dash_qk_norm_rope_bwd": (_c_int, [_vp] * 14 + [_c_size] + [_c_int] * 6 + [_ll, _llp, _llp, _llp, _llp,
-                                                                              _ll, _c_float]
+    "dash_qk_norm_rope_bwd": (_c_int, [_vp] * 14 + [_c_size] + [_c_int] * 6 + [_ll] + [_vp] * 4 + [_ll, _c_float]
                               + [_c_int] * 3 + [_vp]),
     "dash_grad_clip_plan_size": (_c_size, [ctypes.POINTER(_ClipTensor), _c_int]),
     "dash_grad_clip_plan": (_c_int, [ctypes.POINTER(_ClipTensor), _c_int, _vp, _c_size, _vp]),
@@ -56,7 +55,7 @@ _core._SIGNATURES.update({
 
 
 # The checks below run on every call, next to kernels of a few microseconds: conditions first,
-# messages only once one has failed.
+# messages only once one has failed. A device is its index, -1 for the host.
 
 def _raise(status: int, where: str):
     if status:
@@ -67,57 +66,62 @@ def _bad(what: str):
     raise ValueError(what)
 
 
-def _stream(t, stream) -> int:
-    """The raw handle of `stream`, or of torch's current stream on t's device."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.device.index)
-    return _core._stream(t, stream)
-
-
-def _cuda(t, name: str, device=None):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _device(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
         _bad(f"{name}: expected a CUDA tensor")
-    if device is not None and t.device != device:
-        _bad(f"{name}: expected a tensor on {device}")
+    return dev
+
+
+def _on(t, name: str, dev: int):
+    if t.get_device() != dev:
+        _bad(f"{name}: expected a tensor on cuda:{dev}")
+
+
+def _stream(dev: int, stream) -> int:
+    """The raw handle of `stream`, or of torch's current stream on the device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rows(t, name: str):
-    """A 2-D tensor whose rows are contiguous; returns the elements between rows."""
-    if t.dim() != 2 or (t.shape[1] != 1 and t.stride(1) != 1):
-        _bad(f"{name}: expected 2-D rows of contiguous elements")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    """A 2-D tensor whose rows are contiguous: its sizes and the elements between rows."""
+    if t.dim() != 2:
+        _bad(f"{name}: expected two dimensions")
+    n, d = t.shape
+    ld, one = t.stride()
+    if one != 1 and d > 1:
+        _bad(f"{name}: expected rows of contiguous elements")
+    return n, d, ld if n > 1 else max(d, 1)
 
 
-def _index(t, name: str, device):
-    _cuda(t, name, device)
+def _index(t, name: str, dev: int):
     bits = _ID_BITS.get(t.dtype)
-    if bits is None or not t.is_contiguous():
-        _bad(f"{name}: expected contiguous int32 or int64")
+    if bits is None or t.get_device() != dev or not t.is_contiguous():
+        _bad(f"{name}: expected contiguous int32 or int64 on cuda:{dev}")
     return bits
 
 
-def _vector(t, name: str, n: int, device):
+def _vector(t, name: str, n: int, dev: int):
     """A contiguous fp32 [n] tensor's address."""
-    _cuda(t, name, device)
-    if t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
-        _bad(f"{name}: expected contiguous float32 [{n}]")
+    if t.dtype != _F32 or t.get_device() != dev or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        _bad(f"{name}: expected contiguous float32 [{n}] on cuda:{dev}")
     return t.data_ptr()
 
 
-def _status_word(t, device):
+def _status_word(t, dev: int):
     if t is None:
         return None
-    _cuda(t, "status", device)
-    if t.dtype != torch.int32 or t.numel() != 1:
-        _bad("status: expected one int32")
+    if t.dtype != torch.int32 or t.numel() != 1 or t.get_device() != dev:
+        _bad(f"status: expected one int32 on cuda:{dev}")
     return t.data_ptr()
 
 
-def _ws(workspace, device):
-    _cuda(workspace, "workspace", device)
-    if not workspace.is_contiguous():
-        _bad("workspace: expected contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def _ws(t, dev: int):
+    if t.get_device() != dev or not t.is_contiguous():
+        _bad(f"workspace: expected a contiguous tensor on cuda:{dev}")
+    return t.data_ptr(), t.nbytes
 
 
 def _finish(workspace, stream, check: bool, where: str):
@@ -133,22 +137,20 @@ def embed_forward(table, ids, scale: float = 1.0, out=None, status=None, stream=
     table: [V, D] bf16, fp16 or fp32 with contiguous rows; ids: contiguous int32 or int64 of
     any shape. status: an optional int32 CUDA tensor of one element, which reads
     DASH_ERR_BOUNDS when an id was out of range (its row is NaN). Returns [*ids.shape, D]."""
-    _cuda(table, "table")
-    dtype, dev = table.dtype, table.device
-    if dtype not in _DTYPE:
+    dev = _device(table, "table")
+    dtype = _DTYPE.get(table.dtype)
+    if dtype is None:
         _bad("table: expected bfloat16, float16 or float32")
-    ld = _rows(table, "table")
+    V, D, ld = _rows(table, "table")
     bits = _index(ids, "ids", dev)
-    V, D = table.shape
     if out is None:
-        out = torch.empty((*ids.shape, D), dtype=dtype, device=dev)
-    else:
-        _cuda(out, "out", dev)
-        if out.dtype != dtype or out.shape != (*ids.shape, D) or not out.is_contiguous():
-            _bad("out: expected contiguous [*ids.shape, D] of the table's type")
+        out = table.new_empty((*ids.shape, D))
+    elif (out.dtype != table.dtype or out.shape != (*ids.shape, D) or not out.is_contiguous()
+          or out.get_device() != dev):
+        _bad(f"out: expected contiguous [*ids.shape, D] of the table's type on cuda:{dev}")
     _raise(_core.load().dash_embed_fwd(
         table.data_ptr(), ids.data_ptr(), out.data_ptr(), _status_word(status, dev), ids.numel(), V, D, ld, D,
-        scale, _DTYPE[dtype], bits, _stream(table, stream)), "dash_embed_fwd")
+        scale, dtype, bits, _stream(dev, stream)), "dash_embed_fwd")
     return out
 
 
@@ -171,37 +173,38 @@ def embed_backward(dout, ids, vocab: int, scale: float = 1.0, padding_idx=None, 
     dout: [*ids.shape, D] (2-D: rows may be strided); ids as in embed_forward. padding_idx:
     an id whose tokens are left out. dtable: an optional contiguous [vocab, D] tensor of
     dout's type or fp32 to write to, or to add to with accumulate=True. Returns dtable."""
-    _cuda(dout, "dout")
-    dtype, dev = dout.dtype, dout.device
-    if dtype not in _DTYPE:
+    dev = _device(dout, "dout")
+    dtype = _DTYPE.get(dout.dtype)
+    if dtype is None:
         _bad("dout: expected bfloat16, float16 or float32")
     bits = _index(ids, "ids", dev)
-    if dout.dim() < 1 or dout.shape[:-1] != ids.shape:
+    shape = dout.shape
+    if not shape or shape[:-1] != ids.shape:
         _bad("dout: expected [*ids.shape, D]")
-    T, D = ids.numel(), dout.shape[-1]
-    if dout.dim() == 2:
-        ld = _rows(dout, "dout")
+    T, D = ids.numel(), shape[-1]
+    if len(shape) == 2:
+        ld = _rows(dout, "dout")[2]
     else:
         if not dout.is_contiguous():
             _bad("dout: expected contiguous")
-        ld = D
+        ld = max(D, 1)
     if dtable is None:
         if accumulate:
             _bad("accumulate: needs dtable")
-        dtable = torch.empty((vocab, D), dtype=dtype, device=dev)
-    else:
-        _cuda(dtable, "dtable", dev)
-        if dtable.dtype not in (dtype, torch.float32) or dtable.shape != (vocab, D) or not dtable.is_contiguous():
-            _bad("dtable: expected contiguous [vocab, D] of dout's type or float32")
-    if padding_idx is not None and not 0 <= padding_idx < vocab:
+        dtable = dout.new_empty((vocab, D))
+    elif (dtable.dtype not in (dout.dtype, _F32) or dtable.shape != (vocab, D) or not dtable.is_contiguous()
+          or dtable.get_device() != dev):
+        _bad(f"dtable: expected contiguous [vocab, D] of dout's type or float32 on cuda:{dev}")
+    if padding_idx is None:
+        padding_idx = -1
+    elif not 0 <= padding_idx < vocab:
         _bad("padding_idx: out of range")
     if workspace is None:
-        workspace = new_embed_workspace(T, vocab, D, dev)
+        workspace = new_embed_workspace(T, vocab, D, dout.device)
     ws, nbytes = _ws(workspace, dev)
     _raise(_core.load().dash_embed_bwd(
-        dout.data_ptr(), ids.data_ptr(), dtable.data_ptr(), ws, nbytes, T, vocab, D, ld, scale,
-        -1 if padding_idx is None else padding_idx, int(accumulate), _DTYPE[dtype], _DTYPE[dtable.dtype], bits,
-        _stream(dout, stream)), "dash_embed_bwd")
+        dout.data_ptr(), ids.data_ptr(), dtable.data_ptr(), ws, nbytes, T, vocab, D, ld, scale, padding_idx,
+        accumulate, dtype, _DTYPE[dtable.dtype], bits, _stream(dev, stream)), "dash_embed_bwd")
     _finish(workspace, stream, check, "dash_embed_bwd")
     return dtable
 
@@ -218,36 +221,39 @@ def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, device="c
 
 @functools.lru_cache(maxsize=1024)
 def _strides(batch: int, token: int, head: int):
-    return _c3(batch, token, head)
+    """Three strides as the C calls read them: the array (kept by the cache while calls use it)
+    and its address."""
+    arr = _c3(batch, token, head)
+    return arr, ctypes.addressof(arr)
 
 
-def _heads(t, name: str):
+def _heads(t, name: str, dtype, dev: int):
     """[B, S, H, D] with contiguous D: its sizes and its {batch, token, head} strides. Strides of
     dimensions of one element are never used and count as zero."""
-    if t.dim() != 4 or (t.shape[3] != 1 and t.stride(3) != 1):
-        _bad(f"{name}: expected [B, S, H, D], D contiguous")
+    if t.dtype != dtype or t.get_device() != dev or t.dim() != 4:
+        _bad(f"{name}: expected [B, S, H, D] of type {dtype} on cuda:{dev}")
     B, S, H, D = t.shape
-    sb, ss, sh, _ = t.stride()
+    sb, ss, sh, one = t.stride()
+    if one != 1 and D > 1:
+        _bad(f"{name}: expected D contiguous")
     return B, S, H, D, _strides(sb if B > 1 else 0, ss if S > 1 else 0, sh if H > 1 else 0)
 
 
 def _qk_args(q, k, wq, wk, cos, sin, positions):
-    dev = q.device
-    _cuda(q, "q")
-    _cuda(k, "k", dev)
-    if q.dtype not in _DTYPE or k.dtype != q.dtype:
-        _bad("q and k: expected bfloat16, float16 or float32, both alike")
-    B, S, Hq, D, qs = _heads(q, "q")
-    Bk, Sk, Hk, Dk, ks = _heads(k, "k")
-    if (Bk, Sk, Dk) != (B, S, D):
+    dev = _device(q, "q")
+    dtype = q.dtype
+    if dtype not in _DTYPE:
+        _bad("q: expected bfloat16, float16 or float32")
+    B, S, Hq, D, qs = _heads(q, "q", dtype, dev)
+    Bk, Sk, Hk, Dk, ks = _heads(k, "k", dtype, dev)
+    if Bk != B or Sk != S or Dk != D:
         _bad("k: expected the [B, S, ., D] of q")
     pwq = None if wq is None else _vector(wq, "wq", D, dev)
     pwk = None if wk is None else _vector(wk, "wk", D, dev)
-    _cuda(cos, "cos", dev)
-    _cuda(sin, "sin", dev)
-    if (cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape
-            or not cos.is_contiguous() or not sin.is_contiguous()):
-        _bad("cos and sin: expected contiguous float32 [P, R / 2]")
+    if (cos.dtype != _F32 or sin.dtype != _F32 or cos.dim() != 2 or cos.shape != sin.shape
+            or not cos.is_contiguous() or not sin.is_contiguous() or cos.get_device() != dev
+            or sin.get_device() != dev):
+        _bad(f"cos and sin: expected contiguous float32 [P, R / 2] on cuda:{dev}")
     P, half = cos.shape
     pos, stride, bits = None, 0, 32
     if positions is not None:
@@ -258,7 +264,8 @@ def _qk_args(q, k, wq, wk, cos, sin, positions):
         elif shape != (S,) and shape != (1, S):
             _bad("positions: expected [B, S] or [S]")
         pos = positions.data_ptr()
-    return (pwq, pwk, cos.data_ptr(), sin.data_ptr(), pos), (B, S, Hq, Hk, D, 2 * half, P, qs, ks), stride, bits
+    return dev, (pwq, pwk, cos.data_ptr(), sin.data_ptr(), pos), (B, S, Hq, Hk, D, 2 * half, P, qs[1], ks[1]), \
+        stride, bits
 
 
 def qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -270,13 +277,11 @@ def qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions=None, eps: float = 1e
     None; cos, sin: fp32 [P, R / 2] (rope_table); positions: int [B, S] or [S], default 0 .. S - 1;
     interleaved: pairs (2i, 2i + 1) rather than (i, i + R / 2). status as in embed_forward.
     Returns contiguous (q_out, k_out) as attn_forward takes them."""
-    tables, sizes, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
-    dev, dtype = q.device, q.dtype
-    q_out = torch.empty(q.shape, dtype=dtype, device=dev)
-    k_out = torch.empty(k.shape, dtype=dtype, device=dev)
+    dev, tables, sizes, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
+    q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)
     _raise(_core.load().dash_qk_norm_rope_fwd(
         q.data_ptr(), k.data_ptr(), *tables, q_out.data_ptr(), k_out.data_ptr(), _status_word(status, dev),
-        *sizes, stride, eps, int(interleaved), _DTYPE[dtype], bits, _stream(q, stream)), "dash_qk_norm_rope_fwd")
+        *sizes, stride, eps, interleaved, _DTYPE[q.dtype], bits, _stream(dev, stream)), "dash_qk_norm_rope_fwd")
     return q_out, k_out
 
 
@@ -300,32 +305,33 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None
     dq_out, dk_out: contiguous, as attn_backward returns them. dq, dk: optional tensors to
     write to, strided like q and k may be (parts of a fused projection's gradient). Returns
     (dq, dk, dwq, dwk), the last two fp32 [D] or None where the weight is None."""
-    tables, sizes, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
-    dev, dtype = q.device, q.dtype
-    B, S, Hq, Hk, D = sizes[:5]
-    for t, like, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
-        _cuda(t, name, dev)
-        if t.dtype != dtype or t.shape != like.shape or not t.is_contiguous():
-            _bad(f"{name}: expected contiguous, of the input's type and shape")
+    dev, tables, sizes, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
+    dtype, qshape, kshape, D = q.dtype, q.shape, k.shape, sizes[4]
+    if (dq_out.dtype != dtype or dq_out.shape != qshape or not dq_out.is_contiguous() or dq_out.get_device() != dev
+            or dk_out.dtype != dtype or dk_out.shape != kshape or not dk_out.is_contiguous()
+            or dk_out.get_device() != dev):
+        _bad(f"dq_out and dk_out: expected contiguous, of the type and shape of q and k, on cuda:{dev}")
     if dq is None:
-        dq = torch.empty(q.shape, dtype=dtype, device=dev)
+        dq = q.new_empty(qshape)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=dtype, device=dev)
-    for t, like, name in ((dq, q, "dq"), (dk, k, "dk")):
-        _cuda(t, name, dev)
-        if t.dtype != dtype or t.shape != like.shape:
-            _bad(f"{name}: expected the input's type and shape")
-    dqs, dks = _heads(dq, "dq")[4], _heads(dk, "dk")[4]
-    dws = torch.empty((2, D), dtype=torch.float32, device=dev)
-    dwq, dwk = (None if wq is None else dws[0]), (None if wk is None else dws[1])
+        dk = k.new_empty(kshape)
+    dqn, dkn = _heads(dq, "dq", dtype, dev), _heads(dk, "dk", dtype, dev)
+    if dqn[:4] != qshape or dkn[:4] != kshape:
+        _bad("dq and dk: expected the shapes of q and k")
+    dwq = pdwq = dwk = pdwk = None
+    if wq is not None:
+        dwq = wq.new_empty(D)
+        pdwq = dwq.data_ptr()
+    if wk is not None:
+        dwk = wk.new_empty(D)
+        pdwk = dwk.data_ptr()
     if workspace is None:
-        workspace = new_qk_norm_rope_workspace(B, S, Hq, Hk, D, dev)
+        workspace = new_qk_norm_rope_workspace(*sizes[:5], q.device)
     ws, nbytes = _ws(workspace, dev)
     _raise(_core.load().dash_qk_norm_rope_bwd(
         dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), *tables, dq.data_ptr(), dk.data_ptr(),
-        None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), ws, nbytes, *sizes,
-        dqs, dks, stride, eps, int(interleaved), _DTYPE[dtype], bits, _stream(q, stream)),
-        "dash_qk_norm_rope_bwd")
+        pdwq, pdwk, ws, nbytes, *sizes, dqn[4][1], dkn[4][1], stride, eps, interleaved, _DTYPE[dtype], bits,
+        _stream(dev, stream)), "dash_qk_norm_rope_bwd")
     _finish(workspace, stream, check, "dash_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -338,6 +344,7 @@ class GradClipPlan:
 
     def __init__(self, grads, outs, table, norm):
         self.grads, self.outs, self.table, self.norm = grads, outs, table, norm
+        self.device = table.get_device()
 
 
 def grad_clip_plan(grads, out=None, stream=None) -> GradClipPlan:
@@ -348,13 +355,12 @@ def grad_clip_plan(grads, out=None, stream=None) -> GradClipPlan:
     outs = grads if out is None else list(out)
     if not grads or len(outs) != len(grads):
         _bad("grads: expected tensors, as many as out")
-    _cuda(grads[0], "grads[0]")
-    dev = grads[0].device
+    dev = _device(grads[0], "grads[0]")
     arr = (_ClipTensor * len(grads))()
     spans = set()
     for i, (g, o) in enumerate(zip(grads, outs)):
         for t, name in ((g, "grads"), (o, "out")):
-            _cuda(t, f"{name}[{i}]", dev)
+            _on(t, f"{name}[{i}]", dev)
             if t.dtype not in _DTYPE or not t.is_contiguous():
                 _bad(f"{name}[{i}]: expected contiguous bfloat16, float16 or float32")
             if t.numel():
@@ -369,10 +375,10 @@ def grad_clip_plan(grads, out=None, stream=None) -> GradClipPlan:
     nbytes = lib.dash_grad_clip_plan_size(arr, len(grads))
     if nbytes == 0:
         raise DashError(DASH_ERR_UNSUPPORTED, "dash_grad_clip_plan_size")
-    table = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _raise(lib.dash_grad_clip_plan(arr, len(grads), table.data_ptr(), nbytes, _stream(table, stream)),
+    table = torch.empty(nbytes, dtype=torch.uint8, device=grads[0].device)
+    _raise(lib.dash_grad_clip_plan(arr, len(grads), table.data_ptr(), nbytes, _stream(dev, stream)),
            "dash_grad_clip_plan")
-    return GradClipPlan(grads, outs, table, torch.empty((), dtype=torch.float32, device=dev))
+    return GradClipPlan(grads, outs, table, torch.empty((), dtype=_F32, device=grads[0].device))
 
 
 def grad_clip(plan: GradClipPlan, max_norm: float, stream=None):
@@ -380,7 +386,7 @@ def grad_clip(plan: GradClipPlan, max_norm: float, stream=None):
     above max_norm. Returns (norm, tensors): norm is a device fp32 scalar that the next call
     overwrites."""
     _raise(_core.load().dash_grad_clip(plan.table.data_ptr(), max_norm, plan.norm.data_ptr(),
-                                       _stream(plan.table, stream)), "dash_grad_clip")
+                                       _stream(plan.device, stream)), "dash_grad_clip")
     return plan.norm, plan.outs
 
 
@@ -399,19 +405,17 @@ def new_linear_xent_workspace(T: int, V: int, D: int, device) -> torch.Tensor:
 
 
 def _xent_args(x, w, targets):
-    dev = x.device
-    _cuda(x, "x")
-    _cuda(w, "w", dev)
-    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
-        _bad("x and w: expected bfloat16")
-    ldx, ldw = _rows(x, "x"), _rows(w, "w")
-    bits = _index(targets, "targets", dev)
-    T, D = x.shape
-    if w.shape[1] != D:
+    dev = _device(x, "x")
+    if x.dtype != _BF16 or w.dtype != _BF16 or w.get_device() != dev:
+        _bad(f"x and w: expected bfloat16 on cuda:{dev}")
+    T, D, ldx = _rows(x, "x")
+    V, Dw, ldw = _rows(w, "w")
+    if Dw != D:
         _bad("w: expected as many columns as x")
-    if targets.shape != (T,):
+    bits = _index(targets, "targets", dev)
+    if targets.dim() != 1 or targets.numel() != T:
         _bad("targets: expected one index a row of x")
-    return T, w.shape[0], D, ldx, ldw, bits
+    return dev, bits, (T, V, D, ldx, ldw)
 
 
 def linear_xent_forward(x, w, targets, ignore_index: int = -100, scale: float = 1.0, workspace=None,
@@ -420,15 +424,16 @@ def linear_xent_forward(x, w, targets, ignore_index: int = -100, scale: float = 
 
     x: bf16 [T, D] hidden states, w: bf16 [V, D] output embedding, targets: int [T].
     Returns (loss, lse), fp32 [T]; rows whose target is ignore_index have loss 0."""
-    T, V, D, ldx, ldw, bits = _xent_args(x, w, targets)
+    dev, bits, sizes = _xent_args(x, w, targets)
+    T = sizes[0]
     if workspace is None:
-        workspace = new_linear_xent_workspace(T, V, D, x.device)
-    out = torch.empty((2, T), dtype=torch.float32, device=x.device)
-    loss, lse = out[0], out[1]
-    ws, nbytes = _ws(workspace, x.device)
+        workspace = new_linear_xent_workspace(*sizes[:3], x.device)
+    loss = torch.empty(T, dtype=_F32, device=x.device)
+    lse = loss.new_empty(T)
+    ws, nbytes = _ws(workspace, dev)
     _raise(_core.load().dash_linear_xent_fwd(
-        x.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws, nbytes,
-        T, V, D, ldx, ldw, scale, ignore_index, bits, _stream(x, stream)), "dash_linear_xent_fwd")
+        x.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws, nbytes, *sizes,
+        scale, ignore_index, bits, _stream(dev, stream)), "dash_linear_xent_fwd")
     _finish(workspace, stream, check, "dash_linear_xent_fwd")
     return loss, lse
 
@@ -441,23 +446,22 @@ def linear_xent_backward(x, w, targets, lse, dloss, ignore_index: int = -100, sc
     lse: from linear_xent_forward; dloss: fp32 [T]. dw: an optional [V, D] bf16 or fp32
     tensor to write to, or to add to with accumulate=True (tied embeddings, several
     micro-batches); else one of dw_dtype (bf16) is allocated. Returns (dx, dw)."""
-    T, V, D, ldx, ldw, bits = _xent_args(x, w, targets)
-    dev = x.device
+    dev, bits, sizes = _xent_args(x, w, targets)
+    T, V, D = sizes[:3]
     plse, pdloss = _vector(lse, "lse", T, dev), _vector(dloss, "dloss", T, dev)
     if dw is None:
         if accumulate:
             _bad("accumulate: needs dw")
-        dw = torch.empty((V, D), dtype=dw_dtype or torch.bfloat16, device=dev)
-    _cuda(dw, "dw", dev)
-    if dw.dtype not in (torch.bfloat16, torch.float32) or dw.shape != (V, D) or not dw.is_contiguous():
-        _bad("dw: expected contiguous bfloat16 or float32 [V, D]")
+        dw = torch.empty((V, D), dtype=dw_dtype or _BF16, device=x.device)
+    if dw.dtype not in (_BF16, _F32) or dw.shape != (V, D) or not dw.is_contiguous() or dw.get_device() != dev:
+        _bad(f"dw: expected contiguous bfloat16 or float32 [V, D] on cuda:{dev}")
     if workspace is None:
         workspace = new_linear_xent_workspace(T, V, D, x.device)
-    dx = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
-    ws, nbytes = _ws(workspace, x.device)
+    dx = x.new_empty((T, D))
+    ws, nbytes = _ws(workspace, dev)
     _raise(_core.load().dash_linear_xent_bwd(
-        x.data_ptr(), w.data_ptr(), targets.data_ptr(), plse, pdloss, dx.data_ptr(),
-        dw.data_ptr(), ws, nbytes, T, V, D, ldx, ldw, scale, ignore_index, bits, _DTYPE[dw.dtype],
-        int(accumulate), _stream(x, stream)), "dash_linear_xent_bwd")
+        x.data_ptr(), w.data_ptr(), targets.data_ptr(), plse, pdloss, dx.data_ptr(), dw.data_ptr(), ws, nbytes,
+        *sizes, scale, ignore_index, bits, _DTYPE[dw.dtype], accumulate, _stream(dev, stream)),
+        "dash_linear_xent_bwd")
     _finish(workspace, stream, check, "dash_linear_xent_bwd")
     return dx, dw

@@ -86,7 +86,7 @@ struct SortArgs {
   long long T, V, padding_idx;
   int passes, digit_bits;
   int* header;
-  unsigned *keys[2], *toks[2];   // the last pass writes index (passes - 1) & 1
+  uint2* sorted[2];           // (id, token); the last pass writes index (passes - 1) & 1
 };
 
 // Zeroes n bytes at p, both even. The kernel before it is this call's sort, which starts only
@@ -133,33 +133,31 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.digit_bits;
-    const unsigned* kin = a.keys[(pass + 1) & 1];
-    const unsigned* tin = a.toks[(pass + 1) & 1];
-    unsigned* kout = a.keys[pass & 1];
-    unsigned* tout = a.toks[pass & 1];
-    auto key_at = [&](long long t) -> unsigned {
-      if (pass > 0) return __ldcg(kin + t);
+    const uint2* src = a.sorted[(pass + 1) & 1];
+    uint2* dst = a.sorted[pass & 1];
+    auto pair_at = [&](long long t) -> uint2 {
+      if (pass > 0) return __ldcg(src + t);
       const long long id = load_index(a.ids, t, a.id_bits);
-      return id < 0 || id >= a.V || id == a.padding_idx ? (unsigned)a.V : (unsigned)id;
+      return make_uint2(id < 0 || id >= a.V || id == a.padding_idx ? (unsigned)a.V : (unsigned)id, (unsigned)t);
     };
-    auto load_strips = [&](long long s, unsigned (&key)[kAheadStrips]) {
+    auto load_strips = [&](long long s, uint2 (&pair)[kAheadStrips]) {
 #pragma unroll
       for (int k = 0; k < kAheadStrips; ++k) {
         const long long t = (s + k) * 32 + lane;
-        key[k] = s + k < last && t < a.T ? key_at(t) : 0;
+        pair[k] = s + k < last && t < a.T ? pair_at(t) : make_uint2(0, 0);
       }
     };
     for (int d = lane; d < bins; d += 32) mine[d] = 0;
     __syncwarp();
-    unsigned key[kAheadStrips];
+    uint2 pair[kAheadStrips];
     for (long long s = first; s < last; s += kAheadStrips) {
-      load_strips(s, key);
+      load_strips(s, pair);
 #pragma unroll
       for (int k = 0; k < kAheadStrips; ++k) {
         const bool in = s + k < last && (s + k) * 32 + lane < a.T;
         const unsigned live = __ballot_sync(0xffffffffu, in);
         if (in) {
-          const unsigned d = (key[k] >> shift) & (bins - 1);
+          const unsigned d = (pair[k].x >> shift) & (bins - 1);
           const unsigned peers = __match_any_sync(live, d);
           if ((peers & lt) == 0) mine[d] += __popc(peers);
         }
@@ -207,13 +205,7 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     if (d < bins) base[d] = before + scan - total + lower;
     __syncthreads();
     for (long long s = first; s < last; s += kAheadStrips) {
-      unsigned tok[kAheadStrips];
-      if (last - first > kAheadStrips) load_strips(s, key);   // else they are still there
-#pragma unroll
-      for (int k = 0; k < kAheadStrips; ++k) {
-        const long long t = (s + k) * 32 + lane;
-        tok[k] = pass > 0 && s + k < last && t < a.T ? __ldcg(tin + t) : (unsigned)t;
-      }
+      if (last - first > kAheadStrips) load_strips(s, pair);   // else they are still there
 #pragma unroll
       for (int k = 0; k < kAheadStrips; ++k) {
         const long long t = (s + k) * 32 + lane;
@@ -221,12 +213,12 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
         const unsigned live = __ballot_sync(0xffffffffu, in);
         unsigned dg = 0, peers = 0;
         if (in) {
-          dg = (key[k] >> shift) & (bins - 1);
+          dg = (pair[k].x >> shift) & (bins - 1);
           peers = __match_any_sync(live, dg);
-          const unsigned at = base[dg] + mine[dg] + __popc(peers & lt);
-          kout[at] = key[k];
-          tout[at] = tok[k];
-          if (pass == 0 && key[k] >= a.V) {
+          // one store for both: an SM takes some cycles for each place of a scattered store,
+          // which is most of what a pass costs
+          dst[base[dg] + mine[dg] + __popc(peers & lt)] = pair[k];
+          if (pass == 0 && pair[k].x >= a.V) {
             const long long id = load_index(a.ids, t, a.id_bits);
             if (id < 0 || id >= a.V) report_index(a.header, CHK_TOKEN_ID, t, id, a.V);
           }
@@ -243,7 +235,7 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 // ---- the rows -----------------------------------------------------------------------------
 
 struct RowArgs {
-  const unsigned *keys, *toks;
+  const uint2* sorted;        // (id, token) by id
   long long T, V;
   int D;
   long long ld_dout;
@@ -320,10 +312,9 @@ __global__ void __launch_bounds__(kRowThreads)
   const long long p0 = run * kRun;
   const int n = (int)min((long long)kRun, a.T - p0);
   const unsigned V = (unsigned)a.V;
-  const unsigned* keys = a.keys + p0;
-  const unsigned* toks = a.toks + p0;
-  unsigned key = keys[0];
-  bool begun = run > 0 && keys[-1] == key;
+  const uint2* sorted = a.sorted + p0;
+  unsigned key = sorted[0].x;
+  bool begun = run > 0 && sorted[-1].x == key;
   float acc[N] = {};
   constexpr int U = 8;                             // rows in flight a thread (16: 17 -> 23 us for 16384 x 2048)
 #pragma unroll 1
@@ -332,7 +323,7 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       v[i] = {};
-      if (p + i < n) v[i].load(dout + toks[p + i] * a.ld_dout + col, a.tx, nc);
+      if (p + i < n) v[i].load(dout + sorted[p + i].y * a.ld_dout + col, a.tx, nc);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -342,7 +333,7 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
         for (int k = 0; k < N; ++k) acc[k] += f[k];
         const bool more = p0 + p + i + 1 < a.T;
-        const unsigned next = more ? keys[p + i + 1] : 0xffffffffu;
+        const unsigned next = more ? sorted[p + i + 1].x : 0xffffffffu;
         if (next != key || p + i + 1 == n) {
           const bool goes_on = next == key;
           if (!begun && !goes_on) {
@@ -398,9 +389,9 @@ __global__ void __launch_bounds__(256) embed_join_kernel(TO* dtable, const RowAr
     // the run's last key, the next one and the one before the run, at once
     unsigned k = 0xffffffffu;
     if (p0 + kRun < a.T) {
-      if (lane == 0) k = a.keys[p0 + kRun - 1];
-      if (lane == 1) k = a.keys[p0 + kRun];
-      if (lane == 2 && run > 0) k = a.keys[p0 - 1];
+      if (lane == 0) k = a.sorted[p0 + kRun - 1].x;
+      if (lane == 1) k = a.sorted[p0 + kRun].x;
+      if (lane == 2 && run > 0) k = a.sorted[p0 - 1].x;
     }
     const unsigned key = __shfl_sync(0xffffffffu, k, 0);
     const bool cross = key < (unsigned)a.V && __shfl_sync(0xffffffffu, k, 1) == key &&
@@ -409,7 +400,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(TO* dtable, const RowAr
     if (cross) {
       for (;;) {
         const long long r = run + 1 + follow + lane;
-        const unsigned same = __ballot_sync(0xffffffffu, r < a.runs && a.keys[r * kRun] == key);
+        const unsigned same = __ballot_sync(0xffffffffu, r < a.runs && a.sorted[r * kRun].x == key);
         follow += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
         if (same != 0xffffffffu) break;
       }
@@ -468,7 +459,7 @@ int pow2_lanes(int need, int most) {
 }
 
 struct Layout {
-  size_t keys0, keys1, toks0, toks1, part, total;
+  size_t sorted0, sorted1, part, total;
   long long runs;
   int Dp;
 };
@@ -483,10 +474,8 @@ Layout layout(long long T, int D) {
   };
   l.runs = ceil_div<long long>(T, kRun);
   l.Dp = (int)round_up_to(D, 8);
-  l.keys0 = take((size_t)T * 4);
-  l.keys1 = take((size_t)T * 4);
-  l.toks0 = take((size_t)T * 4);
-  l.toks1 = take((size_t)T * 4);
+  l.sorted0 = take((size_t)T * sizeof(uint2));
+  l.sorted1 = take((size_t)T * sizeof(uint2));
   l.part = take((size_t)l.runs * 2 * l.Dp * 4);
   l.total = at;
   return l;
@@ -595,10 +584,8 @@ dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, vo
   const size_t table_bytes = (size_t)V * D * elt_bytes(dtable_dtype);
   const size_t zero_blocks = ceil_div<size_t>(table_bytes, kZeroBytes);
   if (zero_blocks >= (1ull << 31)) return DASH_ERR_UNSUPPORTED;
-  s.keys[0] = (unsigned*)(ws + l.keys0);
-  s.keys[1] = (unsigned*)(ws + l.keys1);
-  s.toks[0] = (unsigned*)(ws + l.toks0);
-  s.toks[1] = (unsigned*)(ws + l.toks1);
+  s.sorted[0] = (uint2*)(ws + l.sorted0);
+  s.sorted[1] = (uint2*)(ws + l.sorted1);
   const size_t smem = ((size_t)(kSortWarps + 2) << s.digit_bits) * 4;
   DASH_TRY(allow_shared((const void*)embed_sort_kernel, (int)(((size_t)(kSortWarps + 2) << kMaxDigitBits) * 4)));
   embed_sort_kernel<<<kSortCtas, kSortThreads, smem, stream>>>(s);
@@ -607,8 +594,7 @@ dash_status_t dash_embed_bwd(const void* dout, const void* ids, void* dtable, vo
     DASH_TRY(launch_after(embed_zero_kernel, dim3((unsigned)zero_blocks), kZeroThreads, 0, stream, (char*)dtable,
                           table_bytes));
   RowArgs a;
-  a.keys = s.keys[(s.passes - 1) & 1];
-  a.toks = s.toks[(s.passes - 1) & 1];
+  a.sorted = s.sorted[(s.passes - 1) & 1];
   a.T = T;
   a.V = V;
   a.D = D;

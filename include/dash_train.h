@@ -147,10 +147,13 @@ dash_status_t dash_grad_clip_plan(const dash_clip_tensor_t* tensors, int n, void
  * grad). Squares are summed in fp32 over at most 32768 elements of a tensor, these sums in
  * fp64; where squares would overflow or vanish in fp32 the elements are rescaled by a power
  * of two first. When the norm is not finite *norm says so and the values are passed unscaled.
- *   plan : from dash_grad_clip_plan, on this device        norm : device fp32 (written)
+ *   plan : from dash_grad_clip_plan, on this device, of plan_bytes (dash_grad_clip_plan_size);
+ *          something else gives the norm NaN and touches no tensor
+ *   norm : device fp32 (written)
  * max_norm >= 0 (may be infinite: the norm alone, with copies where out is not grad).
  */
-dash_status_t dash_grad_clip(void* plan, float max_norm, float* norm, cudaStream_t stream);
+dash_status_t dash_grad_clip(void* plan, size_t plan_bytes, float max_norm, float* norm,
+                             cudaStream_t stream);
 
 /* ---- Softmax cross entropy from hidden states --------------------------------------- */
 

@@ -44,6 +44,11 @@ struct Header {
 };
 constexpr size_t kTableOff = (sizeof(Header) + 255) / 256 * 256;
 
+// Whether this is a plan, and the launch has its blocks.
+__device__ __forceinline__ bool plan_fits(const Header* h) {
+  return h->magic == kMagic && h->blocks <= (int)gridDim.x;
+}
+
 // Sum of squares of this thread's elements of a piece. 32 bits hold the sum unless it
 // overflows or is so small that squares may have vanished; then the elements are scaled by
 // the power of two that brings their largest to [1/2, 1).
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const
   __shared__ double shared[kThreads / 32];
   __shared__ bool last;
   grid_next();
-  if (h->magic != kMagic) {
+  if (!plan_fits(h)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = NAN;
     return;
   }
@@ -140,9 +145,9 @@ __global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const
   double sum = 0.0;
   Piece next = {};
   if (blockIdx.x < pieces) next = table[blockIdx.x];
-  for (long long i = blockIdx.x; i < pieces; i += kBlocks) {
+  for (long long i = blockIdx.x; i < pieces; i += blocks) {
     const Piece pc = next;
-    if (i + kBlocks < pieces) next = table[i + kBlocks];
+    if (i + blocks < pieces) next = table[i + blocks];
     sum += pc.dtype == DASH_BF16   ? squares_of<__nv_bfloat16>(pc)
            : pc.dtype == DASH_FP16 ? squares_of<__half>(pc)
                                    : squares_of<float>(pc);
@@ -207,18 +212,20 @@ __device__ __forceinline__ void scale_of(const Piece& pc, float f, bool copy) {
 
 __global__ void __launch_bounds__(kThreads, 2) clip_scale_kernel(const Header* h, const Piece* table,
                                                               float max_norm) {
+  // the table and its header's constants are the plan's, not the kernel's before
+  const bool ok = plan_fits(h);
+  const long long first = ok ? h->pieces - 1 - blockIdx.x : -1;
+  Piece next = {};
+  if (first >= 0) next = table[first];
   grid_wait();
-  if (h->magic != kMagic) return;
+  if (!ok) return;
   const double n = h->norm;
   const bool copy = !(n > (double)max_norm) || isinf(n);
   if (copy && h->all_in_place) return;
   const float f = copy ? 1.f : (float)((double)max_norm / n);
-  const long long first = h->pieces - 1 - blockIdx.x;
-  Piece next = {};
-  if (first >= 0) next = table[first];
-  for (long long i = first; i >= 0; i -= kBlocks) {
+  for (long long i = first; i >= 0; i -= gridDim.x) {
     const Piece pc = next;
-    if (i >= kBlocks) next = table[i - kBlocks];
+    if (i >= gridDim.x) next = table[i - gridDim.x];
     if (copy && pc.out == pc.grad) continue;
     if (pc.dtype == DASH_BF16) scale_of<__nv_bfloat16>(pc, f, copy);
     else if (pc.dtype == DASH_FP16) scale_of<__half>(pc, f, copy);
@@ -291,14 +298,17 @@ dash_status_t dash_grad_clip_plan(const dash_clip_tensor_t* tensors, int n, void
   return DASH_OK;
 }
 
-dash_status_t dash_grad_clip(void* plan, float max_norm, float* norm, cudaStream_t stream) {
+dash_status_t dash_grad_clip(void* plan, size_t plan_bytes, float max_norm, float* norm, cudaStream_t stream) {
   if (!plan || !norm || !is_aligned(plan, 256) || !is_aligned(norm, 4)) return DASH_ERR_INVALID_ARG;
+  if (plan_bytes < kTableOff) return DASH_ERR_WORKSPACE_TOO_SMALL;
   if (!(max_norm >= 0.f)) return DASH_ERR_INVALID_ARG;
   Header* h = (Header*)plan;
   const Piece* table = (const Piece*)((char*)plan + kTableOff);
-  clip_norm_kernel<<<kBlocks, kThreads, 0, stream>>>(h, table, norm);
+  // no more blocks than the table can hold pieces for (the header has the exact number)
+  const int grid = (int)std::max<size_t>(1, std::min<size_t>(kBlocks, (plan_bytes - kTableOff) / sizeof(Piece)));
+  clip_norm_kernel<<<grid, kThreads, 0, stream>>>(h, table, norm);
   DASH_TRY(cudaGetLastError());
-  DASH_TRY(launch_after(clip_scale_kernel, dim3(kBlocks), kThreads, 0, stream, h, table, max_norm));
+  DASH_TRY(launch_after(clip_scale_kernel, dim3(grid), kThreads, 0, stream, h, table, max_norm));
   return DASH_OK;
 }
 

@@ -45,7 +45,7 @@ _core._SIGNATURES.update({
                               + [_c_int] * 3 + [_vp]),
     "dash_grad_clip_plan_size": (_c_size, [ctypes.POINTER(_ClipTensor), _c_int]),
     "dash_grad_clip_plan": (_c_int, [ctypes.POINTER(_ClipTensor), _c_int, _vp, _c_size, _vp]),
-    "dash_grad_clip": (_c_int, [_vp, _c_float, _vp, _vp]),
+    "dash_grad_clip": (_c_int, [_vp, _c_size, _c_float, _vp, _vp]),
     "dash_linear_xent_workspace_size": (_c_size, [_ll, _ll, _c_int]),
     "dash_linear_xent_fwd": (_c_int, [_vp] * 6 + [_c_size, _ll, _ll, _c_int, _ll, _ll, _c_float, _ll,
                                                   _c_int, _vp]),
@@ -385,7 +385,7 @@ def grad_clip(plan: GradClipPlan, max_norm: float, stream=None):
     """Global L2 norm of the plan's gradients, which are scaled by max_norm / norm when it is
     above max_norm. Returns (norm, tensors): norm is a device fp32 scalar that the next call
     overwrites."""
-    _raise(_core.load().dash_grad_clip(plan.table.data_ptr(), max_norm, plan.norm.data_ptr(),
+    _raise(_core.load().dash_grad_clip(plan.table.data_ptr(), plan.table.nbytes, max_norm, plan.norm.data_ptr(),
                                        _stream(plan.device, stream)), "dash_grad_clip")
     return plan.norm, plan.outs
 

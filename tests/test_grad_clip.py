@@ -150,3 +150,18 @@ def test_bitwise_reproducible_streams_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, [norm] + got))
+
+
+def test_something_else_than_a_plan_gives_nan_and_touches_nothing():
+    grads = _tensors([100000, 500], [torch.float32], seed=7)
+    keep = [g.clone() for g in grads]
+    plan = da.grad_clip_plan(grads)
+    lib, norm = da.load(), torch.zeros((), device="cuda")
+    blank = torch.zeros(plan.table.numel(), dtype=torch.uint8, device="cuda")
+    for table, size in ((blank, blank.numel()), (plan.table, plan.table.numel() - 24 * 20)):
+        norm.zero_()
+        assert lib.dash_grad_clip(table.data_ptr(), size, 0.5, norm.data_ptr(), 0) == da.DASH_OK
+        torch.cuda.synchronize()
+        assert math.isnan(float(norm)) and all(torch.equal(a, b) for a, b in zip(grads, keep))
+    got, _ = da.grad_clip(plan, 0.5)
+    assert math.isfinite(float(got))

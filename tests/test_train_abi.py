@@ -126,11 +126,9 @@ def test_clip_refuses(lib):
     assert plan(grad=17) == INV and plan(dtype=2, out=18) == INV and plan(where=128) == INV and plan(where=None) == INV
     assert plan(size=100) == SMALL and plan(n=2 ** 50) == UNS
     assert lib.dash_grad_clip_plan_size((_ClipTensor * 1)(_ClipTensor(16, 16, -1, 0)), 1) == 0
-    assert lib.dash_grad_clip(None, 1.0, 16, None) == INV
-    assert lib.dash_grad_clip(256, 1.0, None, None) == INV
-    assert lib.dash_grad_clip(256, -1.0, 16, None) == INV
-    assert lib.dash_grad_clip(256, float("nan"), 16, None) == INV
-    assert lib.dash_grad_clip(128, 1.0, 16, None) == INV
+    clip = lambda plan=256, size=1 << 20, limit=1.0, norm=16: lib.dash_grad_clip(plan, size, limit, norm, None)
+    assert clip(plan=None) == INV and clip(norm=None) == INV and clip(plan=128) == INV and clip(norm=2) == INV
+    assert clip(limit=-1.0) == INV and clip(limit=float("nan")) == INV and clip(size=256) == SMALL
 
 
 def test_binding_refuses_host_tensors():

@@ -102,7 +102,8 @@ dash_status_t dash_qk_norm_rope_fwd(const void* q, const void* k, const float* w
  * dx = r (w d - x r mean(w d x r)). r is recomputed from x, nothing is saved by the forward.
  *   dq_out, dk_out : contiguous [B, S, Hq, D], [B, S, Hk, D] (read)
  *   dq, dk   : strided as dq_strides and dk_strides say (written), so that they may be the
- *              parts of a fused projection's gradient
+ *              parts of a fused projection's gradient; a stride of zero over more than one
+ *              element is refused here (inputs may have it: heads or batches that are shared)
  *   dwq, dwk : fp32 [D] (written; NULL: not wanted)
  *   workspace: dash_qk_norm_rope_bwd_workspace_size(B, S, Hq, Hk, D) bytes
  * A position out of range gives NaN rows in dq and dk (and NaN in dwq, dwk) and the status

@@ -6,7 +6,9 @@
 // last block to finish adds the blocks' totals in order (so the sum's order never depends on
 // which block that is). clip_scale then walks the pieces from the end, where the cache still
 // holds what the norm read last, and returns at once when nothing has to be written. Both
-// are bound by HBM.
+// are bound by HBM: the norm of 0.5 GB takes 78 us (6.4 TB/s), 2.4 GB clipped into buffers
+// 1.09 ms (7.3 GB moved, 6.6 TB/s); four loads of 16 bytes in flight a thread instead of
+// eight, and the table read when it is needed: 147 us and 2.0 ms.
 #include <algorithm>
 #include <exception>
 #include <vector>

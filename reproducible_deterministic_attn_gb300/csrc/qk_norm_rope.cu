@@ -570,6 +570,11 @@ bool strides_ok(const long long* s) {
   return true;
 }
 
+// Strides of a tensor to write: no two of its elements in one place by a stride of zero.
+bool distinct(const long long* s, int B, int S, int H) {
+  return (B < 2 || s[0] > 0) && (S < 2 || s[1] > 0) && (H < 2 || s[2] > 0);
+}
+
 // Arguments that both directions share.
 dash_status_t check(const void* q, const void* k, const float* wq, const float* wk, const float* cos,
                     const float* sin, const void* positions, int B, int S, int Hq, int Hk, int D, int R,
@@ -674,6 +679,7 @@ dash_status_t dash_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
   if (st != DASH_OK) return st;
   if (!workspace || !dq_strides || !dk_strides) return DASH_ERR_INVALID_ARG;
   if (!strides_ok(dq_strides) || !strides_ok(dk_strides)) return DASH_ERR_UNSUPPORTED;
+  if (!distinct(dq_strides, B, S, Hq) || !distinct(dk_strides, B, S, Hk)) return DASH_ERR_INVALID_ARG;
   const bool any = (long long)B * S > 0;
   if (any && ((Hq > 0 && (!dq_out || !dq)) || (Hk > 0 && (!dk_out || !dk)))) return DASH_ERR_INVALID_ARG;
   for (const void* p : {dq_out, dk_out, (const void*)dq, (const void*)dk})

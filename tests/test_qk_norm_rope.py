@@ -137,6 +137,19 @@ def test_strided_inputs_and_gradients():
     assert bool((fused[:, :, 6:] == 7).all())
 
 
+def test_inputs_shared_by_heads_and_batches():
+    """Keys expanded over heads and queries over batches (strides of zero) are read in place;
+    gradients come per head and batch."""
+    x = _inputs(3, 7, 4, 4, 64, 64, torch.bfloat16, seed=15)
+    x["k"] = x["k"][:, :, :1].expand(3, 7, 4, 64)
+    x["q"] = x["q"][:1].expand(3, 7, 4, 64)
+    outs, grads = _both(x, False)
+    _check(x, 64, False, 1e-6, outs, grads)
+    with pytest.raises(da.DashError) as e:
+        _both(x, False, dq=torch.empty(1, 7, 4, 64, dtype=torch.bfloat16, device="cuda").expand(3, 7, 4, 64))
+    assert e.value.status == da.DASH_ERR_INVALID_ARG
+
+
 def test_empty():
     x = _inputs(2, 3, 4, 2, 64, 64, torch.bfloat16)
     e = lambda t: t[:, :0]

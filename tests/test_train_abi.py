@@ -85,7 +85,7 @@ QK_BWD = dict(dqo=16, dko=16, q=16, k=16, wq=16, wk=16, cos=16, sin=16, pos=16, 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(dqo=None), INV), (dict(dk=None), INV), (dict(ws=None), INV), (dict(ws=64), INV), (dict(wsb=300), SMALL),
-    (dict(dqs=None), INV), (dict(dks=S3(0, 60, 64)), UNS), (dict(dwq=2), INV), (dict(dq=8), INV), (dict(R=1), INV)])
+    (dict(dqs=None), INV), (dict(dks=S3(0, 60, 64)), UNS), (dict(dqs=S3(0, 128, 0)), INV), (dict(dks=S3(0, 0, 64)), INV), (dict(dwq=2), INV), (dict(dq=8), INV), (dict(R=1), INV)])
 def test_qk_bwd_refuses(lib, kw, want):
     assert _call(lib.dash_qk_norm_rope_bwd, QK_BWD, **kw) == want
 

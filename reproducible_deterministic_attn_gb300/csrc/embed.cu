@@ -196,6 +196,10 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
         total += v;
       }
     }
+    // After the last pass nobody reads the sorted array here: a CTA only has to stay until the
+    // others have read its totals, so they say so now and wait at the end.
+    const bool last_pass = pass + 1 == a.passes;
+    if (last_pass) cluster.barrier_arrive();
     unsigned scan = total;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -231,7 +235,8 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
         __syncwarp();
       }
     }
-    cluster.sync();   // the totals have been read; the sorted arrays are visible
+    if (last_pass) cluster.barrier_wait();
+    else cluster.sync();                // the totals have been read; the sorted array is visible
   }
 }
 
@@ -303,21 +308,28 @@ template <typename TI, typename TO, bool STRIDED>
 __global__ void __launch_bounds__(kRowThreads)
     embed_rows_kernel(const TI* dout, TO* dtable, const RowArgs a) {
   constexpr int N = STRIDED ? kStridedCols : 16 / sizeof(TI);
-  grid_next();
-  grid_wait();
   const int x = threadIdx.x % a.tx, y = threadIdx.x / a.tx, ty = kRowThreads / a.tx;
   const int tile = a.tx * N;                       // columns a team of tx threads covers
   const int off = STRIDED ? x : x * N;
-  const long long run = (blockIdx.x / a.col_tiles) * (long long)ty + y;
+  // the places of the block's runs, with the one before and the one after each
+  extern __shared__ uint2 rows_smem[];
+  grid_next();
+  grid_wait();
+  const long long run0 = (blockIdx.x / a.col_tiles) * (long long)ty;
+  for (int i = threadIdx.x; i < ty * (kRun + 2); i += kRowThreads) {
+    const long long at = (run0 + i / (kRun + 2)) * kRun + i % (kRun + 2) - 1;
+    rows_smem[i] = at >= 0 && at < a.T ? a.sorted[at] : make_uint2(0xffffffffu, 0);
+  }
+  __syncthreads();
+  const long long run = run0 + y;
   const int c0 = (int)(blockIdx.x % a.col_tiles) * tile, col = c0 + off;
   if (run >= a.runs || col >= a.D) return;
   const int nc = STRIDED ? min(N, (a.D - col + a.tx - 1) / a.tx) : N;   // columns that are there
-  const long long p0 = run * kRun;
-  const int n = (int)min((long long)kRun, a.T - p0);
+  const int n = (int)min((long long)kRun, a.T - run * kRun);
   const unsigned V = (unsigned)a.V;
-  const uint2* sorted = a.sorted + p0;
+  const uint2* sorted = rows_smem + y * (kRun + 2) + 1;
   unsigned key = sorted[0].x;
-  bool begun = run > 0 && sorted[-1].x == key;
+  bool begun = sorted[-1].x == key;
   float acc[N] = {};
   constexpr int U = 8;                             // rows in flight a thread (16: 17 -> 23 us for 16384 x 2048)
 #pragma unroll 1
@@ -335,11 +347,9 @@ __global__ void __launch_bounds__(kRowThreads)
         v[i].get(f);
 #pragma unroll
         for (int k = 0; k < N; ++k) acc[k] += f[k];
-        const bool more = p0 + p + i + 1 < a.T;
-        const unsigned next = more ? sorted[p + i + 1].x : 0xffffffffu;
+        const unsigned next = sorted[p + i + 1].x;
         if (next != key || p + i + 1 == n) {
-          const bool goes_on = next == key;
-          if (!begun && !goes_on) {
+          if (!begun && next != key) {
             put_cols<TO, N, STRIDED>(dtable + (long long)key * a.D + col, acc, a.scale, a.accumulate, a.tx, nc);
           } else {
             put_cols<float, N, STRIDED>(a.part + (run * 2 + (begun ? 0 : 1)) * a.Dp + col, acc, 1.f, 0, a.tx, nc);
@@ -511,7 +521,8 @@ dash_status_t rows_typed(const void* dout, void* dtable, RowArgs a, cudaStream_t
   const long long blocks = ceil_div<long long>(a.runs, kRowThreads / a.tx) * a.col_tiles;
   if (blocks >= (1ll << 31)) return DASH_ERR_UNSUPPORTED;
   DASH_TRY(launch_after(wide ? embed_rows_kernel<TI, TO, false> : embed_rows_kernel<TI, TO, true>,
-                        dim3((unsigned)blocks), kRowThreads, 0, stream, (const TI*)dout, (TO*)dtable, a));
+                        dim3((unsigned)blocks), kRowThreads, kRowThreads / a.tx * (kRun + 2) * sizeof(uint2), stream,
+                        (const TI*)dout, (TO*)dtable, a));
   if (a.runs > 1)
     DASH_TRY(launch_after(embed_join_kernel<TO>,
                           dim3((unsigned)ceil_div<long long>(a.runs, 8), (unsigned)ceil_div(a.Dp, 128)), 256, 0,

@@ -182,7 +182,7 @@ dash_status_t dash_linear_xent_fwd(const void* x, const void* w, const void* tar
   DASH_TRY(cudaMemsetAsync(ws, 0, dash::kWsHeaderBytes, stream));
   st = launch<LSE>(p, maps, sms, true, stream);
   if (st != DASH_OK) return st;
-  DASH_TRY(dash::launch_after(lse_join_kernel, dim3((unsigned)ceil_div<long long>(T, 32)), 256, 0, stream, p.part,
+  DASH_TRY(dash::launch_after(lse_join_kernel, dim3((unsigned)ceil_div<long long>(T, 32)), 1024, 0, stream, p.part,
                               p.ztgt, 2 * ceil_div((int)V, kTN), (int)T, targets, id_bits, ignore_index, V, loss,
                               lse, p.header));
   return DASH_OK;
@@ -266,7 +266,8 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     if (st != DASH_OK) return st;
     if (pl.dx_splits > 1) {
       const size_t n = (size_t)T * D;
-      DASH_TRY(dash::launch_after(dx_join_kernel, dim3((unsigned)ceil_div<size_t>(n, 2048)), 256, 0, stream, p.acc,
+      DASH_TRY(dash::launch_after(dx_join_kernel, dim3((unsigned)ceil_div<size_t>(n, 4 * kJoinThreads)),
+                                  kJoinThreads, 0, stream, p.acc,
                                   p.splits, n, (float*)(ws + pl.acc), (int)first, (int)last, (__nv_bfloat16*)dx));
     }
     // dW of the piece = G^T X

@@ -13,7 +13,7 @@
 //
 // Bound by the tensor cores, over a whole pass by the power they draw. Measured at 8192 tokens,
 // 65536 ids, D = 4096: LSE 2.35 ms, GRAD, DX and DW of a quarter of the ids 0.59, 0.60 and 0.61
-// ms by themselves (1800 to 1870 TFLOP/s), the four in a loop 10.8 ms (1630; cuBLAS sustains
+// ms by themselves (1800 to 1870 TFLOP/s), the four in a loop 10.5 ms (1675; cuBLAS sustains
 // 1683 on this card). Tiles of 128 x 256 on single CTAs: 0.65 to 0.67 ms, 11.5 ms in a loop.
 // Loss and lse differ from exact sums by some 1e-6 of the largest logit, the rounding of the
 // tensor core's own fp32 additions along K.
@@ -104,30 +104,50 @@ __device__ __forceinline__ void unit_of(const Params& p, int u, int& mi, int& ni
   ni = r / gm;
 }
 
+// 32 bytes of one output row in one store (`wide`: the address is a multiple of 32) or two: a
+// thread owns a row, so its store should fill a whole 32-byte sector of L2. In 16-byte stores
+// each sector was written up to three times and dW of 128 tokens x 65536 ids x 2048 took 121
+// us instead of the 40 that its bytes need.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // 32 consecutive columns of one output row: fp32 values to bf16 or fp32, added to what is
-// there where the mode says so. `n` columns are valid (a multiple of 8).
+// there (or in `old32`) where the mode says so. `n` columns are valid (a multiple of 8).
 template <bool ADD>
 __device__ __forceinline__ void put_bf16(__nv_bfloat16* dst, const float* old32, const float (&v)[32],
-                                         int n) {
+                                         int n, bool wide) {
 #pragma unroll
-  for (int c = 0; c < 32; c += 8) {
-    if (c < n) {
+  for (int c = 0; c < 32; c += 16) {
+    uint32_t w[8];
+#pragma unroll
+    for (int h = 0; h < 16; h += 8) {
       float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = v[c + i];
-      if (ADD) {
+      for (int i = 0; i < 8; ++i) x[i] = v[c + h + i];
+      if (ADD && c + h < n) {
         float o[8];
-        if (old32) train::load_f32<float, 8>(old32 + c, o);
-        else train::load_f32<__nv_bfloat16, 8>(dst + c, o);
+        if (old32) train::load_f32<float, 8>(old32 + c + h, o);
+        else train::load_f32<__nv_bfloat16, 8>(dst + c + h, o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] += o[i];
       }
-      train::store_f32<__nv_bfloat16, 8>(dst + c, x);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) w[(h + i) >> 1] = ptx::pack_bf16(x[i], x[i + 1]);
     }
+    if (c + 8 < n) store32(dst + c, w, wide);
+    else if (c < n) *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 template <bool ADD>
-__device__ __forceinline__ void put_f32(float* dst, const float (&v)[32], int n) {
+__device__ __forceinline__ void put_f32(float* dst, const float (&v)[32], int n, bool wide) {
 #pragma unroll
   for (int c = 0; c < 32; c += 8) {
     if (c < n) {
@@ -140,7 +160,10 @@ __device__ __forceinline__ void put_f32(float* dst, const float (&v)[32], int n)
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] += o[i];
       }
-      train::store_f32<float, 8>(dst + c, x);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+      store32(dst + c, w, wide);
     }
   }
 }
@@ -324,22 +347,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
             w[c >> 1] = gs == 0.f ? 0u : ptx::pack_bf16(a * gs, b * gs);
           }
           if (live && n > 0) {
-            uint4* dst = reinterpret_cast<uint4*>(p.g + (size_t)row * p.ldg + col);
+            __nv_bfloat16* dst = p.g + (size_t)row * p.ldg + col;     // ldg: a multiple of 256
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t h[8] = {w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
+                                     w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
+              store32(dst + 16 * i, h, true);
+            }
           }
         } else {
           if (live && n > 0) {
             const size_t at = (size_t)row * p.N + col;
             __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
-            if (p.out_mode == OUT_BF16) put_bf16<false>(ob, nullptr, v, n);
-            else if (p.out_mode == OUT_BF16_ADD) put_bf16<true>(ob, OP == DX ? p.acc + at : nullptr, v, n);
-            else if (OP == DX && p.out_mode == OUT_PART) put_f32<false>(p.acc + (size_t)split * p.M * p.N + at, v, n);
-            else {
-              float* of = (OP == DX ? p.acc : reinterpret_cast<float*>(p.out)) + at;
-              if (p.out_mode == OUT_F32) put_f32<false>(of, v, n);
-              else put_f32<true>(of, v, n);
-            }
+            float* of = (OP == DX ? p.acc + (p.out_mode == OUT_PART ? (size_t)split * p.M * p.N : 0)
+                                  : reinterpret_cast<float*>(p.out)) + at;
+            const bool wide16 = ((uintptr_t)ob & 31) == 0, wide32 = ((uintptr_t)of & 31) == 0;
+            if (p.out_mode == OUT_BF16) put_bf16<false>(ob, nullptr, v, n, wide16);
+            else if (p.out_mode == OUT_BF16_ADD) put_bf16<true>(ob, OP == DX ? of : nullptr, v, n, wide16);
+            else if (p.out_mode == OUT_F32_ADD) put_f32<true>(of, v, n, wide32);
+            else put_f32<false>(of, v, n, wide32);
           }
         }
       }
@@ -366,38 +392,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
   }
 }
 
+__device__ __forceinline__ void add_part(float& m, float& s, const float2& x) {
+  const float nm = fmaxf(m, x.x);
+  const float base = nm == -INFINITY ? 0.f : nm;
+  s = s * ptx::ex2(m - base) + x.y * ptx::ex2(x.x - base);
+  m = nm;
+}
+
 // Joins the half tiles' (max, sum) of every row in a fixed order: 32 rows a block, the parts
-// cut into 8 runs, one thread each, then the runs in order.
-__global__ void __launch_bounds__(256) lse_join_kernel(const float2* part, const float* ztgt, int parts,
-                                                       int T, const void* targets, int id_bits,
-                                                       long long ignore_index, long long V, float* loss,
-                                                       float* lse, int* header) {
-  __shared__ float2 runs[8][32];
+// cut into 32 runs, a warp each, 8 loads in flight; then the runs in order.
+__global__ void __launch_bounds__(1024) lse_join_kernel(const float2* part, const float* ztgt, int parts,
+                                                        int T, const void* targets, int id_bits,
+                                                        long long ignore_index, long long V, float* loss,
+                                                        float* lse, int* header) {
+  __shared__ float2 runs[32][32];
   train::grid_wait();
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int row = blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.f;
   if (row < T) {
-    const int per = (parts + 7) / 8;
+    const int per = (parts + 31) / 32;
     const int end = min(parts, (g + 1) * per);
-    for (int k = g * per; k < end; ++k) {
-      const float2 x = part[(size_t)k * T + row];
-      const float nm = fmaxf(m, x.x);
-      const float base = nm == -INFINITY ? 0.f : nm;
-      s = s * ptx::ex2(m - base) + x.y * ptx::ex2(x.x - base);
-      m = nm;
+    int k = g * per;
+    for (; k + 8 <= end; k += 8) {
+      float2 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = part[(size_t)(k + i) * T + row];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) add_part(m, s, x[i]);
     }
+    for (; k < end; ++k) add_part(m, s, part[(size_t)k * T + row]);
   }
   runs[g][lane] = make_float2(m, s);
   __syncthreads();
   if (g == 0 && row < T) {
-    for (int k = 1; k < 8; ++k) {
-      const float2 x = runs[k][lane];
-      const float nm = fmaxf(m, x.x);
-      const float base = nm == -INFINITY ? 0.f : nm;
-      s = s * ptx::ex2(m - base) + x.y * ptx::ex2(x.x - base);
-      m = nm;
-    }
+    for (int k = 1; k < 32; ++k) add_part(m, s, runs[k][lane]);
     const float l = (m == -INFINITY ? 0.f : m) * kLn2 + logf(s);
     lse[row] = l;
     const long long y = train::load_index(targets, row, id_bits);
@@ -415,23 +444,35 @@ __global__ void __launch_bounds__(256) lse_join_kernel(const float2* part, const
 }
 
 // dX from the K ranges' partials, added in order (after what the pieces before left in acc,
-// when there are any); the last piece stores bf16.
-__global__ void __launch_bounds__(256) dx_join_kernel(const float* part, int splits, size_t n, float* acc,
-                                                      int first, int last, __nv_bfloat16* dx) {
-  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
+// when there are any); the last piece stores bf16. 4 columns a thread, 8 loads in flight.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) dx_join_kernel(const float* part, int splits, size_t n,
+                                                               float* acc, int first, int last,
+                                                               __nv_bfloat16* dx) {
+  const size_t i = ((size_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
   train::grid_next();
   train::grid_wait();
   if (i >= n) return;
-  float x[8] = {};
-  if (!first) train::load_f32<float, 8>(acc + i, x);
-  for (int s = 0; s < splits; ++s) {
-    float y[8];
-    train::load_f32<float, 8>(part + (size_t)s * n + i, y);
+  float x[4] = {};
+  if (!first) train::load_f32<float, 4>(acc + i, x);
+  auto add = [&](const train::Vec<float, 4>& v) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] += y[k];
+    for (int k = 0; k < 4; ++k) x[k] += __uint_as_float(v.w[k]);
+  };
+  int s = 0;
+  for (; s + 8 <= splits; s += 8) {
+    train::Vec<float, 4> v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = train::load_vec<float, 4>(part + (size_t)(s + k) * n + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) add(v[k]);
   }
-  if (last) train::store_f32<__nv_bfloat16, 8>(dx + i, x);
-  else train::store_f32<float, 8>(acc + i, x);
+  for (; s < splits; ++s) add(train::load_vec<float, 4>(part + (size_t)s * n + i));
+  if (last) {
+    *reinterpret_cast<uint2*>(dx + i) = make_uint2(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]));
+  } else {
+    train::store_f32<float, 4>(acc + i, x);
+  }
 }
 
 // Clears the header and reports targets out of range (the backward treats them as ignored).

@@ -15,8 +15,6 @@
 // 65536 ids, D = 4096: LSE 2.35 ms, GRAD, DX and DW of a quarter of the ids 0.59, 0.60 and 0.61
 // ms by themselves (1800 to 1870 TFLOP/s), the four in a loop 10.5 ms (1675; cuBLAS sustains
 // 1683 on this card). Tiles of 128 x 256 on single CTAs: 0.65 to 0.67 ms, 11.5 ms in a loop.
-// Loss and lse differ from exact sums by some 1e-6 of the largest logit, the rounding of the
-// tensor core's own fp32 additions along K.
 //
 // Warp roles (384 threads a CTA): 0 = TMA producer (64 of K per stage, 6 stages of 32 KB), 1 =
 // MMA issuer (the pair's first CTA), 4..11 = epilogue (one 32-row quarter and one half of the
@@ -87,6 +85,14 @@ constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kBarOff = kStages * kStageBytes;
 constexpr int kSmem = kBarOff + 256 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
+// LSE sums K in segments of 1024: the tensor core truncates its fp32 additions, which over
+// 4096 of K made lse 1.7e-5 too small (2.2e-6 of it; fp32 multiply-adds to nearest: 3.9e-7); a
+// segment's sum is added in registers, to nearest, while the next one is computed. Segments of
+// 512, 1024, 2048: errors of 2.6e-7, 5.4e-7, 1.1e-6, and 1.9, 0.7, 0.2 % more time for the step
+// above. The gradient needs none: G is rounded to 2^-8.
+constexpr int kSegSteps = 1024 / kTK;
+template <int OP>
+__device__ __forceinline__ constexpr int seg_steps() { return OP == LSE ? kSegSteps : 1 << 30; }
 enum { B_FULL = 0, B_EMPTY = B_FULL + kStages, B_ACC_FULL = B_EMPTY + kStages,
        B_ACC_EMPTY = B_ACC_FULL + 2, B_DRAIN = B_ACC_EMPTY + 2, B_COUNT };
 static_assert(8 * B_COUNT + 8 <= 256, "barrier space");
@@ -255,29 +261,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
       long long kb = 0;
       int it = 0;
       bool ok = true;
-      for (int u = pair; ok && u < units; u += pairs, ++it) {
-        const int acc = it & 1;
+      for (int u = pair; ok && u < units; u += pairs) {
         int mi, ni, split;
         unit_of(p, u, mi, ni, split);
-        const int k_begin = split * p.ksteps_per_split;
-        const int k_end = min(ksteps, (split + 1) * p.ksteps_per_split);
-        if (it >= 2 && !(ok = ptx::mbar_wait(bars + B_ACC_EMPTY + acc, ((it >> 1) - 1) & 1, abort_flag, tmo)))
-          break;
-        ptx::tc_fence_after();
-        for (int k = k_begin; k < k_end; ++k, ++kb) {
-          const int s = (int)(kb % kStages);
-          if (!(ok = ptx::mbar_wait(bars + B_FULL + s, (int)(kb / kStages) & 1, abort_flag, tmo))) break;
+        const int u_end = min(ksteps, (split + 1) * p.ksteps_per_split);
+        for (int k_begin = split * p.ksteps_per_split; k_begin < u_end; k_begin += seg_steps<OP>(), ++it) {
+          const int acc = it & 1;
+          const int k_end = OP == LSE ? min(u_end, k_begin + kSegSteps) : u_end;
+          if (it >= 2 && !(ok = ptx::mbar_wait(bars + B_ACC_EMPTY + acc, ((it >> 1) - 1) & 1, abort_flag, tmo)))
+            break;
           ptx::tc_fence_after();
-          const uint32_t a_lo = ptx::sdesc_lo(s0 + s * kStageBytes, A_MN ? 8192 : 16);
-          const uint32_t b_lo = ptx::sdesc_lo(s0 + s * kStageBytes + kABytes, B_MN ? 8192 : 16);
+          for (int k = k_begin; k < k_end; ++k, ++kb) {
+            const int s = (int)(kb % kStages);
+            if (!(ok = ptx::mbar_wait(bars + B_FULL + s, (int)(kb / kStages) & 1, abort_flag, tmo))) break;
+            ptx::tc_fence_after();
+            const uint32_t a_lo = ptx::sdesc_lo(s0 + s * kStageBytes, A_MN ? 8192 : 16);
+            const uint32_t b_lo = ptx::sdesc_lo(s0 + s * kStageBytes + kABytes, B_MN ? 8192 : 16);
 #pragma unroll
-          for (int ks = 0; ks < kTK / 16; ++ks)
-            ptx::mma_lo_pair(tmem + acc * kTN, a_lo + ks * A_STEP, b_lo + ks * B_STEP, ID,
-                             (k > k_begin || ks > 0) ? 1u : 0u);
-          ptx::mma_commit_pair(bars + B_EMPTY + s);
+            for (int ks = 0; ks < kTK / 16; ++ks)
+              ptx::mma_lo_pair(tmem + acc * kTN, a_lo + ks * A_STEP, b_lo + ks * B_STEP, ID,
+                               (k > k_begin || ks > 0) ? 1u : 0u);
+            ptx::mma_commit_pair(bars + B_EMPTY + s);
+          }
+          if (!ok) break;
+          ptx::mma_commit_pair(bars + B_ACC_FULL + acc);
         }
-        if (!ok) break;
-        ptx::mma_commit_pair(bars + B_ACC_FULL + acc);
       }
       ptx::mma_commit_pair(bars + B_DRAIN);
     }
@@ -286,8 +294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
     int it = 0;
-    for (int u = pair; u < units; u += pairs, ++it) {
-      const int acc = it & 1;
+    bool ok = true;
+    for (int u = pair; ok && u < units; u += pairs) {
       int mi, ni, split;
       unit_of(p, u, mi, ni, split);
       const int row = mi * kTM + rank * kCtaM + quarter * 32 + lane;
@@ -307,35 +315,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
         if (tgt == p.ignore_index) tgt = -1;
         tgt -= p.b_row0;
       }
-      if (!ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo)) break;
+      if constexpr (OP == LSE) {
+        float z[kTN / 64][32];
+        for (int k = 0; k < ksteps; k += kSegSteps, ++it) {
+          const int acc = it & 1;
+          if (!(ok = ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo))) break;
+          ptx::tc_fence_after();
+          const uint32_t from = tmem + lane_addr + acc * kTN + half * (kTN / 2);
+#pragma unroll
+          for (int c = 0; c < kTN / 64; ++c) {
+            if (k == 0) {
+              ptx::tmem_ld32(from + c * 32, z[c]);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                float t[16];
+                ptx::tmem_ld16(from + c * 32 + h, t);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z[c][h + i] += t[i];
+              }
+            }
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_peer(ptx::peer_smem(bars + B_ACC_EMPTY + acc, 0));
+        }
+        if (!ok) break;
+        float m2 = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int c0 = 0; c0 < kTN / 2; c0 += 32) {
+          float (&v)[32] = z[c0 / 32];
+          const int col = col0 + c0;                       // first column of the 32
+          const int n = p.N - col;                         // valid ones
+          if (n > 0) {
+            const long long tc = tgt - col;
+            float cm = -INFINITY;
+            float zt = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              if (c == tc) zt = v[c];
+              v[c] = c < n ? v[c] * p.scale_log2 : -INFINITY;
+              cm = fmaxf(cm, v[c]);
+            }
+            if (tc >= 0 && tc < 32 && tc < n) p.ztgt[row] = zt * p.scale;
+            const float nm = fmaxf(m2, cm);
+            const float base = nm == -INFINITY ? 0.f : nm;
+            float s = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s += ptx::ex2(v[c] - base);
+            sum = sum * ptx::ex2(m2 - base) + s;
+            m2 = nm;
+          }
+        }
+        if (live) p.part[(size_t)(ni * 2 + half) * p.M + row] = make_float2(m2, sum);
+        continue;
+      }
+      const int acc = it & 1;
+      if (!(ok = ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo))) break;
       ptx::tc_fence_after();
-      float m2 = -INFINITY, sum = 0.f;
 #pragma unroll 1
       for (int c0 = 0; c0 < kTN / 2; c0 += 32) {
         float v[32];
         ptx::tmem_ld32(tmem + lane_addr + acc * kTN + half * (kTN / 2) + c0, v);
         const int col = col0 + c0;                       // first column of the 32
         const int n = p.N - col;                         // valid ones
-        if (OP == LSE) {
-          if (n <= 0) break;
-          const long long tc = tgt - col;
-          float cm = -INFINITY;
-          float zt = 0.f;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (c == tc) zt = v[c];
-            v[c] = c < n ? v[c] * p.scale_log2 : -INFINITY;
-            cm = fmaxf(cm, v[c]);
-          }
-          if (tc >= 0 && tc < 32 && tc < n) p.ztgt[row] = zt * p.scale;
-          const float nm = fmaxf(m2, cm);
-          const float base = nm == -INFINITY ? 0.f : nm;
-          float s = 0.f;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) s += ptx::ex2(v[c] - base);
-          sum = sum * ptx::ex2(m2 - base) + s;
-          m2 = nm;
-        } else if (OP == GRAD) {
+        if (OP == GRAD) {
           const long long tc = tgt - col;
           uint32_t w[16];
 #pragma unroll
@@ -372,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_peer(ptx::peer_smem(bars + B_ACC_EMPTY + acc, 0));
-      if (OP == LSE && live) p.part[(size_t)(ni * 2 + half) * p.M + row] = make_float2(m2, sum);
+      ++it;
     }
   }
 

@@ -66,7 +66,8 @@ typedef enum {
   DASH_ERR_CUDA = 4,                /* a CUDA runtime call failed; see dash_last_error() */
   DASH_ERR_SYNC_TIMEOUT = 5,        /* a wait (dQ semaphore or in-kernel pipeline) hit its limit */
   DASH_ERR_DEADLOCK_RISK = 6,       /* the schedule's waits form a cycle on this grid */
-  DASH_ERR_BOUNDS = 7               /* checked build: a table index failed a device-side check */
+  DASH_ERR_BOUNDS = 7               /* checked build: a table index failed a device-side check;
+                                       dash_train.h: a caller's index is out of range */
 } dash_status_t;
 
 /*
@@ -188,6 +189,10 @@ dash_status_t dash_attn_bwd_static(const void* q, const void* k, const void* v, 
  * DASH_ERR_BOUNDS: an index read from the schedule tables failed its check, the CTA
  * stopped before using it, and dash_last_error() names the table, the head, the value
  * and the bound. Also returns DASH_ERR_CUDA if the stream reports an error.
+ * The workspaces of dash_train.h's calls are read the same way: DASH_ERR_BOUNDS (in either
+ * build) when a token id, a position or a target was out of range, with its row, value and
+ * bound in dash_last_error(), DASH_ERR_SYNC_TIMEOUT when a wait of the cross entropy's kernel
+ * ran out.
  */
 dash_status_t dash_attn_get_status(const void* workspace, cudaStream_t stream);
 

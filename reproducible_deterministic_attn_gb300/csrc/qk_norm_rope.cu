@@ -8,7 +8,7 @@
 // Both directions read and write every value once: bound by HBM, with the instructions next
 // (8 values a lane and shuffled partners took 22 an element forward, 31 backward, and 105 and
 // 167 us for 16384 tokens x 64 heads x 128, where the bytes take 80 and 119). A warp walks over
-// a run of (token, heads) items of its own and copies the next items' rows into its part of
+// tokens, the grid's warps apart, and copies the next items' rows into its part of
 // shared memory while it computes one (cp.async, two items ahead), so that loads are in flight
 // all the time without registers; a token's angles are loaded once for all its heads.
 #include <algorithm>
@@ -29,7 +29,7 @@ constexpr int kMaxD = 256;
 // constant and not the device's SM count: one block for each that 152 SMs hold.
 constexpr int kFwdBlocks = 456;
 constexpr int kBwdBlocks = 304;
-static_assert(2 * (kBwdBlocks + 1) <= 1024, "dw_join looks at all blocks at once");
+static_assert(kBwdBlocks + 2 <= 1024, "dw_join looks at all blocks at once");
 
 struct Side {                       // queries or keys
   const void* x;
@@ -43,6 +43,10 @@ struct Side {                       // queries or keys
   int* bad;                         // backward: [blocks], lowest token whose position is out of range
   int H;
   int blocks;                       // of the grid
+  // A unit of work is one token and gp of its head groups: parts units a token, taken step units
+  // apart by a warp. The step in (part, token, batch) digits saves divisions.
+  int groups, gp, parts, step_part, step_s, step_b;
+  unsigned units, step;
 };
 
 struct Args {
@@ -76,9 +80,13 @@ struct Lane {
   int c0, c1;
   bool in0, in1;
   __device__ __forceinline__ Lane(const Args& a, int j) {
-    const int rot = M == HALF ? a.R >> 4 : 0;      // lanes whose chunks are rotated
-    c0 = j < rot ? 8 * j : 16 * rot + 16 * (j - rot);
-    c1 = j < rot ? c0 + 8 * rot : c0 + 8;
+    // lanes side by side hold chunks side by side, so that a warp's accesses fill whole sectors:
+    // the first R / 16 lanes the halves of the rotated columns, the others those of the rest
+    const int rot = M == HALF ? a.R >> 4 : 0, from = 16 * rot;
+    const int rest = (a.D - from + 15) >> 4;
+    c0 = j < rot ? 8 * j : from + 8 * (j - rot);
+    c1 = c0 + 8 * (j < rot ? rot : rest);
+    if (j >= rot + rest) c0 = c1 = a.D;            // nothing for this lane
     in0 = c0 < a.D;
     in1 = c1 < a.D;
   }
@@ -154,39 +162,60 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
-// A warp's place in its run of items: item = (token, head group), groups first.
+// A warp's place in its work: units of one token and `gp` groups of its heads, the grid's warps
+// apart (so that together they sweep the tensor in order), group by group.
 struct Cursor {
-  int b, s, grp, groups, S;
-  unsigned left;                                  // items from here on
-  __device__ __forceinline__ Cursor(unsigned item, unsigned end, int groups_, int S_)
-      : groups(groups_), S(S_), left(end - item) {
-    const unsigned token = item / groups;
-    grp = (int)(item - token * groups);
-    b = (int)(token / S);
-    s = (int)(token - b * S);
+  int b, s, part, grp, end;
+  unsigned unit;
+  bool fresh;                                     // at the unit's first group
+  __device__ __forceinline__ Cursor(const Args& a, const Side& sd, unsigned first) : unit(first) {
+    const unsigned token = first / sd.parts;
+    part = (int)(first - token * sd.parts);
+    b = (int)(token / a.S);
+    s = (int)(token - b * a.S);
+    start(sd);
   }
-  __device__ __forceinline__ void next() {
-    --left;
-    if (++grp == groups) {
-      grp = 0;
-      if (++s == S) {
-        s = 0;
+  __device__ __forceinline__ bool more(const Side& sd) const { return unit < sd.units; }
+  __device__ __forceinline__ void start(const Side& sd) {
+    grp = part * sd.gp;
+    end = min(grp + sd.gp, sd.groups);
+    fresh = true;
+  }
+  __device__ __forceinline__ void next(const Args& a, const Side& sd) {
+    fresh = false;
+    if (++grp == end) {                           // step units on, in mixed digits
+      unit += sd.step;
+      part += sd.step_part;
+      s += sd.step_s;
+      b += sd.step_b;
+      if (part >= sd.parts) {
+        part -= sd.parts;
+        ++s;
+      }
+      if (s >= a.S) {
+        s -= a.S;
         ++b;
       }
+      start(sd);
     }
   }
 };
 
 // 8 values from global to shared memory without registers; zeros where `live` is false. A warp's
-// 16-byte pieces lie side by side, 512 bytes a piece of every lane.
+// 16-byte pieces lie side by side, 512 bytes a piece of every lane. The two pieces of 8 fp32
+// values share a sector, which L1 keeps for the second.
 template <typename T>
 __device__ __forceinline__ void copy8(uint32_t dst, const T* src, bool live) {
   const int n = live ? 16 : 0;
+  if constexpr (sizeof(T) == 2) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  } else {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512),
-                 "l"(reinterpret_cast<const char*>(src) + (live ? i * 16 : 0)), "r"(n)
-                 : "memory");
+    for (int i = 0; i < 2; ++i)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512),
+                   "l"(reinterpret_cast<const char*>(src) + (live ? i * 16 : 0)), "r"(n)
+                   : "memory");
+  }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -209,38 +238,41 @@ __device__ __forceinline__ void from_shared(const char* at, float* f) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = y[i];
 }
+// 8 fp32 values in one store where the address allows it: a whole sector.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  if (sizeof(T) == 4 && ((uintptr_t)p & 31) == 0)
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]),
+                 "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+  else
+    store_f32<T, 8>(p, x);
+}
 template <typename T, int M>
 __device__ __forceinline__ void store16(T* row, const Lane<M>& ln, const float (&v)[16]) {
   float x[8];
   if (ln.in0) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = v[i];
-    store_f32<T, 8>(row + ln.c0, x);
+    store8<T>(row + ln.c0, x);
   }
   if (ln.in1) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = v[8 + i];
-    store_f32<T, 8>(row + ln.c1, x);
+    store8<T>(row + ln.c1, x);
   }
 }
 
-constexpr int kItemsAhead = 2;                    // items in shared memory beside the one in work
+// Items in shared memory beside the one in work: two of U groups of heads. The backward takes
+// one group an item, which needs fewer registers, and as many bytes ahead.
+template <typename T, bool BWD>
+constexpr int kItemsAhead = BWD && sizeof(T) == 2 ? 4 : 2;
 
 // Bytes of one row of every lane group of a warp: 8 values a lane, twice.
 template <typename T>
 constexpr int kChunkBytes = 32 * 8 * (int)sizeof(T);
 template <typename T, int U, bool BWD>
-constexpr int kSharedBytes = kWarps * (kItemsAhead + 1) * U * (BWD ? 4 : 2) * kChunkBytes<T>;
-
-// This warp's run of a tensor's items.
-template <int U, int L>
-__device__ __forceinline__ Cursor warp_items(const Args& a, const Side& sd, int block) {
-  constexpr int RW = 32 / L;
-  const unsigned groups = (unsigned)(sd.H + U * RW - 1) / (U * RW), items = (unsigned)a.tokens * groups;
-  const unsigned warps = (unsigned)sd.blocks * kWarps, per = (items + warps - 1) / warps;
-  const unsigned first = min(items, ((unsigned)block * kWarps + (threadIdx.x >> 5)) * per);
-  return Cursor(first, min(items, first + per), (int)groups, a.S);
-}
+constexpr int kSharedBytes = kWarps * (kItemsAhead<T, BWD> + 1) * U * (BWD ? 4 : 2) * kChunkBytes<T>;
 
 // The token's position, -1 when it is out of range.
 __device__ __forceinline__ long long position(const Args& a, int b, int s) {
@@ -250,7 +282,7 @@ __device__ __forceinline__ long long position(const Args& a, int b, int s) {
 
 template <typename T, int L, int M, int U>
 __global__ void __launch_bounds__(kThreads, M == ANY ? 2 : 3) fwd_kernel(const Args a) {
-  constexpr int RW = 32 / L, kStages = kItemsAhead + 1;   // RW: heads a warp handles at once
+  constexpr int RW = 32 / L, kAhead = kItemsAhead<T, false>, kStages = kAhead + 1;   // RW: heads a warp handles at once
   extern __shared__ char qk_smem[];
   const int which = blockIdx.x >= a.side[0].blocks;
   const Side& sd = a.side[which];
@@ -259,10 +291,10 @@ __global__ void __launch_bounds__(kThreads, M == ANY ? 2 : 3) fwd_kernel(const A
   const float inv_d = 1.f / a.D;
   char* mine = qk_smem + warp * (kStages * U * 2 * kChunkBytes<T>) + lane * 16;
   const uint32_t mine_s = (uint32_t)__cvta_generic_to_shared(mine);
-  Cursor at = warp_items<U, L>(a, sd, blockIdx.x - (which ? a.side[0].blocks : 0));
+  Cursor at(a, sd, (blockIdx.x - (which ? a.side[0].blocks : 0)) * kWarps + warp);
   Cursor ahead = at;
   auto fetch = [&](int stage) {                    // the item at `ahead`; an empty group past the end
-    if (ahead.left > 0) {
+    if (ahead.more(sd)) {
       const T* x = (const T*)sd.x + ahead.b * sd.sb + ahead.s * sd.ss;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -273,20 +305,19 @@ __global__ void __launch_bounds__(kThreads, M == ANY ? 2 : 3) fwd_kernel(const A
         copy8<T>(to, live && ln.in0 ? row + ln.c0 : row, live && ln.in0);
         copy8<T>(to + kChunkBytes<T>, live && ln.in1 ? row + ln.c1 : row, live && ln.in1);
       }
-      ahead.next();
+      ahead.next(a, sd);
     }
     copies_commit();
   };
 #pragma unroll
-  for (int k = 0; k < kItemsAhead; ++k) fetch(k);
+  for (int k = 0; k < kAhead; ++k) fetch(k);
   // a pair's output is r (x_a (w_a c) - x_b (w_b s)), r (x_b (w_b c) + x_a (w_a s))
   float ac[8], bs[8], bc[8], as[8], w[16];
   if (M == ANY) load_weights(sd.w, ln, w);
   long long p = 0;
-  bool fresh = true;                               // the token's angles are not here yet
-  for (int stage = 0; at.left > 0;) {
+  for (int stage = 0; at.more(sd);) {
     fetch(stage >= 1 ? stage - 1 : kStages - 1);   // into the stage that the last item left
-    if (fresh || at.grp == 0) {
+    if (at.fresh) {
       p = position(a, at.b, at.s);
       if (p < 0 && a.status) *a.status = kStatusBounds;
       if constexpr (M != ANY) {
@@ -302,9 +333,8 @@ __global__ void __launch_bounds__(kThreads, M == ANY ? 2 : 3) fwd_kernel(const A
           as[i] = wa * s[i];
         }
       }
-      fresh = false;
     }
-    copies_wait<kItemsAhead>();
+    copies_wait<kAhead>();
     T* out = (T*)sd.out + at.b * sd.ob + at.s * sd.os;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -337,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, M == ANY ? 2 : 3) fwd_kernel(const A
       }
       if (h < sd.H) store16<T, M>(out + h * sd.oh, ln, y);
     }
-    at.next();
+    at.next(a, sd);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 }
@@ -347,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, M == ANY ? 2 : 3) fwd_kernel(const A
 // columns' part of dw in registers; the block's warps are added in order.
 template <typename T, int L, int M, int U>
 __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args a) {
-  constexpr int RW = 32 / L, kStages = kItemsAhead + 1;
+  constexpr int RW = 32 / L, kAhead = kItemsAhead<T, true>, kStages = kAhead + 1;
   extern __shared__ char qk_smem[];
   __shared__ float dws[kWarps][kMaxD];
   __shared__ int bad;
@@ -362,10 +392,10 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args a) {
   const float inv_d = 1.f / a.D;
   char* mine = qk_smem + warp * (kStages * U * 4 * kChunkBytes<T>) + lane * 16;
   const uint32_t mine_s = (uint32_t)__cvta_generic_to_shared(mine);
-  Cursor at = warp_items<U, L>(a, sd, block);
+  Cursor at(a, sd, (unsigned)block * kWarps + warp);
   Cursor ahead = at;
   auto fetch = [&](int stage) {
-    if (ahead.left > 0) {
+    if (ahead.more(sd)) {
       const T* x = (const T*)sd.x + ahead.b * sd.sb + ahead.s * sd.ss;
       const T* d = (const T*)sd.dout + ((long long)ahead.b * a.S + ahead.s) * sd.H * a.D;
 #pragma unroll
@@ -380,25 +410,23 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args a) {
         copy8<T>(to + 2 * kChunkBytes<T>, l0 ? dr + ln.c0 : dr, l0);
         copy8<T>(to + 3 * kChunkBytes<T>, l1 ? dr + ln.c1 : dr, l1);
       }
-      ahead.next();
+      ahead.next(a, sd);
     }
     copies_commit();
   };
 #pragma unroll
-  for (int k = 0; k < kItemsAhead; ++k) fetch(k);
+  for (int k = 0; k < kAhead; ++k) fetch(k);
   float w[16], dw[16] = {}, c[8], s[8];
   load_weights(sd.w, ln, w);
   long long p = 0;
-  bool fresh = true;
-  for (int stage = 0; at.left > 0;) {
+  for (int stage = 0; at.more(sd);) {
     fetch(stage >= 1 ? stage - 1 : kStages - 1);
-    if (fresh || at.grp == 0) {
+    if (at.fresh) {
       p = position(a, at.b, at.s);
       if (p < 0 && lane == 0) atomicMin(&bad, at.b * a.S + at.s);
       if constexpr (M != ANY) load_angles<M>(a, ln, p, c, s);
-      fresh = false;
     }
-    copies_wait<kItemsAhead>();
+    copies_wait<kAhead>();
     T* out = (T*)sd.out + at.b * sd.ob + at.s * sd.os;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -440,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(const Args a) {
       }
       if (h < sd.H) store16<T, M>(out + h * sd.oh, ln, e);
     }
-    at.next();
+    at.next(a, sd);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   // heads of the warp, then warps, in order
@@ -469,7 +497,7 @@ __global__ void __launch_bounds__(1024) dw_join_kernel(const Args a) {
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     if (threadIdx.x == 0) first = kNoToken;
     __syncthreads();
-    const int n = a.side[0].blocks, b = threadIdx.x;      // at most 1024 blocks
+    const int n = a.side[0].blocks, b = threadIdx.x;      // at most kBwdBlocks + 2
     if (b < n + a.side[1].blocks) {
       const int t = b < n ? a.side[0].bad[b] : a.side[1].bad[b - n];
       if (t != kNoToken) atomicMin(&first, t);
@@ -511,25 +539,36 @@ __global__ void __launch_bounds__(1024) dw_join_kernel(const Args a) {
 template <typename T, int L, int M>
 dash_status_t launch(Args a, bool bwd, cudaStream_t stream) {
   constexpr int RW = 32 / L;
-  constexpr int U = sizeof(T) == 4 ? 1 : 2;
+  constexpr int UF = sizeof(T) == 4 ? 1 : 2;
   // heads in flight a warp: U when that leaves every warp of the chip (about 10^4) an item,
   // else one, which spreads few tokens over more warps
   const long long rows = (long long)a.tokens * (a.side[0].H + a.side[1].H);
-  const bool many = rows / (U * RW) >= 9728;
-  const int per = many ? U * RW : RW;
+  const bool many = !bwd && rows / (UF * RW) >= 9728;
+  const int per = many ? UF * RW : RW;
   // each tensor's share of the blocks goes by its heads
   const int H = a.side[0].H + a.side[1].H, most = bwd ? kBwdBlocks : kFwdBlocks;
   for (int i = 0; i < 2; ++i) {
     const long long items = (long long)a.tokens * ceil_div(a.side[i].H, per);
     const long long share = H > 0 ? std::max<long long>(1, ((long long)most * a.side[i].H + H / 2) / H) : 0;
     a.side[i].blocks = (int)std::min<long long>(ceil_div<long long>(items, kWarps), share);
+    // whole tokens a unit when every warp gets several, else parts of them
+    Side& sd = a.side[i];
+    const long long warps = (long long)sd.blocks * kWarps;
+    sd.groups = std::max(1, ceil_div(sd.H, per));
+    const long long parts = a.tokens > 0 ? std::min<long long>(sd.groups, ceil_div<long long>(4 * warps, a.tokens)) : 1;
+    sd.gp = (int)ceil_div<long long>(sd.groups, std::max<long long>(parts, 1));
+    sd.parts = ceil_div(sd.groups, sd.gp);
+    sd.units = (unsigned)a.tokens * sd.parts;
+    sd.step = (unsigned)warps;
+    sd.step_part = (int)(warps % sd.parts);
+    const long long tokens = warps / sd.parts;
+    sd.step_s = a.S > 0 ? (int)(tokens % a.S) : 0;
+    sd.step_b = a.S > 0 ? (int)(tokens / a.S) : 0;
   }
   const unsigned grid = a.side[0].blocks + a.side[1].blocks;
   if (grid > 0) {
-    const auto kernel = bwd ? (many ? bwd_kernel<T, L, M, U> : bwd_kernel<T, L, M, 1>)
-                            : (many ? fwd_kernel<T, L, M, U> : fwd_kernel<T, L, M, 1>);
-    const int smem = bwd ? (many ? kSharedBytes<T, U, true> : kSharedBytes<T, 1, true>)
-                         : (many ? kSharedBytes<T, U, false> : kSharedBytes<T, 1, false>);
+    const auto kernel = bwd ? bwd_kernel<T, L, M, 1> : many ? fwd_kernel<T, L, M, UF> : fwd_kernel<T, L, M, 1>;
+    const int smem = bwd ? kSharedBytes<T, 1, true> : many ? kSharedBytes<T, UF, false> : kSharedBytes<T, 1, false>;
     DASH_TRY(allow_shared((const void*)kernel, smem));
     kernel<<<grid, kThreads, smem, stream>>>(a);
     DASH_TRY(cudaGetLastError());

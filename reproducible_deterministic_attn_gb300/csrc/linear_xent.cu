@@ -23,7 +23,10 @@ struct Plan {
   long long piece;            // vocabulary rows a piece, a multiple of 256
   int pieces;
   long long ldg;
+  bool two;                   // G as two bf16 terms (up to kTwoTermRows tokens)
+  long long g_rows;           // rows of G, and of one K range's dX
   int dx_splits, dx_ksteps;   // K ranges of dX within a full piece
+  bool joined;                // dX goes through partials and a join
   size_t part, ztgt;          // forward
   size_t g, acc, dx_part;     // backward
   size_t total;
@@ -49,7 +52,9 @@ void dx_ranges(long long T, int D, long long piece, int* splits, int* per) {
 Plan make_plan(long long T, long long V, int D) {
   Plan pl;
   const long long rows = std::max<long long>(T, 1);
-  pl.piece = std::max<long long>(1, (long long)(kPieceBytes / 2 / kTN) / rows) * kTN;
+  pl.two = T <= kTwoTermRows;
+  pl.g_rows = pl.two ? 2 * kTwoTermRows : rows;
+  pl.piece = std::max<long long>(1, (long long)(kPieceBytes / 2 / kTN) / pl.g_rows) * kTN;
   pl.piece = std::min(pl.piece, ceil_div<long long>(V, kTN) * kTN);
   pl.pieces = (int)ceil_div<long long>(V, pl.piece);
   pl.ldg = pl.piece;
@@ -64,9 +69,10 @@ Plan make_plan(long long T, long long V, int D) {
   pl.part = take((size_t)2 * ceil_div<long long>(V, kTN) * rows * sizeof(float2));
   const size_t fwd = at;
   at = dash::kWsHeaderBytes;
-  pl.g = take((size_t)rows * pl.ldg * 2);
+  pl.g = take((size_t)pl.g_rows * pl.ldg * 2);
   pl.acc = take(pl.pieces > 1 ? (size_t)rows * D * 4 : 0);
-  pl.dx_part = take(pl.dx_splits > 1 ? (size_t)pl.dx_splits * rows * D * 4 : 0);
+  pl.joined = pl.dx_splits > 1 || pl.two;
+  pl.dx_part = take(pl.joined ? (size_t)pl.dx_splits * pl.g_rows * D * 4 : 0);
   pl.total = std::max(fwd, at);
   return pl;
 }
@@ -228,6 +234,8 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   base.timeout_ns = dash::sync_timeout_ns();
   base.withhold = dash::sync_withheld();
   base.splits = 1;
+  base.two = pl.two;
+  base.rows = (int)T;
   Maps grad, dxm, dwm;
   if (!map_2d(&grad.a, x, T, D, ldx, kCtaM) || !map_2d(&grad.b, w, V, D, ldw, kCtaN) ||
       !map_2d(&dxm.b, w, V, D, ldw, kTK) || !map_2d(&dwm.b, x, T, D, ldx, kTK))
@@ -238,7 +246,10 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   for (int i = 0; i < pl.pieces; ++i) {
     const long long v0 = i * pl.piece, vp = std::min(pl.piece, V - v0);
     const bool first = i == 0, last = i == pl.pieces - 1;
-    if (!map_2d(&dxm.a, g, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a, g, T, vp, pl.ldg, kTK)) return bad_map();
+    const __nv_bfloat16* g2 = pl.two ? g + kTwoTermRows * pl.ldg : g;      // the second terms
+    if (!map_2d(&dxm.a, g, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a, g, T, vp, pl.ldg, kTK) ||
+        !map_2d(&dxm.a2, g2, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a2, g2, T, vp, pl.ldg, kTK))
+      return bad_map();
     Params p = base;
     p.b_row0 = (int)v0;
     // G of the piece
@@ -256,7 +267,8 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     p.ksteps_per_split = ceil_div((int)vp, kTK);
     p.acc = (float*)(ws + pl.acc);
     p.out_mode = first ? (last ? OUT_BF16 : OUT_F32) : (last ? OUT_BF16_ADD : OUT_F32_ADD);
-    if (pl.dx_splits > 1) {
+    if (pl.joined) {
+      p.M = (int)pl.g_rows;
       p.ksteps_per_split = pl.dx_ksteps;
       p.splits = ceil_div(ceil_div((int)vp, kTK), pl.dx_ksteps);
       p.out_mode = OUT_PART;
@@ -264,18 +276,20 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     }
     st = launch<DX>(p, dxm, sms, false, stream);
     if (st != DASH_OK) return st;
-    if (pl.dx_splits > 1) {
+    if (pl.joined) {
       const size_t n = (size_t)T * D;
       DASH_TRY(dash::launch_after(dx_join_kernel, dim3((unsigned)ceil_div<size_t>(n, 4 * kJoinThreads)),
                                   kJoinThreads, 0, stream, p.acc,
-                                  p.splits, n, (float*)(ws + pl.acc), (int)first, (int)last, (__nv_bfloat16*)dx));
+                                  p.splits, n, (size_t)pl.g_rows * D,
+                                  pl.two ? (size_t)kTwoTermRows * D : (size_t)0, (float*)(ws + pl.acc), (int)first,
+                                  (int)last, (__nv_bfloat16*)dx));
     }
     // dW of the piece = G^T X
     p.M = (int)vp;
     p.N = D;
     p.K = (int)T;
     p.splits = 1;
-    p.ksteps_per_split = ceil_div((int)T, kTK);
+    p.ksteps_per_split = (pl.two ? 2 : 1) * ceil_div((int)T, kTK);
     p.out = (char*)dw + (size_t)v0 * D * dw_elt;
     p.out_mode = dw_dtype == DASH_FP32 ? (accumulate ? OUT_F32_ADD : OUT_F32)
                                        : (accumulate ? OUT_BF16_ADD : OUT_BF16);

@@ -5,6 +5,10 @@
 //   GRAD  Z = X W^T again  the tile becomes G = g (exp(z - lse) - [v = y]) in bf16
 //   DX    dX = G W         K = the vocabulary (of one piece), W read N-major
 //   DW    dW = G^T X       K = the tokens, both operands MN-major
+// Up to 128 tokens half of a tile's rows would be empty. There G is held as two bf16 terms, the
+// second one what the first one's rounding left: DX puts the second terms into the other half
+// (its join adds them), DW takes them as 128 more tokens. So G's rounding costs no precision
+// where few tokens do not average it out, and no time.
 // A unit of work is one output tile of 256 x 256 (for DX one K range of it), dealt round robin
 // to pairs of CTAs on neighbouring SMs (cta_group::2): each CTA loads its 128 rows of A and
 // its 128 columns of B, one thread of the pair issues MMAs of 256 x 256 x 16 over both, and
@@ -59,7 +63,7 @@ struct Params {
   // GRAD
   const float* lse;
   const float* dloss;
-  __nv_bfloat16* g;          // [M][ldg]
+  __nv_bfloat16* g;          // [M][ldg]; two terms: [2 * 128][ldg]
   long long ldg;
   long long V;
   // DX, DW
@@ -68,12 +72,16 @@ struct Params {
   float* acc;                // DX: fp32 [M][N] over the pieces, or the K ranges' partials
   int* header;
   long long timeout_ns;
+  int two;                   // G is held as two terms
+  int rows;                  // tokens
   int withhold;              // testing hook: load no tiles, so the waits for them run out
 };
 
 struct Maps {
   CUtensorMap a, b;
+  CUtensorMap a2;            // DX, DW: G's second terms
 };
+constexpr int kTwoTermRows = 128;
 
 constexpr int kXentThreads = 384;
 constexpr int kTM = 256, kTN = 256, kTK = 64;         // of a pair
@@ -189,7 +197,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const long long tmo = p.timeout_ns;
   const int units = p.tiles_m * p.tiles_n * p.splits;
-  const int ksteps = (p.K + kTK - 1) / kTK;
+  const int ksteps1 = (p.K + kTK - 1) / kTK;               // of one term
+  const int ksteps = OP == DW && p.two ? 2 * ksteps1 : ksteps1;
 
   if (threadIdx.x == 0) {
     ptx::prefetch_map(&maps.a);
@@ -234,12 +243,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
           if (rank == 0) ptx::mbar_expect_tx(bars + B_FULL + s, 2 * kStageBytes);
           uint8_t* sa = sm + s * kStageBytes;
           uint8_t* sb = sa + kABytes;
-          const int k0 = k * kTK;
+          int k0 = k * kTK, row = m0;
+          const CUtensorMap* map_a = &maps.a;
+          if (OP == DW && k >= ksteps1) {
+            map_a = &maps.a2;
+            k0 -= ksteps1 * kTK;
+          }
+          if (OP == DX && p.two && rank == 1) {
+            map_a = &maps.a2;
+            row = 0;
+          }
           if (A_MN) {
             for (int i = 0; i < kCtaM / 64; ++i)
-              ptx::tma_load_2d_pair(sa + i * 8192, &maps.a, m0 + i * 64, k0, full);
+              ptx::tma_load_2d_pair(sa + i * 8192, map_a, row + i * 64, k0, full);
           } else {
-            ptx::tma_load_2d_pair(sa, &maps.a, k0, m0, full);
+            ptx::tma_load_2d_pair(sa, map_a, k0, row, full);
           }
           if (B_MN) {
             const int kr = OP == DX ? p.b_row0 + k0 : k0;
@@ -300,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
       unit_of(p, u, mi, ni, split);
       const int row = mi * kTM + rank * kCtaM + quarter * 32 + lane;
       const int col0 = ni * kTN + half * (kTN / 2);
-      const bool live = row < p.M;
+      const bool live = OP == DX && p.two ? (row & (kTwoTermRows - 1)) < p.rows : row < p.M;
       // what the row needs besides the tile, fetched before the wait
       long long tgt = -1;
       float nlse2 = 0.f, gs = 0.f;
@@ -381,14 +399,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
         const int n = p.N - col;                         // valid ones
         if (OP == GRAD) {
           const long long tc = tgt - col;
-          uint32_t w[16];
+          uint32_t w[16], w2[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             float a = ptx::ex2(fmaf(v[c], p.scale_log2, nlse2));
             float b = ptx::ex2(fmaf(v[c + 1], p.scale_log2, nlse2));
             if (c == tc) a -= 1.f;
             if (c + 1 == tc) b -= 1.f;
-            w[c >> 1] = gs == 0.f ? 0u : ptx::pack_bf16(a * gs, b * gs);
+            a = gs == 0.f ? 0.f : a * gs;
+            b = gs == 0.f ? 0.f : b * gs;
+            w[c >> 1] = ptx::pack_bf16(a, b);
+            if (p.two)
+              w2[c >> 1] = ptx::pack_bf16(a - __uint_as_float(w[c >> 1] << 16),
+                                          b - __uint_as_float(w[c >> 1] & 0xffff0000u));
           }
           if (live && n > 0) {
             __nv_bfloat16* dst = p.g + (size_t)row * p.ldg + col;     // ldg: a multiple of 256
@@ -397,6 +420,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
               const uint32_t h[8] = {w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
                                      w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
               store32(dst + 16 * i, h, true);
+              if (p.two) {
+                const uint32_t l[8] = {w2[8 * i], w2[8 * i + 1], w2[8 * i + 2], w2[8 * i + 3],
+                                       w2[8 * i + 4], w2[8 * i + 5], w2[8 * i + 6], w2[8 * i + 7]};
+                store32(dst + kTwoTermRows * p.ldg + 16 * i, l, true);
+              }
             }
           }
         } else {
@@ -487,12 +515,13 @@ __global__ void __launch_bounds__(1024) lse_join_kernel(const float2* part, cons
   }
 }
 
-// dX from the K ranges' partials, added in order (after what the pieces before left in acc,
-// when there are any); the last piece stores bf16. 4 columns a thread, 8 loads in flight.
+// dX from the K ranges' partials of n values each, added in order (after what the pieces before
+// left in acc, when there are any), each with its second term's `second` values on where there
+// is one; the last piece stores bf16. 4 columns a thread, 8 loads in flight.
 constexpr int kJoinThreads = 128;
 __global__ void __launch_bounds__(kJoinThreads) dx_join_kernel(const float* part, int splits, size_t n,
-                                                               float* acc, int first, int last,
-                                                               __nv_bfloat16* dx) {
+                                                               size_t stride, size_t second, float* acc,
+                                                               int first, int last, __nv_bfloat16* dx) {
   const size_t i = ((size_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
   train::grid_next();
   train::grid_wait();
@@ -503,15 +532,18 @@ __global__ void __launch_bounds__(kJoinThreads) dx_join_kernel(const float* part
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] += __uint_as_float(v.w[k]);
   };
-  int s = 0;
-  for (; s + 8 <= splits; s += 8) {
-    train::Vec<float, 4> v[8];
+  for (int term = 0; term < (second ? 2 : 1); ++term) {
+    const float* from = part + term * second + i;
+    int s = 0;
+    for (; s + 8 <= splits; s += 8) {
+      train::Vec<float, 4> v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = train::load_vec<float, 4>(part + (size_t)(s + k) * n + i);
+      for (int k = 0; k < 8; ++k) v[k] = train::load_vec<float, 4>(from + (s + k) * stride);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) add(v[k]);
+      for (int k = 0; k < 8; ++k) add(v[k]);
+    }
+    for (; s < splits; ++s) add(train::load_vec<float, 4>(from + s * stride));
   }
-  for (; s < splits; ++s) add(train::load_vec<float, 4>(part + (size_t)s * n + i));
   if (last) {
     *reinterpret_cast<uint2*>(dx + i) = make_uint2(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]));
   } else {

@@ -77,13 +77,16 @@ Plan make_plan(long long T, long long V, int D) {
   return pl;
 }
 
-// Row-major bf16 [rows][cols], `ld` elements between rows; box = 64 columns x box_rows.
-bool map_2d(CUtensorMap* m, const void* ptr, long long rows, long long cols, long long ld, int box_rows) {
+// Row-major bf16 (or fp32) [rows][cols], `ld` elements between rows; box = 128 bytes of columns x
+// box_rows.
+bool map_2d(CUtensorMap* m, const void* ptr, long long rows, long long cols, long long ld, int box_rows,
+            bool f32 = false) {
+  const int e = f32 ? 4 : 2;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * e};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / e), (cuuint32_t)box_rows};
   const cuuint32_t es[2] = {1, 1};
-  return dash::tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims,
+  return dash::tensor_map_encoder()(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims,
                                     strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -119,13 +122,13 @@ dash_status_t launch(Params p, const Maps& maps, int sms, bool first, cudaStream
     dash::set_last_error("too many output tiles for one call");
     return DASH_ERR_UNSUPPORTED;
   }
-  DASH_TRY(dash::allow_shared((const void*)gemm_kernel<OP>, kSmem));
+  DASH_TRY(dash::allow_shared((const void*)gemm_kernel<OP>, kSmem<OP>));
   const int grid = 2 * (int)std::min<long long>(units, sms / 2);
   if (first) {
-    gemm_kernel<OP><<<grid, kXentThreads, kSmem, stream>>>(p, maps);
+    gemm_kernel<OP><<<grid, kXentThreads, kSmem<OP>, stream>>>(p, maps);
     DASH_TRY(cudaGetLastError());
   } else {
-    DASH_TRY(dash::launch_after(gemm_kernel<OP>, dim3(grid), kXentThreads, kSmem, stream, p, maps));
+    DASH_TRY(dash::launch_after(gemm_kernel<OP>, dim3(grid), kXentThreads, kSmem<OP>, stream, p, maps));
   }
   return DASH_OK;
 }
@@ -248,7 +251,8 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     const bool first = i == 0, last = i == pl.pieces - 1;
     const __nv_bfloat16* g2 = pl.two ? g + kTwoTermRows * pl.ldg : g;      // the second terms
     if (!map_2d(&dxm.a, g, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a, g, T, vp, pl.ldg, kTK) ||
-        !map_2d(&dxm.a2, g2, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a2, g2, T, vp, pl.ldg, kTK))
+        !map_2d(&dxm.a2, g2, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a2, g2, T, vp, pl.ldg, kTK) ||
+        !map_2d(&dwm.c, (char*)dw + (size_t)v0 * D * dw_elt, vp, D, D, 32, dw_dtype == DASH_FP32))
       return bad_map();
     Params p = base;
     p.b_row0 = (int)v0;

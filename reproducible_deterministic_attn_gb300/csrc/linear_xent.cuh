@@ -80,6 +80,7 @@ struct Params {
 struct Maps {
   CUtensorMap a, b;
   CUtensorMap a2;            // DX, DW: G's second terms
+  CUtensorMap c;             // DW, not accumulated: the output, boxes of 32 rows x 128 bytes
 };
 constexpr int kTwoTermRows = 128;
 
@@ -91,8 +92,12 @@ constexpr int kGroupM = 8;
 constexpr int kABytes = kCtaM * kTK * 2, kBBytes = kCtaN * kTK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kBarOff = kStages * kStageBytes;
-constexpr int kSmem = kBarOff + 256 + 1024;
-static_assert(kSmem <= 232448, "shared memory budget");
+// DW stores its tiles from shared memory, 32 rows x 128 bytes a warp at a time: whole lines. From
+// registers, 32 bytes of a row a thread, dW of 64 tokens x 32768 ids x 1024 took 31 us (2.1 TB/s).
+constexpr int kStoreOff = kBarOff + 1024, kStoreBytes = 4096;
+template <int OP>
+constexpr int kSmem = (OP == 3 ? kStoreOff + 8 * kStoreBytes : kBarOff + 256) + 1024;
+static_assert(kSmem<3> <= 232448, "shared memory budget");
 // LSE sums K in segments of 1024: the tensor core truncates its fp32 additions, which over
 // 4096 of K made lse 1.7e-5 too small (2.2e-6 of it; fp32 multiply-adds to nearest: 3.9e-7); a
 // segment's sum is added in registers, to nearest, while the next one is computed. Segments of
@@ -178,6 +183,40 @@ __device__ __forceinline__ void put_f32(float* dst, const float (&v)[32], int n,
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
       store32(dst + c, w, wide);
+    }
+  }
+}
+
+// A warp's 32 rows x 128 columns of dW from its accumulator, through its place in shared memory
+// (rows of 128 bytes, 16-byte chunks swizzled as the tensor map has them).
+template <bool F32>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint8_t* buf, uint32_t tmem_from, int col,
+                                           int row0, int rows, int cols, int lane) {
+  constexpr int W = F32 ? 32 : 64;                         // columns of 128 bytes
+#pragma unroll 1
+  for (int c0 = 0; c0 < kTN / 2; c0 += W) {
+    if (lane == 0) ptx::bulk_wait_read_all();              // the last store has left the buffer
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < W; q += 32) {
+      float v[32];
+      ptx::tmem_ld32(tmem_from + c0 + q, v);
+      constexpr int CH = F32 ? 8 : 4;                      // 16-byte chunks of 32 columns
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = (q / 32) * CH + i;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = F32 ? __float_as_uint(v[4 * i + k]) : ptx::pack_bf16(v[(8 * i + 2 * k) & 31], v[(8 * i + 2 * k + 1) & 31]);
+        ptx::st_shared_v4(ptx::smem_u32(buf) + lane * 128 + ((c ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+      }
+    }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && row0 < rows && col + c0 < cols) {
+      ptx::tma_store_2d(map, buf, col + c0, row0);
+      ptx::bulk_commit();
     }
   }
 }
@@ -391,10 +430,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
       const int acc = it & 1;
       if (!(ok = ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo))) break;
       ptx::tc_fence_after();
+      const uint32_t from = tmem + lane_addr + acc * kTN + half * (kTN / 2);
+      const bool by_tile = OP == DW && (p.out_mode == OUT_BF16 || p.out_mode == OUT_F32);
+      if (OP == DW && by_tile) {
+        uint8_t* buf = sm + kStoreOff + (warp - 4) * kStoreBytes;
+        const int row0 = row - lane;
+        if (p.out_mode == OUT_F32) store_tile<true>(&maps.c, buf, from, col0, row0, p.M, p.N, lane);
+        else store_tile<false>(&maps.c, buf, from, col0, row0, p.M, p.N, lane);
+      }
 #pragma unroll 1
-      for (int c0 = 0; c0 < kTN / 2; c0 += 32) {
+      for (int c0 = 0; c0 < (by_tile ? 0 : kTN / 2); c0 += 32) {
         float v[32];
-        ptx::tmem_ld32(tmem + lane_addr + acc * kTN + half * (kTN / 2) + c0, v);
+        ptx::tmem_ld32(from + c0, v);
         const int col = col0 + c0;                       // first column of the 32
         const int n = p.N - col;                         // valid ones
         if (OP == GRAD) {
@@ -446,6 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
       if (lane == 0) ptx::mbar_arrive_peer(ptx::peer_smem(bars + B_ACC_EMPTY + acc, 0));
       ++it;
     }
+    if (OP == DW && lane == 0) ptx::bulk_wait_all();       // the stores have been performed
   }
 
   // Every MMA and with it every copy of the pair has ended once DRAIN completes; neither CTA

@@ -92,8 +92,9 @@ constexpr int kGroupM = 8;
 constexpr int kABytes = kCtaM * kTK * 2, kBBytes = kCtaN * kTK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kBarOff = kStages * kStageBytes;
-// DW stores its tiles from shared memory, 32 rows x 128 bytes a warp at a time: whole lines. From
-// registers, 32 bytes of a row a thread, dW of 64 tokens x 32768 ids x 1024 took 31 us (2.1 TB/s).
+// DW stores its tiles from shared memory, 32 rows x 128 bytes a warp at a time: whole lines. For
+// few tokens its stores are all there is: gradients of 128 tokens x 65536 ids x 2048 take 201 us,
+// 215 with 32 bytes of a row a thread.
 constexpr int kStoreOff = kBarOff + 1024, kStoreBytes = 4096;
 template <int OP>
 constexpr int kSmem = (OP == 3 ? kStoreOff + 8 * kStoreBytes : kBarOff + 256) + 1024;
@@ -124,9 +125,8 @@ __device__ __forceinline__ void unit_of(const Params& p, int u, int& mi, int& ni
 }
 
 // 32 bytes of one output row in one store (`wide`: the address is a multiple of 32) or two: a
-// thread owns a row, so its store should fill a whole 32-byte sector of L2. In 16-byte stores
-// each sector was written up to three times and dW of 128 tokens x 65536 ids x 2048 took 121
-// us instead of the 40 that its bytes need.
+// thread owns a row, so its store should fill a whole 32-byte sector of L2 (16-byte stores wrote
+// each sector up to three times: gradients of 128 tokens x 65536 ids x 2048 took 240 us, 203 so).
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),

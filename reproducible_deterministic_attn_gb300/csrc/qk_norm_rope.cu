@@ -7,7 +7,8 @@
 // for interleaved pairs, a value's partner is read once more, which hits L1.)
 // Both directions read and write every value once: bound by HBM, with the instructions next
 // (8 values a lane and shuffled partners took 22 an element forward, 31 backward, and 105 and
-// 167 us for 16384 tokens x 64 heads x 128, where the bytes take 80 and 119). A warp walks over
+// 167 us for 16384 tokens x 64 heads x 128; now 15 and 23, and 232 us for both, where the bytes
+// take 200). A warp walks over
 // tokens, the grid's warps apart, and copies the next items' rows into its part of
 // shared memory while it computes one (cp.async, two items ahead), so that loads are in flight
 // all the time without registers; a token's angles are loaded once for all its heads.
@@ -25,8 +26,9 @@ using namespace dash::train;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 256;
-// Blocks that share the rows. The backward's number fixes how dw's sum is split, so it is a
-// constant and not the device's SM count: one block for each that 152 SMs hold.
+// Blocks that share the rows: three (forward) and two (backward) for each of 152 SMs, which is
+// what an SM holds. The backward's number fixes how dw's sum is split, so it is a constant and
+// not the device's SM count.
 constexpr int kFwdBlocks = 456;
 constexpr int kBwdBlocks = 304;
 static_assert(kBwdBlocks + 2 <= 1024, "dw_join looks at all blocks at once");

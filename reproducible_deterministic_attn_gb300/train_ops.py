@@ -221,8 +221,8 @@ def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, device="c
 
 @functools.lru_cache(maxsize=1024)
 def _strides(batch: int, token: int, head: int):
-    """Three strides as the C calls read them: the array (kept by the cache while calls use it)
-    and its address."""
+    """Three strides as the C calls read them: the array, which the caller holds for the time
+    of its call, and its address."""
     arr = _c3(batch, token, head)
     return arr, ctypes.addressof(arr)
 
@@ -265,7 +265,7 @@ def _qk_args(q, k, wq, wk, cos, sin, positions):
             _bad("positions: expected [B, S] or [S]")
         pos = positions.data_ptr()
     return dev, (pwq, pwk, cos.data_ptr(), sin.data_ptr(), pos), (B, S, Hq, Hk, D, 2 * half, P, qs[1], ks[1]), \
-        stride, bits
+        stride, bits, (qs, ks)
 
 
 def qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -277,7 +277,7 @@ def qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions=None, eps: float = 1e
     None; cos, sin: fp32 [P, R / 2] (rope_table); positions: int [B, S] or [S], default 0 .. S - 1;
     interleaved: pairs (2i, 2i + 1) rather than (i, i + R / 2). status as in embed_forward.
     Returns contiguous (q_out, k_out) as attn_forward takes them."""
-    dev, tables, sizes, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
+    dev, tables, sizes, stride, bits, held = _qk_args(q, k, wq, wk, cos, sin, positions)
     q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)
     _raise(_core.load().dash_qk_norm_rope_fwd(
         q.data_ptr(), k.data_ptr(), *tables, q_out.data_ptr(), k_out.data_ptr(), _status_word(status, dev),
@@ -305,7 +305,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None
     dq_out, dk_out: contiguous, as attn_backward returns them. dq, dk: optional tensors to
     write to, strided like q and k may be (parts of a fused projection's gradient). Returns
     (dq, dk, dwq, dwk), the last two fp32 [D] or None where the weight is None."""
-    dev, tables, sizes, stride, bits = _qk_args(q, k, wq, wk, cos, sin, positions)
+    dev, tables, sizes, stride, bits, held = _qk_args(q, k, wq, wk, cos, sin, positions)
     dtype, qshape, kshape, D = q.dtype, q.shape, k.shape, sizes[4]
     if (dq_out.dtype != dtype or dq_out.shape != qshape or not dq_out.is_contiguous() or dq_out.get_device() != dev
             or dk_out.dtype != dtype or dk_out.shape != kshape or not dk_out.is_contiguous()

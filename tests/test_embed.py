@@ -86,6 +86,17 @@ def test_lookup_shapes_strides_and_no_tokens():
     assert da.embed_forward(table, ids[:0]).shape == (0, 6, 88)
 
 
+def test_lookup_into_strided_rows():
+    """The C call's output stride: the elements between the rows stay as they are."""
+    for D, ld in ((64, 72), (64, 67), (33, 40)):
+        table = torch.randn(20, D, device="cuda").bfloat16()
+        ids = torch.randint(0, 20, (9,), device="cuda")
+        out = torch.full((9, ld), 5.0, dtype=torch.bfloat16, device="cuda")
+        assert da.load().dash_embed_fwd(table.data_ptr(), ids.data_ptr(), out.data_ptr(), None, 9, 20, D, D, ld, 1.0,
+                                        da.DASH_BF16, 64, torch.cuda.current_stream().cuda_stream) == da.DASH_OK
+        assert torch.equal(out[:, :D], table[ids]) and bool((out[:, D:] == 5).all())
+
+
 def test_lookup_out_of_range_gives_nan_rows_and_the_status():
     table = torch.randn(50, 64, device="cuda").bfloat16()
     ids = torch.tensor([3, 50, -1, 7, 2 ** 40], device="cuda")

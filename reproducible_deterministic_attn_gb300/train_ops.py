@@ -1,7 +1,8 @@
 """Thin Python binding of the training-step operators in libdash_attn (include/dash_train.h).
 
 As in dash_attn.py the functions only check and marshal their arguments; every step runs in
-the library's CUDA kernels on torch's current stream of the tensors' device (or `stream`).
+the library's CUDA kernels on torch's current stream of the tensors' device (or `stream`, on
+which a call then also allocates what it returns and uses).
 Wrong types, shapes or devices raise ValueError before anything is queued, a status other
 than DASH_OK raises DashError. With check=True a call that has a workspace waits for the
 stream and raises what the device reported (an index out of range); check=False leaves that
@@ -78,11 +79,19 @@ def _on(t, name: str, dev: int):
         _bad(f"{name}: expected a tensor on cuda:{dev}")
 
 
-def _stream(dev: int, stream) -> int:
-    """The raw handle of `stream`, or of torch's current stream on the device."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+def _stream(dev: int) -> int:
+    """The raw handle of torch's current stream on the device."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _using(stream, t):
+    """Makes `stream` (a torch stream or a raw handle) the current one, so that what a call
+    allocates belongs to the stream that its kernels run on."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=t.device) if handle
+                  else torch.cuda.default_stream(t.device))
+    return torch.cuda.stream(stream)
 
 
 def _rows(t, name: str):
@@ -124,9 +133,9 @@ def _ws(t, dev: int):
     return t.data_ptr(), t.nbytes
 
 
-def _finish(workspace, stream, check: bool, where: str):
+def _finish(workspace, check: bool, where: str):
     if check:
-        _raise(dash_attn_get_status(workspace, stream), where + " (device status)")
+        _raise(dash_attn_get_status(workspace), where + " (device status)")
 
 
 # ---- token embedding --------------------------------------------------------------------------
@@ -137,6 +146,9 @@ def embed_forward(table, ids, scale: float = 1.0, out=None, status=None, stream=
     table: [V, D] bf16, fp16 or fp32 with contiguous rows; ids: contiguous int32 or int64 of
     any shape. status: an optional int32 CUDA tensor of one element, which reads
     DASH_ERR_BOUNDS when an id was out of range (its row is NaN). Returns [*ids.shape, D]."""
+    if stream is not None:
+        with _using(stream, table):
+            return embed_forward(table, ids, scale, out, status)
     dev = _device(table, "table")
     dtype = _DTYPE.get(table.dtype)
     if dtype is None:
@@ -150,7 +162,7 @@ def embed_forward(table, ids, scale: float = 1.0, out=None, status=None, stream=
         _bad(f"out: expected contiguous [*ids.shape, D] of the table's type on cuda:{dev}")
     _raise(_core.load().dash_embed_fwd(
         table.data_ptr(), ids.data_ptr(), out.data_ptr(), _status_word(status, dev), ids.numel(), V, D, ld, D,
-        scale, dtype, bits, _stream(dev, stream)), "dash_embed_fwd")
+        scale, dtype, bits, _stream(dev)), "dash_embed_fwd")
     return out
 
 
@@ -173,6 +185,9 @@ def embed_backward(dout, ids, vocab: int, scale: float = 1.0, padding_idx=None, 
     dout: [*ids.shape, D] (2-D: rows may be strided); ids as in embed_forward. padding_idx:
     an id whose tokens are left out. dtable: an optional contiguous [vocab, D] tensor of
     dout's type or fp32 to write to, or to add to with accumulate=True. Returns dtable."""
+    if stream is not None:
+        with _using(stream, dout):
+            return embed_backward(dout, ids, vocab, scale, padding_idx, dtable, accumulate, workspace, check=check)
     dev = _device(dout, "dout")
     dtype = _DTYPE.get(dout.dtype)
     if dtype is None:
@@ -204,8 +219,8 @@ def embed_backward(dout, ids, vocab: int, scale: float = 1.0, padding_idx=None, 
     ws, nbytes = _ws(workspace, dev)
     _raise(_core.load().dash_embed_bwd(
         dout.data_ptr(), ids.data_ptr(), dtable.data_ptr(), ws, nbytes, T, vocab, D, ld, scale, padding_idx,
-        accumulate, dtype, _DTYPE[dtable.dtype], bits, _stream(dev, stream)), "dash_embed_bwd")
-    _finish(workspace, stream, check, "dash_embed_bwd")
+        accumulate, dtype, _DTYPE[dtable.dtype], bits, _stream(dev)), "dash_embed_bwd")
+    _finish(workspace, check, "dash_embed_bwd")
     return dtable
 
 
@@ -277,11 +292,14 @@ def qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions=None, eps: float = 1e
     None; cos, sin: fp32 [P, R / 2] (rope_table); positions: int [B, S] or [S], default 0 .. S - 1;
     interleaved: pairs (2i, 2i + 1) rather than (i, i + R / 2). status as in embed_forward.
     Returns contiguous (q_out, k_out) as attn_forward takes them."""
+    if stream is not None:
+        with _using(stream, q):
+            return qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions, eps, interleaved, status)
     dev, tables, sizes, stride, bits, held = _qk_args(q, k, wq, wk, cos, sin, positions)
     q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)
     _raise(_core.load().dash_qk_norm_rope_fwd(
         q.data_ptr(), k.data_ptr(), *tables, q_out.data_ptr(), k_out.data_ptr(), _status_word(status, dev),
-        *sizes, stride, eps, interleaved, _DTYPE[q.dtype], bits, _stream(dev, stream)), "dash_qk_norm_rope_fwd")
+        *sizes, stride, eps, interleaved, _DTYPE[q.dtype], bits, _stream(dev)), "dash_qk_norm_rope_fwd")
     return q_out, k_out
 
 
@@ -305,6 +323,10 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None
     dq_out, dk_out: contiguous, as attn_backward returns them. dq, dk: optional tensors to
     write to, strided like q and k may be (parts of a fused projection's gradient). Returns
     (dq, dk, dwq, dwk), the last two fp32 [D] or None where the weight is None."""
+    if stream is not None:
+        with _using(stream, q):
+            return qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq,
+                                         dk, workspace, check=check)
     dev, tables, sizes, stride, bits, held = _qk_args(q, k, wq, wk, cos, sin, positions)
     dtype, qshape, kshape, D = q.dtype, q.shape, k.shape, sizes[4]
     if (dq_out.dtype != dtype or dq_out.shape != qshape or not dq_out.is_contiguous() or dq_out.get_device() != dev
@@ -331,8 +353,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None
     _raise(_core.load().dash_qk_norm_rope_bwd(
         dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), *tables, dq.data_ptr(), dk.data_ptr(),
         pdwq, pdwk, ws, nbytes, *sizes, dqn[4][1], dkn[4][1], stride, eps, interleaved, _DTYPE[dtype], bits,
-        _stream(dev, stream)), "dash_qk_norm_rope_bwd")
-    _finish(workspace, stream, check, "dash_qk_norm_rope_bwd")
+        _stream(dev)), "dash_qk_norm_rope_bwd")
+    _finish(workspace, check, "dash_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -355,6 +377,9 @@ def grad_clip_plan(grads, out=None, stream=None) -> GradClipPlan:
     outs = grads if out is None else list(out)
     if not grads or len(outs) != len(grads):
         _bad("grads: expected tensors, as many as out")
+    if stream is not None:
+        with _using(stream, grads[0]):
+            return grad_clip_plan(grads, None if out is None else outs)
     dev = _device(grads[0], "grads[0]")
     arr = (_ClipTensor * len(grads))()
     spans = set()
@@ -376,7 +401,7 @@ def grad_clip_plan(grads, out=None, stream=None) -> GradClipPlan:
     if nbytes == 0:
         raise DashError(DASH_ERR_UNSUPPORTED, "dash_grad_clip_plan_size")
     table = torch.empty(nbytes, dtype=torch.uint8, device=grads[0].device)
-    _raise(lib.dash_grad_clip_plan(arr, len(grads), table.data_ptr(), nbytes, _stream(dev, stream)),
+    _raise(lib.dash_grad_clip_plan(arr, len(grads), table.data_ptr(), nbytes, _stream(dev)),
            "dash_grad_clip_plan")
     return GradClipPlan(grads, outs, table, torch.empty((), dtype=_F32, device=grads[0].device))
 
@@ -385,8 +410,11 @@ def grad_clip(plan: GradClipPlan, max_norm: float, stream=None):
     """Global L2 norm of the plan's gradients, which are scaled by max_norm / norm when it is
     above max_norm. Returns (norm, tensors): norm is a device fp32 scalar that the next call
     overwrites."""
+    if stream is not None:
+        with _using(stream, plan.table):
+            return grad_clip(plan, max_norm)
     _raise(_core.load().dash_grad_clip(plan.table.data_ptr(), plan.table.nbytes, max_norm, plan.norm.data_ptr(),
-                                       _stream(plan.device, stream)), "dash_grad_clip")
+                                       _stream(plan.device)), "dash_grad_clip")
     return plan.norm, plan.outs
 
 
@@ -424,6 +452,9 @@ def linear_xent_forward(x, w, targets, ignore_index: int = -100, scale: float = 
 
     x: bf16 [T, D] hidden states, w: bf16 [V, D] output embedding, targets: int [T].
     Returns (loss, lse), fp32 [T]; rows whose target is ignore_index have loss 0."""
+    if stream is not None:
+        with _using(stream, x):
+            return linear_xent_forward(x, w, targets, ignore_index, scale, workspace, check=check)
     dev, bits, sizes = _xent_args(x, w, targets)
     T = sizes[0]
     if workspace is None:
@@ -433,8 +464,8 @@ def linear_xent_forward(x, w, targets, ignore_index: int = -100, scale: float = 
     ws, nbytes = _ws(workspace, dev)
     _raise(_core.load().dash_linear_xent_fwd(
         x.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws, nbytes, *sizes,
-        scale, ignore_index, bits, _stream(dev, stream)), "dash_linear_xent_fwd")
-    _finish(workspace, stream, check, "dash_linear_xent_fwd")
+        scale, ignore_index, bits, _stream(dev)), "dash_linear_xent_fwd")
+    _finish(workspace, check, "dash_linear_xent_fwd")
     return loss, lse
 
 
@@ -446,6 +477,10 @@ def linear_xent_backward(x, w, targets, lse, dloss, ignore_index: int = -100, sc
     lse: from linear_xent_forward; dloss: fp32 [T]. dw: an optional [V, D] bf16 or fp32
     tensor to write to, or to add to with accumulate=True (tied embeddings, several
     micro-batches); else one of dw_dtype (bf16) is allocated. Returns (dx, dw)."""
+    if stream is not None:
+        with _using(stream, x):
+            return linear_xent_backward(x, w, targets, lse, dloss, ignore_index, scale, dw, accumulate, dw_dtype,
+                                        workspace, check=check)
     dev, bits, sizes = _xent_args(x, w, targets)
     T, V, D = sizes[:3]
     plse, pdloss = _vector(lse, "lse", T, dev), _vector(dloss, "dloss", T, dev)
@@ -461,7 +496,7 @@ def linear_xent_backward(x, w, targets, lse, dloss, ignore_index: int = -100, sc
     ws, nbytes = _ws(workspace, dev)
     _raise(_core.load().dash_linear_xent_bwd(
         x.data_ptr(), w.data_ptr(), targets.data_ptr(), plse, pdloss, dx.data_ptr(), dw.data_ptr(), ws, nbytes,
-        *sizes, scale, ignore_index, bits, _DTYPE[dw.dtype], accumulate, _stream(dev, stream)),
+        *sizes, scale, ignore_index, bits, _DTYPE[dw.dtype], accumulate, _stream(dev)),
         "dash_linear_xent_bwd")
-    _finish(workspace, stream, check, "dash_linear_xent_bwd")
+    _finish(workspace, check, "dash_linear_xent_bwd")
     return dx, dw

@@ -7,6 +7,7 @@ import os
 import pytest
 import torch
 
+import reproducible_deterministic_attn_gb300 as da
 from tests._lib import ensure_built, has_gpu
 
 pytestmark = [pytest.mark.gpu,
@@ -66,3 +67,45 @@ def test_step_gradients_match_float64_autograd(example):
     for n, t in tr.grads.items():
         err = (t.double() - p[n].grad).abs().max() / p[n].grad.abs().max()
         assert float(err) <= 10 * 2.0 ** -8, (n, float(err))
+
+
+def test_calls_on_a_given_stream_allocate_there(example):
+    """Each call with stream= (a torch stream or its handle), without a workspace and without
+    waiting, while other work fills and frees memory on the current stream."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    T, V, W = 256, 600, 128
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    table = torch.randn(V, W, generator=g, device="cuda").bfloat16()
+    dout = torch.randn(T, W, generator=g, device="cuda").bfloat16()
+    qkv = torch.randn(1, T, 6, 64, generator=g, device="cuda").bfloat16()
+    q, k = qkv[:, :, :2], qkv[:, :, 2:4]
+    dq = torch.randn(1, T, 2, 64, generator=g, device="cuda").bfloat16()
+    cos, sin = da.rope_table(T, 64)
+    w = torch.ones(64, device="cuda")
+    dl = torch.full((T,), 1.0 / T, device="cuda")
+    grad = torch.randn(100000, generator=g, device="cuda")
+
+    def run(stream):
+        x = da.embed_forward(table, ids, 2.0, stream=stream)
+        qk = da.qk_norm_rope_forward(q, k, w, w, cos, sin, stream=stream)
+        loss, lse = da.linear_xent_forward(x, table, ids, stream=stream, check=False)
+        out = [x, *qk, loss, lse]
+        out += da.linear_xent_backward(x, table, ids, lse, dl, stream=stream, check=False)
+        out += da.qk_norm_rope_backward(dq, dq, q, k, w, w, cos, sin, stream=stream, check=False)
+        out.append(da.embed_backward(dout, ids, V, 2.0, stream=stream, check=False))
+        clipped = torch.empty_like(grad)
+        plan = da.grad_clip_plan([grad], [clipped], stream=stream)
+        out.append(da.grad_clip(plan, 1.0, stream=stream)[0].clone() if stream is None
+                   else da.grad_clip(plan, 1.0, stream=stream)[0])
+        return out + [clipped]
+
+    want = run(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for given in (s, s.cuda_stream):
+        s.wait_stream(torch.cuda.current_stream())
+        got = run(given)
+        for _ in range(20):                       # memory that a wrong owner would hand out again
+            torch.full((1 << 20,), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -169,7 +169,7 @@ dash_status_t dash_linear_xent_fwd(const void* x, const void* w, const void* tar
     return DASH_OK;
   }
   const Plan pl = make_plan(T, V, D);
-  Maps maps;
+  Maps maps = {};
   if (!map_2d(&maps.a, x, T, D, ldx, kCtaM) || !map_2d(&maps.b, w, V, D, ldw, kCtaN)) return bad_map();
   Params p = {};
   p.M = (int)T;
@@ -239,7 +239,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   base.splits = 1;
   base.two = pl.two;
   base.rows = (int)T;
-  Maps grad, dxm, dwm;
+  Maps grad = {}, dxm = {}, dwm = {};
   if (!map_2d(&grad.a, x, T, D, ldx, kCtaM) || !map_2d(&grad.b, w, V, D, ldw, kCtaN) ||
       !map_2d(&dxm.b, w, V, D, ldw, kTK) || !map_2d(&dwm.b, x, T, D, ldx, kTK))
     return bad_map();
@@ -249,9 +249,15 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   for (int i = 0; i < pl.pieces; ++i) {
     const long long v0 = i * pl.piece, vp = std::min(pl.piece, V - v0);
     const bool first = i == 0, last = i == pl.pieces - 1;
-    const __nv_bfloat16* g2 = pl.two ? g + kTwoTermRows * pl.ldg : g;      // the second terms
-    if (!map_2d(&dxm.a, g, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a, g, T, vp, pl.ldg, kTK) ||
-        !map_2d(&dxm.a2, g2, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a2, g2, T, vp, pl.ldg, kTK) ||
+    if (!map_2d(&dxm.a, g, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a, g, T, vp, pl.ldg, kTK)) return bad_map();
+    dxm.a2 = dxm.a;
+    dwm.a2 = dwm.a;
+    if (pl.two) {
+      const __nv_bfloat16* g2 = g + kTwoTermRows * pl.ldg;
+      if (!map_2d(&dxm.a2, g2, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a2, g2, T, vp, pl.ldg, kTK)) return bad_map();
+    }
+    dwm.c = dwm.a;                       // read only where dW is not accumulated
+    if (!accumulate &&
         !map_2d(&dwm.c, (char*)dw + (size_t)v0 * D * dw_elt, vp, D, D, 32, dw_dtype == DASH_FP32))
       return bad_map();
     Params p = base;

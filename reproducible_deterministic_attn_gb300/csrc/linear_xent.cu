@@ -113,11 +113,17 @@ dash_status_t check_args(const void* x, const void* w, const void* targets, cons
   return DASH_OK;
 }
 
+// Fills in the tiles of a product and returns its units of work.
+long long set_tiles(Params* p) {
+  p->tiles_m = ceil_div(p->M, kTM);
+  p->tiles_n = ceil_div(p->N, kTN);
+  return (long long)p->tiles_m * p->tiles_n * p->splits;
+}
+
 template <int OP>
-dash_status_t launch(Params p, const Maps& maps, int sms, bool first, cudaStream_t stream) {
-  p.tiles_m = ceil_div(p.M, kTM);
-  p.tiles_n = ceil_div(p.N, kTN);
-  const long long units = (long long)p.tiles_m * p.tiles_n * p.splits;
+dash_status_t launch(Params p, const Maps& maps, Second<OP> second, int sms, bool first, cudaStream_t stream) {
+  long long units = set_tiles(&p);
+  if constexpr (OP == BOTH) units += set_tiles(&second.p);
   if (units >= (1ll << 31) - 1024) {
     dash::set_last_error("too many output tiles for one call");
     return DASH_ERR_UNSUPPORTED;
@@ -125,10 +131,10 @@ dash_status_t launch(Params p, const Maps& maps, int sms, bool first, cudaStream
   DASH_TRY(dash::allow_shared((const void*)gemm_kernel<OP>, kSmem<OP>));
   const int grid = 2 * (int)std::min<long long>(units, sms / 2);
   if (first) {
-    gemm_kernel<OP><<<grid, kXentThreads, kSmem<OP>, stream>>>(p, maps);
+    gemm_kernel<OP><<<grid, kXentThreads, kSmem<OP>, stream>>>(p, maps, second);
     DASH_TRY(cudaGetLastError());
   } else {
-    DASH_TRY(dash::launch_after(gemm_kernel<OP>, dim3(grid), kXentThreads, kSmem<OP>, stream, p, maps));
+    DASH_TRY(dash::launch_after(gemm_kernel<OP>, dim3(grid), kXentThreads, kSmem<OP>, stream, p, maps, second));
   }
   return DASH_OK;
 }
@@ -189,7 +195,7 @@ dash_status_t dash_linear_xent_fwd(const void* x, const void* w, const void* tar
   p.timeout_ns = dash::sync_timeout_ns();
   p.withhold = dash::sync_withheld();
   DASH_TRY(cudaMemsetAsync(ws, 0, dash::kWsHeaderBytes, stream));
-  st = launch<LSE>(p, maps, sms, true, stream);
+  st = launch<LSE>(p, maps, {}, sms, true, stream);
   if (st != DASH_OK) return st;
   DASH_TRY(dash::launch_after(lse_join_kernel, dim3((unsigned)ceil_div<long long>(T, 32)), 1024, 0, stream, p.part,
                               p.ztgt, 2 * ceil_div((int)V, kTN), (int)T, targets, id_bits, ignore_index, V, loss,
@@ -267,7 +273,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     p.N = (int)vp;
     p.K = D;
     p.ksteps_per_split = ceil_div(D, kTK);
-    st = launch<GRAD>(p, grad, sms, false, stream);
+    st = launch<GRAD>(p, grad, {}, sms, false, stream);
     if (st != DASH_OK) return st;
     // dX += G W
     p.N = D;
@@ -284,7 +290,21 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
       p.out_mode = OUT_PART;
       p.acc = (float*)(ws + pl.dx_part);
     }
-    st = launch<DX>(p, dxm, sms, false, stream);
+    // dW of the piece = G^T X
+    Second<BOTH> dwp;
+    dwp.maps = dwm;
+    Params& d = dwp.p;
+    d = base;
+    d.M = (int)vp;
+    d.N = D;
+    d.K = (int)T;
+    d.splits = 1;
+    d.ksteps_per_split = (pl.two ? 2 : 1) * ceil_div((int)T, kTK);
+    d.out = (char*)dw + (size_t)v0 * D * dw_elt;
+    d.out_mode = dw_dtype == DASH_FP32 ? (accumulate ? OUT_F32_ADD : OUT_F32)
+                                       : (accumulate ? OUT_BF16_ADD : OUT_BF16);
+    const bool together = set_tiles(&p) + set_tiles(&d) <= kTogetherRounds * (sms / 2);
+    st = together ? launch<BOTH>(p, dxm, dwp, sms, false, stream) : launch<DX>(p, dxm, {}, sms, false, stream);
     if (st != DASH_OK) return st;
     if (pl.joined) {
       const size_t n = (size_t)T * D;
@@ -294,17 +314,10 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
                                   pl.two ? (size_t)kTwoTermRows * D : (size_t)0, (float*)(ws + pl.acc), (int)first,
                                   (int)last, (__nv_bfloat16*)dx));
     }
-    // dW of the piece = G^T X
-    p.M = (int)vp;
-    p.N = D;
-    p.K = (int)T;
-    p.splits = 1;
-    p.ksteps_per_split = (pl.two ? 2 : 1) * ceil_div((int)T, kTK);
-    p.out = (char*)dw + (size_t)v0 * D * dw_elt;
-    p.out_mode = dw_dtype == DASH_FP32 ? (accumulate ? OUT_F32_ADD : OUT_F32)
-                                       : (accumulate ? OUT_BF16_ADD : OUT_BF16);
-    st = launch<DW>(p, dwm, sms, false, stream);
-    if (st != DASH_OK) return st;
+    if (!together) {
+      st = launch<DW>(d, dwm, {}, sms, false, stream);
+      if (st != DASH_OK) return st;
+    }
   }
   return DASH_OK;
 }

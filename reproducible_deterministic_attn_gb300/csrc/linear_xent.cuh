@@ -1,5 +1,5 @@
 // Softmax cross entropy from hidden states (X [T, D], W [V, D], both bf16) without stored
-// logits, and its gradient. Four products share one persistent tensor-core kernel:
+// logits, and its gradient. Four products share one persistent tensor-core kernel's code:
 //   LSE   Z = X W^T        a 256 x 256 tile of logits is reduced to (max, sum of exp2) per
 //                          row and half tile; the target's logit is stored
 //   GRAD  Z = X W^T again  the tile becomes G = g (exp(z - lse) - [v = y]) in bf16
@@ -9,6 +9,8 @@
 // second one what the first one's rounding left: DX puts the second terms into the other half
 // (its join adds them), DW takes them as 128 more tokens. So G's rounding costs no precision
 // where few tokens do not average it out, and no time.
+// DX and DW of a piece share a launch (BOTH) where they are few tiles (kTogetherRounds): neither
+// reads what the other writes, and their tiles fill the chip's last round together.
 // A unit of work is one output tile of 256 x 256 (for DX one K range of it), dealt round robin
 // to pairs of CTAs on neighbouring SMs (cta_group::2): each CTA loads its 128 rows of A and
 // its 128 columns of B, one thread of the pair issues MMAs of 256 x 256 x 16 over both, and
@@ -38,7 +40,7 @@ namespace xent {
 
 using namespace dash::tc;
 
-enum Op : int { LSE = 0, GRAD = 1, DX = 2, DW = 3 };
+enum Op : int { LSE = 0, GRAD = 1, DX = 2, DW = 3, BOTH = 4 };
 
 // What DX does with a finished tile, and DW by type and accumulation.
 enum OutMode : int {
@@ -96,9 +98,16 @@ constexpr int kBarOff = kStages * kStageBytes;
 // few tokens its stores are all there is: gradients of 128 tokens x 65536 ids x 2048 take 201 us,
 // 215 with 32 bytes of a row a thread.
 constexpr int kStoreOff = kBarOff + 1024, kStoreBytes = 4096;
+// DX and DW run in one launch up to this many units a pair of SMs. Backward pass, two launches /
+// one: 333 tokens x 5003 ids at D = 64, 1024, 4096 (1, 2, 5 a pair) 19.8 / 15.3, 33.4 / 28.8,
+// 64.0 / 59.7 us; 64 x 32768 at 1024 (7.7) 61.7 / 60.2; 1024 x 32768 at 1024 (7.6) 143.3 / 143.3;
+// 2048 x 32768 at 2048 (14) 504.3 / 505.4; 128 x 65536 at 2048 (28) 203 / 210, where reads of W
+// then run among writes of dW.
+constexpr int kTogetherRounds = 8;
+
 template <int OP>
-constexpr int kSmem = (OP == 3 ? kStoreOff + 8 * kStoreBytes : kBarOff + 256) + 1024;
-static_assert(kSmem<3> <= 232448, "shared memory budget");
+constexpr int kSmem = (OP == DW || OP == BOTH ? kStoreOff + 8 * kStoreBytes : kBarOff + 256) + 1024;
+static_assert(kSmem<BOTH> <= 232448, "shared memory budget");
 // LSE sums K in segments of 1024: the tensor core truncates its fp32 additions, which over
 // 4096 of K made lse 1.7e-5 too small (2.2e-6 of it; fp32 multiply-adds to nearest: 3.9e-7); a
 // segment's sum is added in registers, to nearest, while the next one is computed. Segments of
@@ -221,292 +230,375 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, uint8_t* buf,
   }
 }
 
+// What the roles of a CTA share.
+struct Cta {
+  uint8_t* sm;
+  uint64_t* bars;
+  volatile int* abort_flag;
+  uint32_t tmem;
+  int rank, warp, lane;        // rank 0: the pair's first CTA
+  long long tmo;
+};
 template <int OP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
-    gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
-  constexpr bool A_MN = OP == DW, B_MN = OP == DX || OP == DW;
-  extern __shared__ uint8_t smem_xent[];
-  train::grid_next();
-  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_xent + 1023) & ~(uintptr_t)1023);
-  uint64_t* bars = (uint64_t*)(sm + kBarOff);
-  uint32_t* tmem_slot = (uint32_t*)(sm + kBarOff + 8 * B_COUNT);
-  volatile int* abort_flag = (volatile int*)(sm + kBarOff + 8 * B_COUNT + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)ptx::cluster_rank();               // 0: the pair's first CTA
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const long long tmo = p.timeout_ns;
-  const int units = p.tiles_m * p.tiles_n * p.splits;
-  const int ksteps1 = (p.K + kTK - 1) / kTK;               // of one term
-  const int ksteps = OP == DW && p.two ? 2 * ksteps1 : ksteps1;
+constexpr bool kAMn = OP == DW;
+template <int OP>
+constexpr bool kBMn = OP == DX || OP == DW;
+// K steps of one of G's terms, and of a unit's whole K.
+__device__ __forceinline__ int ksteps_one(const Params& p) { return (p.K + kTK - 1) / kTK; }
+template <int OP>
+__device__ __forceinline__ int ksteps_all(const Params& p) {
+  return OP == DW && p.two ? 2 * ksteps_one(p) : ksteps_one(p);
+}
+__device__ __forceinline__ int units_of(const Params& p) { return p.tiles_m * p.tiles_n * p.splits; }
 
-  if (threadIdx.x == 0) {
-    ptx::prefetch_map(&maps.a);
-    ptx::prefetch_map(&maps.b);
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bars + B_FULL + s, 1);
-      ptx::mbar_init(bars + B_EMPTY + s, 1);
+// TMA producer, one unit. kb: K blocks so far.
+template <int OP>
+__device__ __forceinline__ void load_unit(const Params& p, const Maps& maps, const Cta& c, int u, long long& kb,
+                                          bool& ok) {
+  constexpr bool A_MN = kAMn<OP>, B_MN = kBMn<OP>;
+  uint8_t* sm = c.sm;
+  uint64_t* bars = c.bars;
+  volatile int* abort_flag = c.abort_flag;
+  const int rank = c.rank, ksteps1 = ksteps_one(p), ksteps = ksteps_all<OP>(p);
+  const long long tmo = c.tmo;
+  int mi, ni, split;
+  unit_of(p, u, mi, ni, split);
+  const int m0 = mi * kTM + rank * kCtaM, n0 = ni * kTN + rank * kCtaN;
+  const int k_end = min(ksteps, (split + 1) * p.ksteps_per_split);
+  for (int k = split * p.ksteps_per_split; k < k_end; ++k, ++kb) {
+    const int s = (int)(kb % kStages);
+    if (kb >= kStages &&
+        !(ok = ptx::mbar_wait(bars + B_EMPTY + s, (int)((kb / kStages) - 1) & 1, abort_flag, tmo)))
+      break;
+    // the first CTA expects both CTAs' bytes; the other's may arrive before that
+    const uint32_t full = ptx::peer_smem(bars + B_FULL + s, 0);
+    if (rank == 0) ptx::mbar_expect_tx(bars + B_FULL + s, 2 * kStageBytes);
+    uint8_t* sa = sm + s * kStageBytes;
+    uint8_t* sb = sa + kABytes;
+    int k0 = k * kTK, row = m0;
+    const CUtensorMap* map_a = &maps.a;
+    if (OP == DW && k >= ksteps1) {
+      map_a = &maps.a2;
+      k0 -= ksteps1 * kTK;
     }
-    for (int a = 0; a < 2; ++a) {
-      ptx::mbar_init(bars + B_ACC_FULL + a, 1);
-      ptx::mbar_init(bars + B_ACC_EMPTY + a, 16);          // 8 epilogue warps of each CTA
+    if (OP == DX && p.two && rank == 1) {
+      map_a = &maps.a2;
+      row = 0;
     }
-    ptx::mbar_init(bars + B_DRAIN, 1);
-    *abort_flag = 0;
-    ptx::fence_barrier_init();
+    if (A_MN) {
+      for (int i = 0; i < kCtaM / 64; ++i)
+        ptx::tma_load_2d_pair(sa + i * 8192, map_a, row + i * 64, k0, full);
+    } else {
+      ptx::tma_load_2d_pair(sa, map_a, k0, row, full);
+    }
+    if (B_MN) {
+      const int kr = OP == DX ? p.b_row0 + k0 : k0;
+      for (int i = 0; i < kCtaN / 64; ++i)
+        ptx::tma_load_2d_pair(sb + i * 8192, &maps.b, n0 + i * 64, kr, full);
+    } else {
+      ptx::tma_load_2d_pair(sb, &maps.b, k0, p.b_row0 + n0, full);
+    }
   }
-  __syncwarp();
-  if (warp == 1) ptx::tmem_alloc_pair(tmem_slot, 512);
-  ptx::tc_fence_before();
-  ptx::cluster_sync();
-  ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  train::grid_wait();
+}
 
-  if (warp == 0) {
-    // ===================================== TMA producer =====================================
-    if (lane == 0) {
-      long long kb = 0;
-      bool ok = p.withhold == 0;
-      for (int u = pair; ok && u < units; u += pairs) {
-        int mi, ni, split;
-        unit_of(p, u, mi, ni, split);
-        const int m0 = mi * kTM + rank * kCtaM, n0 = ni * kTN + rank * kCtaN;
-        const int k_end = min(ksteps, (split + 1) * p.ksteps_per_split);
-        for (int k = split * p.ksteps_per_split; k < k_end; ++k, ++kb) {
-          const int s = (int)(kb % kStages);
-          if (kb >= kStages &&
-              !(ok = ptx::mbar_wait(bars + B_EMPTY + s, (int)((kb / kStages) - 1) & 1, abort_flag, tmo)))
-            break;
-          // the first CTA expects both CTAs' bytes; the other's may arrive before that
-          const uint32_t full = ptx::peer_smem(bars + B_FULL + s, 0);
-          if (rank == 0) ptx::mbar_expect_tx(bars + B_FULL + s, 2 * kStageBytes);
-          uint8_t* sa = sm + s * kStageBytes;
-          uint8_t* sb = sa + kABytes;
-          int k0 = k * kTK, row = m0;
-          const CUtensorMap* map_a = &maps.a;
-          if (OP == DW && k >= ksteps1) {
-            map_a = &maps.a2;
-            k0 -= ksteps1 * kTK;
-          }
-          if (OP == DX && p.two && rank == 1) {
-            map_a = &maps.a2;
-            row = 0;
-          }
-          if (A_MN) {
-            for (int i = 0; i < kCtaM / 64; ++i)
-              ptx::tma_load_2d_pair(sa + i * 8192, map_a, row + i * 64, k0, full);
-          } else {
-            ptx::tma_load_2d_pair(sa, map_a, k0, row, full);
-          }
-          if (B_MN) {
-            const int kr = OP == DX ? p.b_row0 + k0 : k0;
-            for (int i = 0; i < kCtaN / 64; ++i)
-              ptx::tma_load_2d_pair(sb + i * 8192, &maps.b, n0 + i * 64, kr, full);
-          } else {
-            ptx::tma_load_2d_pair(sb, &maps.b, k0, p.b_row0 + n0, full);
-          }
-        }
-      }
+// MMA issuer, one unit (one thread of the pair's first CTA). it: accumulators filled so far.
+template <int OP>
+__device__ __forceinline__ void issue_unit(const Params& p, const Cta& c, int u, long long& kb, int& it,
+                                           bool& ok) {
+  constexpr bool A_MN = kAMn<OP>, B_MN = kBMn<OP>;
+  constexpr uint32_t ID = ptx::idesc_bf16(kTM, kTN, A_MN, B_MN);
+  // a K step of 16: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major block
+  constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
+  uint64_t* bars = c.bars;
+  volatile int* abort_flag = c.abort_flag;
+  const uint32_t s0 = ptx::smem_u32(c.sm), tmem = c.tmem;
+  const int ksteps = ksteps_all<OP>(p);
+  const long long tmo = c.tmo;
+  int mi, ni, split;
+  unit_of(p, u, mi, ni, split);
+  const int u_end = min(ksteps, (split + 1) * p.ksteps_per_split);
+  for (int k_begin = split * p.ksteps_per_split; k_begin < u_end; k_begin += seg_steps<OP>(), ++it) {
+    const int acc = it & 1;
+    const int k_end = OP == LSE ? min(u_end, k_begin + kSegSteps) : u_end;
+    if (it >= 2 && !(ok = ptx::mbar_wait(bars + B_ACC_EMPTY + acc, ((it >> 1) - 1) & 1, abort_flag, tmo)))
+      break;
+    ptx::tc_fence_after();
+    for (int k = k_begin; k < k_end; ++k, ++kb) {
+      const int s = (int)(kb % kStages);
+      if (!(ok = ptx::mbar_wait(bars + B_FULL + s, (int)(kb / kStages) & 1, abort_flag, tmo))) break;
+      ptx::tc_fence_after();
+      const uint32_t a_lo = ptx::sdesc_lo(s0 + s * kStageBytes, A_MN ? 8192 : 16);
+      const uint32_t b_lo = ptx::sdesc_lo(s0 + s * kStageBytes + kABytes, B_MN ? 8192 : 16);
+#pragma unroll
+      for (int ks = 0; ks < kTK / 16; ++ks)
+        ptx::mma_lo_pair(tmem + acc * kTN, a_lo + ks * A_STEP, b_lo + ks * B_STEP, ID,
+                         (k > k_begin || ks > 0) ? 1u : 0u);
+      ptx::mma_commit_pair(bars + B_EMPTY + s);
     }
-  } else if (warp == 1) {
-    // ====================================== MMA issuer ======================================
-    if (lane == 0 && rank == 0) {
-      constexpr uint32_t ID = ptx::idesc_bf16(kTM, kTN, A_MN, B_MN);
-      // a K step of 16: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major block
-      constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
-      const uint32_t s0 = ptx::smem_u32(sm);
-      long long kb = 0;
-      int it = 0;
-      bool ok = true;
-      for (int u = pair; ok && u < units; u += pairs) {
-        int mi, ni, split;
-        unit_of(p, u, mi, ni, split);
-        const int u_end = min(ksteps, (split + 1) * p.ksteps_per_split);
-        for (int k_begin = split * p.ksteps_per_split; k_begin < u_end; k_begin += seg_steps<OP>(), ++it) {
-          const int acc = it & 1;
-          const int k_end = OP == LSE ? min(u_end, k_begin + kSegSteps) : u_end;
-          if (it >= 2 && !(ok = ptx::mbar_wait(bars + B_ACC_EMPTY + acc, ((it >> 1) - 1) & 1, abort_flag, tmo)))
-            break;
-          ptx::tc_fence_after();
-          for (int k = k_begin; k < k_end; ++k, ++kb) {
-            const int s = (int)(kb % kStages);
-            if (!(ok = ptx::mbar_wait(bars + B_FULL + s, (int)(kb / kStages) & 1, abort_flag, tmo))) break;
-            ptx::tc_fence_after();
-            const uint32_t a_lo = ptx::sdesc_lo(s0 + s * kStageBytes, A_MN ? 8192 : 16);
-            const uint32_t b_lo = ptx::sdesc_lo(s0 + s * kStageBytes + kABytes, B_MN ? 8192 : 16);
-#pragma unroll
-            for (int ks = 0; ks < kTK / 16; ++ks)
-              ptx::mma_lo_pair(tmem + acc * kTN, a_lo + ks * A_STEP, b_lo + ks * B_STEP, ID,
-                               (k > k_begin || ks > 0) ? 1u : 0u);
-            ptx::mma_commit_pair(bars + B_EMPTY + s);
-          }
-          if (!ok) break;
-          ptx::mma_commit_pair(bars + B_ACC_FULL + acc);
-        }
-      }
-      ptx::mma_commit_pair(bars + B_DRAIN);
+    if (!ok) break;
+    ptx::mma_commit_pair(bars + B_ACC_FULL + acc);
+  }
+}
+
+// Epilogue, one unit: a warp's 32 rows and half of the columns.
+template <int OP>
+__device__ __forceinline__ void finish_unit(const Params& p, const Maps& maps, const Cta& c, int u, int& it,
+                                            bool& ok) {
+  uint8_t* sm = c.sm;
+  uint64_t* bars = c.bars;
+  volatile int* abort_flag = c.abort_flag;
+  const int rank = c.rank, warp = c.warp, lane = c.lane, ksteps = ksteps_all<OP>(p);
+  const uint32_t tmem = c.tmem;
+  const long long tmo = c.tmo;
+  const int quarter = warp & 3, half = (warp - 4) >> 2;
+  const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
+  int mi, ni, split;
+  unit_of(p, u, mi, ni, split);
+  const int row = mi * kTM + rank * kCtaM + quarter * 32 + lane;
+  const int col0 = ni * kTN + half * (kTN / 2);
+  const bool live = OP == DX && p.two ? (row & (kTwoTermRows - 1)) < p.rows : row < p.M;
+  // what the row needs besides the tile, fetched before the wait
+  long long tgt = -1;
+  float nlse2 = 0.f, gs = 0.f;
+  if (OP == LSE || OP == GRAD) {
+    if (live) tgt = train::load_index(p.targets, row, p.id_bits);
+    if (OP == GRAD && live) {
+      const bool used = tgt != p.ignore_index && tgt >= 0 && tgt < p.V;
+      gs = used ? p.scale * __ldg(p.dloss + row) : 0.f;
+      nlse2 = -__ldg(p.lse + row) * kLog2e;
+      if (!used) tgt = -1;
     }
-  } else if (warp >= 4) {
-    // ======================================= epilogue =======================================
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
-    int it = 0;
-    bool ok = true;
-    for (int u = pair; ok && u < units; u += pairs) {
-      int mi, ni, split;
-      unit_of(p, u, mi, ni, split);
-      const int row = mi * kTM + rank * kCtaM + quarter * 32 + lane;
-      const int col0 = ni * kTN + half * (kTN / 2);
-      const bool live = OP == DX && p.two ? (row & (kTwoTermRows - 1)) < p.rows : row < p.M;
-      // what the row needs besides the tile, fetched before the wait
-      long long tgt = -1;
-      float nlse2 = 0.f, gs = 0.f;
-      if (OP == LSE || OP == GRAD) {
-        if (live) tgt = train::load_index(p.targets, row, p.id_bits);
-        if (OP == GRAD && live) {
-          const bool used = tgt != p.ignore_index && tgt >= 0 && tgt < p.V;
-          gs = used ? p.scale * __ldg(p.dloss + row) : 0.f;
-          nlse2 = -__ldg(p.lse + row) * kLog2e;
-          if (!used) tgt = -1;
-        }
-        if (tgt == p.ignore_index) tgt = -1;
-        tgt -= p.b_row0;
-      }
-      if constexpr (OP == LSE) {
-        float z[kTN / 64][32];
-        for (int k = 0; k < ksteps; k += kSegSteps, ++it) {
-          const int acc = it & 1;
-          if (!(ok = ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo))) break;
-          ptx::tc_fence_after();
-          const uint32_t from = tmem + lane_addr + acc * kTN + half * (kTN / 2);
-#pragma unroll
-          for (int c = 0; c < kTN / 64; ++c) {
-            if (k == 0) {
-              ptx::tmem_ld32(from + c * 32, z[c]);
-            } else {
-#pragma unroll
-              for (int h = 0; h < 32; h += 16) {
-                float t[16];
-                ptx::tmem_ld16(from + c * 32 + h, t);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) z[c][h + i] += t[i];
-              }
-            }
-          }
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_peer(ptx::peer_smem(bars + B_ACC_EMPTY + acc, 0));
-        }
-        if (!ok) break;
-        float m2 = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int c0 = 0; c0 < kTN / 2; c0 += 32) {
-          float (&v)[32] = z[c0 / 32];
-          const int col = col0 + c0;                       // first column of the 32
-          const int n = p.N - col;                         // valid ones
-          if (n > 0) {
-            const long long tc = tgt - col;
-            float cm = -INFINITY;
-            float zt = 0.f;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (c == tc) zt = v[c];
-              v[c] = c < n ? v[c] * p.scale_log2 : -INFINITY;
-              cm = fmaxf(cm, v[c]);
-            }
-            if (tc >= 0 && tc < 32 && tc < n) p.ztgt[row] = zt * p.scale;
-            const float nm = fmaxf(m2, cm);
-            const float base = nm == -INFINITY ? 0.f : nm;
-            float s = 0.f;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) s += ptx::ex2(v[c] - base);
-            sum = sum * ptx::ex2(m2 - base) + s;
-            m2 = nm;
-          }
-        }
-        if (live) p.part[(size_t)(ni * 2 + half) * p.M + row] = make_float2(m2, sum);
-        continue;
-      }
+    if (tgt == p.ignore_index) tgt = -1;
+    tgt -= p.b_row0;
+  }
+  if constexpr (OP == LSE) {
+    float z[kTN / 64][32];
+    for (int k = 0; k < ksteps; k += kSegSteps, ++it) {
       const int acc = it & 1;
       if (!(ok = ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo))) break;
       ptx::tc_fence_after();
       const uint32_t from = tmem + lane_addr + acc * kTN + half * (kTN / 2);
-      const bool by_tile = OP == DW && (p.out_mode == OUT_BF16 || p.out_mode == OUT_F32);
-      if (OP == DW && by_tile) {
-        uint8_t* buf = sm + kStoreOff + (warp - 4) * kStoreBytes;
-        const int row0 = row - lane;
-        if (p.out_mode == OUT_F32) store_tile<true>(&maps.c, buf, from, col0, row0, p.M, p.N, lane);
-        else store_tile<false>(&maps.c, buf, from, col0, row0, p.M, p.N, lane);
-      }
-#pragma unroll 1
-      for (int c0 = 0; c0 < (by_tile ? 0 : kTN / 2); c0 += 32) {
-        float v[32];
-        ptx::tmem_ld32(from + c0, v);
-        const int col = col0 + c0;                       // first column of the 32
-        const int n = p.N - col;                         // valid ones
-        if (OP == GRAD) {
-          const long long tc = tgt - col;
-          uint32_t w[16], w2[16];
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float a = ptx::ex2(fmaf(v[c], p.scale_log2, nlse2));
-            float b = ptx::ex2(fmaf(v[c + 1], p.scale_log2, nlse2));
-            if (c == tc) a -= 1.f;
-            if (c + 1 == tc) b -= 1.f;
-            a = gs == 0.f ? 0.f : a * gs;
-            b = gs == 0.f ? 0.f : b * gs;
-            w[c >> 1] = ptx::pack_bf16(a, b);
-            if (p.two)
-              w2[c >> 1] = ptx::pack_bf16(a - __uint_as_float(w[c >> 1] << 16),
-                                          b - __uint_as_float(w[c >> 1] & 0xffff0000u));
-          }
-          if (live && n > 0) {
-            __nv_bfloat16* dst = p.g + (size_t)row * p.ldg + col;     // ldg: a multiple of 256
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t h[8] = {w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
-                                     w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
-              store32(dst + 16 * i, h, true);
-              if (p.two) {
-                const uint32_t l[8] = {w2[8 * i], w2[8 * i + 1], w2[8 * i + 2], w2[8 * i + 3],
-                                       w2[8 * i + 4], w2[8 * i + 5], w2[8 * i + 6], w2[8 * i + 7]};
-                store32(dst + kTwoTermRows * p.ldg + 16 * i, l, true);
-              }
-            }
-          }
+      for (int c = 0; c < kTN / 64; ++c) {
+        if (k == 0) {
+          ptx::tmem_ld32(from + c * 32, z[c]);
         } else {
-          if (live && n > 0) {
-            const size_t at = (size_t)row * p.N + col;
-            __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
-            float* of = (OP == DX ? p.acc + (p.out_mode == OUT_PART ? (size_t)split * p.M * p.N : 0)
-                                  : reinterpret_cast<float*>(p.out)) + at;
-            const bool wide16 = ((uintptr_t)ob & 31) == 0, wide32 = ((uintptr_t)of & 31) == 0;
-            if (p.out_mode == OUT_BF16) put_bf16<false>(ob, nullptr, v, n, wide16);
-            else if (p.out_mode == OUT_BF16_ADD) put_bf16<true>(ob, OP == DX ? of : nullptr, v, n, wide16);
-            else if (p.out_mode == OUT_F32_ADD) put_f32<true>(of, v, n, wide32);
-            else put_f32<false>(of, v, n, wide32);
+#pragma unroll
+          for (int h = 0; h < 32; h += 16) {
+            float t[16];
+            ptx::tmem_ld16(from + c * 32 + h, t);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[c][h + i] += t[i];
           }
         }
       }
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_peer(ptx::peer_smem(bars + B_ACC_EMPTY + acc, 0));
-      ++it;
     }
-    if (OP == DW && lane == 0) ptx::bulk_wait_all();       // the stores have been performed
+    if (!ok) return;
+    float m2 = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int c0 = 0; c0 < kTN / 2; c0 += 32) {
+      float (&v)[32] = z[c0 / 32];
+      const int col = col0 + c0;                       // first column of the 32
+      const int n = p.N - col;                         // valid ones
+      if (n > 0) {
+        const long long tc = tgt - col;
+        float cm = -INFINITY;
+        float zt = 0.f;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          if (c == tc) zt = v[c];
+          v[c] = c < n ? v[c] * p.scale_log2 : -INFINITY;
+          cm = fmaxf(cm, v[c]);
+        }
+        if (tc >= 0 && tc < 32 && tc < n) p.ztgt[row] = zt * p.scale;
+        const float nm = fmaxf(m2, cm);
+        const float base = nm == -INFINITY ? 0.f : nm;
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s += ptx::ex2(v[c] - base);
+        sum = sum * ptx::ex2(m2 - base) + s;
+        m2 = nm;
+      }
+    }
+    if (live) p.part[(size_t)(ni * 2 + half) * p.M + row] = make_float2(m2, sum);
+    return;
+  }
+  const int acc = it & 1;
+  if (!(ok = ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo))) return;
+  ptx::tc_fence_after();
+  const uint32_t from = tmem + lane_addr + acc * kTN + half * (kTN / 2);
+  const bool by_tile = OP == DW && (p.out_mode == OUT_BF16 || p.out_mode == OUT_F32);
+  if (OP == DW && by_tile) {
+    uint8_t* buf = sm + kStoreOff + (warp - 4) * kStoreBytes;
+    const int row0 = row - lane;
+    if (p.out_mode == OUT_F32) store_tile<true>(&maps.c, buf, from, col0, row0, p.M, p.N, lane);
+    else store_tile<false>(&maps.c, buf, from, col0, row0, p.M, p.N, lane);
+  }
+#pragma unroll 1
+  for (int c0 = 0; c0 < (by_tile ? 0 : kTN / 2); c0 += 32) {
+    float v[32];
+    ptx::tmem_ld32(from + c0, v);
+    const int col = col0 + c0;                       // first column of the 32
+    const int n = p.N - col;                         // valid ones
+    if (OP == GRAD) {
+      const long long tc = tgt - col;
+      uint32_t w[16], w2[16];
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        float a = ptx::ex2(fmaf(v[c], p.scale_log2, nlse2));
+        float b = ptx::ex2(fmaf(v[c + 1], p.scale_log2, nlse2));
+        if (c == tc) a -= 1.f;
+        if (c + 1 == tc) b -= 1.f;
+        a = gs == 0.f ? 0.f : a * gs;
+        b = gs == 0.f ? 0.f : b * gs;
+        w[c >> 1] = ptx::pack_bf16(a, b);
+        if (p.two)
+          w2[c >> 1] = ptx::pack_bf16(a - __uint_as_float(w[c >> 1] << 16),
+                                      b - __uint_as_float(w[c >> 1] & 0xffff0000u));
+      }
+      if (live && n > 0) {
+        __nv_bfloat16* dst = p.g + (size_t)row * p.ldg + col;     // ldg: a multiple of 256
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t h[8] = {w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
+                                 w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
+          store32(dst + 16 * i, h, true);
+          if (p.two) {
+            const uint32_t l[8] = {w2[8 * i], w2[8 * i + 1], w2[8 * i + 2], w2[8 * i + 3],
+                                   w2[8 * i + 4], w2[8 * i + 5], w2[8 * i + 6], w2[8 * i + 7]};
+            store32(dst + kTwoTermRows * p.ldg + 16 * i, l, true);
+          }
+        }
+      }
+    } else {
+      if (live && n > 0) {
+        const size_t at = (size_t)row * p.N + col;
+        __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+        float* of = (OP == DX ? p.acc + (p.out_mode == OUT_PART ? (size_t)split * p.M * p.N : 0)
+                              : reinterpret_cast<float*>(p.out)) + at;
+        const bool wide16 = ((uintptr_t)ob & 31) == 0, wide32 = ((uintptr_t)of & 31) == 0;
+        if (p.out_mode == OUT_BF16) put_bf16<false>(ob, nullptr, v, n, wide16);
+        else if (p.out_mode == OUT_BF16_ADD) put_bf16<true>(ob, OP == DX ? of : nullptr, v, n, wide16);
+        else if (p.out_mode == OUT_F32_ADD) put_f32<true>(of, v, n, wide32);
+        else put_f32<false>(of, v, n, wide32);
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive_peer(ptx::peer_smem(bars + B_ACC_EMPTY + acc, 0));
+  ++it;
+}
+
+// The second product of a launch: DW's in BOTH, else nothing.
+template <int OP>
+struct Second {};
+template <>
+struct Second<BOTH> {
+  Params p;
+  Maps maps;
+};
+
+template <int OP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
+    gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps,
+                const __grid_constant__ Second<OP> second) {
+  constexpr int OP1 = OP == BOTH ? DX : OP;
+  extern __shared__ uint8_t smem_xent[];
+  train::grid_next();
+  Cta c;
+  c.sm = (uint8_t*)(((uintptr_t)smem_xent + 1023) & ~(uintptr_t)1023);
+  c.bars = (uint64_t*)(c.sm + kBarOff);
+  uint32_t* tmem_slot = (uint32_t*)(c.sm + kBarOff + 8 * B_COUNT);
+  c.abort_flag = (volatile int*)(c.sm + kBarOff + 8 * B_COUNT + 4);
+  c.warp = threadIdx.x >> 5;
+  c.lane = threadIdx.x & 31;
+  c.rank = (int)ptx::cluster_rank();
+  c.tmo = p.timeout_ns;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int units1 = units_of(p);
+  int units = units1;
+  if constexpr (OP == BOTH) units += units_of(second.p);
+
+  if (threadIdx.x == 0) {
+    ptx::prefetch_map(&maps.a);
+    ptx::prefetch_map(&maps.b);
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(c.bars + B_FULL + s, 1);
+      ptx::mbar_init(c.bars + B_EMPTY + s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(c.bars + B_ACC_FULL + a, 1);
+      ptx::mbar_init(c.bars + B_ACC_EMPTY + a, 16);        // 8 epilogue warps of each CTA
+    }
+    ptx::mbar_init(c.bars + B_DRAIN, 1);
+    *c.abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  __syncwarp();
+  if (c.warp == 1) ptx::tmem_alloc_pair(tmem_slot, 512);
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  c.tmem = *tmem_slot;
+  train::grid_wait();
+
+  long long kb = 0;
+  int it = 0;
+  bool ok = true;
+  if (c.warp == 0) {
+    if (c.lane == 0) {
+      ok = p.withhold == 0;
+      for (int u = pair; ok && u < units; u += pairs) {
+        if constexpr (OP == BOTH) {
+          if (u >= units1) {
+            load_unit<DW>(second.p, second.maps, c, u - units1, kb, ok);
+            continue;
+          }
+        }
+        load_unit<OP1>(p, maps, c, u, kb, ok);
+      }
+    }
+  } else if (c.warp == 1) {
+    if (c.lane == 0 && c.rank == 0) {
+      for (int u = pair; ok && u < units; u += pairs) {
+        if constexpr (OP == BOTH) {
+          if (u >= units1) {
+            issue_unit<DW>(second.p, c, u - units1, kb, it, ok);
+            continue;
+          }
+        }
+        issue_unit<OP1>(p, c, u, kb, it, ok);
+      }
+      ptx::mma_commit_pair(c.bars + B_DRAIN);
+    }
+  } else if (c.warp >= 4) {
+    for (int u = pair; ok && u < units; u += pairs) {
+      if constexpr (OP == BOTH) {
+        if (u >= units1) {
+          finish_unit<DW>(second.p, second.maps, c, u - units1, it, ok);
+          continue;
+        }
+      }
+      finish_unit<OP1>(p, maps, c, u, it, ok);
+    }
+    if ((OP == DW || OP == BOTH) && c.lane == 0) ptx::bulk_wait_all();   // the stores have been performed
   }
 
   // Every MMA and with it every copy of the pair has ended once DRAIN completes; neither CTA
   // leaves before the other, whose barriers and copies it may signal.
-  if (threadIdx.x == 0) ptx::mbar_drain(bars + B_DRAIN, 0, 1000000000ll);
+  if (threadIdx.x == 0) ptx::mbar_drain(c.bars + B_DRAIN, 0, 1000000000ll);
   __syncwarp();
   ptx::tc_fence_before();
   ptx::cluster_sync();
-  if (warp == 1) {
+  if (c.warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc_pair(tmem, 512);
+    ptx::tmem_dealloc_pair(c.tmem, 512);
   }
-  if (threadIdx.x == 0 && *abort_flag && atomicCAS(p.header + WS_STATUS, 0, kStatusSyncTimeout) == 0) {
+  if (threadIdx.x == 0 && *c.abort_flag && atomicCAS(p.header + WS_STATUS, 0, kStatusSyncTimeout) == 0) {
     p.header[WS_BH] = -1;
     p.header[WS_QTILE] = blockIdx.x;
   }

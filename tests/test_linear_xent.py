@@ -102,6 +102,15 @@ def test_several_pieces_with_split_ranges():
     _check(x, w, y, dl, loss, lse, dx, dw)
 
 
+@pytest.mark.parametrize("T,V,D", [(64, 40000, 1024), (1300, 20000, 2048)])
+def test_products_of_many_tiles(T, V, D):
+    """dX and dW in launches of their own (few tiles share one), dX split over K and not."""
+    x, w, y, dl = _inputs(T, V, D, seed=T)
+    loss, lse = da.linear_xent_forward(x, w, y)
+    dx, dw = da.linear_xent_backward(x, w, y, lse, dl)
+    _check(x, w, y, dl, loss, lse, dx, dw)
+
+
 def test_row_strides():
     T, V, D = 130, 300, 64
     x, w, y, dl = _inputs(T, V, D, seed=8)

@@ -185,9 +185,10 @@ dash_status_t dash_linear_xent_fwd(const void* x, const void* w, const void* tar
  *   G[t][v] = scale * dloss[t] * (exp(z[t][v] - lse[t]) - [v = y_t])  (0 for ignored rows),
  *   dX = G W,   dW = G^T X.
  * The logits are recomputed piece by piece of the vocabulary; a piece of G is held in the
- * workspace in bf16, as the tensor cores need it (a rounding of at most 2^-8 of each entry;
- * up to 128 tokens, where it would show, as two terms: 2^-16), the products are summed in
- * fp32.
+ * workspace in bf16, as the tensor cores need it, the products are summed in fp32. G is rounded
+ * no more than the result that it goes into: by at most 2^-8 of each entry for dx and a bf16 dw;
+ * by 2^-16 (two terms) for an fp32 dw, whose product takes twice as long for it, and for both
+ * results up to 128 tokens.
  *   lse     : fp32 [T] from dash_linear_xent_fwd (read)
  *   dloss   : fp32 [T] (read)
  *   dx      : bf16 [T, D] contiguous (written)

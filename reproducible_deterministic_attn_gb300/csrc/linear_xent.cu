@@ -23,8 +23,9 @@ struct Plan {
   long long piece;            // vocabulary rows a piece, a multiple of 256
   int pieces;
   long long ldg;
-  bool two;                   // G as two bf16 terms (up to kTwoTermRows tokens)
-  long long g_rows;           // rows of G, and of one K range's dX
+  bool two;                   // up to kTwoTermRows tokens: G's two terms share DX's tiles
+  long long g2_rows;          // rows from G's first terms to its second ones (0: there are none)
+  long long dx_rows;          // rows of one K range's dX
   int dx_splits, dx_ksteps;   // K ranges of dX within a full piece
   bool joined;                // dX goes through partials and a join
   size_t part, ztgt;          // forward
@@ -49,12 +50,14 @@ void dx_ranges(long long T, int D, long long piece, int* splits, int* per) {
   *splits = (int)ceil_div<long long>(steps, *per);
 }
 
-Plan make_plan(long long T, long long V, int D) {
+Plan make_plan(long long T, long long V, int D, bool dw_f32) {
   Plan pl;
   const long long rows = std::max<long long>(T, 1);
   pl.two = T <= kTwoTermRows;
-  pl.g_rows = pl.two ? 2 * kTwoTermRows : rows;
-  pl.piece = std::max<long long>(1, (long long)(kPieceBytes / 2 / kTN) / pl.g_rows) * kTN;
+  pl.g2_rows = pl.two ? kTwoTermRows : dw_f32 ? rows : 0;
+  pl.dx_rows = pl.two ? 2 * kTwoTermRows : rows;
+  const long long g_rows = (pl.two ? kTwoTermRows : rows) + pl.g2_rows;
+  pl.piece = std::max<long long>(1, (long long)(kPieceBytes / 2 / kTN) / g_rows) * kTN;
   pl.piece = std::min(pl.piece, ceil_div<long long>(V, kTN) * kTN);
   pl.pieces = (int)ceil_div<long long>(V, pl.piece);
   pl.ldg = pl.piece;
@@ -69,12 +72,17 @@ Plan make_plan(long long T, long long V, int D) {
   pl.part = take((size_t)2 * ceil_div<long long>(V, kTN) * rows * sizeof(float2));
   const size_t fwd = at;
   at = dash::kWsHeaderBytes;
-  pl.g = take((size_t)pl.g_rows * pl.ldg * 2);
+  pl.g = take((size_t)g_rows * pl.ldg * 2);
   pl.acc = take(pl.pieces > 1 ? (size_t)rows * D * 4 : 0);
   pl.joined = pl.dx_splits > 1 || pl.two;
-  pl.dx_part = take(pl.joined ? (size_t)pl.dx_splits * pl.g_rows * D * 4 : 0);
+  pl.dx_part = take(pl.joined ? (size_t)pl.dx_splits * pl.dx_rows * D * 4 : 0);
   pl.total = std::max(fwd, at);
   return pl;
+}
+
+// What both directions need, whatever dW's type.
+size_t workspace_size(long long T, long long V, int D) {
+  return std::max(make_plan(T, V, D, false).total, make_plan(T, V, D, true).total);
 }
 
 // Row-major bf16 (or fp32) [rows][cols], `ld` elements between rows; box = 128 bytes of columns x
@@ -105,7 +113,7 @@ dash_status_t check_args(const void* x, const void* w, const void* targets, cons
       !is_aligned(a, 4) || !is_aligned(b, 4))
     return DASH_ERR_INVALID_ARG;
   if (!is_aligned(workspace, 256)) return DASH_ERR_INVALID_ARG;
-  if (workspace_bytes < make_plan(T, V, D).total) return DASH_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < workspace_size(T, V, D)) return DASH_ERR_WORKSPACE_TOO_SMALL;
   if (!dash::tensor_map_encoder()) {
     dash::set_last_error("cuTensorMapEncodeTiled is not available from the driver");
     return DASH_ERR_CUDA;
@@ -156,7 +164,7 @@ dash_status_t sm_count(int* sms) {
 extern "C" {
 
 size_t dash_linear_xent_workspace_size(long long T, long long V, int D) {
-  return sizes_ok(T, V, D) ? make_plan(T, V, D).total : 0;
+  return sizes_ok(T, V, D) ? workspace_size(T, V, D) : 0;
 }
 
 dash_status_t dash_linear_xent_fwd(const void* x, const void* w, const void* targets, float* loss,
@@ -174,7 +182,7 @@ dash_status_t dash_linear_xent_fwd(const void* x, const void* w, const void* tar
     DASH_TRY(cudaMemsetAsync(ws, 0, dash::kWsHeaderBytes, stream));
     return DASH_OK;
   }
-  const Plan pl = make_plan(T, V, D);
+  const Plan pl = make_plan(T, V, D, false);
   Maps maps = {};
   if (!map_2d(&maps.a, x, T, D, ldx, kCtaM) || !map_2d(&maps.b, w, V, D, ldw, kCtaN)) return bad_map();
   Params p = {};
@@ -226,7 +234,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     if (!accumulate) DASH_TRY(cudaMemsetAsync(dw, 0, (size_t)V * D * dw_elt, stream));
     return DASH_OK;
   }
-  const Plan pl = make_plan(T, V, D);
+  const Plan pl = make_plan(T, V, D, dw_dtype == DASH_FP32);
   __nv_bfloat16* g = (__nv_bfloat16*)(ws + pl.g);
   Params base = {};
   base.id_bits = id_bits;
@@ -237,6 +245,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   base.lse = lse;
   base.dloss = dloss;
   base.g = g;
+  base.g2 = pl.g2_rows > 0 ? g + pl.g2_rows * pl.ldg : nullptr;
   base.ldg = pl.ldg;
   base.V = V;
   base.header = (int*)ws;
@@ -258,10 +267,8 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     if (!map_2d(&dxm.a, g, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a, g, T, vp, pl.ldg, kTK)) return bad_map();
     dxm.a2 = dxm.a;
     dwm.a2 = dwm.a;
-    if (pl.two) {
-      const __nv_bfloat16* g2 = g + kTwoTermRows * pl.ldg;
-      if (!map_2d(&dxm.a2, g2, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a2, g2, T, vp, pl.ldg, kTK)) return bad_map();
-    }
+    if (base.g2 && (!map_2d(&dxm.a2, base.g2, T, vp, pl.ldg, kCtaM) || !map_2d(&dwm.a2, base.g2, T, vp, pl.ldg, kTK)))
+      return bad_map();
     dwm.c = dwm.a;                       // read only where dW is not accumulated
     if (!accumulate &&
         !map_2d(&dwm.c, (char*)dw + (size_t)v0 * D * dw_elt, vp, D, D, 32, dw_dtype == DASH_FP32))
@@ -284,7 +291,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     p.acc = (float*)(ws + pl.acc);
     p.out_mode = first ? (last ? OUT_BF16 : OUT_F32) : (last ? OUT_BF16_ADD : OUT_F32_ADD);
     if (pl.joined) {
-      p.M = (int)pl.g_rows;
+      p.M = (int)pl.dx_rows;
       p.ksteps_per_split = pl.dx_ksteps;
       p.splits = ceil_div(ceil_div((int)vp, kTK), pl.dx_ksteps);
       p.out_mode = OUT_PART;
@@ -299,7 +306,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     d.N = D;
     d.K = (int)T;
     d.splits = 1;
-    d.ksteps_per_split = (pl.two ? 2 : 1) * ceil_div((int)T, kTK);
+    d.ksteps_per_split = (base.g2 ? 2 : 1) * ceil_div((int)T, kTK);
     d.out = (char*)dw + (size_t)v0 * D * dw_elt;
     d.out_mode = dw_dtype == DASH_FP32 ? (accumulate ? OUT_F32_ADD : OUT_F32)
                                        : (accumulate ? OUT_BF16_ADD : OUT_BF16);
@@ -310,7 +317,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
       const size_t n = (size_t)T * D;
       DASH_TRY(dash::launch_after(dx_join_kernel, dim3((unsigned)ceil_div<size_t>(n, 4 * kJoinThreads)),
                                   kJoinThreads, 0, stream, p.acc,
-                                  p.splits, n, (size_t)pl.g_rows * D,
+                                  p.splits, n, (size_t)pl.dx_rows * D,
                                   pl.two ? (size_t)kTwoTermRows * D : (size_t)0, (float*)(ws + pl.acc), (int)first,
                                   (int)last, (__nv_bfloat16*)dx));
     }

@@ -5,10 +5,11 @@
 //   GRAD  Z = X W^T again  the tile becomes G = g (exp(z - lse) - [v = y]) in bf16
 //   DX    dX = G W         K = the vocabulary (of one piece), W read N-major
 //   DW    dW = G^T X       K = the tokens, both operands MN-major
-// Up to 128 tokens half of a tile's rows would be empty. There G is held as two bf16 terms, the
-// second one what the first one's rounding left: DX puts the second terms into the other half
-// (its join adds them), DW takes them as 128 more tokens. So G's rounding costs no precision
-// where few tokens do not average it out, and no time.
+// G is rounded no more than the results: it is one bf16 term where they are bf16. Up to 128 tokens
+// half of a tile's rows would be empty: there G is held as two terms, the second one what the
+// first one's rounding left; DX puts the second terms into the other half (its join adds them),
+// DW takes them as 128 more tokens, and neither takes longer. An fp32 dW of more tokens gets the
+// two terms too, as twice as many tokens (DX, which is bf16, the first alone).
 // DX and DW of a piece share a launch (BOTH) where they are few tiles (kTogetherRounds): neither
 // reads what the other writes, and their tiles fill the chip's last round together.
 // A unit of work is one output tile of 256 x 256 (for DX one K range of it), dealt round robin
@@ -65,7 +66,8 @@ struct Params {
   // GRAD
   const float* lse;
   const float* dloss;
-  __nv_bfloat16* g;          // [M][ldg]; two terms: [2 * 128][ldg]
+  __nv_bfloat16* g;          // [M][ldg]
+  __nv_bfloat16* g2;         // G's second terms, laid out as g, or null
   long long ldg;
   long long V;
   // DX, DW
@@ -74,7 +76,7 @@ struct Params {
   float* acc;                // DX: fp32 [M][N] over the pieces, or the K ranges' partials
   int* header;
   long long timeout_ns;
-  int two;                   // G is held as two terms
+  int two;                   // DX: the second terms lie in the tile's other half
   int rows;                  // tokens
   int withhold;              // testing hook: load no tiles, so the waits for them run out
 };
@@ -247,7 +249,7 @@ constexpr bool kBMn = OP == DX || OP == DW;
 __device__ __forceinline__ int ksteps_one(const Params& p) { return (p.K + kTK - 1) / kTK; }
 template <int OP>
 __device__ __forceinline__ int ksteps_all(const Params& p) {
-  return OP == DW && p.two ? 2 * ksteps_one(p) : ksteps_one(p);
+  return OP == DW && p.g2 ? 2 * ksteps_one(p) : ksteps_one(p);
 }
 __device__ __forceinline__ int units_of(const Params& p) { return p.tiles_m * p.tiles_n * p.splits; }
 
@@ -275,12 +277,10 @@ __device__ __forceinline__ void load_unit(const Params& p, const Maps& maps, con
     if (rank == 0) ptx::mbar_expect_tx(bars + B_FULL + s, 2 * kStageBytes);
     uint8_t* sa = sm + s * kStageBytes;
     uint8_t* sb = sa + kABytes;
-    int k0 = k * kTK, row = m0;
-    const CUtensorMap* map_a = &maps.a;
-    if (OP == DW && k >= ksteps1) {
-      map_a = &maps.a2;
-      k0 -= ksteps1 * kTK;
-    }
+    int row = m0;
+    const bool second = OP == DW && k >= ksteps1;
+    const int k0 = (second ? k - ksteps1 : k) * kTK;
+    const CUtensorMap* map_a = second ? &maps.a2 : &maps.a;
     if (OP == DX && p.two && rank == 1) {
       map_a = &maps.a2;
       row = 0;
@@ -455,7 +455,7 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Maps& maps, c
         a = gs == 0.f ? 0.f : a * gs;
         b = gs == 0.f ? 0.f : b * gs;
         w[c >> 1] = ptx::pack_bf16(a, b);
-        if (p.two)
+        if (p.g2)
           w2[c >> 1] = ptx::pack_bf16(a - __uint_as_float(w[c >> 1] << 16),
                                       b - __uint_as_float(w[c >> 1] & 0xffff0000u));
       }
@@ -466,10 +466,10 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Maps& maps, c
           const uint32_t h[8] = {w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
                                  w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
           store32(dst + 16 * i, h, true);
-          if (p.two) {
+          if (p.g2) {
             const uint32_t l[8] = {w2[8 * i], w2[8 * i + 1], w2[8 * i + 2], w2[8 * i + 3],
                                    w2[8 * i + 4], w2[8 * i + 5], w2[8 * i + 6], w2[8 * i + 7]};
-            store32(dst + kTwoTermRows * p.ldg + 16 * i, l, true);
+            store32(p.g2 + (size_t)row * p.ldg + col + 16 * i, l, true);
           }
         }
       }

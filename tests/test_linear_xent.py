@@ -259,3 +259,26 @@ def test_waits_that_run_out_are_reported_and_the_context_survives():
     loss, lse = da.linear_xent_forward(x, w, y, workspace=ws)
     got = (loss, lse) + da.linear_xent_backward(x, w, y, lse, dl, workspace=ws)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("T,V,D", [(300, 900, 136), (700, 5003, 64), (2500, 700, 320)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_an_fp32_gradient_is_not_held_to_16_bits(T, V, D, accumulate):
+    """dw in fp32 of more than 128 tokens: G enters it as two terms (u^2 |G|), so what is left
+    beside the logits' error is the fp32 sums. They lie below half a step of bf16 where the
+    targets dominate."""
+    x, w, y, dl = _inputs(T, V, D, seed=T + 1)
+    _, lse = da.linear_xent_forward(x, w, y)
+    base = torch.randn(V, D, device="cuda").mul_(1e-3) if accumulate else None
+    dw = base.clone() if accumulate else torch.full((V, D), float("nan"), device="cuda")
+    da.linear_xent_backward(x, w, y, lse, dl, dw=dw, accumulate=accumulate)
+    _, lse64 = ref.xent(x, w, y, IGN)
+    _, dw64, G, gp = ref.xent_grad(x, w, y, dl, IGN)
+    if accumulate:
+        dw64 = dw64 + base.double()
+    xd = x.double().abs()
+    ez = (D * 2.0 ** -23 + 2.0 ** -22) * (xd @ w.double().abs().t()).amax(1)
+    tol = 2 * ez + 2.0 ** -21 + 2.0 ** -14 + 2.0 ** -23 * lse64.abs()
+    eG = U * U * G.abs() + gp * (tol[:, None] + ez[:, None] + 2.0 ** -20)
+    bw = eG.t() @ xd + T * 2.0 ** -23 * (G.abs().t() @ xd) + 2.0 ** -24 * dw64.abs() * 1.01 + 1e-30
+    assert bool(((dw.double() - dw64).abs() <= bw).all()), float(((dw.double() - dw64).abs() / bw).max())

@@ -128,7 +128,7 @@ long long set_tiles(Params* p) {
   return (long long)p->tiles_m * p->tiles_n * p->splits;
 }
 
-template <int OP>
+template <int OP, bool SEGMENTS = false>
 dash_status_t launch(Params p, const Maps& maps, Second<OP> second, int sms, bool first, cudaStream_t stream) {
   long long units = set_tiles(&p);
   if constexpr (OP == BOTH) units += set_tiles(&second.p);
@@ -136,13 +136,13 @@ dash_status_t launch(Params p, const Maps& maps, Second<OP> second, int sms, boo
     dash::set_last_error("too many output tiles for one call");
     return DASH_ERR_UNSUPPORTED;
   }
-  DASH_TRY(dash::allow_shared((const void*)gemm_kernel<OP>, kSmem<OP>));
+  DASH_TRY(dash::allow_shared((const void*)gemm_kernel<OP, SEGMENTS>, kSmem<OP>));
   const int grid = 2 * (int)std::min<long long>(units, sms / 2);
   if (first) {
-    gemm_kernel<OP><<<grid, kXentThreads, kSmem<OP>, stream>>>(p, maps, second);
+    gemm_kernel<OP, SEGMENTS><<<grid, kXentThreads, kSmem<OP>, stream>>>(p, maps, second);
     DASH_TRY(cudaGetLastError());
   } else {
-    DASH_TRY(dash::launch_after(gemm_kernel<OP>, dim3(grid), kXentThreads, kSmem<OP>, stream, p, maps, second));
+    DASH_TRY(dash::launch_after(gemm_kernel<OP, SEGMENTS>, dim3(grid), kXentThreads, kSmem<OP>, stream, p, maps, second));
   }
   return DASH_OK;
 }
@@ -252,6 +252,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
   base.timeout_ns = dash::sync_timeout_ns();
   base.withhold = dash::sync_withheld();
   base.splits = 1;
+  base.seg_steps = kSegSteps16;
   base.two = pl.two;
   base.rows = (int)T;
   Maps grad = {}, dxm = {}, dwm = {};
@@ -306,12 +307,16 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
     d.N = D;
     d.K = (int)T;
     d.splits = 1;
+    if (dw_dtype == DASH_FP32) d.seg_steps = kSegSteps32;
     d.ksteps_per_split = (base.g2 ? 2 : 1) * ceil_div((int)T, kTK);
     d.out = (char*)dw + (size_t)v0 * D * dw_elt;
     d.out_mode = dw_dtype == DASH_FP32 ? (accumulate ? OUT_F32_ADD : OUT_F32)
                                        : (accumulate ? OUT_BF16_ADD : OUT_BF16);
-    const bool together = set_tiles(&p) + set_tiles(&d) <= kTogetherRounds * (sms / 2);
-    st = together ? launch<BOTH>(p, dxm, dwp, sms, false, stream) : launch<DX>(p, dxm, {}, sms, false, stream);
+    const bool dx_long = p.ksteps_per_split > p.seg_steps, dw_long = d.ksteps_per_split > d.seg_steps;
+    const bool together = !dx_long && !dw_long && set_tiles(&p) + set_tiles(&d) <= kTogetherRounds * (sms / 2);
+    st = together  ? launch<BOTH>(p, dxm, dwp, sms, false, stream)
+         : dx_long ? launch<DX, true>(p, dxm, {}, sms, false, stream)
+                   : launch<DX>(p, dxm, {}, sms, false, stream);
     if (st != DASH_OK) return st;
     if (pl.joined) {
       const size_t n = (size_t)T * D;
@@ -322,7 +327,7 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
                                   (int)last, (__nv_bfloat16*)dx));
     }
     if (!together) {
-      st = launch<DW>(d, dwm, {}, sms, false, stream);
+      st = dw_long ? launch<DW, true>(d, dwm, {}, sms, false, stream) : launch<DW>(d, dwm, {}, sms, false, stream);
       if (st != DASH_OK) return st;
     }
   }

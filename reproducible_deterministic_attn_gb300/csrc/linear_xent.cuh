@@ -76,6 +76,7 @@ struct Params {
   float* acc;                // DX: fp32 [M][N] over the pieces, or the K ranges' partials
   int* header;
   long long timeout_ns;
+  int seg_steps;             // DX, DW: K steps of a segment
   int two;                   // DX: the second terms lie in the tile's other half
   int rows;                  // tokens
   int withhold;              // testing hook: load no tiles, so the waits for them run out
@@ -114,10 +115,18 @@ static_assert(kSmem<BOTH> <= 232448, "shared memory budget");
 // 4096 of K made lse 1.7e-5 too small (2.2e-6 of it; fp32 multiply-adds to nearest: 3.9e-7); a
 // segment's sum is added in registers, to nearest, while the next one is computed. Segments of
 // 512, 1024, 2048: errors of 2.6e-7, 5.4e-7, 1.1e-6, and 1.9, 0.7, 0.2 % more time for the step
-// above. The gradient needs none: G is rounded to 2^-8.
+// above. GRAD needs none: its logits go into G, which is rounded more. DX and DW sum long axes,
+// where truncation is a bias that grows with K: terms of one sign lose some 2^-25.5 of their sum
+// with each 16 of K (dW of 262144 such tokens was 3e-4 too small). bf16 results get segments of
+// 16384 ids or tokens, which leave 2^-15.5, an fp32 dW segments of 4096 tokens, 2^-17.5 and less
+// than G's rounding. Kernels for K of one segment are compiled without (SEGMENTS), which spares
+// the backward of 8192 tokens 3 %.
 constexpr int kSegSteps = 1024 / kTK;
-template <int OP>
-__device__ __forceinline__ constexpr int seg_steps() { return OP == LSE ? kSegSteps : 1 << 30; }
+constexpr int kSegSteps16 = 16384 / kTK, kSegSteps32 = 4096 / kTK;
+template <int OP, bool SEGMENTS>
+__device__ __forceinline__ int seg_steps(const Params& p) {
+  return OP == LSE ? kSegSteps : SEGMENTS ? p.seg_steps : 1 << 30;
+}
 enum { B_FULL = 0, B_EMPTY = B_FULL + kStages, B_ACC_FULL = B_EMPTY + kStages,
        B_ACC_EMPTY = B_ACC_FULL + 2, B_DRAIN = B_ACC_EMPTY + 2, B_COUNT };
 static_assert(8 * B_COUNT + 8 <= 256, "barrier space");
@@ -302,7 +311,7 @@ __device__ __forceinline__ void load_unit(const Params& p, const Maps& maps, con
 }
 
 // MMA issuer, one unit (one thread of the pair's first CTA). it: accumulators filled so far.
-template <int OP>
+template <int OP, bool SEGMENTS>
 __device__ __forceinline__ void issue_unit(const Params& p, const Cta& c, int u, long long& kb, int& it,
                                            bool& ok) {
   constexpr bool A_MN = kAMn<OP>, B_MN = kBMn<OP>;
@@ -316,10 +325,10 @@ __device__ __forceinline__ void issue_unit(const Params& p, const Cta& c, int u,
   const long long tmo = c.tmo;
   int mi, ni, split;
   unit_of(p, u, mi, ni, split);
-  const int u_end = min(ksteps, (split + 1) * p.ksteps_per_split);
-  for (int k_begin = split * p.ksteps_per_split; k_begin < u_end; k_begin += seg_steps<OP>(), ++it) {
+  const int u_end = min(ksteps, (split + 1) * p.ksteps_per_split), seg = seg_steps<OP, SEGMENTS>(p);
+  for (int k_begin = split * p.ksteps_per_split; k_begin < u_end; k_begin += seg, ++it) {
     const int acc = it & 1;
-    const int k_end = OP == LSE ? min(u_end, k_begin + kSegSteps) : u_end;
+    const int k_end = OP == LSE || SEGMENTS ? min(u_end, k_begin + seg) : u_end;
     if (it >= 2 && !(ok = ptx::mbar_wait(bars + B_ACC_EMPTY + acc, ((it >> 1) - 1) & 1, abort_flag, tmo)))
       break;
     ptx::tc_fence_after();
@@ -340,8 +349,26 @@ __device__ __forceinline__ void issue_unit(const Params& p, const Cta& c, int u,
   }
 }
 
+// Adds the next accumulator's part of a thread's row to z, or sets z to it at the first one.
+__device__ __forceinline__ void add_segment(float (&z)[kTN / 64][32], uint32_t from, bool first) {
+#pragma unroll
+  for (int c = 0; c < kTN / 64; ++c) {
+    if (first) {
+      ptx::tmem_ld32(from + c * 32, z[c]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 32; h += 16) {
+        float t[16];
+        ptx::tmem_ld16(from + c * 32 + h, t);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[c][h + i] += t[i];
+      }
+    }
+  }
+}
+
 // Epilogue, one unit: a warp's 32 rows and half of the columns.
-template <int OP>
+template <int OP, bool SEGMENTS>
 __device__ __forceinline__ void finish_unit(const Params& p, const Maps& maps, const Cta& c, int u, int& it,
                                             bool& ok) {
   uint8_t* sm = c.sm;
@@ -378,20 +405,7 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Maps& maps, c
       if (!(ok = ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo))) break;
       ptx::tc_fence_after();
       const uint32_t from = tmem + lane_addr + acc * kTN + half * (kTN / 2);
-#pragma unroll
-      for (int c = 0; c < kTN / 64; ++c) {
-        if (k == 0) {
-          ptx::tmem_ld32(from + c * 32, z[c]);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 32; h += 16) {
-            float t[16];
-            ptx::tmem_ld16(from + c * 32 + h, t);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[c][h + i] += t[i];
-          }
-        }
-      }
+      add_segment(z, from, k == 0);
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_peer(ptx::peer_smem(bars + B_ACC_EMPTY + acc, 0));
@@ -425,6 +439,32 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Maps& maps, c
     }
     if (live) p.part[(size_t)(ni * 2 + half) * p.M + row] = make_float2(m2, sum);
     return;
+  }
+  if constexpr (SEGMENTS) {
+    // all segments but the last into registers, and their sum to the last one's place in TMEM
+    const int k0 = split * p.ksteps_per_split, n = min(ksteps, k0 + p.ksteps_per_split) - k0;
+    if (n > p.seg_steps) {
+      float z[kTN / 64][32];
+#pragma unroll 1
+      for (int k = 0;;) {
+        const int acc = it & 1;
+        if (!(ok = ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo))) return;
+        ptx::tc_fence_after();
+        const uint32_t from = tmem + lane_addr + acc * kTN + half * (kTN / 2);
+        add_segment(z, from, k == 0);
+        k += p.seg_steps;
+        if (k >= n) {
+#pragma unroll
+          for (int c = 0; c < kTN / 64; ++c)
+            ptx::tmem_st32(from + c * 32, reinterpret_cast<const uint32_t(&)[32]>(z[c]));
+          break;
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_peer(ptx::peer_smem(bars + B_ACC_EMPTY + acc, 0));
+        ++it;
+      }
+    }
   }
   const int acc = it & 1;
   if (!(ok = ptx::warp_wait(bars + B_ACC_FULL + acc, (it >> 1) & 1, abort_flag, tmo))) return;
@@ -502,7 +542,7 @@ struct Second<BOTH> {
   Maps maps;
 };
 
-template <int OP>
+template <int OP, bool SEGMENTS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
     gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps,
                 const __grid_constant__ Second<OP> second) {
@@ -567,11 +607,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
       for (int u = pair; ok && u < units; u += pairs) {
         if constexpr (OP == BOTH) {
           if (u >= units1) {
-            issue_unit<DW>(second.p, c, u - units1, kb, it, ok);
+            issue_unit<DW, false>(second.p, c, u - units1, kb, it, ok);
             continue;
           }
         }
-        issue_unit<OP1>(p, c, u, kb, it, ok);
+        issue_unit<OP1, SEGMENTS>(p, c, u, kb, it, ok);
       }
       ptx::mma_commit_pair(c.bars + B_DRAIN);
     }
@@ -579,11 +619,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXentThreads, 1)
     for (int u = pair; ok && u < units; u += pairs) {
       if constexpr (OP == BOTH) {
         if (u >= units1) {
-          finish_unit<DW>(second.p, second.maps, c, u - units1, it, ok);
+          finish_unit<DW, false>(second.p, second.maps, c, u - units1, it, ok);
           continue;
         }
       }
-      finish_unit<OP1>(p, maps, c, u, it, ok);
+      finish_unit<OP1, SEGMENTS>(p, maps, c, u, it, ok);
     }
     if ((OP == DW || OP == BOTH) && c.lane == 0) ptx::bulk_wait_all();   // the stores have been performed
   }

@@ -282,3 +282,37 @@ def test_an_fp32_gradient_is_not_held_to_16_bits(T, V, D, accumulate):
     eG = U * U * G.abs() + gp * (tol[:, None] + ez[:, None] + 2.0 ** -20)
     bw = eG.t() @ xd + T * 2.0 ** -23 * (G.abs().t() @ xd) + 2.0 ** -24 * dw64.abs() * 1.01 + 1e-30
     assert bool(((dw.double() - dw64).abs() <= bw).all()), float(((dw.double() - dw64).abs() / bw).max())
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_a_long_sum_of_one_sign_is_not_truncated(accumulate):
+    """dw over 2^18 tokens whose terms have one sign. The tensor core truncates its additions of
+    16 tokens, one or two steps of 2^-23 each; left to itself over 2^14 of them that is some
+    3e-4. The bound is what segments of 1024 tokens, added to nearest, would leave at most: 64
+    2^-22 within a segment and 2^8 2^-24 over them. With w = 0 the logits are 0 and p = 1/2 exactly; G is two terms (2^-16)."""
+    T, V, D = 1 << 18, 2, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (1 + torch.rand(T, D, generator=g, device="cuda")).bfloat16()
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(T, dtype=torch.int64, device="cuda")
+    dl = 0.5 + torch.rand(T, generator=g, device="cuda")
+    base = torch.ones(V, D, device="cuda")
+    _, lse = da.linear_xent_forward(x, w, y)
+    dw = base.clone()
+    da.linear_xent_backward(x, w, y, lse, dl, dw=dw, accumulate=accumulate)
+    want = 0.5 * (dl.double()[:, None] * x.double()).sum(0)
+    want = torch.stack((-want, want)) + (base.double() if accumulate else 0)
+    assert bool(((dw.double() - want).abs() <= (64 * 2.0 ** -22 + 2.0 ** -16 + 2.0 ** -16) * want.abs()).all())
+
+
+def test_a_long_sum_into_bf16_with_and_without_the_tile_store():
+    """More than 16384 tokens in one call, whose products reach dw in several segments."""
+    T, V, D = 33001, 600, 72
+    x, w, y, dl = _inputs(T, V, D, seed=21)
+    loss, lse = da.linear_xent_forward(x, w, y)
+    dx, dw = da.linear_xent_backward(x, w, y, lse, dl)
+    _check(x, w, y, dl, loss, lse, dx, dw)
+    base = torch.randn(V, D, device="cuda").mul_(1e-3).bfloat16()
+    dw = base.clone()
+    da.linear_xent_backward(x, w, y, lse, dl, dw=dw, accumulate=True)
+    _check(x, w, y, dl, loss, lse, dx, dw, base=base)

@@ -209,3 +209,12 @@ def test_rows_beyond_32_bit_offsets():
     grad = da.embed_backward(out, ids, V, dtable=table)
     assert torch.equal(grad[V - 1].float(), (2 * out[0].float()).bfloat16().float())
     assert float(grad[:V - 1].abs().max()) == 0
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V,D", [(32769, 5, 24), (40000, 70, 129), (70001, 300000, 16)])
+def test_gradient_of_more_tokens_than_a_warp_holds(t, T, V, D):
+    """Above 32768 tokens a warp of the sort has more strips than it keeps and reads them twice."""
+    ids = torch.randint(0, V, (T,), generator=_gen(T), device="cuda")
+    _run_grad(T, V, D, ids, t)
+    _run_grad(T, V, D, ids.to(torch.int32), t, torch.float32, padding_idx=3, accumulate=True)

@@ -165,3 +165,21 @@ def test_something_else_than_a_plan_gives_nan_and_touches_nothing():
         assert math.isnan(float(norm)) and all(torch.equal(a, b) for a, b in zip(grads, keep))
     got, _ = da.grad_clip(plan, 0.5)
     assert math.isfinite(float(got))
+
+
+@pytest.mark.parametrize("types", [[t] for t in TYPES] + [TYPES])
+@pytest.mark.parametrize("factor", [0.3, 2.0])
+def test_lists_whose_pieces_are_whole(types, factor):
+    """More than 20 million elements, so that pieces have 32768 and a thread its full number of
+    loads in flight, aligned and not; into buffers and in place."""
+    buf = _tensors([9000002], [types[0]], seed=8)[0]
+    grads = _tensors([16777221, 70001, 33], types, seed=9) + [buf[1:]]
+    keep = [g.clone() for g in grads]
+    max_norm = factor * float(ref.clip(grads, math.inf)[0])
+    outs = [torch.full_like(g, float("nan")) for g in grads]
+    norm, got = da.grad_clip(da.grad_clip_plan(grads, outs), max_norm)
+    _check(keep, got, norm, max_norm)
+    assert all(torch.equal(a, b) for a, b in zip(grads, keep))
+    norm2, got2 = da.grad_clip(da.grad_clip_plan(grads), max_norm)
+    assert torch.equal(norm, norm2)
+    assert all(torch.equal(a, b) for a, b in zip(outs, got2))

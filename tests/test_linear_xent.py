@@ -316,3 +316,61 @@ def test_a_long_sum_into_bf16_with_and_without_the_tile_store():
     dw = base.clone()
     da.linear_xent_backward(x, w, y, lse, dl, dw=dw, accumulate=True)
     _check(x, w, y, dl, loss, lse, dx, dw, base=base)
+
+
+@pytest.mark.parametrize("T,V,D", [(20, 700, 1032), (64, 300, 1096), (130, 520, 3080), (64, 300, 4096)])
+def test_hidden_sizes_of_several_segments(T, V, D):
+    """K of the logits in one and more segments of 1024, the last of them short."""
+    x, w, y, dl = _inputs(T, V, D, seed=D)
+    loss, lse = da.linear_xent_forward(x, w, y)
+    dx, dw = da.linear_xent_backward(x, w, y, lse, dl)
+    _check(x, w, y, dl, loss, lse, dx, dw)
+
+
+def test_a_long_logit_of_one_sign_is_not_truncated():
+    """Logits over K = 16384 whose products have one sign: 64 additions of 16 products within a
+    segment of 1024, one or two steps of 2^-23 of the segment's growing sum each (32 2^-22 at
+    most), 15 additions of segments and the scalings to nearest. One sum over all of K would be
+    2e-5 too small, more than twice this bound."""
+    T, V, D = 64, 300, 16384
+    g = torch.Generator(device="cuda").manual_seed(22)
+    x = (0.5 + torch.rand(T, D, generator=g, device="cuda")).bfloat16()
+    w = ((0.5 + torch.rand(V, D, generator=g, device="cuda")) * (60.0 / D)).bfloat16()
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    loss, lse = da.linear_xent_forward(x, w, y)
+    loss64, lse64 = ref.xent(x, w, y, IGN)
+    tol = (32 * 2.0 ** -22 + 20 * 2.0 ** -24) * lse64.abs() + 2.0 ** -19
+    assert bool(((lse.double() - lse64).abs() <= tol).all())
+    assert bool(((loss.double() - loss64).abs() <= 2 * tol).all())
+
+
+def test_pieces_whose_products_are_not_split():
+    """dX summed over the pieces of the vocabulary tile by tile: the first piece, one in the
+    middle and the last, with more tiles than a split of K starts from."""
+    T, V, D = 4096, 66000, 520
+    x, w, y, dl = _inputs(T, V, D, seed=23)
+    loss, lse = da.linear_xent_forward(x, w, y)
+    dx, dw = da.linear_xent_backward(x, w, y, lse, dl)
+    _check(x, w, y, dl, loss, lse, dx, dw)
+
+
+def test_a_long_range_of_the_vocabulary_in_one_unit():
+    """dX over 30000 ids in one unit of work: several segments of K."""
+    T, V, D = 2500, 30000, 1024
+    x, w, y, dl = _inputs(T, V, D, seed=24)
+    loss, lse = da.linear_xent_forward(x, w, y)
+    dx, dw = da.linear_xent_backward(x, w, y, lse, dl)
+    _check(x, w, y, dl, loss, lse, dx, dw)
+
+
+@pytest.mark.parametrize("dwt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V,D", [(64, 999, 200), (64, 524300, 8), (4096, 40000, 64), (1300, 20000, 2048)])
+def test_accumulation_by_terms_pieces_and_launches(T, V, D, dwt):
+    """dw added to what it holds: two terms of G in the empty half of a tile, those over two
+    pieces, several pieces of many tokens, and products in launches of their own."""
+    x, w, y, dl = _inputs(T, V, D, seed=T + D)
+    loss, lse = da.linear_xent_forward(x, w, y)
+    base = torch.randn(V, D, device="cuda").mul_(1e-3).to(dwt)
+    dw = base.clone()
+    dx, _ = da.linear_xent_backward(x, w, y, lse, dl, dw=dw, accumulate=True)
+    _check(x, w, y, dl, loss, lse, dx, dw, base=base)

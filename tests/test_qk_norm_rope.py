@@ -222,3 +222,21 @@ def test_feeds_the_attention():
     x["dq"], x["dk"] = dq, dk
     _, grads = _both(x, False)
     _check(x, 64, False, 1e-6, None, grads)
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("il", [False, True])
+@pytest.mark.parametrize("B,S,Hq,Hk,D,R", [(1, 4901, 27, 5, 64, 64), (2, 1361, 23, 6, 128, 64),
+                                           (1, 3001, 23, 6, 96, 24), (1, 3001, 9, 4, 256, 20)])
+def test_two_groups_of_heads_in_flight(t, il, B, S, Hq, Hk, D, R):
+    """Rows enough that every warp of the forward handles two groups of heads at once (19456
+    groups), with head counts that fill no group, all and part of the head rotated."""
+    L = 4 if D <= 64 else 8 if D <= 128 else 16
+    assert B * S * (Hq + Hk) // (2 * (32 // L)) >= 9728
+    x = _inputs(B, S, Hq, Hk, D, R, t, seed=D + R)
+    outs, grads = _both(x, il)
+    _check(x, R, il, 1e-6, outs, grads)
+    y = dict(x)
+    y["q"] = x["q"].transpose(1, 2).contiguous().transpose(1, 2)
+    got, _ = _both(y, il)
+    assert all(torch.equal(a, b) for a, b in zip(outs, got))

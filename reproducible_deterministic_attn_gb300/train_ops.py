@@ -1,8 +1,9 @@
 """Thin Python binding of the training-step operators in libdash_attn (include/dash_train.h).
 
 As in dash_attn.py the functions only check and marshal their arguments; every step runs in
-the library's CUDA kernels on torch's current stream of the tensors' device (or `stream`, on
-which a call then also allocates what it returns and uses).
+the library's CUDA kernels on torch's current stream of the tensors' device, which a call makes
+the current one for its time (or on `stream`, a stream of that device, on which it then also
+allocates what it returns and uses).
 Wrong types, shapes or devices raise ValueError before anything is queued, a status other
 than DASH_OK raises DashError. With check=True a call that has a workspace waits for the
 stream and raises what the device reported (an index out of range); check=False leaves that
@@ -84,6 +85,10 @@ def _stream(dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
 def _using(stream, t):
     """Makes `stream` (a torch stream or a raw handle) the current one, so that what a call
     allocates belongs to the stream that its kernels run on."""
@@ -91,6 +96,8 @@ def _using(stream, t):
         handle = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
         stream = (torch.cuda.ExternalStream(handle, device=t.device) if handle
                   else torch.cuda.default_stream(t.device))
+    if stream.device.index != t.get_device():
+        _bad(f"stream: expected a stream of the tensors' device, {t.device}")
     return torch.cuda.stream(stream)
 
 
@@ -150,6 +157,9 @@ def embed_forward(table, ids, scale: float = 1.0, out=None, status=None, stream=
         with _using(stream, table):
             return embed_forward(table, ids, scale, out, status)
     dev = _device(table, "table")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return embed_forward(table, ids, scale, out, status)
     dtype = _DTYPE.get(table.dtype)
     if dtype is None:
         _bad("table: expected bfloat16, float16 or float32")
@@ -189,6 +199,9 @@ def embed_backward(dout, ids, vocab: int, scale: float = 1.0, padding_idx=None, 
         with _using(stream, dout):
             return embed_backward(dout, ids, vocab, scale, padding_idx, dtable, accumulate, workspace, check=check)
     dev = _device(dout, "dout")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return embed_backward(dout, ids, vocab, scale, padding_idx, dtable, accumulate, workspace, check=check)
     dtype = _DTYPE.get(dout.dtype)
     if dtype is None:
         _bad("dout: expected bfloat16, float16 or float32")
@@ -296,6 +309,9 @@ def qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions=None, eps: float = 1e
         with _using(stream, q):
             return qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions, eps, interleaved, status)
     dev, tables, sizes, stride, bits, held = _qk_args(q, k, wq, wk, cos, sin, positions)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions, eps, interleaved, status)
     q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)
     _raise(_core.load().dash_qk_norm_rope_fwd(
         q.data_ptr(), k.data_ptr(), *tables, q_out.data_ptr(), k_out.data_ptr(), _status_word(status, dev),
@@ -328,6 +344,10 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None
             return qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq,
                                          dk, workspace, check=check)
     dev, tables, sizes, stride, bits, held = _qk_args(q, k, wq, wk, cos, sin, positions)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq,
+                                         dk, workspace, check=check)
     dtype, qshape, kshape, D = q.dtype, q.shape, k.shape, sizes[4]
     if (dq_out.dtype != dtype or dq_out.shape != qshape or not dq_out.is_contiguous() or dq_out.get_device() != dev
             or dk_out.dtype != dtype or dk_out.shape != kshape or not dk_out.is_contiguous()
@@ -381,6 +401,9 @@ def grad_clip_plan(grads, out=None, stream=None) -> GradClipPlan:
         with _using(stream, grads[0]):
             return grad_clip_plan(grads, None if out is None else outs)
     dev = _device(grads[0], "grads[0]")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return grad_clip_plan(grads, None if out is None else outs)
     arr = (_ClipTensor * len(grads))()
     spans = set()
     for i, (g, o) in enumerate(zip(grads, outs)):
@@ -412,6 +435,9 @@ def grad_clip(plan: GradClipPlan, max_norm: float, stream=None):
     overwrites."""
     if stream is not None:
         with _using(stream, plan.table):
+            return grad_clip(plan, max_norm)
+    if plan.device != _current_device():
+        with torch.cuda.device(plan.device):
             return grad_clip(plan, max_norm)
     _raise(_core.load().dash_grad_clip(plan.table.data_ptr(), plan.table.nbytes, max_norm, plan.norm.data_ptr(),
                                        _stream(plan.device)), "dash_grad_clip")
@@ -456,6 +482,9 @@ def linear_xent_forward(x, w, targets, ignore_index: int = -100, scale: float = 
         with _using(stream, x):
             return linear_xent_forward(x, w, targets, ignore_index, scale, workspace, check=check)
     dev, bits, sizes = _xent_args(x, w, targets)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return linear_xent_forward(x, w, targets, ignore_index, scale, workspace, check=check)
     T = sizes[0]
     if workspace is None:
         workspace = new_linear_xent_workspace(*sizes[:3], x.device)
@@ -482,6 +511,10 @@ def linear_xent_backward(x, w, targets, lse, dloss, ignore_index: int = -100, sc
             return linear_xent_backward(x, w, targets, lse, dloss, ignore_index, scale, dw, accumulate, dw_dtype,
                                         workspace, check=check)
     dev, bits, sizes = _xent_args(x, w, targets)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return linear_xent_backward(x, w, targets, lse, dloss, ignore_index, scale, dw, accumulate, dw_dtype,
+                                        workspace, check=check)
     T, V, D = sizes[:3]
     plse, pdloss = _vector(lse, "lse", T, dev), _vector(dloss, "dloss", T, dev)
     if dw is None:

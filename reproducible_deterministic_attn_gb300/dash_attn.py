@@ -2,9 +2,9 @@
 the attention forward/backward runs in the library's CUDA kernels.
 
 The functions keep the C names. Tensors are torch CUDA tensors (BSHD bf16, LSE fp32
-[B, H, S]); the stream defaults to torch's current stream on the tensors' device. A
-status other than DASH_OK raises DashError. There is no CPU path: calling into the
-library without the built shared object raises immediately.
+[B, H, S]); the stream defaults to torch's current stream on the tensors' device, which a
+call makes the current one for its time. A status other than DASH_OK raises DashError. There
+is no CPU path: calling into the library without the built shared object raises immediately.
 """
 
 from __future__ import annotations
@@ -125,9 +125,10 @@ def _shape(q: torch.Tensor):
 def dash_attn_fwd(q, k, v, o, lse, scale: float, mask: int, stream=None) -> None:
     """O and LSE of softmax attention (writes into o and lse)."""
     B, S, H, D = _shape(q)
-    _check(load().dash_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                lse.data_ptr(), B, S, H, D, float(scale), int(mask),
-                                _stream(q, stream)), "dash_attn_fwd")
+    with torch.cuda.device_of(q):
+        _check(load().dash_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                    lse.data_ptr(), B, S, H, D, float(scale), int(mask),
+                                    _stream(q, stream)), "dash_attn_fwd")
 
 
 def dash_attn_fwd_ex(q, k, v, o, lse, scale: float, mask: int, status=None, stream=None) -> None:
@@ -135,10 +136,11 @@ def dash_attn_fwd_ex(q, k, v, o, lse, scale: float, mask: int, status=None, stre
     None): cleared by the call, set to DASH_ERR_SYNC_TIMEOUT by the kernel if a wait ran
     out."""
     B, S, H, D = _shape(q)
-    _check(load().dash_attn_fwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                   lse.data_ptr(), B, S, H, D, float(scale), int(mask),
-                                   status.data_ptr() if status is not None else None,
-                                   _stream(q, stream)), "dash_attn_fwd_ex")
+    with torch.cuda.device_of(q):
+        _check(load().dash_attn_fwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                       lse.data_ptr(), B, S, H, D, float(scale), int(mask),
+                                       status.data_ptr() if status is not None else None,
+                                       _stream(q, stream)), "dash_attn_fwd_ex")
 
 
 def dash_attn_bwd_workspace_size(B: int, S: int, H: int, D: int) -> int:
@@ -149,11 +151,12 @@ def dash_attn_bwd(q, k, v, o, dO, lse, dq, dk, dv, workspace, scale: float, mask
                   schedule: int, deterministic: int, stream=None) -> None:
     """dQ, dK, dV (written into dq, dk, dv). workspace: a uint8 CUDA tensor."""
     B, S, H, D = _shape(q)
-    _check(load().dash_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                dO.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                dv.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                B, S, H, D, float(scale), int(mask), int(schedule),
-                                int(deterministic), _stream(q, stream)), "dash_attn_bwd")
+    with torch.cuda.device_of(q):
+        _check(load().dash_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                    dO.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                    dv.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                    B, S, H, D, float(scale), int(mask), int(schedule),
+                                    int(deterministic), _stream(q, stream)), "dash_attn_bwd")
 
 
 def dash_attn_bwd_static(q, k, v, o, dO, lse, dq, dk, dv, scale: float, mask: int,
@@ -161,18 +164,20 @@ def dash_attn_bwd_static(q, k, v, o, dO, lse, dq, dk, dv, scale: float, mask: in
     """dash_attn_bwd without a workspace: the scratch is the library's static device array
     (no device allocation). status_out: optional int32 CUDA tensor for the status word."""
     B, S, H, D = _shape(q)
-    _check(load().dash_attn_bwd_static(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                       dO.data_ptr(), lse.data_ptr(), dq.data_ptr(),
-                                       dk.data_ptr(), dv.data_ptr(),
-                                       None if status_out is None else status_out.data_ptr(),
-                                       B, S, H, D, float(scale), int(mask), int(schedule),
-                                       int(deterministic), _stream(q, stream)),
-           "dash_attn_bwd_static")
+    with torch.cuda.device_of(q):
+        _check(load().dash_attn_bwd_static(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                           dO.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+                                           dk.data_ptr(), dv.data_ptr(),
+                                           None if status_out is None else status_out.data_ptr(),
+                                           B, S, H, D, float(scale), int(mask), int(schedule),
+                                           int(deterministic), _stream(q, stream)),
+               "dash_attn_bwd_static")
 
 
 def dash_attn_get_status(workspace, stream=None) -> int:
     """Synchronises the stream and returns the status the last backward recorded."""
-    return int(load().dash_attn_get_status(workspace.data_ptr(), _stream(workspace, stream)))
+    with torch.cuda.device_of(workspace):
+        return int(load().dash_attn_get_status(workspace.data_ptr(), _stream(workspace, stream)))
 
 
 def dash_status_string(status: int) -> str:
@@ -322,10 +327,11 @@ def dash_gemm_splitk(a: torch.Tensor, b: torch.Tensor, c: torch.Tensor, workspac
     """C = A B^T (a: bf16 [M, K], b: bf16 [N, K], c: fp32 [M, N]), K in `splits` chunks."""
     M, K = a.shape
     N = b.shape[0]
-    _check(load().dash_gemm_splitk(a.data_ptr(), b.data_ptr(), c.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), int(M), int(N),
-                                   int(K), int(splits), int(deterministic), _stream(a, stream)),
-           "dash_gemm_splitk")
+    with torch.cuda.device_of(a):
+        _check(load().dash_gemm_splitk(a.data_ptr(), b.data_ptr(), c.data_ptr(),
+                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(M), int(N),
+                                       int(K), int(splits), int(deterministic), _stream(a, stream)),
+               "dash_gemm_splitk")
 
 
 def gemm_splitk(a: torch.Tensor, b: torch.Tensor, splits: int, deterministic: int = 1,

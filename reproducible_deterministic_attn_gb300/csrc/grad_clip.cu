@@ -46,9 +46,11 @@ struct Header {
 };
 constexpr size_t kTableOff = (sizeof(Header) + 255) / 256 * 256;
 
-// Whether this is a plan, and the launch has its blocks.
-__device__ __forceinline__ bool plan_fits(const Header* h) {
-  return h->magic == kMagic && h->blocks <= (int)gridDim.x;
+// Whether this is a plan whose table lies within the caller's buffer (`capacity` pieces) and
+// whose blocks the launch has. No other plan's table is read.
+__device__ __forceinline__ bool plan_fits(const Header* h, long long capacity) {
+  return h->magic == kMagic && h->pieces >= 0 && h->pieces <= capacity && h->blocks >= 1 &&
+         h->blocks <= (int)gridDim.x;
 }
 
 // Sum of squares of this thread's elements of a piece. 32 bits hold the sum unless it
@@ -133,11 +135,12 @@ __device__ __forceinline__ double block_sum(double v, double* shared) {
   return t;                              // thread 0's
 }
 
-__global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const Piece* table, float* norm) {
+__global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const Piece* table,
+                                                                 long long capacity, float* norm) {
   __shared__ double shared[kThreads / 32];
   __shared__ bool last;
   grid_next();
-  if (!plan_fits(h)) {
+  if (!plan_fits(h, capacity)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = NAN;
     return;
   }
@@ -213,9 +216,9 @@ __device__ __forceinline__ void scale_of(const Piece& pc, float f, bool copy) {
 }
 
 __global__ void __launch_bounds__(kThreads, 2) clip_scale_kernel(const Header* h, const Piece* table,
-                                                              float max_norm) {
+                                                                  long long capacity, float max_norm) {
   // the table and its header's constants are the plan's, not the kernel's before
-  const bool ok = plan_fits(h);
+  const bool ok = plan_fits(h, capacity);
   const long long first = ok ? h->pieces - 1 - blockIdx.x : -1;
   Piece next = {};
   if (first >= 0) next = table[first];
@@ -307,10 +310,11 @@ dash_status_t dash_grad_clip(void* plan, size_t plan_bytes, float max_norm, floa
   Header* h = (Header*)plan;
   const Piece* table = (const Piece*)((char*)plan + kTableOff);
   // no more blocks than the table can hold pieces for (the header has the exact number)
-  const int grid = (int)std::max<size_t>(1, std::min<size_t>(kBlocks, (plan_bytes - kTableOff) / sizeof(Piece)));
-  clip_norm_kernel<<<grid, kThreads, 0, stream>>>(h, table, norm);
+  const long long capacity = (long long)((plan_bytes - kTableOff) / sizeof(Piece));
+  const int grid = (int)std::max<long long>(1, std::min<long long>(kBlocks, capacity));
+  clip_norm_kernel<<<grid, kThreads, 0, stream>>>(h, table, capacity, norm);
   DASH_TRY(cudaGetLastError());
-  DASH_TRY(launch_after(clip_scale_kernel, dim3(grid), kThreads, 0, stream, h, table, max_norm));
+  DASH_TRY(launch_after(clip_scale_kernel, dim3(grid), kThreads, 0, stream, h, table, capacity, max_norm));
   return DASH_OK;
 }
 

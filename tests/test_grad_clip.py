@@ -183,3 +183,18 @@ def test_lists_whose_pieces_are_whole(types, factor):
     norm2, got2 = da.grad_clip(da.grad_clip_plan(grads), max_norm)
     assert torch.equal(norm, norm2)
     assert all(torch.equal(a, b) for a, b in zip(outs, got2))
+
+
+@pytest.mark.parametrize("short", [1, 30])
+def test_a_plan_of_more_pieces_than_blocks_in_a_buffer_too_short(short):
+    """The whole table is there, but the call says that its buffer ends some entries earlier."""
+    grads = _tensors([700 * 4096], [torch.float32], seed=11)
+    keep = [g.clone() for g in grads]
+    plan = da.grad_clip_plan(grads)
+    lib, norm = da.load(), torch.zeros((), device="cuda")
+    size = plan.table.numel() - 256 - 24 * short
+    assert lib.dash_grad_clip(plan.table.data_ptr(), size, 0.5, norm.data_ptr(), 0) == da.DASH_OK
+    torch.cuda.synchronize()
+    assert math.isnan(float(norm)) and all(torch.equal(a, b) for a, b in zip(grads, keep))
+    got, _ = da.grad_clip(plan, 0.5)
+    assert math.isfinite(float(got))

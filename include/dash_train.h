@@ -147,7 +147,8 @@ dash_status_t dash_grad_clip_plan(const dash_clip_tensor_t* tensors, int n, void
  * tensor when *norm > max_norm, out = grad otherwise (nothing is written then where out is
  * grad). Squares are summed in fp32 over at most 32768 elements of a tensor, these sums in
  * fp64; where squares would overflow or vanish in fp32 the elements are rescaled by a power
- * of two first. When the norm is not finite *norm says so and the values are passed unscaled.
+ * of two first. When the norm is not finite in fp32 *norm says so and the values are passed
+ * unscaled.
  *   plan : from dash_grad_clip_plan, on this device, of plan_bytes (dash_grad_clip_plan_size);
  *          something else gives the norm NaN and touches no tensor
  *   norm : device fp32 (written)

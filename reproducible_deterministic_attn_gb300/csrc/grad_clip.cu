@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) clip_scale_kernel(const Header* h
   grid_wait();
   if (!ok) return;
   const double n = h->norm;
-  const bool copy = !(n > (double)max_norm) || isinf(n);
+  const bool copy = !(n > (double)max_norm) || isinf((float)n);   // as the caller's norm says
   if (copy && h->all_in_place) return;
   const float f = copy ? 1.f : (float)((double)max_norm / n);
   for (long long i = first; i >= 0; i -= gridDim.x) {

@@ -198,3 +198,16 @@ def test_a_plan_of_more_pieces_than_blocks_in_a_buffer_too_short(short):
     assert math.isnan(float(norm)) and all(torch.equal(a, b) for a, b in zip(grads, keep))
     got, _ = da.grad_clip(plan, 0.5)
     assert math.isfinite(float(got))
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+def test_a_norm_beyond_fp32_leaves_the_values(t):
+    """The elements are finite and so is their norm in 64 bits; in 32, as the caller gets it, it
+    is not."""
+    grads = [torch.full((3,), 3e38, dtype=t, device="cuda"), torch.randn(5000, device="cuda")]
+    keep = [g.clone() for g in grads]
+    outs = [torch.zeros_like(g) for g in grads]
+    norm, got = da.grad_clip(da.grad_clip_plan(grads, outs), 1.0)
+    assert float(norm) == math.inf and all(torch.equal(a, b) for a, b in zip(got, keep))
+    norm, _ = da.grad_clip(da.grad_clip_plan(grads), 1.0)
+    assert float(norm) == math.inf and all(torch.equal(a, b) for a, b in zip(grads, keep))

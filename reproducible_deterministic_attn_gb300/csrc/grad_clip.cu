@@ -177,17 +177,31 @@ __global__ void __launch_bounds__(kThreads, 2) clip_norm_kernel(Header* h, const
   }
 }
 
+// The factor max_norm / norm as a product, the second one a power of two: 1, unless a single
+// fp32 would be below the normal range and lose bits.
+struct Factor {
+  float f, g;
+  __device__ __forceinline__ float operator()(float x) const { return x * f * g; }
+};
+__device__ __forceinline__ Factor factor(double x) {
+  if (x >= 0x1p-126 || x == 0.0) return {(float)x, 1.f};
+  int e;
+  frexp(x, &e);
+  const double g = ldexp(1.0, max(e, -149));
+  return {(float)(x / g), (float)g};
+}
+
 template <typename T, int VEC>
-__device__ __forceinline__ Vec<T, VEC> scaled(const Vec<T, VEC>& v, float f, bool copy) {
+__device__ __forceinline__ Vec<T, VEC> scaled(const Vec<T, VEC>& v, Factor f, bool copy) {
   float z[VEC];
   unpack<T, VEC>(v, z);
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) z[k] *= f;
+  for (int k = 0; k < VEC; ++k) z[k] = f(z[k]);
   return copy ? v : pack<T, VEC>(z);
 }
 
 template <typename T, int VEC>
-__device__ __forceinline__ void scale_piece(const T* x, T* y, int count, float f, bool copy) {
+__device__ __forceinline__ void scale_piece(const T* x, T* y, int count, Factor f, bool copy) {
   constexpr int kStep = kThreads * VEC;
   const int whole = count / VEC * VEC;
   int i = threadIdx.x * VEC;
@@ -203,11 +217,11 @@ __device__ __forceinline__ void scale_piece(const T* x, T* y, int count, float f
   for (; i < whole; i += kStep) store_vec<T, VEC>(y + i, scaled<T, VEC>(load_vec<T, VEC>(x + i), f, copy));
 #pragma unroll 1
   for (int j = whole + threadIdx.x; j < count; j += kThreads)
-    y[j] = copy ? x[j] : from_f32<T>(to_f32(x[j]) * f);
+    y[j] = copy ? x[j] : from_f32<T>(f(to_f32(x[j])));
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_of(const Piece& pc, float f, bool copy) {
+__device__ __forceinline__ void scale_of(const Piece& pc, Factor f, bool copy) {
   constexpr int W = 16 / sizeof(T);
   const T* x = (const T*)pc.grad;
   T* y = (T*)pc.out;
@@ -227,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2) clip_scale_kernel(const Header* h
   const double n = h->norm;
   const bool copy = !(n > (double)max_norm) || isinf((float)n);   // as the caller's norm says
   if (copy && h->all_in_place) return;
-  const float f = copy ? 1.f : (float)((double)max_norm / n);
+  const Factor f = factor(copy ? 1.0 : (double)max_norm / n);
   for (long long i = first; i >= 0; i -= gridDim.x) {
     const Piece pc = next;
     if (i >= gridDim.x) next = table[i - gridDim.x];

@@ -211,3 +211,17 @@ def test_a_norm_beyond_fp32_leaves_the_values(t):
     assert float(norm) == math.inf and all(torch.equal(a, b) for a, b in zip(got, keep))
     norm, _ = da.grad_clip(da.grad_clip_plan(grads), 1.0)
     assert float(norm) == math.inf and all(torch.equal(a, b) for a, b in zip(grads, keep))
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size,max_norm", [(1e36, 1e-6), (1e33, 1e-9), (1e36, 1e-37), (1.0, 1e-38)])
+def test_a_limit_far_below_the_norm(t, size, max_norm):
+    """The factor is below fp32's normal range, or the clipped values are."""
+    grads = [(torch.randn(50021, device="cuda", dtype=torch.float64) * size).to(t),
+             torch.randn(300, device="cuda")]
+    keep = [g.clone() for g in grads]
+    outs = [torch.full_like(g, float("nan")) for g in grads]
+    norm, got = da.grad_clip(da.grad_clip_plan(grads, outs), max_norm)
+    _check(keep, got, norm, max_norm)
+    norm, got = da.grad_clip(da.grad_clip_plan(grads), max_norm)
+    assert all(torch.equal(a, b) for a, b in zip(outs, got))

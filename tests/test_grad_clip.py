@@ -225,3 +225,21 @@ def test_a_limit_far_below_the_norm(t, size, max_norm):
     _check(keep, got, norm, max_norm)
     norm, got = da.grad_clip(da.grad_clip_plan(grads), max_norm)
     assert all(torch.equal(a, b) for a, b in zip(outs, got))
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("aligned", [True, False])
+def test_mostly_zero_rows_and_single_values_among_zeros(t, aligned):
+    """A table's gradient whose rows are mostly zero, of either sign, and threads that hold one
+    value, small enough that its square is lost in fp32, among zeros."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(3001, 1024, generator=g, device="cuda").to(t)
+    x[torch.rand(3001, generator=g, device="cuda") < 0.8] = -0.0
+    low = torch.zeros(200000, device="cuda", dtype=t)
+    low[:3001] = -0.0
+    low[::4099] = torch.finfo(t).tiny * 0.75
+    x, low = (v.reshape(-1)[0 if aligned else 1:] for v in (x, low))
+    for grads in ([x], [low], [x, low], [torch.full_like(x, -0.0)]):
+        n64 = float(ref.clip(grads, math.inf)[0])
+        norm, _ = da.grad_clip(da.grad_clip_plan(grads), math.inf)
+        assert abs(float(norm) - n64) <= NORM_REL * n64 + 2.0 ** -149

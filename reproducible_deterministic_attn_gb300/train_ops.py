@@ -382,11 +382,13 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None
 
 class GradClipPlan:
     """The tensors of grad_clip and their table on the device. Holds the tensors, so that the
-    addresses in the table stay theirs; build a new plan when a gradient is replaced."""
+    addresses in the table stay theirs; build a new plan when a gradient is replaced, and keep
+    the plan as long as a graph that captured a call on it is replayed."""
 
     def __init__(self, grads, outs, table, norm):
         self.grads, self.outs, self.table, self.norm = grads, outs, table, norm
         self.device = table.get_device()
+        self.stream = _stream(self.device)           # that its memory was allocated on
 
 
 def grad_clip_plan(grads, out=None, stream=None) -> GradClipPlan:
@@ -439,8 +441,13 @@ def grad_clip(plan: GradClipPlan, max_norm: float, stream=None):
     if plan.device != _current_device():
         with torch.cuda.device(plan.device):
             return grad_clip(plan, max_norm)
+    at = _stream(plan.device)
+    if at != plan.stream:                            # its memory stays until this call's work has ended
+        here = torch.cuda.current_stream(plan.device)
+        plan.table.record_stream(here)
+        plan.norm.record_stream(here)
     _raise(_core.load().dash_grad_clip(plan.table.data_ptr(), plan.table.nbytes, max_norm, plan.norm.data_ptr(),
-                                       _stream(plan.device)), "dash_grad_clip")
+                                       at), "dash_grad_clip")
     return plan.norm, plan.outs
 
 

@@ -243,3 +243,22 @@ def test_mostly_zero_rows_and_single_values_among_zeros(t, aligned):
         n64 = float(ref.clip(grads, math.inf)[0])
         norm, _ = da.grad_clip(da.grad_clip_plan(grads), math.inf)
         assert abs(float(norm) - n64) <= NORM_REL * n64 + 2.0 ** -149
+
+
+def test_a_plan_dropped_while_another_stream_still_uses_it():
+    """Its memory is not given out again before that stream's work has ended."""
+    grads = _tensors([5000, 70001], [torch.float32], seed=13)
+    want = [g.clone() for g in grads]
+    want_norm = da.grad_clip(da.grad_clip_plan(want), 1.0)[0].clone()
+    plan = da.grad_clip_plan(grads)
+    where, size = plan.table.data_ptr(), plan.table.numel()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    norm, got = da.grad_clip(plan, 1.0, stream=s)
+    del plan
+    new = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(t.data_ptr() != where for t in new)
+    s.synchronize()
+    assert torch.equal(norm, want_norm) and all(torch.equal(a, b) for a, b in zip(got, want))

@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(1024) check_targets_kernel(const void* targets
   if (threadIdx.x < kWsHeaderBytes / 4) header[threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll 4
-  for (int t = threadIdx.x; t < T; t += 1024) {
+  for (unsigned t = threadIdx.x; t < (unsigned)T; t += 1024) {     // T may be within 1024 of 2^31
     const long long y = train::load_index(targets, t, id_bits);
     if (y != ignore_index && (y < 0 || y >= V)) train::report_index(header, CHK_TARGET, t, y, V);
   }

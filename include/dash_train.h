@@ -145,9 +145,9 @@ dash_status_t dash_grad_clip_plan(const dash_clip_tensor_t* tensors, int n, void
 /*
  * *norm = sqrt(sum of all elements squared), and out = grad * (max_norm / *norm) for every
  * tensor when *norm > max_norm, out = grad otherwise (nothing is written then where out is
- * grad). Squares are summed in fp32 over at most 32768 elements of a tensor, these sums in
- * fp64; where squares would overflow or vanish in fp32 the elements are rescaled by a power
- * of two first. When the norm is not finite in fp32 *norm says so and the values are passed
+ * grad). Squares are summed in fp32 over at most 64 elements of a tensor, these sums in fp64;
+ * where squares would overflow or vanish in fp32 the elements are rescaled by a power of two
+ * first. When the norm is not finite in fp32 *norm says so and the values are passed
  * unscaled.
  *   plan : from dash_grad_clip_plan, on this device, of plan_bytes (dash_grad_clip_plan_size);
  *          something else gives the norm NaN and touches no tensor
@@ -170,7 +170,8 @@ dash_status_t dash_grad_clip(void* plan, size_t plan_bytes, float max_norm, floa
  *   loss    : fp32 [T] (written)        lse : fp32 [T] (written)
  *   workspace : dash_linear_xent_workspace_size(T, V, D) bytes
  * T >= 0, V >= 1, D a positive multiple of 8, ldx and ldw multiples of 8 not below D,
- * scale > 0; x, w, dx and dw 16-byte aligned, the others as their elements. T * D, V * D up to 2^40; T, V below 2^31 - 256.
+ * scale > 0; x, w, dx and dw 16-byte aligned, the others as their elements. T * D, V * D up to
+ * 2^40; T, V below 2^31 - 256.
  * Returns DASH_ERR_UNSUPPORTED for other sizes. bf16 only, as the attention: the gradient
  * passes G below through the tensor cores in the operands' type, and fp16 would lose its
  * small probabilities.

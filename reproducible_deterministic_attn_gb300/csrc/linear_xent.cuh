@@ -21,7 +21,7 @@
 // Bound by the tensor cores, over a whole pass by the power they draw. Measured at 8192 tokens,
 // 65536 ids, D = 4096: LSE 2.35 ms, GRAD, DX and DW of a quarter of the ids 0.59, 0.60 and 0.61
 // ms by themselves (1800 to 1870 TFLOP/s), the four in a loop 10.5 ms (1675; cuBLAS sustains
-// 1683 on this card). Tiles of 128 x 256 on single CTAs: 0.65 to 0.67 ms, 11.5 ms in a loop.
+// 1683 on this card), 10.95 on another. With an fp32 dW the backward takes 11.1 ms instead of 7.8. Tiles of 128 x 256 on single CTAs: 0.65 to 0.67 ms, 11.5 ms in a loop.
 //
 // Warp roles (384 threads a CTA): 0 = TMA producer (64 of K per stage, 6 stages of 32 KB), 1 =
 // MMA issuer (the pair's first CTA), 4..11 = epilogue (one 32-row quarter and one half of the

@@ -4,7 +4,8 @@
 // (rounded up to a power of two) and the mean of squares is a shuffle tree over them. The
 // chunks are chosen so that rotation partners meet in one lane: chunks j and j + R / 16 for
 // half-split pairs, neighbours for interleaved ones. (Where R / 2 is no multiple of 8, or of 4
-// for interleaved pairs, a value's partner is read once more, which hits L1.)
+// for interleaved pairs, a value's partner is read once more, which hits L1: 16384 tokens x 40
+// heads x 96 with R = 24 take 178 us forward and 169 backward, where the bytes take 37 and 56.)
 // Both directions read and write every value once: bound by HBM, with the instructions next
 // (8 values a lane and shuffled partners took 22 an element forward, 31 backward, and 105 and
 // 167 us for 16384 tokens x 64 heads x 128; now 15 and 23, and 232 us for both, where the bytes

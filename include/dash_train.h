@@ -207,6 +207,57 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
                                    long long ignore_index, int id_bits, int dw_dtype,
                                    int accumulate, cudaStream_t stream);
 
+/* ---- Cross attention to states of another length ----------------------------------------- */
+
+/*
+ * O = softmax(scale * Q K^T) V over the first kv_lens[b] keys of batch b, and the natural-log
+ * LSE per row. Hq / Hk query heads share a key head (query head h reads key head h * Hk / Hq).
+ *   q        : bf16 [B, Sq, Hq, D], k, v : bf16 [B, Sk, Hk, D], D contiguous, with element strides
+ *              {batch, token, head} in q_strides, k_strides, v_strides: the parts of a fused
+ *              projection, [B, H, S, D], and batches or heads that are shared (a stride of zero)
+ *              are read in place (multiples of 8)
+ *   kv_lens  : [B] int32 or int64, 0 <= kv_lens[b] <= Sk, or NULL: all Sk keys. A batch without
+ *              keys has O = 0 and LSE = -inf. What lies behind a length is never used: it may
+ *              hold infinities or NaN
+ *   o        : bf16 contiguous [B, Sq, Hq, D] (written)    lse : fp32 [B, Hq, Sq] (written)
+ *   status   : optional device int32 (NULL = none), cleared by the call: DASH_ERR_BOUNDS for a
+ *              length out of range, whose batch gets NaN in o and lse; DASH_ERR_SYNC_TIMEOUT for
+ *              a wait that ran out, with NaN in lse
+ *   workspace: dash_cross_attn_fwd_workspace_size(B, Sq, Sk, Hq, Hk, D) bytes
+ * B, Sq, Sk >= 0; Hq a multiple of Hk; D a multiple of 8 up to 128; Sq, Sk up to 2^24 and
+ * B * Hq * max(Sq, Sk) below 2^31 - 256; scale > 0 and finite. q, k, v, o 16-byte aligned, the
+ * others as their elements. bf16 only, as the attention.
+ */
+size_t dash_cross_attn_fwd_workspace_size(int B, int Sq, int Sk, int Hq, int Hk, int D);
+dash_status_t dash_cross_attn_fwd(const void* q, const void* k, const void* v, const void* kv_lens,
+                                  void* o, float* lse, int* status, void* workspace,
+                                  size_t workspace_bytes, int B, int Sq, int Sk, int Hq, int Hk,
+                                  int D, const long long* q_strides, const long long* k_strides,
+                                  const long long* v_strides, float scale, int id_bits,
+                                  cudaStream_t stream);
+
+/*
+ * Gradients of the above, with P = exp(scale * Q K^T - LSE) recomputed: dV = P^T dO,
+ * dS = P * (dO V^T - rowsum(dO * O)), dQ = scale * dS K, dK = scale * dS^T Q; dK and dV sum over
+ * the query heads that share a key head.
+ *   o, do    : bf16 contiguous [B, Sq, Hq, D], lse : fp32 [B, Hq, Sq] (read)
+ *   dq, dk, dv : strided as dq_strides, dk_strides, dv_strides say (written; no stride of zero over
+ *              more than one element). Rows of dk and dv behind a length are zero; a batch
+ *              without keys has dq = 0, one whose length is out of range NaN in dq, dk and dv
+ *   workspace: dash_cross_attn_bwd_workspace_size(B, Sq, Sk, Hq, Hk, D) bytes
+ * The workspace's status reads DASH_ERR_BOUNDS or DASH_ERR_SYNC_TIMEOUT as above. Other
+ * arguments and errors as for the forward.
+ */
+size_t dash_cross_attn_bwd_workspace_size(int B, int Sq, int Sk, int Hq, int Hk, int D);
+dash_status_t dash_cross_attn_bwd(const void* q, const void* k, const void* v, const void* kv_lens,
+                                  const void* o, const void* d_o, const float* lse, void* dq, void* dk,
+                                  void* dv, void* workspace, size_t workspace_bytes, int B, int Sq,
+                                  int Sk, int Hq, int Hk, int D, const long long* q_strides,
+                                  const long long* k_strides, const long long* v_strides,
+                                  const long long* dq_strides, const long long* dk_strides,
+                                  const long long* dv_strides, float scale, int id_bits,
+                                  cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

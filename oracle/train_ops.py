@@ -82,3 +82,51 @@ def clip(grads, max_norm):
     norm = torch.sqrt(sum((g.double() ** 2).sum() for g in grads))
     f = max_norm / norm if norm > max_norm else 1.0
     return norm, [g.double() * f for g in grads]
+
+
+def _group(x, g):
+    """Key heads [B, S, Hk, D] for each query head, [B, Hk * g, S, D]."""
+    return x.double().transpose(1, 2).repeat_interleave(g, 1)
+
+
+def cross_attn(q, k, v, lens, scale):
+    """(O [B, Sq, Hq, D], LSE [B, Hq, Sq], P) of queries over the first lens[b] keys; keys and
+    values behind a length are not looked at."""
+    B, Sq, Hq, D = q.shape
+    Sk, g = k.shape[1], Hq // k.shape[2]
+    out = torch.zeros(B, Hq, Sq, D, dtype=torch.float64, device=q.device)
+    lse = torch.full((B, Hq, Sq), float("-inf"), dtype=torch.float64, device=q.device)
+    p = torch.zeros(B, Hq, Sq, Sk, dtype=torch.float64, device=q.device)
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        z = scale * q[b].double().transpose(0, 1) @ _group(k[b:b + 1, :n], g)[0].transpose(1, 2)
+        lse[b] = torch.logsumexp(z, -1)
+        p[b, :, :, :n] = torch.softmax(z, -1)
+        out[b] = p[b, :, :, :n] @ _group(v[b:b + 1, :n], g)[0]
+    return out.transpose(1, 2), lse, p
+
+
+def cross_attn_grad(q, k, v, o, do, lse, lens, scale):
+    """(dQ, dK, dV, P, dS) with P = exp(scale q k - lse) and the given o, as the operator is defined;
+    P and dS are [B, Hq, Sq, Sk]."""
+    B, Sq, Hq, D = q.shape
+    Sk, Hk = k.shape[1], k.shape[2]
+    g = Hq // Hk
+    qd, dd = q.double().transpose(1, 2), do.double().transpose(1, 2)
+    delta = (dd * o.double().transpose(1, 2)).sum(-1, keepdim=True)
+    p = torch.zeros(B, Hq, Sq, Sk, dtype=torch.float64, device=q.device)
+    ds = torch.zeros_like(p)
+    dq = torch.zeros_like(qd)
+    dk = torch.zeros(B, Sk, Hk, D, dtype=torch.float64, device=q.device)
+    dv = torch.zeros_like(dk)
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        kb, vb = _group(k[b:b + 1, :n], g)[0], _group(v[b:b + 1, :n], g)[0]
+        p[b, :, :, :n] = torch.exp(scale * qd[b] @ kb.transpose(1, 2) - lse[b].double()[..., None])
+        ds[b, :, :, :n] = p[b, :, :, :n] * (dd[b] @ vb.transpose(1, 2) - delta[b])
+        dq[b] = scale * ds[b, :, :, :n] @ kb
+        dk[b] = scale * (ds[b].transpose(1, 2) @ qd[b]).view(Hk, g, Sk, D).sum(1).transpose(0, 1)
+        dv[b] = (p[b].transpose(1, 2) @ dd[b]).view(Hk, g, Sk, D).sum(1).transpose(0, 1)
+    return dq.transpose(1, 2), dk, dv, p, ds

@@ -20,9 +20,10 @@ from .dash_attn import (  # noqa: F401
     TRACE_TOTAL,
 )
 from .train_ops import (  # noqa: F401
-    DASH_BF16, DASH_FP16, DASH_FP32, GradClipPlan, dash_embed_bwd_workspace_size,
+    DASH_BF16, DASH_FP16, DASH_FP32, GradClipPlan, cross_attn_backward, cross_attn_forward,
+    dash_cross_attn_bwd_workspace_size, dash_cross_attn_fwd_workspace_size, dash_embed_bwd_workspace_size,
     dash_linear_xent_workspace_size, dash_qk_norm_rope_bwd_workspace_size, embed_backward,
     embed_forward, grad_clip, grad_clip_plan, linear_xent_backward, linear_xent_forward,
-    new_embed_workspace, new_linear_xent_workspace, new_qk_norm_rope_workspace,
+    new_cross_attn_workspace, new_embed_workspace, new_linear_xent_workspace, new_qk_norm_rope_workspace,
     qk_norm_rope_backward, qk_norm_rope_forward, rope_table,
 )

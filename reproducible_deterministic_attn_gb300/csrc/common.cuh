@@ -34,7 +34,7 @@ constexpr int kStatusBounds = 7;
 enum : int {
   CHK_CTA_RANGE = 1, CHK_PIECE = 2, CHK_TASK = 3, CHK_ORDINAL = 4,
   // checked in every build: indexes that come from the caller's tensors
-  CHK_TOKEN_ID = 5, CHK_POSITION = 6, CHK_TARGET = 7
+  CHK_TOKEN_ID = 5, CHK_POSITION = 6, CHK_TARGET = 7, CHK_LENGTH = 8
 };
 // The fixed dQ order of a block runs as k = deterministic interleaved chains (1 <= k <=
 // kDqChains): contribution o adds, in order, into accumulator copy o % k after

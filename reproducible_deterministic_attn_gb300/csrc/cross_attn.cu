@@ -1,0 +1,393 @@
+// Host side of cross attention (dash_cross_attn_*): argument checks, how the work is cut, tensor
+// maps and launches. The kernels are in cross_fwd.cuh and cross_bwd.cuh.
+#include <algorithm>
+#include <climits>
+
+#include "cross_bwd.cuh"
+#include "cross_fwd.cuh"
+#include "dash_train.h"
+#include "host_common.h"
+
+namespace {
+
+using namespace dash;
+using namespace dash::cross;
+
+// Work is cut for a chip of 152 SMs whatever the device has, so that equal arguments give equal
+// bits everywhere.
+constexpr int kChip = 152;
+
+bool sizes_ok(int B, int Sq, int Sk, int Hq, int Hk, int D) {
+  return B >= 1 && Sq >= 0 && Sk >= 0 && Hq >= 1 && Hk >= 1 && Hq % Hk == 0 && D >= 8 && D <= 128 && D % 8 == 0 &&
+         B <= (1 << 20) && Hq <= (1 << 16) && Sq <= (1 << 24) && Sk <= (1 << 24) &&
+         (long long)B * Hq * std::max(Sq, Sk) < (1ll << 31) - 256;
+}
+
+Shape make_shape(int B, int Sq, int Sk, int Hq, int Hk, int D, bool may_pack) {
+  Shape s = {};
+  s.B = B;
+  s.Sq = Sq;
+  s.Sk = Sk;
+  s.Hq = Hq;
+  s.Hk = Hk;
+  s.g = Hq / Hk;
+  s.D = D;
+  s.nk = ceil_div(Sk, kTile);
+  s.tpt = kTile;
+  s.nq = ceil_div(Sq, kTile);
+  s.ntile = s.nq * s.g;
+  // all heads of a group in one row tile where that takes fewer tiles: 7 sequences' single tokens
+  // with 4 heads a group are 56 tiles, not 224
+  if (may_pack && s.g > 1 && s.g <= kTile) {
+    const int tpt = kTile / s.g, n = ceil_div(Sq, tpt);
+    if (n < s.ntile) {
+      s.packed = 1;
+      s.tpt = tpt;
+      s.nq = s.ntile = n;
+    }
+  }
+  return s;
+}
+
+// Key ranges of the forward.
+struct FwdPlan {
+  int pairs, splits, kper;
+  size_t part_o, part_l, total;      // workspace offsets and size
+};
+FwdPlan fwd_plan(const Shape& s) {
+  FwdPlan p;
+  p.pairs = ceil_div(s.ntile, 2);
+  const long long units = (long long)s.B * s.Hk * p.pairs;
+  p.splits = 1;
+  p.kper = std::max(1, s.nk);
+  if (units > 0 && units * 2 <= kChip && s.nk > 1) {
+    p.splits = (int)std::min<long long>(s.nk, kChip / units);
+    p.kper = ceil_div(s.nk, p.splits);
+    p.splits = ceil_div(s.nk, p.kper);
+  }
+  const size_t rows = p.splits > 1 ? (size_t)p.splits * s.B * s.Hk * s.ntile * kTile : 0;
+  p.part_o = kWsHeaderBytes;
+  p.part_l = p.part_o + rows * (s.D <= 64 ? 64 : 128) * sizeof(float);
+  p.total = round_up_to(p.part_l + rows * sizeof(float), 256);
+  return p;
+}
+
+// {D, H, S, B} with element strides st = {batch, token, head}; dimensions of one place have one
+// element and the coordinate 0.
+bool map_heads(CUtensorMap* m, const void* ptr, int B, int S, int H, int D, const long long* st, int box_heads,
+               int box_tokens) {
+  const cuuint64_t pitch = (cuuint64_t)D * 2;
+  const bool one_h = H == 1 || st[2] == 0, one_s = S == 1, one_b = B == 1 || st[0] == 0;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(one_h ? 1 : H), (cuuint64_t)S, (cuuint64_t)(one_b ? 1 : B)};
+  const cuuint64_t strides[3] = {one_h ? pitch : (cuuint64_t)st[2] * 2, one_s ? pitch : (cuuint64_t)st[1] * 2,
+                                 one_b ? pitch : (cuuint64_t)st[0] * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return dash::tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides,
+                                    box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Element strides {batch, token, head} of a tensor that is read.
+bool strides_ok(const long long* st, int S) {
+  for (int i = 0; i < 3; ++i)
+    if (st[i] < 0 || st[i] % 8 || st[i] > (1ll << 38)) return false;
+  return S < 2 || st[1] > 0;
+}
+
+dash_status_t check(const void* q, const void* k, const void* v, const void* lens, const void* o, const float* lse,
+                    int B, int Sq, int Sk, int Hq, int Hk, int D, const long long* qs, const long long* ks,
+                    const long long* vs, float scale, int id_bits) {
+  if (B < 0 || Sq < 0 || Sk < 0 || Hq < 1 || Hk < 1 || D < 1 || Hq % Hk) return DASH_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale <= 3.4e38f)) return DASH_ERR_INVALID_ARG;
+  if (id_bits != 32 && id_bits != 64) return DASH_ERR_INVALID_ARG;
+  if (B > 0 && !sizes_ok(B, Sq, Sk, Hq, Hk, D)) return DASH_ERR_UNSUPPORTED;
+  if (!qs || !ks || !vs) return DASH_ERR_INVALID_ARG;
+  if (!strides_ok(qs, Sq) || !strides_ok(ks, Sk) || !strides_ok(vs, Sk)) return DASH_ERR_UNSUPPORTED;
+  const bool rows = (long long)B * Sq > 0, keys = (long long)B * Sk > 0;
+  if ((rows && (!q || !o || !lse)) || (keys && (!k || !v))) return DASH_ERR_INVALID_ARG;
+  if (!is_aligned(q, 16) || !is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(o, 16) || !is_aligned(lse, 4) ||
+      !is_aligned(lens, id_bits / 8))
+    return DASH_ERR_INVALID_ARG;
+  if (!dash::tensor_map_encoder()) {
+    dash::set_last_error("cuTensorMapEncodeTiled is not available from the driver");
+    return DASH_ERR_CUDA;
+  }
+  return DASH_OK;
+}
+
+dash_status_t bad_map() {
+  dash::set_last_error("cuTensorMapEncodeTiled rejected a tensor");
+  return DASH_ERR_CUDA;
+}
+
+dash_status_t sm_count(int* sms) {
+  int dev = 0;
+  DASH_TRY(cudaGetDevice(&dev));
+  DASH_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  return DASH_OK;
+}
+
+// Shared memory of a kernel that moves registers between its warpgroups: their shares add up to
+// what it was launched with only if it was built with exactly that count.
+dash_status_t prepare(const void* kernel, int smem, int regs) {
+  cudaFuncAttributes fa;
+  DASH_TRY(cudaFuncGetAttributes(&fa, kernel));
+  if (fa.numRegs != regs) {
+    dash::set_last_error("cross attention kernel was not built with the register count its warp roles share");
+    return DASH_ERR_CUDA;
+  }
+  DASH_TRY(dash::allow_shared(kernel, smem));
+  return DASH_OK;
+}
+
+// A tensor without elements still needs a map: any readable place will do, as no tile is loaded.
+bool make_maps(Maps* m, const Shape& s, const void* q, const void* k, const void* v, const long long* qs,
+               const long long* ks, const long long* vs) {
+  const int bh = s.packed ? s.g : 1, bt = s.packed ? s.tpt : kTile;
+  if (!map_heads(&m->q, q, s.B, s.Sq, s.Hq, s.D, qs, bh, bt)) return false;
+  if (s.Sk == 0) return true;
+  return map_heads(&m->k, k, s.B, s.Sk, s.Hk, s.D, ks, 1, kTile) &&
+         map_heads(&m->v, v, s.B, s.Sk, s.Hk, s.D, vs, 1, kTile);
+}
+
+void set_places(Shape* s, const long long* qs, const long long* ks, const long long* vs) {
+  s->q_b = qs[0] != 0;
+  s->q_h = qs[2] != 0;
+  s->k_b = ks[0] != 0;
+  s->k_h = ks[2] != 0;
+  s->v_b = vs[0] != 0;
+  s->v_h = vs[2] != 0;
+}
+
+template <int DT>
+dash_status_t launch_fwd(FwdArgs a, const Maps& maps, cudaStream_t stream) {
+  const dash_status_t st = prepare((const void*)cross_fwd_kernel<DT>, FwdLay<DT>::ALLOC, kFwdRegsLaunch);
+  if (st != DASH_OK) return st;
+  int sms = 0;
+  if (const dash_status_t e = sm_count(&sms)) return e;
+  cross_fwd_kernel<DT><<<std::min(a.units, sms), kFwdThreads, FwdLay<DT>::ALLOC, stream>>>(a, maps);
+  DASH_TRY(cudaGetLastError());
+  if (a.splits > 1) {
+    const long long rows = (long long)a.s.B * a.s.Hk * a.s.ntile * kTile;
+    DASH_TRY(dash::launch_after(cross_join_kernel<DT>, dim3((unsigned)ceil_div<long long>(rows, 8)), 256, 0, stream, a));
+  }
+  return DASH_OK;
+}
+
+// Strides of a tensor to write: no two of its elements in one place by a stride of zero.
+bool distinct(const long long* st, int B, int S, int H) {
+  return (B < 2 || st[0] > 0) && (S < 2 || st[1] > 0) && (H < 2 || st[2] > 0);
+}
+
+// How the backward is cut: row segments and key segments of a group. Every cut costs partials
+// (written and read once more) and the start of another unit, too few leave SMs idle, so the plan
+// is the cheapest by a count of tasks: a unit takes its tasks, one more for each key tile (the
+// read-out of dK and dV) and two to start; units run in rounds of the chip; partials cost what
+// memory takes for them (a task is about 3 us, in which the chip moves 15 MB). A segment has at
+// most 128 row tiles: the tensor core truncates its additions, which over 16384 rows of one sign
+// loses at most 2^-15.5 of a sum.
+struct BwdPlan {
+  int qsegs, qper, ksegs, kper;
+  size_t nnl, delta, dq_acc, dkv_part, total;
+};
+BwdPlan bwd_plan(const Shape& s) {
+  BwdPlan p = {};
+  const long long groups = (long long)s.B * s.Hk;
+  const int nt = s.ntile, nk = s.nk, dt = s.D <= 64 ? 64 : 128;
+  p.kper = std::max(1, nk);
+  p.qper = std::max(1, nt);
+  if (nt > 0 && nk > 0) {
+    double best = 1e300;
+    const int most = (int)std::min<long long>(nt, ceil_div(nt, 128) + 2 * kChip / std::min<long long>(groups, 2 * kChip));
+    for (int qs = ceil_div(nt, 128); qs <= most; ++qs) {
+      const int qper = ceil_div(nt, qs);
+      if (ceil_div(nt, qper) != qs) continue;
+      for (int ks = 1; ks <= nk; ks = ks < nk && 2 * ks > nk ? nk : 2 * ks) {
+        const int kper = ceil_div(nk, ks);
+        if (ceil_div(nk, kper) != ks) continue;
+        if (ks > 1 && groups * qs * ks > 16 * kChip) break;
+        const long long units = groups * qs * ks;
+        const double rounds = (double)ceil_div<long long>(units, kChip);
+        const double unit = (double)kper * (qper + 1) + 2;
+        const double rows = (double)groups * nt * kTile * dt * 4, keys = (double)groups * nk * kTile * dt * 8;
+        const double bytes = (qs > 1 ? 2 * qs * keys : 0) + (ks > 1 ? 2 * ks * rows : 0);
+        // few units run with what they have: the chip's last round is not cut finer than a unit
+        const double cost = std::max(rounds * unit, (double)units * unit / kChip) + bytes / 15e6 + (qs > 1 || ks > 1);
+        if (cost < best) {
+          best = cost;
+          p.qsegs = qs;
+          p.qper = qper;
+          p.ksegs = ks;
+          p.kper = kper;
+        }
+      }
+    }
+  } else {
+    p.qsegs = nt > 0 ? 1 : 0;                      // no units; dk and dv (or dq) are zeros
+    p.ksegs = 1;
+  }
+  const size_t rows = (size_t)groups * nt * kTile;
+  p.nnl = kWsHeaderBytes;
+  p.delta = p.nnl + rows * sizeof(float);
+  p.dq_acc = round_up_to(p.delta + rows * sizeof(float), 256);
+  p.dkv_part = p.dq_acc + (p.kper > 1 || p.ksegs > 1 ? p.ksegs * rows * dt * sizeof(float) : 0);
+  p.total = p.dkv_part + (p.qsegs > 1 ? (size_t)p.qsegs * groups * nk * 2 * kTile * dt * sizeof(float) : 0);
+  p.total = round_up_to(std::max(p.total, kWsHeaderBytes), 256);
+  return p;
+}
+
+template <int DT>
+dash_status_t launch_bwd(BwdArgs a, const Maps& maps, cudaStream_t stream) {
+  int sms = 0;
+  if (const dash_status_t e = sm_count(&sms)) return e;
+  if (a.units > 0) {
+    const dash_status_t st = prepare((const void*)cross_bwd_kernel<DT>, BwdLay<DT>::ALLOC, BwdLay<DT>::REGS_LAUNCH);
+    if (st != DASH_OK) return st;
+  }
+  const long long rows = (long long)a.s.B * a.s.Hk * a.s.ntile * kTile;
+  cross_pre_kernel<<<(unsigned)std::max(1ll, ceil_div<long long>(rows, 16)), 256, 0, stream>>>(a);
+  DASH_TRY(cudaGetLastError());
+  if (a.units > 0)
+    DASH_TRY(dash::launch_after(cross_bwd_kernel<DT>, dim3(std::min(a.units, sms)), kThreads, BwdLay<DT>::ALLOC,
+                                stream, a, maps));
+  if (a.s.lens || a.units == 0 || a.qsegs > 1 || a.ksegs > 1) {
+    const int per = a.s.D / 8;
+    const unsigned dqb = a.s.lens || a.units == 0 || a.ksegs > 1
+                             ? (unsigned)ceil_div<long long>((long long)a.s.B * a.s.Sq * a.s.Hq * per, 256) : 0;
+    const unsigned dkb = (unsigned)ceil_div<long long>((long long)a.s.B * a.s.Sk * a.s.Hk * per, 256);
+    if (dqb + dkb > 0)
+      DASH_TRY(dash::launch_after(cross_grad_join_kernel<DT>, dim3(dqb + dkb), 256, 0, stream, a, dqb));
+  }
+  return DASH_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dash_cross_attn_fwd_workspace_size(int B, int Sq, int Sk, int Hq, int Hk, int D) {
+  if (!sizes_ok(B, Sq, Sk, Hq, Hk, D)) return 0;
+  return std::max(fwd_plan(make_shape(B, Sq, Sk, Hq, Hk, D, true)).total,
+                  fwd_plan(make_shape(B, Sq, Sk, Hq, Hk, D, false)).total);
+}
+
+dash_status_t dash_cross_attn_fwd(const void* q, const void* k, const void* v, const void* kv_lens, void* o,
+                                  float* lse, int* status, void* workspace, size_t workspace_bytes, int B, int Sq,
+                                  int Sk, int Hq, int Hk, int D, const long long* q_strides,
+                                  const long long* k_strides, const long long* v_strides, float scale, int id_bits,
+                                  cudaStream_t stream) {
+  const dash_status_t st = check(q, k, v, kv_lens, o, lse, B, Sq, Sk, Hq, Hk, D, q_strides, k_strides, v_strides,
+                                 scale, id_bits);
+  if (st != DASH_OK) return st;
+  if (!is_aligned(status, 4) || !is_aligned(workspace, 256)) return DASH_ERR_INVALID_ARG;
+  FwdArgs a = {};
+  a.s = make_shape(B, Sq, Sk, Hq, Hk, D, q_strides[2] != 0);
+  a.s.lens = kv_lens;
+  a.s.id_bits = id_bits;
+  set_places(&a.s, q_strides, k_strides, v_strides);
+  const FwdPlan pl = fwd_plan(a.s);
+  if (pl.splits > 1) {
+    if (!workspace) return DASH_ERR_INVALID_ARG;
+    if (workspace_bytes < pl.total) return DASH_ERR_WORKSPACE_TOO_SMALL;
+    a.part_o = (float*)((char*)workspace + pl.part_o);
+    a.part_l = (float*)((char*)workspace + pl.part_l);
+  }
+  a.o = (__nv_bfloat16*)o;
+  a.lse = lse;
+  a.pairs = pl.pairs;
+  a.splits = pl.splits;
+  a.kper = pl.kper;
+  const long long units = (long long)B * Hk * pl.pairs * pl.splits;
+  a.units = (int)units;
+  a.scale_log2 = scale * kLog2e;
+  a.status = status;
+  a.timeout_ns = sync_timeout_ns();
+  a.withhold = sync_withheld();
+  if (status) DASH_TRY(cudaMemsetAsync(status, 0, sizeof(int), stream));
+  if ((long long)B * Sq == 0) return DASH_OK;
+  Maps maps;
+  if (!make_maps(&maps, a.s, q, k, v, q_strides, k_strides, v_strides)) return bad_map();
+  return D <= 64 ? launch_fwd<64>(a, maps, stream) : launch_fwd<128>(a, maps, stream);
+}
+
+size_t dash_cross_attn_bwd_workspace_size(int B, int Sq, int Sk, int Hq, int Hk, int D) {
+  if (!sizes_ok(B, Sq, Sk, Hq, Hk, D)) return 0;
+  return std::max(bwd_plan(make_shape(B, Sq, Sk, Hq, Hk, D, true)).total,
+                  bwd_plan(make_shape(B, Sq, Sk, Hq, Hk, D, false)).total);
+}
+
+dash_status_t dash_cross_attn_bwd(const void* q, const void* k, const void* v, const void* kv_lens, const void* o,
+                                  const void* d_o, const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                                  size_t workspace_bytes, int B, int Sq, int Sk, int Hq, int Hk, int D,
+                                  const long long* q_strides, const long long* k_strides,
+                                  const long long* v_strides, const long long* dq_strides,
+                                  const long long* dk_strides, const long long* dv_strides, float scale,
+                                  int id_bits, cudaStream_t stream) {
+  const dash_status_t st = check(q, k, v, kv_lens, o, lse, B, Sq, Sk, Hq, Hk, D, q_strides, k_strides, v_strides,
+                                 scale, id_bits);
+  if (st != DASH_OK) return st;
+  if (!dq_strides || !dk_strides || !dv_strides || !workspace) return DASH_ERR_INVALID_ARG;
+  if (!strides_ok(dq_strides, Sq) || !strides_ok(dk_strides, Sk) || !strides_ok(dv_strides, Sk))
+    return DASH_ERR_UNSUPPORTED;
+  if (!distinct(dq_strides, B, Sq, Hq) || !distinct(dk_strides, B, Sk, Hk) || !distinct(dv_strides, B, Sk, Hk))
+    return DASH_ERR_INVALID_ARG;
+  if (((long long)B * Sq > 0 && (!d_o || !dq)) || ((long long)B * Sk > 0 && (!dk || !dv))) return DASH_ERR_INVALID_ARG;
+  for (const void* t : {d_o, (const void*)dq, (const void*)dk, (const void*)dv})
+    if (!is_aligned(t, 16)) return DASH_ERR_INVALID_ARG;
+  if (!is_aligned(workspace, 256)) return DASH_ERR_INVALID_ARG;
+  if (workspace_bytes < kWsHeaderBytes) return DASH_ERR_WORKSPACE_TOO_SMALL;
+  if (B == 0) {
+    DASH_TRY(cudaMemsetAsync(workspace, 0, kWsHeaderBytes, stream));
+    return DASH_OK;
+  }
+  BwdArgs a = {};
+  a.s = make_shape(B, Sq, Sk, Hq, Hk, D, q_strides[2] != 0);
+  a.s.lens = kv_lens;
+  a.s.id_bits = id_bits;
+  set_places(&a.s, q_strides, k_strides, v_strides);
+  const BwdPlan pl = bwd_plan(a.s);
+  if (workspace_bytes < pl.total) return DASH_ERR_WORKSPACE_TOO_SMALL;
+  char* ws = (char*)workspace;
+  a.header = (int*)ws;
+  a.nnl = (float*)(ws + pl.nnl);
+  a.delta = (float*)(ws + pl.delta);
+  a.dq_acc = (float*)(ws + pl.dq_acc);
+  a.dkv_part = (float*)(ws + pl.dkv_part);
+  a.o = (const __nv_bfloat16*)o;
+  a.dO = (const __nv_bfloat16*)d_o;
+  a.lse = lse;
+  a.dq = (__nv_bfloat16*)dq;
+  a.dk = (__nv_bfloat16*)dk;
+  a.dv = (__nv_bfloat16*)dv;
+  a.dq_b = dq_strides[0];
+  a.dq_s = dq_strides[1];
+  a.dq_h = dq_strides[2];
+  a.dk_b = dk_strides[0];
+  a.dk_s = dk_strides[1];
+  a.dk_h = dk_strides[2];
+  a.dv_b = dv_strides[0];
+  a.dv_s = dv_strides[1];
+  a.dv_h = dv_strides[2];
+  a.qsegs = pl.qsegs;
+  a.qper = pl.qper;
+  a.ksegs = pl.ksegs;
+  a.kper = pl.kper;
+  a.units = (int)((long long)B * Hk * pl.qsegs * pl.ksegs);
+  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
+  a.timeout_ns = sync_timeout_ns();
+  a.withhold = sync_withheld();
+  Maps maps;
+  if (a.units > 0) {
+    const long long os[3] = {(long long)Sq * Hq * D, (long long)Hq * D, (long long)D};
+    const int bh = a.s.packed ? a.s.g : 1, bt = a.s.packed ? a.s.tpt : kTile;
+    if (!make_maps(&maps, a.s, q, k, v, q_strides, k_strides, v_strides) ||
+        !map_heads(&maps.dO, d_o, B, Sq, Hq, D, os, bh, bt))
+      return bad_map();
+  }
+  return D <= 64 ? launch_bwd<64>(a, maps, stream) : launch_bwd<128>(a, maps, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,128 @@
+// Cross attention (dash_cross_attn_*): what the forward and the backward share.
+//
+// Queries [B, Sq, Hq, D] look at keys [B, Sk, Hk, D] of another length, of which batch b has the
+// first len_b. The g = Hq / Hk query heads that share a key head form a group; the query rows of
+// a group are cut into row tiles of up to 128 rows, one TMEM lane each. A row tile is 128
+// consecutive tokens of one head, or (packed, chosen where it takes fewer tiles, as for single
+// tokens) 128 / g consecutive tokens with all g heads: row = token * g + head, which a 4-D tensor
+// map loads as one box. Tensors are read through 4-D maps {D, head, token, batch}, so rows and
+// columns beyond a tensor's extent arrive as zeros and strides need only be multiples of 16 bytes.
+#pragma once
+
+#include "tc_shared.cuh"
+#include "train_common.cuh"
+
+namespace dash {
+namespace cross {
+
+using namespace dash::tc;
+
+struct Shape {
+  int B, Sq, Sk, Hq, Hk, g, D;
+  int packed;                // row tiles hold all heads of a group
+  int tpt;                   // tokens of a row tile (128, or 128 / g when packed)
+  int nq;                    // row tiles along the tokens
+  int ntile;                 // row tiles of a group: nq, times g when not packed
+  int nk;                    // key tiles of 128
+  // 1, or 0 where a tensor's batches or heads lie in one place (a stride of zero)
+  int q_b, q_h, k_b, k_h, v_b, v_h;
+  const void* lens;          // [B], or null: every length is Sk
+  int id_bits;
+};
+
+struct Maps {
+  CUtensorMap q, k, v, dO;   // 4-D bf16 {D, H, S, B}
+};
+
+// The batch's number of keys; -1 when it is out of range (treated as none).
+__device__ __forceinline__ int length_of(const Shape& s, int b) {
+  if (!s.lens) return s.Sk;
+  const long long n = train::load_index(s.lens, b, s.id_bits);
+  return n >= 0 && n <= s.Sk ? (int)n : -1;
+}
+
+// Row r of row tile t of a group: its token and its head within the group; false where the tile
+// has no such row.
+__device__ __forceinline__ bool row_of(const Shape& s, int t, int r, int& token, int& head) {
+  if (s.packed) {
+    const int i = r / s.g;
+    token = t * s.tpt + i;
+    head = r - i * s.g;
+    return i < s.tpt && token < s.Sq;
+  }
+  head = t / s.nq;
+  token = (t - head * s.nq) * kTile + r;
+  return token < s.Sq;
+}
+
+// Loads the 64-column blocks of row tile t into shared memory, `rows` of 128 bytes each.
+template <int DT>
+__device__ __forceinline__ uint32_t row_tile_bytes(const Shape& s) {
+  return (uint32_t)(DT / 64) * 128u * (s.packed ? (uint32_t)(s.g * s.tpt) : (uint32_t)kTile);
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(ptx::smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+template <int DT>
+__device__ __forceinline__ void load_row_tile(const Shape& s, const CUtensorMap* map, uint8_t* dst, int b, int hk,
+                                              int t, int mul_b, int mul_h, uint64_t* bar) {
+  int head = 0, token = t * s.tpt;
+  if (!s.packed) {
+    head = t / s.nq;
+    token = (t - head * s.nq) * kTile;
+  }
+#pragma unroll
+  for (int cb = 0; cb < DT / 64; ++cb)
+    tma_load_4d(dst + cb * kTile * 128, map, cb * 64, (hk * s.g + head) * mul_h, token, b * mul_b, bar);
+}
+template <int DT>
+__device__ __forceinline__ void load_key_tile(const CUtensorMap* map, uint8_t* dst, int b, int hk, int t, int mul_b,
+                                              int mul_h, uint64_t* bar) {
+#pragma unroll
+  for (int cb = 0; cb < DT / 64; ++cb)
+    tma_load_4d(dst + cb * kTile * 128, map, cb * 64, hk * mul_h, t * kTile, b * mul_b, bar);
+}
+
+// Zeroes rows [from, to) of a tile in shared memory (one warp): keys that a length leaves out may
+// hold anything, and 0 * NaN in a product over the keys would be NaN.
+template <int DT>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int to, int lane) {
+  const int pieces = (to - from) * 8;              // of 16 bytes, in each 64-column block
+#pragma unroll
+  for (int cb = 0; cb < DT / 64; ++cb)
+    for (int i = lane; i < pieces; i += 32)
+      reinterpret_cast<uint4*>(tile + cb * kTile * 128 + from * 128)[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// 32 bytes of a row in one store where its address allows it: a whole sector.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// 32 values times f as bf16 to columns [0, n) of dst, n a multiple of 8 (n <= 0: none).
+__device__ __forceinline__ void store_bf16_32(__nv_bfloat16* dst, const float (&v)[32], float f, int n) {
+  const bool wide = ((uintptr_t)dst & 31) == 0;
+#pragma unroll
+  for (int c = 0; c < 32; c += 16) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16(v[c + 2 * i] * f, v[c + 2 * i + 1] * f);
+    if (c + 16 <= n) store32(dst + c, w, wide);
+    else if (c < n) *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+}  // namespace cross
+}  // namespace dash

@@ -622,11 +622,11 @@ dash_status_t dash_attn_get_status(const void* workspace, cudaStream_t stream) {
   }
   if (words[dash::WS_STATUS] == dash::kStatusBounds) {
     static const char* const sites[] = {"?", "a CTA's piece range", "a piece", "a task",
-                                         "a dQ ordinal", "a token id", "a position", "a target"};
+                                         "a dQ ordinal", "a token id", "a position", "a target", "a length"};
     const int site = words[dash::WS_QTILE];
     char buf[200];
     snprintf(buf, sizeof(buf), "bounds check failed on %s: %s=%d value=%d bound=%d",
-             sites[site >= 1 && site <= dash::CHK_TARGET ? site : 0],
+             sites[site >= 1 && site <= dash::CHK_LENGTH ? site : 0],
              site >= dash::CHK_TOKEN_ID ? "row" : "bh/cta", words[dash::WS_BH],
              words[dash::WS_EXPECT], words[dash::WS_SEEN]);
     g_last_error = buf;

@@ -53,6 +53,10 @@ _core._SIGNATURES.update({
                                                   _c_int, _vp]),
     "dash_linear_xent_bwd": (_c_int, [_vp] * 8 + [_c_size, _ll, _ll, _c_int, _ll, _ll, _c_float, _ll,
                                                   _c_int, _c_int, _c_int, _vp]),
+    "dash_cross_attn_fwd_workspace_size": (_c_size, [_c_int] * 6),
+    "dash_cross_attn_fwd": (_c_int, [_vp] * 8 + [_c_size] + [_c_int] * 6 + [_vp] * 3 + [_c_float, _c_int, _vp]),
+    "dash_cross_attn_bwd_workspace_size": (_c_size, [_c_int] * 6),
+    "dash_cross_attn_bwd": (_c_int, [_vp] * 11 + [_c_size] + [_c_int] * 6 + [_vp] * 6 + [_c_float, _c_int, _vp]),
 })
 
 
@@ -540,3 +544,113 @@ def linear_xent_backward(x, w, targets, lse, dloss, ignore_index: int = -100, sc
         "dash_linear_xent_bwd")
     _finish(workspace, check, "dash_linear_xent_bwd")
     return dx, dw
+
+
+# ---- cross attention ----------------------------------------------------------------------------
+
+def dash_cross_attn_fwd_workspace_size(B: int, Sq: int, Sk: int, Hq: int, Hk: int, D: int) -> int:
+    return int(_core.load().dash_cross_attn_fwd_workspace_size(B, Sq, Sk, Hq, Hk, D))
+
+
+def dash_cross_attn_bwd_workspace_size(B: int, Sq: int, Sk: int, Hq: int, Hk: int, D: int) -> int:
+    return int(_core.load().dash_cross_attn_bwd_workspace_size(B, Sq, Sk, Hq, Hk, D))
+
+
+def new_cross_attn_workspace(B: int, Sq: int, Sk: int, Hq: int, Hk: int, D: int, device,
+                             forward_only: bool = False) -> torch.Tensor:
+    """A workspace of cross_attn_forward and, unless forward_only, of cross_attn_backward (uint8)."""
+    nbytes = dash_cross_attn_fwd_workspace_size(B, Sq, Sk, Hq, Hk, D)
+    if nbytes and not forward_only:
+        nbytes = max(nbytes, dash_cross_attn_bwd_workspace_size(B, Sq, Sk, Hq, Hk, D))
+    if nbytes == 0:
+        raise DashError(DASH_ERR_UNSUPPORTED, "dash_cross_attn_fwd_workspace_size")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _cross_args(q, k, v, kv_lens):
+    dev = _device(q, "q")
+    if q.dtype != _BF16:
+        _bad("q: expected bfloat16")
+    B, Sq, Hq, D, qs = _heads(q, "q", _BF16, dev)
+    Bk, Sk, Hk, Dk, ks = _heads(k, "k", _BF16, dev)
+    Bv, Sv, Hv, Dv, vs = _heads(v, "v", _BF16, dev)
+    if Bk != B or Dk != D or Hk < 1 or Hq % Hk:
+        _bad("k: expected [B, Sk, Hk, D] with the B and D of q and a divisor of its heads")
+    if (Bv, Sv, Hv, Dv) != (Bk, Sk, Hk, Dk):
+        _bad("v: expected the shape of k")
+    lens, bits = None, 32
+    if kv_lens is not None:
+        bits = _index(kv_lens, "kv_lens", dev)
+        if kv_lens.dim() != 1 or kv_lens.numel() != B:
+            _bad("kv_lens: expected one length a batch")
+        lens = kv_lens.data_ptr()
+    return dev, lens, bits, (B, Sq, Sk, Hq, Hk, D), (qs, ks, vs)
+
+
+def cross_attn_forward(q, k, v, scale: float, kv_lens=None, workspace=None, status=None, stream=None):
+    """Attention of queries to the keys and values of states of another length.
+
+    q: bf16 [B, Sq, Hq, D]; k, v: bf16 [B, Sk, Hk, D], Hk a divisor of Hq, D contiguous, any strides
+    that are multiples of 8 (parts of a fused projection, transposed [B, H, S, D], expanded batches
+    or heads). kv_lens: int [B], how many of the Sk keys each batch has (None: all; 0: its rows are
+    O = 0, LSE = -inf); what lies behind them is never used. status as in embed_forward: it reads
+    DASH_ERR_BOUNDS when a length was out of range (its rows are NaN). Returns (o, lse): contiguous
+    bf16 [B, Sq, Hq, D] and fp32 [B, Hq, Sq]."""
+    if stream is not None:
+        with _using(stream, q):
+            return cross_attn_forward(q, k, v, scale, kv_lens, workspace, status)
+    dev, lens, bits, sizes, held = _cross_args(q, k, v, kv_lens)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return cross_attn_forward(q, k, v, scale, kv_lens, workspace, status)
+    o = torch.empty(q.shape, dtype=_BF16, device=q.device)
+    lse = torch.empty((sizes[0], sizes[3], sizes[1]), dtype=_F32, device=q.device)
+    if workspace is None and o.numel():
+        workspace = new_cross_attn_workspace(*sizes, q.device, forward_only=True)
+    ws, nbytes = (None, 0) if workspace is None else _ws(workspace, dev)
+    _raise(_core.load().dash_cross_attn_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, o.data_ptr(), lse.data_ptr(), _status_word(status, dev), ws,
+        nbytes, *sizes, held[0][1], held[1][1], held[2][1], scale, bits, _stream(dev)), "dash_cross_attn_fwd")
+    return o, lse
+
+
+def cross_attn_backward(q, k, v, o, do, lse, scale: float, kv_lens=None, dq=None, dk=None, dv=None, workspace=None,
+                        stream=None, check: bool = True):
+    """Gradients of cross_attn_forward with respect to q, k and v.
+
+    o and lse as the forward returned them, do contiguous like o. dq, dk, dv: optional tensors to
+    write to, strided like q, k and v may be (parts of a fused projection's gradient), without
+    strides of zero. Rows of dk and dv behind a length are zero. Returns (dq, dk, dv)."""
+    if stream is not None:
+        with _using(stream, q):
+            return cross_attn_backward(q, k, v, o, do, lse, scale, kv_lens, dq, dk, dv, workspace, check=check)
+    dev, lens, bits, sizes, held = _cross_args(q, k, v, kv_lens)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return cross_attn_backward(q, k, v, o, do, lse, scale, kv_lens, dq, dk, dv, workspace, check=check)
+    for t, name in ((o, "o"), (do, "do")):
+        if t.dtype != _BF16 or t.shape != q.shape or not t.is_contiguous() or t.get_device() != dev:
+            _bad(f"{name}: expected contiguous bfloat16 of the shape of q on cuda:{dev}")
+    if (lse.dtype != _F32 or lse.shape != (sizes[0], sizes[3], sizes[1]) or not lse.is_contiguous()
+            or lse.get_device() != dev):
+        _bad(f"lse: expected contiguous float32 [B, Hq, Sq] on cuda:{dev}")
+    dq = torch.empty(q.shape, dtype=_BF16, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=_BF16, device=q.device) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=_BF16, device=q.device) if dv is None else dv
+    outs = [_heads(t, n, _BF16, dev) for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv"))]
+    if outs[0][:4] != q.shape or outs[1][:4] != k.shape or outs[2][:4] != v.shape:
+        _bad("dq, dk and dv: expected the shapes of q, k and v")
+    if workspace is None:
+        if not q.numel() and not k.numel():
+            return dq, dk, dv
+        nbytes = dash_cross_attn_bwd_workspace_size(*sizes)
+        if nbytes == 0:
+            raise DashError(DASH_ERR_UNSUPPORTED, "dash_cross_attn_bwd_workspace_size")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    ws, nbytes = _ws(workspace, dev)
+    _raise(_core.load().dash_cross_attn_bwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, o.data_ptr(), do.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), ws, nbytes, *sizes, held[0][1], held[1][1], held[2][1], outs[0][4][1],
+        outs[1][4][1], outs[2][4][1], scale, bits, _stream(dev)), "dash_cross_attn_bwd")
+    _finish(workspace, check, "dash_cross_attn_bwd")
+    return dq, dk, dv

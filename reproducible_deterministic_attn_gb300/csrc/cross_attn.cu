@@ -254,8 +254,8 @@ dash_status_t launch_bwd(BwdArgs a, const Maps& maps, cudaStream_t stream) {
                                 stream, a, maps));
   if (a.s.lens || a.units == 0 || a.qsegs > 1 || a.ksegs > 1) {
     const int per = a.s.D / 8;
-    const unsigned dqb = a.s.lens || a.units == 0 || a.ksegs > 1
-                             ? (unsigned)ceil_div<long long>((long long)a.s.B * a.s.Sq * a.s.Hq * per, 256) : 0;
+    const long long tiles = (long long)a.s.B * a.s.Hk * a.s.ntile;
+    const unsigned dqb = a.s.lens || a.units == 0 || a.ksegs > 1 ? (unsigned)tiles : 0;
     const unsigned dkb = (unsigned)ceil_div<long long>((long long)a.s.B * a.s.Sk * a.s.Hk * per, 256);
     if (dqb + dkb > 0)
       DASH_TRY(dash::launch_after(cross_grad_join_kernel<DT>, dim3(dqb + dkb), 256, 0, stream, a, dqb));

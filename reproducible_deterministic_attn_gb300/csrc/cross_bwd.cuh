@@ -41,7 +41,7 @@ struct BwdArgs {
   const float* lse;
   __nv_bfloat16 *dq, *dk, *dv;
   long long dq_b, dq_s, dq_h, dk_b, dk_s, dk_h, dv_b, dv_s, dv_h;
-  float* dq_acc;             // [key segment][group][tile][128][DT]
+  float* dq_acc;             // [key segment][group][tile][32][DT][4]: rows in fours, of each column
   float* dkv_part;           // [row segment][group][key tile][dK, dV][128][DT]
   int qsegs, qper, ksegs, kper;
   int units;
@@ -58,16 +58,19 @@ struct BwdLay {
   static constexpr int OFFS = 2 * kTile * 4;                   // -LSE log2e and Delta of a row tile
   static constexpr int NQ = DT == 64 ? 3 : 2;
   static constexpr int K_OFF = 0, V_OFF = TILE, Q_OFF = 2 * TILE;
+  static constexpr int NDO = 2;
   static constexpr int DO_OFF = Q_OFF + NQ * TILE;
-  static constexpr int DS_OFF = DO_OFF + TILE;
+  static constexpr int DS_OFF = DO_OFF + NDO * TILE;
   // DT = 64: zeros after which K^T is padded to 128 rows, so that dQ^T is an M = 128 product
   static constexpr int ZERO_OFF = DS_OFF + DS_BYTES;
   static constexpr int ZERO_BYTES = DT == 64 ? TILE : 0;
   static constexpr int OFFS_OFF = ZERO_OFF + ZERO_BYTES;
   static constexpr int BAR_OFF = OFFS_OFF + NQ * OFFS;
-  static constexpr int ALLOC = BAR_OFF + 256 + 1024;
+  static constexpr int ALLOC = BAR_OFF + 256;                  // the base is 1024-aligned (checked)
   static_assert(ALLOC <= 232448, "shared memory budget");
-  static constexpr int T_SP = 0, T_DPQ = 128, T_DV = 256, T_DK = 256 + DT;
+  // DT = 64 leaves columns for dQ^T of its own; DT = 128 puts it where dP^T was
+  static constexpr bool kSepDQ = DT == 64;
+  static constexpr int T_SP = 0, T_DP = 128, T_DV = 256, T_DK = 256 + DT, T_DQ = kSepDQ ? 384 : T_DP;
   static constexpr int REGS_LAUNCH = 128, REGS_SINGLE = 88, REGS_READOUT = 168;
   static_assert(REGS_SINGLE + 2 * REGS_LAUNCH + REGS_READOUT == 4 * REGS_LAUNCH,
                 "the four warpgroups must share exactly the launch's registers");
@@ -75,7 +78,7 @@ struct BwdLay {
 
 enum {
   C_KV_FULL = 0, C_KV_READY, C_KV_EMPTY, C_Q_FULL, C_Q_EMPTY = C_Q_FULL + 3, C_DO_FULL = C_Q_EMPTY + 3,
-  C_DO_EMPTY, C_S_FULL, C_SP_FREE, C_P_FULL, C_DP_FULL, C_DS_FULL, C_DQ_FULL, C_DQ_EMPTY, C_ACC_FULL,
+  C_DO_EMPTY = C_DO_FULL + 2, C_S_FULL = C_DO_EMPTY + 2, C_SP_FREE, C_P_FULL, C_DP_FULL, C_DS_FULL, C_DQ_FULL, C_DQ_EMPTY, C_ACC_FULL,
   C_ACC_EMPTY, C_DRAIN, C_COUNT
 };
 static_assert(8 * C_COUNT + 8 <= 256, "barrier area");
@@ -137,6 +140,13 @@ __device__ __forceinline__ void issue_dq(uint32_t d, uint32_t& a, uint32_t& b, u
   }
 }
 
+__device__ __forceinline__ void ld_relaxed_v4(const float* p, float* v) {
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "l"(p)
+               : "memory");
+}
+
 // Delta = rowsum(dO * O) and -LSE log2e per row, in row tiles; 16 lanes a row. The first block
 // clears the workspace's header and looks for lengths out of range.
 __global__ void __launch_bounds__(256) cross_pre_kernel(const __grid_constant__ BwdArgs p) {
@@ -180,8 +190,8 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_bwd_kernel(const __grid_constant__ BwdArgs p, const __grid_constant__ Maps maps) {
   using L = BwdLay<DT>;
-  extern __shared__ uint8_t smem_crossb[];
-  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_crossb + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem_crossb[];
+  uint8_t* sm = smem_crossb;
   uint64_t* bars = (uint64_t*)(sm + L::BAR_OFF);
   uint32_t* tmem_slot = (uint32_t*)(sm + L::BAR_OFF + 8 * C_COUNT);
   volatile int* abort_flag = (volatile int*)(sm + L::BAR_OFF + 8 * C_COUNT + 4);
@@ -190,6 +200,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int dsteps = (p.s.D + 15) >> 4;
 
   train::grid_next();
+  // The layout fills most of the opt-in maximum, so there is no room to realign the base.
+  if (ptx::smem_u32(sm) & 1023u) {
+    train::grid_wait();
+    if (threadIdx.x == 0) atomicCAS(p.header + WS_STATUS, 0, kStatusSmemLayout);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int k = 0; k < C_COUNT; ++k) {
       const int n = k == C_P_FULL || k == C_DS_FULL ? 8 : k == C_DQ_EMPTY || k == C_ACC_EMPTY ? 4 : 1;
@@ -202,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *(uint4*)(sm + L::ZERO_OFF + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
   // packed row tiles may leave rows that no copy ever writes: zeros, as 0 * NaN would be NaN
   if (p.s.packed)
-    for (int e = threadIdx.x; e < (L::NQ + 1) * L::TILE / 16; e += blockDim.x)
+    for (int e = threadIdx.x; e < (L::NQ + L::NDO) * L::TILE / 16; e += blockDim.x)
       *(uint4*)(sm + L::Q_OFF + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
   ptx::fence_proxy_async_smem();
   if (warp == 1) ptx::tmem_alloc(tmem_slot, kTmemCols);
@@ -217,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
       // ===================================== TMA producer =====================================
       BwdWalk w(p);
-      int it = 0, tl = 0;
+      int it = 0, tl = 0, loaded = 0;              // tasks, key tiles, dO tiles
       bool ok = !p.withhold;
       while (ok && w.next()) {
         const int qb = it % L::NQ;
@@ -241,17 +257,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_key_tile<DT>(&maps.v, sm + L::V_OFF, w.b, w.hk, w.k0 + w.i, p.s.v_b, p.s.v_h, bars + C_KV_FULL);
           ++tl;
         }
-        if (it >= 1) ok = ptx::mbar_wait(bars + C_DO_EMPTY, (it - 1) & 1, abort_flag, tmo);
-        if (ok) {
-          ptx::mbar_expect_tx(bars + C_DO_FULL, row_tile_bytes<DT>(p.s));
-          load_row_tile<DT>(p.s, &maps.dO, sm + L::DO_OFF, w.b, w.hk, w.tile(), 1, 1, bars + C_DO_FULL);
+        const int ob = it % L::NDO;
+        if (it >= L::NDO) ok = ptx::mbar_wait(bars + C_DO_EMPTY + ob, (it / L::NDO - 1) & 1, abort_flag, tmo);
+        if (!ok) {
+          ++it;
+          break;
         }
+        ptx::mbar_expect_tx(bars + C_DO_FULL + ob, row_tile_bytes<DT>(p.s));
+        load_row_tile<DT>(p.s, &maps.dO, sm + L::DO_OFF + ob * L::TILE, w.b, w.hk, w.tile(), 1, 1,
+                          bars + C_DO_FULL + ob);
+        ++loaded;
         ++it;
+        // the unit's first pass over its rows finds them in memory: ask for the tiles after the
+        // buffered ones, so that they wait in L2
+        if (w.i == 0 && w.j + L::NDO < w.nqt) {
+          prefetch_row_tile<DT>(p.s, &maps.q, w.b, w.hk, w.tile() + L::NDO, p.s.q_b, p.s.q_h);
+          prefetch_row_tile<DT>(p.s, &maps.dO, w.b, w.hk, w.tile() + L::NDO, 1, 1);
+        }
       }
       // drain: every issued load has landed before the CTA may exit
       for (int k = max(0, it - L::NQ); k < it; ++k)
         ptx::mbar_drain(bars + C_Q_FULL + k % L::NQ, (k / L::NQ) & 1, 100000000ll);
-      if (it > 0) ptx::mbar_drain(bars + C_DO_FULL, (it - 1) & 1, 100000000ll);
+      for (int k = max(0, loaded - L::NDO); k < loaded; ++k)
+        ptx::mbar_drain(bars + C_DO_FULL + k % L::NDO, (k / L::NDO) & 1, 100000000ll);
       if (tl > 0) ptx::mbar_drain(bars + C_KV_FULL, (tl - 1) & 1, 100000000ll);
     } else if (warp == 2) {
       // ============================== key rows behind a length ================================
@@ -290,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, have = w.next(), s_done = false;   // s_done: S(it) was issued ahead
       while (ok && have) {
         const bool first = w.first_of_tile(), last = w.last_of_tile();
-        const int qb = it % L::NQ, ksteps = (w.keys() + 15) >> 4;
+        const int qb = it % L::NQ, ob = it % L::NDO, ksteps = (w.keys() + 15) >> 4;
         if (first) {
           ++tile;
           ok = ptx::mbar_wait(bars + C_KV_READY, tile & 1, abort_flag, tmo);
@@ -306,11 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mma_commit(bars + C_S_FULL);
         }
         // ---- dP^T(it), once dO(it) has landed and dQ^T(it-1) has left the columns they share
-        ok = ptx::mbar_wait(bars + C_DO_FULL, it & 1, abort_flag, tmo);
-        if (ok && it > 0) ok = ptx::mbar_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
+        ok = ptx::mbar_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
+        if (ok && !L::kSepDQ && it > 0) ok = ptx::mbar_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
         if (!ok) break;
         ptx::tc_fence_after();
-        issue_scores<DT>(tmem + L::T_DPQ, dV_k, ddO_k, ID_S, dsteps);
+        issue_scores<DT>(tmem + L::T_DP, dV_k, ddO_k + ob * BUF_STEP, ID_S, dsteps);
         ptx::mma_commit(bars + C_DP_FULL);
         // ---- dV += P^T dO, once P^T(it) is stored and the last key tile's sums were read out
         ok = ptx::mbar_wait(bars + C_P_FULL, it & 1, abort_flag, tmo);
@@ -318,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t acc0 = first ? 0u : 1u;
-        issue_ts(tmem + L::T_DV, tmem + L::T_SP, ddO_mn, id_ts, acc0);
-        ptx::mma_commit(bars + C_DO_EMPTY);
+        issue_ts(tmem + L::T_DV, tmem + L::T_SP, ddO_mn + ob * BUF_STEP, id_ts, acc0);
+        ptx::mma_commit(bars + C_DO_EMPTY + ob);
         have = w.next();
         // ---- dK += dS^T Q, then dQ^T = K^T dS^T, once dS^T(it) is stored
         ok = ptx::mbar_wait(bars + C_DS_FULL, it & 1, abort_flag, tmo);
@@ -331,8 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- S^T(it+1) of the same keys ahead of dQ^T(it) (DT = 64) or between its halves, so
         // that the softmax gradient has it earlier
         s_done = have && !w.first_of_tile();
+        if (L::kSepDQ && it > 0) ok = ptx::mbar_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
+        if (!ok) break;
         uint32_t dq_a = dKt_mn, dq_b = dDS_mn;
-        if (DT == 128 && s_done) issue_dq<0, 4>(tmem + L::T_DPQ, dq_a, dq_b, ID_DQ, ksteps);
+        if (DT == 128 && s_done) issue_dq<0, 4>(tmem + L::T_DQ, dq_a, dq_b, ID_DQ, ksteps);
         if (s_done) {
           const int qn = (it + 1) % L::NQ;
           ok = ptx::mbar_wait(bars + C_Q_FULL + qn, ((it + 1) / L::NQ) & 1, abort_flag, tmo);
@@ -342,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           issue_scores<DT>(tmem + L::T_SP, dK_k, dQ_k0 + qn * BUF_STEP, ID_S, dsteps);
           ptx::mma_commit(bars + C_S_FULL);
         }
-        if (DT == 128 && s_done) issue_dq<4, 8>(tmem + L::T_DPQ, dq_a, dq_b, ID_DQ, ksteps);
-        else issue_dq<0, 8>(tmem + L::T_DPQ, dq_a, dq_b, ID_DQ, ksteps);
+        if (DT == 128 && s_done) issue_dq<4, 8>(tmem + L::T_DQ, dq_a, dq_b, ID_DQ, ksteps);
+        else issue_dq<0, 8>(tmem + L::T_DQ, dq_a, dq_b, ID_DQ, ksteps);
         ptx::mma_commit(bars + C_DQ_FULL);
         if (last) {
           ptx::mma_commit(bars + C_ACC_FULL);
@@ -398,14 +428,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           pv[35 + c] = ptx::ex2(fmaf(__uint_as_float(b[c + 3]), p.scale_log2, f.w));
         }
       }
-      if (quarter * 32 + 32 > w.keys()) {          // this warp has keys behind the length
-        const bool dead = r >= w.keys();
-#pragma unroll
-        for (int c = 0; c < 64; ++c) pv[c] = dead ? 0.f : pv[c];
-      }
+      const bool dead = r >= w.keys();             // a key behind the length
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         uint32_t u[8];
+        if (dead) {
+#pragma unroll
+          for (int c = 16 * g; c < 16 * g + 16; ++c) pv[c] = 0.f;
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) u[k] = ptx::pack_bf16(pv[16 * g + 2 * k], pv[16 * g + 2 * k + 1]);
         ptx::tmem_st8(tmem + lane_addr + L::T_SP + col0 + 8 * g, u);
@@ -421,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c0 = 0; c0 < 64; c0 += 16) {
         float dp[16];
-        ptx::tmem_ld16(tmem + lane_addr + L::T_DPQ + col0 + c0, dp);
+        ptx::tmem_ld16(tmem + lane_addr + L::T_DP + col0 + c0, dp);
         uint32_t u[8];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
@@ -451,65 +481,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     int it = 0, tl = 0;
     bool ok = true;
     while (ok && w.next()) {
+      const bool holds = quarter * 32 < p.s.D;     // this warp's lanes are columns of dQ
+      const bool begins = w.i == 0, ends = w.i == w.nkt - 1 && p.ksegs == 1;
+      float* acc = p.dq_acc + ((((size_t)w.kseg * p.s.B * p.s.Hk + w.bh) * p.s.ntile + w.tile()) * kTile) * DT + 4 * row;
+      // what the key tiles before added up to, for the last one: fetched while its products run
+      float v[128];
+      if (holds && ends && !begins) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) ld_relaxed_v4(acc + (size_t)c * DT, v + c);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) v[c] = 0.f;
+      }
       ok = ptx::warp_wait(bars + C_DQ_FULL, it & 1, abort_flag, tmo);
       if (!ok) break;
       ptx::tc_fence_after();
-      float v[128];
 #pragma unroll
       for (int c0 = 0; c0 < 128; c0 += 32) {
         float t[32];
-        ptx::tmem_ld32(tmem + lane_addr + L::T_DPQ + c0, t);
+        ptx::tmem_ld32(tmem + lane_addr + L::T_DQ + c0, t);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c0 + c] = t[c];
+        for (int c = 0; c < 32; ++c) v[c0 + c] += t[c];
       }
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bars + C_DQ_EMPTY);   // dQ^T(it) has left TMEM
-      if (quarter * 32 < p.s.D) {
-        const bool begins = w.i == 0, ends = w.i == w.nkt - 1 && p.ksegs == 1;
-        float* acc = p.dq_acc + ((((size_t)w.kseg * p.s.B * p.s.Hk + w.bh) * p.s.ntile + w.tile()) * kTile) * DT + row;
+      if (holds) {
         if (ends) {
-          if (!begins) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c) v[c] += __ldcg(acc + (size_t)c * DT);
-          }
           // Lanes 2k and 2k + 1 hold d = 2k and 2k + 1 of every row: the even lane takes both for
           // even rows, the odd lane for odd ones, so that a store has two of them.
           const int odd = lane & 1, d = row & ~1;
           int token, head;
           row_of(p.s, w.tile(), odd, token, head);
           __nv_bfloat16* dst = p.dq + w.b * p.dq_b + w.hk * p.s.g * p.dq_h + d;
-          // rows left in the tile (packed: tokens), steps of two rows
-          const bool mine = d < p.s.D;
-          const int left = p.s.packed ? min(p.s.tpt - (odd >= p.s.g ? 1 : 0), p.s.Sq - token) : p.s.Sq - token;
           dst += token * p.dq_s + head * p.dq_h;
-          int at = 0;
+          uint32_t two[64];
 #pragma unroll
           for (int c = 0; c < 128; c += 2) {
-            const float give = odd ? v[c] : v[c + 1];
+            const float give = odd ? v[c] : v[c + 1], keep = odd ? v[c + 1] : v[c];
             const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-            const uint32_t two = odd ? ptx::pack_bf16(got * p.scale, v[c + 1] * p.scale)
-                                     : ptx::pack_bf16(v[c] * p.scale, got * p.scale);
-            if (mine && at < left) *reinterpret_cast<uint32_t*>(dst) = two;
-            if (p.s.packed) {                      // two heads on, or into the next token
-              head += 2;
-              dst += 2 * p.dq_h;
-              if (head >= p.s.g) {
-                head -= p.s.g;
-                dst += p.dq_s - p.s.g * p.dq_h;
-                ++at;
+            two[c / 2] = ptx::pack_bf16((odd ? got : keep) * p.scale, (odd ? keep : got) * p.scale);
+          }
+          if (d < p.s.D) {
+            if (!p.s.packed) {
+              const long long step = 2 * p.dq_s;
+              const int left = p.s.Sq - token;
+#pragma unroll
+              for (int c = 0; c < 128; c += 2) {
+                if (c < left) *reinterpret_cast<uint32_t*>(dst) = two[c / 2];
+                dst += step;
               }
             } else {
-              dst += 2 * p.dq_s;
-              at += 2;
+              int left = min(p.s.tpt, p.s.Sq - token);
+#pragma unroll
+              for (int c = 0; c < 128; c += 2) {
+                if (left > 0) *reinterpret_cast<uint32_t*>(dst) = two[c / 2];
+                head += 2;                         // two heads on, or into the next token
+                dst += 2 * p.dq_h;
+                if (head >= p.s.g) {
+                  head -= p.s.g;
+                  dst += p.dq_s - p.s.g * p.dq_h;
+                  --left;
+                }
+              }
             }
           }
-        } else if (begins) {
+        } else if (!begins) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c) acc[(size_t)c * DT] = v[c];
+          for (int c = 0; c < 128; c += 4)
+            ptx::red_add_v4_f32(acc + (size_t)c * DT, v[c], v[c + 1], v[c + 2], v[c + 3]);
         } else {
 #pragma unroll
-          for (int c = 0; c < 128; ++c) ptx::red_add_f32(acc + (size_t)c * DT, v[c]);
+          for (int c = 0; c < 128; c += 4)
+            *(float4*)(acc + (size_t)c * DT) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         }
       }
       if (w.last_of_tile()) {
@@ -557,44 +601,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // What the units left: dq as the sum of the key segments' partials, dk and dv as that of the row
-// segments', in order; zeros where no key was visible, NaN for a length out of range. A thread
-// takes 8 columns of a row.
+// segments', in order; zeros where no key was visible, NaN for a length out of range. The first
+// dq_blocks blocks take a row tile each, 16 rows at a time through shared memory, as the partials
+// hold four rows of a column side by side; a thread of the others 8 columns of a row.
 template <int DT>
 __global__ void __launch_bounds__(256) cross_grad_join_kernel(const __grid_constant__ BwdArgs p, unsigned dq_blocks) {
+  __shared__ float rows16[16][DT + 4];
   train::grid_wait();
-  const int per = p.s.D >> 3;
-  const bool for_dq = blockIdx.x < dq_blocks;
-  const long long item = (long long)(for_dq ? blockIdx.x : blockIdx.x - dq_blocks) * 256 + threadIdx.x;
-  const int c = (int)(item % per) * 8;
-  const long long row = item / per;                // (batch, token, head)
-  const int H = for_dq ? p.s.Hq : p.s.Hk, S = for_dq ? p.s.Sq : p.s.Sk;
-  if (row >= (long long)p.s.B * S * H) return;
-  const int h = (int)(row % H);
-  const int token = (int)(row / H % S), b = (int)(row / H / S);
-  const int len = length_of(p.s, b), tiles = (max(len, 0) + kTile - 1) / kTile;
   const size_t groups = (size_t)p.s.B * p.s.Hk;
   float t[8];
-  if (for_dq) {
+  if (blockIdx.x < dq_blocks) {
+    const size_t tile_id = blockIdx.x;             // group, tile
+    const int tile = (int)(tile_id % p.s.ntile), bh = (int)(tile_id / p.s.ntile);
+    const int b = bh / p.s.Hk, hk = bh - b * p.s.Hk;
+    const int len = length_of(p.s, b), tiles = (max(len, 0) + kTile - 1) / kTile;
     if (len > 0 && p.ksegs == 1) return;           // written by the one unit of these rows
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = len < 0 ? NAN : 0.f;
-    const int hk = h / p.s.g, head = h - hk * p.s.g;
-    const int tile = p.s.packed ? token / p.s.tpt : head * p.s.nq + token / kTile;
-    const int r = p.s.packed ? (token % p.s.tpt) * p.s.g + head : token % kTile;
-    const float* src = p.dq_acc + ((((size_t)b * p.s.Hk + hk) * p.s.ntile + tile) * kTile + r) * DT + c;
-    const size_t step = groups * p.s.ntile * kTile * DT;
     const int n = (tiles + p.kper - 1) / p.kper;
-    for (int s = 0; s < n; ++s) {
-      float x[8];
-      train::load_f32<float, 8>(src + s * step, x);
+    const size_t step = groups * p.s.ntile * kTile * DT;
+    for (int r0 = 0; r0 < kTile; r0 += 16) {
+      const float* src = p.dq_acc + (tile_id * kTile + r0) * DT;
+      for (int e = threadIdx.x; e < 4 * DT; e += 256) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < n; ++s) {
+          const float4 y = __ldg((const float4*)(src + s * step) + e);
+          x.x += y.x;
+          x.y += y.y;
+          x.z += y.z;
+          x.w += y.w;
+        }
+        const int q = e / DT * 4, d = e % DT;
+        rows16[q][d] = x.x;
+        rows16[q + 1][d] = x.y;
+        rows16[q + 2][d] = x.z;
+        rows16[q + 3][d] = x.w;
+      }
+      __syncthreads();
+      const int r = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;
+      int token, head;
+      if (c < p.s.D && row_of(p.s, tile, r0 + r, token, head)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] += x[i];
+        for (int i = 0; i < 8; ++i) t[i] = len < 0 ? NAN : rows16[r][c + i] * p.scale;
+        train::store_f32<__nv_bfloat16, 8>(p.dq + b * p.dq_b + token * p.dq_s + (hk * p.s.g + head) * p.dq_h + c, t);
+      }
+      __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] *= p.scale;
-    train::store_f32<__nv_bfloat16, 8>(p.dq + b * p.dq_b + token * p.dq_s + h * p.dq_h + c, t);
     return;
   }
+  const int per = p.s.D >> 3;
+  const long long item = (long long)(blockIdx.x - dq_blocks) * 256 + threadIdx.x;
+  const int c = (int)(item % per) * 8;
+  const long long row = item / per;                // (batch, key, head)
+  if (row >= (long long)p.s.B * p.s.Sk * p.s.Hk) return;
+  const int h = (int)(row % p.s.Hk);
+  const int token = (int)(row / p.s.Hk % p.s.Sk), b = (int)(row / p.s.Hk / p.s.Sk);
+  const int len = length_of(p.s, b), tiles = (max(len, 0) + kTile - 1) / kTile;
   const int kt = token / kTile;
   if (kt < tiles && p.qsegs == 1) return;
   for (int which = 0; which < 2; ++which) {

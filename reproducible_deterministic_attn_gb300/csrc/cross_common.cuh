@@ -80,6 +80,21 @@ __device__ __forceinline__ void load_row_tile(const Shape& s, const CUtensorMap*
   for (int cb = 0; cb < DT / 64; ++cb)
     tma_load_4d(dst + cb * kTile * 128, map, cb * 64, (hk * s.g + head) * mul_h, token, b * mul_b, bar);
 }
+// Asks for row tile t to be brought into L2.
+template <int DT>
+__device__ __forceinline__ void prefetch_row_tile(const Shape& s, const CUtensorMap* map, int b, int hk, int t,
+                                                  int mul_b, int mul_h) {
+  int head = 0, token = t * s.tpt;
+  if (!s.packed) {
+    head = t / s.nq;
+    token = (t - head * s.nq) * kTile;
+  }
+#pragma unroll
+  for (int cb = 0; cb < DT / 64; ++cb)
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(cb * 64),
+                 "r"((hk * s.g + head) * mul_h), "r"(token), "r"(b * mul_b)
+                 : "memory");
+}
 template <int DT>
 __device__ __forceinline__ void load_key_tile(const CUtensorMap* map, uint8_t* dst, int b, int hk, int t, int mul_b,
                                               int mul_h, uint64_t* bar) {

@@ -120,6 +120,35 @@ dash_status_t dash_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
                                     const long long* dk_strides, long long pos_stride, float eps,
                                     int interleaved, int dtype, int id_bits, cudaStream_t stream);
 
+/*
+ * The same for positions with several axes (time, height and width of an image's or a video's
+ * patches): a token has a position on each of `axes` axes (1 to 4), and pair i turns by column i
+ * of the table's row of its axis' position. The first sections[0] pairs belong to axis 0, the next
+ * sections[1] to axis 1, and so on; the sections add up to R / 2 (one may be empty). The table may
+ * hold one ladder of frequencies over all pairs or one of its own for each section.
+ *   positions: [axes, B, S] int32 or int64, axes axis_stride and batches pos_stride elements apart
+ *   sections : host array of `axes` numbers, read during the call
+ * A token with a position outside [0, P) on any axis is treated as above. P below 2^31. All else,
+ * and the workspace, as for dash_qk_norm_rope_fwd and _bwd.
+ */
+dash_status_t dash_qk_norm_rope_axes_fwd(const void* q, const void* k, const float* wq, const float* wk,
+                                         const float* cos, const float* sin, const void* positions,
+                                         void* q_out, void* k_out, int* status, int B, int S, int Hq,
+                                         int Hk, int D, int R, long long P, const long long* q_strides,
+                                         const long long* k_strides, const int* sections, int axes,
+                                         long long axis_stride, long long pos_stride, float eps,
+                                         int interleaved, int dtype, int id_bits, cudaStream_t stream);
+dash_status_t dash_qk_norm_rope_axes_bwd(const void* dq_out, const void* dk_out, const void* q,
+                                         const void* k, const float* wq, const float* wk,
+                                         const float* cos, const float* sin, const void* positions,
+                                         void* dq, void* dk, float* dwq, float* dwk, void* workspace,
+                                         size_t workspace_bytes, int B, int S, int Hq, int Hk, int D,
+                                         int R, long long P, const long long* q_strides,
+                                         const long long* k_strides, const long long* dq_strides,
+                                         const long long* dk_strides, const int* sections, int axes,
+                                         long long axis_stride, long long pos_stride, float eps,
+                                         int interleaved, int dtype, int id_bits, cudaStream_t stream);
+
 /* ---- Gradient norm and clipping --------------------------------------------------------- */
 
 /* One tensor of a clipping plan: numel elements of `dtype` at `grad`; its clipped values go
@@ -206,6 +235,46 @@ dash_status_t dash_linear_xent_bwd(const void* x, const void* w, const void* tar
                                    long long V, int D, long long ldx, long long ldw, float scale,
                                    long long ignore_index, int id_bits, int dw_dtype,
                                    int accumulate, cudaStream_t stream);
+
+/* ---- Group norm with an activation, channels last ---------------------------------------- */
+
+/* Activations of the group norm. */
+typedef enum { DASH_ACT_NONE = 0, DASH_ACT_SILU = 1 } dash_act_t;
+
+/*
+ * y = act(xh * w + b), xh = (x - mean) / sqrt(var + eps), mean and var (the biased variance) over
+ * all S rows and the C / G channels of each sample's group; act is the identity or
+ * silu(z) = z / (1 + exp(-z)).
+ *   x    : [N, S, C] of `dtype`, C contiguous, with element strides {sample, row} in x_strides (a
+ *          part of a buffer that holds more channels; any strides and alignment, rows of whole
+ *          16-byte pieces are moved as such)
+ *   w, b : fp32 [C], or NULL for ones and zeros
+ *   y    : contiguous [N, S, C] (written; must not overlap x)
+ *   mean, rstd : fp32 [N, G] (written), as the gradient reads them
+ *   workspace  : dash_group_norm_workspace_size(N, S, C, G) bytes, for both directions
+ * The sums are taken per channel around its first value, so that a mean that is large beside the
+ * spread costs no digits. With S = 0 mean is 0 and rstd 1 / sqrt(eps).
+ * N, S >= 0; C a multiple of G, up to 2^18, C / G up to 4096; N below 2^24, N * S and N * G below
+ * 2^31 - 65536, N * S * C up to 2^42. Pointers aligned as their elements.
+ */
+size_t dash_group_norm_workspace_size(long long N, long long S, long long C, int G);
+dash_status_t dash_group_norm_fwd(const void* x, const float* w, const float* b, void* y, float* mean,
+                                  float* rstd, void* workspace, size_t workspace_bytes, long long N,
+                                  long long S, long long C, int G, const long long* x_strides,
+                                  float eps, int act, int dtype, cudaStream_t stream);
+
+/*
+ * Gradients of the above: with dz = dy act'(z), db = sum dz and dw = sum dz xh over samples and
+ * rows, dx = rstd (w dz - mean(w dz) - xh mean(w dz xh)), the means over the group as above. xh and
+ * z are recomputed from x, mean and rstd.
+ *   dy   : contiguous [N, S, C] of `dtype` (read)      dx : contiguous [N, S, C] (written)
+ *   dw, db : fp32 [C] (written; NULL: not wanted)
+ */
+dash_status_t dash_group_norm_bwd(const void* dy, const void* x, const float* w, const float* b,
+                                  const float* mean, const float* rstd, void* dx, float* dw, float* db,
+                                  void* workspace, size_t workspace_bytes, long long N, long long S,
+                                  long long C, int G, const long long* x_strides, int act, int dtype,
+                                  cudaStream_t stream);
 
 /* ---- Cross attention to states of another length ----------------------------------------- */
 

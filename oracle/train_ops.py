@@ -130,3 +130,54 @@ def cross_attn_grad(q, k, v, o, do, lse, lens, scale):
         dk[b] = scale * (ds[b].transpose(1, 2) @ qd[b]).view(Hk, g, Sk, D).sum(1).transpose(0, 1)
         dv[b] = (p[b].transpose(1, 2) @ dd[b]).view(Hk, g, Sk, D).sum(1).transpose(0, 1)
     return dq.transpose(1, 2), dk, dv, p, ds
+
+
+def norm_rope_axes(x, w, cos, sin, pos, sections, eps, interleaved):
+    """norm_rope with a position of each axis: pos [axes, B, S], sections the numbers of pairs."""
+    c, s, i = _axes_tables(cos, sin, pos, sections)
+    return norm_rope(x, w, c, s, i, eps, interleaved)
+
+
+def norm_rope_axes_grad(dout, x, w, cos, sin, pos, sections, eps, interleaved):
+    c, s, i = _axes_tables(cos, sin, pos, sections)
+    return norm_rope_grad(dout, x, w, c, s, i, eps, interleaved)
+
+
+def _axes_tables(cos, sin, pos, sections):
+    """Tables with a row for every token, and the tokens' numbers."""
+    axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    rows = [torch.stack([t[pos[a].flatten().long(), i] for i, a in enumerate(axis)], -1) if axis
+            else t.new_zeros(pos[0].numel(), 0) for t in (cos, sin)]
+    return rows[0], rows[1], torch.arange(pos[0].numel(), device=cos.device).view(pos[0].shape)
+
+
+def group_norm(x, w, b, groups, eps, act):
+    """(y, mean, rstd) for x [N, S, C]."""
+    N, S, C = x.shape
+    xg = x.double().view(N, S, groups, C // groups)
+    mean = xg.mean((1, 3))
+    var = ((xg - mean[:, None, :, None]) ** 2).mean((1, 3))
+    rstd = 1 / torch.sqrt(var + eps)
+    z = _affine(x, w, b, mean, rstd, groups)[1]
+    return (z * torch.sigmoid(z) if act == "silu" else z), mean, rstd
+
+
+def _affine(x, w, b, mean, rstd, groups):
+    per = x.shape[2] // groups
+    m, r = (t.double().repeat_interleave(per, 1)[:, None] for t in (mean, rstd))
+    xh = (x.double() - m) * r
+    z = xh * (1.0 if w is None else w.double()) + (0.0 if b is None else b.double())
+    return xh, z, r
+
+
+def group_norm_grad(dy, x, w, b, mean, rstd, groups, act):
+    """(dx, dw, db, dz, xh) with the given mean and rstd."""
+    N, S, C = x.shape
+    xh, z, r = _affine(x, w, b, mean, rstd, groups)
+    dz = dy.double()
+    if act == "silu":
+        sg = torch.sigmoid(z)
+        dz = dz * (sg + z * sg * (1 - sg))
+    u = dz * (1.0 if w is None else w.double())
+    over = lambda t: t.view(N, S, groups, -1).mean((1, 3)).repeat_interleave(C // groups, 1)[:, None]  # noqa: E731
+    return r * (u - over(u) - xh * over(u * xh)), (dz * xh).sum((0, 1)), dz.sum((0, 1)), dz, xh

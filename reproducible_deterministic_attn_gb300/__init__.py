@@ -21,9 +21,11 @@ from .dash_attn import (  # noqa: F401
 )
 from .train_ops import (  # noqa: F401
     DASH_BF16, DASH_FP16, DASH_FP32, GradClipPlan, cross_attn_backward, cross_attn_forward,
-    dash_cross_attn_bwd_workspace_size, dash_cross_attn_fwd_workspace_size, dash_embed_bwd_workspace_size,
-    dash_linear_xent_workspace_size, dash_qk_norm_rope_bwd_workspace_size, embed_backward,
-    embed_forward, grad_clip, grad_clip_plan, linear_xent_backward, linear_xent_forward,
-    new_cross_attn_workspace, new_embed_workspace, new_linear_xent_workspace, new_qk_norm_rope_workspace,
-    qk_norm_rope_backward, qk_norm_rope_forward, rope_table,
+    dash_cross_attn_bwd_workspace_size, dash_cross_attn_fwd_workspace_size,
+    dash_embed_bwd_workspace_size, dash_group_norm_workspace_size, dash_linear_xent_workspace_size,
+    dash_qk_norm_rope_bwd_workspace_size, embed_backward, embed_forward, grad_clip, grad_clip_plan,
+    group_norm_act_backward, group_norm_act_forward, linear_xent_backward, linear_xent_forward,
+    new_cross_attn_workspace, new_embed_workspace, new_group_norm_workspace,
+    new_linear_xent_workspace, new_qk_norm_rope_workspace, qk_norm_rope_axes_backward,
+    qk_norm_rope_axes_forward, qk_norm_rope_backward, qk_norm_rope_forward, rope_axes_table, rope_table,
 )

@@ -18,8 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdash_attn.so")
 LIB_CHECKED = os.path.join(PKG, "libdash_attn_checked.so")
 
-SOURCES = ["dash_attn.cu", "linear_xent.cu", "embed.cu", "qk_norm_rope.cu", "grad_clip.cu",
-           "cross_attn.cu", "sched.cpp"]
+SOURCES = ["dash_attn.cu", "linear_xent.cu", "embed.cu", "qk_norm_rope.cu",
+           "qk_norm_rope_axes.cu", "group_norm.cu", "grad_clip.cu", "cross_attn.cu", "sched.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -29,6 +29,8 @@ _c_int, _c_float, _c_size, _vp, _ll = (ctypes.c_int, ctypes.c_float, ctypes.c_si
                                        ctypes.c_void_p, ctypes.c_longlong)
 
 _c3 = _ll * 3
+_c2 = _ll * 2
+_ACT = {None: 0, "none": 0, "silu": 1}
 
 
 class _ClipTensor(ctypes.Structure):
@@ -45,6 +47,10 @@ _core._SIGNATURES.update({
     "dash_qk_norm_rope_bwd_workspace_size": (_c_size, [_c_int] * 5),
     "dash_qk_norm_rope_bwd": (_c_int, [_vp] * 14 + [_c_size] + [_c_int] * 6 + [_ll] + [_vp] * 4 + [_ll, _c_float]
                               + [_c_int] * 3 + [_vp]),
+    "dash_qk_norm_rope_axes_fwd": (_c_int, [_vp] * 10 + [_c_int] * 6 + [_ll, _vp, _vp, _vp, _c_int, _ll, _ll, _c_float]
+                                   + [_c_int] * 3 + [_vp]),
+    "dash_qk_norm_rope_axes_bwd": (_c_int, [_vp] * 14 + [_c_size] + [_c_int] * 6 + [_ll] + [_vp] * 5
+                                   + [_c_int, _ll, _ll, _c_float] + [_c_int] * 3 + [_vp]),
     "dash_grad_clip_plan_size": (_c_size, [ctypes.POINTER(_ClipTensor), _c_int]),
     "dash_grad_clip_plan": (_c_int, [ctypes.POINTER(_ClipTensor), _c_int, _vp, _c_size, _vp]),
     "dash_grad_clip": (_c_int, [_vp, _c_size, _c_float, _vp, _vp]),
@@ -53,6 +59,9 @@ _core._SIGNATURES.update({
                                                   _c_int, _vp]),
     "dash_linear_xent_bwd": (_c_int, [_vp] * 8 + [_c_size, _ll, _ll, _c_int, _ll, _ll, _c_float, _ll,
                                                   _c_int, _c_int, _c_int, _vp]),
+    "dash_group_norm_workspace_size": (_c_size, [_ll, _ll, _ll, _c_int]),
+    "dash_group_norm_fwd": (_c_int, [_vp] * 7 + [_c_size, _ll, _ll, _ll, _c_int, _vp, _c_float, _c_int, _c_int, _vp]),
+    "dash_group_norm_bwd": (_c_int, [_vp] * 10 + [_c_size, _ll, _ll, _ll, _c_int, _vp, _c_int, _c_int, _vp]),
     "dash_cross_attn_fwd_workspace_size": (_c_size, [_c_int] * 6),
     "dash_cross_attn_fwd": (_c_int, [_vp] * 8 + [_c_size] + [_c_int] * 6 + [_vp] * 3 + [_c_float, _c_int, _vp]),
     "dash_cross_attn_bwd_workspace_size": (_c_size, [_c_int] * 6),
@@ -335,23 +344,9 @@ def new_qk_norm_rope_workspace(B: int, S: int, Hq: int, Hk: int, D: int, device)
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None, eps: float = 1e-6,
-                          interleaved: bool = False, dq=None, dk=None, workspace=None, stream=None,
-                          check: bool = True):
-    """Gradients of qk_norm_rope_forward with respect to q, k, wq and wk.
-
-    dq_out, dk_out: contiguous, as attn_backward returns them. dq, dk: optional tensors to
-    write to, strided like q and k may be (parts of a fused projection's gradient). Returns
-    (dq, dk, dwq, dwk), the last two fp32 [D] or None where the weight is None."""
-    if stream is not None:
-        with _using(stream, q):
-            return qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq,
-                                         dk, workspace, check=check)
-    dev, tables, sizes, stride, bits, held = _qk_args(q, k, wq, wk, cos, sin, positions)
-    if dev != _current_device():
-        with torch.cuda.device(dev):
-            return qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq,
-                                         dk, workspace, check=check)
+def _qk_grads(dq_out, dk_out, q, k, wq, wk, sizes, dq, dk, workspace, dev):
+    """What the gradients' calls write: (dq, dk, dwq, dwk), the addresses of these and of the
+    workspace, the strides of dq and dk, and the workspace."""
     dtype, qshape, kshape, D = q.dtype, q.shape, k.shape, sizes[4]
     if (dq_out.dtype != dtype or dq_out.shape != qshape or not dq_out.is_contiguous() or dq_out.get_device() != dev
             or dk_out.dtype != dtype or dk_out.shape != kshape or not dk_out.is_contiguous()
@@ -373,12 +368,113 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None
         pdwk = dwk.data_ptr()
     if workspace is None:
         workspace = new_qk_norm_rope_workspace(*sizes[:5], q.device)
-    ws, nbytes = _ws(workspace, dev)
+    return dq, dk, dwq, dwk, (dq.data_ptr(), dk.data_ptr(), pdwq, pdwk, *_ws(workspace, dev)), (dqn[4], dkn[4]), workspace
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions=None, eps: float = 1e-6,
+                          interleaved: bool = False, dq=None, dk=None, workspace=None, stream=None,
+                          check: bool = True):
+    """Gradients of qk_norm_rope_forward with respect to q, k, wq and wk.
+
+    dq_out, dk_out: contiguous, as attn_backward returns them. dq, dk: optional tensors to
+    write to, strided like q and k may be (parts of a fused projection's gradient). Returns
+    (dq, dk, dwq, dwk), the last two fp32 [D] or None where the weight is None."""
+    if stream is not None:
+        with _using(stream, q):
+            return qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq,
+                                         dk, workspace, check=check)
+    dev, tables, sizes, stride, bits, held = _qk_args(q, k, wq, wk, cos, sin, positions)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq,
+                                         dk, workspace, check=check)
+    dq, dk, dwq, dwk, ptrs, outs, workspace = _qk_grads(dq_out, dk_out, q, k, wq, wk, sizes, dq, dk, workspace, dev)
     _raise(_core.load().dash_qk_norm_rope_bwd(
-        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), *tables, dq.data_ptr(), dk.data_ptr(),
-        pdwq, pdwk, ws, nbytes, *sizes, dqn[4][1], dkn[4][1], stride, eps, interleaved, _DTYPE[dtype], bits,
-        _stream(dev)), "dash_qk_norm_rope_bwd")
+        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), *tables, *ptrs, *sizes, outs[0][1],
+        outs[1][1], stride, eps, interleaved, _DTYPE[q.dtype], bits, _stream(dev)), "dash_qk_norm_rope_bwd")
     _finish(workspace, check, "dash_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+def rope_axes_table(positions: int, sections, base: float = 10000.0, own_ladders: bool = False, device="cuda"):
+    """(cos, sin), fp32 [positions, sum(sections)], for qk_norm_rope_axes_forward: one ladder of
+    frequencies over all pairs (base^(-i / pairs) for pair i), or with own_ladders one for each
+    section, which starts anew at 1."""
+    sections = [int(n) for n in sections]
+    if own_ladders:
+        exps = [torch.arange(n, device=device, dtype=torch.float64) / max(n, 1) for n in sections]
+        exps = torch.cat(exps) if exps else torch.empty(0, device=device, dtype=torch.float64)
+    else:
+        exps = torch.arange(sum(sections), device=device, dtype=torch.float64) / max(sum(sections), 1)
+    ang = torch.arange(positions, device=device, dtype=torch.float64)[:, None] * torch.pow(float(base), -exps)
+    return ang.cos().float(), ang.sin().float()
+
+
+@functools.lru_cache(maxsize=1024)
+def _sections(sections: tuple):
+    """Section lengths as the C calls read them: the array, which the caller holds for the time of
+    its call, and its address."""
+    arr = (_c_int * max(len(sections), 1))(*sections)
+    return arr, ctypes.addressof(arr)
+
+
+def _axes_args(q, k, wq, wk, cos, sin, positions, sections):
+    dev, tables, sizes, _, _, held = _qk_args(q, k, wq, wk, cos, sin, None)
+    sections = tuple(int(n) for n in sections)
+    axes, B, S = len(sections), sizes[0], sizes[1]
+    if not 1 <= axes <= 4 or min(sections) < 0 or 2 * sum(sections) != sizes[5]:
+        _bad("sections: expected 1 to 4 numbers of pairs that add up to the tables' columns")
+    bits = _index(positions, "positions", dev)
+    if positions.shape == (axes, B, S):
+        axis_stride, stride = B * S, S
+    elif positions.shape == (axes, S) or positions.shape == (axes, 1, S):
+        axis_stride, stride = S, 0
+    else:
+        _bad("positions: expected [axes, B, S] or [axes, S]")
+    sec = _sections(sections)
+    return dev, (*tables[:4], positions.data_ptr()), sizes, (sec[1], axes, axis_stride, stride), bits, (held, sec)
+
+
+def qk_norm_rope_axes_forward(q, k, wq, wk, cos, sin, positions, sections, eps: float = 1e-6,
+                              interleaved: bool = False, status=None, stream=None):
+    """qk_norm_rope_forward for positions with several axes (time, height and width of patches).
+
+    positions: int [axes, B, S] or [axes, S], a position on each axis; sections: how many of the
+    rotated pairs belong to each axis, in order (1 to 4 numbers that add up to R / 2); cos, sin:
+    fp32 [P, R / 2], column i for pair i (rope_axes_table). All else as in qk_norm_rope_forward."""
+    if stream is not None:
+        with _using(stream, q):
+            return qk_norm_rope_axes_forward(q, k, wq, wk, cos, sin, positions, sections, eps, interleaved, status)
+    dev, tables, sizes, ax, bits, held = _axes_args(q, k, wq, wk, cos, sin, positions, sections)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return qk_norm_rope_axes_forward(q, k, wq, wk, cos, sin, positions, sections, eps, interleaved, status)
+    q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)
+    _raise(_core.load().dash_qk_norm_rope_axes_fwd(
+        q.data_ptr(), k.data_ptr(), *tables, q_out.data_ptr(), k_out.data_ptr(), _status_word(status, dev),
+        *sizes, *ax, eps, interleaved, _DTYPE[q.dtype], bits, _stream(dev)), "dash_qk_norm_rope_axes_fwd")
+    return q_out, k_out
+
+
+def qk_norm_rope_axes_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, sections, eps: float = 1e-6,
+                               interleaved: bool = False, dq=None, dk=None, workspace=None, stream=None,
+                               check: bool = True):
+    """Gradients of qk_norm_rope_axes_forward with respect to q, k, wq and wk, as
+    qk_norm_rope_backward returns them and with its workspace (new_qk_norm_rope_workspace)."""
+    if stream is not None:
+        with _using(stream, q):
+            return qk_norm_rope_axes_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, sections, eps,
+                                              interleaved, dq, dk, workspace, check=check)
+    dev, tables, sizes, ax, bits, held = _axes_args(q, k, wq, wk, cos, sin, positions, sections)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return qk_norm_rope_axes_backward(dq_out, dk_out, q, k, wq, wk, cos, sin, positions, sections, eps,
+                                              interleaved, dq, dk, workspace, check=check)
+    dq, dk, dwq, dwk, ptrs, outs, workspace = _qk_grads(dq_out, dk_out, q, k, wq, wk, sizes, dq, dk, workspace, dev)
+    _raise(_core.load().dash_qk_norm_rope_axes_bwd(
+        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), *tables, *ptrs, *sizes, outs[0][1],
+        outs[1][1], *ax, eps, interleaved, _DTYPE[q.dtype], bits, _stream(dev)), "dash_qk_norm_rope_axes_bwd")
+    _finish(workspace, check, "dash_qk_norm_rope_axes_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -654,3 +750,119 @@ def cross_attn_backward(q, k, v, o, do, lse, scale: float, kv_lens=None, dq=None
         outs[1][4][1], outs[2][4][1], scale, bits, _stream(dev)), "dash_cross_attn_bwd")
     _finish(workspace, check, "dash_cross_attn_bwd")
     return dq, dk, dv
+
+
+# ---- group norm with an activation --------------------------------------------------------------
+
+def dash_group_norm_workspace_size(N: int, S: int, C: int, groups: int) -> int:
+    return int(_core.load().dash_group_norm_workspace_size(int(N), int(S), int(C), int(groups)))
+
+
+def new_group_norm_workspace(N: int, S: int, C: int, groups: int, device) -> torch.Tensor:
+    """The workspace of group_norm_act_forward and _backward for N samples of S rows (uint8)."""
+    nbytes = dash_group_norm_workspace_size(N, S, C, groups)
+    if nbytes == 0:
+        raise DashError(DASH_ERR_UNSUPPORTED, "dash_group_norm_workspace_size")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _row_strides(sample: int, row: int):
+    arr = _c2(sample, row)
+    return arr, ctypes.addressof(arr)
+
+
+def _gn_args(x, w, b, groups, activation):
+    dev = _device(x, "x")
+    dtype, act = _DTYPE.get(x.dtype), _ACT.get(activation)
+    if dtype is None:
+        _bad("x: expected bfloat16, float16 or float32")
+    if act is None:
+        _bad("activation: expected 'none' or 'silu'")
+    if x.dim() < 2:
+        _bad("x: expected [N, ..., C]")
+    shape, st = x.shape, x.stride()
+    N, C = shape[0], shape[-1]
+    if C < 1 or groups < 1 or C % groups:
+        _bad("groups: expected a divisor of the channels")
+    if st[-1] != 1 and C > 1:
+        _bad("x: expected contiguous channels")
+    # the dimensions between are one dimension of rows, the same number of elements apart
+    S, row = 1, 0
+    for n, step in zip(reversed(shape[1:-1]), reversed(st[1:-1])):
+        if n == 1:
+            continue
+        if S > 1 and step != row * S:
+            _bad("x: expected rows evenly spaced over the dimensions between N and C")
+        if S == 1:
+            row = step
+        S *= n
+    pw = None if w is None else _vector(w, "w", C, dev)
+    pb = None if b is None else _vector(b, "b", C, dev)
+    return dev, pw, pb, (N, S, C, groups), _row_strides(st[0] if N > 1 else 0, row), act, dtype
+
+
+def group_norm_act_forward(x, w, b, groups: int, eps: float = 1e-5, activation="silu", out=None, workspace=None,
+                           stream=None):
+    """Group norm over channels-last x with the activation behind it: act(xh * w + b).
+
+    x: [N, ..., C] bf16, fp16 or fp32 with contiguous channels; the dimensions between (rows, or
+    height and width) are normed over together with the C / groups channels of a group, and may be
+    strided as one (a part of a buffer with more channels). w, b: fp32 [C] or None; activation:
+    "silu" or "none". Returns (y, mean, rstd): contiguous y of x's type, fp32 [N, groups]."""
+    if stream is not None:
+        with _using(stream, x):
+            return group_norm_act_forward(x, w, b, groups, eps, activation, out, workspace)
+    dev, pw, pb, sizes, xs, act, dtype = _gn_args(x, w, b, groups, activation)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return group_norm_act_forward(x, w, b, groups, eps, activation, out, workspace)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or out.shape != x.shape or not out.is_contiguous() or out.get_device() != dev:
+        _bad(f"out: expected contiguous, of the type and shape of x, on cuda:{dev}")
+    mean = torch.empty((sizes[0], groups), dtype=_F32, device=x.device)
+    rstd = torch.empty((sizes[0], groups), dtype=_F32, device=x.device)
+    if workspace is None:
+        workspace = new_group_norm_workspace(*sizes, x.device)
+    _raise(_core.load().dash_group_norm_fwd(
+        x.data_ptr(), pw, pb, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), *_ws(workspace, dev), *sizes, xs[1],
+        eps, act, dtype, _stream(dev)), "dash_group_norm_fwd")
+    return out, mean, rstd
+
+
+def group_norm_act_backward(dy, x, w, b, mean, rstd, groups: int, activation="silu", dx=None, workspace=None,
+                            stream=None):
+    """Gradients of group_norm_act_forward with respect to x, w and b.
+
+    dy: contiguous, of x's type and shape; mean, rstd: as the forward returned them. dx: an optional
+    contiguous tensor to write to. Returns (dx, dw, db), the last two fp32 [C] (None where w or b is
+    None)."""
+    if stream is not None:
+        with _using(stream, x):
+            return group_norm_act_backward(dy, x, w, b, mean, rstd, groups, activation, dx, workspace)
+    dev, pw, pb, sizes, xs, act, dtype = _gn_args(x, w, b, groups, activation)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return group_norm_act_backward(dy, x, w, b, mean, rstd, groups, activation, dx, workspace)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    for t, name in ((dy, "dy"), (dx, "dx")):
+        if t.dtype != x.dtype or t.shape != x.shape or not t.is_contiguous() or t.get_device() != dev:
+            _bad(f"{name}: expected contiguous, of the type and shape of x, on cuda:{dev}")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype != _F32 or t.shape != (sizes[0], groups) or not t.is_contiguous() or t.get_device() != dev:
+            _bad(f"{name}: expected contiguous float32 [N, groups] on cuda:{dev}")
+    dw = pdw = db = pdb = None
+    if w is not None:
+        dw = torch.empty(sizes[2], dtype=_F32, device=x.device)
+        pdw = dw.data_ptr()
+    if b is not None:
+        db = torch.empty(sizes[2], dtype=_F32, device=x.device)
+        pdb = db.data_ptr()
+    if workspace is None:
+        workspace = new_group_norm_workspace(*sizes, x.device)
+    _raise(_core.load().dash_group_norm_bwd(
+        dy.data_ptr(), x.data_ptr(), pw, pb, mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), pdw, pdb,
+        *_ws(workspace, dev), *sizes, xs[1], act, dtype, _stream(dev)), "dash_group_norm_bwd")
+    return dx, dw, db

@@ -3,7 +3,7 @@
 // x [N, S, C], channels c of group g = c / (C / G): xh = (x - mean) rstd, z = xh w + b, y = act(z).
 // All sums are sums over rows per channel, in a fixed order: forward s = sum(x - K), q = sum((x -
 // K)^2) with the channel's pivot K = its first value (so that a large mean costs no digits),
-// backward A = sum dz, B = sum dz xh with dz = dy act'(z). Of these come, per group,
+// backward A = sum dz, B = rstd sum dz (x - mean) with dz = dy act'(z). Of these come, per group,
 //   mean, var            from m_c = K + s / S and q - s^2 / S, joined over the group's channels
 //   c1 = mean(w A), c2 = mean(w B);  dx = rstd (w dz - c1 - xh c2),  dw = sum_n B, db = sum_n A.
 //
@@ -33,7 +33,6 @@ constexpr int kWarps = kThreads / 32;
 // Work is cut for a chip of 152 SMs whatever the device has.
 constexpr int kChip = 152;
 constexpr int kMaxShared = 232448;   // a CTA's shared memory at most
-constexpr int kMaxCluster = 16;
 
 enum Act : int { NONE = 0, SILU = 1 };
 
@@ -60,7 +59,12 @@ struct Args {
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + exp(-z)); the reciprocal of infinity is 0
+__device__ __forceinline__ float sigmoid(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-z)));
+  return r;
+}
 template <int ACT>
 __device__ __forceinline__ float activate(float z) { return ACT == SILU ? z * sigmoid(z) : z; }
 // dy times the activation's derivative at z
@@ -68,7 +72,7 @@ template <int ACT>
 __device__ __forceinline__ float activate_grad(float dy, float z) {
   if (ACT == NONE) return dy;
   const float s = sigmoid(z);
-  return dy * s * (1.f + fmaf(-z, s, z));
+  return dy * fmaf(s, fmaf(-z, s, z), s);          // s + s z (1 - s)
 }
 
 template <int V>
@@ -77,8 +81,38 @@ __device__ __forceinline__ void load_channels(const float* p, int c, float other
   for (int i = 0; i < V; ++i) v[i] = p ? __ldg(p + c + i) : other;
 }
 
+// Adds V values to their channels' sums. Forward: m the pivots; backward: z = (x - m) w + b, with
+// w holding w rstd.
+template <int V, int ACT, bool BWD>
+__device__ __forceinline__ void add_sums(const float (&f)[V], const float (&d)[V], const float (&m)[V],
+                                         const float (&w)[V], const float (&b)[V], float (&s)[V], float (&q)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float t = f[i] - m[i];
+    const float u = BWD ? activate_grad<ACT>(d[i], fmaf(t, w[i], b[i])) : t;
+    s[i] += u;
+    q[i] = fmaf(u, t, q[i]);
+  }
+}
+
+// y = act(x a + b) (the rounding of x a is of the size of x's own: 2^-24 |x| rstd w); dx = dz a + x k2 + k1 with a = w rstd, k2 = -rstd^2 c2, k1 = -rstd c1 - mean k2.
+template <int V, int ACT, bool BWD>
+__device__ __forceinline__ void apply(float (&f)[V], const float (&d)[V], const float (&a)[V], const float (&b)[V],
+                                      const float (&k1)[V], const float (&k2)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float z = fmaf(f[i], a[i], b[i]);
+    if (BWD) f[i] = fmaf(activate_grad<ACT>(d[i], z), a[i], fmaf(f[i], k2[i], k1[i]));
+    else f[i] = activate<ACT>(z);
+  }
+}
+
+// Row lanes' sums in block_sums: a warp's lanes are added first where pieces of a row are few.
+__host__ __device__ constexpr bool by_warps(int nv) { return nv <= 16 && (nv & (nv - 1)) == 0; }
+__host__ __device__ constexpr int sum_rows(int nv) { return by_warps(nv) ? kWarps : kThreads / nv; }
+
 // Sums of a block's threads that hold the same channels: thread t holds channels V (t % nv) of row
-// lane t / nv. `red` has room for kThreads * V entries; channel c's sum goes to out[c].
+// lane t / nv. `red` has room for sum_rows(nv) * nv * V entries; channel c's sum goes to out[c].
 template <int V>
 __device__ __forceinline__ void block_sums(float (&s)[V], float (&q)[V], int nv, float2* red, float2* out) {
   const int t = threadIdx.x, cs = nv * V;
@@ -86,7 +120,7 @@ __device__ __forceinline__ void block_sums(float (&s)[V], float (&q)[V], int nv,
   int row = t / nv;
   const int v = t - row * nv;
   bool mine = row < lanes;
-  if (nv <= 16 && (nv & (nv - 1)) == 0) {          // lanes of a warp first
+  if (by_warps(nv)) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       if (o >= nv) {
@@ -223,15 +257,15 @@ struct Seat {
 
 // Resident, both directions. Shared memory: the pieces (x, then dy), the sums.
 template <typename T, int V, int ACT, bool BWD>
-__global__ void __launch_bounds__(kThreads) resident_kernel(const __grid_constant__ Args a, int pieces) {
+__global__ void __launch_bounds__(kThreads, 2) resident_kernel(const __grid_constant__ Args a, int pieces) {
   constexpr int PB = V * (int)sizeof(T);
   extern __shared__ __align__(16) char gn_smem[];
   char* xs = gn_smem + threadIdx.x * PB;
   char* ds = xs + (size_t)pieces * kThreads * PB;
-  float2* red = (float2*)(gn_smem + (((BWD ? 2 : 1) * pieces * kThreads * PB + 15) & ~15));
-  float2* sums = red + kThreads * V;               // [slab] this CTA's
+  float2* sums = (float2*)(gn_smem + (((BWD ? 2 : 1) * pieces * kThreads * PB + 15) & ~15));   // [slab] this CTA's
   float2* total = sums + a.slab;                   // [slab] the cluster's
   float2* grp = total + a.slab;                    // [groups] mean, rstd; backward: c1, c2
+  float2* red = grp + a.slab / a.cpg;
   if (BWD) grid_next();
   const int ranks = (int)cluster_size(), rank = (int)ptx::cluster_rank();
   const Seat<V> st(a, blockIdx.x / ranks, rank);
@@ -247,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) resident_kernel(const __grid_constan
       if (BWD) fetch_piece<T, V>(ds + (size_t)k * kThreads * PB, dy + (long long)r * a.C + c);
     }
   }
-  float w[V], b[V], m[V], rs[V], s[V] = {}, q[V] = {};
+  float w[V], b[V], m[V], s[V] = {}, q[V] = {};
   if (st.on) {
     load_channels<V>(a.w, c, 1.f, w);
     load_channels<V>(a.b, c, 0.f, b);
@@ -256,13 +290,10 @@ __global__ void __launch_bounds__(kThreads) resident_kernel(const __grid_constan
       for (int i = 0; i < V; ++i) {
         const int g = st.n * a.G + (c + i) / a.cpg;
         m[i] = __ldg(a.mean + g);
-        rs[i] = __ldg(a.rstd + g);
+        w[i] *= __ldg(a.rstd + g);
       }
     } else {
-      float f[V];                                  // the pivots
-      read_piece<T, V>((const char*)(x + c), f);
-#pragma unroll
-      for (int i = 0; i < V; ++i) m[i] = f[i];
+      read_piece<T, V>((const char*)(x + c), m);   // the pivots
     }
   }
   fetch_wait();
@@ -271,23 +302,8 @@ __global__ void __launch_bounds__(kThreads) resident_kernel(const __grid_constan
     for (int r = st.r0 + st.row; r < st.r1; r += st.lanes, ++k) {
       float f[V], d[V];
       read_piece<T, V>(xs + (size_t)k * kThreads * PB, f);
-      if constexpr (BWD) {
-        read_piece<T, V>(ds + (size_t)k * kThreads * PB, d);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xh = (f[i] - m[i]) * rs[i];
-          const float dz = activate_grad<ACT>(d[i], fmaf(xh, w[i], b[i]));
-          s[i] += dz;
-          q[i] = fmaf(dz, xh, q[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float t = f[i] - m[i];
-          s[i] += t;
-          q[i] = fmaf(t, t, q[i]);
-        }
-      }
+      if constexpr (BWD) read_piece<T, V>(ds + (size_t)k * kThreads * PB, d);
+      add_sums<V, ACT, BWD>(f, d, m, w, b, s, q);
     }
   }
   block_sums<V>(s, q, st.nv, red, sums);
@@ -300,6 +316,7 @@ __global__ void __launch_bounds__(kThreads) resident_kernel(const __grid_constan
       t.x += y.x;
       t.y += y.y;
     }
+    if (BWD) t.y *= __ldg(a.rstd + st.n * a.G + (st.c0 + e) / a.cpg);
     total[e] = t;
     if (BWD && rank == 0) a.chan[(long long)st.n * a.C + st.c0 + e] = t;
   }
@@ -332,16 +349,20 @@ __global__ void __launch_bounds__(kThreads) resident_kernel(const __grid_constan
   }
   __syncthreads();
   if (st.on) {
-    float c1[V], c2[V];
+    float k1[V], k2[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float2 t = grp[(st.v * V + i) / a.cpg];
+      const int gs = (st.v * V + i) / a.cpg;
+      const float2 t = grp[gs];
       if (BWD) {
-        c1[i] = -rs[i] * t.x;
-        c2[i] = -rs[i] * t.y;
+        const float rs = __ldg(a.rstd + st.n * a.G + g0 + gs);
+        b[i] = fmaf(-m[i], w[i], b[i]);
+        k2[i] = -rs * rs * t.y;
+        k1[i] = fmaf(-m[i], k2[i], -rs * t.x);
       } else {
-        m[i] = t.x;
-        rs[i] = t.y;
+        w[i] *= t.y;
+        b[i] = fmaf(-t.x, w[i], b[i]);
+        k1[i] = k2[i] = 0.f;
       }
     }
     int k = 0;
@@ -349,12 +370,7 @@ __global__ void __launch_bounds__(kThreads) resident_kernel(const __grid_constan
       float f[V], d[V];
       read_piece<T, V>(xs + (size_t)k * kThreads * PB, f);
       if constexpr (BWD) read_piece<T, V>(ds + (size_t)k * kThreads * PB, d);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float xh = (f[i] - m[i]) * rs[i], z = fmaf(xh, w[i], b[i]);
-        if (BWD) f[i] = fmaf(activate_grad<ACT>(d[i], z), w[i] * rs[i], fmaf(xh, c2[i], c1[i]));
-        else f[i] = activate<ACT>(z);
-      }
+      apply<V, ACT, BWD>(f, d, w, b, k1, k2);
       write_piece<T, V>(out + (long long)r * a.C + c, f);
     }
   }
@@ -383,16 +399,69 @@ struct Span {
   }
 };
 
+// Rows that a thread has in flight in the passes, in shared memory, as copies that need no
+// registers: 64 KB a block. (With two to four rows in registers instead the sums of 2 x 65536 x 512
+// took 31 us forward and 78 backward.)
+template <bool BWD>
+constexpr int kAhead = BWD ? 4 : 8;
+template <typename T, int V, bool BWD>
+constexpr int kRingBytes = V > 1 ? kAhead<BWD> * (BWD ? 2 : 1) * kThreads * 16 : 0;
+
+// Calls f(x's values, dy's values) for `left` pieces, the first at px and pd, step_x and step_d apart.
+template <typename T, int V, bool BWD, typename F>
+__device__ __forceinline__ void for_pieces(char* ring, const T* px, const T* pd, long long step_x, long long step_d,
+                                           int left, F f) {
+  if constexpr (V > 1) {
+    constexpr int K = kAhead<BWD>, SLOT = (BWD ? 2 : 1) * kThreads * 16;
+    char* mine = ring + threadIdx.x * 16;
+    int asked = 0;
+    auto ask = [&](int slot) {
+      if (asked < left) {
+        fetch_piece<T, V>(mine + slot * SLOT, px);
+        if (BWD) fetch_piece<T, V>(mine + slot * SLOT + kThreads * 16, pd);
+        px += step_x;
+        pd += step_d;
+        ++asked;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < K; ++k) ask(k);
+    for (int i = 0; i < left;) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (i < left) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(K - 1) : "memory");
+          float x[V], d[V];
+          read_piece<T, V>(mine + k * SLOT, x);
+          if constexpr (BWD) read_piece<T, V>(mine + k * SLOT + kThreads * 16, d);
+          ask(k);
+          f(x, d);
+          ++i;
+        }
+      }
+    }
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < left; ++i) {
+      float x[V], d[V];
+      x[0] = to_f32(px[i * step_x]);
+      if constexpr (BWD) d[0] = to_f32(pd[i * step_d]);
+      f(x, d);
+    }
+  }
+}
+
 template <typename T, int V, int ACT, bool BWD>
-__global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 2) sums_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) char gn_smem[];
-  float2* red = (float2*)gn_smem;
-  float2* sums = red + kThreads * V;
+  float2* sums = (float2*)(gn_smem + kRingBytes<T, V, BWD>);
+  float2* red = sums + a.cols * V;
   grid_next();
   const Span<V> st(a, false);
   const T* x = (const T*)a.x + st.n * a.sb;
   const T* dy = (const T*)a.dy + (long long)st.n * a.S * a.C;
-  float w[V], b[V], m[V], rs[V], s[V] = {}, q[V] = {};
+  float w[V], b[V], m[V], s[V] = {}, q[V] = {};
   if (st.on) {
     if constexpr (BWD) {
       load_channels<V>(a.w, st.c, 1.f, w);
@@ -401,33 +470,15 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
       for (int i = 0; i < V; ++i) {
         const int g = st.n * a.G + (st.c + i) / a.cpg;
         m[i] = __ldg(a.mean + g);
-        rs[i] = __ldg(a.rstd + g);
+        w[i] *= __ldg(a.rstd + g);
       }
     } else {
       read_piece<T, V>((const char*)(x + st.c), m);
     }
-#pragma unroll 4
-    for (int r = st.r0 + st.row; r < st.r1; r += st.lanes) {
-      float f[V], d[V];
-      read_piece<T, V>((const char*)(x + r * a.ss + st.c), f);
-      if constexpr (BWD) {
-        read_piece<T, V>((const char*)(dy + (long long)r * a.C + st.c), d);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xh = (f[i] - m[i]) * rs[i];
-          const float dz = activate_grad<ACT>(d[i], fmaf(xh, w[i], b[i]));
-          s[i] += dz;
-          q[i] = fmaf(dz, xh, q[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float t = f[i] - m[i];
-          s[i] += t;
-          q[i] = fmaf(t, t, q[i]);
-        }
-      }
-    }
+    const long long row = st.r0 + st.row;
+    for_pieces<T, V, BWD>(gn_smem, x + row * a.ss + st.c, dy + row * a.C + st.c, st.lanes * a.ss, (long long)st.lanes * a.C,
+                          (st.r1 - st.r0 - st.row + st.lanes - 1) / st.lanes,
+                          [&](float (&f)[V], float (&d)[V]) { add_sums<V, ACT, BWD>(f, d, m, w, b, s, q); });
   }
   block_sums<V>(s, q, st.nv, red, sums);
   __syncthreads();
@@ -436,40 +487,45 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
 }
 
 // The chunks' sums of a group's channels, in order, and what follows from them; a block a (sample,
-// group): 32 lanes for the chunks of each channel.
+// group). Threads side by side take channels side by side, the others further chunks.
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) char gn_smem[];
   float2* chan = (float2*)gn_smem;                 // [cpg]
-  __shared__ float2 parts[kWarps];
+  __shared__ float2 parts[kThreads];
+  __shared__ float pivots[BWD ? 1 : kThreads];
   grid_next();
-  grid_wait();
   const int n = blockIdx.x / a.G, g = blockIdx.x - n * a.G;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the pivots, which no kernel of this call writes, fetched ahead
+  float first = 0.f;
+  if (!BWD && a.S > 0 && threadIdx.x < a.cpg) first = to_f32(((const T*)a.x)[n * a.sb + (long long)g * a.cpg + threadIdx.x]);
+  grid_wait();
   const float2* from = a.part + (long long)n * a.chunks * a.C + (long long)g * a.cpg;
-  // a warp takes 32 channels side by side, its lanes a channel each, so that reads are whole lines
-  const int cols = min(32, a.cpg), per = 32 / cols, sub = lane / cols;
-  for (int c0 = warp * cols; c0 < a.cpg; c0 += kWarps * cols) {
-    const int c = c0 + lane - sub * cols;
+  if (!BWD) pivots[threadIdx.x] = first;
+  const float rs = BWD ? __ldg(a.rstd + blockIdx.x) : 1.f;
+  for (int c0 = 0; c0 < a.cpg; c0 += kThreads) {
+    const int cols = min(kThreads, a.cpg - c0), per = kThreads / cols;
+    const int sub = (int)threadIdx.x / cols, c = (int)threadIdx.x - sub * cols;
     float2 t = make_float2(0.f, 0.f);
-    if (sub < per && c < a.cpg)
+    if (sub < per)
 #pragma unroll 8
       for (int k = sub; k < a.chunks; k += per) {
-        const float2 x = from[(long long)k * a.C + c];
+        const float2 x = from[(long long)k * a.C + c0 + c];
         t.x += x.x;
         t.y += x.y;
       }
-    for (int p = 1; p < per; ++p) {
-      const float ox = __shfl_sync(0xffffffffu, t.x, (lane + p * cols) & 31);
-      const float oy = __shfl_sync(0xffffffffu, t.y, (lane + p * cols) & 31);
-      if (sub == 0) {
-        t.x += ox;
-        t.y += oy;
+    parts[threadIdx.x] = t;
+    __syncthreads();
+    if (sub == 0) {
+      for (int p = 1; p < per; ++p) {
+        t.x += parts[p * cols + c].x;
+        t.y += parts[p * cols + c].y;
       }
+      chan[c0 + c] = make_float2(t.x, t.y * rs);
     }
-    if (sub == 0 && c < a.cpg) chan[c] = t;
+    __syncthreads();
   }
-  __syncthreads();
   if constexpr (BWD) {
     float c1 = 0.f, c2 = 0.f;
     for (int c = threadIdx.x; c < a.cpg; c += kThreads) {
@@ -495,7 +551,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   } else if (warp == 0) {
     const T* x = (const T*)a.x + n * a.sb + (long long)g * a.cpg;
     float mean, rstd;
-    group_stats(a, [&](int e) { return a.S > 0 ? to_f32(x[e]) : 0.f; }, [&](int e) { return chan[e]; }, &mean, &rstd);
+    group_stats(a, [&](int e) { return e < kThreads ? pivots[e] : to_f32(x[e]); }, [&](int e) { return chan[e]; }, &mean,
+                &rstd);
     if (lane == 0) {
       a.mean[blockIdx.x] = mean;
       a.rstd[blockIdx.x] = rstd;
@@ -504,45 +561,40 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 }
 
 template <typename T, int V, int ACT, bool BWD>
-__global__ void __launch_bounds__(kThreads) apply_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 2) apply_kernel(const __grid_constant__ Args a) {
   grid_next();
   grid_wait();
   const Span<V> st(a, true);
   if (!st.on) return;
-  const T* x = (const T*)a.x + st.n * a.sb;
-  const long long cont = (long long)st.n * a.S * a.C;
-  const T* dy = (const T*)a.dy + cont;
-  T* out = (T*)a.out + cont;
-  float w[V], b[V], m[V], rs[V], c1[V], c2[V];
+  float w[V], b[V], k1[V], k2[V];
   load_channels<V>(a.w, st.c, 1.f, w);
   load_channels<V>(a.b, st.c, 0.f, b);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int g = st.n * a.G + (st.c + i) / a.cpg;
-    m[i] = a.mean[g];
-    rs[i] = a.rstd[g];
+    const float m = a.mean[g], rs = a.rstd[g];
+    w[i] *= rs;
+    b[i] = fmaf(-m, w[i], b[i]);
+    k1[i] = k2[i] = 0.f;
     if (BWD) {
       const float2 t = a.coef[g];
-      c1[i] = -rs[i] * t.x;
-      c2[i] = -rs[i] * t.y;
+      k2[i] = -rs * rs * t.y;
+      k1[i] = fmaf(-m, k2[i], -rs * t.x);
     }
   }
   // backwards within the chunk too
-  const int steps = (st.r1 - st.r0 - st.row + st.lanes - 1) / st.lanes;
-#pragma unroll 4
-  for (int k = steps - 1; k >= 0; --k) {
-    const int r = st.r0 + st.row + k * st.lanes;
-    float f[V], d[V];
-    read_piece<T, V>((const char*)(x + r * a.ss + st.c), f);
-    if constexpr (BWD) read_piece<T, V>((const char*)(dy + (long long)r * a.C + st.c), d);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float xh = (f[i] - m[i]) * rs[i], z = fmaf(xh, w[i], b[i]);
-      if (BWD) f[i] = fmaf(activate_grad<ACT>(d[i], z), w[i] * rs[i], fmaf(xh, c2[i], c1[i]));
-      else f[i] = activate<ACT>(z);
-    }
-    write_piece<T, V>(out + (long long)r * a.C + st.c, f);
-  }
+  extern __shared__ __align__(16) char gn_smem[];
+  const int left = (st.r1 - st.r0 - st.row + st.lanes - 1) / st.lanes;
+  const long long step = (long long)st.lanes * a.C;
+  const long long row = st.r0 + st.row + (long long)(left - 1) * st.lanes;
+  const long long cont = (long long)st.n * a.S * a.C + row * a.C + st.c;
+  T* out = (T*)a.out + cont;
+  for_pieces<T, V, BWD>(gn_smem, (const T*)a.x + st.n * a.sb + row * a.ss + st.c, (const T*)a.dy + cont,
+                        -st.lanes * a.ss, -step, left, [&](float (&f)[V], float (&d)[V]) {
+                          apply<V, ACT, BWD>(f, d, w, b, k1, k2);
+                          write_piece<T, V>(out, f);
+                          out -= step;
+                        });
 }
 
 // dw and db: the samples' channel sums, in order.
@@ -573,54 +625,69 @@ int lcm(int a, int b) {
   return a / x * b;
 }
 
+// Entries that block_sums needs where rows of `all` pieces are taken `nv` at a time (the last time
+// fewer, which may need more).
+long long sum_room(int all, int nv, int V) {
+  const int last = all % nv ? all % nv : nv;
+  return std::max((long long)sum_rows(nv) * nv, (long long)sum_rows(last) * last) * V;
+}
+
 // How a call is cut. resident: clusters of `cluster` CTAs; else chunks of rows.
 struct Plan {
   bool resident;
   int slab, slabs, cluster, rows, pieces, smem;
   int chunks, cols;
 };
+
+// The cut is the one that takes the least time by what the two ways measured (us on the GPU).
+// Resident: each round of the chip's CTAs takes 6 (backward 9) and what its bytes take at 44 GB/s an
+// SM, a third more where a row of a slab is under 64 bytes, and 1 more for each doubling of the
+// cluster (clusters of 8 and 16 wait long for their places: never). In passes: 11 (backward 15) and
+// what three (five) sweeps take at 6.5 TB/s. Measured, resident / in passes: 4 x 4096 x 512 bf16
+// forward 12.6 / 19.2, backward 28.5 / 29.9; 4 x 1024 x 512 9 / 12.7 and 13 / 20; 8 x 1024 x 1280
+// 15.3 / 20.4 and 34 / 31.5; 4 x 16384 x 128 fp32 28 / 17.7 and 51 / 26.
 Plan make_plan(int N, int S, int C, int G, int V, int e, bool bwd) {
   Plan p = {};
   const int cpg = C / G;
-  if (S > 0) {
-    // a slab of whole groups and whole pieces, its rows at least two sectors where C allows it
-    const int unit = lcm(cpg, V);
-    int slab = unit;
-    while (slab * e < 64 && slab + unit <= C) slab += unit;
-    const int nv = slab / V;
-    if (slab <= C && nv <= kThreads && slab <= 2048) {
-      const int lanes = kThreads / nv, slabs = ceil_div(C, slab);
-      const long long slots = (long long)kThreads * V * e * (bwd ? 2 : 1);     // bytes of one piece a thread
-      // the smallest cluster whose CTAs hold their rows in a third of an SM's shared memory, or
-      // that fills the chip twice; larger ones only to fit at all
-      for (int cl = 1; cl <= kMaxCluster; cl *= 2) {
-        const int rows = ceil_div(S, cl), pieces = ceil_div(rows, lanes);
-        const long long bytes = pieces * slots;
-        const long long smem =
-            (long long)round_up_to(bytes, 16) + ((long long)kThreads * V + 2 * slab + slab / cpg) * (int)sizeof(float2);
-        const bool roomy = bytes <= 56 * 1024 || (long long)N * slabs * cl >= 2 * kChip;
-        if (smem <= kMaxShared && (roomy || cl == kMaxCluster || ceil_div(S, 2 * cl) < lanes)) {
-          p.resident = true;
-          p.slab = slab;
-          p.slabs = slabs;
-          p.cluster = cl;
-          p.rows = rows;
-          p.pieces = pieces;
-          p.smem = (int)smem;
-          return p;
-        }
+  const double data = (double)N * S * C * e;
+  double best = (bwd ? 15 : 11) + data * (bwd ? 5 : 3) / 6.5e6;
+  const int unit = S > 0 ? lcm(cpg, V) : C + 1;      // slabs are whole groups and whole pieces
+  for (int slab = unit; slab <= C && slab <= 2048 && slab / V <= kThreads; slab += slab < unit * 4 ? unit : slab) {
+    if (slab * e < 32 && slab + unit <= C) continue;
+    if (slab * e > 512 && slab > unit) break;
+    const int nv = slab / V, lanes = kThreads / nv, slabs = ceil_div(C, slab);
+    for (int cl = 1; cl <= 4; cl *= 2) {
+      const int rows = ceil_div(S, cl), pieces = ceil_div(rows, lanes);
+      const long long bytes = (long long)pieces * kThreads * V * e * (bwd ? 2 : 1);
+      const long long smem = (long long)round_up_to(bytes, 16) +
+                             (sum_room(C / V, nv, V) + 2 * slab + slab / cpg) * (long long)sizeof(float2);
+      if (smem > kMaxShared) continue;
+      const int held = smem + 1024 <= kMaxShared / 2 ? 2 : 1;
+      const long long ctas = (long long)N * slabs * cl, rounds = ceil_div<long long>(ctas, kChip * held);
+      const double moved = (double)rows * slab * e * (bwd ? 3 : 2) * std::min<double>(held, std::max(1.0, (double)ctas / kChip));
+      const double t = rounds * ((bwd ? 9 : 6) + moved * (slab * e < 64 ? 1.33 : 1.0) / 44e3) + (cl == 4 ? 2 : cl - 1);
+      if (t < best) {
+        best = t;
+        p.resident = true;
+        p.slab = slab;
+        p.slabs = slabs;
+        p.cluster = cl;
+        p.rows = rows;
+        p.pieces = pieces;
+        p.smem = (int)smem;
       }
     }
   }
+  if (p.resident) return p;
   const int nv = C / V;
   p.cols = std::min(nv, kThreads);
   const int lanes = kThreads / p.cols;
-  // chunks: several blocks an SM, each with rows enough to pay for its sums
-  const long long blocks = 8ll * kChip;
+  // chunks: the two blocks that an SM holds, each with rows enough to pay for its sums
+  const long long blocks = 2ll * kChip;
   const long long want = std::max<long long>(1, blocks / std::max<long long>(1, (long long)N * ceil_div(nv, p.cols)));
   p.rows = std::max(8 * lanes, (int)ceil_div<long long>(S, want));
   p.chunks = ceil_div(S, p.rows);
-  p.smem = (kThreads * V + p.cols * V) * (int)sizeof(float2);
+  p.smem = (int)(sum_room(nv, p.cols, V) + p.cols * V) * (int)sizeof(float2);
   return p;
 }
 
@@ -654,7 +721,6 @@ dash_status_t launch(Args a, cudaStream_t stream) {
   if (p.resident) {
     const auto kernel = resident_kernel<T, V, ACT, BWD>;
     DASH_TRY(allow_shared((const void*)kernel, p.smem));
-    if (p.cluster > 8) DASH_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.N * p.slabs * p.cluster);
     cfg.blockDim = dim3(kThreads);
@@ -670,13 +736,17 @@ dash_status_t launch(Args a, cudaStream_t stream) {
   } else {
     const dim3 grid((unsigned)a.N * p.chunks, ceil_div(a.C / V, p.cols));
     if (grid.x > 0) {
-      DASH_TRY(allow_shared((const void*)sums_kernel<T, V, ACT, BWD>, p.smem));
-      sums_kernel<T, V, ACT, BWD><<<grid, kThreads, p.smem, stream>>>(a);
+      const int smem = p.smem + kRingBytes<T, V, BWD>;
+      DASH_TRY(allow_shared((const void*)sums_kernel<T, V, ACT, BWD>, smem));
+      sums_kernel<T, V, ACT, BWD><<<grid, kThreads, smem, stream>>>(a);
       DASH_TRY(cudaGetLastError());
     }
     if (a.N > 0)
       DASH_TRY(launch_after(join_kernel<T, BWD>, dim3((unsigned)a.N * a.G), kThreads, a.cpg * sizeof(float2), stream, a));
-    if (grid.x > 0) DASH_TRY(launch_after(apply_kernel<T, V, ACT, BWD>, grid, kThreads, 0, stream, a));
+    if (grid.x > 0) {
+      DASH_TRY(allow_shared((const void*)apply_kernel<T, V, ACT, BWD>, kRingBytes<T, V, BWD>));
+      DASH_TRY(launch_after(apply_kernel<T, V, ACT, BWD>, grid, kThreads, kRingBytes<T, V, BWD>, stream, a));
+    }
   }
   if (BWD && (a.dw || a.db))
     DASH_TRY(launch_after(weight_grad_kernel, dim3(ceil_div(a.C, 256)), 256, 0, stream, a));

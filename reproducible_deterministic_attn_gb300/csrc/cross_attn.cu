@@ -1,9 +1,10 @@
 // Host side of cross attention (dash_cross_attn_*): argument checks, how the work is cut, tensor
-// maps and launches. The kernels are in cross_fwd.cuh and cross_bwd.cuh.
+// maps and launches. The kernels are in cross_fwd.cuh, cross_bwd.cuh
+// and cross_bwd_rows.cuh.
 #include <algorithm>
 #include <climits>
 
-#include "cross_bwd.cuh"
+#include "cross_bwd_rows.cuh"
 #include "cross_fwd.cuh"
 #include "dash_train.h"
 #include "host_common.h"
@@ -181,84 +182,99 @@ bool distinct(const long long* st, int B, int S, int H) {
   return (B < 2 || st[0] > 0) && (S < 2 || st[1] > 0) && (H < 2 || st[2] > 0);
 }
 
-// How the backward is cut: row segments and key segments of a group. Every cut costs partials
-// (written and read once more) and the start of another unit, too few leave SMs idle, so the plan
-// is the cheapest by a count of tasks: a unit takes its tasks, one more for each key tile (the
-// read-out of dK and dV) and two to start; units run in rounds of the chip; partials cost what
-// memory takes for them (a task is about 3 us, in which the chip moves 15 MB). A segment has at
-// most 128 row tiles: the tensor core truncates its additions, which over 16384 rows of one sign
-// loses at most 2^-15.5 of a sum.
+// How the backward is cut: cross_keys_kernel's row segments and cross_rows_kernel's key segments.
+// Every cut costs partials (written and read once more) and the start of another unit, too few leave
+// SMs idle, so each is the cheapest by a count of tasks of 128 x 128 scores: a unit takes its tasks
+// and `start` more, units run in rounds of the chip, and partials cost what memory takes for them (a
+// task is about 2 us, in which the chip moves 10 MB). Where batches have lengths of their own, which
+// the host does not know, a fifth of the units is taken to be empty. A row segment has at most 128 row tiles: the
+// tensor core truncates its additions, which over 16384 rows of one sign loses at most 2^-15.5 of a
+// sum.
+int best_cut(long long units, int tasks, int least, double start, double part_bytes, bool ragged) {
+  int cut = least;
+  double best = 1e300;
+  for (int n = least; n <= tasks; ++n) {
+    const int per = ceil_div(tasks, n);
+    if (ceil_div(tasks, per) != n) continue;
+    const double rounds = (double)ceil_div<long long>(ragged ? ceil_div<long long>(4 * units * n, 5) : units * n, kChip);
+    const double cost = rounds * (per + start) + (n > 1 ? 1 + 2 * n * part_bytes / 10e6 : 0.0);
+    if (cost < best) {
+      best = cost;
+      cut = n;
+    }
+    if (units * n > 8 * kChip) break;
+  }
+  return cut;
+}
 struct BwdPlan {
+  bool one;                          // one key tile: cross_keys_kernel forms dQ too
   int qsegs, qper, ksegs, kper;
-  size_t nnl, delta, dq_acc, dkv_part, total;
+  size_t nnl, delta, dq_part, dkv_part, total;
 };
-BwdPlan bwd_plan(const Shape& s) {
+BwdPlan bwd_plan(const Shape& s, bool ragged) {
   BwdPlan p = {};
   const long long groups = (long long)s.B * s.Hk;
   const int nt = s.ntile, nk = s.nk, dt = s.D <= 64 ? 64 : 128;
-  p.kper = std::max(1, nk);
-  p.qper = std::max(1, nt);
+  const size_t rows = (size_t)groups * nt * kTile, keys = (size_t)groups * nk * kTile;
+  p.one = nk == 1;
+  p.qsegs = p.ksegs = p.qper = p.kper = 1;
   if (nt > 0 && nk > 0) {
-    double best = 1e300;
-    const int most = (int)std::min<long long>(nt, ceil_div(nt, 128) + 2 * kChip / std::min<long long>(groups, 2 * kChip));
-    for (int qs = ceil_div(nt, 128); qs <= most; ++qs) {
-      const int qper = ceil_div(nt, qs);
-      if (ceil_div(nt, qper) != qs) continue;
-      for (int ks = 1; ks <= nk; ks = ks < nk && 2 * ks > nk ? nk : 2 * ks) {
-        const int kper = ceil_div(nk, ks);
-        if (ceil_div(nk, kper) != ks) continue;
-        if (ks > 1 && groups * qs * ks > 16 * kChip) break;
-        const long long units = groups * qs * ks;
-        const double rounds = (double)ceil_div<long long>(units, kChip);
-        const double unit = (double)kper * (qper + 1) + 2;
-        const double rows = (double)groups * nt * kTile * dt * 4, keys = (double)groups * nk * kTile * dt * 8;
-        const double bytes = (qs > 1 ? 2 * qs * keys : 0) + (ks > 1 ? 2 * ks * rows : 0);
-        // few units run with what they have: the chip's last round is not cut finer than a unit
-        const double cost = std::max(rounds * unit, (double)units * unit / kChip) + bytes / 15e6 + (qs > 1 || ks > 1);
-        if (cost < best) {
-          best = cost;
-          p.qsegs = qs;
-          p.qper = qper;
-          p.ksegs = ks;
-          p.kper = kper;
-        }
-      }
+    p.qsegs = best_cut(groups * nk, nt, ceil_div(nt, 128), 2, (double)keys * dt * 8, ragged);
+    p.qper = ceil_div(nt, p.qsegs);
+    if (!p.one) {
+      p.ksegs = best_cut(groups * nt, nk, 1, 2, (double)rows * dt * 4, ragged);
+      p.kper = ceil_div(nk, p.ksegs);
     }
-  } else {
-    p.qsegs = nt > 0 ? 1 : 0;                      // no units; dk and dv (or dq) are zeros
-    p.ksegs = 1;
   }
-  const size_t rows = (size_t)groups * nt * kTile;
   p.nnl = kWsHeaderBytes;
   p.delta = p.nnl + rows * sizeof(float);
-  p.dq_acc = round_up_to(p.delta + rows * sizeof(float), 256);
-  p.dkv_part = p.dq_acc + (p.kper > 1 || p.ksegs > 1 ? p.ksegs * rows * dt * sizeof(float) : 0);
-  p.total = p.dkv_part + (p.qsegs > 1 ? (size_t)p.qsegs * groups * nk * 2 * kTile * dt * sizeof(float) : 0);
+  p.dq_part = round_up_to(p.delta + rows * sizeof(float), 256);
+  p.dkv_part = p.dq_part + (p.ksegs > 1 ? p.ksegs * rows * dt * sizeof(float) : 0);
+  p.total = p.dkv_part + (p.qsegs > 1 ? p.qsegs * keys * 2 * dt * sizeof(float) : 0);
   p.total = round_up_to(std::max(p.total, kWsHeaderBytes), 256);
   return p;
 }
 
+template <int DT, bool DQ>
+dash_status_t launch_keys(BwdArgs a, const Maps& maps, int sms, cudaStream_t stream) {
+  using L = KeysLay<DT, DQ>;
+  const dash_status_t st = prepare((const void*)cross_keys_kernel<DT, DQ>, L::ALLOC, L::REGS_LAUNCH);
+  if (st != DASH_OK) return st;
+  a.units = (int)((long long)a.s.B * a.s.Hk * a.s.nk * a.qsegs);
+  DASH_TRY(dash::launch_after(cross_keys_kernel<DT, DQ>, dim3(std::min(a.units, sms)), kThreads, L::ALLOC, stream, a, maps));
+  return DASH_OK;
+}
+
 template <int DT>
-dash_status_t launch_bwd(BwdArgs a, const Maps& maps, cudaStream_t stream) {
+dash_status_t launch_bwd(BwdArgs a, bool one, const Maps& maps, cudaStream_t stream) {
   int sms = 0;
   if (const dash_status_t e = sm_count(&sms)) return e;
-  if (a.units > 0) {
-    const dash_status_t st = prepare((const void*)cross_bwd_kernel<DT>, BwdLay<DT>::ALLOC, BwdLay<DT>::REGS_LAUNCH);
-    if (st != DASH_OK) return st;
-  }
   const long long rows = (long long)a.s.B * a.s.Hk * a.s.ntile * kTile;
-  cross_pre_kernel<<<(unsigned)std::max(1ll, ceil_div<long long>(rows, 16)), 256, 0, stream>>>(a);
+  const bool work = a.s.ntile > 0 && a.s.nk > 0;
+  const unsigned row_blocks = (unsigned)std::max(1ll, ceil_div<long long>(rows, 16 * kPreRows));
+  // key tiles that no unit visits exist only behind lengths, or where there are no rows
+  const unsigned key_blocks =
+      a.s.lens || !work ? (unsigned)ceil_div<long long>((long long)a.s.B * a.s.Sk * a.s.Hk, 16) : 0;
+  cross_pre_kernel<<<row_blocks + key_blocks, 256, 0, stream>>>(a, row_blocks);
   DASH_TRY(cudaGetLastError());
-  if (a.units > 0)
-    DASH_TRY(dash::launch_after(cross_bwd_kernel<DT>, dim3(std::min(a.units, sms)), kThreads, BwdLay<DT>::ALLOC,
+  if (!work) return DASH_OK;
+  if (const dash_status_t e = one ? launch_keys<DT, true>(a, maps, sms, stream)
+                                  : launch_keys<DT, false>(a, maps, sms, stream))
+    return e;
+  const int per = a.s.D / 8;
+  if (a.qsegs > 1) {
+    const unsigned blocks = (unsigned)ceil_div<long long>((long long)a.s.B * a.s.Sk * a.s.Hk * per, 256);
+    DASH_TRY(dash::launch_after(cross_join_keys_kernel<DT>, dim3(blocks), 256, 0, stream, a));
+  }
+  if (!one) {
+    const dash_status_t st = prepare((const void*)cross_rows_kernel<DT>, RowsLay<DT>::ALLOC, kRowsRegsLaunch);
+    if (st != DASH_OK) return st;
+    a.units = (int)((long long)a.s.B * a.s.Hk * a.s.ntile * a.ksegs);
+    DASH_TRY(dash::launch_after(cross_rows_kernel<DT>, dim3(std::min(a.units, sms)), kRowsThreads, RowsLay<DT>::ALLOC,
                                 stream, a, maps));
-  if (a.s.lens || a.units == 0 || a.qsegs > 1 || a.ksegs > 1) {
-    const int per = a.s.D / 8;
-    const long long tiles = (long long)a.s.B * a.s.Hk * a.s.ntile;
-    const unsigned dqb = a.s.lens || a.units == 0 || a.ksegs > 1 ? (unsigned)tiles : 0;
-    const unsigned dkb = (unsigned)ceil_div<long long>((long long)a.s.B * a.s.Sk * a.s.Hk * per, 256);
-    if (dqb + dkb > 0)
-      DASH_TRY(dash::launch_after(cross_grad_join_kernel<DT>, dim3(dqb + dkb), 256, 0, stream, a, dqb));
+    if (a.ksegs > 1)
+      DASH_TRY(dash::launch_after(cross_join_rows_kernel<DT>, dim3((unsigned)ceil_div<long long>(rows * per, 256)), 256,
+                                  0, stream, a));
   }
   return DASH_OK;
 }
@@ -314,8 +330,11 @@ dash_status_t dash_cross_attn_fwd(const void* q, const void* k, const void* v, c
 
 size_t dash_cross_attn_bwd_workspace_size(int B, int Sq, int Sk, int Hq, int Hk, int D) {
   if (!sizes_ok(B, Sq, Sk, Hq, Hk, D)) return 0;
-  return std::max(bwd_plan(make_shape(B, Sq, Sk, Hq, Hk, D, true)).total,
-                  bwd_plan(make_shape(B, Sq, Sk, Hq, Hk, D, false)).total);
+  size_t most = 0;
+  for (bool pack : {false, true})
+    for (bool ragged : {false, true})
+      most = std::max(most, bwd_plan(make_shape(B, Sq, Sk, Hq, Hk, D, pack), ragged).total);
+  return most;
 }
 
 dash_status_t dash_cross_attn_bwd(const void* q, const void* k, const void* v, const void* kv_lens, const void* o,
@@ -347,13 +366,13 @@ dash_status_t dash_cross_attn_bwd(const void* q, const void* k, const void* v, c
   a.s.lens = kv_lens;
   a.s.id_bits = id_bits;
   set_places(&a.s, q_strides, k_strides, v_strides);
-  const BwdPlan pl = bwd_plan(a.s);
+  const BwdPlan pl = bwd_plan(a.s, kv_lens != nullptr);
   if (workspace_bytes < pl.total) return DASH_ERR_WORKSPACE_TOO_SMALL;
   char* ws = (char*)workspace;
   a.header = (int*)ws;
   a.nnl = (float*)(ws + pl.nnl);
   a.delta = (float*)(ws + pl.delta);
-  a.dq_acc = (float*)(ws + pl.dq_acc);
+  a.dq_part = (float*)(ws + pl.dq_part);
   a.dkv_part = (float*)(ws + pl.dkv_part);
   a.o = (const __nv_bfloat16*)o;
   a.dO = (const __nv_bfloat16*)d_o;
@@ -374,20 +393,19 @@ dash_status_t dash_cross_attn_bwd(const void* q, const void* k, const void* v, c
   a.qper = pl.qper;
   a.ksegs = pl.ksegs;
   a.kper = pl.kper;
-  a.units = (int)((long long)B * Hk * pl.qsegs * pl.ksegs);
   a.scale = scale;
   a.scale_log2 = scale * kLog2e;
   a.timeout_ns = sync_timeout_ns();
   a.withhold = sync_withheld();
   Maps maps;
-  if (a.units > 0) {
+  if (Sq > 0 && Sk > 0) {
     const long long os[3] = {(long long)Sq * Hq * D, (long long)Hq * D, (long long)D};
     const int bh = a.s.packed ? a.s.g : 1, bt = a.s.packed ? a.s.tpt : kTile;
     if (!make_maps(&maps, a.s, q, k, v, q_strides, k_strides, v_strides) ||
         !map_heads(&maps.dO, d_o, B, Sq, Hq, D, os, bh, bt))
       return bad_map();
   }
-  return D <= 64 ? launch_bwd<64>(a, maps, stream) : launch_bwd<128>(a, maps, stream);
+  return D <= 64 ? launch_bwd<64>(a, pl.one, maps, stream) : launch_bwd<128>(a, pl.one, maps, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,365 @@
+// Cross attention backward, dQ = scale dS K of groups with several key tiles. A unit of work is a
+// row tile of a group and a range of its key tiles; a persistent grid takes the units in turn. The
+// row tile's Q and dO stay in shared memory, and dQ accumulates in TMEM, over the key tiles:
+//   S   = Q K^T       M = 128 rows, N = the tile's keys, K = D       TMEM cols [128 b, +128), b = t % 2
+//   dP  = dO V^T      M = 128 rows, N = the tile's keys, K = D       TMEM cols [256, +128)
+//   dS  = P * (dP - Delta), P = exp2(S scale log2e - LSE log2e)      bf16, TMEM, over S's columns
+//   dQ += dS K        M = 128 rows, N = D, K = the tile's keys       TMEM cols [384, +DT), A from TMEM
+// S(t+1) is computed while the softmax gradient works on t, dP(t+1) goes ahead of dQ(t), S(t+2)
+// follows dQ(t). LSE and Delta are one number a thread here, as a thread owns a row (and half of the
+// keys). Key ranges (few row tiles against many keys) leave fp32 partials that
+// cross_join_rows_kernel adds in order.
+//
+// Warp roles (384 threads): 0 = TMA producer, 1 = MMA issuer, 2 = K rows behind a length, 4..11 =
+// softmax gradient (quarter = TMEM lanes = rows, half = 64 keys each) and the epilogue. Every wait
+// is bounded.
+#pragma once
+
+#include "cross_bwd.cuh"
+
+namespace dash {
+namespace cross {
+
+template <int DT>
+struct RowsLay {
+  static constexpr int TILE = kTile * DT * 2;
+  static constexpr int NB = DT == 64 ? 2 : 1;                  // Q and dO buffers
+  static constexpr int STAGES = DT == 64 ? 4 : 2;              // K and V
+  static constexpr int Q_OFF = 0, KV_OFF = 2 * NB * TILE;      // buffer b: Q, dO; stage s: K, V
+  static constexpr int BAR_OFF = KV_OFF + 2 * STAGES * TILE;
+  static constexpr int ALLOC = BAR_OFF + 512 + 1024;           // slack for 1024 alignment
+  static_assert(ALLOC <= 232448, "shared memory budget");
+  static constexpr int T_S = 0, T_DP = 256, T_DQ = 384;
+  static constexpr int Q_FULL = 0, DO_FULL = NB, Q_EMPTY = 2 * NB, S_FULL = 3 * NB, S_FREE = S_FULL + 2,
+                       DP_FULL = S_FREE + 2, DS_FULL = DP_FULL + 1, ACC_FULL = DS_FULL + 1,
+                       ACC_EMPTY = ACC_FULL + 1, DRAIN = ACC_EMPTY + 1, K_FULL = DRAIN + 1,
+                       V_FULL = K_FULL + STAGES, KV_EMPTY = V_FULL + STAGES, CLEAN = KV_EMPTY + STAGES,
+                       COUNT = CLEAN + STAGES;
+  static_assert(8 * COUNT + 8 <= 512, "barrier area");
+};
+constexpr int kRowsThreads = 384;
+constexpr int kRowsRegsLaunch = 168, kRowsRegsCtrl = 88, kRowsRegsSoftmax = 208;
+static_assert(kRowsRegsCtrl + 2 * kRowsRegsSoftmax == 3 * kRowsRegsLaunch,
+              "the three warpgroups must share exactly the launch's registers");
+
+// A CTA's units: u, u + grid, ...; those without keys are passed over (cross_pre_kernel writes their
+// rows, and the join reads no range behind a length).
+struct RowsWalk {
+  const BwdArgs* a;
+  int u, bh, b, hk, tile, kseg, len, t0, nt;
+  __device__ __forceinline__ RowsWalk(const BwdArgs& args) : a(&args), u((int)blockIdx.x - (int)gridDim.x) {}
+  __device__ __forceinline__ bool next() {
+    const BwdArgs& p = *a;
+    do {
+      u += gridDim.x;
+      if (u >= p.units) return false;
+      kseg = u % p.ksegs;
+      const int r = u / p.ksegs;
+      tile = r % p.s.ntile;
+      bh = r / p.s.ntile;
+      b = bh / p.s.Hk;
+      hk = bh - b * p.s.Hk;
+      len = length_of(p.s, b);
+      t0 = kseg * p.kper;
+      nt = min((max(len, 0) + kTile - 1) / kTile, t0 + p.kper) - t0;
+    } while (nt <= 0);
+    return true;
+  }
+  __device__ __forceinline__ int keys(int t) const { return min(kTile, len - (t0 + t) * kTile); }
+  __device__ __forceinline__ int steps(int t) const { return (keys(t) + 15) >> 4; }   // of 16 keys
+  // rows of the K tile that dQ reads although the length leaves them out
+  __device__ __forceinline__ bool unclean(int t) const { return len < a->s.Sk && (keys(t) & 15); }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    cross_rows_kernel(const __grid_constant__ BwdArgs p, const __grid_constant__ Maps maps) {
+  using L = RowsLay<DT>;
+  extern __shared__ uint8_t smem_crossr[];
+  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_crossr + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = (uint64_t*)(sm + L::BAR_OFF);
+  uint32_t* tmem_slot = (uint32_t*)(sm + L::BAR_OFF + 8 * L::COUNT);
+  volatile int* abort_flag = (volatile int*)(sm + L::BAR_OFF + 8 * L::COUNT + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long tmo = p.timeout_ns;
+  const int dsteps = (p.s.D + 15) >> 4;
+
+  train::grid_next();
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < L::COUNT; ++k) {
+      const bool kv = k >= L::KV_EMPTY && k < L::CLEAN;
+      ptx::mbar_init(bars + k, k == L::DS_FULL || k == L::ACC_EMPTY ? 8 : kv && p.s.lens ? 2 : 1);
+    }
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) ptx::tmem_alloc(tmem_slot, kTmemCols);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  train::grid_wait();                              // Delta and LSE are there, the header is clear
+
+  if (warp < 4) {
+    ptx::regs_dec<kRowsRegsCtrl>();
+    if (warp == 0 && lane == 0) {
+      // ===================================== TMA producer =====================================
+      RowsWalk w(p);
+      int n = 0, kv = 0;                           // units and key tiles so far
+      bool ok = !p.withhold;
+      while (ok && w.next()) {
+        const int b = n % L::NB;
+        if (n >= L::NB) ok = ptx::mbar_wait(bars + L::Q_EMPTY + b, (n / L::NB - 1) & 1, abort_flag, tmo);
+        if (!ok) break;
+        uint8_t* q = sm + L::Q_OFF + 2 * b * L::TILE;
+        ptx::mbar_expect_tx(bars + L::Q_FULL + b, row_tile_bytes<DT>(p.s));
+        load_row_tile<DT>(p.s, &maps.q, q, w.b, w.hk, w.tile, p.s.q_b, p.s.q_h, bars + L::Q_FULL + b);
+        ptx::mbar_expect_tx(bars + L::DO_FULL + b, row_tile_bytes<DT>(p.s));
+        load_row_tile<DT>(p.s, &maps.dO, q + L::TILE, w.b, w.hk, w.tile, 1, 1, bars + L::DO_FULL + b);
+        ++n;
+        // the next unit's rows wait in L2
+        RowsWalk ahead = w;
+        if (ahead.next()) {
+          prefetch_row_tile<DT>(p.s, &maps.q, ahead.b, ahead.hk, ahead.tile, p.s.q_b, p.s.q_h);
+          prefetch_row_tile<DT>(p.s, &maps.dO, ahead.b, ahead.hk, ahead.tile, 1, 1);
+        }
+        for (int t = 0; ok && t < w.nt; ++t, ++kv) {
+          const int s = kv % L::STAGES, m = kv / L::STAGES;
+          if (m > 0) ok = ptx::mbar_wait(bars + L::KV_EMPTY + s, (m - 1) & 1, abort_flag, tmo);
+          if (!ok) break;
+          uint8_t* ks = sm + L::KV_OFF + 2 * s * L::TILE;
+          ptx::mbar_expect_tx(bars + L::K_FULL + s, L::TILE);
+          load_key_tile<DT>(&maps.k, ks, w.b, w.hk, w.t0 + t, p.s.k_b, p.s.k_h, bars + L::K_FULL + s);
+          ptx::mbar_expect_tx(bars + L::V_FULL + s, L::TILE);
+          load_key_tile<DT>(&maps.v, ks + L::TILE, w.b, w.hk, w.t0 + t, p.s.v_b, p.s.v_h, bars + L::V_FULL + s);
+        }
+      }
+      // drain: every issued load has landed before the CTA may exit
+      for (int k = max(0, n - L::NB); k < n; ++k) {
+        ptx::mbar_drain(bars + L::Q_FULL + k % L::NB, (k / L::NB) & 1, 100000000ll);
+        ptx::mbar_drain(bars + L::DO_FULL + k % L::NB, (k / L::NB) & 1, 100000000ll);
+      }
+      for (int k = max(0, kv - L::STAGES); k < kv; ++k) {
+        ptx::mbar_drain(bars + L::K_FULL + k % L::STAGES, (k / L::STAGES) & 1, 100000000ll);
+        ptx::mbar_drain(bars + L::V_FULL + k % L::STAGES, (k / L::STAGES) & 1, 100000000ll);
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ====================================== MMA issuer ======================================
+      const uint32_t sQ = ptx::smem_u32(sm + L::Q_OFF), sKV = ptx::smem_u32(sm + L::KV_OFF);
+      const uint32_t id_dq = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
+      constexpr uint32_t TILE16 = L::TILE >> 4;
+      RowsWalk w(p);
+      int n = 0, kv0 = 0;                          // units and key tiles before this unit
+      uint32_t clean = 0;                          // parities of the stages' CLEAN barriers
+      bool ok = true;
+      while (ok && w.next()) {
+        const int b = n % L::NB, par = (n / L::NB) & 1;
+        const uint32_t dQ = ptx::sdesc_lo(sQ, 16) + 2 * b * TILE16, ddO = dQ + TILE16;
+        // S(t): the buffer's last dS has been read by its dQ product, K(t) has landed
+        auto issue_s = [&](int t) {
+          const int k = kv0 + t, s = k % L::STAGES;
+          bool good = ptx::mbar_wait(bars + L::K_FULL + s, (k / L::STAGES) & 1, abort_flag, tmo);
+          if (good && k >= 2) good = ptx::mbar_wait(bars + L::S_FREE + (k & 1), (k / 2 - 1) & 1, abort_flag, tmo);
+          if (!good) return false;
+          ptx::tc_fence_after();
+          issue_scores<DT>(tmem + L::T_S + 128 * (k & 1), dQ, ptx::sdesc_lo(sKV, 16) + 2 * s * TILE16,
+                           ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps);
+          ptx::mma_commit(bars + L::S_FULL + (k & 1));
+          return true;
+        };
+        // dP(t): its columns were read when dS(t-1) was stored
+        auto issue_dp = [&](int t) {
+          const int k = kv0 + t, s = k % L::STAGES;
+          if (!ptx::mbar_wait(bars + L::V_FULL + s, (k / L::STAGES) & 1, abort_flag, tmo)) return false;
+          ptx::tc_fence_after();
+          issue_scores<DT>(tmem + L::T_DP, ddO, ptx::sdesc_lo(sKV, 16) + (2 * s + 1) * TILE16,
+                           ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps);
+          ptx::mma_commit(bars + L::DP_FULL);
+          return true;
+        };
+        ok = ptx::mbar_wait(bars + L::Q_FULL + b, par, abort_flag, tmo) && issue_s(0) &&
+             ptx::mbar_wait(bars + L::DO_FULL + b, par, abort_flag, tmo) && issue_dp(0) && (w.nt < 2 || issue_s(1));
+        for (int t = 0; ok && t < w.nt; ++t) {
+          const int k = kv0 + t, s = k % L::STAGES;
+          ok = ptx::mbar_wait(bars + L::DS_FULL, k & 1, abort_flag, tmo);
+          if (ok && t + 1 < w.nt) ok = issue_dp(t + 1);
+          if (t == max(w.nt - 2, 0)) ptx::mma_commit(bars + L::Q_EMPTY + b);   // S and dP of all tiles are issued
+          if (ok && t == 0 && n > 0) ok = ptx::mbar_wait(bars + L::ACC_EMPTY, (n - 1) & 1, abort_flag, tmo);
+          if (ok && t == w.nt - 1 && w.unclean(t)) {
+            ok = ptx::mbar_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);
+            clean ^= 1u << s;
+          }
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t dK = ptx::sdesc_lo(sKV + 2 * s * L::TILE, kTile * 128);
+          uint32_t a = tmem + L::T_S + 128 * (k & 1);
+          const int steps = w.steps(t);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            if (ks < steps) ptx::mma_ts(tmem + L::T_DQ, a, dK + ks * kMnStep, id_dq, (t > 0 || ks > 0) ? 1u : 0u);
+            a = ks == 3 ? next_ts<3>(a) : next_ts<0>(a);
+          }
+          ptx::mma_commit(bars + L::S_FREE + (k & 1));
+          ptx::mma_commit(bars + L::KV_EMPTY + s);
+          if (t + 2 < w.nt) ok = issue_s(t + 2);
+        }
+        if (!ok) break;
+        ptx::mma_commit(bars + L::ACC_FULL);
+        kv0 += w.nt;
+        ++n;
+      }
+      ptx::mma_commit(bars + L::DRAIN);
+      ptx::mbar_drain(bars + L::DRAIN, 0, 1000000000ll);
+    } else if (warp == 2 && p.s.lens) {
+      // ============================ rows of K behind a sequence's end ==========================
+      // Every tile is waited for and its stage released here too, so that this warp can be neither
+      // ahead of the copies nor behind the products by more than a barrier's phase.
+      RowsWalk w(p);
+      int kv = 0;
+      bool ok = true;
+      while (ok && w.next()) {
+        for (int t = 0; t < w.nt; ++t, ++kv) {
+          const int s = kv % L::STAGES;
+          ok = ptx::warp_wait(bars + L::K_FULL + s, (kv / L::STAGES) & 1, abort_flag, tmo);
+          if (!ok) break;
+          if (t == w.nt - 1 && w.unclean(t)) {
+            clear_rows<DT>(sm + L::KV_OFF + 2 * s * L::TILE, w.keys(t), 16 * w.steps(t), lane);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bars + L::CLEAN + s);
+          }
+          if (lane == 0) ptx::mbar_arrive(bars + L::KV_EMPTY + s);
+        }
+      }
+    }
+  } else {
+    ptx::regs_inc<kRowsRegsSoftmax>();
+    // ================================== softmax gradient ====================================
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const int r = quarter * 32 + lane;             // row within the tile = TMEM lane
+    const int col0 = half * 64;                    // this thread's 64 keys
+    const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
+    RowsWalk w(p);
+    int n = 0, k = 0;                              // units, key tiles so far
+    bool ok = true;
+    while (ok && w.next()) {
+      const size_t row = ((size_t)w.bh * p.s.ntile + w.tile) * kTile + r;
+      const float nnl = __ldg(p.nnl + row), delta = __ldg(p.delta + row);
+      for (int t = 0; t < w.nt; ++t, ++k) {
+        const uint32_t t_s = tmem + lane_addr + L::T_S + 128 * (k & 1) + col0;
+        const int mine = 16 * w.steps(t) - col0;   // columns of this half that the products take
+        ok = ptx::warp_wait(bars + L::S_FULL + (k & 1), (k >> 1) & 1, abort_flag, tmo);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        float pv[64];
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          if (c0 < mine) {
+            float x[32];
+            ptx::tmem_ld32(t_s + c0, x);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pv[c0 + c] = ptx::ex2(fmaf(x[c], p.scale_log2, nnl));
+          }
+        }
+        ok = ptx::warp_wait(bars + L::DP_FULL, k & 1, abort_flag, tmo);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const int live = w.keys(t) - col0;         // keys of this half
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          if (c0 < mine) {
+            float dp[32];
+            ptx::tmem_ld32(tmem + lane_addr + L::T_DP + col0 + c0, dp);
+            uint32_t u[16];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) dp[c] = pv[c0 + c] * (dp[c] - delta);
+            if (c0 + 32 > live) {                  // the sequence ends in here
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (c0 + c >= live) dp[c] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) u[c] = ptx::pack_bf16(dp[2 * c], dp[2 * c + 1]);
+            ptx::tmem_st8(t_s + c0 / 2, u);
+            ptx::tmem_st8(t_s + c0 / 2 + 8, u + 8);
+          }
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bars + L::DS_FULL);
+      }
+      if (!ok) break;
+      ok = ptx::warp_wait(bars + L::ACC_FULL, n & 1, abort_flag, tmo);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      int token, head;
+      const bool live = row_of(p.s, w.tile, r, token, head);
+      __nv_bfloat16* dst = p.dq + w.b * p.dq_b + token * p.dq_s + (w.hk * p.s.g + head) * p.dq_h;
+      float* part = p.dq_part + ((((size_t)w.kseg * p.s.B * p.s.Hk + w.bh) * p.s.ntile + w.tile) * kTile + r) * DT;
+#pragma unroll
+      for (int i = 0; i < DT / 2; i += 32) {
+        const int c0 = half * (DT / 2) + i;
+        if (c0 < p.s.D) {
+          float v[32];
+          ptx::tmem_ld32(tmem + lane_addr + L::T_DQ + c0, v);
+          if (live && p.ksegs == 1) {
+            store_bf16_32(dst + c0, v, p.scale, p.s.D - c0);
+          } else if (live) {
+            float4* d4 = (float4*)(part + c0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) d4[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars + L::ACC_EMPTY);
+      ++n;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.header + WS_STATUS, 0, kStatusSyncTimeout);
+}
+
+// dq as the sum of the key ranges' partials, in order; a thread takes 8 columns of a row.
+template <int DT>
+__global__ void __launch_bounds__(256) cross_join_rows_kernel(const __grid_constant__ BwdArgs p) {
+  train::grid_next();
+  train::grid_wait();
+  const int per = p.s.D >> 3;
+  const long long item = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int c = (int)(item % per) * 8;
+  const long long row = item / per;                // in row tiles
+  const size_t rows = (size_t)p.s.B * p.s.Hk * p.s.ntile * kTile;
+  if (row >= (long long)rows) return;
+  const int r = (int)(row % kTile);
+  const long long rest = row / kTile;
+  const int tile = (int)(rest % p.s.ntile), bh = (int)(rest / p.s.ntile), b = bh / p.s.Hk, hk = bh - b * p.s.Hk;
+  int token, head;
+  if (!row_of(p.s, tile, r, token, head)) return;
+  const int len = length_of(p.s, b);
+  if (len <= 0) return;                            // written by cross_pre_kernel
+  const int n = ((len + kTile - 1) / kTile + p.kper - 1) / p.kper;
+  const float* src = p.dq_part + (size_t)row * DT + c;
+  float t[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    float x[8];
+    train::load_f32<float, 8>(src + s * rows * DT, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] += x[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] *= p.scale;
+  train::store_f32<__nv_bfloat16, 8>(p.dq + b * p.dq_b + token * p.dq_s + (hk * p.s.g + head) * p.dq_h + c, t);
+}
+
+}  // namespace cross
+}  // namespace dash

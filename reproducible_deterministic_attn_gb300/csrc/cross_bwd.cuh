@@ -25,7 +25,7 @@
 // 8192 rows x 512 keys x 16 x 128 took 360 us.
 // No CTA waits for another one.
 //
-// Delta and -LSE log2e come per row from cross_pre_kernel, with -inf for rows a tile does not
+// -Delta and -LSE log2e come per row from cross_pre_kernel, with -inf for rows a tile does not
 // have (P = 0 there). Keys that a length leaves out: warp 2 zeroes their rows of K and V in shared
 // memory, as they may hold anything, and their P is set to 0.
 //
@@ -43,7 +43,7 @@ namespace cross {
 struct BwdArgs {
   Shape s;
   float* nnl;                // [group][tile][128] -LSE log2e
-  float* delta;              // [group][tile][128]
+  float* delta;              // [group][tile][128] -Delta
   const __nv_bfloat16 *o, *dO;
   const float* lse;
   __nv_bfloat16 *dq, *dk, *dv;
@@ -63,7 +63,7 @@ template <int DT, bool DQ>
 struct KeysLay {
   static constexpr int TILE = kTile * DT * 2;
   static constexpr int DS_BYTES = DQ ? kTile * kTile * 2 : 0;
-  static constexpr int OFFS = 2 * kTile * 4;                   // -LSE log2e and Delta of a row tile
+  static constexpr int OFFS = 2 * kTile * 4;                   // -LSE log2e and -Delta of a row tile
   static constexpr int NQ = DT == 64 ? 3 : 2, NDO = 2;
   static constexpr int K_OFF = 0, V_OFF = TILE, Q_OFF = 2 * TILE;
   static constexpr int DO_OFF = Q_OFF + NQ * TILE;
@@ -142,7 +142,7 @@ __device__ __forceinline__ void issue_dq(uint32_t d, uint32_t& a, uint32_t& b, u
   }
 }
 
-// Delta = rowsum(dO * O) and -LSE log2e per row, in row tiles; 16 lanes a row, kPreRows rows one
+// -Delta = -rowsum(dO * O) and -LSE log2e per row, in row tiles; 16 lanes a row, kPreRows rows one
 // after the other. Rows of batches without keys get their dq here: 0, or NaN for a length out of
 // range. The first block clears the workspace's header and looks for such lengths. The blocks from
 // row_blocks on write dk and dv of the key tiles that no unit visits.
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(256, 4) cross_pre_kernel(const __grid_constant
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (l == 0) {
-      p.delta[row0 + 16 * k] = t;
+      p.delta[row0 + 16 * k] = -t;
       p.nnl[row0 + 16 * k] = nl[k];
     }
   }
@@ -459,22 +459,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_ld32_issue(tmem + lane_addr + L::T_SP + col0, a);
         ptx::tmem_ld32_wait(a);
         ptx::tmem_ld32_issue(tmem + lane_addr + L::T_SP + col0 + 32, b);
+        const uint64_t scale2 = two(p.scale_log2, p.scale_log2);
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
-          const float4 f = *(const float4*)(nnl + c);
-          pv[c] = ptx::ex2(fmaf(__uint_as_float(a[c]), p.scale_log2, f.x));
-          pv[c + 1] = ptx::ex2(fmaf(__uint_as_float(a[c + 1]), p.scale_log2, f.y));
-          pv[c + 2] = ptx::ex2(fmaf(__uint_as_float(a[c + 2]), p.scale_log2, f.z));
-          pv[c + 3] = ptx::ex2(fmaf(__uint_as_float(a[c + 3]), p.scale_log2, f.w));
+          const ulonglong2 f = *(const ulonglong2*)(nnl + c);
+          exp2_two(__uint_as_float(a[c]), __uint_as_float(a[c + 1]), scale2, f.x, pv[c], pv[c + 1]);
+          exp2_two(__uint_as_float(a[c + 2]), __uint_as_float(a[c + 3]), scale2, f.y, pv[c + 2], pv[c + 3]);
         }
         ptx::tmem_ld32_wait(b);
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
-          const float4 f = *(const float4*)(nnl + 32 + c);
-          pv[32 + c] = ptx::ex2(fmaf(__uint_as_float(b[c]), p.scale_log2, f.x));
-          pv[33 + c] = ptx::ex2(fmaf(__uint_as_float(b[c + 1]), p.scale_log2, f.y));
-          pv[34 + c] = ptx::ex2(fmaf(__uint_as_float(b[c + 2]), p.scale_log2, f.z));
-          pv[35 + c] = ptx::ex2(fmaf(__uint_as_float(b[c + 3]), p.scale_log2, f.w));
+          const ulonglong2 f = *(const ulonglong2*)(nnl + 32 + c);
+          exp2_two(__uint_as_float(b[c]), __uint_as_float(b[c + 1]), scale2, f.x, pv[32 + c], pv[33 + c]);
+          exp2_two(__uint_as_float(b[c + 2]), __uint_as_float(b[c + 3]), scale2, f.y, pv[34 + c], pv[35 + c]);
         }
       }
       const bool dead = r >= w.keys();             // a key behind the length
@@ -504,10 +501,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t u[8];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
-          const float4 f = *(const float4*)(delta + c0 + 2 * k);
-          u[k] = ptx::pack_bf16(pv[c0 + 2 * k] * (dp[2 * k] - f.x), pv[c0 + 2 * k + 1] * (dp[2 * k + 1] - f.y));
-          u[k + 1] = ptx::pack_bf16(pv[c0 + 2 * k + 2] * (dp[2 * k + 2] - f.z),
-                                    pv[c0 + 2 * k + 3] * (dp[2 * k + 3] - f.w));
+          const ulonglong2 f = *(const ulonglong2*)(delta + c0 + 2 * k);   // -Delta
+          float x, y;
+          untwo(mul2(two(pv[c0 + 2 * k], pv[c0 + 2 * k + 1]), add2(two(dp[2 * k], dp[2 * k + 1]), f.x)), x, y);
+          u[k] = ptx::pack_bf16(x, y);
+          untwo(mul2(two(pv[c0 + 2 * k + 2], pv[c0 + 2 * k + 3]), add2(two(dp[2 * k + 2], dp[2 * k + 3]), f.y)), x, y);
+          u[k + 1] = ptx::pack_bf16(x, y);
         }
         ptx::tmem_st8(tmem + lane_addr + L::T_DS + col0 + c0 / 2, u);
         if (DQ) {

@@ -24,17 +24,19 @@ template <int DT>
 struct RowsLay {
   static constexpr int TILE = kTile * DT * 2;
   static constexpr int NB = DT == 64 ? 2 : 1;                  // Q and dO buffers
-  static constexpr int STAGES = DT == 64 ? 4 : 2;              // K and V
-  static constexpr int Q_OFF = 0, KV_OFF = 2 * NB * TILE;      // buffer b: Q, dO; stage s: K, V
-  static constexpr int BAR_OFF = KV_OFF + 2 * STAGES * TILE;
+  // K waits for dQ, V only for dP: so K has more stages
+  static constexpr int KST = DT == 64 ? 5 : 3, VST = DT == 64 ? 4 : 2;
+  static constexpr int Q_OFF = 0, K_OFF = 2 * NB * TILE;       // buffer b: Q, dO
+  static constexpr int V_OFF = K_OFF + KST * TILE;
+  static constexpr int BAR_OFF = V_OFF + VST * TILE;
   static constexpr int ALLOC = BAR_OFF + 512 + 1024;           // slack for 1024 alignment
   static_assert(ALLOC <= 232448, "shared memory budget");
   static constexpr int T_S = 0, T_DP = 256, T_DQ = 384;
   static constexpr int Q_FULL = 0, DO_FULL = NB, Q_EMPTY = 2 * NB, S_FULL = 3 * NB, S_FREE = S_FULL + 2,
                        DP_FULL = S_FREE + 2, DS_FULL = DP_FULL + 1, ACC_FULL = DS_FULL + 1,
                        ACC_EMPTY = ACC_FULL + 1, DRAIN = ACC_EMPTY + 1, K_FULL = DRAIN + 1,
-                       V_FULL = K_FULL + STAGES, KV_EMPTY = V_FULL + STAGES, CLEAN = KV_EMPTY + STAGES,
-                       COUNT = CLEAN + STAGES;
+                       V_FULL = K_FULL + KST, K_EMPTY = V_FULL + VST, V_EMPTY = K_EMPTY + KST,
+                       CLEAN = V_EMPTY + VST, COUNT = CLEAN + KST;
   static_assert(8 * COUNT + 8 <= 512, "barrier area");
 };
 constexpr int kRowsThreads = 384;
@@ -87,8 +89,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   train::grid_next();
   if (threadIdx.x == 0) {
     for (int k = 0; k < L::COUNT; ++k) {
-      const bool kv = k >= L::KV_EMPTY && k < L::CLEAN;
-      ptx::mbar_init(bars + k, k == L::DS_FULL || k == L::ACC_EMPTY ? 8 : kv && p.s.lens ? 2 : 1);
+      const bool key = k >= L::K_EMPTY && k < L::V_EMPTY;   // the products, and warp 2
+      ptx::mbar_init(bars + k, k == L::DS_FULL || k == L::ACC_EMPTY ? 8 : key && p.s.lens ? 2 : 1);
     }
     *abort_flag = 0;
     ptx::fence_barrier_init();
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (warp == 0 && lane == 0) {
       // ===================================== TMA producer =====================================
       RowsWalk w(p);
-      int n = 0, kv = 0;                           // units and key tiles so far
+      int n = 0, kv = 0, nk = 0;                   // units, key tiles (V), K tiles so far
       bool ok = !p.withhold;
       while (ok && w.next()) {
         const int b = n % L::NB;
@@ -124,14 +126,18 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           prefetch_row_tile<DT>(p.s, &maps.dO, ahead.b, ahead.hk, ahead.tile, 1, 1);
         }
         for (int t = 0; ok && t < w.nt; ++t, ++kv) {
-          const int s = kv % L::STAGES, m = kv / L::STAGES;
-          if (m > 0) ok = ptx::mbar_wait(bars + L::KV_EMPTY + s, (m - 1) & 1, abort_flag, tmo);
+          const int ks = kv % L::KST, km = kv / L::KST, vs = kv % L::VST, vm = kv / L::VST;
+          if (km > 0) ok = ptx::mbar_wait(bars + L::K_EMPTY + ks, (km - 1) & 1, abort_flag, tmo);
           if (!ok) break;
-          uint8_t* ks = sm + L::KV_OFF + 2 * s * L::TILE;
-          ptx::mbar_expect_tx(bars + L::K_FULL + s, L::TILE);
-          load_key_tile<DT>(&maps.k, ks, w.b, w.hk, w.t0 + t, p.s.k_b, p.s.k_h, bars + L::K_FULL + s);
-          ptx::mbar_expect_tx(bars + L::V_FULL + s, L::TILE);
-          load_key_tile<DT>(&maps.v, ks + L::TILE, w.b, w.hk, w.t0 + t, p.s.v_b, p.s.v_h, bars + L::V_FULL + s);
+          ptx::mbar_expect_tx(bars + L::K_FULL + ks, L::TILE);
+          load_key_tile<DT>(&maps.k, sm + L::K_OFF + ks * L::TILE, w.b, w.hk, w.t0 + t, p.s.k_b, p.s.k_h,
+                            bars + L::K_FULL + ks);
+          ++nk;
+          if (vm > 0) ok = ptx::mbar_wait(bars + L::V_EMPTY + vs, (vm - 1) & 1, abort_flag, tmo);
+          if (!ok) break;
+          ptx::mbar_expect_tx(bars + L::V_FULL + vs, L::TILE);
+          load_key_tile<DT>(&maps.v, sm + L::V_OFF + vs * L::TILE, w.b, w.hk, w.t0 + t, p.s.v_b, p.s.v_h,
+                            bars + L::V_FULL + vs);
         }
       }
       // drain: every issued load has landed before the CTA may exit
@@ -139,13 +145,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         ptx::mbar_drain(bars + L::Q_FULL + k % L::NB, (k / L::NB) & 1, 100000000ll);
         ptx::mbar_drain(bars + L::DO_FULL + k % L::NB, (k / L::NB) & 1, 100000000ll);
       }
-      for (int k = max(0, kv - L::STAGES); k < kv; ++k) {
-        ptx::mbar_drain(bars + L::K_FULL + k % L::STAGES, (k / L::STAGES) & 1, 100000000ll);
-        ptx::mbar_drain(bars + L::V_FULL + k % L::STAGES, (k / L::STAGES) & 1, 100000000ll);
-      }
+      for (int k = max(0, nk - L::KST); k < nk; ++k)
+        ptx::mbar_drain(bars + L::K_FULL + k % L::KST, (k / L::KST) & 1, 100000000ll);
+      for (int k = max(0, kv - L::VST); k < kv; ++k)
+        ptx::mbar_drain(bars + L::V_FULL + k % L::VST, (k / L::VST) & 1, 100000000ll);
     } else if (warp == 1 && lane == 0) {
       // ====================================== MMA issuer ======================================
-      const uint32_t sQ = ptx::smem_u32(sm + L::Q_OFF), sKV = ptx::smem_u32(sm + L::KV_OFF);
+      const uint32_t sQ = ptx::smem_u32(sm + L::Q_OFF), sK = ptx::smem_u32(sm + L::K_OFF);
+      const uint32_t sV = ptx::smem_u32(sm + L::V_OFF);
       const uint32_t id_dq = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
       constexpr uint32_t TILE16 = L::TILE >> 4;
       RowsWalk w(p);
@@ -157,30 +164,31 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const uint32_t dQ = ptx::sdesc_lo(sQ, 16) + 2 * b * TILE16, ddO = dQ + TILE16;
         // S(t): the buffer's last dS has been read by its dQ product, K(t) has landed
         auto issue_s = [&](int t) {
-          const int k = kv0 + t, s = k % L::STAGES;
-          bool good = ptx::mbar_wait(bars + L::K_FULL + s, (k / L::STAGES) & 1, abort_flag, tmo);
+          const int k = kv0 + t, s = k % L::KST;
+          bool good = ptx::mbar_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
           if (good && k >= 2) good = ptx::mbar_wait(bars + L::S_FREE + (k & 1), (k / 2 - 1) & 1, abort_flag, tmo);
           if (!good) return false;
           ptx::tc_fence_after();
-          issue_scores<DT>(tmem + L::T_S + 128 * (k & 1), dQ, ptx::sdesc_lo(sKV, 16) + 2 * s * TILE16,
+          issue_scores<DT>(tmem + L::T_S + 128 * (k & 1), dQ, ptx::sdesc_lo(sK, 16) + s * TILE16,
                            ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps);
           ptx::mma_commit(bars + L::S_FULL + (k & 1));
           return true;
         };
         // dP(t): its columns were read when dS(t-1) was stored
         auto issue_dp = [&](int t) {
-          const int k = kv0 + t, s = k % L::STAGES;
-          if (!ptx::mbar_wait(bars + L::V_FULL + s, (k / L::STAGES) & 1, abort_flag, tmo)) return false;
+          const int k = kv0 + t, s = k % L::VST;
+          if (!ptx::mbar_wait(bars + L::V_FULL + s, (k / L::VST) & 1, abort_flag, tmo)) return false;
           ptx::tc_fence_after();
-          issue_scores<DT>(tmem + L::T_DP, ddO, ptx::sdesc_lo(sKV, 16) + (2 * s + 1) * TILE16,
+          issue_scores<DT>(tmem + L::T_DP, ddO, ptx::sdesc_lo(sV, 16) + s * TILE16,
                            ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps);
           ptx::mma_commit(bars + L::DP_FULL);
+          ptx::mma_commit(bars + L::V_EMPTY + s);
           return true;
         };
         ok = ptx::mbar_wait(bars + L::Q_FULL + b, par, abort_flag, tmo) && issue_s(0) &&
              ptx::mbar_wait(bars + L::DO_FULL + b, par, abort_flag, tmo) && issue_dp(0) && (w.nt < 2 || issue_s(1));
         for (int t = 0; ok && t < w.nt; ++t) {
-          const int k = kv0 + t, s = k % L::STAGES;
+          const int k = kv0 + t, s = k % L::KST;
           ok = ptx::mbar_wait(bars + L::DS_FULL, k & 1, abort_flag, tmo);
           if (ok && t + 1 < w.nt) ok = issue_dp(t + 1);
           if (t == max(w.nt - 2, 0)) ptx::mma_commit(bars + L::Q_EMPTY + b);   // S and dP of all tiles are issued
@@ -191,7 +199,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           }
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t dK = ptx::sdesc_lo(sKV + 2 * s * L::TILE, kTile * 128);
+          const uint32_t dK = ptx::sdesc_lo(sK + s * L::TILE, kTile * 128);
           uint32_t a = tmem + L::T_S + 128 * (k & 1);
           const int steps = w.steps(t);
 #pragma unroll
@@ -200,7 +208,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             a = ks == 3 ? next_ts<3>(a) : next_ts<0>(a);
           }
           ptx::mma_commit(bars + L::S_FREE + (k & 1));
-          ptx::mma_commit(bars + L::KV_EMPTY + s);
+          ptx::mma_commit(bars + L::K_EMPTY + s);
           if (t + 2 < w.nt) ok = issue_s(t + 2);
         }
         if (!ok) break;
@@ -219,16 +227,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       bool ok = true;
       while (ok && w.next()) {
         for (int t = 0; t < w.nt; ++t, ++kv) {
-          const int s = kv % L::STAGES;
-          ok = ptx::warp_wait(bars + L::K_FULL + s, (kv / L::STAGES) & 1, abort_flag, tmo);
+          const int s = kv % L::KST;
+          ok = ptx::warp_wait(bars + L::K_FULL + s, (kv / L::KST) & 1, abort_flag, tmo);
           if (!ok) break;
           if (t == w.nt - 1 && w.unclean(t)) {
-            clear_rows<DT>(sm + L::KV_OFF + 2 * s * L::TILE, w.keys(t), 16 * w.steps(t), lane);
+            clear_rows<DT>(sm + L::K_OFF + s * L::TILE, w.keys(t), 16 * w.steps(t), lane);
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bars + L::CLEAN + s);
           }
-          if (lane == 0) ptx::mbar_arrive(bars + L::KV_EMPTY + s);
+          if (lane == 0) ptx::mbar_arrive(bars + L::K_EMPTY + s);
         }
       }
     }
@@ -244,7 +252,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     bool ok = true;
     while (ok && w.next()) {
       const size_t row = ((size_t)w.bh * p.s.ntile + w.tile) * kTile + r;
-      const float nnl = __ldg(p.nnl + row), delta = __ldg(p.delta + row);
+      const float nnl = __ldg(p.nnl + row), delta = __ldg(p.delta + row);   // -LSE log2e, -Delta
+      const uint64_t scale2 = two(p.scale_log2, p.scale_log2), nnl2 = two(nnl, nnl), delta2 = two(delta, delta);
       for (int t = 0; t < w.nt; ++t, ++k) {
         const uint32_t t_s = tmem + lane_addr + L::T_S + 128 * (k & 1) + col0;
         const int mine = 16 * w.steps(t) - col0;   // columns of this half that the products take
@@ -258,7 +267,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             float x[32];
             ptx::tmem_ld32(t_s + c0, x);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) pv[c0 + c] = ptx::ex2(fmaf(x[c], p.scale_log2, nnl));
+            for (int c = 0; c < 32; c += 2) exp2_two(x[c], x[c + 1], scale2, nnl2, pv[c0 + c], pv[c0 + c + 1]);
           }
         }
         ok = ptx::warp_wait(bars + L::DP_FULL, k & 1, abort_flag, tmo);
@@ -272,7 +281,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             ptx::tmem_ld32(tmem + lane_addr + L::T_DP + col0 + c0, dp);
             uint32_t u[16];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) dp[c] = pv[c0 + c] * (dp[c] - delta);
+            for (int c = 0; c < 32; c += 2)
+              untwo(mul2(two(pv[c0 + c], pv[c0 + c + 1]), add2(two(dp[c], dp[c + 1]), delta2)), dp[c], dp[c + 1]);
             if (c0 + 32 > live) {                  // the sequence ends in here
 #pragma unroll
               for (int c = 0; c < 32; ++c)

@@ -114,6 +114,44 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int to, int 
       reinterpret_cast<uint4*>(tile + cb * kTile * 128 + from * 128)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// Two fp32 operations an instruction, each rounded as by itself: a softmax warp's time is that of
+// its instructions, as few warps share a scheduler.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void untwo(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// exp2(x scale + offset) of two values
+__device__ __forceinline__ void exp2_two(float x, float y, uint64_t scale, uint64_t offset, float& ex, float& ey) {
+  float u, v;
+  untwo(fma2(two(x, y), scale, offset), u, v);
+  ex = ptx::ex2(u);
+  ey = ptx::ex2(v);
+}
+
 // 32 bytes of a row in one store where its address allows it: a whole sector.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
   if (wide) {

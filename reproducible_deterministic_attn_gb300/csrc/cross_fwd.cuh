@@ -334,31 +334,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (32 * c + i >= keys) sc[c][i] = 0xff800000u;
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(sc[c][i]));
+            for (int i = 0; i < 32; i += 2)
+              mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(sc[c][i]), __uint_as_float(sc[c][i + 1]));
           }
         }
         const float m_row = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
         const bool moved = m_row > m + kRescaleLog2;
         const float m_new = moved ? m_row : m;
-        float lt4[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = two(p.scale_log2, p.scale_log2), off2 = two(-m_new, -m_new);
+        uint64_t lt[2] = {0ull, 0ull};             // four partial sums
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (c < chunks) {
             uint32_t u[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float e0 = ptx::ex2(fmaf(__uint_as_float(sc[c][2 * k]), p.scale_log2, -m_new));
-              const float e1 = ptx::ex2(fmaf(__uint_as_float(sc[c][2 * k + 1]), p.scale_log2, -m_new));
-              lt4[(2 * k) & 3] += e0;
-              lt4[(2 * k + 1) & 3] += e1;
+              float e0, e1;
+              exp2_two(__uint_as_float(sc[c][2 * k]), __uint_as_float(sc[c][2 * k + 1]), scale2, off2, e0, e1);
+              lt[k & 1] = add2(lt[k & 1], two(e0, e1));
               u[k] = ptx::pack_bf16(e0, e1);
             }
             ptx::tmem_st8(t_pp + 16 * c, u);
             ptx::tmem_st8(t_pp + 16 * c + 8, u + 8);
           }
         }
+        float lt0, lt1;
+        untwo(add2(lt[0], lt[1]), lt0, lt1);
         const float alpha = moved ? ptx::ex2(m - m_new) : 1.f;
-        l = l * alpha + ((lt4[0] + lt4[1]) + (lt4[2] + lt4[3]));
+        l = l * alpha + (lt0 + lt1);
         m = m_new;
         // the products before this S have ended, O's last one among them
         if (t > 0 && __any_sync(0xffffffffu, moved)) {

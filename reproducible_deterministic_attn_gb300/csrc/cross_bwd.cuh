@@ -11,8 +11,8 @@
 //   dV   += P^T dO             M = 128 keys, N = D, K = 128 rows, A from TMEM  [256, +DT)
 //   dK   += dS^T Q             M = 128 keys, N = D, K = 128 rows, A from TMEM  [256 + DT, +DT)
 // dK and dV stay in TMEM over the unit's row tiles. S(t+1) waits for dV(t) (it overwrites P), dP(t+1)
-// for dK(t): so the exponentials of the next task run under this one's dK and dP, its dS under dV and
-// the next S. Units of one key tile leave fp32 partials of dK and dV, which cross_join_keys_kernel
+// for dK(t): two chains, each with an issuer of its own, that only the softmax gradient ties together.
+// The exponentials of the next task run under this one's dK and dP, its dS under dV and the next S. Units of one key tile leave fp32 partials of dK and dV, which cross_join_keys_kernel
 // adds in order.
 //
 // Where a group has one key tile (up to 128 keys: a caption) the same kernel forms dQ too (DQ), as
@@ -29,7 +29,7 @@
 // have (P = 0 there). Keys that a length leaves out: warp 2 zeroes their rows of K and V in shared
 // memory, as they may hold anything, and their P is set to 0.
 //
-// Warp roles (512 threads): 0 = TMA producer, 1 = MMA issuer, 2 = key rows behind a length, 3 idle,
+// Warp roles (512 threads): 0 = TMA producer, 1 and 3 = MMA issuers, 2 = key rows behind a length,
 // 4..11 = softmax gradient (quarter = TMEM lanes = keys, half = 64 rows each), 12..15 = dQ
 // read-out and the epilogue of dK and dV. Every wait is bounded.
 #pragma once
@@ -87,7 +87,7 @@ struct KeysLay {
 enum {
   C_KV_FULL = 0, C_KV_READY, C_KV_EMPTY, C_Q_FULL, C_Q_EMPTY = C_Q_FULL + 3, C_DO_FULL = C_Q_EMPTY + 3,
   C_DO_EMPTY = C_DO_FULL + 2, C_S_FULL = C_DO_EMPTY + 2, C_SP_FREE, C_DP_FREE, C_P_FULL, C_DP_FULL, C_DS_FULL, C_DQ_FULL, C_DQ_EMPTY, C_ACC_FULL,
-  C_ACC_EMPTY, C_DRAIN, C_COUNT
+  C_ACC_EMPTY, C_DRAIN, C_COUNT = C_DRAIN + 2
 };
 static_assert(8 * C_COUNT + 8 <= 256, "barrier area");
 
@@ -131,11 +131,10 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b,
     b = ks == 3 ? next_k<3>(b) : next_k<0>(b);
   }
 }
-// dQ^T's K steps K0 .. K1 - 1 of the n that hold keys (both operands MN-major).
-template <int K0, int K1>
-__device__ __forceinline__ void issue_dq(uint32_t d, uint32_t& a, uint32_t& b, uint32_t id, int n) {
+// dQ^T's K steps of which n hold keys (both operands MN-major).
+__device__ __forceinline__ void issue_dq(uint32_t d, uint32_t a, uint32_t b, uint32_t id, int n) {
 #pragma unroll
-  for (int ks = K0; ks < K1; ++ks) {
+  for (int ks = 0; ks < 8; ++ks) {
     if (ks < n) ptx::mma_lo(d, a, b, id, ks > 0);
     a = ptx::step_add<kMnStep>(a);
     b = ptx::step_add<kMnStep>(b);
@@ -241,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int k = 0; k < C_COUNT; ++k) {
-      const int n = k == C_P_FULL || k == C_DS_FULL ? 8 : k == C_DQ_EMPTY || k == C_ACC_EMPTY ? 4 : 1;
+      const bool both = (DQ && k == C_SP_FREE) || k == C_KV_EMPTY || k == C_ACC_FULL || k == C_DO_EMPTY || k == C_DO_EMPTY + 1;   // issuers
+      const int n = k == C_P_FULL || k == C_DS_FULL ? 8 : k == C_DQ_EMPTY || k == C_ACC_EMPTY ? 4 : both ? 2 : 1;
       ptx::mbar_init(bars + k, n);
     }
     *abort_flag = 0;
@@ -331,108 +331,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bars + C_KV_READY);
         ++tl;
       }
-    } else if (warp == 1 && lane == 0) {
-      // ===================================== MMA issuer =======================================
+    } else if ((warp == 1 || warp == 3) && lane == 0) {
+      // ==================================== MMA issuers =======================================
+      // Warp 1 issues S^T and dV, warp 3 dP^T, dK and dQ^T, each in the tasks' order: so neither
+      // chain waits in line behind the other's barriers.
       const uint32_t sK = ptx::smem_u32(sm + L::K_OFF), sV = ptx::smem_u32(sm + L::V_OFF);
       const uint32_t sQ = ptx::smem_u32(sm + L::Q_OFF), sdO = ptx::smem_u32(sm + L::DO_OFF);
-      const uint32_t sDS = ptx::smem_u32(sm + L::DS_OFF);
-      const uint32_t dK_k = ptx::sdesc_lo(sK, 16), dV_k = ptx::sdesc_lo(sV, 16);
-      const uint32_t dKt_mn = ptx::sdesc_lo(sK, DT == 128 ? kTile * 128 : L::ZERO_OFF - L::K_OFF);
-      const uint32_t dQ_k0 = ptx::sdesc_lo(sQ, 16), dQ_mn0 = ptx::sdesc_lo(sQ, kTile * 128);
-      const uint32_t ddO_k = ptx::sdesc_lo(sdO, 16), ddO_mn = ptx::sdesc_lo(sdO, kTile * 128);
-      const uint32_t dDS_mn = ptx::sdesc_lo(sDS, kTile * 128);
       constexpr uint32_t ID_S = ptx::idesc_bf16(128, 128, 0, 0);
       const uint32_t id_ts = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
-      constexpr uint32_t ID_DQ = ptx::idesc_bf16(128, 128, 1, 1);
       constexpr uint32_t BUF_STEP = L::TILE >> 4;
       KeysWalk w(p);
       int it = 0, tile = -1;
-      bool ok = true, have = w.next(), s_done = false;   // s_done: S(it) was issued ahead
-      while (ok && have) {
-        const bool first = w.first_of_tile(), last = w.last_of_tile();
-        const int qb = it % L::NQ, ob = it % L::NDO, ksteps = (w.keys() + 15) >> 4;
-        if (first) {
-          ++tile;
-          ok = ptx::mbar_wait(bars + C_KV_READY, tile & 1, abort_flag, tmo);
-          if (!ok) break;
-        }
-        // ---- S^T(it), once Q(it) has landed and what lies over its columns has been read: P^T(it-1)
-        // by dV, with DQ also dS^T(it-1) by dK
-        if (!s_done) {
-          ok = ptx::mbar_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
+      bool ok = true;
+      if (warp == 1) {
+        const uint32_t dK_k = ptx::sdesc_lo(sK, 16), dQ_k = ptx::sdesc_lo(sQ, 16);
+        const uint32_t ddO_mn = ptx::sdesc_lo(sdO, kTile * 128);
+        while (ok && w.next()) {
+          const bool first = w.first_of_tile(), last = w.last_of_tile();
+          const int qb = it % L::NQ, ob = it % L::NDO;
+          // ---- S^T(it), once Q(it) has landed and what lies over its columns has been read: P^T(it-1)
+          // by dV, with DQ also dS^T(it-1) by dK
+          if (first) ok = ptx::mbar_wait(bars + C_KV_READY, ++tile & 1, abort_flag, tmo);
+          if (ok) ok = ptx::mbar_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
           if (ok && it > 0) ok = ptx::mbar_wait(bars + C_SP_FREE, (it - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::tc_fence_after();
-          issue_scores<DT>(tmem + L::T_SP, dK_k, dQ_k0 + qb * BUF_STEP, ID_S, dsteps);
+          issue_scores<DT>(tmem + L::T_SP, dK_k, dQ_k + qb * BUF_STEP, ID_S, dsteps);
           ptx::mma_commit(bars + C_S_FULL);
-        }
-        // ---- dP^T(it), once dO(it) has landed and its columns are free: dS^T(it-1) read by dK, with
-        // DQ dQ^T(it-1) out of TMEM
-        ok = ptx::mbar_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
-        if (ok && it > 0) {
-          if (!DQ) ok = ptx::mbar_wait(bars + C_DP_FREE, (it - 1) & 1, abort_flag, tmo);
-          else if (!L::kSepDQ) ok = ptx::mbar_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
-        }
-        if (!ok) break;
-        ptx::tc_fence_after();
-        issue_scores<DT>(tmem + L::T_DP, dV_k, ddO_k + ob * BUF_STEP, ID_S, dsteps);
-        ptx::mma_commit(bars + C_DP_FULL);
-        if (last && !DQ) ptx::mma_commit(bars + C_KV_EMPTY);
-        // ---- dV += P^T dO, once P^T(it) is stored and the last key tile's sums were read out
-        ok = ptx::mbar_wait(bars + C_P_FULL, it & 1, abort_flag, tmo);
-        if (ok && first && tile > 0) ok = ptx::mbar_wait(bars + C_ACC_EMPTY, (tile - 1) & 1, abort_flag, tmo);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        const uint32_t acc0 = first ? 0u : 1u;
-        issue_ts(tmem + L::T_DV, tmem + L::T_SP, ddO_mn + ob * BUF_STEP, id_ts, acc0);
-        ptx::mma_commit(bars + C_DO_EMPTY + ob);
-        if (!DQ) ptx::mma_commit(bars + C_SP_FREE);
-        have = w.next();
-        s_done = have && !w.first_of_tile();       // S^T(it+1) of the same keys goes ahead
-        const int qn = (it + 1) % L::NQ;
-        if (!DQ && s_done) {
-          ok = ptx::mbar_wait(bars + C_Q_FULL + qn, ((it + 1) / L::NQ) & 1, abort_flag, tmo);
-          if (ok) ok = ptx::mbar_wait(bars + C_SP_FREE, it & 1, abort_flag, tmo);
+          if (last) ptx::mma_commit(bars + C_KV_EMPTY);
+          // ---- dV += P^T dO, once P^T(it) is stored and the last key tile's sums were read out
+          ok = ptx::mbar_wait(bars + C_P_FULL, it & 1, abort_flag, tmo);
+          if (ok) ok = ptx::mbar_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
+          if (ok && first && tile > 0) ok = ptx::mbar_wait(bars + C_ACC_EMPTY, (tile - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::tc_fence_after();
-          issue_scores<DT>(tmem + L::T_SP, dK_k, dQ_k0 + qn * BUF_STEP, ID_S, dsteps);
-          ptx::mma_commit(bars + C_S_FULL);
+          issue_ts(tmem + L::T_DV, tmem + L::T_SP, ddO_mn + ob * BUF_STEP, id_ts, first ? 0u : 1u);
+          ptx::mma_commit(bars + C_SP_FREE);
+          ptx::mma_commit(bars + C_DO_EMPTY + ob);
+          if (last) ptx::mma_commit(bars + C_ACC_FULL);
+          ++it;
         }
-        // ---- dK += dS^T Q, once dS^T(it) is stored
-        ok = ptx::mbar_wait(bars + C_DS_FULL, it & 1, abort_flag, tmo);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        issue_ts(tmem + L::T_DK, tmem + L::T_DS, dQ_mn0 + qb * BUF_STEP, id_ts, acc0);
-        ptx::mma_commit(bars + C_Q_EMPTY + qb);
-        ptx::mma_commit(bars + (DQ ? C_SP_FREE : C_DP_FREE));
-        if (DQ) {
-          // ---- dQ^T = K^T dS^T, with S^T(it+1) ahead of it (DT = 64) or between its halves, so that
-          // the softmax gradient has it earlier
-          if (L::kSepDQ && it > 0) ok = ptx::mbar_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
+      } else {
+        const uint32_t dV_k = ptx::sdesc_lo(sV, 16), ddO_k = ptx::sdesc_lo(sdO, 16);
+        const uint32_t dQ_mn = ptx::sdesc_lo(sQ, kTile * 128);
+        const uint32_t dKt_mn = ptx::sdesc_lo(sK, DT == 128 ? kTile * 128 : L::ZERO_OFF - L::K_OFF);
+        const uint32_t dDS_mn = ptx::sdesc_lo(ptx::smem_u32(sm + L::DS_OFF), kTile * 128);
+        constexpr uint32_t ID_DQ = ptx::idesc_bf16(128, 128, 1, 1);
+        while (ok && w.next()) {
+          const bool first = w.first_of_tile(), last = w.last_of_tile();
+          const int qb = it % L::NQ, ob = it % L::NDO, ksteps = (w.keys() + 15) >> 4;
+          // ---- dP^T(it), once dO(it) has landed and its columns are free: dS^T(it-1) read by dK, with
+          // DQ dQ^T(it-1) out of TMEM
+          if (first) ok = ptx::mbar_wait(bars + C_KV_READY, ++tile & 1, abort_flag, tmo);
+          if (ok) ok = ptx::mbar_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
+          if (ok && it > 0) {
+            if (!DQ) ok = ptx::mbar_wait(bars + C_DP_FREE, (it - 1) & 1, abort_flag, tmo);
+            else if (!L::kSepDQ) ok = ptx::mbar_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
+          }
           if (!ok) break;
-          uint32_t dq_a = dKt_mn, dq_b = dDS_mn;
-          if (DT == 128 && s_done) issue_dq<0, 4>(tmem + L::T_DQ, dq_a, dq_b, ID_DQ, ksteps);
-          if (s_done) {
-            ok = ptx::mbar_wait(bars + C_Q_FULL + qn, ((it + 1) / L::NQ) & 1, abort_flag, tmo);
-            if (ok) ok = ptx::mbar_wait(bars + C_SP_FREE, it & 1, abort_flag, tmo);
+          ptx::tc_fence_after();
+          issue_scores<DT>(tmem + L::T_DP, dV_k, ddO_k + ob * BUF_STEP, ID_S, dsteps);
+          ptx::mma_commit(bars + C_DP_FULL);
+          ptx::mma_commit(bars + C_DO_EMPTY + ob);
+          if (last && !DQ) ptx::mma_commit(bars + C_KV_EMPTY);
+          // ---- dK += dS^T Q, once dS^T(it) is stored
+          ok = ptx::mbar_wait(bars + C_DS_FULL, it & 1, abort_flag, tmo);
+          if (ok) ok = ptx::mbar_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
+          if (ok && first && tile > 0) ok = ptx::mbar_wait(bars + C_ACC_EMPTY, (tile - 1) & 1, abort_flag, tmo);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          issue_ts(tmem + L::T_DK, tmem + L::T_DS, dQ_mn + qb * BUF_STEP, id_ts, first ? 0u : 1u);
+          ptx::mma_commit(bars + (DQ ? C_SP_FREE : C_DP_FREE));
+          ptx::mma_commit(bars + C_Q_EMPTY + qb);
+          if (last) ptx::mma_commit(bars + C_ACC_FULL);
+          if (DQ) {
+            // ---- dQ^T = K^T dS^T
+            if (L::kSepDQ && it > 0) ok = ptx::mbar_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
             if (!ok) break;
             ptx::tc_fence_after();
-            issue_scores<DT>(tmem + L::T_SP, dK_k, dQ_k0 + qn * BUF_STEP, ID_S, dsteps);
-            ptx::mma_commit(bars + C_S_FULL);
+            issue_dq(tmem + L::T_DQ, dKt_mn, dDS_mn, ID_DQ, ksteps);
+            ptx::mma_commit(bars + C_DQ_FULL);
+            if (last) ptx::mma_commit(bars + C_KV_EMPTY);
           }
-          if (DT == 128 && s_done) issue_dq<4, 8>(tmem + L::T_DQ, dq_a, dq_b, ID_DQ, ksteps);
-          else issue_dq<0, 8>(tmem + L::T_DQ, dq_a, dq_b, ID_DQ, ksteps);
-          ptx::mma_commit(bars + C_DQ_FULL);
+          ++it;
         }
-        if (last) {
-          ptx::mma_commit(bars + C_ACC_FULL);
-          if (DQ) ptx::mma_commit(bars + C_KV_EMPTY);
-        }
-        ++it;
       }
       // drain: no MMA may be in flight when TMEM is released
-      ptx::mma_commit(bars + C_DRAIN);
-      ptx::mbar_drain(bars + C_DRAIN, 0, 1000000000ll);
+      ptx::mma_commit(bars + C_DRAIN + (warp >> 1));
+      ptx::mbar_drain(bars + C_DRAIN + (warp >> 1), 0, 1000000000ll);
     }
   } else if (warp < 12) {
     // =============================== softmax-gradient warps =================================

@@ -10,7 +10,8 @@
 // keys). Key ranges (few row tiles against many keys) leave fp32 partials that
 // cross_join_rows_kernel adds in order.
 //
-// Warp roles (384 threads): 0 = TMA producer, 1 = MMA issuer, 2 = K rows behind a length, 4..11 =
+// Warp roles (384 threads): 0 = TMA producer, 1 and 3 = MMA issuers (S; dP and
+// dQ), 2 = K rows behind a length, 4..11 =
 // softmax gradient (quarter = TMEM lanes = rows, half = 64 keys each) and the epilogue. Every wait
 // is bounded.
 #pragma once
@@ -34,7 +35,7 @@ struct RowsLay {
   static constexpr int T_S = 0, T_DP = 256, T_DQ = 384;
   static constexpr int Q_FULL = 0, DO_FULL = NB, Q_EMPTY = 2 * NB, S_FULL = 3 * NB, S_FREE = S_FULL + 2,
                        DP_FULL = S_FREE + 2, DS_FULL = DP_FULL + 1, ACC_FULL = DS_FULL + 1,
-                       ACC_EMPTY = ACC_FULL + 1, DRAIN = ACC_EMPTY + 1, K_FULL = DRAIN + 1,
+                       ACC_EMPTY = ACC_FULL + 1, DRAIN = ACC_EMPTY + 1, K_FULL = DRAIN + 2,
                        V_FULL = K_FULL + KST, K_EMPTY = V_FULL + VST, V_EMPTY = K_EMPTY + KST,
                        CLEAN = V_EMPTY + VST, COUNT = CLEAN + KST;
   static_assert(8 * COUNT + 8 <= 512, "barrier area");
@@ -90,7 +91,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   if (threadIdx.x == 0) {
     for (int k = 0; k < L::COUNT; ++k) {
       const bool key = k >= L::K_EMPTY && k < L::V_EMPTY;   // the products, and warp 2
-      ptx::mbar_init(bars + k, k == L::DS_FULL || k == L::ACC_EMPTY ? 8 : key && p.s.lens ? 2 : 1);
+      const bool two_of = (key && p.s.lens) || (k >= L::Q_EMPTY && k < L::S_FULL);          // both issuers
+      ptx::mbar_init(bars + k, k == L::DS_FULL || k == L::ACC_EMPTY ? 8 : two_of ? 2 : 1);
     }
     *abort_flag = 0;
     ptx::fence_barrier_init();
@@ -150,48 +152,63 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       for (int k = max(0, kv - L::VST); k < kv; ++k)
         ptx::mbar_drain(bars + L::V_FULL + k % L::VST, (k / L::VST) & 1, 100000000ll);
     } else if (warp == 1 && lane == 0) {
-      // ====================================== MMA issuer ======================================
+      // ===================================== issuer of S ======================================
+      const uint32_t sQ = ptx::smem_u32(sm + L::Q_OFF), sK = ptx::smem_u32(sm + L::K_OFF);
+      constexpr uint32_t TILE16 = L::TILE >> 4;
+      RowsWalk w(p);
+      int n = 0, k = 0;                            // units and key tiles so far
+      bool ok = true;
+      while (ok && w.next()) {
+        const int b = n % L::NB;
+        const uint32_t dQ = ptx::sdesc_lo(sQ, 16) + 2 * b * TILE16;
+        ok = ptx::mbar_wait(bars + L::Q_FULL + b, (n / L::NB) & 1, abort_flag, tmo);
+        for (int t = 0; ok && t < w.nt; ++t, ++k) {
+          // K(t) has landed, the buffer's last dS has been read by its dQ product
+          const int s = k % L::KST;
+          ok = ptx::mbar_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
+          if (ok && k >= 2) ok = ptx::mbar_wait(bars + L::S_FREE + (k & 1), (k / 2 - 1) & 1, abort_flag, tmo);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          issue_scores<DT>(tmem + L::T_S + 128 * (k & 1), dQ, ptx::sdesc_lo(sK, 16) + s * TILE16,
+                           ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps);
+          ptx::mma_commit(bars + L::S_FULL + (k & 1));
+        }
+        ptx::mma_commit(bars + L::Q_EMPTY + b);
+        ++n;
+      }
+      ptx::mma_commit(bars + L::DRAIN);
+      ptx::mbar_drain(bars + L::DRAIN, 0, 1000000000ll);
+    } else if (warp == 3 && lane == 0) {
+      // ================================= issuer of dP and dQ ==================================
       const uint32_t sQ = ptx::smem_u32(sm + L::Q_OFF), sK = ptx::smem_u32(sm + L::K_OFF);
       const uint32_t sV = ptx::smem_u32(sm + L::V_OFF);
       const uint32_t id_dq = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
       constexpr uint32_t TILE16 = L::TILE >> 4;
       RowsWalk w(p);
-      int n = 0, kv0 = 0;                          // units and key tiles before this unit
+      int n = 0, k0 = 0;                           // units and key tiles before this unit
       uint32_t clean = 0;                          // parities of the stages' CLEAN barriers
       bool ok = true;
       while (ok && w.next()) {
-        const int b = n % L::NB, par = (n / L::NB) & 1;
-        const uint32_t dQ = ptx::sdesc_lo(sQ, 16) + 2 * b * TILE16, ddO = dQ + TILE16;
-        // S(t): the buffer's last dS has been read by its dQ product, K(t) has landed
-        auto issue_s = [&](int t) {
-          const int k = kv0 + t, s = k % L::KST;
-          bool good = ptx::mbar_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
-          if (good && k >= 2) good = ptx::mbar_wait(bars + L::S_FREE + (k & 1), (k / 2 - 1) & 1, abort_flag, tmo);
-          if (!good) return false;
-          ptx::tc_fence_after();
-          issue_scores<DT>(tmem + L::T_S + 128 * (k & 1), dQ, ptx::sdesc_lo(sK, 16) + s * TILE16,
-                           ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps);
-          ptx::mma_commit(bars + L::S_FULL + (k & 1));
-          return true;
-        };
+        const int b = n % L::NB;
+        const uint32_t ddO = ptx::sdesc_lo(sQ, 16) + (2 * b + 1) * TILE16;
         // dP(t): its columns were read when dS(t-1) was stored
         auto issue_dp = [&](int t) {
-          const int k = kv0 + t, s = k % L::VST;
+          const int k = k0 + t, s = k % L::VST;
           if (!ptx::mbar_wait(bars + L::V_FULL + s, (k / L::VST) & 1, abort_flag, tmo)) return false;
           ptx::tc_fence_after();
           issue_scores<DT>(tmem + L::T_DP, ddO, ptx::sdesc_lo(sV, 16) + s * TILE16,
                            ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps);
           ptx::mma_commit(bars + L::DP_FULL);
           ptx::mma_commit(bars + L::V_EMPTY + s);
+          if (t == w.nt - 1) ptx::mma_commit(bars + L::Q_EMPTY + b);
           return true;
         };
-        ok = ptx::mbar_wait(bars + L::Q_FULL + b, par, abort_flag, tmo) && issue_s(0) &&
-             ptx::mbar_wait(bars + L::DO_FULL + b, par, abort_flag, tmo) && issue_dp(0) && (w.nt < 2 || issue_s(1));
+        ok = ptx::mbar_wait(bars + L::DO_FULL + b, (n / L::NB) & 1, abort_flag, tmo) && issue_dp(0);
         for (int t = 0; ok && t < w.nt; ++t) {
-          const int k = kv0 + t, s = k % L::KST;
+          const int k = k0 + t, s = k % L::KST;
           ok = ptx::mbar_wait(bars + L::DS_FULL, k & 1, abort_flag, tmo);
+          if (ok) ok = ptx::mbar_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
           if (ok && t + 1 < w.nt) ok = issue_dp(t + 1);
-          if (t == max(w.nt - 2, 0)) ptx::mma_commit(bars + L::Q_EMPTY + b);   // S and dP of all tiles are issued
           if (ok && t == 0 && n > 0) ok = ptx::mbar_wait(bars + L::ACC_EMPTY, (n - 1) & 1, abort_flag, tmo);
           if (ok && t == w.nt - 1 && w.unclean(t)) {
             ok = ptx::mbar_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);
@@ -209,15 +226,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           }
           ptx::mma_commit(bars + L::S_FREE + (k & 1));
           ptx::mma_commit(bars + L::K_EMPTY + s);
-          if (t + 2 < w.nt) ok = issue_s(t + 2);
         }
         if (!ok) break;
         ptx::mma_commit(bars + L::ACC_FULL);
-        kv0 += w.nt;
+        k0 += w.nt;
         ++n;
       }
-      ptx::mma_commit(bars + L::DRAIN);
-      ptx::mbar_drain(bars + L::DRAIN, 0, 1000000000ll);
+      ptx::mma_commit(bars + L::DRAIN + 1);
+      ptx::mbar_drain(bars + L::DRAIN + 1, 0, 1000000000ll);
     } else if (warp == 2 && p.s.lens) {
       // ============================ rows of K behind a sequence's end ==========================
       // Every tile is waited for and its stage released here too, so that this warp can be neither

@@ -19,8 +19,9 @@
 // tokens against long states) the keys are cut into ranges; a range leaves its rows' normalised O
 // in fp32 and their LSE, which cross_join_kernel combines in order.
 //
-// Warp roles (384 threads): 0 = TMA producer, 1 = MMA issuer, 2 = clears V rows that a length
-// leaves out, 4..7 = softmax of tile A, 8..11 = of tile B. Every wait is bounded; a CTA that gives
+// Warp roles (384 threads): 0 = TMA producer, 1 and 3 = MMA issuers of tiles A and B (one thread that
+// polled both tiles' barriers took 3100 cycles from a P to the next S, of which 1024 are products;
+// 870 TFLOP/s at 8192 x 8192 x 128), 2 = clears V rows that a length leaves out, 4..7 = softmax of tile A, 8..11 = of tile B. Every wait is bounded; a CTA that gives
 // up writes NaN into the LSE of its rows and records DASH_ERR_SYNC_TIMEOUT where asked to.
 #pragma once
 
@@ -46,10 +47,9 @@ struct FwdArgs {
 template <int DT>
 struct FwdLay {
   static constexpr int TILE = kTile * DT * 2;
-  static constexpr int STAGES = DT == 64 ? 4 : 2;
-  static constexpr int Q_OFF = 0;
-  static constexpr int KV_OFF = 2 * TILE;                     // stage s: K, then V
-  static constexpr int BAR_OFF = KV_OFF + 2 * STAGES * TILE;
+  static constexpr int KST = DT == 64 ? 4 : 2, VST = DT == 64 ? 4 : 3;   // stages of K and V
+  static constexpr int Q_OFF = 0, K_OFF = 2 * TILE, V_OFF = K_OFF + KST * TILE;
+  static constexpr int BAR_OFF = V_OFF + VST * TILE;
   static constexpr int ALLOC = BAR_OFF + 512 + 1024;          // slack for 1024 alignment
   static_assert(ALLOC <= 232448, "shared memory budget");
   static constexpr int T_S = 0, T_O = 256;
@@ -59,8 +59,8 @@ struct FwdLay {
   static_assert(T_O + 2 * DT + (kSepP ? 128 : 0) <= 512, "TMEM columns");
   // barriers
   static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6, PV_DONE = 8, DRAIN = 10,
-                       K_FULL = 11, V_FULL = K_FULL + STAGES, KV_EMPTY = V_FULL + STAGES,
-                       CLEAN = KV_EMPTY + STAGES, COUNT = CLEAN + STAGES;
+                       K_FULL = 12, V_FULL = K_FULL + KST, K_EMPTY = V_FULL + VST, V_EMPTY = K_EMPTY + KST,
+                       CLEAN = V_EMPTY + VST, COUNT = CLEAN + VST;
   static_assert(8 * COUNT + 8 <= 512, "barrier area");
 };
 
@@ -72,13 +72,14 @@ static_assert(kFwdRegsCtrl + 2 * kFwdRegsSoftmax == 3 * kFwdRegsLaunch,
 
 // A CTA's units: u, u + grid, ... Every role walks the same ones.
 struct FwdWalk {
-  const FwdArgs& p;
+  const FwdArgs* a;
   int u, bh, b, hk, pair, split;
   int len;                   // the batch's keys (-1: out of range)
   int t0, nt;                // first key tile and their number in this range
   bool has_b;
-  __device__ __forceinline__ FwdWalk(const FwdArgs& a) : p(a), u((int)blockIdx.x - (int)gridDim.x) {}
+  __device__ __forceinline__ FwdWalk(const FwdArgs& args) : a(&args), u((int)blockIdx.x - (int)gridDim.x) {}
   __device__ __forceinline__ bool next() {
+    const FwdArgs& p = *a;
     u += gridDim.x;
     if (u >= p.units) return false;
     split = u % p.splits;
@@ -99,18 +100,8 @@ struct FwdWalk {
   __device__ __forceinline__ int chunks(int t) const { return (keys(t) + 31) >> 5; }
   // Rows of the V tile that the product reads although the length leaves them out (rows beyond
   // the tensor arrive as zeros).
-  __device__ __forceinline__ bool unclean(int t) const { return len < p.s.Sk && (keys(t) & 31); }
+  __device__ __forceinline__ bool unclean(int t) const { return len < a->s.Sk && (keys(t) & 31); }
 };
-
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-      : "=r"(done)
-      : "r"(ptx::smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
 
 template <int DT>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -139,13 +130,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       ptx::mbar_init(bars + L::P_FULL + x, 4);
       ptx::mbar_init(bars + L::PV_DONE + x, 1);
     }
-    for (int s = 0; s < L::STAGES; ++s) {
+    for (int s = 0; s < L::KST; ++s) {
       ptx::mbar_init(bars + L::K_FULL + s, 1);
+      ptx::mbar_init(bars + L::K_EMPTY + s, 2);                   // both tiles
+    }
+    for (int s = 0; s < L::VST; ++s) {
       ptx::mbar_init(bars + L::V_FULL + s, 1);
-      ptx::mbar_init(bars + L::KV_EMPTY + s, p.s.lens ? 2 : 1);   // the products, and warp 2
+      ptx::mbar_init(bars + L::V_EMPTY + s, p.s.lens ? 3 : 2);   // and warp 2
       ptx::mbar_init(bars + L::CLEAN + s, 1);
     }
     ptx::mbar_init(bars + L::DRAIN, 1);
+    ptx::mbar_init(bars + L::DRAIN + 1, 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
@@ -160,7 +155,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (warp == 0 && lane == 0) {
       // ===================================== TMA producer =====================================
       FwdWalk w(p);
-      int nqx[2] = {0, 0}, kv = 0;                 // row tiles and key tiles loaded so far
+      int nqx[2] = {0, 0}, nk = 0, nv = 0;         // row tiles, tiles of K and V loaded so far
       bool ok = true;
       while (ok && w.next()) {
         if (w.nt == 0) continue;
@@ -172,109 +167,112 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             bars + L::Q_FULL + x);
           ++nqx[x];
         }
-        for (int t = 0; ok && t < (p.withhold ? 0 : w.nt); ++t, ++kv) {
-          const int s = kv % L::STAGES, n = kv / L::STAGES;
-          if (n > 0) ok = ptx::mbar_wait(bars + L::KV_EMPTY + s, (n - 1) & 1, abort_flag, tmo);
+        // the next unit's rows wait in L2
+        FwdWalk ahead = w;
+        if (ahead.next() && ahead.nt > 0)
+          for (int x = 0; x < (ahead.has_b ? 2 : 1); ++x)
+            prefetch_row_tile<DT>(p.s, &maps.q, ahead.b, ahead.hk, 2 * ahead.pair + x, p.s.q_b, p.s.q_h);
+        for (int t = 0; ok && t < (p.withhold ? 0 : w.nt); ++t) {
+          const int ks = nk % L::KST, km = nk / L::KST, vs = nv % L::VST, vm = nv / L::VST;
+          if (km > 0) ok = ptx::mbar_wait(bars + L::K_EMPTY + ks, (km - 1) & 1, abort_flag, tmo);
           if (!ok) break;
-          uint8_t* ks = sm + L::KV_OFF + 2 * s * L::TILE;
-          ptx::mbar_expect_tx(bars + L::K_FULL + s, L::TILE);
-          load_key_tile<DT>(&maps.k, ks, w.b, w.hk, w.t0 + t, p.s.k_b, p.s.k_h, bars + L::K_FULL + s);
-          ptx::mbar_expect_tx(bars + L::V_FULL + s, L::TILE);
-          load_key_tile<DT>(&maps.v, ks + L::TILE, w.b, w.hk, w.t0 + t, p.s.v_b, p.s.v_h, bars + L::V_FULL + s);
+          ptx::mbar_expect_tx(bars + L::K_FULL + ks, L::TILE);
+          load_key_tile<DT>(&maps.k, sm + L::K_OFF + ks * L::TILE, w.b, w.hk, w.t0 + t, p.s.k_b, p.s.k_h,
+                            bars + L::K_FULL + ks);
+          ++nk;
+          if (vm > 0) ok = ptx::mbar_wait(bars + L::V_EMPTY + vs, (vm - 1) & 1, abort_flag, tmo);
+          if (!ok) break;
+          ptx::mbar_expect_tx(bars + L::V_FULL + vs, L::TILE);
+          load_key_tile<DT>(&maps.v, sm + L::V_OFF + vs * L::TILE, w.b, w.hk, w.t0 + t, p.s.v_b, p.s.v_h,
+                            bars + L::V_FULL + vs);
+          ++nv;
         }
       }
       // drain: every issued load has landed before the CTA may exit
       for (int x = 0; x < 2; ++x)
         if (nqx[x] > 0) ptx::mbar_drain(bars + L::Q_FULL + x, (nqx[x] - 1) & 1, 100000000ll);
-      for (int k = max(0, kv - L::STAGES); k < kv; ++k) {
-        ptx::mbar_drain(bars + L::K_FULL + k % L::STAGES, (k / L::STAGES) & 1, 100000000ll);
-        ptx::mbar_drain(bars + L::V_FULL + k % L::STAGES, (k / L::STAGES) & 1, 100000000ll);
-      }
-    } else if (warp == 1 && lane == 0) {
-      // ====================================== MMA issuer ======================================
-      // In each unit ns[x] and np[x] are the next S and P V of tile x. The loop polls and issues
-      // what is ready, each tile's P V before either S: the pipe runs products in issue order,
-      // and a P V gates its tile's next S and the key tile's release.
-      const uint32_t sQ = ptx::smem_u32(sm + L::Q_OFF), sKV = ptx::smem_u32(sm + L::KV_OFF);
+      for (int k = max(0, nk - L::KST); k < nk; ++k)
+        ptx::mbar_drain(bars + L::K_FULL + k % L::KST, (k / L::KST) & 1, 100000000ll);
+      for (int k = max(0, nv - L::VST); k < nv; ++k)
+        ptx::mbar_drain(bars + L::V_FULL + k % L::VST, (k / L::VST) & 1, 100000000ll);
+    } else if ((warp == 1 || warp == 3) && lane == 0) {
+      // ================================ MMA issuer of tile x ==================================
+      // S(t) needs K(t); over P's columns (DT = 128) also P(t-1) V(t-1) done. With P in columns of
+      // its own (DT = 64) S(t+1) goes ahead of P(t) V(t).
+      const int x = warp >> 1;
+      const uint32_t dQ = ptx::sdesc_lo(ptx::smem_u32(sm + L::Q_OFF + x * L::TILE), 16);
+      const uint32_t sK = ptx::smem_u32(sm + L::K_OFF), sV = ptx::smem_u32(sm + L::V_OFF);
       const uint32_t id_o = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
-      constexpr uint32_t TILE16 = L::TILE >> 4, MN_STEP = 2048 >> 4;
+      constexpr uint32_t MN_STEP = 2048 >> 4;
       FwdWalk w(p);
-      int tq[2] = {0, 0}, ts[2] = {0, 0}, tp[2] = {0, 0};   // units, S and P V of tile x so far
-      int kv0 = 0;
+      int n = 0, k = 0, pv = 0;                    // this tile's units and products P V, all key tiles so far
       uint32_t clean = 0;                          // parities of the stages' CLEAN barriers
       bool ok = true;
-      long long t_last = global_timer_ns();
       while (ok && w.next()) {
         if (w.nt == 0) continue;
-        const int ntx[2] = {w.nt, w.has_b ? w.nt : 0};
-        const int dirty = w.unclean(w.nt - 1) ? w.nt - 1 : -1;   // the last tile alone can be
-        int ns[2] = {0, 0}, np[2] = {0, 0}, released = 0;
-        while (ok && (np[0] < ntx[0] || np[1] < ntx[1])) {
-          bool progress = false;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int t = np[x], s = (kv0 + t) % L::STAGES;
-            if (t < ns[x] && mbar_test(bars + L::P_FULL + x, tp[x] & 1) &&
-                mbar_test(bars + L::V_FULL + s, ((kv0 + t) / L::STAGES) & 1) &&
-                (t != dirty || mbar_test(bars + L::CLEAN + s, (clean >> s) & 1))) {
-              ptx::tc_fence_after();
-              const uint32_t dV = ptx::sdesc_lo(sKV + (2 * s + 1) * L::TILE, kTile * 128);
-              const int steps = 2 * w.chunks(t);
-#pragma unroll
-              for (int ks = 0; ks < kTile / 16; ++ks)
-                if (ks < steps)
-                  ptx::mma_ts(tmem + L::T_O + DT * x, tmem + L::T_P + L::P_STRIDE * x + 8 * ks, dV + ks * MN_STEP,
-                              id_o, (t > 0 || ks > 0) ? 1u : 0u);
-              ptx::mma_commit(bars + L::PV_DONE + x);
-              ++np[x];
-              ++tp[x];
-              progress = true;
+        const bool last_dirty = w.unclean(w.nt - 1);
+        if (x && !w.has_b) {                       // nothing to issue: the stages are released all the same
+          for (int t = 0; ok && t < w.nt; ++t) {
+            const int ks = (k + t) % L::KST, vs = (k + t) % L::VST;
+            ok = ptx::mbar_wait(bars + L::K_FULL + ks, ((k + t) / L::KST) & 1, abort_flag, tmo);
+            if (ok) ptx::mbar_arrive(bars + L::K_EMPTY + ks);
+            if (ok) ok = ptx::mbar_wait(bars + L::V_FULL + vs, ((k + t) / L::VST) & 1, abort_flag, tmo);
+            if (ok && t == w.nt - 1 && last_dirty) {
+              ok = ptx::mbar_wait(bars + L::CLEAN + vs, (clean >> vs) & 1, abort_flag, tmo);
+              clean ^= 1u << vs;
             }
+            if (ok) ptx::mbar_arrive(bars + L::V_EMPTY + vs);
           }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int t = ns[x], s = (kv0 + t) % L::STAGES;
-            // S_x follows the tile's last P V (over whose P it is written when DT = 128)
-            if (t < ntx[x] && t == np[x] && mbar_test(bars + L::K_FULL + s, ((kv0 + t) / L::STAGES) & 1) &&
-                (t > 0 || mbar_test(bars + L::Q_FULL + x, tq[x] & 1)) &&
-                (L::kSepP || tp[x] == 0 || mbar_test(bars + L::PV_DONE + x, (tp[x] - 1) & 1))) {
-              ptx::tc_fence_after();
-              const uint32_t id_s = ptx::idesc_bf16(128, 32 * w.chunks(t), 0, 0);
-              const uint32_t dQ = ptx::sdesc_lo(sQ, 16) + x * TILE16;
-              const uint32_t dK = ptx::sdesc_lo(sKV, 16) + 2 * s * TILE16;
-#pragma unroll
-              for (int ks = 0; ks < DT / 16; ++ks) {
-                const uint32_t step = ((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4;
-                if (ks < dsteps) ptx::mma_lo(tmem + L::T_S + 128 * x, dQ + step, dK + step, id_s, ks > 0);
-              }
-              ptx::mma_commit(bars + L::S_FULL + x);
-              if (t == w.nt - 1) {
-                ptx::mma_commit(bars + L::Q_EMPTY + x);
-                ++tq[x];
-              }
-              ++ns[x];
-              ++ts[x];
-              progress = true;
-            }
-          }
-          while (released < w.nt && np[0] > released && (!w.has_b || np[1] > released)) {
-            ptx::mma_commit(bars + L::KV_EMPTY + (kv0 + released) % L::STAGES);
-            ++released;
-          }
-          if (progress) {
-            t_last = global_timer_ns();
-          } else if (*abort_flag) {
-            ok = false;
-          } else if (global_timer_ns() - t_last > tmo) {
-            *abort_flag = 1;
-            ok = false;
-          }
+          k += w.nt;
+          continue;
         }
-        if (dirty >= 0) clean ^= 1u << ((kv0 + dirty) % L::STAGES);
-        kv0 += w.nt;
+        auto issue_s = [&](int t) {
+          const int s = (k + t) % L::KST;
+          bool good = ptx::mbar_wait(bars + L::K_FULL + s, ((k + t) / L::KST) & 1, abort_flag, tmo);
+          if (good && !L::kSepP && pv > 0) good = ptx::mbar_wait(bars + L::PV_DONE + x, (pv - 1) & 1, abort_flag, tmo);
+          if (!good) return false;
+          ptx::tc_fence_after();
+          const uint32_t id_s = ptx::idesc_bf16(128, 32 * w.chunks(t), 0, 0);
+          const uint32_t dK = ptx::sdesc_lo(sK + s * L::TILE, 16);
+#pragma unroll
+          for (int ks = 0; ks < DT / 16; ++ks) {
+            const uint32_t step = ((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4;
+            if (ks < dsteps) ptx::mma_lo(tmem + L::T_S + 128 * x, dQ + step, dK + step, id_s, ks > 0);
+          }
+          ptx::mma_commit(bars + L::S_FULL + x);
+          ptx::mma_commit(bars + L::K_EMPTY + s);
+          if (t == w.nt - 1) ptx::mma_commit(bars + L::Q_EMPTY + x);
+          return true;
+        };
+        ok = ptx::mbar_wait(bars + L::Q_FULL + x, n & 1, abort_flag, tmo) && issue_s(0);
+        for (int t = 0; ok && t < w.nt; ++t) {
+          const int s = (k + t) % L::VST;
+          ok = ptx::mbar_wait(bars + L::P_FULL + x, pv & 1, abort_flag, tmo);
+          if (ok && L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1);
+          if (ok) ok = ptx::mbar_wait(bars + L::V_FULL + s, ((k + t) / L::VST) & 1, abort_flag, tmo);
+          if (ok && t == w.nt - 1 && last_dirty) {
+            ok = ptx::mbar_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);
+            clean ^= 1u << s;
+          }
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t dV = ptx::sdesc_lo(sV + s * L::TILE, kTile * 128);
+          const int steps = 2 * w.chunks(t);
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            if (ks < steps)
+              ptx::mma_ts(tmem + L::T_O + DT * x, tmem + L::T_P + L::P_STRIDE * x + 8 * ks, dV + ks * MN_STEP, id_o,
+                          (t > 0 || ks > 0) ? 1u : 0u);
+          ptx::mma_commit(bars + L::PV_DONE + x);
+          ptx::mma_commit(bars + L::V_EMPTY + s);
+          ++pv;
+          if (!L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1);
+        }
+        k += w.nt;
+        ++n;
       }
-      ptx::mma_commit(bars + L::DRAIN);
-      ptx::mbar_drain(bars + L::DRAIN, 0, 1000000000ll);
+      ptx::mma_commit(bars + L::DRAIN + x);
+      ptx::mbar_drain(bars + L::DRAIN + x, 0, 1000000000ll);
     } else if (warp == 2 && p.s.lens) {
       // ============================ rows of V behind a sequence's end ==========================
       // Every tile is waited for and its stage released here too, so that this warp can be neither
@@ -284,16 +282,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       bool ok = true;
       while (ok && w.next()) {
         for (int t = 0; t < w.nt; ++t, ++kv) {
-          const int s = kv % L::STAGES;
-          ok = ptx::warp_wait(bars + L::V_FULL + s, (kv / L::STAGES) & 1, abort_flag, tmo);
+          const int s = kv % L::VST;
+          ok = ptx::warp_wait(bars + L::V_FULL + s, (kv / L::VST) & 1, abort_flag, tmo);
           if (!ok) break;
           if (t == w.nt - 1 && w.unclean(t)) {
-            clear_rows<DT>(sm + L::KV_OFF + (2 * s + 1) * L::TILE, w.keys(t), 32 * w.chunks(t), lane);
+            clear_rows<DT>(sm + L::V_OFF + s * L::TILE, w.keys(t), 32 * w.chunks(t), lane);
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bars + L::CLEAN + s);
           }
-          if (lane == 0) ptx::mbar_arrive(bars + L::KV_EMPTY + s);
+          if (lane == 0) ptx::mbar_arrive(bars + L::V_EMPTY + s);
         }
       }
     }
@@ -341,6 +339,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float m_row = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
         const bool moved = m_row > m + kRescaleLog2;
         const float m_new = moved ? m_row : m;
+        // P's columns, and O where it is rescaled, are the last product's until that is done (DT = 128: it
+        // was, before this S)
+        if (L::kSepP && t > 0) {
+          ok = ptx::warp_wait(bars + L::PV_DONE + x, (steps - 1) & 1, abort_flag, tmo);
+          if (!ok) break;
+          ptx::tc_fence_after();
+        }
         const uint64_t scale2 = two(p.scale_log2, p.scale_log2), off2 = two(-m_new, -m_new);
         uint64_t lt[2] = {0ull, 0ull};             // four partial sums
 #pragma unroll
@@ -363,7 +368,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float alpha = moved ? ptx::ex2(m - m_new) : 1.f;
         l = l * alpha + (lt0 + lt1);
         m = m_new;
-        // the products before this S have ended, O's last one among them
         if (t > 0 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int c0 = 0; c0 < DT; c0 += 32) {

@@ -34,7 +34,6 @@
 // read-out and the epilogue of dK and dV. Every wait is bounded.
 #pragma once
 
-#include "bwd_main.cuh"
 #include "cross_common.cuh"
 
 namespace dash {
@@ -92,6 +91,8 @@ enum {
 static_assert(8 * C_COUNT + 8 <= 256, "barrier area");
 
 // A CTA's tasks: units u, u + grid, ..., of each the row tiles.
+// ALL: a whole warp walks together.
+template <bool ALL = false>
 struct KeysWalk {
   const BwdArgs& p;
   int u, bh, b, hk, qseg, kt, len;
@@ -110,6 +111,7 @@ struct KeysWalk {
       b = bh / p.s.Hk;
       hk = bh - b * p.s.Hk;
       len = length_of(p.s, b);
+      if (ALL) len = same(len);
       q0 = qseg * p.qper;
       nqt = min(p.qper, p.s.ntile - q0);
     } while (kt * kTile >= len);
@@ -120,26 +122,6 @@ struct KeysWalk {
   __device__ __forceinline__ bool last_of_tile() const { return j == nqt - 1; }
   __device__ __forceinline__ int tile() const { return q0 + j; }
 };
-
-// The K steps of a product of two K-major operands, of which `n` are taken.
-template <int DT>
-__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t id, int n) {
-#pragma unroll
-  for (int ks = 0; ks < DT / 16; ++ks) {
-    if (ks < n) ptx::mma_lo(d, a, b, id, ks > 0);
-    a = ks == 3 ? next_k<3>(a) : next_k<0>(a);
-    b = ks == 3 ? next_k<3>(b) : next_k<0>(b);
-  }
-}
-// dQ^T's K steps of which n hold keys (both operands MN-major).
-__device__ __forceinline__ void issue_dq(uint32_t d, uint32_t a, uint32_t b, uint32_t id, int n) {
-#pragma unroll
-  for (int ks = 0; ks < 8; ++ks) {
-    if (ks < n) ptx::mma_lo(d, a, b, id, ks > 0);
-    a = ptx::step_add<kMnStep>(a);
-    b = ptx::step_add<kMnStep>(b);
-  }
-}
 
 // -Delta = -rowsum(dO * O) and -LSE log2e per row, in row tiles; 16 lanes a row, kPreRows rows one
 // after the other. Rows of batches without keys get their dq here: 0, or NaN for a length out of
@@ -227,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = (uint64_t*)(sm + L::BAR_OFF);
   uint32_t* tmem_slot = (uint32_t*)(sm + L::BAR_OFF + 8 * C_COUNT);
   volatile int* abort_flag = (volatile int*)(sm + L::BAR_OFF + 8 * C_COUNT + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = same((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const long long tmo = p.timeout_ns;
   const int dsteps = (p.s.D + 15) >> 4;
 
@@ -258,14 +240,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = same(*tmem_slot);
   train::grid_wait();                              // Delta and LSE are there, the header is clear
 
   if (warp < 4) {
     ptx::regs_dec<L::REGS_SINGLE>();
     if (warp == 0 && lane == 0) {
       // ===================================== TMA producer =====================================
-      KeysWalk w(p);
+      KeysWalk<> w(p);
       int it = 0, tl = 0, loaded = 0;              // tasks, key tiles, dO tiles
       bool ok = !p.withhold;
       while (ok && w.next()) {
@@ -315,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tl > 0) ptx::mbar_drain(bars + C_KV_FULL, (tl - 1) & 1, 100000000ll);
     } else if (warp == 2) {
       // ============================== key rows behind a length ================================
-      KeysWalk w(p);
+      KeysWalk<> w(p);
       int tl = 0;
       bool ok = true;
       while (ok && w.next()) {
@@ -331,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bars + C_KV_READY);
         ++tl;
       }
-    } else if ((warp == 1 || warp == 3) && lane == 0) {
+    } else if (warp == 1 || warp == 3) {
       // ==================================== MMA issuers =======================================
       // Warp 1 issues S^T and dV, warp 3 dP^T, dK and dQ^T, each in the tasks' order: so neither
       // chain waits in line behind the other's barriers.
@@ -340,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t ID_S = ptx::idesc_bf16(128, 128, 0, 0);
       const uint32_t id_ts = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
       constexpr uint32_t BUF_STEP = L::TILE >> 4;
-      KeysWalk w(p);
+      KeysWalk<true> w(p);
+      const uint32_t one = elect_one();
       int it = 0, tile = -1;
       bool ok = true;
       if (warp == 1) {
@@ -351,24 +334,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qb = it % L::NQ, ob = it % L::NDO;
           // ---- S^T(it), once Q(it) has landed and what lies over its columns has been read: P^T(it-1)
           // by dV, with DQ also dS^T(it-1) by dK
-          if (first) ok = ptx::mbar_wait(bars + C_KV_READY, ++tile & 1, abort_flag, tmo);
-          if (ok) ok = ptx::mbar_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
-          if (ok && it > 0) ok = ptx::mbar_wait(bars + C_SP_FREE, (it - 1) & 1, abort_flag, tmo);
+          if (first) ok = ptx::warp_wait(bars + C_KV_READY, ++tile & 1, abort_flag, tmo);
+          if (ok) ok = ptx::warp_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
+          if (ok && it > 0) ok = ptx::warp_wait(bars + C_SP_FREE, (it - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::tc_fence_after();
-          issue_scores<DT>(tmem + L::T_SP, dK_k, dQ_k + qb * BUF_STEP, ID_S, dsteps);
-          ptx::mma_commit(bars + C_S_FULL);
-          if (last) ptx::mma_commit(bars + C_KV_EMPTY);
+          issue_scores<DT>(tmem + L::T_SP, dK_k, dQ_k + qb * BUF_STEP, ID_S, dsteps, one);
+          commit(bars + C_S_FULL, one);
+          if (last) commit(bars + C_KV_EMPTY, one);
           // ---- dV += P^T dO, once P^T(it) is stored and the last key tile's sums were read out
-          ok = ptx::mbar_wait(bars + C_P_FULL, it & 1, abort_flag, tmo);
-          if (ok) ok = ptx::mbar_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
-          if (ok && first && tile > 0) ok = ptx::mbar_wait(bars + C_ACC_EMPTY, (tile - 1) & 1, abort_flag, tmo);
+          ok = ptx::warp_wait(bars + C_P_FULL, it & 1, abort_flag, tmo);
+          if (ok) ok = ptx::warp_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
+          if (ok && first && tile > 0) ok = ptx::warp_wait(bars + C_ACC_EMPTY, (tile - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::tc_fence_after();
-          issue_ts(tmem + L::T_DV, tmem + L::T_SP, ddO_mn + ob * BUF_STEP, id_ts, first ? 0u : 1u);
-          ptx::mma_commit(bars + C_SP_FREE);
-          ptx::mma_commit(bars + C_DO_EMPTY + ob);
-          if (last) ptx::mma_commit(bars + C_ACC_FULL);
+          issue_rows<true>(tmem + L::T_DV, tmem + L::T_SP, ddO_mn + ob * BUF_STEP, id_ts, first ? 0u : 1u, 8, one);
+          commit(bars + C_SP_FREE, one);
+          commit(bars + C_DO_EMPTY + ob, one);
+          if (last) commit(bars + C_ACC_FULL, one);
           ++it;
         }
       } else {
@@ -382,42 +365,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qb = it % L::NQ, ob = it % L::NDO, ksteps = (w.keys() + 15) >> 4;
           // ---- dP^T(it), once dO(it) has landed and its columns are free: dS^T(it-1) read by dK, with
           // DQ dQ^T(it-1) out of TMEM
-          if (first) ok = ptx::mbar_wait(bars + C_KV_READY, ++tile & 1, abort_flag, tmo);
-          if (ok) ok = ptx::mbar_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
+          if (first) ok = ptx::warp_wait(bars + C_KV_READY, ++tile & 1, abort_flag, tmo);
+          if (ok) ok = ptx::warp_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
           if (ok && it > 0) {
-            if (!DQ) ok = ptx::mbar_wait(bars + C_DP_FREE, (it - 1) & 1, abort_flag, tmo);
-            else if (!L::kSepDQ) ok = ptx::mbar_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
+            if (!DQ) ok = ptx::warp_wait(bars + C_DP_FREE, (it - 1) & 1, abort_flag, tmo);
+            else if (!L::kSepDQ) ok = ptx::warp_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
           }
           if (!ok) break;
           ptx::tc_fence_after();
-          issue_scores<DT>(tmem + L::T_DP, dV_k, ddO_k + ob * BUF_STEP, ID_S, dsteps);
-          ptx::mma_commit(bars + C_DP_FULL);
-          ptx::mma_commit(bars + C_DO_EMPTY + ob);
-          if (last && !DQ) ptx::mma_commit(bars + C_KV_EMPTY);
+          issue_scores<DT>(tmem + L::T_DP, dV_k, ddO_k + ob * BUF_STEP, ID_S, dsteps, one);
+          commit(bars + C_DP_FULL, one);
+          commit(bars + C_DO_EMPTY + ob, one);
+          if (last && !DQ) commit(bars + C_KV_EMPTY, one);
           // ---- dK += dS^T Q, once dS^T(it) is stored
-          ok = ptx::mbar_wait(bars + C_DS_FULL, it & 1, abort_flag, tmo);
-          if (ok) ok = ptx::mbar_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
-          if (ok && first && tile > 0) ok = ptx::mbar_wait(bars + C_ACC_EMPTY, (tile - 1) & 1, abort_flag, tmo);
+          ok = ptx::warp_wait(bars + C_DS_FULL, it & 1, abort_flag, tmo);
+          if (ok) ok = ptx::warp_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
+          if (ok && first && tile > 0) ok = ptx::warp_wait(bars + C_ACC_EMPTY, (tile - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::tc_fence_after();
-          issue_ts(tmem + L::T_DK, tmem + L::T_DS, dQ_mn + qb * BUF_STEP, id_ts, first ? 0u : 1u);
-          ptx::mma_commit(bars + (DQ ? C_SP_FREE : C_DP_FREE));
-          ptx::mma_commit(bars + C_Q_EMPTY + qb);
-          if (last) ptx::mma_commit(bars + C_ACC_FULL);
+          issue_rows<true>(tmem + L::T_DK, tmem + L::T_DS, dQ_mn + qb * BUF_STEP, id_ts, first ? 0u : 1u, 8, one);
+          commit(bars + (DQ ? C_SP_FREE : C_DP_FREE), one);
+          commit(bars + C_Q_EMPTY + qb, one);
+          if (last) commit(bars + C_ACC_FULL, one);
           if (DQ) {
             // ---- dQ^T = K^T dS^T
-            if (L::kSepDQ && it > 0) ok = ptx::mbar_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
+            if (L::kSepDQ && it > 0) ok = ptx::warp_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
             if (!ok) break;
             ptx::tc_fence_after();
-            issue_dq(tmem + L::T_DQ, dKt_mn, dDS_mn, ID_DQ, ksteps);
-            ptx::mma_commit(bars + C_DQ_FULL);
-            if (last) ptx::mma_commit(bars + C_KV_EMPTY);
+            issue_mn(tmem + L::T_DQ, dKt_mn, dDS_mn, ID_DQ, ksteps, one);
+            commit(bars + C_DQ_FULL, one);
+            if (last) commit(bars + C_KV_EMPTY, one);
           }
           ++it;
         }
       }
       // drain: no MMA may be in flight when TMEM is released
-      ptx::mma_commit(bars + C_DRAIN + (warp >> 1));
+      commit(bars + C_DRAIN + (warp >> 1), one);
       ptx::mbar_drain(bars + C_DRAIN + (warp >> 1), 0, 1000000000ll);
     }
   } else if (warp < 12) {
@@ -427,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int col0 = half * 64;                    // this thread's 64 rows
     const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
     const uint32_t sDS = ptx::smem_u32(sm + L::DS_OFF);
-    KeysWalk w(p);
+    KeysWalk<> w(p);
     int it = 0;
     bool ok = true;
     while (ok && w.next()) {
@@ -513,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;           // d of dQ^T; key of dK and dV
     const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
-    KeysWalk w(p);
+    KeysWalk<> w(p);
     int it = 0, tl = 0;
     bool ok = true;
     while (ok && w.next()) {

@@ -47,6 +47,8 @@ static_assert(kRowsRegsCtrl + 2 * kRowsRegsSoftmax == 3 * kRowsRegsLaunch,
 
 // A CTA's units: u, u + grid, ...; those without keys are passed over (cross_pre_kernel writes their
 // rows, and the join reads no range behind a length).
+// ALL: a whole warp walks together.
+template <bool ALL = false>
 struct RowsWalk {
   const BwdArgs* a;
   int u, bh, b, hk, tile, kseg, len, t0, nt;
@@ -63,6 +65,7 @@ struct RowsWalk {
       b = bh / p.s.Hk;
       hk = bh - b * p.s.Hk;
       len = length_of(p.s, b);
+      if (ALL) len = same(len);
       t0 = kseg * p.kper;
       nt = min((max(len, 0) + kTile - 1) / kTile, t0 + p.kper) - t0;
     } while (nt <= 0);
@@ -83,7 +86,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   uint64_t* bars = (uint64_t*)(sm + L::BAR_OFF);
   uint32_t* tmem_slot = (uint32_t*)(sm + L::BAR_OFF + 8 * L::COUNT);
   volatile int* abort_flag = (volatile int*)(sm + L::BAR_OFF + 8 * L::COUNT + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = same((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const long long tmo = p.timeout_ns;
   const int dsteps = (p.s.D + 15) >> 4;
 
@@ -101,14 +104,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = same(*tmem_slot);
   train::grid_wait();                              // Delta and LSE are there, the header is clear
 
   if (warp < 4) {
     ptx::regs_dec<kRowsRegsCtrl>();
     if (warp == 0 && lane == 0) {
       // ===================================== TMA producer =====================================
-      RowsWalk w(p);
+      RowsWalk<> w(p);
       int n = 0, kv = 0, nk = 0;                   // units, key tiles (V), K tiles so far
       bool ok = !p.withhold;
       while (ok && w.next()) {
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         load_row_tile<DT>(p.s, &maps.dO, q + L::TILE, w.b, w.hk, w.tile, 1, 1, bars + L::DO_FULL + b);
         ++n;
         // the next unit's rows wait in L2
-        RowsWalk ahead = w;
+        RowsWalk<> ahead = w;
         if (ahead.next()) {
           prefetch_row_tile<DT>(p.s, &maps.q, ahead.b, ahead.hk, ahead.tile, p.s.q_b, p.s.q_h);
           prefetch_row_tile<DT>(p.s, &maps.dO, ahead.b, ahead.hk, ahead.tile, 1, 1);
@@ -151,40 +154,42 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         ptx::mbar_drain(bars + L::K_FULL + k % L::KST, (k / L::KST) & 1, 100000000ll);
       for (int k = max(0, kv - L::VST); k < kv; ++k)
         ptx::mbar_drain(bars + L::V_FULL + k % L::VST, (k / L::VST) & 1, 100000000ll);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ===================================== issuer of S ======================================
       const uint32_t sQ = ptx::smem_u32(sm + L::Q_OFF), sK = ptx::smem_u32(sm + L::K_OFF);
       constexpr uint32_t TILE16 = L::TILE >> 4;
-      RowsWalk w(p);
+      RowsWalk<true> w(p);
+      const uint32_t one = elect_one();
       int n = 0, k = 0;                            // units and key tiles so far
       bool ok = true;
       while (ok && w.next()) {
         const int b = n % L::NB;
         const uint32_t dQ = ptx::sdesc_lo(sQ, 16) + 2 * b * TILE16;
-        ok = ptx::mbar_wait(bars + L::Q_FULL + b, (n / L::NB) & 1, abort_flag, tmo);
+        ok = ptx::warp_wait(bars + L::Q_FULL + b, (n / L::NB) & 1, abort_flag, tmo);
         for (int t = 0; ok && t < w.nt; ++t, ++k) {
           // K(t) has landed, the buffer's last dS has been read by its dQ product
           const int s = k % L::KST;
-          ok = ptx::mbar_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
-          if (ok && k >= 2) ok = ptx::mbar_wait(bars + L::S_FREE + (k & 1), (k / 2 - 1) & 1, abort_flag, tmo);
+          ok = ptx::warp_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
+          if (ok && k >= 2) ok = ptx::warp_wait(bars + L::S_FREE + (k & 1), (k / 2 - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::tc_fence_after();
           issue_scores<DT>(tmem + L::T_S + 128 * (k & 1), dQ, ptx::sdesc_lo(sK, 16) + s * TILE16,
-                           ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps);
-          ptx::mma_commit(bars + L::S_FULL + (k & 1));
+                           ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps, one);
+          commit(bars + L::S_FULL + (k & 1), one);
         }
-        ptx::mma_commit(bars + L::Q_EMPTY + b);
+        commit(bars + L::Q_EMPTY + b, one);
         ++n;
       }
-      ptx::mma_commit(bars + L::DRAIN);
+      commit(bars + L::DRAIN, one);
       ptx::mbar_drain(bars + L::DRAIN, 0, 1000000000ll);
-    } else if (warp == 3 && lane == 0) {
+    } else if (warp == 3) {
       // ================================= issuer of dP and dQ ==================================
       const uint32_t sQ = ptx::smem_u32(sm + L::Q_OFF), sK = ptx::smem_u32(sm + L::K_OFF);
       const uint32_t sV = ptx::smem_u32(sm + L::V_OFF);
       const uint32_t id_dq = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
       constexpr uint32_t TILE16 = L::TILE >> 4;
-      RowsWalk w(p);
+      RowsWalk<true> w(p);
+      const uint32_t one = elect_one();
       int n = 0, k0 = 0;                           // units and key tiles before this unit
       uint32_t clean = 0;                          // parities of the stages' CLEAN barriers
       bool ok = true;
@@ -194,51 +199,45 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         // dP(t): its columns were read when dS(t-1) was stored
         auto issue_dp = [&](int t) {
           const int k = k0 + t, s = k % L::VST;
-          if (!ptx::mbar_wait(bars + L::V_FULL + s, (k / L::VST) & 1, abort_flag, tmo)) return false;
+          if (!ptx::warp_wait(bars + L::V_FULL + s, (k / L::VST) & 1, abort_flag, tmo)) return false;
           ptx::tc_fence_after();
           issue_scores<DT>(tmem + L::T_DP, ddO, ptx::sdesc_lo(sV, 16) + s * TILE16,
-                           ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps);
-          ptx::mma_commit(bars + L::DP_FULL);
-          ptx::mma_commit(bars + L::V_EMPTY + s);
-          if (t == w.nt - 1) ptx::mma_commit(bars + L::Q_EMPTY + b);
+                           ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps, one);
+          commit(bars + L::DP_FULL, one);
+          commit(bars + L::V_EMPTY + s, one);
+          if (t == w.nt - 1) commit(bars + L::Q_EMPTY + b, one);
           return true;
         };
-        ok = ptx::mbar_wait(bars + L::DO_FULL + b, (n / L::NB) & 1, abort_flag, tmo) && issue_dp(0);
+        ok = ptx::warp_wait(bars + L::DO_FULL + b, (n / L::NB) & 1, abort_flag, tmo) && issue_dp(0);
         for (int t = 0; ok && t < w.nt; ++t) {
           const int k = k0 + t, s = k % L::KST;
-          ok = ptx::mbar_wait(bars + L::DS_FULL, k & 1, abort_flag, tmo);
-          if (ok) ok = ptx::mbar_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
+          ok = ptx::warp_wait(bars + L::DS_FULL, k & 1, abort_flag, tmo);
+          if (ok) ok = ptx::warp_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
           if (ok && t + 1 < w.nt) ok = issue_dp(t + 1);
-          if (ok && t == 0 && n > 0) ok = ptx::mbar_wait(bars + L::ACC_EMPTY, (n - 1) & 1, abort_flag, tmo);
+          if (ok && t == 0 && n > 0) ok = ptx::warp_wait(bars + L::ACC_EMPTY, (n - 1) & 1, abort_flag, tmo);
           if (ok && t == w.nt - 1 && w.unclean(t)) {
-            ok = ptx::mbar_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);
+            ok = ptx::warp_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);
             clean ^= 1u << s;
           }
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t dK = ptx::sdesc_lo(sK + s * L::TILE, kTile * 128);
-          uint32_t a = tmem + L::T_S + 128 * (k & 1);
-          const int steps = w.steps(t);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            if (ks < steps) ptx::mma_ts(tmem + L::T_DQ, a, dK + ks * kMnStep, id_dq, (t > 0 || ks > 0) ? 1u : 0u);
-            a = ks == 3 ? next_ts<3>(a) : next_ts<0>(a);
-          }
-          ptx::mma_commit(bars + L::S_FREE + (k & 1));
-          ptx::mma_commit(bars + L::K_EMPTY + s);
+          issue_rows<true>(tmem + L::T_DQ, tmem + L::T_S + 128 * (k & 1), dK, id_dq, t > 0 ? 1u : 0u, w.steps(t), one);
+          commit(bars + L::S_FREE + (k & 1), one);
+          commit(bars + L::K_EMPTY + s, one);
         }
         if (!ok) break;
-        ptx::mma_commit(bars + L::ACC_FULL);
+        commit(bars + L::ACC_FULL, one);
         k0 += w.nt;
         ++n;
       }
-      ptx::mma_commit(bars + L::DRAIN + 1);
+      commit(bars + L::DRAIN + 1, one);
       ptx::mbar_drain(bars + L::DRAIN + 1, 0, 1000000000ll);
     } else if (warp == 2 && p.s.lens) {
       // ============================ rows of K behind a sequence's end ==========================
       // Every tile is waited for and its stage released here too, so that this warp can be neither
       // ahead of the copies nor behind the products by more than a barrier's phase.
-      RowsWalk w(p);
+      RowsWalk<> w(p);
       int kv = 0;
       bool ok = true;
       while (ok && w.next()) {
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const int r = quarter * 32 + lane;             // row within the tile = TMEM lane
     const int col0 = half * 64;                    // this thread's 64 keys
     const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
-    RowsWalk w(p);
+    RowsWalk<> w(p);
     int n = 0, k = 0;                              // units, key tiles so far
     bool ok = true;
     while (ok && w.next()) {

@@ -9,6 +9,7 @@
 // columns beyond a tensor's extent arrive as zeros and strides need only be multiples of 16 bytes.
 #pragma once
 
+#include "bwd_main.cuh"
 #include "tc_shared.cuh"
 #include "train_common.cuh"
 
@@ -101,6 +102,65 @@ __device__ __forceinline__ void load_key_tile(const CUtensorMap* map, uint8_t* d
 #pragma unroll
   for (int cb = 0; cb < DT / 64; ++cb)
     tma_load_4d(dst + cb * kTile * 128, map, cb * 64, hk * mul_h, t * kTile, b * mul_b, bar);
+}
+
+// Products are issued by a warp that stays together, of whose lanes one (`one` != 0) issues: so
+// descriptors and barriers' addresses stay in uniform registers. Issued by a lone thread each step
+// moves its operands there one by one, among the softmax warps that share its scheduler: two
+// products of 128 x 128 x 128 took 1900 to 3100 cycles beside busy warps instead of 1024 to 1530.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+  return one;
+}
+__device__ __forceinline__ uint32_t same(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t one) {
+  asm volatile(
+      "{ .reg .pred p, q; .reg .b64 da, db; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %6, 0; mov.b64 da, {%1, %5}; "
+      "mov.b64 db, {%2, %5}; @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(ptx::kDescHi), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t one) {
+  asm volatile(
+      "{ .reg .pred p, q; .reg .b64 db; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %6, 0; mov.b64 db, {%2, %5}; "
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(ptx::kDescHi), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0; "
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(ptx::smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+
+// The K steps of 16 of a product, n of them. Two K-major operands in shared memory (64 columns a
+// block of 128 rows):
+template <int DT>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t id, int n, uint32_t one) {
+#pragma unroll
+  for (int ks = 0; ks < DT / 16; ++ks) {
+    const uint32_t step = ((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4;
+    if (ks < n) mma_ss(d, a + step, b + step, id, ks > 0, one);
+  }
+}
+// A in TMEM, 16 of K in 8 packed columns, side by side or (SPLIT) in two halves whose bases are 64
+// apart; B MN-major in shared memory:
+template <bool SPLIT>
+__device__ __forceinline__ void issue_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc0, int n,
+                                           uint32_t one) {
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks)
+    if (ks < n) mma_ts(d, a + (SPLIT ? 64 * (ks >> 2) + 8 * (ks & 3) : 8 * ks), b + ks * kMnStep, id, ks > 0 ? 1u : acc0, one);
+}
+// Both operands MN-major in shared memory:
+__device__ __forceinline__ void issue_mn(uint32_t d, uint32_t a, uint32_t b, uint32_t id, int n, uint32_t one) {
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks)
+    if (ks < n) mma_ss(d, a + ks * kMnStep, b + ks * kMnStep, id, ks > 0, one);
 }
 
 // Zeroes rows [from, to) of a tile in shared memory (one warp): keys that a length leaves out may

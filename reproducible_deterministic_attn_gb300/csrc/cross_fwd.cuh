@@ -71,6 +71,8 @@ static_assert(kFwdRegsCtrl + 2 * kFwdRegsSoftmax == 3 * kFwdRegsLaunch,
               "the three warpgroups must share exactly the launch's registers");
 
 // A CTA's units: u, u + grid, ... Every role walks the same ones.
+// ALL: a whole warp walks together.
+template <bool ALL = false>
 struct FwdWalk {
   const FwdArgs* a;
   int u, bh, b, hk, pair, split;
@@ -90,6 +92,7 @@ struct FwdWalk {
     hk = bh - b * p.s.Hk;
     has_b = 2 * pair + 1 < p.s.ntile;
     len = length_of(p.s, b);
+    if (ALL) len = same(len);
     t0 = split * p.kper;
     const int all = (max(len, 0) + kTile - 1) / kTile;
     nt = max(0, min(all, t0 + p.kper) - t0);
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint64_t* bars = (uint64_t*)(sm + L::BAR_OFF);
   uint32_t* tmem_slot = (uint32_t*)(sm + L::BAR_OFF + 8 * L::COUNT);
   volatile int* abort_flag = (volatile int*)(sm + L::BAR_OFF + 8 * L::COUNT + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = same((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const long long tmo = p.timeout_ns;
   const int dsteps = (p.s.D + 15) >> 4;
 
@@ -148,13 +151,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = same(*tmem_slot);
 
   if (warp < 4) {
     ptx::regs_dec<kFwdRegsCtrl>();
     if (warp == 0 && lane == 0) {
       // ===================================== TMA producer =====================================
-      FwdWalk w(p);
+      FwdWalk<> w(p);
       int nqx[2] = {0, 0}, nk = 0, nv = 0;         // row tiles, tiles of K and V loaded so far
       bool ok = true;
       while (ok && w.next()) {
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           ++nqx[x];
         }
         // the next unit's rows wait in L2
-        FwdWalk ahead = w;
+        FwdWalk<> ahead = w;
         if (ahead.next() && ahead.nt > 0)
           for (int x = 0; x < (ahead.has_b ? 2 : 1); ++x)
             prefetch_row_tile<DT>(p.s, &maps.q, ahead.b, ahead.hk, 2 * ahead.pair + x, p.s.q_b, p.s.q_h);
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ptx::mbar_drain(bars + L::K_FULL + k % L::KST, (k / L::KST) & 1, 100000000ll);
       for (int k = max(0, nv - L::VST); k < nv; ++k)
         ptx::mbar_drain(bars + L::V_FULL + k % L::VST, (k / L::VST) & 1, 100000000ll);
-    } else if ((warp == 1 || warp == 3) && lane == 0) {
+    } else if (warp == 1 || warp == 3) {
       // ================================ MMA issuer of tile x ==================================
       // S(t) needs K(t); over P's columns (DT = 128) also P(t-1) V(t-1) done. With P in columns of
       // its own (DT = 64) S(t+1) goes ahead of P(t) V(t).
@@ -203,8 +206,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint32_t dQ = ptx::sdesc_lo(ptx::smem_u32(sm + L::Q_OFF + x * L::TILE), 16);
       const uint32_t sK = ptx::smem_u32(sm + L::K_OFF), sV = ptx::smem_u32(sm + L::V_OFF);
       const uint32_t id_o = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
-      constexpr uint32_t MN_STEP = 2048 >> 4;
-      FwdWalk w(p);
+      FwdWalk<true> w(p);
+      const uint32_t one = elect_one();
       int n = 0, k = 0, pv = 0;                    // this tile's units and products P V, all key tiles so far
       uint32_t clean = 0;                          // parities of the stages' CLEAN barriers
       bool ok = true;
@@ -214,70 +217,62 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (x && !w.has_b) {                       // nothing to issue: the stages are released all the same
           for (int t = 0; ok && t < w.nt; ++t) {
             const int ks = (k + t) % L::KST, vs = (k + t) % L::VST;
-            ok = ptx::mbar_wait(bars + L::K_FULL + ks, ((k + t) / L::KST) & 1, abort_flag, tmo);
-            if (ok) ptx::mbar_arrive(bars + L::K_EMPTY + ks);
-            if (ok) ok = ptx::mbar_wait(bars + L::V_FULL + vs, ((k + t) / L::VST) & 1, abort_flag, tmo);
+            ok = ptx::warp_wait(bars + L::K_FULL + ks, ((k + t) / L::KST) & 1, abort_flag, tmo);
+            if (ok && one) ptx::mbar_arrive(bars + L::K_EMPTY + ks);
+            if (ok) ok = ptx::warp_wait(bars + L::V_FULL + vs, ((k + t) / L::VST) & 1, abort_flag, tmo);
             if (ok && t == w.nt - 1 && last_dirty) {
-              ok = ptx::mbar_wait(bars + L::CLEAN + vs, (clean >> vs) & 1, abort_flag, tmo);
+              ok = ptx::warp_wait(bars + L::CLEAN + vs, (clean >> vs) & 1, abort_flag, tmo);
               clean ^= 1u << vs;
             }
-            if (ok) ptx::mbar_arrive(bars + L::V_EMPTY + vs);
+            if (ok && one) ptx::mbar_arrive(bars + L::V_EMPTY + vs);
           }
           k += w.nt;
           continue;
         }
         auto issue_s = [&](int t) {
           const int s = (k + t) % L::KST;
-          bool good = ptx::mbar_wait(bars + L::K_FULL + s, ((k + t) / L::KST) & 1, abort_flag, tmo);
-          if (good && !L::kSepP && pv > 0) good = ptx::mbar_wait(bars + L::PV_DONE + x, (pv - 1) & 1, abort_flag, tmo);
+          bool good = ptx::warp_wait(bars + L::K_FULL + s, ((k + t) / L::KST) & 1, abort_flag, tmo);
+          if (good && !L::kSepP && pv > 0) good = ptx::warp_wait(bars + L::PV_DONE + x, (pv - 1) & 1, abort_flag, tmo);
           if (!good) return false;
           ptx::tc_fence_after();
           const uint32_t id_s = ptx::idesc_bf16(128, 32 * w.chunks(t), 0, 0);
           const uint32_t dK = ptx::sdesc_lo(sK + s * L::TILE, 16);
-#pragma unroll
-          for (int ks = 0; ks < DT / 16; ++ks) {
-            const uint32_t step = ((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4;
-            if (ks < dsteps) ptx::mma_lo(tmem + L::T_S + 128 * x, dQ + step, dK + step, id_s, ks > 0);
-          }
-          ptx::mma_commit(bars + L::S_FULL + x);
-          ptx::mma_commit(bars + L::K_EMPTY + s);
-          if (t == w.nt - 1) ptx::mma_commit(bars + L::Q_EMPTY + x);
+          issue_scores<DT>(tmem + L::T_S + 128 * x, dQ, dK, id_s, dsteps, one);
+          commit(bars + L::S_FULL + x, one);
+          commit(bars + L::K_EMPTY + s, one);
+          if (t == w.nt - 1) commit(bars + L::Q_EMPTY + x, one);
           return true;
         };
-        ok = ptx::mbar_wait(bars + L::Q_FULL + x, n & 1, abort_flag, tmo) && issue_s(0);
+        ok = ptx::warp_wait(bars + L::Q_FULL + x, n & 1, abort_flag, tmo) && issue_s(0);
         for (int t = 0; ok && t < w.nt; ++t) {
           const int s = (k + t) % L::VST;
-          ok = ptx::mbar_wait(bars + L::P_FULL + x, pv & 1, abort_flag, tmo);
+          ok = ptx::warp_wait(bars + L::P_FULL + x, pv & 1, abort_flag, tmo);
           if (ok && L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1);
-          if (ok) ok = ptx::mbar_wait(bars + L::V_FULL + s, ((k + t) / L::VST) & 1, abort_flag, tmo);
+          if (ok) ok = ptx::warp_wait(bars + L::V_FULL + s, ((k + t) / L::VST) & 1, abort_flag, tmo);
           if (ok && t == w.nt - 1 && last_dirty) {
-            ok = ptx::mbar_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);
+            ok = ptx::warp_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);
             clean ^= 1u << s;
           }
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t dV = ptx::sdesc_lo(sV + s * L::TILE, kTile * 128);
-          const int steps = 2 * w.chunks(t);
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            if (ks < steps)
-              ptx::mma_ts(tmem + L::T_O + DT * x, tmem + L::T_P + L::P_STRIDE * x + 8 * ks, dV + ks * MN_STEP, id_o,
-                          (t > 0 || ks > 0) ? 1u : 0u);
-          ptx::mma_commit(bars + L::PV_DONE + x);
-          ptx::mma_commit(bars + L::V_EMPTY + s);
+          issue_rows<false>(tmem + L::T_O + DT * x, tmem + L::T_P + L::P_STRIDE * x, dV, id_o, t > 0 ? 1u : 0u,
+                            2 * w.chunks(t), one);
+          commit(bars + L::PV_DONE + x, one);
+          commit(bars + L::V_EMPTY + s, one);
           ++pv;
           if (!L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1);
         }
         k += w.nt;
         ++n;
       }
-      ptx::mma_commit(bars + L::DRAIN + x);
+      commit(bars + L::DRAIN + x, one);
       ptx::mbar_drain(bars + L::DRAIN + x, 0, 1000000000ll);
     } else if (warp == 2 && p.s.lens) {
       // ============================ rows of V behind a sequence's end ==========================
       // Every tile is waited for and its stage released here too, so that this warp can be neither
       // ahead of the copies nor behind the products by more than a barrier's phase.
-      FwdWalk w(p);
+      FwdWalk<> w(p);
       int kv = 0;
       bool ok = true;
       while (ok && w.next()) {
@@ -304,7 +299,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t t_s = tmem + lane_addr + L::T_S + 128 * x;
     const uint32_t t_pp = tmem + lane_addr + L::T_P + L::P_STRIDE * x;
     const uint32_t t_o = tmem + lane_addr + L::T_O + DT * x;
-    FwdWalk w(p);
+    FwdWalk<> w(p);
     int steps = 0;                                 // key tiles so far: parity of this tile's barriers
     bool ok = true;
     while (w.next()) {

@@ -11,7 +11,7 @@
 // While one warpgroup turns S into P the products of the other run, and while a unit's rows leave
 // for memory the next unit's tiles load and its first S is computed. The last key tile of a
 // sequence takes only its 32-column chunks with keys (77 keys: 96 columns, not 128).
-// A softmax thread owns a row: it takes the row's scores out of TMEM once, so the maximum and the
+// A softmax thread owns half a row: it takes its scores out of TMEM once, so the maximum and the
 // exponentials need no second read, and moves the exponent's reference m only when the row
 // maximum exceeds it by more than 8 in log2 units (P <= 2^8; O and l share the reference).
 //
@@ -19,10 +19,10 @@
 // tokens against long states) the keys are cut into ranges; a range leaves its rows' normalised O
 // in fp32 and their LSE, which cross_join_kernel combines in order.
 //
-// Warp roles (384 threads): 0 = TMA producer, 1 and 3 = MMA issuers of tiles A and B (one thread that
-// polled both tiles' barriers took 3100 cycles from a P to the next S, of which 1024 are products;
-// 870 TFLOP/s at 8192 x 8192 x 128), 2 = clears V rows that a length leaves out, 4..7 = softmax of tile A, 8..11 = of tile B. Every wait is bounded; a CTA that gives
-// up writes NaN into the LSE of its rows and records DASH_ERR_SYNC_TIMEOUT where asked to.
+// Warp roles (640 threads): 0 = TMA producer, 1 and 3 = MMA issuers of tiles A and B, 2 = clears V
+// rows that a length leaves out, 4..11 = softmax of tile A, 12..19 = of tile B. Every wait is
+// bounded; a CTA that gives up writes NaN into the LSE of its rows and records
+// DASH_ERR_SYNC_TIMEOUT where asked to.
 #pragma once
 
 #include "cross_common.cuh"
@@ -47,9 +47,10 @@ struct FwdArgs {
 template <int DT>
 struct FwdLay {
   static constexpr int TILE = kTile * DT * 2;
-  static constexpr int KST = DT == 64 ? 4 : 2, VST = DT == 64 ? 4 : 3;   // stages of K and V
+  static constexpr int KST = DT == 64 ? 4 : 2, VST = DT == 64 ? 4 : 2;   // stages of K and V
   static constexpr int Q_OFF = 0, K_OFF = 2 * TILE, V_OFF = K_OFF + KST * TILE;
-  static constexpr int BAR_OFF = V_OFF + VST * TILE;
+  static constexpr int EX_OFF = V_OFF + VST * TILE;           // the halves of a row: [tile][half][128]
+  static constexpr int BAR_OFF = EX_OFF + 4 * kTile * 4;
   static constexpr int ALLOC = BAR_OFF + 512 + 1024;          // slack for 1024 alignment
   static_assert(ALLOC <= 232448, "shared memory budget");
   static constexpr int T_S = 0, T_O = 256;
@@ -58,17 +59,17 @@ struct FwdLay {
   static constexpr int P_STRIDE = kSepP ? 64 : 128;
   static_assert(T_O + 2 * DT + (kSepP ? 128 : 0) <= 512, "TMEM columns");
   // barriers
-  static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6, PV_DONE = 8, DRAIN = 10,
-                       K_FULL = 12, V_FULL = K_FULL + KST, K_EMPTY = V_FULL + VST, V_EMPTY = K_EMPTY + KST,
+  static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6, PV_DONE = 8, DRAIN = 10, TURN = 12,
+                       K_FULL = 14, V_FULL = K_FULL + KST, K_EMPTY = V_FULL + VST, V_EMPTY = K_EMPTY + KST,
                        CLEAN = V_EMPTY + VST, COUNT = CLEAN + VST;
   static_assert(8 * COUNT + 8 <= 512, "barrier area");
 };
 
-constexpr int kFwdThreads = 384;
+constexpr int kFwdThreads = 640;
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kFwdRegsLaunch = 168, kFwdRegsCtrl = 88, kFwdRegsSoftmax = 208;
-static_assert(kFwdRegsCtrl + 2 * kFwdRegsSoftmax == 3 * kFwdRegsLaunch,
-              "the three warpgroups must share exactly the launch's registers");
+constexpr int kFwdRegsLaunch = 96, kFwdRegsCtrl = 64, kFwdRegsSoftmax = 104;
+static_assert(kFwdRegsCtrl + 4 * kFwdRegsSoftmax == 5 * kFwdRegsLaunch,
+              "the five warpgroups must share exactly the launch's registers");
 
 // A CTA's units: u, u + grid, ... Every role walks the same ones.
 // ALL: a whole warp walks together.
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       ptx::mbar_init(bars + L::Q_FULL + x, 1);
       ptx::mbar_init(bars + L::Q_EMPTY + x, 1);
       ptx::mbar_init(bars + L::S_FULL + x, 1);
-      ptx::mbar_init(bars + L::P_FULL + x, 4);
+      ptx::mbar_init(bars + L::P_FULL + x, 8);
       ptx::mbar_init(bars + L::PV_DONE + x, 1);
     }
     for (int s = 0; s < L::KST; ++s) {
@@ -144,6 +145,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
     ptx::mbar_init(bars + L::DRAIN, 1);
     ptx::mbar_init(bars + L::DRAIN + 1, 1);
+    ptx::mbar_init(bars + L::TURN, 1);
+    ptx::mbar_init(bars + L::TURN + 1, 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
@@ -202,13 +205,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // ================================ MMA issuer of tile x ==================================
       // S(t) needs K(t); over P's columns (DT = 128) also P(t-1) V(t-1) done. With P in columns of
       // its own (DT = 64) S(t+1) goes ahead of P(t) V(t).
+      // Over several key tiles the two issuers take turns with P(t) V(t) and S(t+1), so that one
+      // tile's products run while the other's scores become P. Left alone they fall into step, both
+      // in the softmax and then both in line for the pipe (8192 x 8192 x 128, 32 heads: 1237 us, with
+      // turns 1092). With one or two key tiles turns only cost (77 keys: 33 us, with turns 38).
       const int x = warp >> 1;
       const uint32_t dQ = ptx::sdesc_lo(ptx::smem_u32(sm + L::Q_OFF + x * L::TILE), 16);
       const uint32_t sK = ptx::smem_u32(sm + L::K_OFF), sV = ptx::smem_u32(sm + L::V_OFF);
       const uint32_t id_o = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
       FwdWalk<true> w(p);
       const uint32_t one = elect_one();
-      int n = 0, k = 0, pv = 0;                    // this tile's units and products P V, all key tiles so far
+      int n = 0, k = 0, pv = 0, turns = 0;         // this tile's units, products P V and turns, all key tiles so far
       uint32_t clean = 0;                          // parities of the stages' CLEAN barriers
       bool ok = true;
       while (ok && w.next()) {
@@ -243,10 +250,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (t == w.nt - 1) commit(bars + L::Q_EMPTY + x, one);
           return true;
         };
+        const bool take_turns = w.has_b && w.nt > 2;
         ok = ptx::warp_wait(bars + L::Q_FULL + x, n & 1, abort_flag, tmo) && issue_s(0);
         for (int t = 0; ok && t < w.nt; ++t) {
           const int s = (k + t) % L::VST;
           ok = ptx::warp_wait(bars + L::P_FULL + x, pv & 1, abort_flag, tmo);
+          // A's first turn ever is its own; A's turn n waits for B's turn n - 1, B's for A's turn n
+          if (ok && take_turns && (x || turns > 0))
+            ok = ptx::warp_wait(bars + L::TURN + x, (x ? turns : turns - 1) & 1, abort_flag, tmo);
           if (ok && L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1);
           if (ok) ok = ptx::warp_wait(bars + L::V_FULL + s, ((k + t) / L::VST) & 1, abort_flag, tmo);
           if (ok && t == w.nt - 1 && last_dirty) {
@@ -262,6 +273,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           commit(bars + L::V_EMPTY + s, one);
           ++pv;
           if (!L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1);
+          if (take_turns) {
+            ++turns;
+            if (one) ptx::mbar_arrive(bars + L::TURN + 1 - x);
+          }
         }
         k += w.nt;
         ++n;
@@ -293,69 +308,87 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   } else {
     ptx::regs_inc<kFwdRegsSoftmax>();
     // ======================================= softmax ========================================
-    const int x = (warp - 4) >> 2, quarter = warp & 3;
+    // Two warps a quarter of a tile: a thread owns a row's 64 keys of its half, and of O its half of
+    // the columns. The halves share the row's maximum and sum through shared memory.
+    const int x = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quarter = warp & 3;
     const int r = quarter * 32 + lane;             // row within the tile = TMEM lane
     const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
-    const uint32_t t_s = tmem + lane_addr + L::T_S + 128 * x;
-    const uint32_t t_pp = tmem + lane_addr + L::T_P + L::P_STRIDE * x;
+    const uint32_t t_s = tmem + lane_addr + L::T_S + 128 * x + 64 * half;
+    const uint32_t t_pp = tmem + lane_addr + L::T_P + L::P_STRIDE * x + 32 * half;
     const uint32_t t_o = tmem + lane_addr + L::T_O + DT * x;
+    float* mine = (float*)(sm + L::EX_OFF) + (x * 2 + half) * kTile + r;
+    const float* other = (const float*)(sm + L::EX_OFF) + (x * 2 + 1 - half) * kTile + r;
+    const int pair_bar = 1 + x * 4 + quarter;      // the two warps' named barrier
     FwdWalk<> w(p);
     int steps = 0;                                 // key tiles so far: parity of this tile's barriers
     bool ok = true;
     while (w.next()) {
       if (x && !w.has_b) continue;
-      float m = -INFINITY, l = 0.f;
-      for (int t = 0; ok && t < w.nt; ++t) {
-        ok = ptx::warp_wait(bars + L::S_FULL + x, steps & 1, abort_flag, tmo);
-        if (!ok) break;
+      float m = -INFINITY, l = 0.f;                // of the row; of this half
+      // A warp whose wait ran out goes on without work, as its partner must find it at every meeting.
+      for (int t = 0; t < w.nt; ++t, ++steps) {
+        if (ok) ok = ptx::warp_wait(bars + L::S_FULL + x, steps & 1, abort_flag, tmo);
         ptx::tc_fence_after();
-        const int keys = w.keys(t), chunks = (keys + 31) >> 5;
-        uint32_t sc[4][32];
+        const int keys = w.keys(t) - 64 * half;    // of this half
+        uint32_t sc[2][32];
+        float mx = -INFINITY;
+        if (ok) {
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < chunks) ptx::tmem_ld32_issue(t_s + 32 * c, sc[c]);
+          for (int c = 0; c < 2; ++c)
+            if (32 * c < keys) ptx::tmem_ld32_issue(t_s + 32 * c, sc[c]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < chunks) ptx::tmem_ld32_wait(sc[c]);
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int c = 0; c < 2; ++c)
+            if (32 * c < keys) ptx::tmem_ld32_wait(sc[c]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < chunks) {
-            if (32 * c + 32 > keys) {              // the sequence ends in this chunk
+          for (int c = 0; c < 2; ++c) {
+            if (32 * c < keys) {
+              if (32 * c + 32 > keys) {            // the sequence ends in this chunk
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (32 * c + i >= keys) sc[c][i] = 0xff800000u;
+                for (int i = 0; i < 32; ++i)
+                  if (32 * c + i >= keys) sc[c][i] = 0xff800000u;
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(sc[c][i]), __uint_as_float(sc[c][i + 1]));
             }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(sc[c][i]), __uint_as_float(sc[c][i + 1]));
           }
+          mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
         }
-        const float m_row = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+        // The place is the partner's to read until its P is stored, which the next S waits for. The
+        // meeting also says that both halves' scores have been read: P lies over half 0's (DT = 128).
+        *mine = mx;
+        ptx::tc_fence_before();
+        ptx::named_bar(pair_bar, 64);
+        ptx::tc_fence_after();
+        if (!ok) continue;
+        const float m_row = fmaxf(mx, *other) * p.scale_log2;
         const bool moved = m_row > m + kRescaleLog2;
         const float m_new = moved ? m_row : m;
         // P's columns, and O where it is rescaled, are the last product's until that is done (DT = 128: it
         // was, before this S)
         if (L::kSepP && t > 0) {
           ok = ptx::warp_wait(bars + L::PV_DONE + x, (steps - 1) & 1, abort_flag, tmo);
-          if (!ok) break;
+          if (!ok) continue;
           ptx::tc_fence_after();
         }
         const uint64_t scale2 = two(p.scale_log2, p.scale_log2), off2 = two(-m_new, -m_new);
         uint64_t lt[2] = {0ull, 0ull};             // four partial sums
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < chunks) {
-            uint32_t u[16];
+        for (int c = 0; c < 2; ++c) {
+          if (32 * c < keys) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float e0, e1;
-              exp2_two(__uint_as_float(sc[c][2 * k]), __uint_as_float(sc[c][2 * k + 1]), scale2, off2, e0, e1);
-              lt[k & 1] = add2(lt[k & 1], two(e0, e1));
-              u[k] = ptx::pack_bf16(e0, e1);
+            for (int k = 0; k < 16; k += 8) {
+              uint32_t u[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float e0, e1;
+                exp2_two(__uint_as_float(sc[c][2 * (k + i)]), __uint_as_float(sc[c][2 * (k + i) + 1]), scale2, off2, e0, e1);
+                lt[i & 1] = add2(lt[i & 1], two(e0, e1));
+                u[i] = ptx::pack_bf16(e0, e1);
+              }
+              ptx::tmem_st8(t_pp + 16 * c + k, u);
             }
-            ptx::tmem_st8(t_pp + 16 * c, u);
-            ptx::tmem_st8(t_pp + 16 * c + 8, u + 8);
           }
         }
         float lt0, lt1;
@@ -365,7 +398,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         m = m_new;
         if (t > 0 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int c0 = 0; c0 < DT; c0 += 32) {
+          for (int i = 0; i < DT / 2; i += 32) {
+            const int c0 = half * (DT / 2) + i;
             if (c0 < p.s.D) {
               uint32_t a[32];
               ptx::tmem_ld32_issue(t_o + c0, a);
@@ -380,10 +414,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bars + L::P_FULL + x);
-        ++steps;
       }
-      if (ok && w.nt > 0) ok = ptx::warp_wait(bars + L::PV_DONE + x, (steps - 1) & 1, abort_flag, tmo);
-      if (ok) ptx::tc_fence_after();
+      if (w.nt > 0) {
+        if (ok) ok = ptx::warp_wait(bars + L::PV_DONE + x, (steps - 1) & 1, abort_flag, tmo);
+        ptx::tc_fence_after();
+        // the row's sum; the maxima in these places have been read, as above
+        *mine = l;
+        ptx::named_bar(pair_bar, 64);
+        l += *other;
+        ptx::named_bar(pair_bar, 64);
+      }
       int token, head;
       const int tile = 2 * w.pair + x;
       const bool live = row_of(p.s, tile, r, token, head);
@@ -391,45 +431,39 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const bool bad = !ok || w.len < 0;
       const float inv = bad ? NAN : none ? 0.f : 1.f / l;
       const float l2 = bad ? NAN : none ? -INFINITY : m + __log2f(l);
-      if (p.splits > 1) {
-        const size_t row = (((size_t)w.split * p.s.B * p.s.Hk + w.bh) * p.s.ntile + tile) * kTile + r;
-        if (live) p.part_l[row] = l2;
-        if (!none && ok) {
+      const size_t row = (((size_t)w.split * p.s.B * p.s.Hk + w.bh) * p.s.ntile + tile) * kTile + r;
+      const int h = w.hk * p.s.g + head;
+      if (live && half == 0) {
+        if (p.splits > 1) p.part_l[row] = l2;
+        else p.lse[((size_t)w.b * p.s.Hq + h) * p.s.Sq + token] = l2 * kLn2;
+      }
+      __nv_bfloat16* dst = p.o + (((size_t)w.b * p.s.Sq + token) * p.s.Hq + h) * p.s.D;
 #pragma unroll
-          for (int c0 = 0; c0 < DT; c0 += 32) {
-            if (c0 < p.s.D) {
-              float v[32];
-              ptx::tmem_ld32(t_o + c0, v);
-              if (live) {
-                float4* d4 = (float4*)(p.part_o + row * DT + c0);
+      for (int i = 0; i < DT / 2; i += 32) {
+        const int c0 = half * (DT / 2) + i;
+        if (c0 < p.s.D) {
+          float v[32];
+          if (none || bad) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  d4[k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
-              }
-            }
+            for (int c = 0; c < 32; ++c) v[c] = 1.f;
+          } else {
+            ptx::tmem_ld32(t_o + c0, v);
           }
-        }
-      } else {
-        const int h = w.hk * p.s.g + head;
-        if (live) p.lse[((size_t)w.b * p.s.Hq + h) * p.s.Sq + token] = l2 * kLn2;
-        __nv_bfloat16* dst = p.o + (((size_t)w.b * p.s.Sq + token) * p.s.Hq + h) * p.s.D;
+          if (live && p.splits > 1) {
+            if (!none && ok) {
+              float4* d4 = (float4*)(p.part_o + row * DT + c0);
 #pragma unroll
-        for (int c0 = 0; c0 < DT; c0 += 32) {
-          if (c0 < p.s.D) {
-            float v[32];
-            if (none || bad) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) v[c] = 1.f;
-            } else {
-              ptx::tmem_ld32(t_o + c0, v);
+              for (int k = 0; k < 8; ++k)
+                d4[k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
             }
-            if (live) store_bf16_32(dst + c0, v, inv, p.s.D - c0);
+          } else if (live) {
+            store_bf16_32(dst + c0, v, inv, p.s.D - c0);
           }
         }
       }
       // O has been read: the next unit's P V may replace it, which waits for this warp's P
       ptx::tc_fence_before();
-      if (w.len < 0 && w.pair == 0 && x == 0 && r == 0 && p.status) atomicCAS(p.status, 0, kStatusBounds);
+      if (w.len < 0 && w.pair == 0 && x == 0 && half == 0 && r == 0 && p.status) atomicCAS(p.status, 0, kStatusBounds);
     }
   }
 

@@ -47,8 +47,8 @@ struct BwdArgs {
   const float* lse;
   __nv_bfloat16 *dq, *dk, *dv;
   long long dq_b, dq_s, dq_h, dk_b, dk_s, dk_h, dv_b, dv_s, dv_h;
-  float* dq_part;            // [key segment][group][tile][128][DT]
-  float* dkv_part;           // [row segment][group][key tile][dK, dV][128][DT]
+  float* dq_part;            // [key segment][group][tile][DT / 8][128][8]
+  float* dkv_part;           // [row segment][group][key tile][dK, dV][DT / 8][128][8]
   int qsegs, qper;           // row segments of cross_keys_kernel, row tiles of one
   int ksegs, kper;           // key segments of cross_rows_kernel, key tiles of one
   int units;                 // of the kernel that is being launched
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ptx::tc_fence_after();
         const int key = w.kt * kTile + row;
-        float* part = p.dkv_part + ((((size_t)w.qseg * p.s.B * p.s.Hk + w.bh) * p.s.nk + w.kt) * 2 * kTile + row) * DT;
+        float* part = p.dkv_part + (((size_t)w.qseg * p.s.B * p.s.Hk + w.bh) * p.s.nk + w.kt) * 2 * kTile * DT;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {  // dK, then dV
           const uint32_t from = tmem + lane_addr + (which ? L::T_DV : L::T_DK);
@@ -569,13 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c0 < p.s.D) {
               float a[32];
               ptx::tmem_ld32(from + c0, a);
-              if (p.qsegs > 1) {
-                float4* d4 = (float4*)(part + which * kTile * DT + c0);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) d4[k] = make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
-              } else if (key < p.s.Sk) {
-                store_bf16_32(dst + c0, a, which ? 1.f : p.scale, p.s.D - c0);
-              }
+              if (p.qsegs > 1) store_part_32(part + which * kTile * DT, row, c0, a, 1.f);
+              else store_rows_bf16(lane, a, which ? 1.f : p.scale, key < p.s.Sk ? dst + c0 : nullptr, p.s.D - c0);
             }
           }
         }
@@ -611,7 +606,7 @@ __global__ void __launch_bounds__(256) cross_join_keys_kernel(const __grid_const
   const int h = (int)(row % p.s.Hk), key = (int)(row / p.s.Hk % p.s.Sk), b = (int)(row / p.s.Hk / p.s.Sk);
   const int kt = key / kTile;
   if (kt * kTile >= length_of(p.s, b)) return;
-  const float* src = p.dkv_part + ((((size_t)b * p.s.Hk + h) * p.s.nk + kt) * 2 * kTile + key % kTile) * DT + c;
+  const float* src = p.dkv_part + ((((size_t)b * p.s.Hk + h) * p.s.nk + kt) * 2 * kTile) * DT + part_at(key % kTile, c);
   const size_t step = (size_t)p.s.B * p.s.Hk * p.s.nk * 2 * kTile * DT;
   float k[8] = {}, v[8] = {};
 #pragma unroll 4

@@ -321,20 +321,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       int token, head;
       const bool live = row_of(p.s, w.tile, r, token, head);
       __nv_bfloat16* dst = p.dq + w.b * p.dq_b + token * p.dq_s + (w.hk * p.s.g + head) * p.dq_h;
-      float* part = p.dq_part + ((((size_t)w.kseg * p.s.B * p.s.Hk + w.bh) * p.s.ntile + w.tile) * kTile + r) * DT;
+      float* part = p.dq_part + ((((size_t)w.kseg * p.s.B * p.s.Hk + w.bh) * p.s.ntile + w.tile) * kTile) * DT;
 #pragma unroll
       for (int i = 0; i < DT / 2; i += 32) {
         const int c0 = half * (DT / 2) + i;
         if (c0 < p.s.D) {
           float v[32];
           ptx::tmem_ld32(tmem + lane_addr + L::T_DQ + c0, v);
-          if (live && p.ksegs == 1) {
-            store_bf16_32(dst + c0, v, p.scale, p.s.D - c0);
-          } else if (live) {
-            float4* d4 = (float4*)(part + c0);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) d4[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-          }
+          if (p.ksegs == 1) store_rows_bf16(lane, v, p.scale, live ? dst + c0 : nullptr, p.s.D - c0);
+          else if (live) store_part_32(part, r, c0, v, 1.f);
         }
       }
       ptx::tc_fence_before();
@@ -372,7 +367,7 @@ __global__ void __launch_bounds__(256) cross_join_rows_kernel(const __grid_const
   const int len = length_of(p.s, b);
   if (len <= 0) return;                            // written by cross_pre_kernel
   const int n = ((len + kTile - 1) / kTile + p.kper - 1) / p.kper;
-  const float* src = p.dq_part + (size_t)row * DT + c;
+  const float* src = p.dq_part + (size_t)(row - r) * DT + part_at(r, c);
   float t[8] = {};
 #pragma unroll 4
   for (int s = 0; s < n; ++s) {

@@ -212,29 +212,47 @@ __device__ __forceinline__ void exp2_two(float x, float y, uint64_t scale, uint6
   ey = ptx::ex2(v);
 }
 
-// 32 bytes of a row in one store where its address allows it: a whole sector.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+// 32 columns of a warp's 32 rows, a row a thread (times f, n of the columns valid, a multiple of 8;
+// dst null: no such row), to global memory as bf16. Four lanes swap 16-byte pieces of their rows, so
+// that they store 64 bytes of a row side by side: 32 bytes of 32 rows in one store took a cycle for
+// each row's line, 5000 cycles for a pair of tiles of 128 columns.
+__device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, bool high, int lanes) {
+  uint4 x = high ? a : b;
+  x.x = __shfl_xor_sync(0xffffffffu, x.x, lanes);
+  x.y = __shfl_xor_sync(0xffffffffu, x.y, lanes);
+  x.z = __shfl_xor_sync(0xffffffffu, x.z, lanes);
+  x.w = __shfl_xor_sync(0xffffffffu, x.w, lanes);
+  if (high) a = x;
+  else b = x;
+}
+__device__ __forceinline__ void store_rows_bf16(int lane, const float (&v)[32], float f, __nv_bfloat16* dst, int n) {
+  uint4 c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = make_uint4(ptx::pack_bf16(v[8 * i] * f, v[8 * i + 1] * f), ptx::pack_bf16(v[8 * i + 2] * f, v[8 * i + 3] * f),
+                      ptx::pack_bf16(v[8 * i + 4] * f, v[8 * i + 5] * f), ptx::pack_bf16(v[8 * i + 6] * f, v[8 * i + 7] * f));
+  swap_pieces(c[0], c[1], lane & 1, 1);
+  swap_pieces(c[2], c[3], lane & 1, 1);
+  swap_pieces(c[0], c[2], lane & 2, 2);
+  swap_pieces(c[1], c[3], lane & 2, 2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {                    // piece `lane & 3` of row i of the four
+    __nv_bfloat16* to = (__nv_bfloat16*)__shfl_sync(0xffffffffu, (unsigned long long)dst, (lane & ~3) + i);
+    if (to && 8 * (lane & 3) < n) *reinterpret_cast<uint4*>(to + 8 * (lane & 3)) = c[i];
   }
 }
 
-// 32 values times f as bf16 to columns [0, n) of dst, n a multiple of 8 (n <= 0: none).
-__device__ __forceinline__ void store_bf16_32(__nv_bfloat16* dst, const float (&v)[32], float f, int n) {
-  const bool wide = ((uintptr_t)dst & 31) == 0;
+// fp32 partials of a tile lie 8 columns of every row side by side, [DT / 8][128][8], so that a warp's
+// stores are whole lines and a row's reads whole sectors: column c (a multiple of 8) of row r is at
+__device__ __forceinline__ size_t part_at(int r, int c) { return (size_t)(c * kTile + r * 8); }
+// 32 columns from c0 (times f) of row r.
+__device__ __forceinline__ void store_part_32(float* tile, int r, int c0, const float (&v)[32], float f) {
 #pragma unroll
-  for (int c = 0; c < 32; c += 16) {
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16(v[c + 2 * i] * f, v[c + 2 * i + 1] * f);
-    if (c + 16 <= n) store32(dst + c, w, wide);
-    else if (c < n) *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  for (int c = 0; c < 32; c += 8)
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(tile + part_at(r, c0 + c)),
+                 "f"(v[c] * f), "f"(v[c + 1] * f), "f"(v[c + 2] * f), "f"(v[c + 3] * f), "f"(v[c + 4] * f),
+                 "f"(v[c + 5] * f), "f"(v[c + 6] * f), "f"(v[c + 7] * f)
+                 : "memory");
 }
 
 }  // namespace cross

@@ -34,7 +34,7 @@ struct FwdArgs {
   Shape s;
   __nv_bfloat16* o;          // [B, Sq, Hq, D]
   float* lse;                // [B, Hq, Sq]
-  float* part_o;             // splits > 1: [split][group][tile][128][DT]
+  float* part_o;             // splits > 1: [split][group][tile][DT / 8][128][8]
   float* part_l;             //             [split][group][tile][128] LSE in log2 units
   int pairs, splits, kper;   // pairs of row tiles a group; key ranges, key tiles a range
   int units;
@@ -47,11 +47,11 @@ struct FwdArgs {
 template <int DT>
 struct FwdLay {
   static constexpr int TILE = kTile * DT * 2;
-  static constexpr int KST = DT == 64 ? 4 : 2, VST = DT == 64 ? 4 : 2;   // stages of K and V
+  static constexpr int KST = DT == 64 ? 4 : 2, VST = DT == 64 ? 4 : 3;   // stages of K and V
   static constexpr int Q_OFF = 0, K_OFF = 2 * TILE, V_OFF = K_OFF + KST * TILE;
   static constexpr int EX_OFF = V_OFF + VST * TILE;           // the halves of a row: [tile][half][128]
   static constexpr int BAR_OFF = EX_OFF + 4 * kTile * 4;
-  static constexpr int ALLOC = BAR_OFF + 512 + 1024;          // slack for 1024 alignment
+  static constexpr int ALLOC = BAR_OFF + 512;                 // the base is 1024-aligned (checked)
   static_assert(ALLOC <= 232448, "shared memory budget");
   static constexpr int T_S = 0, T_O = 256;
   static constexpr bool kSepP = DT == 64;                     // P in columns of its own
@@ -111,8 +111,8 @@ template <int DT>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     cross_fwd_kernel(const __grid_constant__ FwdArgs p, const __grid_constant__ Maps maps) {
   using L = FwdLay<DT>;
-  extern __shared__ uint8_t smem_cross[];
-  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_cross + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem_cross[];
+  uint8_t* sm = smem_cross;
   uint64_t* bars = (uint64_t*)(sm + L::BAR_OFF);
   uint32_t* tmem_slot = (uint32_t*)(sm + L::BAR_OFF + 8 * L::COUNT);
   volatile int* abort_flag = (volatile int*)(sm + L::BAR_OFF + 8 * L::COUNT + 4);
@@ -121,6 +121,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int dsteps = (p.s.D + 15) >> 4;
 
   if (p.splits > 1) train::grid_next();
+  // The layout fills most of the opt-in maximum, so there is no room to realign the base.
+  if (ptx::smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, kStatusSmemLayout);
+    return;
+  }
   if (threadIdx.x == 0) {
     if (p.s.nk > 0) {
       ptx::prefetch_map(&maps.q);
@@ -449,16 +454,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           } else {
             ptx::tmem_ld32(t_o + c0, v);
           }
-          if (live && p.splits > 1) {
-            if (!none && ok) {
-              float4* d4 = (float4*)(p.part_o + row * DT + c0);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                d4[k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
-            }
-          } else if (live) {
-            store_bf16_32(dst + c0, v, inv, p.s.D - c0);
-          }
+          if (p.splits == 1) store_rows_bf16(lane, v, inv, live ? dst + c0 : nullptr, p.s.D - c0);
+          else if (live && !none && ok) store_part_32(p.part_o + (row - r) * DT, r, c0, v, inv);
         }
       }
       // O has been read: the next unit's P V may replace it, which waits for this warp's P
@@ -480,7 +477,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // warp a row; ranges without keys have l_s = -inf and nothing in part_o.
 template <int DT>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ FwdArgs p) {
-  constexpr int PER = DT / 32;
+  constexpr int PER = DT / 32;                     // columns a lane
   const int lane = threadIdx.x & 31;
   const long long rows = (long long)p.s.B * p.s.Hk * p.s.ntile * kTile;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -508,7 +505,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
     if (!(l2 > -INFINITY)) continue;
     const float f = ptx::ex2(l2 - mx);
     total += f;
-    const float* src = p.part_o + ((size_t)s * rows + row) * DT + lane * PER;
+    const float* src = p.part_o + ((size_t)s * rows + row - r) * DT + part_at(r, lane * PER & ~7) + (lane * PER & 7);
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = fmaf(f, src[i], acc[i]);
   }

@@ -2,6 +2,7 @@
 // maps and launches. The kernels are in cross_fwd.cuh, cross_bwd.cuh
 // and cross_bwd_rows.cuh.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "cross_bwd_rows.cuh"
@@ -111,15 +112,12 @@ dash_status_t check(const void* q, const void* k, const void* v, const void* len
   if (!is_aligned(q, 16) || !is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(o, 16) || !is_aligned(lse, 4) ||
       !is_aligned(lens, id_bits / 8))
     return DASH_ERR_INVALID_ARG;
-  if (!dash::tensor_map_encoder()) {
-    dash::set_last_error("cuTensorMapEncodeTiled is not available from the driver");
-    return DASH_ERR_CUDA;
-  }
   return DASH_OK;
 }
 
 dash_status_t bad_map() {
-  dash::set_last_error("cuTensorMapEncodeTiled rejected a tensor");
+  dash::set_last_error(dash::tensor_map_encoder() ? "cuTensorMapEncodeTiled rejected a tensor"
+                                                  : "cuTensorMapEncodeTiled is not available from the driver");
   return DASH_ERR_CUDA;
 }
 
@@ -132,7 +130,12 @@ dash_status_t sm_count(int* sms) {
 
 // Shared memory of a kernel that moves registers between its warpgroups: their shares add up to
 // what it was launched with only if it was built with exactly that count.
-dash_status_t prepare(const void* kernel, int smem, int regs) {
+// (`known`: a bit for each device that has been asked.)
+dash_status_t prepare(const void* kernel, int smem, int regs, std::atomic<uint64_t>* known) {
+  int dev = 0;
+  DASH_TRY(cudaGetDevice(&dev));
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (known->load(std::memory_order_acquire) & bit) return DASH_OK;
   cudaFuncAttributes fa;
   DASH_TRY(cudaFuncGetAttributes(&fa, kernel));
   if (fa.numRegs != regs) {
@@ -140,6 +143,7 @@ dash_status_t prepare(const void* kernel, int smem, int regs) {
     return DASH_ERR_CUDA;
   }
   DASH_TRY(dash::allow_shared(kernel, smem));
+  known->fetch_or(bit, std::memory_order_release);
   return DASH_OK;
 }
 
@@ -147,6 +151,7 @@ dash_status_t prepare(const void* kernel, int smem, int regs) {
 bool make_maps(Maps* m, const Shape& s, const void* q, const void* k, const void* v, const long long* qs,
                const long long* ks, const long long* vs) {
   const int bh = s.packed ? s.g : 1, bt = s.packed ? s.tpt : kTile;
+  if (!dash::tensor_map_encoder()) return false;
   if (!map_heads(&m->q, q, s.B, s.Sq, s.Hq, s.D, qs, bh, bt)) return false;
   if (s.Sk == 0) return true;
   return map_heads(&m->k, k, s.B, s.Sk, s.Hk, s.D, ks, 1, kTile) &&
@@ -164,7 +169,8 @@ void set_places(Shape* s, const long long* qs, const long long* ks, const long l
 
 template <int DT>
 dash_status_t launch_fwd(FwdArgs a, const Maps& maps, cudaStream_t stream) {
-  const dash_status_t st = prepare((const void*)cross_fwd_kernel<DT>, FwdLay<DT>::ALLOC, kFwdRegsLaunch);
+  static std::atomic<uint64_t> known{0};
+  const dash_status_t st = prepare((const void*)cross_fwd_kernel<DT>, FwdLay<DT>::ALLOC, kFwdRegsLaunch, &known);
   if (st != DASH_OK) return st;
   int sms = 0;
   if (const dash_status_t e = sm_count(&sms)) return e;
@@ -238,7 +244,8 @@ BwdPlan bwd_plan(const Shape& s, bool ragged) {
 template <int DT, bool DQ>
 dash_status_t launch_keys(BwdArgs a, const Maps& maps, int sms, cudaStream_t stream) {
   using L = KeysLay<DT, DQ>;
-  const dash_status_t st = prepare((const void*)cross_keys_kernel<DT, DQ>, L::ALLOC, L::REGS_LAUNCH);
+  static std::atomic<uint64_t> known{0};
+  const dash_status_t st = prepare((const void*)cross_keys_kernel<DT, DQ>, L::ALLOC, L::REGS_LAUNCH, &known);
   if (st != DASH_OK) return st;
   a.units = (int)((long long)a.s.B * a.s.Hk * a.s.nk * a.qsegs);
   DASH_TRY(dash::launch_after(cross_keys_kernel<DT, DQ>, dim3(std::min(a.units, sms)), kThreads, L::ALLOC, stream, a, maps));
@@ -251,11 +258,15 @@ dash_status_t launch_bwd(BwdArgs a, bool one, const Maps& maps, cudaStream_t str
   if (const dash_status_t e = sm_count(&sms)) return e;
   const long long rows = (long long)a.s.B * a.s.Hk * a.s.ntile * kTile;
   const bool work = a.s.ntile > 0 && a.s.nk > 0;
-  const unsigned row_blocks = (unsigned)std::max(1ll, ceil_div<long long>(rows, 16 * kPreRows));
-  // key tiles that no unit visits exist only behind lengths, or where there are no rows
+  const unsigned row_blocks =
+      (unsigned)std::max(1ll, ceil_div<long long>((long long)a.s.B * a.s.Sq * a.s.Hq, 16 * kPreRows));
+  // places of row tiles without a row: behind the last token, and where heads fill no tile
+  const bool padded = a.s.Sq % a.s.tpt || (a.s.packed && a.s.g * a.s.tpt < kTile);
+  const unsigned pads = padded ? (unsigned)ceil_div<long long>(rows, 256) : 0;
+  // key tiles that no unit visits: behind lengths, or all where there are no rows
   const unsigned key_blocks =
       a.s.lens || !work ? (unsigned)ceil_div<long long>((long long)a.s.B * a.s.Sk * a.s.Hk, 16) : 0;
-  cross_pre_kernel<<<row_blocks + key_blocks, 256, 0, stream>>>(a, row_blocks);
+  cross_pre_kernel<<<row_blocks + pads + key_blocks, 256, 0, stream>>>(a, row_blocks, pads);
   DASH_TRY(cudaGetLastError());
   if (!work) return DASH_OK;
   if (const dash_status_t e = one ? launch_keys<DT, true>(a, maps, sms, stream)
@@ -267,7 +278,8 @@ dash_status_t launch_bwd(BwdArgs a, bool one, const Maps& maps, cudaStream_t str
     DASH_TRY(dash::launch_after(cross_join_keys_kernel<DT>, dim3(blocks), 256, 0, stream, a));
   }
   if (!one) {
-    const dash_status_t st = prepare((const void*)cross_rows_kernel<DT>, RowsLay<DT>::ALLOC, kRowsRegsLaunch);
+    static std::atomic<uint64_t> known{0};
+    const dash_status_t st = prepare((const void*)cross_rows_kernel<DT>, RowsLay<DT>::ALLOC, kRowsRegsLaunch, &known);
     if (st != DASH_OK) return st;
     a.units = (int)((long long)a.s.B * a.s.Hk * a.s.ntile * a.ksegs);
     DASH_TRY(dash::launch_after(cross_rows_kernel<DT>, dim3(std::min(a.units, sms)), kRowsThreads, RowsLay<DT>::ALLOC,

@@ -95,9 +95,9 @@ static_assert(8 * C_COUNT + 8 <= 256, "barrier area");
 template <bool ALL = false>
 struct KeysWalk {
   const BwdArgs& p;
-  int u, bh, b, hk, qseg, kt, len;
+  int b, u, bh, hk, qseg, kt, len;
   int q0, nqt, j;            // the segment's first row tile, their number, the one at hand
-  __device__ __forceinline__ KeysWalk(const BwdArgs& a) : p(a), u((int)blockIdx.x - (int)gridDim.x), nqt(0), j(0) {}
+  __device__ __forceinline__ KeysWalk(const BwdArgs& a) : p(a), b(-1), u((int)blockIdx.x - (int)gridDim.x), nqt(0), j(0) {}
   __device__ __forceinline__ bool next() {
     if (++j < nqt) return true;
     j = 0;
@@ -108,10 +108,13 @@ struct KeysWalk {
       const int r = u / p.s.nk;
       qseg = r % p.qsegs;
       bh = r / p.qsegs;
-      b = bh / p.s.Hk;
-      hk = bh - b * p.s.Hk;
-      len = length_of(p.s, b);
-      if (ALL) len = same(len);
+      const int batch = bh / p.s.Hk;
+      hk = bh - batch * p.s.Hk;
+      if (batch != b) {                            // else its length is known
+        b = batch;
+        len = length_of(p.s, b);
+        if (ALL) len = same(len);
+      }
       q0 = qseg * p.qper;
       nqt = min(p.qper, p.s.ntile - q0);
     } while (kt * kTile >= len);
@@ -123,13 +126,15 @@ struct KeysWalk {
   __device__ __forceinline__ int tile() const { return q0 + j; }
 };
 
-// -Delta = -rowsum(dO * O) and -LSE log2e per row, in row tiles; 16 lanes a row, kPreRows rows one
-// after the other. Rows of batches without keys get their dq here: 0, or NaN for a length out of
-// range. The first block clears the workspace's header and looks for such lengths. The blocks from
-// row_blocks on write dk and dv of the key tiles that no unit visits.
-constexpr int kPreRows = 4;
-static_assert(kTile % (16 * kPreRows) == 0, "whole blocks a row tile");
-__global__ void __launch_bounds__(256, 4) cross_pre_kernel(const __grid_constant__ BwdArgs p, unsigned row_blocks) {
+// -Delta = -rowsum(dO * O) and -LSE log2e per row; 16 lanes a row, kPreRows rows one after the
+// other, in the order in which they lie in memory. Few rows a thread and many threads, as a block
+// waits for its loads only once (4 rows and half the threads: 36 us for 134 MB, now 28). Rows of
+// batches without keys get their dq here: 0, or NaN for a length out of range. The first block
+// clears the workspace's header and looks for such lengths. The next `pads` blocks write the row
+// tiles' places that have no row, those behind them dk and dv of the key tiles that no unit visits.
+constexpr int kPreRows = 2;
+__global__ void __launch_bounds__(256, 8) cross_pre_kernel(const __grid_constant__ BwdArgs p, unsigned row_blocks,
+                                                           unsigned pads) {
   train::grid_next();
   if (blockIdx.x == 0) {
     if (threadIdx.x < kWsHeaderBytes / 4) p.header[threadIdx.x] = 0;
@@ -140,8 +145,8 @@ __global__ void __launch_bounds__(256, 4) cross_pre_kernel(const __grid_constant
           train::report_index(p.header, CHK_LENGTH, b, train::load_index(p.s.lens, b, p.s.id_bits), p.s.Sk);
   }
   const int l = threadIdx.x & 15;
-  if (blockIdx.x >= row_blocks) {
-    const long long row = (long long)(blockIdx.x - row_blocks) * 16 + (threadIdx.x >> 4);   // (batch, key, head)
+  if (blockIdx.x >= row_blocks + pads) {
+    const long long row = (long long)(blockIdx.x - row_blocks - pads) * 16 + (threadIdx.x >> 4);   // (batch, key, head)
     if (row >= (long long)p.s.B * p.s.Sk * p.s.Hk || 8 * l >= p.s.D) return;
     const int h = (int)(row % p.s.Hk), key = (int)(row / p.s.Hk % p.s.Sk), b = (int)(row / p.s.Hk / p.s.Sk);
     const int len = length_of(p.s, b), tiles = (max(len, 0) + kTile - 1) / kTile;
@@ -153,49 +158,76 @@ __global__ void __launch_bounds__(256, 4) cross_pre_kernel(const __grid_constant
     train::store_f32<__nv_bfloat16, 8>(p.dv + b * p.dv_b + key * p.dv_s + h * p.dv_h + 8 * l, t);
     return;
   }
-  const long long rows = (long long)p.s.B * p.s.Hk * p.s.ntile * kTile;
-  if (rows == 0) return;
-  const long long row0 = (long long)blockIdx.x * 16 * kPreRows + (threadIdx.x >> 4);
-  // a block's rows lie in one row tile
-  const long long tile_id = (long long)blockIdx.x * 16 * kPreRows / kTile;
-  const int tile = (int)(tile_id % p.s.ntile), bh = (int)(tile_id / p.s.ntile), b = bh / p.s.Hk, hk = bh - b * p.s.Hk;
-  if (b >= p.s.B) return;
-  const int r0 = (int)(row0 - tile_id * kTile), len = length_of(p.s, b);
+  if (blockIdx.x >= row_blocks) {
+    const long long at = (long long)(blockIdx.x - row_blocks) * 256 + threadIdx.x;
+    int token, head;
+    if (at < (long long)p.s.B * p.s.Hk * p.s.ntile * kTile &&
+        !row_of(p.s, (int)(at / kTile % p.s.ntile), (int)(at % kTile), token, head)) {
+      p.delta[at] = 0.f;
+      p.nnl[at] = -INFINITY;
+    }
+    return;
+  }
+  // (rows number less than 2^31)
+  const unsigned rows = (unsigned)p.s.B * p.s.Sq * p.s.Hq;
+  const unsigned row0 = (blockIdx.x * 16u + (threadIdx.x >> 4)) * kPreRows;
   train::Vec<__nv_bfloat16, 8> x[kPreRows], y[kPreRows];
-  float nl[kPreRows];
 #pragma unroll
   for (int k = 0; k < kPreRows; ++k) {
-    int token, head;
-    const bool live = row_of(p.s, tile, r0 + 16 * k, token, head);
-    const int h = hk * p.s.g + head;
-    nl[k] = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[k].w[i] = y[k].w[i] = 0u;
-    if (live && 8 * l < p.s.D) {
-      const size_t at = (((size_t)b * p.s.Sq + token) * p.s.Hq + h) * p.s.D + 8 * l;
-      x[k] = train::load_vec<__nv_bfloat16, 8>(p.o + at);
-      y[k] = train::load_vec<__nv_bfloat16, 8>(p.dO + at);
-      if (l == 0) nl[k] = -kLog2e * __ldg(p.lse + ((size_t)b * p.s.Hq + h) * p.s.Sq + token);
-      if (len <= 0) {
-        float t[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = len < 0 ? NAN : 0.f;
-        train::store_f32<__nv_bfloat16, 8>(p.dq + b * p.dq_b + token * p.dq_s + h * p.dq_h + 8 * l, t);
-      }
+    if (row0 + k < rows && 8 * l < p.s.D) {
+      x[k] = train::load_vec<__nv_bfloat16, 8>(p.o + (size_t)(row0 + k) * p.s.D + 8 * l);
+      y[k] = train::load_vec<__nv_bfloat16, 8>(p.dO + (size_t)(row0 + k) * p.s.D + 8 * l);
     }
   }
+  // the first row's place, then from head to head, token to token, batch to batch
+  const unsigned bt = row0 / (unsigned)p.s.Hq;
+  int b = (int)(bt / (unsigned)p.s.Sq), token = (int)(bt - (unsigned)b * p.s.Sq), h = (int)(row0 - bt * p.s.Hq);
+  int hk = (unsigned)h / (unsigned)p.s.g, head = h - hk * p.s.g, tk = (unsigned)token / (unsigned)p.s.tpt;
+  int i = token - tk * p.s.tpt;
 #pragma unroll
   for (int k = 0; k < kPreRows; ++k) {
     float u[8], v[8], t = 0.f;
     train::unpack<__nv_bfloat16, 8>(x[k], u);
     train::unpack<__nv_bfloat16, 8>(y[k], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t = fmaf(u[i], v[i], t);
+    for (int e = 0; e < 8; ++e) t = fmaf(u[e], v[e], t);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (l == 0) {
-      p.delta[row0 + 16 * k] = -t;
-      p.nnl[row0 + 16 * k] = nl[k];
+    if (row0 + k < rows) {
+      if (l == 0) {
+        const int tile = p.s.packed ? tk : head * p.s.nq + tk, r = p.s.packed ? i * p.s.g + head : i;
+        const size_t at = ((size_t)(b * p.s.Hk + hk) * p.s.ntile + tile) * kTile + r;
+        p.delta[at] = -t;
+        p.nnl[at] = -kLog2e * __ldg(p.lse + ((size_t)b * p.s.Hq + h) * p.s.Sq + token);
+      }
+      if ((p.s.lens || p.s.Sk == 0) && 8 * l < p.s.D) {
+        const int len = length_of(p.s, b);
+        if (len <= 0) {
+          float z[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = len < 0 ? NAN : 0.f;
+          train::store_f32<__nv_bfloat16, 8>(p.dq + b * p.dq_b + token * p.dq_s + h * p.dq_h + 8 * l, z);
+        }
+      }
+    }
+    ++h;
+    if (++head == p.s.g) {
+      head = 0;
+      ++hk;
+    }
+    if (h == p.s.Hq) {
+      h = hk = 0;
+      ++token;
+      if (++i == p.s.tpt) {
+        i = 0;
+        ++tk;
+      }
+      if (token == p.s.Sq) {
+        token = tk = i = 0;
+        ++b;
+      }
     }
   }
 }

@@ -51,8 +51,8 @@ static_assert(kRowsRegsCtrl + 2 * kRowsRegsSoftmax == 3 * kRowsRegsLaunch,
 template <bool ALL = false>
 struct RowsWalk {
   const BwdArgs* a;
-  int u, bh, b, hk, tile, kseg, len, t0, nt;
-  __device__ __forceinline__ RowsWalk(const BwdArgs& args) : a(&args), u((int)blockIdx.x - (int)gridDim.x) {}
+  int b, u, bh, hk, tile, kseg, len, t0, nt;
+  __device__ __forceinline__ RowsWalk(const BwdArgs& args) : a(&args), b(-1), u((int)blockIdx.x - (int)gridDim.x) {}
   __device__ __forceinline__ bool next() {
     const BwdArgs& p = *a;
     do {
@@ -62,10 +62,13 @@ struct RowsWalk {
       const int r = u / p.ksegs;
       tile = r % p.s.ntile;
       bh = r / p.s.ntile;
-      b = bh / p.s.Hk;
-      hk = bh - b * p.s.Hk;
-      len = length_of(p.s, b);
-      if (ALL) len = same(len);
+      const int batch = bh / p.s.Hk;
+      hk = bh - batch * p.s.Hk;
+      if (batch != b) {                            // else its length is known
+        b = batch;
+        len = length_of(p.s, b);
+        if (ALL) len = same(len);
+      }
       t0 = kseg * p.kper;
       nt = min((max(len, 0) + kTile - 1) / kTile, t0 + p.kper) - t0;
     } while (nt <= 0);

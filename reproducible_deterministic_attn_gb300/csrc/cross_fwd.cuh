@@ -76,11 +76,11 @@ static_assert(kFwdRegsCtrl + 4 * kFwdRegsSoftmax == 5 * kFwdRegsLaunch,
 template <bool ALL = false>
 struct FwdWalk {
   const FwdArgs* a;
-  int u, bh, b, hk, pair, split;
+  int b, u, bh, hk, pair, split;
   int len;                   // the batch's keys (-1: out of range)
   int t0, nt;                // first key tile and their number in this range
   bool has_b;
-  __device__ __forceinline__ FwdWalk(const FwdArgs& args) : a(&args), u((int)blockIdx.x - (int)gridDim.x) {}
+  __device__ __forceinline__ FwdWalk(const FwdArgs& args) : a(&args), b(-1), u((int)blockIdx.x - (int)gridDim.x) {}
   __device__ __forceinline__ bool next() {
     const FwdArgs& p = *a;
     u += gridDim.x;
@@ -89,11 +89,14 @@ struct FwdWalk {
     const int r = u / p.splits;
     pair = r % p.pairs;
     bh = r / p.pairs;
-    b = bh / p.s.Hk;
-    hk = bh - b * p.s.Hk;
+    const int batch = bh / p.s.Hk;
+    hk = bh - batch * p.s.Hk;
     has_b = 2 * pair + 1 < p.s.ntile;
-    len = length_of(p.s, b);
-    if (ALL) len = same(len);
+    if (batch != b) {                              // else its length is known
+      b = batch;
+      len = length_of(p.s, b);
+      if (ALL) len = same(len);
+    }
     t0 = split * p.kper;
     const int all = (max(len, 0) + kTile - 1) / kTile;
     nt = max(0, min(all, t0 + p.kper) - t0);

@@ -718,7 +718,9 @@ dash_status_t launch(Args a, cudaStream_t stream) {
   a.rows = p.rows;
   a.chunks = p.chunks;
   a.cols = p.cols;
-  if (p.resident) {
+  if (a.N == 0) {
+    // no sample: dw and db are zeros
+  } else if (p.resident) {
     const auto kernel = resident_kernel<T, V, ACT, BWD>;
     DASH_TRY(allow_shared((const void*)kernel, p.smem));
     cudaLaunchConfig_t cfg = {};
@@ -741,8 +743,7 @@ dash_status_t launch(Args a, cudaStream_t stream) {
       sums_kernel<T, V, ACT, BWD><<<grid, kThreads, smem, stream>>>(a);
       DASH_TRY(cudaGetLastError());
     }
-    if (a.N > 0)
-      DASH_TRY(launch_after(join_kernel<T, BWD>, dim3((unsigned)a.N * a.G), kThreads, a.cpg * sizeof(float2), stream, a));
+    DASH_TRY(launch_after(join_kernel<T, BWD>, dim3((unsigned)a.N * a.G), kThreads, a.cpg * sizeof(float2), stream, a));
     if (grid.x > 0) {
       DASH_TRY(allow_shared((const void*)apply_kernel<T, V, ACT, BWD>, kRingBytes<T, V, BWD>));
       DASH_TRY(launch_after(apply_kernel<T, V, ACT, BWD>, grid, kThreads, kRingBytes<T, V, BWD>, stream, a));

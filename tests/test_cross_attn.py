@@ -133,3 +133,184 @@ def test_backward_matches_definition(B, Sq, Sk, Hq, Hk, D, lens):
     o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"])
     grads = da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"])
     _check_backward(x, o, lse, *grads)
+
+
+@pytest.mark.parametrize("B,Sq,Sk,Hq,Hk,D,lens", [
+    (4, 700, 77, 16, 16, 64, (77, 64, 30, 0)),        # more units than SMs, one key tile
+    (3, 1500, 500, 8, 8, 128, (500, 129, 300)),       # several key tiles, the issuers take turns
+    (2, 1100, 130, 12, 4, 96, (128, 130)), (1, 5000, 60, 1, 1, 128, None), (2, 1, 9000, 4, 4, 128, (9000, 4097))])
+def test_more_units_than_multiprocessors(B, Sq, Sk, Hq, Hk, D, lens):
+    x = _inputs(B, Sq, Sk, Hq, Hk, D, lens, seed=Sq)
+    o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"])
+    _check_forward(x, o, lse)
+    _check_backward(x, o, lse, *da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"]))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_maxima_that_grow_along_the_keys(D):
+    """Scores from -40 to 40 in rising order, so that the exponent's reference moves at most key tiles."""
+    x = _inputs(1, 200, 700, 2, 1, D, (650,), seed=3)
+    q = torch.randn(1, 200, 1, D, device="cuda").sign()
+    ramp = torch.linspace(-40, 40, 700, device="cuda")[None, :, None, None] / (D * x["scale"])
+    x["q"] = q.expand(1, 200, 2, D).to(torch.bfloat16).contiguous()
+    x["k"] = x["k"].clone()
+    x["k"][:, :650] = (q[:, :1] * ramp[:, :650]).to(torch.bfloat16)
+    o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"])
+    _check_forward(x, o, lse)
+    _check_backward(x, o, lse, *da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"]))
+
+
+def test_strides_shared_batches_and_heads():
+    x = _inputs(3, 70, 150, 4, 2, 64, (150, 20, 0), seed=5, hide=False)
+    want = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"])
+    gwant = da.cross_attn_backward(x["q"], x["k"], x["v"], want[0], x["do"], want[1], x["scale"], x["t"])
+    y = {n: x[n].transpose(1, 2).contiguous().transpose(1, 2) for n in "qkv"}          # held as [B, H, S, D]
+    got = da.cross_attn_forward(y["q"], y["k"], y["v"], x["scale"], x["t"].long())
+    fused = torch.full((3, 150, 6, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    dq = torch.full((3, 4, 70, 64), 7.0, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    ggot = da.cross_attn_backward(y["q"], y["k"], y["v"], got[0], x["do"], got[1], x["scale"], x["t"].long(), dq=dq,
+                                  dk=fused[:, :, 1:3], dv=fused[:, :, 4:6])
+    assert all(torch.equal(a, b) for a, b in zip(want + gwant, got + ggot))
+    assert bool((fused[:, :, 0] == 7).all()) and bool((fused[:, :, 3] == 7).all())
+    # keys of one batch and one head for all, queries of one head
+    z = dict(x, k=x["k"][:1, :, :1].expand(3, 150, 2, 64), v=x["v"][:1, :, :1].expand(3, 150, 2, 64),
+             q=x["q"][:, :, :1].expand(3, 70, 4, 64))
+    o, lse = da.cross_attn_forward(z["q"], z["k"], z["v"], x["scale"], x["t"])
+    _check_forward(z, o, lse)
+    grads = da.cross_attn_backward(z["q"], z["k"], z["v"], o, x["do"], lse, x["scale"], x["t"])
+    _check_backward(z, o, lse, *grads)
+    with pytest.raises(da.DashError) as e:
+        da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"], dk=z["k"])
+    assert e.value.status == da.DASH_ERR_INVALID_ARG
+
+
+def test_offsets_beyond_32_bits():
+    """Keys of a batch that lies 2^32 elements behind the first one."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    x = _inputs(2, 9, 140, 2, 1, 64, (140, 135), seed=6, hide=False)
+    flat = torch.empty((1 << 32) + 2 * 140 * 64, dtype=torch.bfloat16, device="cuda")
+    far = flat.as_strided((2, 140, 1, 64), (1 << 32, 64, 64, 1))
+    far.copy_(x["k"])
+    o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"])
+    want = (o, lse, *da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"]))
+    got = da.cross_attn_forward(x["q"], far, x["v"], x["scale"], x["t"])
+    dk = flat.as_strided((2, 140, 1, 64), (1 << 32, 64, 64, 1), 140 * 64)
+    got = (*got, *da.cross_attn_backward(x["q"], far, x["v"], o, x["do"], lse, x["scale"], x["t"], dk=dk))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("Sq", [1, 200])
+def test_length_out_of_range(Sq):
+    x = _inputs(4, Sq, 300, 4, 2, 64, (300, 77, 20, 256), seed=7, hide=False)
+    o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"])
+    want = (o, lse, *da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"]))
+    bad = x["t"].clone()
+    bad[1], bad[2] = 301, -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], bad, status=status)
+    assert int(status) == da.DASH_ERR_BOUNDS
+    ws = da.new_cross_attn_workspace(4, Sq, 300, 4, 2, 64, "cuda")
+    got = (*got, *da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], bad, workspace=ws,
+                                         check=False))
+    assert da.dash_attn_get_status(ws) == da.DASH_ERR_BOUNDS and "a length" in da.dash_last_error()
+    for a, b in zip(got, want):
+        assert bool(torch.isnan(a[1:3]).all()) and torch.equal(a[0::3], b[0::3])
+    with pytest.raises(da.DashError):
+        da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], bad)
+
+
+def test_empty():
+    x = _inputs(2, 5, 40, 2, 2, 64, None, seed=8)
+    none = x["k"][:, :0]
+    o, lse = da.cross_attn_forward(x["q"], none, none, x["scale"])
+    assert not bool(o.any()) and bool((lse == float("-inf")).all())
+    dq, dk, dv = da.cross_attn_backward(x["q"], none, none, o, x["do"], lse, x["scale"])
+    assert not bool(dq.any()) and dk.numel() == 0 and dv.numel() == 0
+    q = x["q"][:, :0]
+    o, lse = da.cross_attn_forward(q, x["k"], x["v"], x["scale"])
+    assert o.shape == (2, 0, 2, 64) and lse.shape == (2, 2, 0)
+    dq, dk, dv = da.cross_attn_backward(q, x["k"], x["v"], o, x["do"][:, :0], lse, x["scale"])
+    assert dq.numel() == 0 and not bool(dk.any()) and not bool(dv.any())
+    o, lse = da.cross_attn_forward(x["q"][:0], x["k"][:0], x["v"][:0], x["scale"])
+    assert o.shape == (0, 5, 2, 64)
+
+
+@pytest.mark.parametrize("B,Sq,Sk,Hq,Hk,D,lens", [
+    (2, 300, 77, 4, 4, 64, (77, 50)), (3, 1, 1500, 8, 2, 128, (1500, 10, 700)), (2, 900, 400, 8, 4, 128, (400, 333))])
+def test_bitwise_reproducible_streams_and_graph(B, Sq, Sk, Hq, Hk, D, lens):
+    x = _inputs(B, Sq, Sk, Hq, Hk, D, lens, seed=9)
+    ws = da.new_cross_attn_workspace(B, Sq, Sk, Hq, Hk, D, "cuda")
+
+    def both(**kw):
+        o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"], workspace=ws)
+        return (o, lse, *da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"],
+                                                workspace=ws, **kw))
+    want = both()
+    for _ in range(5):
+        ws.random_(0, 255)
+        assert all(torch.equal(a, b) for a, b in zip(want, both()))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = both(check=False)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"], stream=s)
+    s.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = both(check=False)
+    for t in got:
+        t.zero_()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("Sq,Sk", [(300, 77), (300, 400)])
+def test_a_wait_that_runs_out(Sq, Sk):
+    """The testing hook withholds the tiles: every wait for them runs out, which the status and
+    the LSE say; the next call is unharmed."""
+    x = _inputs(1, Sq, Sk, 2, 2, 64, (Sk - 3,), seed=10)
+    want = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        da.dash_debug_set_sync(50_000_000, 1)
+        o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"], status=status)
+        assert int(status) == da.DASH_ERR_SYNC_TIMEOUT and bool(torch.isnan(lse).all())
+        with pytest.raises(da.DashError) as e:
+            da.cross_attn_backward(x["q"], x["k"], x["v"], want[0], x["do"], want[1], x["scale"], x["t"])
+        assert e.value.status == da.DASH_ERR_SYNC_TIMEOUT
+    finally:
+        da.dash_debug_set_sync(0, 0)
+    o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"])
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    _check_backward(x, o, lse, *da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"]))
+
+
+def test_refusals():
+    x = _inputs(2, 5, 40, 4, 2, 64, (40, 3), seed=11)
+    f = lambda **kw: da.cross_attn_forward(*(dict(x, **kw)[n] for n in ("q", "k", "v", "scale", "t")))  # noqa: E731
+    for kw in (dict(q=x["q"].float()), dict(k=x["k"][:, :, :1].expand(2, 40, 3, 64)), dict(v=x["v"][:, :39]),
+               dict(t=x["t"].float()), dict(t=x["t"][:1]), dict(q=x["q"][:1]), dict(q=x["q"].transpose(2, 3))):
+        with pytest.raises(ValueError):
+            f(**kw)
+    for kw in (dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf"))):
+        with pytest.raises(da.DashError) as e:
+            f(**kw)
+        assert e.value.status == da.DASH_ERR_INVALID_ARG
+    o, lse = f()
+    b = lambda **kw: da.cross_attn_backward(*(dict(x, o=o, lse=lse, **kw)[n] for n in  # noqa: E731
+                                              ("q", "k", "v", "o", "do", "lse", "scale", "t")))
+    for kw in (dict(do=x["do"].transpose(1, 2).contiguous().transpose(1, 2)), dict(do=x["do"][:, :4])):
+        with pytest.raises(ValueError):
+            b(**kw)
+    with pytest.raises(ValueError):
+        da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse[:, :, :4], x["scale"], x["t"])
+    with pytest.raises(da.DashError) as e:
+        da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"],
+                               workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == da.DASH_ERR_WORKSPACE_TOO_SMALL

@@ -110,3 +110,127 @@ def test_matches_definition(N, S, C, G, t, act):
     _check_forward(x, G, 1e-5, act, y, mean, rstd)
     grads = da.group_norm_act_backward(x["dy"], x["x"], x["w"], x["b"], mean, rstd, G, act)
     _check_backward(x, G, act, mean, rstd, *grads)
+
+
+def _both(x, G, act="silu", **kw):
+    y, mean, rstd = da.group_norm_act_forward(x["x"], x["w"], x["b"], G, 1e-5, act, **kw)
+    return (y, mean, rstd, *da.group_norm_act_backward(x["dy"], x["x"], x["w"], x["b"], mean, rstd, G, act, **kw))
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_without_weights_and_with_one_of_them(t):
+    x = _inputs(2, 50, 48, t, seed=1, affine=False)
+    y, mean, rstd, *grads = _both(x, 6)
+    _check_forward(x, 6, 1e-5, "silu", y, mean, rstd)
+    _check_backward(x, 6, "silu", mean, rstd, *grads)
+    w = torch.full((48,), 1.5, device="cuda")
+    y, mean, rstd = da.group_norm_act_forward(x["x"], w, None, 6)
+    dx, dw, db = da.group_norm_act_backward(x["dy"], x["x"], w, None, mean, rstd, 6)
+    assert db is None and dw.shape == (48,)
+    full = da.group_norm_act_backward(x["dy"], x["x"], w, torch.zeros(48, device="cuda"), mean, rstd, 6)
+    assert torch.equal(dx, full[0]) and torch.equal(dw, full[1])
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("N,S,C,G", [(2, 200, 64, 8), (1, 60000, 64, 4)])
+def test_a_mean_far_beyond_the_spread(N, S, C, G, t):
+    """Means a few hundred times the spread: in the first value's distance nothing is lost."""
+    x = _inputs(N, S, C, t, seed=2, mean=0.0)
+    x["x"] = (x["x"].float() + 100.0).to(t)
+    y, mean, rstd, *grads = _both(x, G)
+    _check_forward(x, G, 1e-5, "silu", y, mean, rstd)
+    _check_backward(x, G, "silu", mean, rstd, *grads)
+
+
+def test_constant_channels_and_large_activations():
+    x = _inputs(2, 30, 32, torch.float32, seed=3)
+    x["x"][:, :, :8] = 3.0                            # a group without spread
+    x["b"][8:] = torch.linspace(-90, 90, 24, device="cuda")
+    y, mean, rstd, *grads = _both(x, 4)
+    assert bool(torch.isfinite(y).all()) and all(bool(torch.isfinite(g).all()) for g in grads)
+    want, wm, wr = ref.group_norm(x["x"], x["w"], x["b"], 4, 1e-5, "silu")
+    # the sigmoid's relative error at |z| <= 95: its exponent's argument is off by 2 steps of |z|
+    tol = 2.0 ** -14 * want.abs() + 2.0 ** -16
+    assert bool(((y.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_part_of_a_wider_buffer_and_maps(t):
+    g = torch.Generator(device="cuda").manual_seed(4)
+    wide = torch.randn(2, 6, 7, 96, generator=g, device="cuda").to(t)
+    part = wide[..., 32:64]
+    x = _inputs(2, 42, 32, t, seed=5)
+    x["x"] = part.reshape(2, 42, 32)
+    want = _both(x, 4)
+    y = dict(x, x=part, dy=x["dy"].view(2, 6, 7, 32))
+    got = _both(y, 4)
+    assert got[0].shape == (2, 6, 7, 32)
+    for a, b in zip(want, got):
+        assert torch.equal(a.reshape(b.shape), b)
+    odd = wide[..., 33:65]                            # no 16-byte pieces
+    x["x"] = odd.reshape(2, 42, 32)
+    y["x"] = odd
+    got = _both(y, 4)
+    _check_forward(x, 4, 1e-5, "silu", got[0].reshape(2, 42, 32), *got[1:3])
+    with pytest.raises(ValueError, match="evenly"):
+        da.group_norm_act_forward(wide[:, :, :5], None, None, 4)
+
+
+def test_empty():
+    for N, S in ((0, 5), (3, 0)):
+        x = _inputs(N, S, 16, torch.bfloat16)
+        y, mean, rstd, dx, dw, db = _both(x, 4)
+        assert y.shape == (N, S, 16) and mean.shape == (N, 4)
+        assert not bool(dw.any()) and not bool(db.any()) and not bool(mean.any())
+        assert bool(torch.isfinite(rstd).all())
+
+
+@pytest.mark.parametrize("N,S,C,G", [(2, 64, 320, 32), (4, 2000, 128, 8), (1, 60000, 64, 4)])
+def test_bitwise_reproducible_streams_and_graph(N, S, C, G):
+    x = _inputs(N, S, C, torch.bfloat16, seed=6)
+    ws = da.new_group_norm_workspace(N, S, C, G, "cuda")
+    want = _both(x, G, workspace=ws)
+    for _ in range(5):
+        ws.random_(0, 255)
+        assert all(torch.equal(a, b) for a, b in zip(want, _both(x, G, workspace=ws)))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = _both(x, G)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    y, mean, rstd = da.group_norm_act_forward(x["x"], x["w"], x["b"], G, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = _both(x, G, workspace=ws)
+    for t in got:
+        t.zero_()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_given_outputs_and_refusals():
+    x = _inputs(2, 10, 32, torch.bfloat16, seed=7)
+    want = _both(x, 4)
+    out, dx = torch.empty_like(x["x"]), torch.empty_like(x["x"])
+    y, mean, rstd = da.group_norm_act_forward(x["x"], x["w"], x["b"], 4, out=out)
+    assert y is out and torch.equal(out, want[0])
+    got = da.group_norm_act_backward(x["dy"], x["x"], x["w"], x["b"], mean, rstd, 4, dx=dx)
+    assert got[0] is dx and torch.equal(dx, want[3])
+    bad = [dict(groups=5), dict(groups=0), dict(activation="relu"), dict(w=x["w"][:8]), dict(b=x["b"].double()),
+           dict(x=x["x"].double()), dict(x=x["x"].transpose(1, 2))]
+    for kw in bad:
+        a = dict(dict(x=x["x"], w=x["w"], b=x["b"], groups=4, activation="silu"), **kw)
+        with pytest.raises(ValueError):
+            da.group_norm_act_forward(a["x"], a["w"], a["b"], a["groups"], activation=a["activation"])
+    with pytest.raises(ValueError, match="dy"):
+        da.group_norm_act_backward(x["dy"][:1], x["x"], x["w"], x["b"], mean, rstd, 4)
+    with pytest.raises(ValueError, match="mean"):
+        da.group_norm_act_backward(x["dy"], x["x"], x["w"], x["b"], mean[:, :2], rstd, 4)
+    with pytest.raises(da.DashError) as e:
+        da.group_norm_act_forward(x["x"], x["w"], x["b"], 4, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == da.DASH_ERR_WORKSPACE_TOO_SMALL

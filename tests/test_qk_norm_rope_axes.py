@@ -103,3 +103,67 @@ def test_one_axis_gives_the_one_axis_operators_bits(il):
     outs3, grads3 = _both(y, il)
     for a, b, c in zip(outs + grads, want + gwant, outs3 + grads3):
         assert torch.equal(a, b) and torch.equal(c, b)
+
+
+def test_position_out_of_range_on_one_axis():
+    x = _inputs(1, 12, 2, 1, 64, (8, 12, 12), torch.bfloat16, P=30, seed=7)
+    want, gwant = _both(x, False)
+    x["pos"] = x["pos"].clone()
+    x["pos"][2, 0, 5] = 30
+    x["pos"][0, 0, 6] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a = (x["wq"], x["wk"], x["cos"], x["sin"], x["pos"], x["sections"])
+    outs = da.qk_norm_rope_axes_forward(x["q"], x["k"], *a, status=status)
+    assert int(status) == da.DASH_ERR_BOUNDS
+    ws = da.new_qk_norm_rope_workspace(1, 12, 2, 1, 64, "cuda")
+    grads = da.qk_norm_rope_axes_backward(x["dq"], x["dk"], x["q"], x["k"], *a, workspace=ws, check=False)
+    assert da.dash_attn_get_status(ws) == da.DASH_ERR_BOUNDS and "a position" in da.dash_last_error()
+    keep = [0, 1, 2, 3, 4, 7, 8, 9, 10, 11]
+    for got, w in zip(outs + grads[:2], want + gwant[:2]):
+        assert bool(torch.isnan(got[:, 5:7]).all()) and torch.equal(got[:, keep], w[:, keep])
+
+
+def test_strides_positions_by_row_and_gradients_in_place():
+    x = _inputs(2, 19, 4, 2, 128, (16, 24, 24), torch.bfloat16, seed=5)
+    x["pos"] = x["pos"][:, :1].expand(3, 2, 19).contiguous()
+    want, gwant = _both(x, False)
+    for pos in (x["pos"][:, 0].contiguous(), x["pos"][:, :1].contiguous()):
+        got, _ = _both(dict(x, pos=pos), False)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    y = dict(x, q=x["q"].transpose(1, 2).contiguous().transpose(1, 2))
+    fused = torch.full((2, 19, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    got, ggot = _both(y, False, dq=fused[:, :, :4], dk=fused[:, :, 4:6])
+    assert all(torch.equal(a, b) for a, b in zip(want + gwant, got + ggot)) and bool((fused[:, :, 6:] == 7).all())
+
+
+def test_empty_reproducible_and_graph():
+    x = _inputs(2, 700, 16, 4, 128, (9, 12, 11), torch.bfloat16, seed=8)
+    e = {n: x[n][:, :0] for n in ("q", "k", "dq", "dk")}
+    outs, grads = _both(dict(x, **e, pos=x["pos"][:, :, :0].contiguous()), False)
+    assert outs[0].shape == (2, 0, 16, 128) and not bool(grads[2].any())
+    ws = da.new_qk_norm_rope_workspace(2, 700, 16, 4, 128, "cuda")
+    outs, grads = _both(x, True, workspace=ws)
+    want = outs + grads
+    for _ in range(3):
+        ws.random_(0, 255)
+        outs, grads = _both(x, True, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(want, outs + grads))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs, grads = _both(x, True, workspace=ws, check=False)
+    for t in outs + grads:
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs + grads))
+
+
+def test_refusals():
+    x = _inputs(1, 4, 2, 1, 64, (8, 12, 12), torch.bfloat16)
+    a = (x["q"], x["k"], x["wq"], x["wk"], x["cos"], x["sin"])
+    for sections in ((8, 12, 11), (8, 12, 13), (40, -8), (8, 8, 8, 4, 4), ()):
+        with pytest.raises(ValueError, match="sections"):
+            da.qk_norm_rope_axes_forward(*a, x["pos"], sections)
+    for pos in (x["pos"][:2], x["pos"][:, :, :3], x["pos"].float(), x["pos"][:, 0, 0]):
+        with pytest.raises(ValueError, match="positions"):
+            da.qk_norm_rope_axes_forward(*a, pos, x["sections"])

@@ -167,6 +167,24 @@ void set_places(Shape* s, const long long* qs, const long long* ks, const long l
   s->v_h = vs[2] != 0;
 }
 
+// The units of a kernel whose fastest digits are d0 and d1, and the CTAs that share them.
+Units make_units(const Shape& s, int d0, int d1, int sms, int* grid) {
+  Units n = {};
+  n.radix[0] = d0;
+  n.radix[1] = d1;
+  n.radix[2] = s.Hk;
+  n.batches = s.B;
+  const long long all = (long long)d0 * d1 * s.Hk * s.B;
+  *grid = (int)std::min<long long>(all, sms);
+  int g = *grid;
+  for (int i = 0; i < 3; ++i) {
+    n.step[i] = g % n.radix[i];
+    g /= n.radix[i];
+  }
+  n.step[3] = g;
+  return n;
+}
+
 template <int DT>
 dash_status_t launch_fwd(FwdArgs a, const Maps& maps, cudaStream_t stream) {
   static std::atomic<uint64_t> known{0};
@@ -174,7 +192,9 @@ dash_status_t launch_fwd(FwdArgs a, const Maps& maps, cudaStream_t stream) {
   if (st != DASH_OK) return st;
   int sms = 0;
   if (const dash_status_t e = sm_count(&sms)) return e;
-  cross_fwd_kernel<DT><<<std::min(a.units, sms), kFwdThreads, FwdLay<DT>::ALLOC, stream>>>(a, maps);
+  int grid = 0;
+  a.units = make_units(a.s, a.splits, a.pairs, sms, &grid);
+  cross_fwd_kernel<DT><<<grid, kFwdThreads, FwdLay<DT>::ALLOC, stream>>>(a, maps);
   DASH_TRY(cudaGetLastError());
   if (a.splits > 1) {
     const long long rows = (long long)a.s.B * a.s.Hk * a.s.ntile * kTile;
@@ -247,8 +267,9 @@ dash_status_t launch_keys(BwdArgs a, const Maps& maps, int sms, cudaStream_t str
   static std::atomic<uint64_t> known{0};
   const dash_status_t st = prepare((const void*)cross_keys_kernel<DT, DQ>, L::ALLOC, L::REGS_LAUNCH, &known);
   if (st != DASH_OK) return st;
-  a.units = (int)((long long)a.s.B * a.s.Hk * a.s.nk * a.qsegs);
-  DASH_TRY(dash::launch_after(cross_keys_kernel<DT, DQ>, dim3(std::min(a.units, sms)), kThreads, L::ALLOC, stream, a, maps));
+  int grid = 0;
+  a.units = make_units(a.s, a.s.nk, a.qsegs, sms, &grid);
+  DASH_TRY(dash::launch_after(cross_keys_kernel<DT, DQ>, dim3(grid), kThreads, L::ALLOC, stream, a, maps));
   return DASH_OK;
 }
 
@@ -281,8 +302,9 @@ dash_status_t launch_bwd(BwdArgs a, bool one, const Maps& maps, cudaStream_t str
     static std::atomic<uint64_t> known{0};
     const dash_status_t st = prepare((const void*)cross_rows_kernel<DT>, RowsLay<DT>::ALLOC, kRowsRegsLaunch, &known);
     if (st != DASH_OK) return st;
-    a.units = (int)((long long)a.s.B * a.s.Hk * a.s.ntile * a.ksegs);
-    DASH_TRY(dash::launch_after(cross_rows_kernel<DT>, dim3(std::min(a.units, sms)), kRowsThreads, RowsLay<DT>::ALLOC,
+    int grid = 0;
+    a.units = make_units(a.s, a.ksegs, a.s.ntile, sms, &grid);
+    DASH_TRY(dash::launch_after(cross_rows_kernel<DT>, dim3(grid), kRowsThreads, RowsLay<DT>::ALLOC,
                                 stream, a, maps));
     if (a.ksegs > 1)
       DASH_TRY(dash::launch_after(cross_join_rows_kernel<DT>, dim3((unsigned)ceil_div<long long>(rows * per, 256)), 256,
@@ -327,8 +349,6 @@ dash_status_t dash_cross_attn_fwd(const void* q, const void* k, const void* v, c
   a.pairs = pl.pairs;
   a.splits = pl.splits;
   a.kper = pl.kper;
-  const long long units = (long long)B * Hk * pl.pairs * pl.splits;
-  a.units = (int)units;
   a.scale_log2 = scale * kLog2e;
   a.status = status;
   a.timeout_ns = sync_timeout_ns();

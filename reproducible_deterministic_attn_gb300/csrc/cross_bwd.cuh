@@ -51,7 +51,7 @@ struct BwdArgs {
   float* dkv_part;           // [row segment][group][key tile][dK, dV][DT / 8][128][8]
   int qsegs, qper;           // row segments of cross_keys_kernel, row tiles of one
   int ksegs, kper;           // key segments of cross_rows_kernel, key tiles of one
-  int units;                 // of the kernel that is being launched
+  Units units;               // of the kernel that is being launched
   float scale, scale_log2;
   int* header;
   long long timeout_ns;
@@ -90,37 +90,35 @@ enum {
 };
 static_assert(8 * C_COUNT + 8 <= 256, "barrier area");
 
-// A CTA's tasks: units u, u + grid, ..., of each the row tiles.
-// ALL: a whole warp walks together.
+// A CTA's tasks: of each of its units, [batch][key head][row segment][key tile], the row tiles. ALL: a
+// whole warp walks together.
 template <bool ALL = false>
 struct KeysWalk {
   const BwdArgs& p;
-  int b, u, bh, hk, qseg, kt, len;
+  Place at;                  // d0: key tile, d1: row segment
+  int known, len;            // the batch whose length is at hand (-2: not begun), that length
   int q0, nqt, j;            // the segment's first row tile, their number, the one at hand
-  __device__ __forceinline__ KeysWalk(const BwdArgs& a) : p(a), b(-1), u((int)blockIdx.x - (int)gridDim.x), nqt(0), j(0) {}
+  __device__ __forceinline__ KeysWalk(const BwdArgs& a)
+      : p(a), at(a.units), known(-2), len(0), nqt(0), j(0) {}
   __device__ __forceinline__ bool next() {
     if (++j < nqt) return true;
     j = 0;
     do {
-      u += gridDim.x;
-      if (u >= p.units) return false;
-      kt = u % p.s.nk;
-      const int r = u / p.s.nk;
-      qseg = r % p.qsegs;
-      bh = r / p.qsegs;
-      const int batch = bh / p.s.Hk;
-      hk = bh - batch * p.s.Hk;
-      if (batch != b) {                            // else its length is known
-        b = batch;
-        len = length_of(p.s, b);
+      if (known == -2) known = -1;
+      else at.next(p.units);
+      if (!at.more(p.units)) return false;
+      if (at.b != known) {
+        known = at.b;
+        len = length_of(p.s, known);
         if (ALL) len = same(len);
       }
-      q0 = qseg * p.qper;
-      nqt = min(p.qper, p.s.ntile - q0);
-    } while (kt * kTile >= len);
+    } while (at.d0 * kTile >= len);
+    q0 = at.d1 * p.qper;
+    nqt = min(p.qper, p.s.ntile - q0);
     return true;
   }
-  __device__ __forceinline__ int keys() const { return min(kTile, len - kt * kTile); }
+  __device__ __forceinline__ int group() const { return at.b * p.s.Hk + at.hk; }
+  __device__ __forceinline__ int keys() const { return min(kTile, len - at.d0 * kTile); }
   __device__ __forceinline__ bool first_of_tile() const { return j == 0; }
   __device__ __forceinline__ bool last_of_tile() const { return j == nqt - 1; }
   __device__ __forceinline__ int tile() const { return q0 + j; }
@@ -286,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qb = it % L::NQ;
         if (it >= L::NQ) ok = ptx::mbar_wait(bars + C_Q_EMPTY + qb, (it / L::NQ - 1) & 1, abort_flag, tmo);
         if (!ok) break;
-        const size_t row = ((size_t)w.bh * p.s.ntile + w.tile()) * kTile;
+        const size_t row = ((size_t)w.group() * p.s.ntile + w.tile()) * kTile;
         uint8_t* offs = sm + L::OFFS_OFF + qb * L::OFFS;
         ptx::mbar_expect_tx(bars + C_Q_FULL + qb, row_tile_bytes<DT>(p.s) + L::OFFS);
-        load_row_tile<DT>(p.s, &maps.q, sm + L::Q_OFF + qb * L::TILE, w.b, w.hk, w.tile(), p.s.q_b, p.s.q_h,
+        load_row_tile<DT>(p.s, &maps.q, sm + L::Q_OFF + qb * L::TILE, w.at.b, w.at.hk, w.tile(), p.s.q_b, p.s.q_h,
                           bars + C_Q_FULL + qb);
         ptx::bulk_load(offs, p.nnl + row, kTile * 4, bars + C_Q_FULL + qb);
         ptx::bulk_load(offs + kTile * 4, p.delta + row, kTile * 4, bars + C_Q_FULL + qb);
@@ -300,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           ptx::mbar_expect_tx(bars + C_KV_FULL, 2 * L::TILE);
-          load_key_tile<DT>(&maps.k, sm + L::K_OFF, w.b, w.hk, w.kt, p.s.k_b, p.s.k_h, bars + C_KV_FULL);
-          load_key_tile<DT>(&maps.v, sm + L::V_OFF, w.b, w.hk, w.kt, p.s.v_b, p.s.v_h, bars + C_KV_FULL);
+          load_key_tile<DT>(&maps.k, sm + L::K_OFF, w.at.b, w.at.hk, w.at.d0, p.s.k_b, p.s.k_h, bars + C_KV_FULL);
+          load_key_tile<DT>(&maps.v, sm + L::V_OFF, w.at.b, w.at.hk, w.at.d0, p.s.v_b, p.s.v_h, bars + C_KV_FULL);
           ++tl;
         }
         const int ob = it % L::NDO;
@@ -311,14 +309,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         ptx::mbar_expect_tx(bars + C_DO_FULL + ob, row_tile_bytes<DT>(p.s));
-        load_row_tile<DT>(p.s, &maps.dO, sm + L::DO_OFF + ob * L::TILE, w.b, w.hk, w.tile(), 1, 1,
+        load_row_tile<DT>(p.s, &maps.dO, sm + L::DO_OFF + ob * L::TILE, w.at.b, w.at.hk, w.tile(), 1, 1,
                           bars + C_DO_FULL + ob);
         ++loaded;
         ++it;
         // ask for the tiles after the buffered ones, so that they wait in L2
         if (w.j + L::NDO < w.nqt) {
-          prefetch_row_tile<DT>(p.s, &maps.q, w.b, w.hk, w.tile() + L::NDO, p.s.q_b, p.s.q_h);
-          prefetch_row_tile<DT>(p.s, &maps.dO, w.b, w.hk, w.tile() + L::NDO, 1, 1);
+          prefetch_row_tile<DT>(p.s, &maps.q, w.at.b, w.at.hk, w.tile() + L::NDO, p.s.q_b, p.s.q_h);
+          prefetch_row_tile<DT>(p.s, &maps.dO, w.at.b, w.at.hk, w.tile() + L::NDO, 1, 1);
         }
       }
       // drain: every issued load has landed before the CTA may exit
@@ -552,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int odd = lane & 1, d = row & ~1;
         int token, head;
         row_of(p.s, w.tile(), odd, token, head);
-        __nv_bfloat16* dst = p.dq + w.b * p.dq_b + token * p.dq_s + (w.hk * p.s.g + head) * p.dq_h + d;
+        __nv_bfloat16* dst = p.dq + w.at.b * p.dq_b + token * p.dq_s + (w.at.hk * p.s.g + head) * p.dq_h + d;
         uint32_t two[64];
 #pragma unroll
         for (int c = 0; c < 128; c += 2) {
@@ -589,13 +587,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ptx::warp_wait(bars + C_ACC_FULL, tl & 1, abort_flag, tmo);
         if (!ok) break;
         ptx::tc_fence_after();
-        const int key = w.kt * kTile + row;
-        float* part = p.dkv_part + (((size_t)w.qseg * p.s.B * p.s.Hk + w.bh) * p.s.nk + w.kt) * 2 * kTile * DT;
+        const int key = w.at.d0 * kTile + row;
+        float* part = p.dkv_part + (((size_t)w.at.d1 * p.s.B * p.s.Hk + w.group()) * p.s.nk + w.at.d0) * 2 * kTile * DT;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {  // dK, then dV
           const uint32_t from = tmem + lane_addr + (which ? L::T_DV : L::T_DK);
-          __nv_bfloat16* dst = which ? p.dv + w.b * p.dv_b + key * p.dv_s + w.hk * p.dv_h
-                                     : p.dk + w.b * p.dk_b + key * p.dk_s + w.hk * p.dk_h;
+          __nv_bfloat16* dst = which ? p.dv + w.at.b * p.dv_b + key * p.dv_s + w.at.hk * p.dv_h
+                                     : p.dk + w.at.b * p.dk_b + key * p.dk_s + w.at.hk * p.dk_h;
 #pragma unroll
           for (int c0 = 0; c0 < DT; c0 += 32) {
             if (c0 < p.s.D) {

@@ -45,35 +45,34 @@ constexpr int kRowsRegsLaunch = 168, kRowsRegsCtrl = 88, kRowsRegsSoftmax = 208;
 static_assert(kRowsRegsCtrl + 2 * kRowsRegsSoftmax == 3 * kRowsRegsLaunch,
               "the three warpgroups must share exactly the launch's registers");
 
-// A CTA's units: u, u + grid, ...; those without keys are passed over (cross_pre_kernel writes their
-// rows, and the join reads no range behind a length).
-// ALL: a whole warp walks together.
+// A CTA's units, [batch][key head][row tile][key range]; those without keys are passed over
+// (cross_pre_kernel writes their rows, and the join reads no range behind a length). ALL: a whole
+// warp walks together.
 template <bool ALL = false>
 struct RowsWalk {
   const BwdArgs* a;
-  int b, u, bh, hk, tile, kseg, len, t0, nt;
-  __device__ __forceinline__ RowsWalk(const BwdArgs& args) : a(&args), b(-1), u((int)blockIdx.x - (int)gridDim.x) {}
+  Place at;                  // d0: key range, d1: row tile
+  int known, len;            // the batch whose length is at hand (-2: not begun), that length
+  int t0, nt;                // first key tile and their number in this range
+  __device__ __forceinline__ RowsWalk(const BwdArgs& args)
+      : a(&args), at(args.units), known(-2), len(0) {}
   __device__ __forceinline__ bool next() {
     const BwdArgs& p = *a;
     do {
-      u += gridDim.x;
-      if (u >= p.units) return false;
-      kseg = u % p.ksegs;
-      const int r = u / p.ksegs;
-      tile = r % p.s.ntile;
-      bh = r / p.s.ntile;
-      const int batch = bh / p.s.Hk;
-      hk = bh - batch * p.s.Hk;
-      if (batch != b) {                            // else its length is known
-        b = batch;
-        len = length_of(p.s, b);
+      if (known == -2) known = -1;
+      else at.next(p.units);
+      if (!at.more(p.units)) return false;
+      if (at.b != known) {
+        known = at.b;
+        len = length_of(p.s, known);
         if (ALL) len = same(len);
       }
-      t0 = kseg * p.kper;
+      t0 = at.d0 * p.kper;
       nt = min((max(len, 0) + kTile - 1) / kTile, t0 + p.kper) - t0;
     } while (nt <= 0);
     return true;
   }
+  __device__ __forceinline__ int group() const { return at.b * a->s.Hk + at.hk; }
   __device__ __forceinline__ int keys(int t) const { return min(kTile, len - (t0 + t) * kTile); }
   __device__ __forceinline__ int steps(int t) const { return (keys(t) + 15) >> 4; }   // of 16 keys
   // rows of the K tile that dQ reads although the length leaves them out
@@ -123,28 +122,28 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         if (!ok) break;
         uint8_t* q = sm + L::Q_OFF + 2 * b * L::TILE;
         ptx::mbar_expect_tx(bars + L::Q_FULL + b, row_tile_bytes<DT>(p.s));
-        load_row_tile<DT>(p.s, &maps.q, q, w.b, w.hk, w.tile, p.s.q_b, p.s.q_h, bars + L::Q_FULL + b);
+        load_row_tile<DT>(p.s, &maps.q, q, w.at.b, w.at.hk, w.at.d1, p.s.q_b, p.s.q_h, bars + L::Q_FULL + b);
         ptx::mbar_expect_tx(bars + L::DO_FULL + b, row_tile_bytes<DT>(p.s));
-        load_row_tile<DT>(p.s, &maps.dO, q + L::TILE, w.b, w.hk, w.tile, 1, 1, bars + L::DO_FULL + b);
+        load_row_tile<DT>(p.s, &maps.dO, q + L::TILE, w.at.b, w.at.hk, w.at.d1, 1, 1, bars + L::DO_FULL + b);
         ++n;
         // the next unit's rows wait in L2
         RowsWalk<> ahead = w;
         if (ahead.next()) {
-          prefetch_row_tile<DT>(p.s, &maps.q, ahead.b, ahead.hk, ahead.tile, p.s.q_b, p.s.q_h);
-          prefetch_row_tile<DT>(p.s, &maps.dO, ahead.b, ahead.hk, ahead.tile, 1, 1);
+          prefetch_row_tile<DT>(p.s, &maps.q, ahead.at.b, ahead.at.hk, ahead.at.d1, p.s.q_b, p.s.q_h);
+          prefetch_row_tile<DT>(p.s, &maps.dO, ahead.at.b, ahead.at.hk, ahead.at.d1, 1, 1);
         }
         for (int t = 0; ok && t < w.nt; ++t, ++kv) {
           const int ks = kv % L::KST, km = kv / L::KST, vs = kv % L::VST, vm = kv / L::VST;
           if (km > 0) ok = ptx::mbar_wait(bars + L::K_EMPTY + ks, (km - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::mbar_expect_tx(bars + L::K_FULL + ks, L::TILE);
-          load_key_tile<DT>(&maps.k, sm + L::K_OFF + ks * L::TILE, w.b, w.hk, w.t0 + t, p.s.k_b, p.s.k_h,
+          load_key_tile<DT>(&maps.k, sm + L::K_OFF + ks * L::TILE, w.at.b, w.at.hk, w.t0 + t, p.s.k_b, p.s.k_h,
                             bars + L::K_FULL + ks);
           ++nk;
           if (vm > 0) ok = ptx::mbar_wait(bars + L::V_EMPTY + vs, (vm - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::mbar_expect_tx(bars + L::V_FULL + vs, L::TILE);
-          load_key_tile<DT>(&maps.v, sm + L::V_OFF + vs * L::TILE, w.b, w.hk, w.t0 + t, p.s.v_b, p.s.v_h,
+          load_key_tile<DT>(&maps.v, sm + L::V_OFF + vs * L::TILE, w.at.b, w.at.hk, w.t0 + t, p.s.v_b, p.s.v_h,
                             bars + L::V_FULL + vs);
         }
       }
@@ -269,7 +268,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     int n = 0, k = 0;                              // units, key tiles so far
     bool ok = true;
     while (ok && w.next()) {
-      const size_t row = ((size_t)w.bh * p.s.ntile + w.tile) * kTile + r;
+      const size_t row = ((size_t)w.group() * p.s.ntile + w.at.d1) * kTile + r;
       const float nnl = __ldg(p.nnl + row), delta = __ldg(p.delta + row);   // -LSE log2e, -Delta
       const uint64_t scale2 = two(p.scale_log2, p.scale_log2), nnl2 = two(nnl, nnl), delta2 = two(delta, delta);
       for (int t = 0; t < w.nt; ++t, ++k) {
@@ -322,9 +321,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       int token, head;
-      const bool live = row_of(p.s, w.tile, r, token, head);
-      __nv_bfloat16* dst = p.dq + w.b * p.dq_b + token * p.dq_s + (w.hk * p.s.g + head) * p.dq_h;
-      float* part = p.dq_part + ((((size_t)w.kseg * p.s.B * p.s.Hk + w.bh) * p.s.ntile + w.tile) * kTile) * DT;
+      const bool live = row_of(p.s, w.at.d1, r, token, head);
+      __nv_bfloat16* dst = p.dq + w.at.b * p.dq_b + token * p.dq_s + (w.at.hk * p.s.g + head) * p.dq_h;
+      float* part = p.dq_part + ((((size_t)w.at.d0 * p.s.B * p.s.Hk + w.group()) * p.s.ntile + w.at.d1) * kTile) * DT;
 #pragma unroll
       for (int i = 0; i < DT / 2; i += 32) {
         const int c0 = half * (DT / 2) + i;

@@ -35,6 +35,39 @@ struct Maps {
   CUtensorMap q, k, v, dO;   // 4-D bf16 {D, H, S, B}
 };
 
+// Units of work number a kernel's [batch][key head][radix[1]][radix[0]]; a CTA takes every grid-th. It
+// steps from one to the next digit by digit, as a division takes more than all of a step.
+struct Units {
+  int radix[3];              // of the digits below the batch: the third is Hk
+  int step[4];               // the grid's digits
+  int batches;
+};
+struct Place {
+  int d0, d1, hk, b;
+  __device__ __forceinline__ Place(const Units& n) {
+    int u = (int)blockIdx.x;
+    d0 = u % n.radix[0];
+    u /= n.radix[0];
+    d1 = u % n.radix[1];
+    u /= n.radix[1];
+    hk = u % n.radix[2];
+    b = u / n.radix[2];
+  }
+  __device__ __forceinline__ bool more(const Units& n) const { return b < n.batches; }
+  __device__ __forceinline__ void next(const Units& n) {
+    d0 += n.step[0];
+    const int c0 = d0 >= n.radix[0];
+    d0 -= c0 ? n.radix[0] : 0;
+    d1 += n.step[1] + c0;
+    const int c1 = d1 >= n.radix[1];
+    d1 -= c1 ? n.radix[1] : 0;
+    hk += n.step[2] + c1;
+    const int c2 = hk >= n.radix[2];
+    hk -= c2 ? n.radix[2] : 0;
+    b += n.step[3] + c2;
+  }
+};
+
 // The batch's number of keys; -1 when it is out of range (treated as none).
 __device__ __forceinline__ int length_of(const Shape& s, int b) {
   if (!s.lens) return s.Sk;

@@ -37,7 +37,7 @@ struct FwdArgs {
   float* part_o;             // splits > 1: [split][group][tile][DT / 8][128][8]
   float* part_l;             //             [split][group][tile][128] LSE in log2 units
   int pairs, splits, kper;   // pairs of row tiles a group; key ranges, key tiles a range
-  int units;
+  Units units;
   float scale_log2;
   int* status;
   long long timeout_ns;
@@ -67,41 +67,42 @@ struct FwdLay {
 
 constexpr int kFwdThreads = 640;
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kFwdRegsLaunch = 96, kFwdRegsCtrl = 64, kFwdRegsSoftmax = 104;
+constexpr int kFwdRegsLaunch = 96, kFwdRegsCtrl = 32, kFwdRegsSoftmax = 112;
 static_assert(kFwdRegsCtrl + 4 * kFwdRegsSoftmax == 5 * kFwdRegsLaunch,
               "the five warpgroups must share exactly the launch's registers");
 
-// A CTA's units: u, u + grid, ... Every role walks the same ones.
-// ALL: a whole warp walks together.
+// A CTA's units, [batch][key head][pair][split]. Every role walks the same ones. ALL: a whole warp
+// walks together.
 template <bool ALL = false>
 struct FwdWalk {
   const FwdArgs* a;
-  int b, u, bh, hk, pair, split;
+  Place at;                  // d0: key range, d1: pair of row tiles
+  int known;                 // the batch whose length is at hand (-2: not begun)
   int len;                   // the batch's keys (-1: out of range)
   int t0, nt;                // first key tile and their number in this range
   bool has_b;
-  __device__ __forceinline__ FwdWalk(const FwdArgs& args) : a(&args), b(-1), u((int)blockIdx.x - (int)gridDim.x) {}
+  __device__ __forceinline__ FwdWalk(const FwdArgs& args) : a(&args), at(args.units), known(-2) {}
   __device__ __forceinline__ bool next() {
     const FwdArgs& p = *a;
-    u += gridDim.x;
-    if (u >= p.units) return false;
-    split = u % p.splits;
-    const int r = u / p.splits;
-    pair = r % p.pairs;
-    bh = r / p.pairs;
-    const int batch = bh / p.s.Hk;
-    hk = bh - batch * p.s.Hk;
-    has_b = 2 * pair + 1 < p.s.ntile;
-    if (batch != b) {                              // else its length is known
-      b = batch;
-      len = length_of(p.s, b);
+    if (known == -2) known = -1;
+    else at.next(p.units);
+    if (!at.more(p.units)) return false;
+    has_b = 2 * at.d1 + 1 < p.s.ntile;
+    if (at.b != known) {
+      known = at.b;
+      len = length_of(p.s, known);
       if (ALL) len = same(len);
     }
-    t0 = split * p.kper;
+    t0 = at.d0 * p.kper;
     const int all = (max(len, 0) + kTile - 1) / kTile;
     nt = max(0, min(all, t0 + p.kper) - t0);
     return true;
   }
+  // The keys of a place's range (none: 0 or less).
+  __device__ static __forceinline__ int keys_in_range(const FwdArgs& p, const Place& at) {
+    return min(length_of(p.s, at.b) - at.d0 * p.kper * kTile, p.kper * kTile);
+  }
+  __device__ __forceinline__ int group() const { return at.b * a->s.Hk + at.hk; }
   // Keys of key tile t of this range, and how many 32-column chunks they take.
   __device__ __forceinline__ int keys(int t) const { return min(kTile, len - (t0 + t) * kTile); }
   __device__ __forceinline__ int chunks(int t) const { return (keys(t) + 31) >> 5; }
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (nqx[x] > 0) ok = ptx::mbar_wait(bars + L::Q_EMPTY + x, (nqx[x] - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::mbar_expect_tx(bars + L::Q_FULL + x, row_tile_bytes<DT>(p.s));
-          load_row_tile<DT>(p.s, &maps.q, sm + L::Q_OFF + x * L::TILE, w.b, w.hk, 2 * w.pair + x, p.s.q_b, p.s.q_h,
+          load_row_tile<DT>(p.s, &maps.q, sm + L::Q_OFF + x * L::TILE, w.at.b, w.at.hk, 2 * w.at.d1 + x, p.s.q_b, p.s.q_h,
                             bars + L::Q_FULL + x);
           ++nqx[x];
         }
@@ -185,19 +186,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         FwdWalk<> ahead = w;
         if (ahead.next() && ahead.nt > 0)
           for (int x = 0; x < (ahead.has_b ? 2 : 1); ++x)
-            prefetch_row_tile<DT>(p.s, &maps.q, ahead.b, ahead.hk, 2 * ahead.pair + x, p.s.q_b, p.s.q_h);
+            prefetch_row_tile<DT>(p.s, &maps.q, ahead.at.b, ahead.at.hk, 2 * ahead.at.d1 + x, p.s.q_b, p.s.q_h);
         for (int t = 0; ok && t < (p.withhold ? 0 : w.nt); ++t) {
           const int ks = nk % L::KST, km = nk / L::KST, vs = nv % L::VST, vm = nv / L::VST;
           if (km > 0) ok = ptx::mbar_wait(bars + L::K_EMPTY + ks, (km - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::mbar_expect_tx(bars + L::K_FULL + ks, L::TILE);
-          load_key_tile<DT>(&maps.k, sm + L::K_OFF + ks * L::TILE, w.b, w.hk, w.t0 + t, p.s.k_b, p.s.k_h,
+          load_key_tile<DT>(&maps.k, sm + L::K_OFF + ks * L::TILE, w.at.b, w.at.hk, w.t0 + t, p.s.k_b, p.s.k_h,
                             bars + L::K_FULL + ks);
           ++nk;
           if (vm > 0) ok = ptx::mbar_wait(bars + L::V_EMPTY + vs, (vm - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::mbar_expect_tx(bars + L::V_FULL + vs, L::TILE);
-          load_key_tile<DT>(&maps.v, sm + L::V_OFF + vs * L::TILE, w.b, w.hk, w.t0 + t, p.s.v_b, p.s.v_h,
+          load_key_tile<DT>(&maps.v, sm + L::V_OFF + vs * L::TILE, w.at.b, w.at.hk, w.t0 + t, p.s.v_b, p.s.v_h,
                             bars + L::V_FULL + vs);
           ++nv;
         }
@@ -327,17 +328,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     float* mine = (float*)(sm + L::EX_OFF) + (x * 2 + half) * kTile + r;
     const float* other = (const float*)(sm + L::EX_OFF) + (x * 2 + 1 - half) * kTile + r;
     const int pair_bar = 1 + x * 4 + quarter;      // the two warps' named barrier
-    FwdWalk<> w(p);
+    // (Registers are short here, and a spilled one costs more than a length read again: of the walk
+    // only the place is kept, and of its keys how many are left.)
+    Place at(p.units);
     int steps = 0;                                 // key tiles so far: parity of this tile's barriers
     bool ok = true;
-    while (w.next()) {
-      if (x && !w.has_b) continue;
+    for (; at.more(p.units); at.next(p.units)) {
+      if (x && 2 * at.d1 + 1 >= p.s.ntile) continue;
       float m = -INFINITY, l = 0.f;                // of the row; of this half
+      bool first = true;                           // key tile of the unit
       // A warp whose wait ran out goes on without work, as its partner must find it at every meeting.
-      for (int t = 0; t < w.nt; ++t, ++steps) {
+      for (int left = FwdWalk<>::keys_in_range(p, at); left > 0; left -= kTile, ++steps) {
         if (ok) ok = ptx::warp_wait(bars + L::S_FULL + x, steps & 1, abort_flag, tmo);
         ptx::tc_fence_after();
-        const int keys = w.keys(t) - 64 * half;    // of this half
+        const int keys = min(left, kTile) - 64 * half;   // of this half
         uint32_t sc[2][32];
         float mx = -INFINITY;
         if (ok) {
@@ -352,9 +356,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int c = 0; c < 2; ++c) {
             if (32 * c < keys) {
               if (32 * c + 32 > keys) {            // the sequence ends in this chunk
+                const uint32_t there = (1u << (keys - 32 * c)) - 1u;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (32 * c + i >= keys) sc[c][i] = 0xff800000u;
+                  if (!(there >> i & 1u)) sc[c][i] = 0xff800000u;
               }
 #pragma unroll
               for (int i = 0; i < 32; i += 2)
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float m_new = moved ? m_row : m;
         // P's columns, and O where it is rescaled, are the last product's until that is done (DT = 128: it
         // was, before this S)
-        if (L::kSepP && t > 0) {
+        if (L::kSepP && !first) {
           ok = ptx::warp_wait(bars + L::PV_DONE + x, (steps - 1) & 1, abort_flag, tmo);
           if (!ok) continue;
           ptx::tc_fence_after();
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float alpha = moved ? ptx::ex2(m - m_new) : 1.f;
         l = l * alpha + (lt0 + lt1);
         m = m_new;
-        if (t > 0 && __any_sync(0xffffffffu, moved)) {
+        if (!first && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int i = 0; i < DT / 2; i += 32) {
             const int c0 = half * (DT / 2) + i;
@@ -418,12 +423,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
           }
         }
+        first = false;
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bars + L::P_FULL + x);
       }
-      if (w.nt > 0) {
+      const int len = length_of(p.s, at.b);
+      const bool none = FwdWalk<>::keys_in_range(p, at) <= 0;   // no key: O = 0, LSE = -inf
+      if (!none) {
         if (ok) ok = ptx::warp_wait(bars + L::PV_DONE + x, (steps - 1) & 1, abort_flag, tmo);
         ptx::tc_fence_after();
         // the row's sum; the maxima in these places have been read, as above
@@ -433,19 +441,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ptx::named_bar(pair_bar, 64);
       }
       int token, head;
-      const int tile = 2 * w.pair + x;
+      const int tile = 2 * at.d1 + x, group = at.b * p.s.Hk + at.hk;
       const bool live = row_of(p.s, tile, r, token, head);
-      const bool none = w.nt == 0;                 // no key: O = 0, LSE = -inf (NaN for a bad length)
-      const bool bad = !ok || w.len < 0;
+      const bool bad = !ok || len < 0;             // NaN for a bad length
       const float inv = bad ? NAN : none ? 0.f : 1.f / l;
       const float l2 = bad ? NAN : none ? -INFINITY : m + __log2f(l);
-      const size_t row = (((size_t)w.split * p.s.B * p.s.Hk + w.bh) * p.s.ntile + tile) * kTile + r;
-      const int h = w.hk * p.s.g + head;
+      const size_t row = (((size_t)at.d0 * p.s.B * p.s.Hk + group) * p.s.ntile + tile) * kTile + r;
+      const int h = at.hk * p.s.g + head;
       if (live && half == 0) {
         if (p.splits > 1) p.part_l[row] = l2;
-        else p.lse[((size_t)w.b * p.s.Hq + h) * p.s.Sq + token] = l2 * kLn2;
+        else p.lse[((size_t)at.b * p.s.Hq + h) * p.s.Sq + token] = l2 * kLn2;
       }
-      __nv_bfloat16* dst = p.o + (((size_t)w.b * p.s.Sq + token) * p.s.Hq + h) * p.s.D;
+      __nv_bfloat16* dst = p.o + (((size_t)at.b * p.s.Sq + token) * p.s.Hq + h) * p.s.D;
 #pragma unroll
       for (int i = 0; i < DT / 2; i += 32) {
         const int c0 = half * (DT / 2) + i;
@@ -463,7 +470,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       // O has been read: the next unit's P V may replace it, which waits for this warp's P
       ptx::tc_fence_before();
-      if (w.len < 0 && w.pair == 0 && x == 0 && half == 0 && r == 0 && p.status) atomicCAS(p.status, 0, kStatusBounds);
+      if (len < 0 && at.d1 == 0 && x == 0 && half == 0 && r == 0 && p.status) atomicCAS(p.status, 0, kStatusBounds);
     }
   }
 

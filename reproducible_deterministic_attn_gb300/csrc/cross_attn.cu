@@ -171,8 +171,8 @@ void set_places(Shape* s, const long long* qs, const long long* ks, const long l
 Units make_units(const Shape& s, int d0, int d1, int sms, int* grid) {
   Units n = {};
   n.radix[0] = d0;
-  n.radix[1] = d1;
-  n.radix[2] = s.Hk;
+  n.radix[1] = s.Hk;
+  n.radix[2] = d1;
   n.batches = s.B;
   const long long all = (long long)d0 * d1 * s.Hk * s.B;
   *grid = (int)std::min<long long>(all, sms);

@@ -90,7 +90,7 @@ enum {
 };
 static_assert(8 * C_COUNT + 8 <= 256, "barrier area");
 
-// A CTA's tasks: of each of its units, [batch][key head][row segment][key tile], the row tiles. ALL: a
+// A CTA's tasks: of each of its units, [batch][row segment][key head][key tile], the row tiles. ALL: a
 // whole warp walks together.
 template <bool ALL = false>
 struct KeysWalk {
@@ -313,11 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                           bars + C_DO_FULL + ob);
         ++loaded;
         ++it;
-        // ask for the tiles after the buffered ones, so that they wait in L2
-        if (w.j + L::NDO < w.nqt) {
-          prefetch_row_tile<DT>(p.s, &maps.q, w.at.b, w.at.hk, w.tile() + L::NDO, p.s.q_b, p.s.q_h);
-          prefetch_row_tile<DT>(p.s, &maps.dO, w.at.b, w.at.hk, w.tile() + L::NDO, 1, 1);
-        }
       }
       // drain: every issued load has landed before the CTA may exit
       for (int k = max(0, it - L::NQ); k < it; ++k)

@@ -10,10 +10,13 @@
 // keys). Key ranges (few row tiles against many keys) leave fp32 partials that
 // cross_join_rows_kernel adds in order.
 //
-// Warp roles (384 threads): 0 = TMA producer, 1 and 3 = MMA issuers (S; dP and
-// dQ), 2 = K rows behind a length, 4..11 =
-// softmax gradient (quarter = TMEM lanes = rows, half = 64 keys each) and the epilogue. Every wait
-// is bounded.
+// A unit of few key tiles (a text) lasts little longer than its ends, which the next one's copies run
+// under: Q's under the last dP, dO's under the last dQ (8192 x 512, 16 heads of 128: 94 us, before both
+// waited for the last dP, now 86; warps of their own for the read-out of dQ gained nothing).
+//
+// Warp roles (384 threads): 0 = TMA producer, 1 and 3 = MMA issuers (S; dP and dQ), 2 = K rows
+// behind a length, 4..11 = softmax gradient (quarter = TMEM lanes = rows, half = 64 keys each) and
+// the epilogue. Every wait is bounded.
 #pragma once
 
 #include "cross_bwd.cuh"
@@ -33,7 +36,7 @@ struct RowsLay {
   static constexpr int ALLOC = BAR_OFF + 512 + 1024;           // slack for 1024 alignment
   static_assert(ALLOC <= 232448, "shared memory budget");
   static constexpr int T_S = 0, T_DP = 256, T_DQ = 384;
-  static constexpr int Q_FULL = 0, DO_FULL = NB, Q_EMPTY = 2 * NB, S_FULL = 3 * NB, S_FREE = S_FULL + 2,
+  static constexpr int Q_FULL = 0, DO_FULL = NB, Q_EMPTY = 2 * NB, DO_EMPTY = 3 * NB, S_FULL = 4 * NB, S_FREE = S_FULL + 2,
                        DP_FULL = S_FREE + 2, DS_FULL = DP_FULL + 1, ACC_FULL = DS_FULL + 1,
                        ACC_EMPTY = ACC_FULL + 1, DRAIN = ACC_EMPTY + 1, K_FULL = DRAIN + 2,
                        V_FULL = K_FULL + KST, K_EMPTY = V_FULL + VST, V_EMPTY = K_EMPTY + KST,
@@ -45,7 +48,7 @@ constexpr int kRowsRegsLaunch = 168, kRowsRegsCtrl = 88, kRowsRegsSoftmax = 208;
 static_assert(kRowsRegsCtrl + 2 * kRowsRegsSoftmax == 3 * kRowsRegsLaunch,
               "the three warpgroups must share exactly the launch's registers");
 
-// A CTA's units, [batch][key head][row tile][key range]; those without keys are passed over
+// A CTA's units, [batch][row tile][key head][key range]; those without keys are passed over
 // (cross_pre_kernel writes their rows, and the join reads no range behind a length). ALL: a whole
 // warp walks together.
 template <bool ALL = false>
@@ -96,8 +99,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   if (threadIdx.x == 0) {
     for (int k = 0; k < L::COUNT; ++k) {
       const bool key = k >= L::K_EMPTY && k < L::V_EMPTY;   // the products, and warp 2
-      const bool two_of = (key && p.s.lens) || (k >= L::Q_EMPTY && k < L::S_FULL);          // both issuers
-      ptx::mbar_init(bars + k, k == L::DS_FULL || k == L::ACC_EMPTY ? 8 : two_of ? 2 : 1);
+      ptx::mbar_init(bars + k, k == L::DS_FULL || k == L::ACC_EMPTY ? 8 : key && p.s.lens ? 2 : 1);
     }
     *abort_flag = 0;
     ptx::fence_barrier_init();
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (warp == 0 && lane == 0) {
       // ===================================== TMA producer =====================================
       RowsWalk<> w(p);
-      int n = 0, kv = 0, nk = 0;                   // units, key tiles (V), K tiles so far
+      int n = 0, kv = 0, nk = 0, nd = 0;           // units, key tiles (V), K tiles, dO tiles so far
       bool ok = !p.withhold;
       while (ok && w.next()) {
         const int b = n % L::NB;
@@ -123,15 +125,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         uint8_t* q = sm + L::Q_OFF + 2 * b * L::TILE;
         ptx::mbar_expect_tx(bars + L::Q_FULL + b, row_tile_bytes<DT>(p.s));
         load_row_tile<DT>(p.s, &maps.q, q, w.at.b, w.at.hk, w.at.d1, p.s.q_b, p.s.q_h, bars + L::Q_FULL + b);
-        ptx::mbar_expect_tx(bars + L::DO_FULL + b, row_tile_bytes<DT>(p.s));
-        load_row_tile<DT>(p.s, &maps.dO, q + L::TILE, w.at.b, w.at.hk, w.at.d1, 1, 1, bars + L::DO_FULL + b);
-        ++n;
-        // the next unit's rows wait in L2
-        RowsWalk<> ahead = w;
-        if (ahead.next()) {
-          prefetch_row_tile<DT>(p.s, &maps.q, ahead.at.b, ahead.at.hk, ahead.at.d1, p.s.q_b, p.s.q_h);
-          prefetch_row_tile<DT>(p.s, &maps.dO, ahead.at.b, ahead.at.hk, ahead.at.d1, 1, 1);
-        }
         for (int t = 0; ok && t < w.nt; ++t, ++kv) {
           const int ks = kv % L::KST, km = kv / L::KST, vs = kv % L::VST, vm = kv / L::VST;
           if (km > 0) ok = ptx::mbar_wait(bars + L::K_EMPTY + ks, (km - 1) & 1, abort_flag, tmo);
@@ -140,18 +133,28 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           load_key_tile<DT>(&maps.k, sm + L::K_OFF + ks * L::TILE, w.at.b, w.at.hk, w.t0 + t, p.s.k_b, p.s.k_h,
                             bars + L::K_FULL + ks);
           ++nk;
+          if (t == 0) {
+            // Q is free before dO is (the last S goes ahead of the last dP), so that the next unit's
+            // first S is there when this one's rows have left
+            if (n >= L::NB) ok = ptx::mbar_wait(bars + L::DO_EMPTY + b, (n / L::NB - 1) & 1, abort_flag, tmo);
+            if (!ok) break;
+            ptx::mbar_expect_tx(bars + L::DO_FULL + b, row_tile_bytes<DT>(p.s));
+            load_row_tile<DT>(p.s, &maps.dO, q + L::TILE, w.at.b, w.at.hk, w.at.d1, 1, 1, bars + L::DO_FULL + b);
+            ++nd;
+          }
           if (vm > 0) ok = ptx::mbar_wait(bars + L::V_EMPTY + vs, (vm - 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::mbar_expect_tx(bars + L::V_FULL + vs, L::TILE);
           load_key_tile<DT>(&maps.v, sm + L::V_OFF + vs * L::TILE, w.at.b, w.at.hk, w.t0 + t, p.s.v_b, p.s.v_h,
                             bars + L::V_FULL + vs);
         }
+        ++n;
       }
       // drain: every issued load has landed before the CTA may exit
-      for (int k = max(0, n - L::NB); k < n; ++k) {
+      for (int k = max(0, n - L::NB); k < n; ++k)
         ptx::mbar_drain(bars + L::Q_FULL + k % L::NB, (k / L::NB) & 1, 100000000ll);
+      for (int k = max(0, nd - L::NB); k < nd; ++k)
         ptx::mbar_drain(bars + L::DO_FULL + k % L::NB, (k / L::NB) & 1, 100000000ll);
-      }
       for (int k = max(0, nk - L::KST); k < nk; ++k)
         ptx::mbar_drain(bars + L::K_FULL + k % L::KST, (k / L::KST) & 1, 100000000ll);
       for (int k = max(0, kv - L::VST); k < kv; ++k)
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                            ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps, one);
           commit(bars + L::DP_FULL, one);
           commit(bars + L::V_EMPTY + s, one);
-          if (t == w.nt - 1) commit(bars + L::Q_EMPTY + b, one);
+          if (t == w.nt - 1) commit(bars + L::DO_EMPTY + b, one);
           return true;
         };
         ok = ptx::warp_wait(bars + L::DO_FULL + b, (n / L::NB) & 1, abort_flag, tmo) && issue_dp(0);
@@ -266,10 +269,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const uint32_t lane_addr = ((uint32_t)(quarter * 32) << 16);
     RowsWalk<> w(p);
     int n = 0, k = 0;                              // units, key tiles so far
-    bool ok = true;
-    while (ok && w.next()) {
+    bool ok = true, more = w.next();
+    float nnl, delta;                              // the row's -LSE log2e and -Delta
+    auto fetch = [&]() {
       const size_t row = ((size_t)w.group() * p.s.ntile + w.at.d1) * kTile + r;
-      const float nnl = __ldg(p.nnl + row), delta = __ldg(p.delta + row);   // -LSE log2e, -Delta
+      nnl = __ldg(p.nnl + row);
+      delta = __ldg(p.delta + row);
+    };
+    if (more) fetch();
+    while (ok && more) {
       const uint64_t scale2 = two(p.scale_log2, p.scale_log2), nnl2 = two(nnl, nnl), delta2 = two(delta, delta);
       for (int t = 0; t < w.nt; ++t, ++k) {
         const uint32_t t_s = tmem + lane_addr + L::T_S + 128 * (k & 1) + col0;
@@ -324,6 +332,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const bool live = row_of(p.s, w.at.d1, r, token, head);
       __nv_bfloat16* dst = p.dq + w.at.b * p.dq_b + token * p.dq_s + (w.at.hk * p.s.g + head) * p.dq_h;
       float* part = p.dq_part + ((((size_t)w.at.d0 * p.s.B * p.s.Hk + w.group()) * p.s.ntile + w.at.d1) * kTile) * DT;
+      more = w.next();
+      if (more) fetch();                           // the next unit's, while this one's rows leave
 #pragma unroll
       for (int i = 0; i < DT / 2; i += 32) {
         const int c0 = half * (DT / 2) + i;

@@ -71,7 +71,7 @@ constexpr int kFwdRegsLaunch = 96, kFwdRegsCtrl = 32, kFwdRegsSoftmax = 112;
 static_assert(kFwdRegsCtrl + 4 * kFwdRegsSoftmax == 5 * kFwdRegsLaunch,
               "the five warpgroups must share exactly the launch's registers");
 
-// A CTA's units, [batch][key head][pair][split]. Every role walks the same ones. ALL: a whole warp
+// A CTA's units, [batch][pair][key head][split]. Every role walks the same ones. ALL: a whole warp
 // walks together.
 template <bool ALL = false>
 struct FwdWalk {
@@ -182,11 +182,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             bars + L::Q_FULL + x);
           ++nqx[x];
         }
-        // the next unit's rows wait in L2
-        FwdWalk<> ahead = w;
-        if (ahead.next() && ahead.nt > 0)
-          for (int x = 0; x < (ahead.has_b ? 2 : 1); ++x)
-            prefetch_row_tile<DT>(p.s, &maps.q, ahead.at.b, ahead.at.hk, 2 * ahead.at.d1 + x, p.s.q_b, p.s.q_h);
         for (int t = 0; ok && t < (p.withhold ? 0 : w.nt); ++t) {
           const int ks = nk % L::KST, km = nk / L::KST, vs = nv % L::VST, vm = nv / L::VST;
           if (km > 0) ok = ptx::mbar_wait(bars + L::K_EMPTY + ks, (km - 1) & 1, abort_flag, tmo);

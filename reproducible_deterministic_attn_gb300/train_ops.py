@@ -325,7 +325,8 @@ def qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions=None, eps: float = 1e
     if dev != _current_device():
         with torch.cuda.device(dev):
             return qk_norm_rope_forward(q, k, wq, wk, cos, sin, positions, eps, interleaved, status)
-    q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     _raise(_core.load().dash_qk_norm_rope_fwd(
         q.data_ptr(), k.data_ptr(), *tables, q_out.data_ptr(), k_out.data_ptr(), _status_word(status, dev),
         *sizes, stride, eps, interleaved, _DTYPE[q.dtype], bits, _stream(dev)), "dash_qk_norm_rope_fwd")
@@ -353,18 +354,18 @@ def _qk_grads(dq_out, dk_out, q, k, wq, wk, sizes, dq, dk, workspace, dev):
             or dk_out.get_device() != dev):
         _bad(f"dq_out and dk_out: expected contiguous, of the type and shape of q and k, on cuda:{dev}")
     if dq is None:
-        dq = q.new_empty(qshape)
+        dq = torch.empty(qshape, dtype=q.dtype, device=q.device)
     if dk is None:
-        dk = k.new_empty(kshape)
+        dk = torch.empty(kshape, dtype=k.dtype, device=k.device)
     dqn, dkn = _heads(dq, "dq", dtype, dev), _heads(dk, "dk", dtype, dev)
     if dqn[:4] != qshape or dkn[:4] != kshape:
         _bad("dq and dk: expected the shapes of q and k")
     dwq = pdwq = dwk = pdwk = None
     if wq is not None:
-        dwq = wq.new_empty(D)
+        dwq = torch.empty(D, dtype=_F32, device=q.device)
         pdwq = dwq.data_ptr()
     if wk is not None:
-        dwk = wk.new_empty(D)
+        dwk = torch.empty(D, dtype=_F32, device=q.device)
         pdwk = dwk.data_ptr()
     if workspace is None:
         workspace = new_qk_norm_rope_workspace(*sizes[:5], q.device)
@@ -449,7 +450,8 @@ def qk_norm_rope_axes_forward(q, k, wq, wk, cos, sin, positions, sections, eps: 
     if dev != _current_device():
         with torch.cuda.device(dev):
             return qk_norm_rope_axes_forward(q, k, wq, wk, cos, sin, positions, sections, eps, interleaved, status)
-    q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     _raise(_core.load().dash_qk_norm_rope_axes_fwd(
         q.data_ptr(), k.data_ptr(), *tables, q_out.data_ptr(), k_out.data_ptr(), _status_word(status, dev),
         *sizes, *ax, eps, interleaved, _DTYPE[q.dtype], bits, _stream(dev)), "dash_qk_norm_rope_axes_fwd")

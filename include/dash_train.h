@@ -1,8 +1,10 @@
 /*
  * dash_train.h -- C ABI of the operators around the attention in a training step whose
  * results are reproducible: token embedding and its gradient, the norm and rotation of
- * queries and keys, the cross entropy of a large vocabulary with its gradient, and gradient
- * clipping. Built into the same library as dash_attn.h, whose status codes they return.
+ * queries and keys (by one position a token or one on each of several axes), the cross entropy
+ * of a large vocabulary with its gradient, gradient clipping, group norm with an activation, and
+ * attention to states of another length. Built into the same library as dash_attn.h, whose
+ * status codes they return.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -14,7 +16,7 @@
  * - Calls are asynchronous on `stream`, may be captured into a graph, and return argument
  *   errors synchronously with nothing queued. Workspaces are 256-byte aligned, need no
  *   initialisation, and must not be shared by calls that may overlap.
- * - Indexes read on the device (token ids, positions, targets) are checked there: one out
+ * - Indexes read on the device (token ids, positions, targets, lengths) are checked there: one out
  *   of range is never used as an address. The call's status -- dash_attn_get_status on the
  *   workspace, or the optional `status` word of a call without one -- then reads
  *   DASH_ERR_BOUNDS, and what the row yields is said at the call.

@@ -1,6 +1,5 @@
 // Host side of cross attention (dash_cross_attn_*): argument checks, how the work is cut, tensor
-// maps and launches. The kernels are in cross_fwd.cuh, cross_bwd.cuh
-// and cross_bwd_rows.cuh.
+// maps and launches. The kernels are in cross_fwd.cuh, cross_bwd.cuh and cross_bwd_rows.cuh.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -213,9 +212,9 @@ bool distinct(const long long* st, int B, int S, int H) {
 // SMs idle, so each is the cheapest by a count of tasks of 128 x 128 scores: a unit takes its tasks
 // and `start` more, units run in rounds of the chip, and partials cost what memory takes for them (a
 // task is about 2 us, in which the chip moves 10 MB). Where batches have lengths of their own, which
-// the host does not know, a fifth of the units is taken to be empty. A row segment has at most 128 row tiles: the
-// tensor core truncates its additions, which over 16384 rows of one sign loses at most 2^-15.5 of a
-// sum.
+// the host does not know, a fifth of the units is taken to be empty. A row segment has at most 128
+// row tiles: the tensor core truncates its additions, which over 16384 rows of one sign loses at
+// most 2^-15.5 of a sum.
 int best_cut(long long units, int tasks, int least, double start, double part_bytes, bool ragged) {
   int cut = least;
   double best = 1e300;

@@ -8,7 +8,8 @@
 // S(t+1) is computed while the softmax gradient works on t, dP(t+1) goes ahead of dQ(t), S(t+2)
 // follows dQ(t). LSE and Delta are one number a thread here, as a thread owns a row (and half of the
 // keys). Key ranges (few row tiles against many keys) leave fp32 partials that
-// cross_join_rows_kernel adds in order.
+// cross_join_rows_kernel adds in order. A key tile takes 1 us, where the products take 1536 cycles
+// and shared memory 1800 (two products with both operands there, K and V copied in).
 //
 // A unit of few key tiles (a text) lasts little longer than its ends, which the next one's copies run
 // under: Q's under the last dP, dO's under the last dQ (8192 x 512, 16 heads of 128: 94 us, before both

@@ -14,7 +14,9 @@
 //  - in passes: blocks of rows sum into a workspace, a small kernel joins, blocks of rows apply. x is
 //    read twice, the second time from L2 as far as it is still there: the second pass runs
 //    backwards through the tensor.
-// Both are bound by memory, the backward's activation by instructions next.
+// Both are bound by memory, the backward's activation by instructions next: 2 x 65536 x 512 bf16 (in
+// passes) takes 67 us forward, where 403 MB take 60, and 118 backward, where 671 MB take 99 (sums 55
+// for 40: the activation's derivative; apply 59); 4 x 4096 x 512 takes 13 (resident) and 30.
 #include <algorithm>
 #include <climits>
 

@@ -16,7 +16,9 @@
 // all the time without registers; a token's angles are loaded once for all its heads.
 // With several axes (AXES) a token has a position for each, and every pair of columns turns by the
 // angle of its axis' position: the rows of the angles' tables differ from pair to pair, which only
-// the loads of a token's angles see (16 bytes at a time where four pairs share an axis).
+// the loads of a token's angles see (16 bytes at a time where four pairs share an axis): 252 us for
+// both directions of the size above, of it 159 backward, where one axis takes 140. The wait for the
+// positions and then the table is what is longer there.
 #pragma once
 
 #include <algorithm>

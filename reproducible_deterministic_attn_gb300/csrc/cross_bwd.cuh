@@ -12,12 +12,13 @@
 //   dK   += dS^T Q             M = 128 keys, N = D, K = 128 rows, A from TMEM  [256 + DT, +DT)
 // dK and dV stay in TMEM over the unit's row tiles. S(t+1) waits for dV(t) (it overwrites P), dP(t+1)
 // for dK(t): two chains, each with an issuer of its own, that only the softmax gradient ties together.
-// The exponentials of the next task run under this one's dK and dP, its dS under dV and the next S.
+// The softmax warps go through exp(t), dS(t), exp(t+1) and would wait for S(t+1), so dK(t) gets in line
+// behind dV(t) and S(t+1) (issued as soon as dS(t) is there: 2550 us in place of 2410 below).
 // Units of one key tile leave fp32 partials of dK and dV, which cross_join_keys_kernel adds in order.
-// A task takes 1.87 us (3500 cycles; 64 of them 119 us) where its products take 2048 and shared memory
-// 2300: the rest is the way from product to softmax and back in each chain. P^T in shared memory, which frees
-// S's columns as soon as they are read, made tasks longer (8192 x 8192 x 128, 32 heads, both kernels:
-// 2956 us, so 2630): it adds a fifth to what shared memory moves.
+// A task takes 2600 cycles, 2048 of them products: from P(t) on, 100 until its issuer sees it, dV 700,
+// S 750, the exponentials 950. 8192 x 8192 x 128, 32 heads, both kernels: 2410 us, 1142 TFLOP/s. P^T in
+// shared memory, which frees S's columns as soon as they are read, gained nothing: shared memory has
+// to carry the operands of the products already.
 //
 // Where a group has one key tile (up to 128 keys: a caption) the same kernel forms dQ too (DQ), as
 // nothing has to be summed over key tiles: dS^T also goes to shared memory, [key][row], and
@@ -67,7 +68,7 @@ struct KeysLay {
   static constexpr int TILE = kTile * DT * 2;
   static constexpr int DS_BYTES = DQ ? kTile * kTile * 2 : 0;
   static constexpr int OFFS = 2 * kTile * 4;                   // -LSE log2e and -Delta of a row tile
-  static constexpr int NQ = DT == 64 ? 3 : 2, NDO = 2;
+  static constexpr int NQ = DT == 64 || !DQ ? 3 : 2, NDO = DT == 64 ? 3 : 2;
   static constexpr int K_OFF = 0, V_OFF = TILE, Q_OFF = 2 * TILE;
   static constexpr int DO_OFF = Q_OFF + NQ * TILE;
   static constexpr int DS_OFF = DO_OFF + NDO * TILE;
@@ -75,7 +76,7 @@ struct KeysLay {
   static constexpr int ZERO_OFF = DS_OFF + DS_BYTES;
   static constexpr int ZERO_BYTES = DQ && DT == 64 ? TILE : 0;
   static constexpr int OFFS_OFF = ZERO_OFF + ZERO_BYTES;
-  static constexpr int BAR_OFF = OFFS_OFF + NQ * OFFS;
+  static constexpr int BAR_OFF = OFFS_OFF + NDO * OFFS;       // (they come and go with dO)
   static constexpr int ALLOC = BAR_OFF + 256;                  // the base is 1024-aligned (checked)
   static_assert(ALLOC <= 232448, "shared memory budget");
   // DT = 64 leaves columns for dQ^T of its own; DT = 128 puts it where dP^T was
@@ -89,8 +90,8 @@ struct KeysLay {
 
 enum {
   C_KV_FULL = 0, C_KV_READY, C_KV_EMPTY, C_Q_FULL, C_Q_EMPTY = C_Q_FULL + 3, C_DO_FULL = C_Q_EMPTY + 3,
-  C_DO_EMPTY = C_DO_FULL + 2, C_S_FULL = C_DO_EMPTY + 2, C_SP_FREE, C_DP_FREE, C_P_FULL, C_DP_FULL, C_DS_FULL,
-  C_DQ_FULL, C_DQ_EMPTY, C_ACC_FULL, C_ACC_EMPTY, C_DRAIN, C_COUNT = C_DRAIN + 2
+  C_DO_EMPTY = C_DO_FULL + 3, C_S_FULL = C_DO_EMPTY + 3, C_SP_FREE, C_DP_FREE, C_P_FULL, C_DP_FULL, C_DS_FULL,
+  C_DQ_FULL, C_DQ_EMPTY, C_ACC_FULL, C_ACC_EMPTY, C_TURN, C_DRAIN = C_TURN + 2, C_COUNT = C_DRAIN + 2
 };
 static_assert(8 * C_COUNT + 8 <= 256, "barrier area");
 
@@ -256,9 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int k = 0; k < C_COUNT; ++k) {
-      const bool both = (DQ && k == C_SP_FREE) || k == C_KV_EMPTY || k == C_ACC_FULL || k == C_DO_EMPTY ||
-                        k == C_DO_EMPTY + 1;         // issuers
-      const int n = k == C_P_FULL || k == C_DS_FULL ? 8 : k == C_DQ_EMPTY || k == C_ACC_EMPTY ? 4 : both ? 2 : 1;
+      const bool both = (DQ && k == C_SP_FREE) || k == C_KV_EMPTY || k == C_ACC_FULL;   // issuers
+      const bool rows = k >= C_DO_EMPTY && k < C_S_FULL;   // issuers and softmax-gradient warps
+      const int n = k == C_P_FULL || k == C_DS_FULL ? 8 : k == C_DQ_EMPTY || k == C_ACC_EMPTY ? 4 : rows ? 10 : both ? 2 : 1;
       ptx::mbar_init(bars + k, n);
     }
     *abort_flag = 0;
@@ -289,13 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qb = it % L::NQ;
         if (it >= L::NQ) ok = ptx::mbar_wait(bars + C_Q_EMPTY + qb, (it / L::NQ - 1) & 1, abort_flag, tmo);
         if (!ok) break;
-        const size_t row = ((size_t)w.group() * p.s.ntile + w.tile()) * kTile;
-        uint8_t* offs = sm + L::OFFS_OFF + qb * L::OFFS;
-        ptx::mbar_expect_tx(bars + C_Q_FULL + qb, row_tile_bytes<DT>(p.s) + L::OFFS);
+        ptx::mbar_expect_tx(bars + C_Q_FULL + qb, row_tile_bytes<DT>(p.s));
         load_row_tile<DT>(p.s, &maps.q, sm + L::Q_OFF + qb * L::TILE, w.at.b, w.at.hk, w.tile(), p.s.q_b, p.s.q_h,
                           bars + C_Q_FULL + qb);
-        ptx::bulk_load(offs, p.nnl + row, kTile * 4, bars + C_Q_FULL + qb);
-        ptx::bulk_load(offs + kTile * 4, p.delta + row, kTile * 4, bars + C_Q_FULL + qb);
         if (w.first_of_tile()) {
           if (tl > 0) ok = ptx::mbar_wait(bars + C_KV_EMPTY, (tl - 1) & 1, abort_flag, tmo);
           if (!ok) {
@@ -313,7 +310,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++it;
           break;
         }
-        ptx::mbar_expect_tx(bars + C_DO_FULL + ob, row_tile_bytes<DT>(p.s));
+        const size_t row = ((size_t)w.group() * p.s.ntile + w.tile()) * kTile;
+        uint8_t* offs = sm + L::OFFS_OFF + ob * L::OFFS;
+        ptx::mbar_expect_tx(bars + C_DO_FULL + ob, row_tile_bytes<DT>(p.s) + L::OFFS);
+        ptx::bulk_load(offs, p.nnl + row, kTile * 4, bars + C_DO_FULL + ob);
+        ptx::bulk_load(offs + kTile * 4, p.delta + row, kTile * 4, bars + C_DO_FULL + ob);
         load_row_tile<DT>(p.s, &maps.dO, sm + L::DO_OFF + ob * L::TILE, w.at.b, w.at.hk, w.tile(), 1, 1,
                           bars + C_DO_FULL + ob);
         ++loaded;
@@ -352,37 +353,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t ID_S = ptx::idesc_bf16(128, 128, 0, 0);
       const uint32_t id_ts = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
       constexpr uint32_t BUF_STEP = L::TILE >> 4;
+      // Every instruction between a product's end and the next one's start is time that the chain
+      // loses (with all of a task's waits there: 700 cycles, and 2630 us in place of 2410 at 8192 x
+      // 8192 x 128, 32 heads), so the walk and what else the next product waits for come before.
       KeysWalk<true> w(p);
       const uint32_t one = elect_one();
-      int it = 0, tile = -1;
-      bool ok = true;
+      int it = 0, tile = 0;                        // tasks and key tiles so far
+      bool ok = true, more = w.next();
       if (warp == 1) {
         const uint32_t dK_k = ptx::sdesc_lo(sK, 16), dQ_k = ptx::sdesc_lo(sQ, 16);
         const uint32_t ddO_mn = ptx::sdesc_lo(sdO, kTile * 128);
-        while (ok && w.next()) {
-          const bool first = w.first_of_tile(), last = w.last_of_tile();
-          const int qb = it % L::NQ, ob = it % L::NDO;
-          // ---- S^T(it), once Q(it) has landed and what lies over its columns has been read: P^T(it-1)
-          // by dV, with DQ also dS^T(it-1) by dK
-          if (first) ok = ptx::warp_wait(bars + C_KV_READY, ++tile & 1, abort_flag, tmo);
-          if (ok) ok = ptx::warp_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
-          if (ok && it > 0) ok = ptx::warp_wait(bars + C_SP_FREE, (it - 1) & 1, abort_flag, tmo);
-          if (!ok) break;
+        // S^T(it), once Q(it) has landed and what lies over its columns has been read: P^T(it-1) by dV,
+        // with DQ also dS^T(it-1) by dK
+        auto issue_s = [&](bool landed) {
+          const int qb = it % L::NQ;
+          if (!landed) {
+            if (w.first_of_tile() && !ptx::warp_wait(bars + C_KV_READY, tile & 1, abort_flag, tmo)) return false;
+            if (!ptx::warp_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo)) return false;
+          }
+          if (it > 0 && !ptx::warp_wait(bars + C_SP_FREE, (it - 1) & 1, abort_flag, tmo)) return false;
           ptx::tc_fence_after();
           issue_scores<DT>(tmem + L::T_SP, dK_k, dQ_k + qb * BUF_STEP, ID_S, dsteps, one);
           commit(bars + C_S_FULL, one);
-          if (last) commit(bars + C_KV_EMPTY, one);
-          // ---- dV += P^T dO, once P^T(it) is stored and the last key tile's sums were read out
-          ok = ptx::warp_wait(bars + C_P_FULL, it & 1, abort_flag, tmo);
-          if (ok) ok = ptx::warp_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
+          if (!DQ && one) ptx::mbar_arrive(bars + C_TURN + (it & 1));
+          if (w.last_of_tile()) commit(bars + C_KV_EMPTY, one);
+          return true;
+        };
+        if (more) ok = issue_s(false);
+        while (ok && more) {
+          const bool first = w.first_of_tile(), last = w.last_of_tile();
+          const int ob = it % L::NDO;
+          more = w.next();
+          const bool landed = !last && is_complete(bars + C_Q_FULL + (it + 1) % L::NQ, ((it + 1) / L::NQ) & 1);
+          // dV += P^T dO, once P^T(it) is stored and the last key tile's sums were read out
+          ok = ptx::warp_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
           if (ok && first && tile > 0) ok = ptx::warp_wait(bars + C_ACC_EMPTY, (tile - 1) & 1, abort_flag, tmo);
+          if (ok) ok = ptx::warp_wait(bars + C_P_FULL, it & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::tc_fence_after();
           issue_rows<true>(tmem + L::T_DV, tmem + L::T_SP, ddO_mn + ob * BUF_STEP, id_ts, first ? 0u : 1u, 8, one);
           commit(bars + C_SP_FREE, one);
           commit(bars + C_DO_EMPTY + ob, one);
-          if (last) commit(bars + C_ACC_FULL, one);
+          if (last) {
+            commit(bars + C_ACC_FULL, one);
+            ++tile;
+          }
           ++it;
+          if (more) ok = issue_s(landed);
         }
       } else {
         const uint32_t dV_k = ptx::sdesc_lo(sV, 16), ddO_k = ptx::sdesc_lo(sdO, 16);
@@ -390,35 +407,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dKt_mn = ptx::sdesc_lo(sK, DT == 128 ? kTile * 128 : L::ZERO_OFF - L::K_OFF);
         const uint32_t dDS_mn = ptx::sdesc_lo(ptx::smem_u32(sm + L::DS_OFF), kTile * 128);
         constexpr uint32_t ID_DQ = ptx::idesc_bf16(128, 128, 1, 1);
-        while (ok && w.next()) {
-          const bool first = w.first_of_tile(), last = w.last_of_tile();
-          const int qb = it % L::NQ, ob = it % L::NDO, ksteps = (w.keys() + 15) >> 4;
-          // ---- dP^T(it), once dO(it) has landed and its columns are free: dS^T(it-1) read by dK, with
-          // DQ dQ^T(it-1) out of TMEM
-          if (first) ok = ptx::warp_wait(bars + C_KV_READY, ++tile & 1, abort_flag, tmo);
-          if (ok) ok = ptx::warp_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
-          if (ok && it > 0) {
-            if (!DQ) ok = ptx::warp_wait(bars + C_DP_FREE, (it - 1) & 1, abort_flag, tmo);
-            else if (!L::kSepDQ) ok = ptx::warp_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
+        // dP^T(it), once dO(it) has landed and its columns are free: dS^T(it-1) read by dK, with DQ
+        // dQ^T(it-1) out of TMEM
+        auto issue_dp = [&](bool landed) {
+          const int ob = it % L::NDO;
+          if (!landed) {
+            if (w.first_of_tile() && !ptx::warp_wait(bars + C_KV_READY, tile & 1, abort_flag, tmo)) return false;
+            if (!ptx::warp_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo)) return false;
           }
-          if (!ok) break;
+          if ((!DQ || !L::kSepDQ) && it > 0 &&
+              !ptx::warp_wait(bars + (DQ ? C_DQ_EMPTY : C_DP_FREE), (it - 1) & 1, abort_flag, tmo))
+            return false;
           ptx::tc_fence_after();
           issue_scores<DT>(tmem + L::T_DP, dV_k, ddO_k + ob * BUF_STEP, ID_S, dsteps, one);
           commit(bars + C_DP_FULL, one);
           commit(bars + C_DO_EMPTY + ob, one);
-          if (last && !DQ) commit(bars + C_KV_EMPTY, one);
-          // ---- dK += dS^T Q, once dS^T(it) is stored
-          ok = ptx::warp_wait(bars + C_DS_FULL, it & 1, abort_flag, tmo);
-          if (ok) ok = ptx::warp_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
+          if (w.last_of_tile() && !DQ) commit(bars + C_KV_EMPTY, one);
+          return true;
+        };
+        if (more) ok = issue_dp(false);
+        while (ok && more) {
+          const bool first = w.first_of_tile(), last = w.last_of_tile();
+          const int qb = it % L::NQ, ksteps = (w.keys() + 15) >> 4;
+          more = w.next();
+          const bool landed = !last && is_complete(bars + C_DO_FULL + (it + 1) % L::NDO, ((it + 1) / L::NDO) & 1);
+          // dK += dS^T Q, once dS^T(it) is stored
+          ok = ptx::warp_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo);
           if (ok && first && tile > 0) ok = ptx::warp_wait(bars + C_ACC_EMPTY, (tile - 1) & 1, abort_flag, tmo);
+          if (ok) ok = ptx::warp_wait(bars + C_DS_FULL, it & 1, abort_flag, tmo);
+          // The softmax waits for S^T(it+1) next, and that for dV(it): this chain's products get in line
+          // behind both, for the time that the exponentials take. (Two barriers in turn: S^T(it+3)
+          // cannot be issued before dP^T(it+1) is done.)
+          if (!DQ && ok && !last) ok = ptx::warp_wait(bars + C_TURN + ((it + 1) & 1), ((it + 1) >> 1) & 1, abort_flag, tmo);
           if (!ok) break;
           ptx::tc_fence_after();
           issue_rows<true>(tmem + L::T_DK, tmem + L::T_DS, dQ_mn + qb * BUF_STEP, id_ts, first ? 0u : 1u, 8, one);
           commit(bars + (DQ ? C_SP_FREE : C_DP_FREE), one);
-          commit(bars + C_Q_EMPTY + qb, one);
-          if (last) commit(bars + C_ACC_FULL, one);
           if (DQ) {
-            // ---- dQ^T = K^T dS^T
+            // dQ^T = K^T dS^T
             if (L::kSepDQ && it > 0) ok = ptx::warp_wait(bars + C_DQ_EMPTY, (it - 1) & 1, abort_flag, tmo);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -426,7 +452,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             commit(bars + C_DQ_FULL, one);
             if (last) commit(bars + C_KV_EMPTY, one);
           }
+          commit(bars + C_Q_EMPTY + qb, one);
+          if (last) {
+            commit(bars + C_ACC_FULL, one);
+            ++tile;
+          }
           ++it;
+          if (more) ok = issue_dp(landed);
         }
       }
       // drain: no MMA may be in flight when TMEM is released
@@ -444,13 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int it = 0;
     bool ok = true;
     while (ok && w.next()) {
-      const int qb = it % L::NQ;
-      // (the offsets beside Q were copied by TMA: their own barrier is waited for as well)
-      ok = ptx::warp_wait(bars + C_Q_FULL + qb, (it / L::NQ) & 1, abort_flag, tmo) &&
+      const int ob = it % L::NDO;
+      // (the offsets beside dO were copied by TMA: their own barrier is waited for as well)
+      ok = ptx::warp_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo) &&
            ptx::warp_wait(bars + C_S_FULL, it & 1, abort_flag, tmo);
       if (!ok) break;
       ptx::tc_fence_after();
-      const float* nnl = (const float*)(sm + L::OFFS_OFF + qb * L::OFFS) + col0;
+      const float* nnl = (const float*)(sm + L::OFFS_OFF + ob * L::OFFS) + col0;
       const float* delta = nnl + kTile;
       float pv[64];
       {
@@ -517,7 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (DQ) ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + C_DS_FULL);
+      if (lane == 0) {
+        ptx::mbar_arrive(bars + C_DS_FULL);
+        ptx::mbar_arrive(bars + C_DO_EMPTY + ob);   // the offsets are read
+      }
       ++it;
     }
   } else {

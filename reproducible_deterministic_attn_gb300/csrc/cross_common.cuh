@@ -125,6 +125,16 @@ __device__ __forceinline__ void load_key_tile(const CUtensorMap* map, uint8_t* d
     tma_load_4d(dst + cb * kTile * 128, map, cb * 64, hk * mul_h, t * kTile, b * mul_b, bar);
 }
 
+// Whether a phase is complete, without waiting; the warp agrees.
+__device__ __forceinline__ bool is_complete(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(done)
+               : "r"(ptx::smem_u32(bar)), "r"(parity)
+               : "memory");
+  return __all_sync(0xffffffffu, done) != 0;
+}
+
 // Products are issued by a warp that stays together, of whose lanes one (`one` != 0) issues: so
 // descriptors and barriers' addresses stay in uniform registers. Issued by a lone thread each step
 // moves its operands there one by one, among the softmax warps that share its scheduler: two

@@ -203,9 +203,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const int b = n % L::NB;
         const uint32_t ddO = ptx::sdesc_lo(sQ, 16) + (2 * b + 1) * TILE16;
         // dP(t): its columns were read when dS(t-1) was stored
-        auto issue_dp = [&](int t) {
+        auto issue_dp = [&](int t, bool landed) {
           const int k = k0 + t, s = k % L::VST;
-          if (!ptx::warp_wait(bars + L::V_FULL + s, (k / L::VST) & 1, abort_flag, tmo)) return false;
+          if (!landed && !ptx::warp_wait(bars + L::V_FULL + s, (k / L::VST) & 1, abort_flag, tmo)) return false;
           ptx::tc_fence_after();
           issue_scores<DT>(tmem + L::T_DP, ddO, ptx::sdesc_lo(sV, 16) + s * TILE16,
                            ptx::idesc_bf16(128, 16 * w.steps(t), 0, 0), dsteps, one);
@@ -214,17 +214,20 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           if (t == w.nt - 1) commit(bars + L::DO_EMPTY + b, one);
           return true;
         };
-        ok = ptx::warp_wait(bars + L::DO_FULL + b, (n / L::NB) & 1, abort_flag, tmo) && issue_dp(0);
+        ok = ptx::warp_wait(bars + L::DO_FULL + b, (n / L::NB) & 1, abort_flag, tmo) && issue_dp(0, false);
         for (int t = 0; ok && t < w.nt; ++t) {
           const int k = k0 + t, s = k % L::KST;
-          ok = ptx::warp_wait(bars + L::DS_FULL, k & 1, abort_flag, tmo);
-          if (ok) ok = ptx::warp_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
-          if (ok && t + 1 < w.nt) ok = issue_dp(t + 1);
+          // the rest of what the products wait for comes before, out of the way from dS to them
+          const int vk = k + 1, vs = vk % L::VST;
+          const bool landed = t + 1 < w.nt && is_complete(bars + L::V_FULL + vs, (vk / L::VST) & 1);
+          ok = ptx::warp_wait(bars + L::K_FULL + s, (k / L::KST) & 1, abort_flag, tmo);
           if (ok && t == 0 && n > 0) ok = ptx::warp_wait(bars + L::ACC_EMPTY, (n - 1) & 1, abort_flag, tmo);
           if (ok && t == w.nt - 1 && w.unclean(t)) {
             ok = ptx::warp_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);
             clean ^= 1u << s;
           }
+          if (ok) ok = ptx::warp_wait(bars + L::DS_FULL, k & 1, abort_flag, tmo);
+          if (ok && t + 1 < w.nt) ok = issue_dp(t + 1, landed);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t dK = ptx::sdesc_lo(sK + s * L::TILE, kTile * 128);

@@ -246,9 +246,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           k += w.nt;
           continue;
         }
-        auto issue_s = [&](int t) {
+        const bool take_turns = w.has_b && w.nt > 2;
+        auto issue_s = [&](int t, bool landed) {
           const int s = (k + t) % L::KST;
-          bool good = ptx::warp_wait(bars + L::K_FULL + s, ((k + t) / L::KST) & 1, abort_flag, tmo);
+          bool good = landed || ptx::warp_wait(bars + L::K_FULL + s, ((k + t) / L::KST) & 1, abort_flag, tmo);
           if (good && !L::kSepP && pv > 0) good = ptx::warp_wait(bars + L::PV_DONE + x, (pv - 1) & 1, abort_flag, tmo);
           if (!good) return false;
           ptx::tc_fence_after();
@@ -260,20 +261,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (t == w.nt - 1) commit(bars + L::Q_EMPTY + x, one);
           return true;
         };
-        const bool take_turns = w.has_b && w.nt > 2;
-        ok = ptx::warp_wait(bars + L::Q_FULL + x, n & 1, abort_flag, tmo) && issue_s(0);
+        ok = ptx::warp_wait(bars + L::Q_FULL + x, n & 1, abort_flag, tmo) && issue_s(0, false);
         for (int t = 0; ok && t < w.nt; ++t) {
-          const int s = (k + t) % L::VST;
-          ok = ptx::warp_wait(bars + L::P_FULL + x, pv & 1, abort_flag, tmo);
-          // A's first turn ever is its own; A's turn n waits for B's turn n - 1, B's for A's turn n
-          if (ok && take_turns && (x || turns > 0))
-            ok = ptx::warp_wait(bars + L::TURN + x, (x ? turns : turns - 1) & 1, abort_flag, tmo);
-          if (ok && L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1);
-          if (ok) ok = ptx::warp_wait(bars + L::V_FULL + s, ((k + t) / L::VST) & 1, abort_flag, tmo);
+          const int s = (k + t) % L::VST, nk = k + t + 1, ns = nk % L::KST;
+          // what else the products wait for comes before P and the turn, out of the way
+          ok = ptx::warp_wait(bars + L::V_FULL + s, ((k + t) / L::VST) & 1, abort_flag, tmo);
           if (ok && t == w.nt - 1 && last_dirty) {
             ok = ptx::warp_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);
             clean ^= 1u << s;
           }
+          const bool landed = t + 1 < w.nt && is_complete(bars + L::K_FULL + ns, (nk / L::KST) & 1);
+          // A's first turn ever is its own; A's turn n waits for B's turn n - 1, B's for A's turn n
+          if (ok && take_turns && (x || turns > 0))
+            ok = ptx::warp_wait(bars + L::TURN + x, (x ? turns : turns - 1) & 1, abort_flag, tmo);
+          if (ok) ok = ptx::warp_wait(bars + L::P_FULL + x, pv & 1, abort_flag, tmo);
+          if (ok && L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1, landed);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t dV = ptx::sdesc_lo(sV + s * L::TILE, kTile * 128);
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           commit(bars + L::PV_DONE + x, one);
           commit(bars + L::V_EMPTY + s, one);
           ++pv;
-          if (!L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1);
+          if (!L::kSepP && t + 1 < w.nt) ok = issue_s(t + 1, landed);
           if (take_turns) {
             ++turns;
             if (one) ptx::mbar_arrive(bars + L::TURN + 1 - x);

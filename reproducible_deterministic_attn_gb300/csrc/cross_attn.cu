@@ -211,7 +211,7 @@ bool distinct(const long long* st, int B, int S, int H) {
 // Every cut costs partials (written and read once more) and the start of another unit, too few leave
 // SMs idle, so each is the cheapest by a count of tasks of 128 x 128 scores: a unit takes its tasks
 // and `start` more, units run in rounds of the chip, and partials cost what memory takes for them (a
-// task is about 2 us, in which the chip moves 10 MB). Where batches have lengths of their own, which
+// task is about 1.5 us, in which the chip moves 10 MB). Where batches have lengths of their own, which
 // the host does not know, a fifth of the units is taken to be empty. A row segment has at most 128
 // row tiles: the tensor core truncates its additions, which over 16384 rows of one sign loses at
 // most 2^-15.5 of a sum.

@@ -13,10 +13,10 @@
 // dK and dV stay in TMEM over the unit's row tiles. S(t+1) waits for dV(t) (it overwrites P), dP(t+1)
 // for dK(t): two chains, each with an issuer of its own, that only the softmax gradient ties together.
 // The softmax warps go through exp(t), dS(t), exp(t+1) and would wait for S(t+1), so dK(t) gets in line
-// behind dV(t) and S(t+1) (issued as soon as dS(t) is there: 2550 us in place of 2410 below).
+// behind dV(t) and S(t+1) (issued as soon as dS(t) is there: 2550 us, so 2430).
 // Units of one key tile leave fp32 partials of dK and dV, which cross_join_keys_kernel adds in order.
 // A task takes 2600 cycles, 2048 of them products: from P(t) on, 100 until its issuer sees it, dV 700,
-// S 750, the exponentials 950. 8192 x 8192 x 128, 32 heads, both kernels: 2410 us, 1142 TFLOP/s. P^T in
+// S 750, the exponentials 950. 8192 x 8192 x 128, 32 heads, both kernels: 2350 us, 1168 TFLOP/s. P^T in
 // shared memory, which frees S's columns as soon as they are read, gained nothing: shared memory has
 // to carry the operands of the products already.
 //
@@ -354,8 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_ts = ptx::idesc_bf16(128, dsteps * 16, 0, 1);
       constexpr uint32_t BUF_STEP = L::TILE >> 4;
       // Every instruction between a product's end and the next one's start is time that the chain
-      // loses (with all of a task's waits there: 700 cycles, and 2630 us in place of 2410 at 8192 x
-      // 8192 x 128, 32 heads), so the walk and what else the next product waits for come before.
+      // loses (with all of a task's waits there: 700 cycles; 2630 us at 8192 x 8192 x 128, 32
+      // heads, so 2550), so the walk and what else the next product waits for come before.
       KeysWalk<true> w(p);
       const uint32_t one = elect_one();
       int it = 0, tile = 0;                        // tasks and key tiles so far

@@ -13,7 +13,7 @@
 //
 // A unit of few key tiles (a text) lasts little longer than its ends, which the next one's copies run
 // under: Q's under the last dP, dO's under the last dQ (8192 x 512, 16 heads of 128: 94 us, before both
-// waited for the last dP, now 86; warps of their own for the read-out of dQ gained nothing).
+// waited for the last dP, then 86, now 81; warps of their own for the read-out of dQ gained nothing).
 //
 // Warp roles (384 threads): 0 = TMA producer, 1 and 3 = MMA issuers (S; dP and dQ), 2 = K rows
 // behind a length, 4..11 = softmax gradient (quarter = TMEM lanes = rows, half = 64 keys each) and

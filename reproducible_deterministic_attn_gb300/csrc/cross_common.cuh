@@ -37,7 +37,7 @@ struct Maps {
 
 // Units of work number a kernel's [batch][d1][key head][d0]; a CTA takes every grid-th. The heads lie
 // side by side, so that CTAs that run together read a token's heads, whole lines of memory, together
-// (8192 x 512, 16 heads of 128, forward: 75 us with the heads behind d1, 71 so). Nothing is asked of
+// (8192 x 512, 16 heads of 128, forward: 75 us with the heads behind d1, then 71). Nothing is asked of
 // L2 ahead of time: such requests took the copies' own turns (68 us without them). A CTA steps from
 // unit to unit digit by digit, as a division takes more than all of a step.
 struct Units {

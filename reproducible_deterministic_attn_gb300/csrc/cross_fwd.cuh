@@ -15,11 +15,11 @@
 // exponentials need no second read, and moves the exponent's reference m only when the row
 // maximum exceeds it by more than 8 in log2 units (P <= 2^8; O and l share the reference).
 //
-// Bound, with long states, by the tensor cores and by shared memory, which a pair of key steps keeps
-// busy for as long (2048 cycles: operands of four products, of which two have A in TMEM, and the
-// copies): 8192 x 8192 x 128, 32 heads, takes 869 us (1265 TFLOP/s), 4096 x 4096 x 64, 32 heads, where a
-// product has half the work for the same softmax, 211 us. With captions a unit is one step and its
-// ends: 16 heads of 64, 4 x 4096 rows x 77 keys, 28 us where the bytes take 10.
+// Bound, with long states, by the tensor cores and the turns: of a tile's 1750 cycles 1024 are
+// products, the rest the ways from P to its issuer, from O to S and to the other tile. 8192 x 8192 x 128,
+// 32 heads, takes 773 to 806 us (1364 to 1422 TFLOP/s by card), 4096 x 4096 x 64, 32 heads, where the
+// products have half the work for the same softmax, 195 to 213. With captions a unit is one step and its
+// ends: 16 heads of 64, 4 x 4096 rows x 77 keys, 27 us where the bytes take 10.
 //
 // Key ranges (splits > 1): where the pairs of row tiles would leave most of the chip idle (single
 // tokens against long states) the keys are cut into ranges; a range leaves its rows' normalised O
@@ -217,8 +217,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // its own (DT = 64) S(t+1) goes ahead of P(t) V(t).
       // Over several key tiles the two issuers take turns with P(t) V(t) and S(t+1), so that one
       // tile's products run while the other's scores become P. Left alone they fall into step, both
-      // in the softmax and then both in line for the pipe (8192 x 8192 x 128, 32 heads: 1237 us, with
-      // turns 1092). With one or two key tiles turns only cost (77 keys: 33 us, with turns 38).
+      // in the softmax and then both in line for the pipe (8192 x 8192 x 128, 32 heads, when this was built:
+      // 1237 us, with turns 1092; a turn that passes before S is all issued: 829 for 806). With one or two
+      // key tiles turns only cost (77 keys: 33 us, with turns 38).
       const int x = warp >> 1;
       const uint32_t dQ = ptx::sdesc_lo(ptx::smem_u32(sm + L::Q_OFF + x * L::TILE), 16);
       const uint32_t sK = ptx::smem_u32(sm + L::K_OFF), sV = ptx::smem_u32(sm + L::V_OFF);
@@ -264,7 +265,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ok = ptx::warp_wait(bars + L::Q_FULL + x, n & 1, abort_flag, tmo) && issue_s(0, false);
         for (int t = 0; ok && t < w.nt; ++t) {
           const int s = (k + t) % L::VST, nk = k + t + 1, ns = nk % L::KST;
-          // what else the products wait for comes before P and the turn, out of the way
+          // what else the products wait for comes before P and the turn, out of the way (a wait costs 100
+          // cycles when it is over already; all of them in the way: 880 us in place of 782 at 16384 x 4096)
           ok = ptx::warp_wait(bars + L::V_FULL + s, ((k + t) / L::VST) & 1, abort_flag, tmo);
           if (ok && t == w.nt - 1 && last_dirty) {
             ok = ptx::warp_wait(bars + L::CLEAN + s, (clean >> s) & 1, abort_flag, tmo);

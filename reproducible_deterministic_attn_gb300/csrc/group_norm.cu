@@ -588,8 +588,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   } else if (warp == 0) {
     const T* x = (const T*)a.x + n * a.sb + (long long)g * a.cpg;
     float mean, rstd;
-    group_stats(a, [&](int e) { return e < kThreads ? pivots[e] : to_f32(x[e]); }, [&](int e) { return chan[e]; }, &mean,
-                &rstd);
+    // (S = 0: x has no element to look at)
+    group_stats(a, [&](int e) { return e < kThreads ? pivots[e] : a.S > 0 ? to_f32(x[e]) : 0.f; },
+                [&](int e) { return chan[e]; }, &mean, &rstd);
     if (lane == 0) {
       a.mean[blockIdx.x] = mean;
       a.rstd[blockIdx.x] = rstd;

@@ -254,8 +254,10 @@ typedef enum { DASH_ACT_NONE = 0, DASH_ACT_SILU = 1 } dash_act_t;
  *   y    : contiguous [N, S, C] (written; must not overlap x)
  *   mean, rstd : fp32 [N, G] (written), as the gradient reads them
  *   workspace  : dash_group_norm_workspace_size(N, S, C, G) bytes, for both directions
- * The sums are taken per channel around its first value, so that a mean that is large beside the
- * spread costs no digits. With S = 0 mean is 0 and rstd 1 / sqrt(eps).
+ * The sums are taken per channel around the median K of five of its values, at rows spread over the
+ * sample: a large mean or an unlike row costs no digits, the variance is off by some 2^-24 (1 + (K -
+ * mean)^2 / variance) of itself for each of the few dozen additions that a value goes through. With S = 0
+ * mean is 0 and rstd 1 / sqrt(eps).
  * N, S >= 0; C a multiple of G, up to 2^18, C / G up to 4096; N below 2^24, N * S and N * G below
  * 2^31 - 65536, N * S * C up to 2^42. Pointers aligned as their elements.
  */

@@ -2,7 +2,7 @@
 //
 // x [N, S, C], channels c of group g = c / (C / G): xh = (x - mean) rstd, z = xh w + b, y = act(z).
 // All sums are sums over rows per channel, in a fixed order: forward s = sum(x - K), q = sum((x -
-// K)^2) with the channel's pivot K = its first value (so that a large mean costs no digits),
+// K)^2) with the channel's pivot K, the median of five of its values at rows spread over the sample;
 // backward A = sum dz, B = rstd sum dz (x - mean) with dz = dy act'(z). Of these come, per group,
 //   mean, var            from m_c = K + s / S and q - s^2 / S, joined over the group's channels
 //   c1 = mean(w A), c2 = mean(w B);  dx = rstd (w dz - c1 - xh c2),  dw = sum_n B, db = sum_n A.
@@ -81,6 +81,26 @@ template <int V>
 __device__ __forceinline__ void load_channels(const float* p, int c, float other, float (&v)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = p ? __ldg(p + c + i) : other;
+}
+
+// The pivots of V channels of a sample (x: its first row's; S > 0). Sums around a pivot lose what
+// (K - mean)^2 exceeds the variance by, so one value is not enough: with the first row of a map (a
+// corner, which padding makes unlike the rest) 300 spreads away, 65536 rows lost 1e-3 of the variance. A
+// median of five rows is as far off only where three of the five are, and such rows are much of the spread.
+__device__ __forceinline__ float median(float a, float b, float c, float d, float e) {
+  const float lo = fmaxf(fminf(a, b), fminf(c, d)), hi = fminf(fmaxf(a, b), fmaxf(c, d));
+  return fmaxf(fminf(lo, hi), fminf(fmaxf(lo, hi), e));
+}
+template <typename T, int V>
+__device__ __forceinline__ void load_pivots(const T* x, long long ss, int S, float (&m)[V]) {
+  Vec<T, V> row[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) row[k] = load_vec<T, V>(x + (long long)S * (2 * k + 1) / 10 * ss);
+  float f[5][V];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) unpack<T, V>(row[k], f[k]);
+#pragma unroll
+  for (int i = 0; i < V; ++i) m[i] = median(f[0][i], f[1][i], f[2][i], f[3][i], f[4][i]);
 }
 
 // Adds V values to their channels' sums. Forward: m the pivots; backward: z = (x - m) w + b, with
@@ -300,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 2) resident_kernel(const __grid_cons
   float2* sums = (float2*)(gn_smem + (((BWD ? 2 : 1) * pieces * kThreads * PB + 15) & ~15));   // [slab] this CTA's
   float2* total = sums + a.slab;                   // [slab] the cluster's
   float2* grp = total + a.slab;                    // [groups] mean, rstd; backward: c1, c2
-  float2* red = grp + a.slab / a.cpg;
+  float* pivots = (float*)(grp + a.slab / a.cpg);  // [slab] forward
+  float2* red = grp + a.slab / a.cpg + (BWD ? 0 : (a.slab + 1) / 2);
   if (BWD) grid_next();
   const int ranks = (int)cluster_size(), rank = (int)ptx::cluster_rank();
   const Seat<V> st(a, blockIdx.x / ranks, rank);
@@ -328,7 +349,11 @@ __global__ void __launch_bounds__(kThreads, 2) resident_kernel(const __grid_cons
         w[i] *= __ldg(a.rstd + g);
       }
     } else {
-      read_piece<T, V>((const char*)(x + c), m);   // the pivots
+      load_pivots<T, V>(x + c, a.ss, a.S, m);
+      if (st.row == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) pivots[st.v * V + i] = m[i];
+      }
     }
   }
   fetch_wait();
@@ -373,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 2) resident_kernel(const __grid_cons
       if (lane == 0) grp[g] = make_float2(c1, c2);
     } else {
       float mean, rstd;
-      group_stats(a, [&](int e) { return to_f32(x[st.c0 + ch + e]); }, [&](int e) { return total[ch + e]; }, &mean, &rstd);
+      group_stats(a, [&](int e) { return pivots[ch + e]; }, [&](int e) { return total[ch + e]; }, &mean, &rstd);
       if (lane == 0) {
         grp[g] = make_float2(mean, rstd);
         if (rank == 0) {
@@ -509,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 2) sums_kernel(const __grid_constant
         w[i] *= __ldg(a.rstd + g);
       }
     } else {
-      read_piece<T, V>((const char*)(x + st.c), m);
+      load_pivots<T, V>(x + st.c, a.ss, a.S, m);
     }
     const long long row = st.r0 + st.row;
     for_pieces<T, V, BWD>(gn_smem, x + row * a.ss + st.c, dy + row * a.C + st.c, st.lanes * a.ss, (long long)st.lanes * a.C,
@@ -535,8 +560,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   const int n = blockIdx.x / a.G, g = blockIdx.x - n * a.G;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // the pivots, which no kernel of this call writes, fetched ahead
-  float first = 0.f;
-  if (!BWD && a.S > 0 && threadIdx.x < a.cpg) first = to_f32(((const T*)a.x)[n * a.sb + (long long)g * a.cpg + threadIdx.x]);
+  const auto pivot = [&](int e) {                  // (S = 0: x has no element to look at)
+    float m[1] = {0.f};
+    if (a.S > 0) load_pivots<T, 1>((const T*)a.x + n * a.sb + (long long)g * a.cpg + e, a.ss, a.S, m);
+    return m[0];
+  };
+  const float first = !BWD && threadIdx.x < a.cpg ? pivot(threadIdx.x) : 0.f;
   grid_wait();
   const float2* from = a.part + (long long)n * a.chunks * a.C + (long long)g * a.cpg;
   if (!BWD) pivots[threadIdx.x] = first;
@@ -586,11 +615,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
       a.coef[blockIdx.x] = make_float2(t.x / m, t.y / m);
     }
   } else if (warp == 0) {
-    const T* x = (const T*)a.x + n * a.sb + (long long)g * a.cpg;
     float mean, rstd;
-    // (S = 0: x has no element to look at)
-    group_stats(a, [&](int e) { return e < kThreads ? pivots[e] : a.S > 0 ? to_f32(x[e]) : 0.f; },
-                [&](int e) { return chan[e]; }, &mean, &rstd);
+    group_stats(a, [&](int e) { return e < kThreads ? pivots[e] : pivot(e); }, [&](int e) { return chan[e]; }, &mean,
+                &rstd);
     if (lane == 0) {
       a.mean[blockIdx.x] = mean;
       a.rstd[blockIdx.x] = rstd;
@@ -698,7 +725,8 @@ Plan make_plan(int N, int S, int C, int G, int V, int e, bool bwd) {
       const int rows = ceil_div(S, cl), pieces = ceil_div(rows, lanes);
       const long long bytes = (long long)pieces * kThreads * V * e * (bwd ? 2 : 1);
       const long long smem = (long long)round_up_to(bytes, 16) +
-                             (sum_room(C / V, nv, V) + 2 * slab + slab / cpg) * (long long)sizeof(float2);
+                             (sum_room(C / V, nv, V) + 2 * slab + slab / cpg + (bwd ? 0 : (slab + 1) / 2)) *
+                                 (long long)sizeof(float2);
       if (smem > kMaxShared) continue;
       const int held = smem + 1024 <= kMaxShared / 2 ? 2 : 1;
       const long long ctas = (long long)N * slabs * cl, rounds = ceil_div<long long>(ctas, kChip * held);

@@ -62,3 +62,49 @@ def test_a_row_unlike_the_others(N, S, C, G, where, mean, t):
     dr = wr * (dv * wr ** 2 / 2 + 8 * E) * 1.01
     assert bool(((mu.double() - wm).abs() <= dm).all()), float(((mu.double() - wm).abs() / dm).max())
     assert bool(((rstd.double() - wr).abs() <= dr).all()), float(((rstd.double() - wr).abs() / dr).max())
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("N,S,C,G", [(2, 64, 64, 4), (1, 20000, 64, 4), (1, 20000, 24, 8), (2, 50, 25, 5)])
+def test_groups_of_one_value(N, S, C, G, t):
+    """x - mean is 0, so y is act(b) whatever the size of the mean and of rstd; dx has no part along xh."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    v = torch.tensor([1000.0, -640.0, 3.0, 0.0], device="cuda").repeat(8)[:G].repeat_interleave(C // G)
+    x = v.to(t).expand(N, S, C).contiguous()
+    w, b = torch.randn(C, generator=g, device="cuda"), torch.randn(C, generator=g, device="cuda")
+    u = torch.finfo(t).eps / 2
+    for act in ("none", "silu"):
+        y, mean, rstd = da.group_norm_act_forward(x, w, b, G, 1e-5, act)
+        want, wm, wr = ref.group_norm(x, w, b, G, 1e-5, act)
+        assert torch.equal(mean.double(), wm)
+        err = (y.double() - want).abs()
+        assert bool((err <= (u + 2.0 ** -20) * want.abs() + 2.0 ** -25).all()), float(err.max())
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("N,S,C,G", [(2, 64, 64, 4), (1, 20000, 64, 4), (1, 20000, 24, 8), (2, 50, 25, 5)])
+def test_gradient_far_from_zero(N, S, C, G, act):
+    """fp32 values within a factor of two of the given mean: x - mean is exact, so nothing of the mean's
+    size is in the gradients' errors. z is off by 4 steps of its terms, the sigmoid and its slope by
+    2^-20 (1 + |z|); the group's means are sums of n = S C / G values that pass through at most 256
+    additions here."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(N, S, C, generator=g, device="cuda") + 1000.0
+    dy = torch.randn(N, S, C, generator=g, device="cuda")
+    w, b = 1 + 0.2 * torch.randn(C, generator=g, device="cuda"), 0.3 * torch.randn(C, generator=g, device="cuda")
+    _, mean, rstd = da.group_norm_act_forward(x, w, b, G, 1e-5, act)
+    dx, dw, db = da.group_norm_act_backward(dy, x, w, b, mean, rstd, G, act)
+    wdx, wdw, wdb, dz, xh = ref.group_norm_grad(dy, x, w, b, mean, rstd, G, act)
+    _, z, r = ref._affine(x, w, b, mean, rstd, G)
+    wa = w.double().abs()
+    ez = 4 * E * (z.abs() + wa * xh.abs() + b.double().abs())
+    ddz = dy.double().abs() * ((0.5 * ez + 2.0 ** -20 * (1 + z.abs())) if act == "silu" else 0 * z) + 4 * E * dz.abs()
+    over = lambda t: _sums(x, G)(t).repeat_interleave(C // G, 1)[:, None]  # noqa: E731
+    u1, u2 = (dz * wa).abs(), (dz * xh * wa).abs()
+    e1, e2 = over(ddz * wa + 256 * E * u1), over(ddz * xh.abs() * wa + 260 * E * u2)
+    tol = r * (ddz * wa + e1 + xh.abs() * e2 + 8 * E * (u1 + over(u1) + xh.abs() * over(u2)))
+    err = (dx.double() - wdx).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    ddw = (ddz * xh.abs() + 260 * E * (dz * xh).abs()).sum((0, 1))
+    assert bool(((dw.double() - wdw).abs() <= ddw).all())
+    assert bool(((db.double() - wdb).abs() <= (ddz + 256 * E * dz.abs()).sum((0, 1))).all())

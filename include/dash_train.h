@@ -251,7 +251,7 @@ typedef enum { DASH_ACT_NONE = 0, DASH_ACT_SILU = 1 } dash_act_t;
  *          part of a buffer that holds more channels; any strides and alignment, rows of whole
  *          16-byte pieces are moved as such)
  *   w, b : fp32 [C], or NULL for ones and zeros
- *   y    : contiguous [N, S, C] (written; must not overlap x)
+ *   y    : contiguous [N, S, C] (written; x itself where that is contiguous, else apart from it)
  *   mean, rstd : fp32 [N, G] (written), as the gradient reads them
  *   workspace  : dash_group_norm_workspace_size(N, S, C, G) bytes, for both directions
  * The sums are taken per channel around the median K of five of its values, at rows spread over the
@@ -271,7 +271,8 @@ dash_status_t dash_group_norm_fwd(const void* x, const float* w, const float* b,
  * Gradients of the above: with dz = dy act'(z), db = sum dz and dw = sum dz xh over samples and
  * rows, dx = rstd (w dz - mean(w dz) - xh mean(w dz xh)), the means over the group as above. xh and
  * z are recomputed from x, mean and rstd.
- *   dy   : contiguous [N, S, C] of `dtype` (read)      dx : contiguous [N, S, C] (written)
+ *   dy   : contiguous [N, S, C] of `dtype` (read)
+ *   dx   : contiguous [N, S, C] (written; dy itself, or x where that is contiguous, else apart from them)
  *   dw, db : fp32 [C] (written; NULL: not wanted)
  */
 dash_status_t dash_group_norm_bwd(const void* dy, const void* x, const float* w, const float* b,

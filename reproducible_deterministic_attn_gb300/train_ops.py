@@ -804,6 +804,15 @@ def _gn_args(x, w, b, groups, activation):
     return dev, pw, pb, (N, S, C, groups), _row_strides(st[0] if N > 1 else 0, row), act, dtype
 
 
+def _in_place_or_apart(out, name, t, other):
+    """An output may lie over an input element for element, not otherwise."""
+    if out.data_ptr() == t.data_ptr() and t.is_contiguous() or not t.numel():
+        return
+    end = t.data_ptr() + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+    if out.data_ptr() < end and t.data_ptr() < out.data_ptr() + out.element_size() * out.numel():
+        _bad(f"{name}: overlaps {other} other than element for element")
+
+
 def group_norm_act_forward(x, w, b, groups: int, eps: float = 1e-5, activation="silu", out=None, workspace=None,
                            stream=None):
     """Group norm over channels-last x with the activation behind it: act(xh * w + b).
@@ -811,7 +820,8 @@ def group_norm_act_forward(x, w, b, groups: int, eps: float = 1e-5, activation="
     x: [N, ..., C] bf16, fp16 or fp32 with contiguous channels; the dimensions between (rows, or
     height and width) are normed over together with the C / groups channels of a group, and may be
     strided as one (a part of a buffer with more channels). w, b: fp32 [C] or None; activation:
-    "silu" or "none". Returns (y, mean, rstd): contiguous y of x's type, fp32 [N, groups]."""
+    "silu" or "none". out: an optional contiguous tensor to write to, which may be x itself. Returns
+    (y, mean, rstd): contiguous y of x's type, fp32 [N, groups]."""
     if stream is not None:
         with _using(stream, x):
             return group_norm_act_forward(x, w, b, groups, eps, activation, out, workspace)
@@ -823,6 +833,8 @@ def group_norm_act_forward(x, w, b, groups: int, eps: float = 1e-5, activation="
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     elif out.dtype != x.dtype or out.shape != x.shape or not out.is_contiguous() or out.get_device() != dev:
         _bad(f"out: expected contiguous, of the type and shape of x, on cuda:{dev}")
+    else:
+        _in_place_or_apart(out, "out", x, "x")
     mean = torch.empty((sizes[0], groups), dtype=_F32, device=x.device)
     rstd = torch.empty((sizes[0], groups), dtype=_F32, device=x.device)
     if workspace is None:
@@ -838,8 +850,8 @@ def group_norm_act_backward(dy, x, w, b, mean, rstd, groups: int, activation="si
     """Gradients of group_norm_act_forward with respect to x, w and b.
 
     dy: contiguous, of x's type and shape; mean, rstd: as the forward returned them. dx: an optional
-    contiguous tensor to write to. Returns (dx, dw, db), the last two fp32 [C] (None where w or b is
-    None)."""
+    contiguous tensor to write to, which may be dy or a contiguous x itself. Returns (dx, dw, db), the
+    last two fp32 [C] (None where w or b is None)."""
     if stream is not None:
         with _using(stream, x):
             return group_norm_act_backward(dy, x, w, b, mean, rstd, groups, activation, dx, workspace)
@@ -847,11 +859,15 @@ def group_norm_act_backward(dy, x, w, b, mean, rstd, groups: int, activation="si
     if dev != _current_device():
         with torch.cuda.device(dev):
             return group_norm_act_backward(dy, x, w, b, mean, rstd, groups, activation, dx, workspace)
+    given = dx is not None
     if dx is None:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     for t, name in ((dy, "dy"), (dx, "dx")):
         if t.dtype != x.dtype or t.shape != x.shape or not t.is_contiguous() or t.get_device() != dev:
             _bad(f"{name}: expected contiguous, of the type and shape of x, on cuda:{dev}")
+    if given:
+        _in_place_or_apart(dx, "dx", x, "x")
+        _in_place_or_apart(dx, "dx", dy, "dy")
     for t, name in ((mean, "mean"), (rstd, "rstd")):
         if t.dtype != _F32 or t.shape != (sizes[0], groups) or not t.is_contiguous() or t.get_device() != dev:
             _bad(f"{name}: expected contiguous float32 [N, groups] on cuda:{dev}")

@@ -108,3 +108,39 @@ def test_gradient_far_from_zero(N, S, C, G, act):
     ddw = (ddz * xh.abs() + 260 * E * (dz * xh).abs()).sum((0, 1))
     assert bool(((dw.double() - wdw).abs() <= ddw).all())
     assert bool(((db.double() - wdb).abs() <= (ddz + 256 * E * dz.abs()).sum((0, 1))).all())
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("N,S,C,G", [(2, 64, 320, 32), (4, 2000, 128, 8), (4, 4096, 512, 32), (1, 60000, 64, 4), (3, 50, 25, 5)])
+def test_in_place(N, S, C, G, t):
+    """y over x, and dx over x or over dy: the bits of the call with an output of its own."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(N, S, C, generator=g, device="cuda").to(t)
+    dy = torch.randn(N, S, C, generator=g, device="cuda").to(t)
+    w, b = torch.randn(C, generator=g, device="cuda"), torch.randn(C, generator=g, device="cuda")
+    want = da.group_norm_act_forward(x, w, b, G)
+    grads = da.group_norm_act_backward(dy, x, w, b, *want[1:], G)
+    for _ in range(3):
+        y = x.clone()
+        got = da.group_norm_act_forward(y, w, b, G, out=y)
+        assert got[0] is y and all(torch.equal(p, q) for p, q in zip(got, want))
+        for over in (0, 1):
+            a = [x.clone(), dy.clone()]
+            got = da.group_norm_act_backward(a[1], a[0], w, b, *want[1:], G, dx=a[over])
+            assert got[0] is a[over] and all(torch.equal(p, q) for p, q in zip(got, grads))
+
+
+def test_outputs_that_overlap_otherwise_are_refused():
+    flat = torch.randn(4000, device="cuda")
+    x, w = flat[:3200].view(2, 50, 32), torch.ones(32, device="cuda")
+    _, mean, rstd = da.group_norm_act_forward(x, w, None, 4)
+    shifted, wide = flat[32:3232].view(2, 50, 32), flat[:3840].view(2, 60, 32)[:, :50]
+    part = flat[:3200].view(2, 25, 64)[..., :32]
+    for y, out in ((x, shifted), (shifted, x), (wide, x), (part, flat[:1600].view(2, 25, 32))):
+        with pytest.raises(ValueError, match="overlap"):
+            da.group_norm_act_forward(y, w, None, 4, out=out)
+    dy = torch.randn_like(x)
+    with pytest.raises(ValueError, match="overlap"):
+        da.group_norm_act_backward(dy, x, w, None, mean, rstd, 4, dx=shifted)
+    with pytest.raises(ValueError, match="overlap"):
+        da.group_norm_act_backward(shifted, dy, w, None, mean, rstd, 4, dx=x)

@@ -570,7 +570,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   grid_wait();
   const float2* from = a.part + (long long)n * a.chunks * a.C + (long long)g * a.cpg;
   if (!BWD) pivots[threadIdx.x] = first;
-  const float rs = BWD ? __ldg(a.rstd + blockIdx.x) : 1.f;
+  // (without rows the sums are 0 and rstd is infinite where eps is 0)
+  const float rs = BWD && a.S > 0 ? __ldg(a.rstd + blockIdx.x) : 1.f;
   for (int c0 = 0; c0 < a.cpg; c0 += kThreads) {
     const int cols = min(kThreads, a.cpg - c0), per = kThreads / cols;
     const int sub = (int)threadIdx.x / cols, c = (int)threadIdx.x - sub * cols;

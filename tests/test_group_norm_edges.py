@@ -144,3 +144,13 @@ def test_outputs_that_overlap_otherwise_are_refused():
         da.group_norm_act_backward(dy, x, w, None, mean, rstd, 4, dx=shifted)
     with pytest.raises(ValueError, match="overlap"):
         da.group_norm_act_backward(shifted, dy, w, None, mean, rstd, 4, dx=x)
+
+
+def test_gradient_without_rows_and_eps():
+    """rstd is infinite, the sums over no row are 0 all the same."""
+    x = torch.empty(2, 0, 32, device="cuda")
+    w, b = torch.rand(32, device="cuda"), torch.rand(32, device="cuda")
+    y, mean, rstd = da.group_norm_act_forward(x, w, b, 4, 0.0)
+    assert bool(torch.isinf(rstd).all())
+    dx, dw, db = da.group_norm_act_backward(x, x, w, b, mean, rstd, 4)
+    assert not bool(dw.any()) and not bool(db.any())

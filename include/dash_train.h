@@ -291,8 +291,9 @@ dash_status_t dash_group_norm_bwd(const void* dy, const void* x, const float* w,
  *              projection, [B, H, S, D], and batches or heads that are shared (a stride of zero)
  *              are read in place (multiples of 8)
  *   kv_lens  : [B] int32 or int64, 0 <= kv_lens[b] <= Sk, or NULL: all Sk keys. A batch without
- *              keys has O = 0 and LSE = -inf. What lies behind a length is never used: it may
- *              hold infinities or NaN
+ *              keys has O = 0 and LSE = -inf, and so has a row whose scores are all -inf (a key
+ *              with such a score has the weight 0). What lies behind a length is never used: it
+ *              may hold infinities or NaN
  *   o        : bf16 contiguous [B, Sq, Hq, D] (written)    lse : fp32 [B, Hq, Sq] (written)
  *   status   : optional device int32 (NULL = none), cleared by the call: DASH_ERR_BOUNDS for a
  *              length out of range, whose batch gets NaN in o and lse; DASH_ERR_SYNC_TIMEOUT for

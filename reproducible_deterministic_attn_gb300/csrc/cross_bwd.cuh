@@ -31,7 +31,7 @@
 // No CTA waits for another one.
 //
 // -Delta and -LSE log2e come per row from cross_pre_kernel, with -inf for rows a tile does not
-// have (P = 0 there). Keys that a length leaves out: warp 2 zeroes their rows of K and V in shared
+// have and for rows whose scores are all -inf (P = 0 there). Keys that a length leaves out: warp 2 zeroes their rows of K and V in shared
 // memory, as they may hold anything, and their P is set to 0.
 //
 // Warp roles (512 threads): 0 = TMA producer, 1 and 3 = MMA issuers, 2 = key rows behind a length,
@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(256, 8) cross_pre_kernel(const __grid_constant
         const int tile = p.s.packed ? tk : head * p.s.nq + tk, r = p.s.packed ? i * p.s.g + head : i;
         const size_t at = ((size_t)(b * p.s.Hk + hk) * p.s.ntile + tile) * kTile + r;
         p.delta[at] = -t;
-        p.nnl[at] = -kLog2e * __ldg(p.lse + ((size_t)b * p.s.Hq + h) * p.s.Sq + token);
+        const float nnl = -kLog2e * __ldg(p.lse + ((size_t)b * p.s.Hq + h) * p.s.Sq + token);
+        p.nnl[at] = nnl == INFINITY ? -nnl : nnl;   // a row that sees nothing: P = 0
       }
       if ((p.s.lens || p.s.Sk == 0) && 8 * l < p.s.D) {
         const int len = length_of(p.s, b);

@@ -73,6 +73,9 @@ struct FwdLay {
 
 constexpr int kFwdThreads = 640;
 constexpr float kRescaleLog2 = 8.f;
+// The reference of a row without a score above -inf so far: finite, so that such scores get the weight
+// exp2(-inf) = 0 (around a reference of -inf it would be NaN) and a later one moves it.
+constexpr float kLowest = -3.4028234663852886e38f;
 constexpr int kFwdRegsLaunch = 96, kFwdRegsCtrl = 32, kFwdRegsSoftmax = 112;
 static_assert(kFwdRegsCtrl + 4 * kFwdRegsSoftmax == 5 * kFwdRegsLaunch,
               "the five warpgroups must share exactly the launch's registers");
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     bool ok = true;
     for (; at.more(p.units); at.next(p.units)) {
       if (x && 2 * at.d1 + 1 >= p.s.ntile) continue;
-      float m = -INFINITY, l = 0.f;                // of the row; of this half
+      float m = kLowest, l = 0.f;                  // of the row; of this half
       bool first = true;                           // key tile of the unit
       // A warp whose wait ran out goes on without work, as its partner must find it at every meeting.
       for (int left = FwdWalk<>::keys_in_range(p, at); left > 0; left -= kTile, ++steps) {
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int tile = 2 * at.d1 + x, group = at.b * p.s.Hk + at.hk;
       const bool live = row_of(p.s, tile, r, token, head);
       const bool bad = !ok || len < 0;             // NaN for a bad length
-      const float inv = bad ? NAN : none ? 0.f : 1.f / l;
+      const float inv = bad ? NAN : none || l == 0.f ? 0.f : 1.f / l;   // l = 0: all scores are -inf
       const float l2 = bad ? NAN : none ? -INFINITY : m + __log2f(l);
       const size_t row = (((size_t)at.d0 * p.s.B * p.s.Hk + group) * p.s.ntile + tile) * kTile + r;
       const int h = at.hk * p.s.g + head;

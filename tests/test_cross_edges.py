@@ -1,0 +1,49 @@
+"""GPU: cross attention at the edges of what it accepts: scores of minus infinity, gradients that are
+not finite, long states."""
+import pytest
+import torch
+
+import reproducible_deterministic_attn_gb300 as da
+from tests._lib import ensure_built, has_gpu
+from tests.test_cross_attn import _check_forward, _inputs
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not has_gpu(), reason="needs a CUDA GPU")]
+
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+@pytest.mark.parametrize("B,Sq,Sk,Hq,Hk,D,n", [
+    (1, 300, 700, 2, 1, 64, 130), (1, 300, 700, 2, 1, 128, 130), (2, 1, 1500, 8, 2, 128, 900),
+    (1, 2000, 400, 16, 16, 64, 256), (1, 2000, 400, 16, 16, 128, 257), (3, 40, 90, 4, 2, 80, 89), (1, 1, 9000, 1, 1, 64, 8999)])
+def test_leading_scores_of_minus_infinity(B, Sq, Sk, Hq, Hk, D, n):
+    """The first n keys have a score of -inf with every query: their weight is 0, whatever the other
+    key tiles and ranges hold."""
+    x = _inputs(B, Sq, Sk, Hq, Hk, D, None, seed=n)
+    x["q"], x["k"] = x["q"].clone(), x["k"].clone()
+    x["q"][..., 3] = x["q"][..., 3].abs() + 0.5
+    x["k"][:, :n, :, 3] = -INF
+    o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"])
+    y = dict(x, k=x["k"][:, n:], v=x["v"][:, n:], lens=[Sk - n] * B)
+    _check_forward(y, o, lse)
+
+
+@pytest.mark.parametrize("Sq,Sk,Hq,D", [(128, 77, 2, 64), (256, 300, 2, 128), (2048, 300, 16, 64), (1, 1500, 4, 128)])
+def test_rows_whose_scores_are_all_minus_infinity(Sq, Sk, Hq, D):
+    """They see no key: O = 0 and LSE = -inf, as with a length of 0, and no gradient reaches v from them."""
+    x = _inputs(1, Sq, Sk, Hq, Hq, D, None, seed=Sk)
+    q, k, v, do = x["q"].clone(), x["k"].clone(), x["v"], x["do"]
+    q[..., 3] = 0.5 + q[..., 3].abs()
+    k[:, :, 0, 3] = -INF                              # head 0
+    o, lse = da.cross_attn_forward(q, k, v, x["scale"])
+    assert not bool(o[:, :, 0].any()) and bool((lse[:, 0] == -INF).all())
+    some = lambda t: t[:, :, 1:]  # noqa: E731
+    _check_forward(dict(x, q=some(q), k=some(k), v=some(v)), some(o).contiguous(), lse[:, 1:])
+    dq, dk, dv = da.cross_attn_backward(q, k, v, o, do, lse, x["scale"])
+    assert Sq == 1 or not bool(dv[:, :, 0].any())
+    assert all(bool(torch.isfinite(t[:, :, 1:]).all()) for t in (dq, dk, dv))

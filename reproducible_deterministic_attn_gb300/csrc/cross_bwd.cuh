@@ -31,7 +31,8 @@
 // No CTA waits for another one.
 //
 // -Delta and -LSE log2e come per row from cross_pre_kernel, with -inf for rows a tile does not
-// have and for rows whose scores are all -inf (P = 0 there). Keys that a length leaves out: warp 2 zeroes their rows of K and V in shared
+// have and for rows whose scores are all -inf (P = 0 there; a tile without
+// its last row gets these zeros by hand, as a row of zeros against an infinite key is NaN). Keys that a length leaves out: warp 2 zeroes their rows of K and V in shared
 // memory, as they may hold anything, and their P is set to 0.
 //
 // Warp roles (512 threads): 0 = TMA producer, 1 and 3 = MMA issuers, 2 = key rows behind a length,
@@ -479,12 +480,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && w.next()) {
       const int ob = it % L::NDO;
       // (the offsets beside dO were copied by TMA: their own barrier is waited for as well)
-      ok = ptx::warp_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo) &&
-           ptx::warp_wait(bars + C_S_FULL, it & 1, abort_flag, tmo);
-      if (!ok) break;
-      ptx::tc_fence_after();
       const float* nnl = (const float*)(sm + L::OFFS_OFF + ob * L::OFFS) + col0;
       const float* delta = nnl + kTile;
+      ok = ptx::warp_wait(bars + C_DO_FULL + ob, (it / L::NDO) & 1, abort_flag, tmo);
+      const bool pads = nnl[kTile - 1 - col0] == -INFINITY;   // rows that a tile does not have come last
+      if (ok) ok = ptx::warp_wait(bars + C_S_FULL, it & 1, abort_flag, tmo);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (pads) {
+        // (here, as anything about it among the exponentials below takes 4 % of the kernel's time)
+#pragma unroll 1
+        for (int c0 = 0; c0 < 64; c0 += 16) {
+          float s[16];
+          ptx::tmem_ld16(tmem + lane_addr + L::T_SP + col0 + c0, s);
+          uint32_t u[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(nnl[c0 + c] == -INFINITY ? 0.f : s[c]);
+          ptx::tmem_st8(tmem + lane_addr + L::T_SP + col0 + c0, u);
+          ptx::tmem_st8(tmem + lane_addr + L::T_SP + col0 + c0 + 8, u + 8);
+        }
+        ptx::tmem_wait_st();
+      }
       float pv[64];
       {
         uint32_t a[32], b[32];

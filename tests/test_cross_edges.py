@@ -47,3 +47,23 @@ def test_rows_whose_scores_are_all_minus_infinity(Sq, Sk, Hq, D):
     dq, dk, dv = da.cross_attn_backward(q, k, v, o, do, lse, x["scale"])
     assert Sq == 1 or not bool(dv[:, :, 0].any())
     assert all(bool(torch.isfinite(t[:, :, 1:]).all()) for t in (dq, dk, dv))
+
+
+@pytest.mark.parametrize("B,Sq,Sk,Hq,Hk,D,lens", [
+    (1, 130, 77, 2, 2, 64, None), (1, 130, 300, 2, 1, 128, None), (2, 40, 90, 6, 2, 128, (90, 80)),
+    (3, 1, 1500, 8, 2, 64, (1500, 700, 900)), (1, 1000, 500, 16, 16, 64, None), (1, 200, 60, 3, 1, 128, None)])
+def test_places_of_a_row_tile_without_a_row(B, Sq, Sk, Hq, Hk, D, lens):
+    """Keys whose scores are -inf with every query weigh 0 and get no gradient; nor may the places behind a
+    tile's last row give them one (zeros times an infinite key). The others' gradients are those of the call
+    without such keys."""
+    x = _inputs(B, Sq, Sk, Hq, Hk, D, lens, seed=Sq, hide=False)
+    x["q"] = x["q"].clone()
+    x["q"][..., 3] = 0.5 + x["q"][..., 3].abs()
+    k = x["k"].clone()
+    k[:, 5::7, :, 3] = -INF
+    o, lse = da.cross_attn_forward(x["q"], k, x["v"], x["scale"], x["t"])
+    _, dk, dv = da.cross_attn_backward(x["q"], k, x["v"], o, x["do"], lse, x["scale"], x["t"])
+    assert not bool(dk[:, 5::7].any()) and not bool(dv[:, 5::7].any())
+    _, dk0, dv0 = da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"])
+    keep = torch.arange(Sk, device="cuda") % 7 != 5
+    assert torch.equal(dk[:, keep], dk0[:, keep]) and torch.equal(dv[:, keep], dv0[:, keep])

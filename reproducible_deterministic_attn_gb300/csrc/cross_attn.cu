@@ -283,7 +283,7 @@ dash_status_t launch_bwd(BwdArgs a, bool one, const Maps& maps, cudaStream_t str
   // places of row tiles without a row: behind the last token, and where heads fill no tile
   const bool padded = a.s.Sq % a.s.tpt || (a.s.packed && a.s.g * a.s.tpt < kTile);
   const unsigned pads = padded ? (unsigned)ceil_div<long long>(rows, 256) : 0;
-  // key tiles that no unit visits: behind lengths, or all where there are no rows
+  // keys that no unit's sums go to: behind lengths, or all where there are no rows
   const unsigned key_blocks =
       a.s.lens || !work ? (unsigned)ceil_div<long long>((long long)a.s.B * a.s.Sk * a.s.Hk, 16) : 0;
   cross_pre_kernel<<<row_blocks + pads + key_blocks, 256, 0, stream>>>(a, row_blocks, pads);

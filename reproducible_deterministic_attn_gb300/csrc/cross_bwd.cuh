@@ -135,7 +135,8 @@ struct KeysWalk {
 // waits for its loads only once (4 rows and half the threads: 36 us for 134 MB, now 28). Rows of
 // batches without keys get their dq here: 0, or NaN for a length out of range. The first block
 // clears the workspace's header and looks for such lengths. The next `pads` blocks write the row
-// tiles' places that have no row, those behind them dk and dv of the key tiles that no unit visits.
+// tiles' places that have no row, those behind them dk and dv of the keys that a length leaves out, all of
+// them, as a unit's sums for such a key are not zeros where dO is not finite (0 times NaN).
 constexpr int kPreRows = 2;
 __global__ void __launch_bounds__(256, 8) cross_pre_kernel(const __grid_constant__ BwdArgs p, unsigned row_blocks,
                                                            unsigned pads) {
@@ -153,8 +154,8 @@ __global__ void __launch_bounds__(256, 8) cross_pre_kernel(const __grid_constant
     const long long row = (long long)(blockIdx.x - row_blocks - pads) * 16 + (threadIdx.x >> 4);   // (batch, key, head)
     if (row >= (long long)p.s.B * p.s.Sk * p.s.Hk || 8 * l >= p.s.D) return;
     const int h = (int)(row % p.s.Hk), key = (int)(row / p.s.Hk % p.s.Sk), b = (int)(row / p.s.Hk / p.s.Sk);
-    const int len = length_of(p.s, b), tiles = (max(len, 0) + kTile - 1) / kTile;
-    if (key / kTile < tiles && p.s.ntile > 0) return;
+    const int len = length_of(p.s, b);
+    if (key < len && p.s.ntile > 0) return;
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = len < 0 ? NAN : 0.f;
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float a[32];
               ptx::tmem_ld32(from + c0, a);
               if (p.qsegs > 1) store_part_32(part + which * kTile * DT, row, c0, a, 1.f);
-              else store_rows_bf16(lane, a, which ? 1.f : p.scale, key < p.s.Sk ? dst + c0 : nullptr, p.s.D - c0);
+              else store_rows_bf16(lane, a, which ? 1.f : p.scale, row < w.keys() ? dst + c0 : nullptr, p.s.D - c0);
             }
           }
         }
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.header + WS_STATUS, 0, kStatusSyncTimeout);
 }
 
-// dk and dv of the visited key tiles as the sums of the row segments' partials, in order; a thread
+// dk and dv of the keys within the lengths as the sums of the row segments' partials, in order; a thread
 // takes 8 columns of a row.
 template <int DT>
 __global__ void __launch_bounds__(256) cross_join_keys_kernel(const __grid_constant__ BwdArgs p) {
@@ -686,8 +687,8 @@ __global__ void __launch_bounds__(256) cross_join_keys_kernel(const __grid_const
   const long long row = item / per;                // (batch, key, head)
   if (row >= (long long)p.s.B * p.s.Sk * p.s.Hk) return;
   const int h = (int)(row % p.s.Hk), key = (int)(row / p.s.Hk % p.s.Sk), b = (int)(row / p.s.Hk / p.s.Sk);
+  if (key >= length_of(p.s, b)) return;
   const int kt = key / kTile;
-  if (kt * kTile >= length_of(p.s, b)) return;
   const float* src = p.dkv_part + ((((size_t)b * p.s.Hk + h) * p.s.nk + kt) * 2 * kTile) * DT + part_at(key % kTile, c);
   const size_t step = (size_t)p.s.B * p.s.Hk * p.s.nk * 2 * kTile * DT;
   float k[8] = {}, v[8] = {};

@@ -67,3 +67,18 @@ def test_places_of_a_row_tile_without_a_row(B, Sq, Sk, Hq, Hk, D, lens):
     _, dk0, dv0 = da.cross_attn_backward(x["q"], x["k"], x["v"], o, x["do"], lse, x["scale"], x["t"])
     keep = torch.arange(Sk, device="cuda") % 7 != 5
     assert torch.equal(dk[:, keep], dk0[:, keep]) and torch.equal(dv[:, keep], dv0[:, keep])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+@pytest.mark.parametrize("B,Sq,Sk,Hq,Hk,D,lens", [
+    (2, 300, 77, 4, 2, 64, (50, 77)), (2, 300, 77, 4, 2, 128, (50, 0)), (2, 300, 513, 4, 1, 128, (400, 257)),
+    (1, 1, 1500, 4, 4, 64, (700,)), (1, 5000, 60, 1, 1, 128, (33,))])
+def test_rows_behind_a_length_are_zero_whatever_the_gradient(B, Sq, Sk, Hq, Hk, D, lens, bad):
+    x = _inputs(B, Sq, Sk, Hq, Hk, D, lens, seed=12)
+    o, lse = da.cross_attn_forward(x["q"], x["k"], x["v"], x["scale"], x["t"])
+    do = x["do"].clone()
+    do[:, Sq // 2, Hq - 1, D // 2] = bad
+    dq, dk, dv = da.cross_attn_backward(x["q"], x["k"], x["v"], o, do, lse, x["scale"], x["t"])
+    for b, m in enumerate(lens):
+        assert not bool(dk[b, m:].any()) and not bool(dv[b, m:].any())
+        assert m == 0 or not bool(torch.isfinite(dv[b, :m, Hk - 1, D // 2]).any())

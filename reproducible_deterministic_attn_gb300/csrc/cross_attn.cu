@@ -50,6 +50,11 @@ Shape make_shape(int B, int Sq, int Sk, int Hq, int Hk, int D, bool may_pack) {
   return s;
 }
 
+// Key tiles that O or dQ sums in TMEM at most: the tensor core truncates its additions, so that sums of
+// one sign come out small. Measured: O over 16384 keys by 1e-4, over these 65536 by 3.4e-4 (dQ by 4e-5), a
+// twelfth of bf16's rounding; without a bound by 2 % over 4 M keys. Up to 65536 keys nothing is cut for it.
+constexpr int kMaxKeyTiles = 512;
+
 // Key ranges of the forward.
 struct FwdPlan {
   int pairs, splits, kper;
@@ -59,13 +64,11 @@ FwdPlan fwd_plan(const Shape& s) {
   FwdPlan p;
   p.pairs = ceil_div(s.ntile, 2);
   const long long units = (long long)s.B * s.Hk * p.pairs;
-  p.splits = 1;
-  p.kper = std::max(1, s.nk);
-  if (units > 0 && units * 2 <= kChip && s.nk > 1) {
-    p.splits = (int)std::min<long long>(s.nk, kChip / units);
-    p.kper = ceil_div(s.nk, p.splits);
-    p.splits = ceil_div(s.nk, p.kper);
-  }
+  p.splits = std::max(1, ceil_div(s.nk, kMaxKeyTiles));
+  if (units > 0 && units * 2 <= kChip && s.nk > 1)
+    p.splits = std::max(p.splits, (int)std::min<long long>(s.nk, kChip / units));
+  p.kper = std::max(1, ceil_div(s.nk, p.splits));
+  p.splits = std::max(1, ceil_div(s.nk, p.kper));
   const size_t rows = p.splits > 1 ? (size_t)p.splits * s.B * s.Hk * s.ntile * kTile : 0;
   p.part_o = kWsHeaderBytes;
   p.part_l = p.part_o + rows * (s.D <= 64 ? 64 : 128) * sizeof(float);
@@ -213,8 +216,8 @@ bool distinct(const long long* st, int B, int S, int H) {
 // and `start` more, units run in rounds of the chip, and partials cost what memory takes for them (a
 // task is about 1.5 us, in which the chip moves 10 MB). Where batches have lengths of their own, which
 // the host does not know, a fifth of the units is taken to be empty. A row segment has at most 128
-// row tiles: the tensor core truncates its additions, which over 16384 rows of one sign loses at
-// most 2^-15.5 of a sum.
+// row tiles, as the tensor core's truncation loses at most 2^-15.5 of a sum of one sign over them (a key
+// range at most kMaxKeyTiles).
 int best_cut(long long units, int tasks, int least, double start, double part_bytes, bool ragged) {
   int cut = least;
   double best = 1e300;
@@ -247,7 +250,7 @@ BwdPlan bwd_plan(const Shape& s, bool ragged) {
     p.qsegs = best_cut(groups * nk, nt, ceil_div(nt, 128), 2, (double)keys * dt * 8, ragged);
     p.qper = ceil_div(nt, p.qsegs);
     if (!p.one) {
-      p.ksegs = best_cut(groups * nt, nk, 1, 2, (double)rows * dt * 4, ragged);
+      p.ksegs = best_cut(groups * nt, nk, ceil_div(nk, kMaxKeyTiles), 2, (double)rows * dt * 4, ragged);
       p.kper = ceil_div(nk, p.ksegs);
     }
   }

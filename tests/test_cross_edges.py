@@ -1,5 +1,7 @@
 """GPU: cross attention at the edges of what it accepts: scores of minus infinity, gradients that are
 not finite, long states."""
+import math
+
 import pytest
 import torch
 
@@ -82,3 +84,48 @@ def test_rows_behind_a_length_are_zero_whatever_the_gradient(B, Sq, Sk, Hq, Hk, 
     for b, m in enumerate(lens):
         assert not bool(dk[b, m:].any()) and not bool(dv[b, m:].any())
         assert m == 0 or not bool(torch.isfinite(dv[b, :m, Hk - 1, D // 2]).any())
+
+
+def _same_rows(Sq, Sk, H, seed):
+    """Queries that are all alike, so that one row says what each is: scores of any sign, values and a key
+    column whose products with dS have one sign."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    sign = (torch.randint(0, 2, (Sk,), generator=g, device="cuda") * 2 - 1).bfloat16()
+    k = torch.zeros(1, Sk, 1, 64, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    k[0, :, 0, 0] = torch.randn(Sk, generator=g, device="cuda").bfloat16()
+    k[0, :, 0, 1] = sign                               # the queries' column 1 is 0
+    v[0, :, 0, 0] = sign
+    v[0, :, 0, 1] = 1.0
+    q = torch.zeros(1, Sq, H, 64, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    do = torch.zeros_like(q)
+    do[..., 0] = 1.0
+    return q, k, v, do
+
+
+@pytest.mark.parametrize("Sk", [1 << 16, (1 << 16) + 1, (1 << 21) + 77, 1 << 22])
+def test_long_states(Sk):
+    """Sums of one sign over millions of keys. The tensor core truncates: each of the n / 16 additions of
+    a unit loses up to two steps (2^-23) of the sum so far, half the last one on average, n 2^-27 in all, 2^-11
+    over the 65536 keys that a unit takes at most; beside the roundings of P or dS (2^-8 of each, which average:
+    8 times 2^-8 / sqrt(n)) and of the result."""
+    H, Sq = 1, 77 * 256
+    q, k, v, do = _same_rows(Sq, Sk, H, seed=Sk)
+    o, lse = da.cross_attn_forward(q, k, v, 1.0)
+    z = k[0, :, 0, 0].double()
+    s = v[0, :, 0, 0].double()
+    p = torch.softmax(z, 0)
+    u = 2.0 ** -8
+    tol = 2.0 ** -11 + u / math.sqrt(Sk) * 8 + 2.0 ** -20
+    assert bool(((lse.double() - torch.logsumexp(z, 0)).abs() <= 2.0 ** -16).all())
+    # (a bf16 value just below 1 is off by at most 2^-9)
+    assert bool(((o[..., 1].double() - 1).abs() <= u / 2 + tol).all()), float(o[..., 1].float().min())
+    want = float((p * s).sum())
+    assert bool(((o[..., 0].double() - want).abs() <= u * abs(want) + tol).all())
+    # dS = P (s - delta), dQ's column 1 = sum dS s, of one sign
+    delta = o[0, 0, 0, 0].double()
+    dq, dk, dv = da.cross_attn_backward(q, k, v, o, do, lse, 1.0)
+    want = float((torch.exp(z - lse[0, 0, 0].double()) * (s - delta) * s).sum())
+    assert bool(((dq[..., 1].double() - want).abs() <= (u / 2 + tol) * abs(want) + 2.0 ** -20).all()), (
+        float(dq[..., 1].float().min()), want)

@@ -298,7 +298,8 @@ dash_status_t dash_group_norm_bwd(const void* dy, const void* x, const float* w,
  *   status   : optional device int32 (NULL = none), cleared by the call: DASH_ERR_BOUNDS for a
  *              length out of range, whose batch gets NaN in o and lse; DASH_ERR_SYNC_TIMEOUT for
  *              a wait that ran out, with NaN in lse
- *   workspace: dash_cross_attn_fwd_workspace_size(B, Sq, Sk, Hq, Hk, D) bytes
+ *   workspace: dash_cross_attn_fwd_workspace_size(B, Sq, Sk, Hq, Hk, D) bytes, which is 0 for
+ *              sizes that are not taken and for B = 0 (then nothing is used; NULL will do)
  * B, Sq, Sk >= 0; Hq a multiple of Hk; D a multiple of 8 up to 128; Sq, Sk up to 2^24 and
  * B * Hq * max(Sq, Sk) below 2^31 - 256; scale > 0 and finite. q, k, v, o 16-byte aligned, the
  * others as their elements. bf16 only, as the attention.
@@ -319,7 +320,8 @@ dash_status_t dash_cross_attn_fwd(const void* q, const void* k, const void* v, c
  *   dq, dk, dv : strided as dq_strides, dk_strides, dv_strides say (written; no stride of zero over
  *              more than one element). Rows of dk and dv behind a length are zero; a batch
  *              without keys has dq = 0, one whose length is out of range NaN in dq, dk and dv
- *   workspace: dash_cross_attn_bwd_workspace_size(B, Sq, Sk, Hq, Hk, D) bytes
+ *   workspace: dash_cross_attn_bwd_workspace_size(B, Sq, Sk, Hq, Hk, D) bytes, 0 as above; for
+ *              B = 0 the 256 bytes of the status
  * The workspace's status reads DASH_ERR_BOUNDS or DASH_ERR_SYNC_TIMEOUT as above. Other
  * arguments and errors as for the forward.
  */

@@ -657,6 +657,7 @@ def dash_cross_attn_bwd_workspace_size(B: int, Sq: int, Sk: int, Hq: int, Hk: in
 def new_cross_attn_workspace(B: int, Sq: int, Sk: int, Hq: int, Hk: int, D: int, device,
                              forward_only: bool = False) -> torch.Tensor:
     """A workspace of cross_attn_forward and, unless forward_only, of cross_attn_backward (uint8)."""
+    B = max(B, 1)                                    # (the sizes are those of at least one batch)
     nbytes = dash_cross_attn_fwd_workspace_size(B, Sq, Sk, Hq, Hk, D)
     if nbytes and not forward_only:
         nbytes = max(nbytes, dash_cross_attn_bwd_workspace_size(B, Sq, Sk, Hq, Hk, D))

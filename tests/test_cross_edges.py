@@ -129,3 +129,12 @@ def test_long_states(Sk):
     want = float((torch.exp(z - lse[0, 0, 0].double()) * (s - delta) * s).sum())
     assert bool(((dq[..., 1].double() - want).abs() <= (u / 2 + tol) * abs(want) + 2.0 ** -20).all()), (
         float(dq[..., 1].float().min()), want)
+
+
+def test_no_batch_with_a_workspace():
+    ws = da.new_cross_attn_workspace(0, 5, 40, 2, 1, 64, "cuda")
+    q, k = torch.empty(0, 5, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 40, 1, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = da.cross_attn_forward(q, k, k, 1.0, workspace=ws)
+    grads = da.cross_attn_backward(q, k, k, o, q, lse, 1.0, workspace=ws)
+    assert o.shape == q.shape and [t.shape for t in grads] == [q.shape, k.shape, k.shape]
+    assert da.dash_attn_get_status(ws) == da.DASH_OK

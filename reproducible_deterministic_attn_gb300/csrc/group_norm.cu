@@ -706,18 +706,21 @@ struct Plan {
   int chunks, cols;
 };
 
-// The cut is the one that takes the least time by what the two ways measured (us on the GPU).
-// Resident: each round of the chip's CTAs takes 6 (backward 9) and what its bytes take at 44 GB/s an
-// SM, a third more where a row of a slab is under 64 bytes, and 1 more for each doubling of the
-// cluster (clusters of 8 and 16 wait long for their places: never). In passes: 11 (backward 15) and
-// what three (five) sweeps take at 6.5 TB/s. Measured, resident / in passes: 4 x 4096 x 512 bf16
-// forward 12.6 / 19.2, backward 28.5 / 29.9; 4 x 1024 x 512 9 / 12.7 and 13 / 20; 8 x 1024 x 1280
-// 15.3 / 20.4 and 34 / 31.5; 4 x 16384 x 128 fp32 28 / 17.7 and 51 / 26.
+// How a call is cut, by what both ways measured (us on the GPU).
+// Resident: among the cuts that fit, the one of the least count: each round of the chip's CTAs takes 6
+// (backward 9) and what its bytes take at 44 GB/s an SM, a third more where a row of a slab is under 64
+// bytes, and 1 more for each doubling of the cluster (clusters of 8 and 16 wait long for their places: never).
+// Resident or in passes: instructions for each element are what either takes next to its latency, so a round
+// takes 6.7 and 0.15 for each 1000 elements of an SM (backward 7.8 and 0.26), the passes 11.4 and 1.03 for
+// each million elements (15.3 and 1.54). Resident / in passes, the chosen one with a star:
+//   bf16        4 x 1024 x 512   4 x 4096 x 512   8 x 1024 x 1280   8 x 4096 x 320   8 x 4096 x 512
+//   forward     9.4* / 13.3      15.5* / 21.1     18.2* / 23.1      19.2* / 21.5     29.7 / 26.7*
+//   backward    13.3* / 19.5     30.6 / 29.7*     39.4 / 32.1*      39.6 / 29.3*     58 / 40*
+//   fp32 4 x 4096 x 512: 24.2 / 21.4* and 43 / 32*; bf16 2 x 4096 x 320: 12.4* / 13.2 and 20.1* / 18.3
 Plan make_plan(int N, int S, int C, int G, int V, int e, bool bwd) {
   Plan p = {};
   const int cpg = C / G;
-  const double data = (double)N * S * C * e;
-  double best = (bwd ? 15 : 11) + data * (bwd ? 5 : 3) / 6.5e6;
+  double best = 1e300, resident = 0;
   const int unit = S > 0 ? lcm(cpg, V) : C + 1;      // slabs are whole groups and whole pieces
   for (int slab = unit; slab <= C && slab <= 2048 && slab / V <= kThreads; slab += slab < unit * 4 ? unit : slab) {
     if (slab * e < 32 && slab + unit <= C) continue;
@@ -736,6 +739,7 @@ Plan make_plan(int N, int S, int C, int G, int V, int e, bool bwd) {
       const double t = rounds * ((bwd ? 9 : 6) + moved * (slab * e < 64 ? 1.33 : 1.0) / 44e3) + (cl == 4 ? 2 : cl - 1);
       if (t < best) {
         best = t;
+        resident = rounds * ((bwd ? 7.8 : 6.7) + moved / ((bwd ? 3 : 2) * e) * (bwd ? 0.26e-3 : 0.15e-3));
         p.resident = true;
         p.slab = slab;
         p.slabs = slabs;
@@ -746,7 +750,9 @@ Plan make_plan(int N, int S, int C, int G, int V, int e, bool bwd) {
       }
     }
   }
+  p.resident = p.resident && resident <= (bwd ? 15.3 : 11.4) + (double)N * S * C * (bwd ? 1.54e-6 : 1.03e-6);
   if (p.resident) return p;
+  p = {};
   const int nv = C / V;
   p.cols = std::min(nv, kThreads);
   const int lanes = kThreads / p.cols;

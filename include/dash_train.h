@@ -316,7 +316,10 @@ dash_status_t dash_cross_attn_fwd(const void* q, const void* k, const void* v, c
  * Gradients of the above, with P = exp(scale * Q K^T - LSE) recomputed: dV = P^T dO,
  * dS = P * (dO V^T - rowsum(dO * O)), dQ = scale * dS K, dK = scale * dS^T Q; dK and dV sum over
  * the query heads that share a key head.
- *   o, do    : bf16 contiguous [B, Sq, Hq, D], lse : fp32 [B, Hq, Sq] (read)
+ *   o, do    : bf16 contiguous [B, Sq, Hq, D], lse : fp32 [B, Hq, Sq] (read). P and dS are rounded
+ *              to bf16 as operands: each gradient is about 2.4e-3 off in norm for this o, 1.7e-3 of it
+ *              its own rounding. That o is rounded to bf16 adds to it where a row has few keys and
+ *              dO V^T - rowsum(dO * O) cancels: dq and dk of 2 keys are 3.7e-3 off, of 8 2.7e-3
  *   dq, dk, dv : strided as dq_strides, dk_strides, dv_strides say (written; no stride of zero over
  *              more than one element). Rows of dk and dv behind a length are zero; a batch
  *              without keys has dq = 0, one whose length is out of range NaN in dq, dk and dv

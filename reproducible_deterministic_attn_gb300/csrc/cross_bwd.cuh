@@ -16,7 +16,7 @@
 // behind dV(t) and S(t+1) (issued as soon as dS(t) is there: 2550 us, so 2430).
 // Units of one key tile leave fp32 partials of dK and dV, which cross_join_keys_kernel adds in order.
 // A task takes 2600 cycles, 2048 of them products: from P(t) on, 100 until its issuer sees it, dV 700,
-// S 750, the exponentials 950. 8192 x 8192 x 128, 32 heads, both kernels: 2350 us, 1168 TFLOP/s. P^T in
+// S 750, the exponentials 950. 8192 x 8192 x 128, 32 heads, both kernels: 2350 to 2490 us by card, 1104 to 1168 TFLOP/s. P^T in
 // shared memory, which frees S's columns as soon as they are read, gained nothing: shared memory has
 // to carry the operands of the products already.
 //

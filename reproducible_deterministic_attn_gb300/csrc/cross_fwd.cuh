@@ -17,7 +17,7 @@
 //
 // Bound, with long states, by the tensor cores and the turns: of a tile's 1750 cycles 1024 are
 // products, the rest the ways from P to its issuer, from O to S and to the other tile. 8192 x 8192 x 128,
-// 32 heads, takes 773 to 806 us (1364 to 1422 TFLOP/s by card), 4096 x 4096 x 64, 32 heads, where the
+// 32 heads, takes 773 to 832 us (1322 to 1422 TFLOP/s by card), 4096 x 4096 x 64, 32 heads, where the
 // products have half the work for the same softmax, 195 to 213. With captions a unit is one step and its
 // ends: 16 heads of 64, 4 x 4096 rows x 77 keys, 27 us where the bytes take 10.
 //

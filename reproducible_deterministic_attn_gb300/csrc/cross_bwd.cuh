@@ -16,9 +16,9 @@
 // behind dV(t) and S(t+1) (issued as soon as dS(t) is there: 2550 us, so 2430).
 // Units of one key tile leave fp32 partials of dK and dV, which cross_join_keys_kernel adds in order.
 // A task takes 2600 cycles, 2048 of them products: from P(t) on, 100 until its issuer sees it, dV 700,
-// S 750, the exponentials 950. 8192 x 8192 x 128, 32 heads, both kernels: 2350 to 2490 us by card, 1104 to 1168 TFLOP/s. P^T in
-// shared memory, which frees S's columns as soon as they are read, gained nothing: shared memory has
-// to carry the operands of the products already.
+// S 750, the exponentials 950. 8192 x 8192 x 128, 32 heads, both kernels: 2350 to 2490 us by card, 1104 to
+// 1168 TFLOP/s. P^T in shared memory, which frees S's columns as soon as they are read, gained nothing:
+// shared memory has to carry the operands of the products already.
 //
 // Where a group has one key tile (up to 128 keys: a caption) the same kernel forms dQ too (DQ), as
 // nothing has to be summed over key tiles: dS^T also goes to shared memory, [key][row], and
@@ -30,10 +30,10 @@
 // 8192 rows x 512 keys x 16 x 128 took 360 us.
 // No CTA waits for another one.
 //
-// -Delta and -LSE log2e come per row from cross_pre_kernel, with -inf for rows a tile does not
-// have and for rows whose scores are all -inf (P = 0 there; a tile without
-// its last row gets these zeros by hand, as a row of zeros against an infinite key is NaN). Keys that a length leaves out: warp 2 zeroes their rows of K and V in shared
-// memory, as they may hold anything, and their P is set to 0.
+// -Delta and -LSE log2e come per row from cross_pre_kernel, with -inf for rows a tile does not have and for
+// rows whose scores are all -inf (P = 0 there; in a tile without its last row such scores are set to 0
+// first, as a row of zeros against an infinite key is NaN). Keys that a length leaves out: warp 2 zeroes
+// their rows of K and V in shared memory, as they may hold anything, and their P is set to 0.
 //
 // Warp roles (512 threads): 0 = TMA producer, 1 and 3 = MMA issuers, 2 = key rows behind a length,
 // 4..11 = softmax gradient (quarter = TMEM lanes = keys, half = 64 rows each), 12..15 = dQ
@@ -489,9 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       if (pads) {
-        // (here, as anything about it among the exponentials below takes 4 % of the kernel's time)
+        // (apart from the exponentials below, where any test takes 4 % of the kernel's time. Here the tiles that
+        // have such rows pay: 4 x 300 rows x 2000 keys, 24 / 8 heads of 64, whose tiles all have: 87 us, now 92)
 #pragma unroll 1
         for (int c0 = 0; c0 < 64; c0 += 16) {
+          if (nnl[c0 + 15] != -INFINITY) continue;
           float s[16];
           ptx::tmem_ld16(tmem + lane_addr + L::T_SP + col0 + c0, s);
           uint32_t u[16];

@@ -321,7 +321,7 @@ dash_status_t dash_cross_attn_fwd(const void* q, const void* k, const void* v, c
  *              its own rounding. That o is rounded to bf16 adds to it where a row has few keys and
  *              dO V^T - rowsum(dO * O) cancels: dq and dk of 2 keys are 3.7e-3 off, of 8 2.7e-3
  *   dq, dk, dv : strided as dq_strides, dk_strides, dv_strides say (written; no stride of zero over
- *              more than one element). Rows of dk and dv behind a length are zero; a batch
+ *              more than one element; apart from all that is read and from one another). Rows of dk and dv behind a length are zero; a batch
  *              without keys has dq = 0, one whose length is out of range NaN in dq, dk and dv
  *   workspace: dash_cross_attn_bwd_workspace_size(B, Sq, Sk, Hq, Hk, D) bytes, 0 as above; for
  *              B = 0 the 256 bytes of the status

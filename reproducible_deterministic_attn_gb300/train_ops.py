@@ -719,7 +719,7 @@ def cross_attn_backward(q, k, v, o, do, lse, scale: float, kv_lens=None, dq=None
 
     o and lse as the forward returned them, do contiguous like o. dq, dk, dv: optional tensors to
     write to, strided like q, k and v may be (parts of a fused projection's gradient), without
-    strides of zero. Rows of dk and dv behind a length are zero. Returns (dq, dk, dv)."""
+    strides of zero, and apart from all that the call reads and from one another. Rows of dk and dv behind a length are zero. Returns (dq, dk, dv)."""
     if stream is not None:
         with _using(stream, q):
             return cross_attn_backward(q, k, v, o, do, lse, scale, kv_lens, dq, dk, dv, workspace, check=check)
@@ -733,6 +733,13 @@ def cross_attn_backward(q, k, v, o, do, lse, scale: float, kv_lens=None, dq=None
     if (lse.dtype != _F32 or lse.shape != (sizes[0], sizes[3], sizes[1]) or not lse.is_contiguous()
             or lse.get_device() != dev):
         _bad(f"lse: expected contiguous float32 [B, Hq, Sq] on cuda:{dev}")
+    taken = None
+    for t, name in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
+        if t is not None and t.numel() and 0 not in t.stride():      # (those are refused below)
+            taken = taken or {x.data_ptr() for x in (q, k, v, o, do)}
+            if t.data_ptr() in taken:
+                _bad(f"{name}: lies over another tensor of the call")
+            taken.add(t.data_ptr())
     dq = torch.empty(q.shape, dtype=_BF16, device=q.device) if dq is None else dq
     dk = torch.empty(k.shape, dtype=_BF16, device=q.device) if dk is None else dk
     dv = torch.empty(v.shape, dtype=_BF16, device=q.device) if dv is None else dv

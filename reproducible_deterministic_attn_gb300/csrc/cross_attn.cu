@@ -55,7 +55,9 @@ Shape make_shape(int B, int Sq, int Sk, int Hq, int Hk, int D, bool may_pack) {
 // twelfth of bf16's rounding; without a bound by 2 % over 4 M keys. Up to 65536 keys nothing is cut for it.
 constexpr int kMaxKeyTiles = 512;
 
-// Key ranges of the forward.
+// Key ranges of the forward: as many as keep the units within one round of the chip, which takes at least two
+// for each. Two where they make a second round cost more than they gain: 80 units of single tokens (5 x 16 key
+// heads of 128) take 24 us with 1500 keys and 199 with 16384, in two ranges 29 and 204.
 struct FwdPlan {
   int pairs, splits, kper;
   size_t part_o, part_l, total;      // workspace offsets and size
